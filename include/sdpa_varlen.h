@@ -49,7 +49,8 @@ typedef enum sdpa_status {
   SDPA_ERR_STRIDE = 5,    /* a row/head stride is not a multiple of 8 elements       */
   SDPA_ERR_ALIGN = 6,     /* a tensor pointer is not 16-byte aligned                 */
   SDPA_ERR_WORKSPACE = 7, /* workspace NULL or smaller than the query says           */
-  SDPA_ERR_ARG = 8,       /* window < 0, scale not finite, unknown route policy      */
+  SDPA_ERR_ARG = 8,       /* window < 0, scale not finite, unknown route policy,
+                             a rotation's sections or rotated dims                   */
   SDPA_ERR_CUDA = 9       /* a CUDA call failed; see sdpa_last_error()               */
 } sdpa_status;
 
@@ -64,6 +65,8 @@ typedef enum sdpa_status {
 #define SDPA_SEG_OVERLAP 16   /* two valid segments share a packed row: every row of both
                                  has an unspecified output                                */
 #define SDPA_DEV_TIMEOUT 32   /* a bounded device wait gave up; the output is unspecified */
+#define SDPA_ROPE_BAD_POS 64  /* a row's position lies outside the rotation table: the row is
+                                 written as 0 and nothing of it goes into a store         */
 
 /* Route policy (process-wide).  AUTO sends segments with q_len * (Hq / Hkv) >= 128 to the
  * tensor-memory prefill kernel when the call's such segments hold at least 2^30 of work
@@ -183,6 +186,126 @@ sdpa_status sdpa_seq_clone(void* k_store, void* v_store, int64_t rows, int cols,
 sdpa_status sdpa_causal_prefill(const void* q, const void* k, const void* v, int64_t Lq,
                                 int64_t Lkv, int Hq, int Hkv, int D, float scale, void* out,
                                 void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Rotary positions.  The first rot_dims dims of a head are rot_dims / 2 pairs; pair j of a row at
+ * position p (of the axis the pair belongs to) is turned by the angle whose cosine and sine are
+ * table[p][j]: (a, b) -> (a cos - b sin, a sin + b cos).  Pairs are dims (j, j + rot_dims / 2), or
+ * (2j, 2j + 1) when `interleaved`; dims from rot_dims on pass unchanged.  Results are the exact
+ * ones rounded to fp32 and then to bf16.
+ *  table       [table_rows, rot_dims / 2] pairs of fp32 (cos, sin), contiguous device memory,
+ *              16-byte aligned, table_rows in [1, 2^31 - 1].
+ *  rot_dims    a multiple of 16, at most D.
+ *  positions   device int32 [axes, T] with `pos_stride` elements between axes: the position of
+ *              packed row t on each axis (for example time, height and width), read on the device.
+ *              For the append entries it may be NULL when axes is 1: a row's position is then its
+ *              position in its sequence, kv_end - q_len + i.
+ *  sections    axes (1 to 4) counts that sum to rot_dims / 2: the first sections[0] pairs belong to
+ *              axis 0, the next sections[1] to axis 1, and so on.
+ * A row with a position outside [0, table_rows) on an axis that has pairs is reported by
+ * SDPA_ROPE_BAD_POS.
+ */
+typedef struct sdpa_rotation {
+  const float* table;
+  int64_t table_rows;
+  const int32_t* positions;
+  int64_t pos_stride;
+  int32_t rot_dims;
+  int32_t axes;
+  int32_t sections[4];
+  int32_t interleaved;
+} sdpa_rotation;
+
+/*
+ * Rotate packed rows: out[t, h, :] = x[t, h, :] turned by row t's angles; `inverse` nonzero turns
+ * the other way, which is the gradient: for y = rope(x), dL/dx = rope(dL/dy, inverse).
+ *  x, out   [T, H, D] bf16 with their own strides (multiples of 8 elements, 16-byte aligned
+ *           pointers); out may be x (the same strides), else the two may not overlap.
+ * A row with a position outside the table is written as 0.  D in {64, 128, 256}, T >= 0, H >= 1.
+ * With T = 0 this entry and the ones below do nothing, and row pointers may be NULL.
+ * Errors: SDPA_ERR_NULL, _SHAPE, _HEAD_DIM, _STRIDE, _ALIGN, _ARG (the rotation), _CUDA.
+ */
+sdpa_status sdpa_rope(const void* x, int64_t T, int H, int D, int64_t x_row_stride, int64_t x_head_stride,
+                      const sdpa_rotation* rotation, int inverse, void* out, int64_t o_row_stride,
+                      int64_t o_head_stride, int32_t* status_dev, void* stream);
+
+/*
+ * A step's rows on their way to attention: queries rotated into q_out, keys rotated and values as
+ * they are written into the column store, in one kernel.  An attention call over the store follows.
+ *  q, k_new, v_new   [T, Hq, D] and [T, Hkv, D] bf16, each with its own row and head strides
+ *                    (non-negative multiples of 8 elements), so that they may be parts of one
+ *                    projection's rows; read only (q_out may be q, with the same strides).
+ *  k_store, v_store, seq_info, S   as for sdpa_varlen_append: row i of a live segment has position
+ *                    p = kv_end - q_len + i and goes to store row p % rows of its column.
+ *  seg_mode, window  what decides, as for the attention call that follows, which segments are
+ *                    valid: seg_mode NULL, or [S, 2] as for sdpa_varlen_modes (replacing window).
+ *  q_out             [T, Hq, D] bf16; every row is written: rows that no live segment covers, rows
+ *                    with p < 0 and rows with a position outside the table as 0.  None of these
+ *                    writes to the store.
+ * Two live segments that write the same (row, column) cell leave it unspecified.  status_dev takes
+ * the segment bits and SDPA_ROPE_BAD_POS.  No workspace.
+ * Errors: SDPA_ERR_NULL, _SHAPE, _HEAD_DIM, _GQA, _STRIDE, _ALIGN, _ARG, _CUDA.
+ */
+sdpa_status sdpa_rope_append(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* k_new,
+                             int64_t k_row_stride, int64_t k_head_stride, const void* v_new, int64_t v_row_stride,
+                             int64_t v_head_stride, int64_t T, int Hq, int Hkv, int D,
+                             const sdpa_rotation* rotation, void* k_store, void* v_store, int64_t rows, int cols,
+                             const int32_t* seq_info, const int32_t* seg_mode, int S, int window, void* q_out,
+                             int64_t o_row_stride, int64_t o_head_stride, int32_t* status_dev, void* stream);
+
+/*
+ * The 4-bit column store.  K and V are each a pair of byte arrays on the device, contiguous and
+ * 16-byte aligned:
+ *  codes   [cols, Hkv, rows, D / 2]: byte i of a row holds dim 2i in its low nibble and dim 2i + 1 in
+ *          its high one;
+ *  scales  [cols, Hkv, rows, D / 32]: one byte per 32 dims.
+ * Nibble c under scale byte b stands for (c - 8) * 2^((b >> 3) - 21) * (1 + (b & 7) / 8): exact in
+ * bf16, and finite for every byte pattern.  rows is a multiple of 16 (a ring may have more rows than
+ * it needs).  Position j of a column lives in store row j % rows, as in the bf16 store.
+ * A group of 32 bf16 values x is stored under the scale nearest to max|x| / 7 (ties to the even
+ * byte), with codes 8 + clamp(round(x / scale), -7, 7), halves to even: no value is off by more than
+ * half a step, 0.54 / 7 of its group's largest magnitude at most.  Magnitudes above 13440 saturate;
+ * a NaN is stored as 0.
+ */
+typedef struct sdpa_q4_store {
+  uint8_t* k_codes;
+  uint8_t* k_scales;
+  uint8_t* v_codes;
+  uint8_t* v_scales;
+} sdpa_q4_store;
+
+/* sdpa_rope_append into a 4-bit store: the rotated keys, rounded to bf16, and the values take their
+ * 4 bits on the way. */
+sdpa_status sdpa_rope_append_fourbit(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* k_new,
+                                int64_t k_row_stride, int64_t k_head_stride, const void* v_new,
+                                int64_t v_row_stride, int64_t v_head_stride, int64_t T, int Hq, int Hkv, int D,
+                                const sdpa_rotation* rotation, const sdpa_q4_store* store, int64_t rows, int cols,
+                                const int32_t* seq_info, const int32_t* seg_mode, int S, int window, void* q_out,
+                                int64_t o_row_stride, int64_t o_head_stride, int32_t* status_dev, void* stream);
+
+/* Rows of a segment table read back from a 4-bit store: k_out, v_out [T, Hkv, D] bf16 with common
+ * strides; packed row q_start + i of a live segment receives position kv_end - q_len + i (a segment
+ * with q_len = kv_end reads its whole column).  Other rows are written as 0. */
+sdpa_status sdpa_fourbit_unpack(const sdpa_q4_store* store, int64_t rows, int cols, int Hkv, int D,
+                           const int32_t* seq_info, const int32_t* seg_mode, int S, int window, int64_t T,
+                           void* k_out, void* v_out, int64_t o_row_stride, int64_t o_head_stride,
+                           int32_t* status_dev, void* stream);
+
+/* Bytes of device workspace sdpa_varlen_fourbit needs for these bounds. */
+size_t sdpa_varlen_fourbit_workspace_bytes(int64_t T, int Hq, int Hkv, int D, int S, int64_t rows, int cols);
+
+/*
+ * sdpa_varlen over a 4-bit store: the attention of the values the codes stand for.  seg_mode is NULL,
+ * or [S, 2] (causal, window) per segment as for sdpa_varlen_modes, replacing causal and window.
+ * Arguments, checks and status bits otherwise as for sdpa_varlen, with the store's own (pointers
+ * 16-byte aligned, rows a multiple of 16), scale >= 0, and workspace of at least
+ * sdpa_varlen_fourbit_workspace_bytes bytes.
+ */
+sdpa_status sdpa_varlen_fourbit(const void* q, int64_t T, int Hq, int D, int64_t q_row_stride, int64_t q_head_stride,
+                           const sdpa_q4_store* store, int64_t rows, int cols, int Hkv, const int32_t* seq_info,
+                           const int32_t* seg_mode, int S, int causal, int window, float scale, void* out,
+                           int64_t o_row_stride, int64_t o_head_stride, void* workspace, size_t ws_bytes,
+                           int32_t* status_dev, void* stream);
 
 /* Set the process-wide route policy (SDPA_ROUTE_*).  Returns SDPA_ERR_ARG if unknown. */
 sdpa_status sdpa_set_route_policy(int policy);

@@ -12,7 +12,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
-from typing import Optional
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 
@@ -20,14 +20,16 @@ from . import _build
 
 __all__ = [
     "sdpa_varlen", "sdpa_varlen_modes", "sdpa_varlen_append", "sdpa_seq_clone", "sdpa_causal_prefill",
-    "sdpa_varlen_splitk_static", "workspace_bytes", "workspace_status", "prefill_available", "set_route_policy",
+    "sdpa_varlen_splitk_static", "sdpa_rope", "sdpa_rope_append", "sdpa_rope_append_q4", "sdpa_q4_unpack",
+    "sdpa_varlen_q4", "Q4Store", "q4_store", "rope_table", "q4_workspace_bytes", "workspace_bytes", "workspace_status", "prefill_available", "set_route_policy",
     "set_timing_events", "library",
     "SDPA_OK", "SEG_BAD_QRANGE", "SEG_BAD_COL", "SEG_BAD_KV", "SEG_SPAN", "SEG_OVERLAP",
-    "DEV_TIMEOUT", "ROUTE_AUTO", "ROUTE_SPLITK", "ROUTE_PREFILL", "SdpaError",
+    "DEV_TIMEOUT", "ROPE_BAD_POS", "ROUTE_AUTO", "ROUTE_SPLITK", "ROUTE_PREFILL", "SdpaError",
 ]
 
 SDPA_OK = 0
 SEG_BAD_QRANGE, SEG_BAD_COL, SEG_BAD_KV, SEG_SPAN, SEG_OVERLAP, DEV_TIMEOUT = 1, 2, 4, 8, 16, 32
+ROPE_BAD_POS = 64
 ROUTE_AUTO, ROUTE_SPLITK, ROUTE_PREFILL = 0, 1, 2
 
 STATUS_NAMES = {
@@ -40,7 +42,8 @@ EXPORTS = [
     "sdpa_varlen_workspace_bytes", "sdpa_varlen", "sdpa_causal_prefill", "sdpa_set_route_policy",
     "sdpa_set_timing_events", "sdpa_last_error", "sdpa_version", "sdpa_varlen_splitk_static",
     "sdpa_varlen_append", "sdpa_seq_clone", "sdpa_varlen_modes", "sdpa_prefill_available",
-    "sdpa_workspace_status",
+    "sdpa_workspace_status", "sdpa_rope", "sdpa_rope_append", "sdpa_rope_append_fourbit", "sdpa_fourbit_unpack",
+    "sdpa_varlen_fourbit", "sdpa_varlen_fourbit_workspace_bytes",
 ]
 
 
@@ -48,6 +51,17 @@ class SdpaError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"{STATUS_NAMES.get(code, code)}: {msg}")
         self.code = code
+
+
+class _Rotation(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("table_rows", ctypes.c_int64), ("positions", ctypes.c_void_p),
+                ("pos_stride", ctypes.c_int64), ("rot_dims", ctypes.c_int32), ("axes", ctypes.c_int32),
+                ("sections", ctypes.c_int32 * 4), ("interleaved", ctypes.c_int32)]
+
+
+class _Q4Pointers(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p)]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -100,6 +114,23 @@ def library(build_if_missing: bool = True) -> ctypes.CDLL:
                                               c_vp]
     lib.sdpa_workspace_status.restype = c_int
     lib.sdpa_workspace_status.argtypes = [c_vp, ctypes.c_size_t, ctypes.POINTER(ctypes.c_int32), c_vp]
+    c_rot, c_q4 = ctypes.POINTER(_Rotation), ctypes.POINTER(_Q4Pointers)
+    lib.sdpa_rope.restype = c_int
+    lib.sdpa_rope.argtypes = [c_vp, c_i64, c_int, c_int, c_i64, c_i64, c_rot, c_int, c_vp, c_i64, c_i64, c_vp, c_vp]
+    step = [c_vp, c_i64, c_i64] * 3 + [c_i64, c_int, c_int, c_int, c_rot]  # q, k_new, v_new, sizes, rotation
+    table = [c_i64, c_int, c_vp, c_vp, c_int, c_int]                       # rows, cols, seq_info .. window
+    lib.sdpa_rope_append.restype = c_int
+    lib.sdpa_rope_append.argtypes = step + [c_vp, c_vp] + table + [c_vp, c_i64, c_i64, c_vp, c_vp]
+    lib.sdpa_rope_append_fourbit.restype = c_int
+    lib.sdpa_rope_append_fourbit.argtypes = step + [c_q4] + table + [c_vp, c_i64, c_i64, c_vp, c_vp]
+    lib.sdpa_fourbit_unpack.restype = c_int
+    lib.sdpa_fourbit_unpack.argtypes = [c_q4, c_i64, c_int, c_int, c_int, c_vp, c_vp, c_int, c_int, c_i64, c_vp, c_vp,
+                                   c_i64, c_i64, c_vp, c_vp]
+    lib.sdpa_varlen_fourbit_workspace_bytes.restype = ctypes.c_size_t
+    lib.sdpa_varlen_fourbit_workspace_bytes.argtypes = [c_i64, c_int, c_int, c_int, c_int, c_i64, c_int]
+    lib.sdpa_varlen_fourbit.restype = c_int
+    lib.sdpa_varlen_fourbit.argtypes = [c_vp, c_i64, c_int, c_int, c_i64, c_i64, c_q4, c_i64, c_int, c_int, c_vp, c_vp,
+                                   c_int, c_int, c_int, c_f, c_vp, c_i64, c_i64, c_vp, ctypes.c_size_t, c_vp, c_vp]
     _lib = lib
     return lib
 
@@ -347,4 +378,278 @@ def sdpa_varlen_splitk_static(q: torch.Tensor, k_store: torch.Tensor, v_store: t
         seq_info.data_ptr() if S else None, S, int(bool(causal)), int(window), float(scale), out.data_ptr(),
         out.stride(0), out.stride(1), status.data_ptr() if status is not None else None, _stream_ptr(stream))
     _check(code)
+    return out
+
+
+# ------------------------------------------------ rotary positions and the 4-bit column store
+
+def _same_device(*tensors) -> torch.device:
+    """The one CUDA device of the tensors given (None passes)."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda or (dev is not None and t.device != dev):
+            raise ValueError("every tensor must be on the same CUDA device")
+        dev = t.device
+    return dev
+
+
+def _run(entry, device: torch.device, stream, *args) -> None:
+    """Calls a C entry with `device` current and its stream (the given one, else the device's
+    current one) as the last argument."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    handle = (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        code = entry(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            code = entry(*args, handle)
+    if code != SDPA_OK:
+        _check(code)
+
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """An uninitialised tensor whose memory belongs to the stream that will write it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _check_rows(name: str, t: torch.Tensor, H: Optional[int] = None, D: Optional[int] = None,
+                T: Optional[int] = None) -> None:
+    if t.dim() != 3 or t.dtype != torch.bfloat16 or t.stride(2) != 1:
+        raise ValueError(f"{name} must be bf16 [T, heads, D] with unit inner stride")
+    if (T is not None and t.shape[0] != T) or (H is not None and t.shape[1] != H) or \
+            (D is not None and t.shape[2] != D):
+        raise ValueError(f"{name} must be [{T}, {H}, {D}], not {list(t.shape)}")
+
+
+def _status_ptr(status: Optional[torch.Tensor]):
+    if status is None:
+        return None
+    if status.dtype != torch.int32 or status.numel() < 1:
+        raise ValueError("status must be an int32 tensor")
+    return status.data_ptr()
+
+
+def _check_table(seq_info: torch.Tensor, seg_mode: Optional[torch.Tensor]) -> int:
+    """Checks a segment table and its modes; returns the number of segments."""
+    if seq_info.dtype != torch.int32 or not seq_info.is_contiguous() or \
+            (seq_info.numel() and (seq_info.dim() != 2 or seq_info.shape[1] != 4)):
+        raise ValueError("seq_info must be a contiguous int32 [S, 4] tensor")
+    S = seq_info.shape[0] if seq_info.numel() else 0
+    if seg_mode is not None and (seg_mode.dtype != torch.int32 or not seg_mode.is_contiguous()
+                                 or (S and tuple(seg_mode.shape) != (S, 2))):
+        raise ValueError("seg_mode must be a contiguous int32 [S, 2] tensor")
+    return S
+
+
+def _rotation(table: torch.Tensor, positions: Optional[torch.Tensor], sections: Optional[Sequence[int]],
+              interleaved: bool, T: int) -> _Rotation:
+    if table.dim() != 3 or table.shape[2] != 2 or table.dtype != torch.float32 or not table.is_contiguous():
+        raise ValueError("table must be contiguous fp32 [positions, rotated pairs, 2]")
+    half = table.shape[1]
+    sections = (half,) if sections is None else tuple(sections)
+    axes = len(sections)
+    if not 1 <= axes <= 4:
+        raise ValueError(f"sections has {axes} position axes: 1 to 4")
+    stride = 0
+    if positions is not None:
+        if positions.dtype != torch.int32:
+            raise ValueError("positions must be int32")
+        if positions.dim() == 1 and axes == 1:
+            positions = positions.unsqueeze(0)
+        if positions.dim() != 2 or tuple(positions.shape) != (axes, T) or (T > 1 and positions.stride(1) != 1):
+            raise ValueError(f"positions must be int32 [{axes}, {T}] with unit inner stride")
+        stride = positions.stride(0)
+    elif axes > 1:
+        raise ValueError("several position axes need positions")
+    return _Rotation(table.data_ptr(), table.shape[0], positions.data_ptr() if positions is not None else None, stride,
+                     2 * half, axes, (ctypes.c_int32 * 4)(*sections), int(bool(interleaved)))
+
+
+def rope_table(positions: int, rot_dims: int, base: float = 10000.0, device=None) -> torch.Tensor:
+    """A rotation table fp32 [positions, rot_dims / 2, 2]: cos and sin of p * base ** (-2 j / rot_dims),
+    taken in 64 bits (a far position's angle needs them).  A program makes it once."""
+    j = torch.arange(rot_dims // 2, dtype=torch.float64, device=device)
+    p = torch.arange(positions, dtype=torch.float64, device=device)
+    a = p[:, None] * base ** (-2.0 * j / rot_dims)
+    return torch.stack([a.cos(), a.sin()], dim=-1).float()
+
+
+def sdpa_rope(x: torch.Tensor, table: torch.Tensor, positions: torch.Tensor, *,
+              sections: Optional[Sequence[int]] = None, interleaved: bool = False, inverse: bool = False,
+              out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+              stream=None) -> torch.Tensor:
+    """out[T, H, D] = the rows x turned by the angles of their positions.
+
+    x: bf16 [T, H, D] (inner stride 1; ``out`` may be x).  table: fp32 [P, pairs, 2] (cos, sin), the
+    first 2 * pairs dims are turned.  positions: int32 [T], or [axes, T] with ``sections`` = the
+    number of pairs of each axis (for example time, height and width).  Pairs are dims
+    (j, j + pairs), or (2j, 2j + 1) when ``interleaved``.  ``inverse`` turns the other way: the
+    gradient.  Rows with a position outside the table are 0 and set ROPE_BAD_POS in ``status``."""
+    _check_rows("x", x)
+    T, H, D = x.shape
+    if positions is None:
+        raise ValueError("positions must be given")
+    rot = _rotation(table, positions, sections, interleaved, T)
+    if out is not None:
+        _check_rows("out", out, H, D, T)
+    dev = _same_device(x, table, positions, out, status)
+    if out is None:
+        out = _empty((T, H, D), torch.bfloat16, dev, stream)
+    _run(library().sdpa_rope, dev, stream, x.data_ptr(), T, H, D, x.stride(0), x.stride(1), rot, int(bool(inverse)),
+         out.data_ptr(), out.stride(0), out.stride(1), _status_ptr(status))
+    return out
+
+
+class Q4Store(NamedTuple):
+    """A 4-bit column store: uint8 codes [cols, Hkv, rows, D / 2] and scales [cols, Hkv, rows, D / 32]
+    of the keys, then of the values.  Nibble c (byte i: dim 2i low, dim 2i + 1 high) under scale byte b
+    stands for (c - 8) * 2**((b >> 3) - 21) * (1 + (b & 7) / 8)."""
+    k_codes: torch.Tensor
+    k_scales: torch.Tensor
+    v_codes: torch.Tensor
+    v_scales: torch.Tensor
+
+
+def q4_store(rows: int, cols: int, Hkv: int, D: int, device=None) -> Q4Store:
+    """An empty 4-bit store (every value 0); rows a multiple of 16."""
+    if rows <= 0 or rows % 16 or cols <= 0 or Hkv <= 0 or D not in (64, 128, 256):
+        raise ValueError("rows must be a multiple of 16, D 64, 128 or 256")
+    codes = lambda: torch.full((cols, Hkv, rows, D // 2), 0x88, dtype=torch.uint8, device=device)  # noqa: E731
+    scales = lambda: torch.zeros((cols, Hkv, rows, D // 32), dtype=torch.uint8, device=device)  # noqa: E731
+    return Q4Store(codes(), scales(), codes(), scales())
+
+
+def _check_q4(store: Q4Store):
+    """(rows, cols, Hkv, D, pointers) of a 4-bit store."""
+    kc, ks, vc, vs = store
+    if kc.dim() != 4 or kc.shape != vc.shape or ks.shape != vs.shape or \
+            tuple(ks.shape) != tuple(kc.shape[:3]) + (kc.shape[3] // 16,):
+        raise ValueError("a 4-bit store is codes [cols, Hkv, rows, D / 2] and scales [cols, Hkv, rows, D / 32], twice")
+    for t in store:
+        if t.dtype != torch.uint8 or not t.is_contiguous():
+            raise ValueError("a 4-bit store's tensors must be contiguous uint8")
+    cols, Hkv, rows, half = kc.shape
+    return rows, cols, Hkv, 2 * half, _Q4Pointers(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr())
+
+
+def _rope_append(q, k_new, v_new, store_tensors, rows, cols, Hkv, D, seq_info, table, positions, sections,
+                 interleaved, window, seg_mode, q_out, status, stream, entry, store_args):
+    _check_rows("q", q)
+    T, Hq, Dq = q.shape
+    if Dq != D:
+        raise ValueError("head dims of q and the store differ")
+    _check_rows("k_new", k_new, Hkv, D, T)
+    _check_rows("v_new", v_new, Hkv, D, T)
+    S = _check_table(seq_info, seg_mode)
+    rot = _rotation(table, positions, sections, interleaved, T)
+    if q_out is not None:
+        _check_rows("q_out", q_out, Hq, D, T)
+    dev = _same_device(q, k_new, v_new, *store_tensors, seq_info, table, positions, seg_mode, q_out, status)
+    if q_out is None:
+        q_out = _empty((T, Hq, D), torch.bfloat16, dev, stream)
+    _run(entry, dev, stream, q.data_ptr(), q.stride(0), q.stride(1), k_new.data_ptr(), k_new.stride(0),
+         k_new.stride(1), v_new.data_ptr(), v_new.stride(0), v_new.stride(1), T, Hq, Hkv, D, rot, *store_args, rows,
+         cols, seq_info.data_ptr() if S else None, seg_mode.data_ptr() if S and seg_mode is not None else None, S,
+         int(window), q_out.data_ptr(), q_out.stride(0), q_out.stride(1), _status_ptr(status))
+    return q_out
+
+
+def sdpa_rope_append(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, k_store: torch.Tensor,
+                     v_store: torch.Tensor, seq_info: torch.Tensor, table: torch.Tensor, *,
+                     positions: Optional[torch.Tensor] = None, sections: Optional[Sequence[int]] = None,
+                     interleaved: bool = False, window: int = 0, seg_mode: Optional[torch.Tensor] = None,
+                     q_out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """A step's rows on their way to ``sdpa_varlen``: returns the rotated queries; rotated keys and
+    the values go into the bf16 column stores (in place).
+
+    q: bf16 [T, Hq, D]; k_new, v_new: bf16 [T, Hkv, D], each with its own strides.  The rotation is
+    ``sdpa_rope``'s; with ``positions`` None a row's position is its place in its sequence.
+    ``window`` / ``seg_mode``: as for the attention that follows (they decide which segments are
+    valid).  Rows of no live segment: q_out 0, nothing stored."""
+    if k_store.dim() != 4 or k_store.shape != v_store.shape:
+        raise ValueError("the stores must both be [rows, cols, Hkv, D]")
+    for name, t in (("k_store", k_store), ("v_store", v_store)):
+        if t.dtype != torch.bfloat16 or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous bf16")
+    rows, cols, Hkv, D = k_store.shape
+    return _rope_append(q, k_new, v_new, (k_store, v_store), rows, cols, Hkv, D, seq_info, table, positions, sections,
+                        interleaved, window, seg_mode, q_out, status, stream, library().sdpa_rope_append,
+                        (k_store.data_ptr(), v_store.data_ptr()))
+
+
+def sdpa_rope_append_q4(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, store: Q4Store,
+                        seq_info: torch.Tensor, table: torch.Tensor, *, positions: Optional[torch.Tensor] = None,
+                        sections: Optional[Sequence[int]] = None, interleaved: bool = False, window: int = 0,
+                        seg_mode: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                        status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """``sdpa_rope_append`` into a 4-bit store, for ``sdpa_varlen_q4``: the rotated keys, rounded to
+    bf16, and the values take their 4 bits on the way."""
+    rows, cols, Hkv, D, ptrs = _check_q4(store)
+    return _rope_append(q, k_new, v_new, store, rows, cols, Hkv, D, seq_info, table, positions, sections, interleaved,
+                        window, seg_mode, q_out, status, stream, library().sdpa_rope_append_fourbit, (ptrs,))
+
+
+def sdpa_q4_unpack(store: Q4Store, seq_info: torch.Tensor, T: int, *, window: int = 0,
+                   seg_mode: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                   v_out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
+    """(k, v) bf16 [T, Hkv, D]: the rows of a segment table as a 4-bit store holds them (exact).
+    Row i of a live segment is position kv_end - q_len + i; other rows are 0."""
+    rows, cols, Hkv, D, ptrs = _check_q4(store)
+    S = _check_table(seq_info, seg_mode)
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is not None:
+            _check_rows(name, t, Hkv, D, T)
+    dev = _same_device(*store, seq_info, seg_mode, k_out, v_out, status)
+    k_out = _empty((T, Hkv, D), torch.bfloat16, dev, stream) if k_out is None else k_out
+    v_out = _empty((T, Hkv, D), torch.bfloat16, dev, stream) if v_out is None else v_out
+    if k_out.stride() != v_out.stride():
+        raise ValueError("k_out and v_out must share strides")
+    _run(library().sdpa_fourbit_unpack, dev, stream, ptrs, rows, cols, Hkv, D, seq_info.data_ptr() if S else None,
+         seg_mode.data_ptr() if S and seg_mode is not None else None, S, int(window), T, k_out.data_ptr(),
+         v_out.data_ptr(), k_out.stride(0), k_out.stride(1), _status_ptr(status))
+    return k_out, v_out
+
+
+def q4_workspace_bytes(T: int, Hq: int, store: Q4Store, S: int) -> int:
+    """Bytes of workspace ``sdpa_varlen_q4`` needs for these sizes, on the current device."""
+    cols, Hkv, rows, half = store.k_codes.shape
+    return int(library().sdpa_varlen_fourbit_workspace_bytes(T, Hq, Hkv, 2 * half, S, rows, cols))
+
+
+def sdpa_varlen_q4(q: torch.Tensor, store: Q4Store, seq_info: torch.Tensor, *, causal: bool, window: int = 0,
+                   seg_mode: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                   out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """``sdpa_varlen`` over a 4-bit store: the attention of the values its codes stand for.
+    ``seg_mode`` (int32 [S, 2] (causal, window) per segment) replaces causal and window."""
+    _check_rows("q", q)
+    T, Hq, D = q.shape
+    rows, cols, Hkv, Ds, ptrs = _check_q4(store)
+    if Ds != D:
+        raise ValueError("head dims of q and the store differ")
+    S = _check_table(seq_info, seg_mode)
+    if out is not None:
+        _check_rows("out", out, Hq, D, T)
+    dev = _same_device(q, *store, seq_info, seg_mode, out, workspace, status)
+    if out is None:
+        out = _empty((T, Hq, D), torch.bfloat16, dev, stream)
+    lib = library()
+    if workspace is None:
+        with torch.cuda.device(dev):
+            need = lib.sdpa_varlen_fourbit_workspace_bytes(T, Hq, Hkv, D, S, rows, cols)
+        workspace = _empty(max(int(need), 256), torch.uint8, dev, stream)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _run(lib.sdpa_varlen_fourbit, dev, stream, q.data_ptr(), T, Hq, D, q.stride(0), q.stride(1), ptrs, rows, cols, Hkv,
+         seq_info.data_ptr() if S else None, seg_mode.data_ptr() if S and seg_mode is not None else None, S,
+         int(bool(causal)), int(window), float(1.0 / math.sqrt(D) if scale is None else scale), out.data_ptr(),
+         out.stride(0), out.stride(1), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+         _status_ptr(status))
     return out

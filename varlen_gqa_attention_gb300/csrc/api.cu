@@ -14,6 +14,7 @@
 #include <cudaTypedefs.h>
 
 #include "common.cuh"
+#include "q4.cuh"
 
 namespace sdpa {
 
@@ -33,7 +34,7 @@ static cudaError_t mark(int i, cudaStream_t st) {
 }
 static std::atomic<int> g_policy{SDPA_ROUTE_AUTO};
 
-static sdpa_status fail(sdpa_status code, const char* fmt, ...) {
+sdpa_status fail(sdpa_status code, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
   vsnprintf(g_err, sizeof(g_err), fmt, ap);
@@ -50,6 +51,7 @@ struct DevInfo {
   bool ready = false;
   int sms = 0;
   int splitk_per_sm[3] = {0, 0, 0};  // D = 64, 128, 256
+  int q4_per_sm[3] = {0, 0, 0};
   bool prefill_ok[3] = {false, false, false};
 };
 static std::mutex g_mu;
@@ -91,6 +93,14 @@ static sdpa_status device_info(DevInfo* out) {
       e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, f, kSplitkThreads, smem);
       if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "occupancy: %s", cudaGetErrorString(e));
       di.splitk_per_sm[k] = nb > 0 ? nb : 1;
+      const void* q4 = q4_splitk_kernel_ptr(Ds[k]);
+      e = cudaFuncSetAttribute(q4, cudaFuncAttributeMaxDynamicSharedMemorySize, q4_splitk_smem_bytes(Ds[k]));
+      if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "smem attribute: %s", cudaGetErrorString(e));
+      e = cudaFuncSetAttribute(q4, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+      if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "carveout attribute: %s", cudaGetErrorString(e));
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, q4, kQ4Threads, q4_splitk_smem_bytes(Ds[k]));
+      if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "occupancy: %s", cudaGetErrorString(e));
+      di.q4_per_sm[k] = nb > 0 ? nb : 1;
       e = cudaFuncSetAttribute(combine_kernel_ptr(Ds[k]), cudaFuncAttributePreferredSharedMemoryCarveout, 100);
       if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "carveout attribute: %s", cudaGetErrorString(e));
       const void* pf = prefill_kernel_ptr(Ds[k]);
@@ -153,9 +163,9 @@ static bool make_tensor_maps(const void* q, int64_t T, int Hq, int D, int64_t q_
 struct Grids {
   int64_t splitk, prefill;
 };
-static Grids grids_for(const DevInfo& di, int D) {
+static Grids grids_for(const DevInfo& di, int D, bool q4 = false) {
   Grids g;
-  g.splitk = (int64_t)di.sms * di.splitk_per_sm[d_index(D)];
+  g.splitk = (int64_t)di.sms * (q4 ? di.q4_per_sm : di.splitk_per_sm)[d_index(D)];
   g.prefill = di.sms;
   return g;
 }
@@ -182,6 +192,15 @@ sdpa_status check_tensors(const void* q, const void* k, const void* v, void* out
     return fail(SDPA_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
   if (q_rs % 8 || q_hs % 8 || o_rs % 8 || o_hs % 8 || q_rs < 0 || q_hs < 0 || o_rs < 0 || o_hs < 0)
     return fail(SDPA_ERR_STRIDE, "row/head strides must be non-negative multiples of 8 elements");
+  return SDPA_OK;
+}
+
+sdpa_status check_q4_store(const Q4Store& q4, int64_t rows) {
+  if (!q4.kc || !q4.ks || !q4.vc || !q4.vs) return fail(SDPA_ERR_NULL, "a 4-bit store pointer is NULL");
+  if (!aligned16(q4.kc) || !aligned16(q4.ks) || !aligned16(q4.vc) || !aligned16(q4.vs))
+    return fail(SDPA_ERR_ALIGN, "4-bit store pointers must be 16-byte aligned");
+  if (rows % kQ4RowAlign)
+    return fail(SDPA_ERR_SHAPE, "a 4-bit store has a multiple of %d rows, not %lld", kQ4RowAlign, (long long)rows);
   return SDPA_OK;
 }
 
@@ -225,7 +244,7 @@ static bool prefill_launch(const SchedArgs& sa, int64_t T) {
 }
 
 static sdpa_status launch_all(const SchedArgs& sa, const AttnArgs& aa, int D, const Grids& g,
-                              const TensorMaps& tm, const AppendArgs* ap, cudaStream_t st) {
+                              const TensorMaps& tm, const AppendArgs* ap, const Q4Store* q4, cudaStream_t st) {
   cudaError_t e = mark(0, st);
   if (e == cudaSuccess) {
     e = launch_sched(sa, st);
@@ -269,7 +288,12 @@ static sdpa_status launch_all(const SchedArgs& sa, const AttnArgs& aa, int D, co
     if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "prefill launch: %s", cudaGetErrorString(e));
   }
   if (e == cudaSuccess) e = mark(2, st);
-  if (e == cudaSuccess) {
+  if (e == cudaSuccess && q4) {
+    Q4AttnArgs ga{aa, *q4};
+    void* args[] = {(void*)&ga};
+    e = launch_k(q4_splitk_kernel_ptr(D), (unsigned)g.splitk, kQ4Threads, args, q4_splitk_smem_bytes(D), st, true);
+    if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "4-bit split-K launch: %s", cudaGetErrorString(e));
+  } else if (e == cudaSuccess) {
     void* args[] = {(void*)&aa};
     e = launch_k(splitk_kernel_ptr(D), (unsigned)g.splitk, kSplitkThreads, args, splitk_smem_bytes(D), st, true);
     if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "split-K launch: %s", cudaGetErrorString(e));
@@ -292,10 +316,12 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
                        const int32_t* seq_info, int S, const int32_t* inl, int causal, int window,
                        float scale, void* out, int64_t o_rs, int64_t o_hs, void* ws, size_t ws_bytes,
                        int32_t* status_dev, void* stream, const AppendArgs* ap = nullptr,
-                       const int32_t* seg_mode = nullptr) {
+                       const int32_t* seg_mode = nullptr, const Q4Store* q4 = nullptr) {
   g_err[0] = 0;
   sdpa_status st = check_common(T, Hq, Hkv, D, S, rows, cols, window, scale);
   if (st) return st;
+  if (q4 && (st = check_q4_store(*q4, rows))) return st;
+  if (q4 && T == 0) return SDPA_OK;
   // the dense entry passes its one segment by value: no table pointer to check
   if ((st = check_tensors(q, k, v, out, seq_info, inl ? 0 : S, q_rs, q_hs, o_rs, o_hs))) return st;
   if (!ws) return fail(SDPA_ERR_WORKSPACE, "workspace is NULL");
@@ -304,7 +330,7 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
 
   DevInfo di;
   if ((st = device_info(&di))) return st;
-  const Grids g = grids_for(di, D);
+  const Grids g = grids_for(di, D, q4 != nullptr);
   Workspace W;
   const size_t need = layout_workspace((char*)ws, T, Hq, Hkv, D, S, g.splitk, g.prefill, &W);
   if (ws_bytes < need)
@@ -330,7 +356,8 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
   const int group = Hq / Hkv;
   const bool group_fits = group <= kPrefillRows && (kPrefillRows % group) == 0;
   sa.tile_pf = prefill_tile_keys(D);
-  sa.prefill_ok = di.prefill_ok[d_index(D)] && group_fits && prefill_launch(sa, T) &&
+  sa.lo_align = q4 ? kQ4RowAlign : 1;
+  sa.prefill_ok = !q4 && di.prefill_ok[d_index(D)] && group_fits && prefill_launch(sa, T) &&
                   make_tensor_maps(q, T, Hq, D, q_rs, q_hs, k, v, rows, cols, Hkv, group, sa.tile_pf,
                                    &tm.q, &tm.k, &tm.v);
   sa.grid[0] = 0;
@@ -365,7 +392,7 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
     apw = *ap;
     apw.segs = W.segs;
   }
-  return launch_all(sa, aa, D, g, tm, ap ? &apw : nullptr, (cudaStream_t)stream);
+  return launch_all(sa, aa, D, g, tm, ap ? &apw : nullptr, q4, (cudaStream_t)stream);
 }
 
 }  // namespace sdpa
@@ -439,6 +466,36 @@ sdpa_status sdpa_varlen_modes(const void* q, int64_t T, int Hq, int D, int64_t q
   return run(q, T, Hq, D, q_row_stride, q_head_stride, k_store, v_store, rows, cols, Hkv, seq_info,
              S, nullptr, 1, 0, scale, out, o_row_stride, o_head_stride, workspace, ws_bytes,
              status_dev, stream, nullptr, seg_mode);
+}
+
+size_t sdpa_varlen_fourbit_workspace_bytes(int64_t T, int Hq, int Hkv, int D, int S, int64_t rows, int cols) {
+  if (T < 0 || S < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || rows <= 0 || cols <= 0) return 0;
+  if (D != 64 && D != 128 && D != 256) return 0;
+  DevInfo di;
+  Grids g;
+  if (device_info(&di) == SDPA_OK) {
+    g = grids_for(di, D, true);
+  } else {
+    g.splitk = 4096;  // no device: a bound above any real grid
+    g.prefill = 1024;
+    g_err[0] = 0;
+  }
+  return layout_workspace(nullptr, T, Hq, Hkv, D, S, g.splitk, g.prefill, nullptr);
+}
+
+sdpa_status sdpa_varlen_fourbit(const void* q, int64_t T, int Hq, int D, int64_t q_row_stride, int64_t q_head_stride,
+                           const sdpa_q4_store* store, int64_t rows, int cols, int Hkv, const int32_t* seq_info,
+                           const int32_t* seg_mode, int S, int causal, int window, float scale, void* out,
+                           int64_t o_row_stride, int64_t o_head_stride, void* workspace, size_t ws_bytes,
+                           int32_t* status_dev, void* stream) {
+  g_err[0] = 0;
+  if (!store) return fail(SDPA_ERR_NULL, "store is NULL");
+  // the running maximum is taken over unscaled scores
+  if (scale < 0.f) return fail(SDPA_ERR_ARG, "scale %g < 0", (double)scale);
+  const Q4Store q4{store->k_codes, store->k_scales, store->v_codes, store->v_scales};
+  return run(q, T, Hq, D, q_row_stride, q_head_stride, q4.kc, q4.vc, rows, cols, Hkv, seq_info, S, nullptr, causal,
+             window, scale, out, o_row_stride, o_head_stride, workspace, ws_bytes, status_dev, stream, nullptr,
+             seg_mode, &q4);
 }
 
 sdpa_status sdpa_seq_clone(void* k_store, void* v_store, int64_t rows, int cols, int Hkv, int D,

@@ -213,6 +213,7 @@ struct SchedArgs {
   int policy;      // SDPA_ROUTE_*
   int prefill_ok;  // prefill kernel usable for this call (group divides 128, tensor maps made)
   int tile_pf;     // keys per prefill tile
+  int lo_align;    // split-K units' key ranges begin at a multiple of this (a power of two, at least 1)
   int64_t grid[3];
   Workspace ws;
   int32_t* status_dev;
@@ -248,8 +249,9 @@ int prefill_pair_block_threads(int D);
 int prefill_smem_bytes(int D);
 int prefill_tile_keys(int D);
 int prefill_block_threads(int D);
-// Sets the message sdpa_last_error() returns on this thread.
+// Sets the message sdpa_last_error() returns on this thread; fail() formats it and returns `code`.
 void set_last_error(const char* msg);
+sdpa_status fail(sdpa_status code, const char* fmt, ...);
 // Argument checks shared by the attention entry points (api.cu); each sets the message of
 // sdpa_last_error() and returns its code, SDPA_OK when the arguments pass.
 sdpa_status check_common(int64_t T, int Hq, int Hkv, int D, int S, int64_t rows, int cols, int window,

@@ -135,6 +135,7 @@ extern "C" sdpa_status sdpa_varlen_splitk_static(
   sa.policy = SDPA_ROUTE_SPLITK;
   sa.prefill_ok = 0;
   sa.tile_pf = kPrefillTile;
+  sa.lo_align = 1;
   sa.grid[0] = 0;
   sa.grid[1] = grid;
   sa.grid[2] = 0;

@@ -209,6 +209,8 @@ __device__ __forceinline__ UnitRec make_unit(const SchedArgs& A, int s, const Se
   const RowWin w1 = row_window(i1, g.q_len, g.kv_end, g.causal, g.window);
   ur.lo = w0.lo;  // lo and hi grow with the query row
   ur.hi = max(w1.hi, w0.lo);
+  // (keys added below a unit's first are masked like any other that a row does not see)
+  if (q == kRouteSplitk && ur.hi > ur.lo) ur.lo &= -A.lo_align;
   // key tiles: the prefill kernel's stop at a ring wrap (two TMA ranges), the split-K
   // kernel's wrap per row
   const int64_t nt = q == kRoutePrefill ? key_tiles(ur.lo, ur.hi, A.rows, tl).n

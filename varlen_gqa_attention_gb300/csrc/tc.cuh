@@ -283,6 +283,11 @@ __device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
   return __uint_as_float(r);
 }
 
+// Named barrier over `count` threads.
+__device__ __forceinline__ void bar_sync_n(int id, int count) {
+  asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(count) : "memory");
+}
+
 // Named barrier over `count` threads that also ANDs a predicate across them: every
 // participant arrives whatever its own state, so a participant that gave up a wait can
 // never leave its partners blocked here.
