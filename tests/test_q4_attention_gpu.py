@@ -293,3 +293,76 @@ def test_the_bf16_store_agrees_with_the_4_bit_one_on_its_values(dev):
     bf = pkg.sdpa_varlen(q.to(dev), k, v, torch.tensor(seq, dtype=torch.int32, device=dev), causal=True)
     check(got, st, q, store, seq, True)
     check(bf, st, q, store, seq, True, p_step=2.0 ** -8)
+
+
+# ------------------------------------------- the tensor-memory route: columns staged in bf16 first
+
+@pytest.fixture
+def prefill_route():
+    pkg.set_route_policy(pkg.ROUTE_PREFILL)
+    yield
+    pkg.set_route_policy(pkg.ROUTE_AUTO)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_staged_route_small_shapes(dev, prefill_route, D):
+    seq = [[0, 1, 3, 100], [1, 70, 1, 300], [75, 130, 0, 131], [210, 5, 2, 2]]
+    store, q = random_store(304, 4, 2, D, D), queries(218, 4, D, 30)
+    for causal in (True, False):
+        got, st = run_q4(q, store, seq, dev, causal=causal)
+        check(got, st, q, store, seq, causal, p_step=2.0 ** -8)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_staged_route_on_rings(dev, prefill_route, D):
+    rows, window = 272, 150
+    rng = np.random.default_rng(D)
+    seq, t = [], 0
+    for s in range(6):
+        n = int(rng.integers(1, rows - window + 2))
+        seq.append([t, n, s, int(rng.integers(1, 9 * rows))])
+        t += n
+    store, q = random_store(rows, 6, 1, D, rows + D), queries(t, 8, D, 31)
+    got, st = run_q4(q, store, seq, dev, causal=True, window=window)
+    check(got, st, q, store, seq, True, window, p_step=2.0 ** -8)
+    modes = [[s % 2, [window, 40, 1][s % 3]] for s in range(6)]
+    got, st = run_q4(q, store, seq, dev, causal=True, seg_mode=modes)
+    check(got, st, q, store, seq, True, 0, modes, p_step=2.0 ** -8)
+
+
+def test_staged_route_many_segments(dev, prefill_route):
+    # more segments than the small scheduler takes, two of them on one column, some not live
+    seq = [[3 * i, 3, i % 37, 20 + i] for i in range(45)]
+    seq[4][2], seq[9][1] = 99, 5
+    store, q = random_store(80, 40, 1, 64, 32), queries(136, 4, 64, 32)
+    got, st = run_q4(q, store, seq, dev, causal=True)
+    check(got, st, q, store, seq, True, p_step=2.0 ** -8)
+
+
+@pytest.mark.parametrize("S_", [11, 40])
+def test_segments_beyond_the_staged_columns_take_the_other_route(dev, prefill_route, S_):
+    # 2^20 rows of 64 dims are 256 MiB of bf16 K and V a column: eight are staged
+    rows = 1 << 20
+    store = pkg.q4_store(rows, 12, 1, 64, device=dev)
+    small = random_store(320, 12, 1, 64, 33)
+    for big, s in zip(store, small):
+        big[:, :, :320] = s.to(dev)
+    q = queries(9 * S_, 8, 64, 33)
+    seq = [[9 * i, 8 + (i % 2), (5 * i) % 12, 300 - 7 * (i % 40)] for i in range(S_)]
+    seq[2][1] = 0
+    seqd = torch.tensor(seq, dtype=torch.int32, device=dev)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    got = pkg.sdpa_varlen_q4(q.to(dev), store, seqd, causal=True, status=status)
+    check(got, int(status), q, small, seq, True, p_step=2.0 ** -8)
+
+
+def test_a_long_chunk_beside_single_tokens(dev):
+    # automatic routing: the chunk goes through staged columns, the tokens do not
+    store = random_store(4096, 4, 2, 128, 34)
+    seq = [[0, 1, 3, 4096], [1, 700, 1, 4090], [701, 1, 0, 77], [705, 300, 2, 301]]
+    q = queries(1006, 8, 128, 34)
+    rows = [0, 1, 2, 128, 333, 700, 701, 702, 704, 705, 706, 900, 1004, 1005]
+    got, st = run_q4(q, store, seq, dev, causal=True)
+    check(got, st, q, store, seq, True, p_step=2.0 ** -8, rows_subset=rows)
+    got, st = run_q4(q, store, seq, dev, causal=True, window=100)
+    check(got, st, q, store, seq, True, 100, p_step=2.0 ** -8, rows_subset=rows)

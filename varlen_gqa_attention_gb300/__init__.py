@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from typing import NamedTuple, Optional, Sequence
 
 import torch
@@ -53,15 +54,9 @@ class SdpaError(RuntimeError):
         self.code = code
 
 
-class _Rotation(ctypes.Structure):
-    _fields_ = [("table", ctypes.c_void_p), ("table_rows", ctypes.c_int64), ("positions", ctypes.c_void_p),
-                ("pos_stride", ctypes.c_int64), ("rot_dims", ctypes.c_int32), ("axes", ctypes.c_int32),
-                ("sections", ctypes.c_int32 * 4), ("interleaved", ctypes.c_int32)]
-
-
-class _Q4Pointers(ctypes.Structure):
-    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
-                ("v_scales", ctypes.c_void_p)]
+# the C structs sdpa_rotation and sdpa_q4_store, packed (their padding included) as bytes
+_ROTATION = struct.Struct("@PqPq7i4x")
+_Q4_POINTERS = struct.Struct("@4P")
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -114,7 +109,7 @@ def library(build_if_missing: bool = True) -> ctypes.CDLL:
                                               c_vp]
     lib.sdpa_workspace_status.restype = c_int
     lib.sdpa_workspace_status.argtypes = [c_vp, ctypes.c_size_t, ctypes.POINTER(ctypes.c_int32), c_vp]
-    c_rot, c_q4 = ctypes.POINTER(_Rotation), ctypes.POINTER(_Q4Pointers)
+    c_rot = c_q4 = c_vp  # packed structs (_ROTATION, _Q4_POINTERS)
     lib.sdpa_rope.restype = c_int
     lib.sdpa_rope.argtypes = [c_vp, c_i64, c_int, c_int, c_i64, c_i64, c_rot, c_int, c_vp, c_i64, c_i64, c_vp, c_vp]
     step = [c_vp, c_i64, c_i64] * 3 + [c_i64, c_int, c_int, c_int, c_rot]  # q, k_new, v_new, sizes, rotation
@@ -382,93 +377,105 @@ def sdpa_varlen_splitk_static(q: torch.Tensor, k_store: torch.Tensor, v_store: t
 
 
 # ------------------------------------------------ rotary positions and the 4-bit column store
+#
+# A decode step calls these once a layer and its kernels take a few microseconds, so the checks read
+# each tensor's attributes once and the device and stream come as plain numbers.
 
-def _same_device(*tensors) -> torch.device:
-    """The one CUDA device of the tensors given (None passes)."""
-    dev = None
+_bf16, _i32, _u8 = torch.bfloat16, torch.int32, torch.uint8
+
+
+def _device_of(*tensors) -> int:
+    """Index of the one CUDA device that every tensor given is on (None passes)."""
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda or (dev is not None and t.device != dev):
+        if t is not None and t.get_device() != dev:
             raise ValueError("every tensor must be on the same CUDA device")
-        dev = t.device
+    if dev < 0:
+        raise ValueError("every tensor must be on a CUDA device")
     return dev
 
 
-def _run(entry, device: torch.device, stream, *args) -> None:
-    """Calls a C entry with `device` current and its stream (the given one, else the device's
+def _call(entry, dev: int, stream, *args) -> None:
+    """Calls a C entry with device `dev` current and its stream (the given one, else the device's
     current one) as the last argument."""
-    if stream is not None and stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-    handle = (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
-    if torch.cuda.current_device() == device.index:
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device_index != dev:
+        raise ValueError(f"the stream is on device {stream.device_index}, the tensors on {dev}")
+    else:
+        handle = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
         code = entry(*args, handle)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(dev):
             code = entry(*args, handle)
     if code != SDPA_OK:
         _check(code)
 
 
-def _empty(shape, dtype, device, stream) -> torch.Tensor:
-    """An uninitialised tensor whose memory belongs to the stream that will write it."""
+def _rows_like(like: torch.Tensor, shape, stream) -> torch.Tensor:
+    """Uninitialised bf16 rows on `like`'s device, of memory that belongs to the stream that will
+    write them."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=_bf16, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=_bf16, device=like.device)
 
 
-def _check_rows(name: str, t: torch.Tensor, H: Optional[int] = None, D: Optional[int] = None,
-                T: Optional[int] = None) -> None:
-    if t.dim() != 3 or t.dtype != torch.bfloat16 or t.stride(2) != 1:
-        raise ValueError(f"{name} must be bf16 [T, heads, D] with unit inner stride")
-    if (T is not None and t.shape[0] != T) or (H is not None and t.shape[1] != H) or \
-            (D is not None and t.shape[2] != D):
-        raise ValueError(f"{name} must be [{T}, {H}, {D}], not {list(t.shape)}")
+def _strides(name: str, t: torch.Tensor, shape=None):
+    """Row and head strides of bf16 rows [T, heads, D], checked against `shape` when it is given."""
+    if t.dim() != 3 or t.dtype != _bf16:
+        raise ValueError(f"{name} must be bf16 [T, heads, D], not {t.dtype} {list(t.shape)}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+    rs, hs, inner = t.stride()
+    if inner != 1:
+        raise ValueError(f"{name} must have unit inner stride")
+    return rs, hs
 
 
 def _status_ptr(status: Optional[torch.Tensor]):
     if status is None:
         return None
-    if status.dtype != torch.int32 or status.numel() < 1:
+    if status.dtype != _i32 or status.numel() < 1:
         raise ValueError("status must be an int32 tensor")
     return status.data_ptr()
 
 
-def _check_table(seq_info: torch.Tensor, seg_mode: Optional[torch.Tensor]) -> int:
-    """Checks a segment table and its modes; returns the number of segments."""
-    if seq_info.dtype != torch.int32 or not seq_info.is_contiguous() or \
-            (seq_info.numel() and (seq_info.dim() != 2 or seq_info.shape[1] != 4)):
+def _table(seq_info: torch.Tensor, seg_mode: Optional[torch.Tensor]):
+    """(seq_info pointer, seg_mode pointer, segments) of a segment table."""
+    S = seq_info.shape[0] if seq_info.dim() else 0
+    if seq_info.dtype != _i32 or not seq_info.is_contiguous() or (seq_info.numel() and
+                                                                  (seq_info.dim() != 2 or seq_info.shape[1] != 4)):
         raise ValueError("seq_info must be a contiguous int32 [S, 4] tensor")
-    S = seq_info.shape[0] if seq_info.numel() else 0
-    if seg_mode is not None and (seg_mode.dtype != torch.int32 or not seg_mode.is_contiguous()
-                                 or (S and tuple(seg_mode.shape) != (S, 2))):
-        raise ValueError("seg_mode must be a contiguous int32 [S, 2] tensor")
-    return S
+    if seg_mode is not None:
+        if seg_mode.dtype != _i32 or not seg_mode.is_contiguous() or (S and tuple(seg_mode.shape) != (S, 2)):
+            raise ValueError("seg_mode must be a contiguous int32 [S, 2] tensor")
+    if not S or not seq_info.numel():
+        return None, None, 0
+    return seq_info.data_ptr(), None if seg_mode is None else seg_mode.data_ptr(), S
 
 
 def _rotation(table: torch.Tensor, positions: Optional[torch.Tensor], sections: Optional[Sequence[int]],
-              interleaved: bool, T: int) -> _Rotation:
+              interleaved: bool, T: int) -> bytes:
     if table.dim() != 3 or table.shape[2] != 2 or table.dtype != torch.float32 or not table.is_contiguous():
         raise ValueError("table must be contiguous fp32 [positions, rotated pairs, 2]")
-    half = table.shape[1]
+    P, half, _ = table.shape
     sections = (half,) if sections is None else tuple(sections)
     axes = len(sections)
     if not 1 <= axes <= 4:
         raise ValueError(f"sections has {axes} position axes: 1 to 4")
-    stride = 0
+    ptr = stride = 0
     if positions is not None:
-        if positions.dtype != torch.int32:
-            raise ValueError("positions must be int32")
-        if positions.dim() == 1 and axes == 1:
-            positions = positions.unsqueeze(0)
-        if positions.dim() != 2 or tuple(positions.shape) != (axes, T) or (T > 1 and positions.stride(1) != 1):
+        shape = positions.shape
+        if positions.dtype != _i32 or not (shape == (axes, T) or (axes == 1 and shape == (T,))) or \
+                (T > 1 and positions.stride(-1) != 1):
             raise ValueError(f"positions must be int32 [{axes}, {T}] with unit inner stride")
-        stride = positions.stride(0)
+        ptr, stride = positions.data_ptr(), positions.stride(0) if axes > 1 else 0
     elif axes > 1:
         raise ValueError("several position axes need positions")
-    return _Rotation(table.data_ptr(), table.shape[0], positions.data_ptr() if positions is not None else None, stride,
-                     2 * half, axes, (ctypes.c_int32 * 4)(*sections), int(bool(interleaved)))
+    return _ROTATION.pack(table.data_ptr(), P, ptr, stride, 2 * half, axes, *sections, *(0,) * (4 - axes),
+                          1 if interleaved else 0)
 
 
 def rope_table(positions: int, rot_dims: int, base: float = 10000.0, device=None) -> torch.Tensor:
@@ -491,18 +498,18 @@ def sdpa_rope(x: torch.Tensor, table: torch.Tensor, positions: torch.Tensor, *,
     number of pairs of each axis (for example time, height and width).  Pairs are dims
     (j, j + pairs), or (2j, 2j + 1) when ``interleaved``.  ``inverse`` turns the other way: the
     gradient.  Rows with a position outside the table are 0 and set ROPE_BAD_POS in ``status``."""
-    _check_rows("x", x)
-    T, H, D = x.shape
+    rs, hs = _strides("x", x)
+    shape = x.shape
+    T, H, D = shape
     if positions is None:
         raise ValueError("positions must be given")
     rot = _rotation(table, positions, sections, interleaved, T)
-    if out is not None:
-        _check_rows("out", out, H, D, T)
-    dev = _same_device(x, table, positions, out, status)
+    dev = _device_of(x, table, positions, out, status)
     if out is None:
-        out = _empty((T, H, D), torch.bfloat16, dev, stream)
-    _run(library().sdpa_rope, dev, stream, x.data_ptr(), T, H, D, x.stride(0), x.stride(1), rot, int(bool(inverse)),
-         out.data_ptr(), out.stride(0), out.stride(1), _status_ptr(status))
+        out = _rows_like(x, shape, stream)
+    ors, ohs = _strides("out", out, shape)
+    _call(library().sdpa_rope, dev, stream, x.data_ptr(), T, H, D, rs, hs, rot, 1 if inverse else 0, out.data_ptr(),
+          ors, ohs, _status_ptr(status))
     return out
 
 
@@ -520,43 +527,43 @@ def q4_store(rows: int, cols: int, Hkv: int, D: int, device=None) -> Q4Store:
     """An empty 4-bit store (every value 0); rows a multiple of 16."""
     if rows <= 0 or rows % 16 or cols <= 0 or Hkv <= 0 or D not in (64, 128, 256):
         raise ValueError("rows must be a multiple of 16, D 64, 128 or 256")
-    codes = lambda: torch.full((cols, Hkv, rows, D // 2), 0x88, dtype=torch.uint8, device=device)  # noqa: E731
-    scales = lambda: torch.zeros((cols, Hkv, rows, D // 32), dtype=torch.uint8, device=device)  # noqa: E731
+    codes = lambda: torch.full((cols, Hkv, rows, D // 2), 0x88, dtype=_u8, device=device)  # noqa: E731
+    scales = lambda: torch.zeros((cols, Hkv, rows, D // 32), dtype=_u8, device=device)  # noqa: E731
     return Q4Store(codes(), scales(), codes(), scales())
 
 
-def _check_q4(store: Q4Store):
-    """(rows, cols, Hkv, D, pointers) of a 4-bit store."""
+def _q4(store: Q4Store):
+    """(rows, cols, Hkv, D, packed pointers) of a 4-bit store."""
     kc, ks, vc, vs = store
-    if kc.dim() != 4 or kc.shape != vc.shape or ks.shape != vs.shape or \
-            tuple(ks.shape) != tuple(kc.shape[:3]) + (kc.shape[3] // 16,):
+    shape = kc.shape
+    if len(shape) != 4 or vc.shape != shape or ks.shape != vs.shape or \
+            ks.shape != (shape[0], shape[1], shape[2], shape[3] // 16):
         raise ValueError("a 4-bit store is codes [cols, Hkv, rows, D / 2] and scales [cols, Hkv, rows, D / 32], twice")
     for t in store:
-        if t.dtype != torch.uint8 or not t.is_contiguous():
+        if t.dtype != _u8 or not t.is_contiguous():
             raise ValueError("a 4-bit store's tensors must be contiguous uint8")
-    cols, Hkv, rows, half = kc.shape
-    return rows, cols, Hkv, 2 * half, _Q4Pointers(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr())
+    cols, Hkv, rows, half = shape
+    return rows, cols, Hkv, 2 * half, _Q4_POINTERS.pack(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr())
 
 
-def _rope_append(q, k_new, v_new, store_tensors, rows, cols, Hkv, D, seq_info, table, positions, sections,
-                 interleaved, window, seg_mode, q_out, status, stream, entry, store_args):
-    _check_rows("q", q)
-    T, Hq, Dq = q.shape
+def _rope_append(entry, q, k_new, v_new, store_tensors, store_args, rows, cols, Hkv, D, seq_info, table, positions,
+                 sections, interleaved, window, seg_mode, q_out, status, stream):
+    qrs, qhs = _strides("q", q)
+    shape = q.shape
+    T, Hq, Dq = shape
     if Dq != D:
         raise ValueError("head dims of q and the store differ")
-    _check_rows("k_new", k_new, Hkv, D, T)
-    _check_rows("v_new", v_new, Hkv, D, T)
-    S = _check_table(seq_info, seg_mode)
+    krs, khs = _strides("k_new", k_new, (T, Hkv, D))
+    vrs, vhs = _strides("v_new", v_new, (T, Hkv, D))
+    seq_ptr, mode_ptr, S = _table(seq_info, seg_mode)
     rot = _rotation(table, positions, sections, interleaved, T)
-    if q_out is not None:
-        _check_rows("q_out", q_out, Hq, D, T)
-    dev = _same_device(q, k_new, v_new, *store_tensors, seq_info, table, positions, seg_mode, q_out, status)
+    dev = _device_of(q, k_new, v_new, *store_tensors, seq_info, table, positions, seg_mode, q_out, status)
     if q_out is None:
-        q_out = _empty((T, Hq, D), torch.bfloat16, dev, stream)
-    _run(entry, dev, stream, q.data_ptr(), q.stride(0), q.stride(1), k_new.data_ptr(), k_new.stride(0),
-         k_new.stride(1), v_new.data_ptr(), v_new.stride(0), v_new.stride(1), T, Hq, Hkv, D, rot, *store_args, rows,
-         cols, seq_info.data_ptr() if S else None, seg_mode.data_ptr() if S and seg_mode is not None else None, S,
-         int(window), q_out.data_ptr(), q_out.stride(0), q_out.stride(1), _status_ptr(status))
+        q_out = _rows_like(q, shape, stream)
+    ors, ohs = _strides("q_out", q_out, shape)
+    _call(entry, dev, stream, q.data_ptr(), qrs, qhs, k_new.data_ptr(), krs, khs, v_new.data_ptr(), vrs, vhs, T, Hq,
+          Hkv, D, rot, *store_args, rows, cols, seq_ptr, mode_ptr, S, int(window), q_out.data_ptr(), ors, ohs,
+          _status_ptr(status))
     return q_out
 
 
@@ -573,15 +580,16 @@ def sdpa_rope_append(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, 
     ``sdpa_rope``'s; with ``positions`` None a row's position is its place in its sequence.
     ``window`` / ``seg_mode``: as for the attention that follows (they decide which segments are
     valid).  Rows of no live segment: q_out 0, nothing stored."""
-    if k_store.dim() != 4 or k_store.shape != v_store.shape:
+    shape = k_store.shape
+    if len(shape) != 4 or v_store.shape != shape:
         raise ValueError("the stores must both be [rows, cols, Hkv, D]")
     for name, t in (("k_store", k_store), ("v_store", v_store)):
-        if t.dtype != torch.bfloat16 or not t.is_contiguous():
+        if t.dtype != _bf16 or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous bf16")
-    rows, cols, Hkv, D = k_store.shape
-    return _rope_append(q, k_new, v_new, (k_store, v_store), rows, cols, Hkv, D, seq_info, table, positions, sections,
-                        interleaved, window, seg_mode, q_out, status, stream, library().sdpa_rope_append,
-                        (k_store.data_ptr(), v_store.data_ptr()))
+    rows, cols, Hkv, D = shape
+    return _rope_append(library().sdpa_rope_append, q, k_new, v_new, (k_store, v_store),
+                        (k_store.data_ptr(), v_store.data_ptr()), rows, cols, Hkv, D, seq_info, table, positions,
+                        sections, interleaved, window, seg_mode, q_out, status, stream)
 
 
 def sdpa_rope_append_q4(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, store: Q4Store,
@@ -591,9 +599,9 @@ def sdpa_rope_append_q4(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tenso
                         status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """``sdpa_rope_append`` into a 4-bit store, for ``sdpa_varlen_q4``: the rotated keys, rounded to
     bf16, and the values take their 4 bits on the way."""
-    rows, cols, Hkv, D, ptrs = _check_q4(store)
-    return _rope_append(q, k_new, v_new, store, rows, cols, Hkv, D, seq_info, table, positions, sections, interleaved,
-                        window, seg_mode, q_out, status, stream, library().sdpa_rope_append_fourbit, (ptrs,))
+    rows, cols, Hkv, D, ptrs = _q4(store)
+    return _rope_append(library().sdpa_rope_append_fourbit, q, k_new, v_new, store, (ptrs,), rows, cols, Hkv, D,
+                        seq_info, table, positions, sections, interleaved, window, seg_mode, q_out, status, stream)
 
 
 def sdpa_q4_unpack(store: Q4Store, seq_info: torch.Tensor, T: int, *, window: int = 0,
@@ -601,26 +609,27 @@ def sdpa_q4_unpack(store: Q4Store, seq_info: torch.Tensor, T: int, *, window: in
                    v_out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
     """(k, v) bf16 [T, Hkv, D]: the rows of a segment table as a 4-bit store holds them (exact).
     Row i of a live segment is position kv_end - q_len + i; other rows are 0."""
-    rows, cols, Hkv, D, ptrs = _check_q4(store)
-    S = _check_table(seq_info, seg_mode)
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if t is not None:
-            _check_rows(name, t, Hkv, D, T)
-    dev = _same_device(*store, seq_info, seg_mode, k_out, v_out, status)
-    k_out = _empty((T, Hkv, D), torch.bfloat16, dev, stream) if k_out is None else k_out
-    v_out = _empty((T, Hkv, D), torch.bfloat16, dev, stream) if v_out is None else v_out
-    if k_out.stride() != v_out.stride():
+    rows, cols, Hkv, D, ptrs = _q4(store)
+    seq_ptr, mode_ptr, S = _table(seq_info, seg_mode)
+    shape = (T, Hkv, D)
+    dev = _device_of(*store, seq_info, seg_mode, k_out, v_out, status)
+    if k_out is None:
+        k_out = _rows_like(seq_info, shape, stream)
+    if v_out is None:
+        v_out = _rows_like(seq_info, shape, stream)
+    rs, hs = _strides("k_out", k_out, shape)
+    if _strides("v_out", v_out, shape) != (rs, hs):
         raise ValueError("k_out and v_out must share strides")
-    _run(library().sdpa_fourbit_unpack, dev, stream, ptrs, rows, cols, Hkv, D, seq_info.data_ptr() if S else None,
-         seg_mode.data_ptr() if S and seg_mode is not None else None, S, int(window), T, k_out.data_ptr(),
-         v_out.data_ptr(), k_out.stride(0), k_out.stride(1), _status_ptr(status))
+    _call(library().sdpa_fourbit_unpack, dev, stream, ptrs, rows, cols, Hkv, D, seq_ptr, mode_ptr, S, int(window), T,
+          k_out.data_ptr(), v_out.data_ptr(), rs, hs, _status_ptr(status))
     return k_out, v_out
 
 
 def q4_workspace_bytes(T: int, Hq: int, store: Q4Store, S: int) -> int:
-    """Bytes of workspace ``sdpa_varlen_q4`` needs for these sizes, on the current device."""
+    """Bytes of workspace ``sdpa_varlen_q4`` needs for these sizes, on the store's device."""
     cols, Hkv, rows, half = store.k_codes.shape
-    return int(library().sdpa_varlen_fourbit_workspace_bytes(T, Hq, Hkv, 2 * half, S, rows, cols))
+    with torch.cuda.device(store.k_codes.device):
+        return int(library().sdpa_varlen_fourbit_workspace_bytes(T, Hq, Hkv, 2 * half, S, rows, cols))
 
 
 def sdpa_varlen_q4(q: torch.Tensor, store: Q4Store, seq_info: torch.Tensor, *, causal: bool, window: int = 0,
@@ -629,27 +638,23 @@ def sdpa_varlen_q4(q: torch.Tensor, store: Q4Store, seq_info: torch.Tensor, *, c
                    status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """``sdpa_varlen`` over a 4-bit store: the attention of the values its codes stand for.
     ``seg_mode`` (int32 [S, 2] (causal, window) per segment) replaces causal and window."""
-    _check_rows("q", q)
-    T, Hq, D = q.shape
-    rows, cols, Hkv, Ds, ptrs = _check_q4(store)
+    rs, hs = _strides("q", q)
+    shape = q.shape
+    T, Hq, D = shape
+    rows, cols, Hkv, Ds, ptrs = _q4(store)
     if Ds != D:
         raise ValueError("head dims of q and the store differ")
-    S = _check_table(seq_info, seg_mode)
-    if out is not None:
-        _check_rows("out", out, Hq, D, T)
-    dev = _same_device(q, *store, seq_info, seg_mode, out, workspace, status)
+    seq_ptr, mode_ptr, S = _table(seq_info, seg_mode)
+    dev = _device_of(q, *store, seq_info, seg_mode, out, workspace, status)
     if out is None:
-        out = _empty((T, Hq, D), torch.bfloat16, dev, stream)
-    lib = library()
+        out = _rows_like(q, shape, stream)
+    ors, ohs = _strides("out", out, shape)
     if workspace is None:
-        with torch.cuda.device(dev):
-            need = lib.sdpa_varlen_fourbit_workspace_bytes(T, Hq, Hkv, D, S, rows, cols)
-        workspace = _empty(max(int(need), 256), torch.uint8, dev, stream)
+        with torch.cuda.stream(stream):
+            workspace = torch.empty(max(q4_workspace_bytes(T, Hq, store, S), 256), dtype=_u8, device=q.device)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    _run(lib.sdpa_varlen_fourbit, dev, stream, q.data_ptr(), T, Hq, D, q.stride(0), q.stride(1), ptrs, rows, cols, Hkv,
-         seq_info.data_ptr() if S else None, seg_mode.data_ptr() if S and seg_mode is not None else None, S,
-         int(bool(causal)), int(window), float(1.0 / math.sqrt(D) if scale is None else scale), out.data_ptr(),
-         out.stride(0), out.stride(1), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-         _status_ptr(status))
+    _call(library().sdpa_varlen_fourbit, dev, stream, q.data_ptr(), T, Hq, D, rs, hs, ptrs, rows, cols, Hkv, seq_ptr,
+          mode_ptr, S, 1 if causal else 0, int(window), D ** -0.5 if scale is None else float(scale), out.data_ptr(),
+          ors, ohs, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _status_ptr(status))
     return out

@@ -228,6 +228,25 @@ static cudaError_t launch_k(const void* f, unsigned grid, unsigned block, void**
   return cudaLaunchKernelExC(&cfg, f, args);
 }
 
+// Columns a 4-bit call stages in bf16 for the prefill kernel: one per segment that can fill a 128-row
+// tile, as far as 2 GiB of workspace hold them (at least one while that takes at most 8 GiB); none
+// when the automatic route cannot reach kPrefillMinWork.  Depends on sizes and the route policy only.
+static int64_t q4_stage_bytes_per_column(int64_t rows, int Hkv, int D) { return rows * Hkv * D * 2; }
+static int q4_stage_cols(int64_t T, int Hq, int Hkv, int D, int S, int64_t rows) {
+  const int policy = g_policy.load();
+  const int group = Hq / Hkv;
+  if (policy == SDPA_ROUTE_SPLITK || group > kPrefillRows || kPrefillRows % group || S <= 0 || T <= 0) return 0;
+  const int64_t packed = T * group;
+  int64_t n = S;
+  if (policy == SDPA_ROUTE_AUTO) {
+    if (packed < kPrefillRows || (double)packed * Hkv * D * (double)rows < (double)kPrefillMinWork) return 0;
+    n = std::min<int64_t>(n, packed / kPrefillRows);
+  }
+  const int64_t col = 2 * q4_stage_bytes_per_column(rows, Hkv, D);  // K and V
+  if (col > (8ll << 30)) return 0;
+  return (int)std::min<int64_t>(n, std::max<int64_t>(1, (2ll << 30) / col));
+}
+
 // Whether a call may route segments to the prefill kernel: not under the split-K policy, and
 // (automatic routing) not when no segment can fill a 128-row tile (T * group < 128) or the
 // call cannot hold kPrefillMinWork of prefill work: that is at most packed rows * Hkv * D *
@@ -244,7 +263,8 @@ static bool prefill_launch(const SchedArgs& sa, int64_t T) {
 }
 
 static sdpa_status launch_all(const SchedArgs& sa, const AttnArgs& aa, int D, const Grids& g,
-                              const TensorMaps& tm, const AppendArgs* ap, const Q4Store* q4, cudaStream_t st) {
+                              const TensorMaps& tm, const AppendArgs* ap, const Q4Store* q4,
+                              const Q4StageArgs* stage, cudaStream_t st) {
   cudaError_t e = mark(0, st);
   if (e == cudaSuccess) {
     e = launch_sched(sa, st);
@@ -280,8 +300,18 @@ static sdpa_status launch_all(const SchedArgs& sa, const AttnArgs& aa, int D, co
   // costs ~5 us on prefill steps of a few tiles per CTA).
   const int64_t packed = aa.T * aa.group;
   const bool pf_possible = sa.prefill_ok;
+  if (e == cudaSuccess && pf_possible && stage) {
+    void* args[] = {(void*)stage};
+    const int64_t chunks = sa.rows_pf * stage->Hkv * (D / 8);  // of one column
+    const int64_t per = std::max<int64_t>(1, std::min<int64_t>(8 * g.prefill, chunks / (4 * kQ4StageThreads)));
+    e = cudaLaunchKernel(q4_stage_kernel_ptr(D), dim3((unsigned)per, (unsigned)stage->pf_cols),
+                         dim3(kQ4StageThreads), args, 0, st);
+    if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "4-bit staging launch: %s", cudaGetErrorString(e));
+  }
   if (e == cudaSuccess && pf_possible) {
-    void* args[] = {(void*)&aa, (void*)&tm.q, (void*)&tm.k, (void*)&tm.v};
+    AttnArgs pa = aa;
+    pa.rows = sa.rows_pf;
+    void* args[] = {(void*)&pa, (void*)&tm.q, (void*)&tm.k, (void*)&tm.v};
     const bool chained = packed < (int64_t)kPrefillRows * std::max(sa.S, 1);
     e = launch_k(prefill_kernel_ptr(D), (unsigned)g.prefill, prefill_block_threads(D), args,
                  prefill_smem_bytes(D), st, chained);
@@ -332,7 +362,14 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
   if ((st = device_info(&di))) return st;
   const Grids g = grids_for(di, D, q4 != nullptr);
   Workspace W;
-  const size_t need = layout_workspace((char*)ws, T, Hq, Hkv, D, S, g.splitk, g.prefill, &W);
+  size_t need = layout_workspace((char*)ws, T, Hq, Hkv, D, S, g.splitk, g.prefill, &W);
+  Q4StageArgs sg{};
+  if (q4 && (sg.pf_cols = q4_stage_cols(T, Hq, Hkv, D, S, rows)) > 0) {
+    const int64_t store = align_up(q4_stage_bytes_per_column(rows, Hkv, D) * sg.pf_cols, 256);
+    sg.k = (__nv_bfloat16*)((char*)ws + need);
+    sg.v = (__nv_bfloat16*)((char*)ws + need + store);
+    need += 2 * store;
+  }
   if (ws_bytes < need)
     return fail(SDPA_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need);
 
@@ -357,9 +394,13 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
   const bool group_fits = group <= kPrefillRows && (kPrefillRows % group) == 0;
   sa.tile_pf = prefill_tile_keys(D);
   sa.lo_align = q4 ? kQ4RowAlign : 1;
-  sa.prefill_ok = !q4 && di.prefill_ok[d_index(D)] && group_fits && prefill_launch(sa, T) &&
-                  make_tensor_maps(q, T, Hq, D, q_rs, q_hs, k, v, rows, cols, Hkv, group, sa.tile_pf,
-                                   &tm.q, &tm.k, &tm.v);
+  sa.pf_cols = sg.pf_cols;
+  // (a call-wide window bounds the positions that a staged column has to hold)
+  sa.rows_pf = q4 && window > 0 && !sa.seg_mode ? std::min<int64_t>(rows, T + window - 1) : rows;
+  sa.prefill_ok = (!q4 || sg.pf_cols > 0) && di.prefill_ok[d_index(D)] && group_fits && prefill_launch(sa, T) &&
+                  make_tensor_maps(q, T, Hq, D, q_rs, q_hs, q4 ? sg.k : k, q4 ? sg.v : v, sa.rows_pf,
+                                   q4 ? sg.pf_cols : cols, Hkv, group, sa.tile_pf, &tm.q, &tm.k, &tm.v);
+  if (!sa.prefill_ok) sa.pf_cols = 0;
   sa.grid[0] = 0;
   sa.grid[1] = g.splitk;
   sa.grid[2] = g.prefill;
@@ -392,7 +433,16 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
     apw = *ap;
     apw.segs = W.segs;
   }
-  return launch_all(sa, aa, D, g, tm, ap ? &apw : nullptr, q4, (cudaStream_t)stream);
+  if (sa.pf_cols > 0) {
+    sg.segs = W.segs;
+    sg.S = S;
+    sg.Hkv = Hkv;
+    sg.D = D;
+    sg.rows = rows;
+    sg.rows_pf = sa.rows_pf;
+    sg.st = *q4;
+  }
+  return launch_all(sa, aa, D, g, tm, ap ? &apw : nullptr, q4, sa.pf_cols > 0 ? &sg : nullptr, (cudaStream_t)stream);
 }
 
 }  // namespace sdpa
@@ -480,7 +530,8 @@ size_t sdpa_varlen_fourbit_workspace_bytes(int64_t T, int Hq, int Hkv, int D, in
     g.prefill = 1024;
     g_err[0] = 0;
   }
-  return layout_workspace(nullptr, T, Hq, Hkv, D, S, g.splitk, g.prefill, nullptr);
+  const int64_t store = align_up(q4_stage_bytes_per_column(rows, Hkv, D) * q4_stage_cols(T, Hq, Hkv, D, S, rows), 256);
+  return layout_workspace(nullptr, T, Hq, Hkv, D, S, g.splitk, g.prefill, nullptr) + 2 * store;
 }
 
 sdpa_status sdpa_varlen_fourbit(const void* q, int64_t T, int Hq, int D, int64_t q_row_stride, int64_t q_head_stride,

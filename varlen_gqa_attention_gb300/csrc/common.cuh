@@ -39,7 +39,7 @@ struct SegRec {
   int32_t route;     // kRoute*: none for invalid, overlapping or empty segments
   int32_t nrb;       // row blocks per KV head (units per KV head)
   int32_t bits;      // SDPA_SEG_* bits of this segment
-  int32_t pad;
+  int32_t pf_col;    // 4-bit store: the staged column of a prefill-route segment
   int32_t ubase[4];  // per route: units of all earlier segments on that route (monotone in
                      // the segment index, so a binary search maps a unit to its segment)
   int32_t causal, window;  // the segment's mask mode (the call's, or its row of seg_mode)
@@ -214,6 +214,10 @@ struct SchedArgs {
   int prefill_ok;  // prefill kernel usable for this call (group divides 128, tensor maps made)
   int tile_pf;     // keys per prefill tile
   int lo_align;    // split-K units' key ranges begin at a multiple of this (a power of two, at least 1)
+  int64_t rows_pf; // store rows the prefill kernel sees (a ring wraps there)
+  int pf_cols;     // 4-bit store: columns staged for the prefill kernel, the first pf_cols segments
+                   // of that route taking one each and the others the split-K route; 0: the
+                   // prefill kernel reads the store itself, every segment its own column
   int64_t grid[3];
   Workspace ws;
   int32_t* status_dev;

@@ -136,6 +136,7 @@ extern "C" sdpa_status sdpa_varlen_splitk_static(
   sa.prefill_ok = 0;
   sa.tile_pf = kPrefillTile;
   sa.lo_align = 1;
+  sa.rows_pf = rows;
   sa.grid[0] = 0;
   sa.grid[1] = grid;
   sa.grid[2] = 0;

@@ -42,11 +42,26 @@ __device__ __forceinline__ uint32_t q4_code(float x, float s) {
   return x == x ? (uint32_t)((int)n + 8) : 8u;
 }
 
+// (w & mask) | bits in one instruction: the compiler splits it in two when both are constants, so
+// `bits` comes in a register.
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;\n" : "=r"(r) : "r"(w), "n"(MASK), "r"(bits));
+  return r;
+}
+// A constant that the compiler keeps in a register.
+__device__ __forceinline__ uint32_t in_register(uint32_t v) {
+  asm volatile("" : "+r"(v));
+  return v;
+}
+
 // Two bf16 values from nibbles i and i + 4 of a word (shifted so that they are bits 0-3 and 16-19):
 // 0x4300 | c is 128 + c, and (128 + c) s - 136 s = (c - 8) s.  136 s = 8 * 17 * (8 to 15) eighths
 // has at most 8 significant bits (17 * 15 = 255), so the addend, and with it the result, is exact.
-__device__ __forceinline__ uint32_t q4_pair_bf16(uint32_t w, __nv_bfloat162 s2, __nv_bfloat162 z2) {
-  const uint32_t x = (w & 0x000F000Fu) | 0x43004300u;
+constexpr uint32_t kQ4Bf16 = 0x43004300u;
+__device__ __forceinline__ uint32_t q4_pair_bf16(uint32_t w, uint32_t bits, __nv_bfloat162 s2, __nv_bfloat162 z2) {
+  const uint32_t x = and_or<0x000F000Fu>(w, bits);  // bits: kQ4Bf16
   const __nv_bfloat162 v = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x), s2, z2);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
@@ -63,15 +78,16 @@ __device__ __forceinline__ uint4 q4_words8(uint32_t w, uint32_t scale_byte) {
   q4_scales_bf16(scale_byte, &s2, &z2);
   uint32_t x[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = q4_pair_bf16(w >> (4 * i), s2, z2);  // dims i and i + 4
+  for (int i = 0; i < 4; ++i) x[i] = q4_pair_bf16(w >> (4 * i), kQ4Bf16, s2, z2);  // dims i and i + 4
   return make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410),
                     __byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632));
 }
 
 // Two fp16 values from nibbles shifted to bits 6-9 and 22-25: 0x4800 | c << 6 is 8 + c / 2, and
 // (8 + c / 2) 2s - 24 s = (c - 8) s; 24 s <= 46080 has 5 significant bits.
-__device__ __forceinline__ uint32_t q4_pair_f16(uint32_t w, __half2 s2, __half2 z2) {
-  const uint32_t x = (w & 0x03C003C0u) | 0x48004800u;
+constexpr uint32_t kQ4F16 = 0x48004800u;
+__device__ __forceinline__ uint32_t q4_pair_f16(uint32_t w, uint32_t bits, __half2 s2, __half2 z2) {
+  const uint32_t x = and_or<0x03C003C0u>(w, bits);  // bits: kQ4F16
   const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&x), s2, z2);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
@@ -96,6 +112,20 @@ struct Q4AttnArgs {
   AttnArgs a;  // k, v unused
   Q4Store st;
 };
+
+// The keys and values of the prefill route's segments, brought to bf16 for the tensor-memory kernel:
+// position p of the segment with staged column c goes to row p % rows_pf of column c of a bf16
+// column store [rows_pf, pf_cols, Hkv, D] (q4_stage.cu).
+struct Q4StageArgs {
+  const SegRec* segs;  // the scheduler's records
+  int S, Hkv, D, pf_cols;
+  int64_t rows, rows_pf;
+  Q4Store st;
+  __nv_bfloat16* k;
+  __nv_bfloat16* v;
+};
+constexpr int kQ4StageThreads = 256;
+const void* q4_stage_kernel_ptr(int D);
 
 // Entry points (q4_attn.cu).
 constexpr int kQ4Threads = 160;  // four warps of attention, one that loads

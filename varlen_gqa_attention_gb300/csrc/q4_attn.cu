@@ -9,44 +9,49 @@
 // each brings 256 values to convert, so the instructions that convert (11 to 12 per 8 values, see
 // q4.cuh) weigh as much as the loads.  Everything else is therefore kept off the issue slots:
 //   * a fifth warp loads: whole runs of store rows by bulk copies (one thread, four copies per
-//     128 keys) into a ring of stages, across the borders of pieces, so that the next piece's
-//     first keys (and its query rows) travel while this one is finished;
+//     stage) into a ring of stages, across the borders of pieces, so that the next piece's first
+//     keys (and its query rows) travel while this one is finished;
 //   * no value is written back to shared memory: codes are read once per warp, as whole words, in
 //     an order that makes them operand fragments at once.  The contraction over dims does not care
 //     about their order, so a lane of K takes D / 4 dims of its key side by side (with their one
 //     or two scales), and the query fragments follow; a lane of V takes D / 8 dims side by side of
-//     four keys, and the output's columns follow;
-//   * scales are multiplied in by the conversion's own fused multiply-add, exactly.
+//     four keys, and the output's rows follow;
+//   * scales are multiplied in by the conversion's own fused multiply-add, exactly;
+//   * the products are taken transposed, S^T = K Q^T and O^T = V^T P^T: keys and dims fill the
+//     16 rows of an m16n8k16 product and the query rows its 8 columns, so that a decode unit of up
+//     to 8 rows (one token's heads) wastes no half of each product, score and output register.
+//     (With the query rows as the 16 rows the 64-sequence, 32768-key decode took 675 us against
+//     XXX.)  P^T is the transpose of what S^T leaves in the lanes: one movmatrix per 8 x 8 block.
 // P is rounded to fp16 (half a step is at most 2^-11 of it, against 2^-8 in bf16) and V is exact in
 // fp16; Q and K are multiplied in bf16, where both are exact.  Sums are fp32.  The lazily updated
 // maximum leaves P at most 2^8 above it, so P is kept 2^7 times larger, its sum too: at most 2^15,
 // and a row's largest at least 2^7, so that a P that fp16's smallest step (2^-24) cannot hold is
 // less than 2^-32 of its row: a million such keys are still lost in the output's rounding.
+#include <type_traits>
+
 #include "q4.cuh"
 #include "tc.cuh"
 
 namespace sdpa {
 
-constexpr int kQ4Stage = 128;     // keys per stage of the ring
 constexpr int kQ4Consumers = 128; // threads of the four attention warps
 constexpr float kQ4PLift = 7.f;    // P is held 2^7 times larger
-constexpr int kQ4MergePitch = 68; // floats per row of the merge buffer: 64 and a step that spreads banks
 
 template <int D>
 struct Q4Smem {
   static constexpr int kRowBytes = D / 2;
   static constexpr int kScaleBytes = D / kQ4Group;
-  static constexpr int kStages = 4;
-  static constexpr int kQBufs = 2;
-  // CTAs per SM that registers (the output alone is D / 2 of them) and shared memory allow
-  static constexpr int kPerSm = D == 64 ? 3 : D == 128 ? 2 : 1;
-  static constexpr int kCodes = kQ4Stage * kRowBytes;
-  static constexpr int kScales = kQ4Stage * kScaleBytes;
+  static constexpr int kKeys = D == 256 ? 64 : 128;  // keys per stage of the ring
+  static constexpr int kStages = D == 128 ? 3 : 4;
+  // CTAs per SM that registers and shared memory allow
+  static constexpr int kPerSm = D == 256 ? 2 : 3;
+  static constexpr int kCodes = kKeys * kRowBytes;
+  static constexpr int kScales = kKeys * kScaleBytes;
   static constexpr int kStageBytes = 2 * (kCodes + kScales);
   static constexpr int kQPitch = D * 2 + 16;
   static constexpr int kQBytes = kSplitkRows * kQPitch;
-  static constexpr int kMergeBytes = 4 * 16 * kQ4MergePitch * 4;
-  static constexpr int kBytes = kStages * kStageBytes + kQBufs * kQBytes + kMergeBytes;
+  static constexpr int kMergeBytes = 4 * 16 * 36 * 4;
+  static constexpr int kBytes = kStages * kStageBytes + kQBytes + kMergeBytes;
 };
 
 // One piece of a unit as the loading warp hands it on.
@@ -72,6 +77,12 @@ __device__ __forceinline__ void mma_f16_16816(float* d, const uint32_t* a, uint3
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// Transpose of an 8x8 block of 16-bit values: a lane holds two of row lane / 4, before and after.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(v));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -83,19 +94,11 @@ __device__ __forceinline__ bool q4_wait(uint32_t bar, uint32_t parity, volatile 
   return __all_sync(0xffffffffu, !*abort && mbar_wait(bar, parity, abort));
 }
 
-// The query rows' operand fragments for one word (8 dims) of a lane's K chunk: two k-steps.
-// The conversion pairs nibbles i and i + 4, so the fragments pair dims i and i + 4.
-__device__ __forceinline__ void q4_q_frags(const char* row0, const char* row8, uint32_t (&f)[2][4]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(row0);
-  const uint4 b = *reinterpret_cast<const uint4*>(row8);
-  f[0][0] = __byte_perm(a.x, a.z, 0x5410);
-  f[0][2] = __byte_perm(a.x, a.z, 0x7632);
-  f[1][0] = __byte_perm(a.y, a.w, 0x5410);
-  f[1][2] = __byte_perm(a.y, a.w, 0x7632);
-  f[0][1] = __byte_perm(b.x, b.z, 0x5410);
-  f[0][3] = __byte_perm(b.x, b.z, 0x7632);
-  f[1][1] = __byte_perm(b.y, b.w, 0x5410);
-  f[1][3] = __byte_perm(b.y, b.w, 0x7632);
+// 8 dims of a query row (16 bytes) as the operand words of two k-steps: the conversion of K pairs
+// nibbles i and i + 4 of a word, so the fragments pair dims i and i + 4.
+__device__ __forceinline__ uint4 q4_q_order(const uint4& a) {
+  return make_uint4(__byte_perm(a.x, a.z, 0x5410), __byte_perm(a.x, a.z, 0x7632),
+                    __byte_perm(a.y, a.w, 0x5410), __byte_perm(a.y, a.w, 0x7632));
 }
 
 // Bytes [p, p + 4 N) of shared memory into N words.
@@ -115,169 +118,225 @@ __device__ __forceinline__ void lds_words(const char* p, uint32_t (&w)[N]) {
   }
 }
 
-// The four attention warps on one piece: 16 packed rows (mt) x every NCS-th run of 32 keys (cs).
-template <int D, int NCS>
-__device__ __forceinline__ void q4_unit(const AttnArgs& A, const Q4Piece& pc, const char* ring, const char* sQ,
-                                        float* merge, uint32_t full, uint32_t empty, uint32_t& it,
+// The four attention warps on one piece.  4 / NCS groups of 8 NR query rows; the NCS warps of a group
+// take every NCS-th run of 16 KT keys.
+template <int D, int NR, int NCS, int KT>
+__device__ __forceinline__ void q4_unit(const AttnArgs& A, const Q4Piece& pc, const char* ring, char* sQ,
+                                        float* merge, uint32_t full, uint32_t empty, uint32_t qempty, uint32_t& it,
                                         volatile int* abort, float2* s_ml, int32_t** s_count) {
   using S = Q4Smem<D>;
   constexpr int WK = D / 32;  // words of a lane's K chunk (D / 4 dims)
   constexpr int WV = D / 64;  // words of a lane's V chunk (D / 8 dims)
-  constexpr int ND = D / 8;   // n8 blocks of the output
-  constexpr bool kQRegs = D <= 128;  // query fragments stay in registers
+  constexpr int ND = D / 16;  // m16 blocks of the output
+  constexpr int GR = 8 * NR;  // query rows of a group
+  constexpr bool kQRegs = NR == 1;  // query fragments stay in registers
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int mt = warp / NCS, cs = warp % NCS;
+  const int grp = warp / NCS, cs = warp % NCS;
   const int gq = lane >> 2, tq = lane & 3;
   const UnitRec& ur = pc.ur;
   const int R = ur.rows;
   const int64_t r0 = (int64_t)ur.rb * kSplitkRows;
-  const int64_t pos_lo = pc.pos_lo, pos_hi = pc.pos_hi;
+  const int64_t pos_lo = pc.pos_lo;
+  const int nkeys = (int)(pc.pos_hi - pos_lo);
 
-  // this lane's two rows: local rows mt*16 + gq and +8
-  int32_t rlo[2], rhi[2];
-  bool live[2];
+  // this lane's query rows, 2 tq and 2 tq + 1 of every 8: the keys each sees, as offsets from
+  // pos_lo: [first, first + count)
+  int first[NR][2];
+  uint32_t count[NR][2];
+  int lo_max = 0, hi_min = INT32_MAX;
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int rl = mt * 16 + gq + 8 * e;
-    live[e] = rl < R;
-    rlo[e] = INT32_MIN;  // rows past the unit's: never stored, whatever they come to
-    rhi[e] = INT32_MAX;
-    if (live[e]) {
-      const RowWin w = row_window((int)((r0 + rl) / A.group), ur.q_len, ur.kv_end, ur.causal, ur.window);
-      rlo[e] = (int32_t)max((int64_t)w.lo, pos_lo);
-      rhi[e] = (int32_t)min((int64_t)w.hi, pos_hi);
+  for (int r = 0; r < NR; ++r) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int rl = grp * GR + r * 8 + 2 * tq + c;
+      first[r][c] = 0;
+      count[r][c] = INT32_MAX;  // rows past the unit's: never stored, whatever they come to
+      if (rl < R) {
+        const RowWin w = row_window((int)((r0 + rl) / A.group), ur.q_len, ur.kv_end, ur.causal, ur.window);
+        const int a = (int)min(max((int64_t)w.lo - pos_lo, (int64_t)0), (int64_t)nkeys);
+        const int b = (int)min(max((int64_t)w.hi - pos_lo, (int64_t)a), (int64_t)nkeys);
+        first[r][c] = a;
+        count[r][c] = b - a;
+        lo_max = max(lo_max, a);
+        hi_min = min(hi_min, b);
+      }
     }
   }
-  const int32_t lo_max = max(rlo[0], rlo[1]), hi_min = min(rhi[0], rhi[1]);
+  // keys that every row of the warp sees
+  lo_max = __reduce_max_sync(0xffffffffu, lo_max);
+  hi_min = __reduce_min_sync(0xffffffffu, hi_min);
 
-  const char* q0 = sQ + (mt * 16 + gq) * S::kQPitch + tq * (D / 2);
-  uint32_t qf[kQRegs ? WK : 1][2][4];
+  const char* qrow = sQ + (grp * GR + gq) * S::kQPitch + tq * (D / 2);
+  uint4 qf[kQRegs ? WK : 1];
   if constexpr (kQRegs) {
 #pragma unroll
-    for (int w = 0; w < WK; ++w) q4_q_frags(q0 + 16 * w, q0 + 8 * S::kQPitch + 16 * w, qf[w]);
+    for (int w = 0; w < WK; ++w) qf[w] = q4_q_order(*reinterpret_cast<const uint4*>(qrow + 16 * w));
+    __syncwarp();
+    if (lane == 0) mbar_arrive(qempty);
+  } else {
+    // reordered in place once, read again for every run of keys
+    for (int idx = tid; idx < R * (D / 8); idx += kQ4Consumers) {
+      uint4* p = reinterpret_cast<uint4*>(sQ + (idx / (D / 8)) * S::kQPitch + (idx % (D / 8)) * 16);
+      *p = q4_q_order(*p);
+    }
+    bar_sync_n(1, kQ4Consumers);
   }
 
-  float o[ND][4];
+  float o[ND][NR][4];
 #pragma unroll
-  for (int nd = 0; nd < ND; ++nd) o[nd][0] = o[nd][1] = o[nd][2] = o[nd][3] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  for (int nd = 0; nd < ND; ++nd)
+#pragma unroll
+    for (int r = 0; r < NR; ++r) o[nd][r][0] = o[nd][r][1] = o[nd][r][2] = o[nd][r][3] = 0.f;
+  float m[NR][2], l[NR][2];
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    m[r][0] = m[r][1] = -INFINITY;
+    l[r][0] = l[r][1] = 0.f;
+  }
   const float sl2 = A.scale_log2;
-  // Column n of an 8-key block stands for key n, with the two of every other pair swapped: the
-  // four lanes of a quad then read V rows of both parities (rows of one parity share banks).
-  const int kn = gq ^ ((gq >> 1) & 1);        // the key of this lane's K column
-  const int ko = 2 * tq + (tq & 1);           // the keys of its two score columns: ko and ko ^ 1
+  const uint32_t kbits = in_register(kQ4Bf16), vbits = in_register(kQ4F16);
+  // Row n of 8 keys stands for key n, with the two of every other pair swapped: the four lanes of a
+  // quad then read V rows of both parities (rows of one parity share banks).
+  const int kn = gq ^ ((gq >> 1) & 1);  // the key of this lane's K row
+  const int ko = 2 * tq + (tq & 1);     // the keys of its V columns: ko and ko ^ 1
 
-  for (int64_t base = pos_lo; base < pos_hi; base += kQ4Stage, ++it) {
+  for (int base = 0; base < nkeys; base += S::kKeys, ++it) {
     const uint32_t st = it % S::kStages;
     q4_wait(full + 8 * st, (it / S::kStages) & 1, abort);
     const char* kc = ring + st * S::kStageBytes;
     const char* vc = kc + S::kCodes;
     const char* ks = vc + S::kCodes;
     const char* vs = ks + S::kScales;
-    const int nst = (int)min((int64_t)kQ4Stage, pos_hi - base);
+    const int nst = min(S::kKeys, nkeys - base);
 #pragma unroll 1
-    for (int k0 = cs * 32; k0 < nst; k0 += NCS * 32) {
-      // S = Q K^T over 32 keys
-      float s[4][4];
+    for (int k0 = cs * (16 * KT); k0 < nst; k0 += NCS * 16 * KT) {
+      // S^T = K Q^T over 16 KT keys
+      float s[KT][NR][4];
 #pragma unroll
-      for (int nb = 0; nb < 4; ++nb) s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.f;
+      for (int kt = 0; kt < KT; ++kt) {
 #pragma unroll
-      for (int nb = 0; nb < 4; ++nb) {
-        const int key = k0 + nb * 8 + kn;
-        uint32_t kw[WK];
-        lds_words<WK>(kc + key * S::kRowBytes + tq * (D / 8), kw);
-        __nv_bfloat162 s2, z2;
+        for (int r = 0; r < NR; ++r) s[kt][r][0] = s[kt][r][1] = s[kt][r][2] = s[kt][r][3] = 0.f;
+        const int key = k0 + kt * 16 + kn;
+        uint32_t kw[2][WK];  // keys key and key + 8
+        __nv_bfloat162 s2[2], z2[2];
         const uint8_t* sb = reinterpret_cast<const uint8_t*>(ks) + key * S::kScaleBytes + tq * D / 128;
-        q4_scales_bf16(sb[0], &s2, &z2);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          lds_words<WK>(kc + (key + 8 * h) * S::kRowBytes + tq * (D / 8), kw[h]);
+          q4_scales_bf16(sb[8 * h * S::kScaleBytes], &s2[h], &z2[h]);
+        }
 #pragma unroll
         for (int w = 0; w < WK; ++w) {
           if constexpr (D == 256) {
-            if (w == 4) q4_scales_bf16(sb[1], &s2, &z2);
-          }
-          uint32_t b[4];
+            if (w == 4) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) b[i] = q4_pair_bf16(kw[w] >> (4 * i), s2, z2);
-          if constexpr (kQRegs) {
-            mma_bf16_16816(s[nb], qf[w][0], b[0], b[1]);
-            mma_bf16_16816(s[nb], qf[w][1], b[2], b[3]);
-          } else {
-            uint32_t f[2][4];
-            q4_q_frags(q0 + 16 * w, q0 + 8 * S::kQPitch + 16 * w, f);
-            mma_bf16_16816(s[nb], f[0], b[0], b[1]);
-            mma_bf16_16816(s[nb], f[1], b[2], b[3]);
+              for (int h = 0; h < 2; ++h) q4_scales_bf16(sb[8 * h * S::kScaleBytes + 1], &s2[h], &z2[h]);
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {  // two k-steps of 16 dims
+            uint32_t a[4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              a[2 * i] = q4_pair_bf16(kw[0][w] >> (8 * x + 4 * i), kbits, s2[0], z2[0]);
+              a[2 * i + 1] = q4_pair_bf16(kw[1][w] >> (8 * x + 4 * i), kbits, s2[1], z2[1]);
+            }
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+              uint2 b;
+              if constexpr (kQRegs)
+                b = x ? make_uint2(qf[w].z, qf[w].w) : make_uint2(qf[w].x, qf[w].y);
+              else
+                b = *reinterpret_cast<const uint2*>(qrow + r * 8 * S::kQPitch + 16 * w + 8 * x);
+              mma_bf16_16816(s[kt][r], a, b.x, b.y);
+            }
           }
         }
       }
 
       // mask by select, online softmax in base 2 with a lazily updated maximum (O and l are only
       // rescaled when a row's maximum grows by more than 2^8)
-      const int64_t tile0 = base + k0;
-      const bool all = tile0 >= lo_max && tile0 + 32 <= hi_min;
-      float mx[2] = {-INFINITY, -INFINITY};
+      const int off = base + k0;
+      if (off < lo_max || off + 16 * KT > hi_min) {
 #pragma unroll
-      for (int nb = 0; nb < 4; ++nb) {
+        for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int rr = e >> 1;
-          float x = s[nb][e];
-          if (!all) {
-            const int64_t j = tile0 + nb * 8 + (ko ^ (e & 1));
-            x = !live[rr] || (j >= rlo[rr] && j < rhi[rr]) ? x : -INFINITY;
-          }
-          s[nb][e] = x;
-          mx[rr] = fmaxf(mx[rr], x);
-        }
+          for (int r = 0; r < NR; ++r)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t j = off + kt * 16 + 8 * (e >> 1) + kn - first[r][e & 1];
+              if (j >= count[r][e & 1]) s[kt][r][e] = -INFINITY;
+            }
       }
-      float alpha[2], nmu[2];
+      float mx[NR][2], alpha[NR][2], nmu[NR][2];
       bool resc = false;
 #pragma unroll
-      for (int rr = 0; rr < 2; ++rr) {
-        mx[rr] = fmaxf(mx[rr], __shfl_xor_sync(0xffffffffu, mx[rr], 1));
-        mx[rr] = fmaxf(mx[rr], __shfl_xor_sync(0xffffffffu, mx[rr], 2));
-        const float mn = fmaxf(m[rr], mx[rr] * sl2);
-        const bool up = mn > m[rr] + 8.f;  // false while nothing is visible
-        alpha[rr] = up ? exp2_approx(m[rr] - mn) : 1.f;
-        if (up) m[rr] = mn;
-        resc |= up;
-        nmu[rr] = m[rr] == -INFINITY ? 0.f : kQ4PLift - m[rr];
-      }
-      float ls[2] = {0.f, 0.f};
+      for (int r = 0; r < NR; ++r) {
 #pragma unroll
-      for (int nb = 0; nb < 4; ++nb) {
+        for (int c = 0; c < 2; ++c) {
+          float x = fmaxf(s[0][r][c], s[0][r][c + 2]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float p = exp2_approx(fmaf(s[nb][e], sl2, nmu[e >> 1]));
-          s[nb][e] = p;
-          ls[e >> 1] += p;
+          for (int kt = 1; kt < KT; ++kt) x = fmaxf(x, fmaxf(s[kt][r][c], s[kt][r][c + 2]));
+          mx[r][c] = x;
         }
       }
 #pragma unroll
-      for (int rr = 0; rr < 2; ++rr) l[rr] = l[rr] * alpha[rr] + ls[rr];
+      for (int d = 4; d < 32; d <<= 1)
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) mx[r][c] = fmaxf(mx[r][c], __shfl_xor_sync(0xffffffffu, mx[r][c], d));
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float mn = fmaxf(m[r][c], mx[r][c] * sl2);
+          const bool up = mn > m[r][c] + 8.f;  // false while nothing is visible
+          alpha[r][c] = up ? exp2_approx(m[r][c] - mn) : 1.f;
+          if (up) m[r][c] = mn;
+          resc |= up;
+          nmu[r][c] = m[r][c] == -INFINITY ? 0.f : kQ4PLift - m[r][c];
+        }
+      }
       if (__any_sync(0xffffffffu, resc)) {
 #pragma unroll
-        for (int nd = 0; nd < ND; ++nd) {
-          o[nd][0] *= alpha[0];
-          o[nd][1] *= alpha[0];
-          o[nd][2] *= alpha[1];
-          o[nd][3] *= alpha[1];
+        for (int r = 0; r < NR; ++r) {
+          l[r][0] *= alpha[r][0];
+          l[r][1] *= alpha[r][1];
+#pragma unroll
+          for (int nd = 0; nd < ND; ++nd) {
+            o[nd][r][0] *= alpha[r][0];
+            o[nd][r][1] *= alpha[r][1];
+            o[nd][r][2] *= alpha[r][0];
+            o[nd][r][3] *= alpha[r][1];
+          }
         }
       }
-
-      // O += P V, 16 keys at a time
 #pragma unroll
-      for (int bp = 0; bp < 2; ++bp) {
-        uint32_t a[4];
-        a[0] = pack_f16x2(s[2 * bp][0], s[2 * bp][1]);
-        a[1] = pack_f16x2(s[2 * bp][2], s[2 * bp][3]);
-        a[2] = pack_f16x2(s[2 * bp + 1][0], s[2 * bp + 1][1]);
-        a[3] = pack_f16x2(s[2 * bp + 1][2], s[2 * bp + 1][3]);
-        const int key = k0 + bp * 16;
-        uint32_t vw[4][WV];  // keys ko, ko ^ 1 of the first block, then of the second
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[kt][r][e] = exp2_approx(fmaf(s[kt][r][e], sl2, nmu[r][e & 1]));
+            l[r][e & 1] += s[kt][r][e];
+          }
+
+      // O^T += V^T P^T, 16 keys at a time
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) {
+        uint32_t b[NR][2];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          b[r][0] = transpose_8x8(pack_f16x2(s[kt][r][0], s[kt][r][1]));
+          b[r][1] = transpose_8x8(pack_f16x2(s[kt][r][2], s[kt][r][3]));
+        }
+        uint32_t vw[4][WV];  // keys ko, ko ^ 1 of the first 8, then of the second
         uint32_t sb[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int k = key + 8 * (e >> 1) + (ko ^ (e & 1));
+          const int k = k0 + kt * 16 + 8 * (e >> 1) + (ko ^ (e & 1));
           lds_words<WV>(vc + k * S::kRowBytes + gq * (D / 16), vw[e]);
           sb[e] = reinterpret_cast<const uint8_t*>(vs)[k * S::kScaleBytes + gq * D / 256];
         }
@@ -291,11 +350,14 @@ __device__ __forceinline__ void q4_unit(const AttnArgs& A, const Q4Piece& pc, co
             const uint32_t x0 = __byte_perm(vw[0][w], vw[1][w], hf ? 0x7632 : 0x5410);
             const uint32_t x1 = __byte_perm(vw[2][w], vw[3][w], hf ? 0x7632 : 0x5410);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t y0 = i < 2 ? x0 << (6 - 4 * i) : x0 >> (4 * i - 6);
-              const uint32_t y1 = i < 2 ? x1 << (6 - 4 * i) : x1 >> (4 * i - 6);
-              mma_f16_16816(o[8 * w + 4 * hf + i], a, q4_pair_f16(y0, s2[0], z2[0]),
-                            q4_pair_f16(y1, s2[1], z2[1]));
+            for (int i = 0; i < 4; i += 2) {
+              uint32_t a[4];
+              a[0] = q4_pair_f16(i == 0 ? x0 << 6 : x0 >> 2, vbits, s2[0], z2[0]);
+              a[1] = q4_pair_f16(i == 0 ? x0 << 2 : x0 >> 6, vbits, s2[0], z2[0]);
+              a[2] = q4_pair_f16(i == 0 ? x1 << 6 : x1 >> 2, vbits, s2[1], z2[1]);
+              a[3] = q4_pair_f16(i == 0 ? x1 << 2 : x1 >> 6, vbits, s2[1], z2[1]);
+#pragma unroll
+              for (int r = 0; r < NR; ++r) mma_f16_16816(o[4 * w + 2 * hf + i / 2][r], a, b[r][0], b[r][1]);
             }
           }
         }
@@ -304,35 +366,43 @@ __device__ __forceinline__ void q4_unit(const AttnArgs& A, const Q4Piece& pc, co
     __syncwarp();
     if (lane == 0) mbar_arrive(empty + 8 * st);
   }
+  if constexpr (!kQRegs) {
+    fence_proxy_async_smem();  // the rows were written here, and a bulk copy writes them next
+    __syncwarp();
+    if (lane == 0) mbar_arrive(qempty);
+  }
 
-  // row sums over the quad
+  // row sums over the lanes that share a row
 #pragma unroll
-  for (int rr = 0; rr < 2; ++rr) {
-    l[rr] += __shfl_xor_sync(0xffffffffu, l[rr], 1);
-    l[rr] += __shfl_xor_sync(0xffffffffu, l[rr], 2);
-    // a row whose scores are NaN has no maximum: it is joined as one, and comes out NaN
-    if (l[rr] != l[rr]) m[rr] = 0.f;
-  }
-  if (tq == 0) {
-    s_ml[warp * 16 + gq] = make_float2(m[0], l[0]);
-    s_ml[warp * 16 + gq + 8] = make_float2(m[1], l[1]);
+  for (int r = 0; r < NR; ++r) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) l[r][c] += __shfl_xor_sync(0xffffffffu, l[r][c], d);
+      // a row whose scores are NaN has no maximum: it is joined as one, and comes out NaN
+      if (l[r][c] != l[r][c]) m[r][c] = 0.f;
+      if (gq == 0) s_ml[warp * GR + r * 8 + 2 * tq + c] = make_float2(m[r][c], l[r][c]);
+    }
   }
 
-  // The warps' runs are joined through shared memory, 64 dims at a time: output block nd of column
-  // n is dim n * (D / 8) + nd, so a pass over 8 blocks is 8 dims side by side of every column.
+  // The warps' runs are joined through shared memory.  A lane has the D / 8 dims [gq D / 8, ...) of its
+  // rows; a pass takes XP of them.
+  constexpr int XP = NR == 1 ? 8 : 4;
+  constexpr int kPitch = 8 * XP + 4;
   const bool direct = ur.nslots == 1;
 #pragma unroll
-  for (int p = 0; p < D / 64; ++p) {
+  for (int p = 0; p < D / (8 * XP); ++p) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int r = 0; r < NR; ++r) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float* dst = merge + (warp * 16 + gq + 8 * e) * kQ4MergePitch + (2 * tq + c) * 8;
-        const int x = 2 * e + c;
-        *reinterpret_cast<float4*>(dst) =
-            make_float4(o[8 * p][x], o[8 * p + 1][x], o[8 * p + 2][x], o[8 * p + 3][x]);
-        *reinterpret_cast<float4*>(dst + 4) =
-            make_float4(o[8 * p + 4][x], o[8 * p + 5][x], o[8 * p + 6][x], o[8 * p + 7][x]);
+        float* dst = merge + (warp * GR + r * 8 + 2 * tq + c) * kPitch + gq * XP;
+#pragma unroll
+        for (int x = 0; x < XP; x += 4) {
+          const int nd = (p * XP + x) / 2;
+          *reinterpret_cast<float4*>(dst + x) =
+              make_float4(o[nd][r][c], o[nd][r][2 + c], o[nd + 1][r][c], o[nd + 1][r][2 + c]);
+        }
       }
     }
     bar_sync_n(1, kQ4Consumers);
@@ -344,44 +414,44 @@ __device__ __forceinline__ void q4_unit(const AttnArgs& A, const Q4Piece& pc, co
     }
     for (int idx = tid; idx < R * 8; idx += kQ4Consumers) {
       const int rl = idx >> 3, n = idx & 7;
-      const int mtr = rl / 16, rin = rl % 16;
+      const int w0 = rl / GR * NCS, rin = rl % GR;
       float M = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < NCS; ++c) M = fmaxf(M, s_ml[(mtr * NCS + c) * 16 + rin].x);
+      for (int c = 0; c < NCS; ++c) M = fmaxf(M, s_ml[(w0 + c) * GR + rin].x);
       const float Mu = M == -INFINITY ? 0.f : M;
-      float L = 0.f, acc[8];
+      float L = 0.f, acc[XP];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+      for (int k = 0; k < XP; ++k) acc[k] = 0.f;
 #pragma unroll
       for (int c = 0; c < NCS; ++c) {
-        const int w = (mtr * NCS + c) * 16 + rin;
+        const int w = (w0 + c) * GR + rin;
         const float2 ml = s_ml[w];
         const float f = exp2_approx(ml.x - Mu);
         L += ml.y * f;
-        const float* src = merge + w * kQ4MergePitch + n * 8;
-        const float4 u0 = *reinterpret_cast<const float4*>(src);
-        const float4 u1 = *reinterpret_cast<const float4*>(src + 4);
-        acc[0] += u0.x * f; acc[1] += u0.y * f; acc[2] += u0.z * f; acc[3] += u0.w * f;
-        acc[4] += u1.x * f; acc[5] += u1.y * f; acc[6] += u1.z * f; acc[7] += u1.w * f;
+#pragma unroll
+        for (int x = 0; x < XP; x += 4) {
+          const float4 u = *reinterpret_cast<const float4*>(merge + w * kPitch + n * XP + x);
+          acc[x] += u.x * f; acc[x + 1] += u.y * f; acc[x + 2] += u.z * f; acc[x + 3] += u.w * f;
+        }
       }
-      const int d0 = n * (D / 8) + 8 * p;
+      const int d0 = n * (D / 8) + XP * p;
       if (direct) {
         const float inv = L > 0.f ? 1.f / L : 0.f;
         const int64_t r = r0 + rl;
         const int64_t i = r / A.group;
         const int h = ur.hk * A.group + (int)(r % A.group);
-        uint4 pk;
-        pk.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-        pk.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
-        pk.z = pack_bf16x2(acc[4] * inv, acc[5] * inv);
-        pk.w = pack_bf16x2(acc[6] * inv, acc[7] * inv);
-        *reinterpret_cast<uint4*>(A.out + (ur.q_start + i) * A.o_rs + (int64_t)h * A.o_hs + d0) = pk;
+        __nv_bfloat16* dst = A.out + (ur.q_start + i) * A.o_rs + (int64_t)h * A.o_hs + d0;
+#pragma unroll
+        for (int x = 0; x < XP; x += 4)
+          *reinterpret_cast<uint2*>(dst + x) = make_uint2(pack_bf16x2(acc[x] * inv, acc[x + 1] * inv),
+                                                          pack_bf16x2(acc[x + 2] * inv, acc[x + 3] * inv));
       } else {
         const int64_t pi = ur.slot_base + (int64_t)pc.slot * R + rl;
         if (p == 0 && n == 0) A.ws.part_ml[kRouteSplitk][pi] = make_float2(M, L);
         float* dst = A.ws.part_o[kRouteSplitk] + pi * D + d0;
-        *reinterpret_cast<float4*>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-        *reinterpret_cast<float4*>(dst + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
+#pragma unroll
+        for (int x = 0; x < XP; x += 4)
+          *reinterpret_cast<float4*>(dst + x) = make_float4(acc[x], acc[x + 1], acc[x + 2], acc[x + 3]);
       }
     }
     bar_sync_n(1, kQ4Consumers);
@@ -404,12 +474,13 @@ __device__ __forceinline__ void q4_load(const Q4AttnArgs& G, char* ring, char* s
   uint32_t it = 0, n = 0;
   for (;; ++n) {
     const bool more = walk_next(wk, ur, ta, tb);
-    const uint32_t b = n % S::kQBufs;
-    if (n >= S::kQBufs && !q4_wait(qempty + 8 * b, (n / S::kQBufs - 1) & 1, abort)) break;
+    // (the rows' buffer is free once every warp has read them, or is past them; the record of the
+    // piece before that is then no longer in use)
+    if (n > 0 && !q4_wait(qempty, (n - 1) & 1, abort)) break;
     const int64_t pos_lo = (int64_t)ur.lo + ta * kSplitkTile;
     const int64_t pos_hi = min((int64_t)ur.lo + tb * kSplitkTile, (int64_t)ur.hi);
     if (lane == 0) {
-      Q4Piece& p = pieces[b];
+      Q4Piece& p = pieces[n & 1];
       p.valid = more;
       if (more) {
         p.ur = ur;
@@ -417,9 +488,9 @@ __device__ __forceinline__ void q4_load(const Q4AttnArgs& G, char* ring, char* s
         p.pos_hi = pos_hi;
         p.unit = wk.u - 1;  // the walk has moved past the piece's unit
         p.slot = (int32_t)(blockIdx.x - ur.g_first);
-        mbar_expect_tx(qfull + 8 * b, (uint32_t)ur.rows * (D * 2));
+        mbar_expect_tx(qfull, (uint32_t)ur.rows * (D * 2));
       } else {
-        mbar_arrive(qfull + 8 * b);
+        mbar_arrive(qfull);
       }
     }
     __syncwarp();
@@ -428,16 +499,16 @@ __device__ __forceinline__ void q4_load(const Q4AttnArgs& G, char* ring, char* s
       const int64_t r = (int64_t)ur.rb * kSplitkRows + lane;
       const int64_t i = r / A.group;
       const int h = ur.hk * A.group + (int)(r % A.group);
-      bulk_load(smem_u32(sQ + b * S::kQBytes + lane * S::kQPitch),
-                A.q + (ur.q_start + i) * A.q_rs + (int64_t)h * A.q_hs, D * 2, qfull + 8 * b);
+      bulk_load(smem_u32(sQ + lane * S::kQPitch),
+                A.q + (ur.q_start + i) * A.q_rs + (int64_t)h * A.q_hs, D * 2, qfull);
     }
     const int64_t plane = ((int64_t)ur.col * A.Hkv + ur.hk) * A.rows;  // first row of the column's head
     int64_t row = pos_lo % A.rows;
     bool ok = true;
-    for (int64_t pos = pos_lo; pos < pos_hi; pos += kQ4Stage, ++it) {
+    for (int64_t pos = pos_lo; pos < pos_hi; pos += S::kKeys, ++it) {
       const uint32_t st = it % S::kStages;
       if (it >= S::kStages && !(ok = q4_wait(empty + 8 * st, (it / S::kStages - 1) & 1, abort))) break;
-      const int rows16 = (int)(min((int64_t)kQ4Stage, pos_hi - pos) + 15) & ~15;
+      const int rows16 = (int)(min((int64_t)S::kKeys, pos_hi - pos) + 15) & ~15;
       const int first = (int)min((int64_t)rows16, A.rows - row), second = rows16 - first;
       if (lane == 0) {
         const uint32_t bar = full + 8 * st;
@@ -465,25 +536,24 @@ __device__ __forceinline__ void q4_load(const Q4AttnArgs& G, char* ring, char* s
   int none = 0;
   for (uint32_t k = it > S::kStages ? it - S::kStages : 0; k < it; ++k)
     mbar_wait(full + 8 * (k % S::kStages), (k / S::kStages) & 1, &none);
-  for (uint32_t k = n > S::kQBufs ? n - S::kQBufs : 0; k < n; ++k)
-    mbar_wait(qfull + 8 * (k % S::kQBufs), (k / S::kQBufs) & 1, &none);
+  if (n > 0) mbar_wait(qfull, (n - 1) & 1, &none);
 }
 
 template <int D>
 __global__ void __launch_bounds__(kQ4Threads, Q4Smem<D>::kPerSm) sdpa_q4_splitk_kernel(Q4AttnArgs G) {
   using S = Q4Smem<D>;
   extern __shared__ __align__(128) char smem[];
-  __shared__ __align__(8) uint64_t bars[2 * S::kStages + 2 * S::kQBufs];
-  __shared__ __align__(16) Q4Piece pieces[S::kQBufs];
+  __shared__ __align__(8) uint64_t bars[2 * S::kStages + 2];
+  __shared__ __align__(16) Q4Piece pieces[2];
   __shared__ float2 s_ml[4 * 16];
   __shared__ int32_t* s_count[2];
   __shared__ int s_abort;
   const AttnArgs& A = G.a;
   char* ring = smem;
   char* sQ = smem + S::kStages * S::kStageBytes;
-  float* merge = reinterpret_cast<float*>(sQ + S::kQBufs * S::kQBytes);
+  float* merge = reinterpret_cast<float*>(sQ + S::kQBytes);
   const uint32_t full = smem_u32(bars), empty = full + 8 * S::kStages;
-  const uint32_t qfull = empty + 8 * S::kStages, qempty = qfull + 8 * S::kQBufs;
+  const uint32_t qfull = empty + 8 * S::kStages, qempty = qfull + 8;
 
   if (threadIdx.x == 0) {
     s_abort = 0;
@@ -492,10 +562,8 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Smem<D>::kPerSm) sdpa_q4_splitk_
       mbar_init(full + 8 * k, 1);
       mbar_init(empty + 8 * k, 4);
     }
-    for (int k = 0; k < S::kQBufs; ++k) {
-      mbar_init(qfull + 8 * k, 1);
-      mbar_init(qempty + 8 * k, 4);
-    }
+    mbar_init(qfull, 1);
+    mbar_init(qempty, 4);
     mbar_fence_init();
   }
   __syncthreads();
@@ -507,21 +575,35 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Smem<D>::kPerSm) sdpa_q4_splitk_
   } else {
     uint32_t it = 0;
     for (uint32_t n = 0;; ++n) {
-      const uint32_t b = n % S::kQBufs;
-      const bool got = q4_wait(qfull + 8 * b, (n / S::kQBufs) & 1, &s_abort);
+      const bool got = q4_wait(qfull, n & 1, &s_abort);
       // the four warps go on together or not at all: what follows is their common control flow
       if (!bar_and(1, kQ4Consumers, got)) break;
-      const Q4Piece& pc = pieces[b];
+      const Q4Piece& pc = pieces[n & 1];
       if (!pc.valid) break;
       if (threadIdx.x == 0) s_count[1] = pc.ur.nslots > 1 ? A.ws.unit_done + pc.unit : nullptr;
-      if (pc.ur.rows <= 16)
-        q4_unit<D, 4>(A, pc, ring, sQ + b * S::kQBytes, merge, full, empty, it, &s_abort, s_ml, s_count);
-      else
-        q4_unit<D, 2>(A, pc, ring, sQ + b * S::kQBytes, merge, full, empty, it, &s_abort, s_ml, s_count);
+      auto unit = [&](auto nr, auto ncs, auto kt) {
+        q4_unit<D, decltype(nr)::value, decltype(ncs)::value, decltype(kt)::value>(
+            A, pc, ring, sQ, merge, full, empty, qempty, it, &s_abort, s_ml, s_count);
+      };
+      using std::integral_constant;
+      const int rows = pc.ur.rows;
+      if constexpr (D == 256) {  // an output of 16 rows would take 128 registers
+        if (rows <= 8)
+          unit(integral_constant<int, 1>(), integral_constant<int, 4>(), integral_constant<int, 1>());
+        else if (rows <= 16)
+          unit(integral_constant<int, 1>(), integral_constant<int, 2>(), integral_constant<int, 1>());
+        else
+          unit(integral_constant<int, 1>(), integral_constant<int, 1>(), integral_constant<int, 1>());
+      } else {
+        if (rows <= 8)
+          unit(integral_constant<int, 1>(), integral_constant<int, 4>(), integral_constant<int, 2>());
+        else if (rows <= 16)
+          unit(integral_constant<int, 2>(), integral_constant<int, 4>(), integral_constant<int, 1>());
+        else
+          unit(integral_constant<int, 2>(), integral_constant<int, 2>(), integral_constant<int, 1>());
+      }
       // (the unit ended on a barrier of the four warps)
       if (threadIdx.x == 0) s_count[0] = s_count[1];
-      __syncwarp();
-      if ((threadIdx.x & 31) == 0) mbar_arrive(qempty + 8 * b);
     }
     if (threadIdx.x == 0 && s_count[0] != nullptr) red_add_release(s_count[0], 1);
   }

@@ -178,7 +178,7 @@ __device__ __forceinline__ float prefill_work(const SchedArgs& A, int32_t q_len,
 
 // A segment's entry as the unit builder reads it.
 struct SegView {
-  int32_t q_start, q_len, col, kv_end, nrb, ubase, causal, window;
+  int32_t q_start, q_len, col, kv_end, nrb, ubase, causal, window, pf_col;
 };
 
 // Record of unit uq of route q, which belongs to segment s: its (KV head, row block), rows,
@@ -195,7 +195,7 @@ __device__ __forceinline__ UnitRec make_unit(const SchedArgs& A, int s, const Se
   ur.seg = s;
   ur.q_start = g.q_start;
   ur.q_len = g.q_len;
-  ur.col = g.col;
+  ur.col = q == kRoutePrefill && A.pf_cols > 0 ? g.pf_col : g.col;
   ur.kv_end = g.kv_end;
   ur.causal = g.causal;
   ur.window = g.window;
@@ -213,7 +213,7 @@ __device__ __forceinline__ UnitRec make_unit(const SchedArgs& A, int s, const Se
   if (q == kRouteSplitk && ur.hi > ur.lo) ur.lo &= -A.lo_align;
   // key tiles: the prefill kernel's stop at a ring wrap (two TMA ranges), the split-K
   // kernel's wrap per row
-  const int64_t nt = q == kRoutePrefill ? key_tiles(ur.lo, ur.hi, A.rows, tl).n
+  const int64_t nt = q == kRoutePrefill ? key_tiles(ur.lo, ur.hi, A.rows_pf, tl).n
                                         : (ur.hi > ur.lo ? udiv((int64_t)(ur.hi - ur.lo) + tl - 1, tl) : 0);
   ur.nslots = 0;
   ur.g_first = 0;
@@ -289,7 +289,7 @@ __device__ __forceinline__ int64_t place_unit(const SchedArgs& A, UnitRec& ur, i
 constexpr int kSegCache = 1024;
 constexpr int kRowCache = 8192;
 constexpr int kUnitCache = 1024;
-constexpr size_t kSchedSmem = (size_t)kSegCache * (16 + 8 + 8 + 8 + 4 + 4) + (size_t)kRowCache * 4 +
+constexpr size_t kSchedSmem = (size_t)kSegCache * (16 + 8 + 8 + 8 + 4 + 4 + 4) + (size_t)kRowCache * 4 +
                               (size_t)kUnitCache * sizeof(UnitRec);
 
 __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_kernel(SchedArgs A) {
@@ -307,7 +307,8 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_kernel(SchedArgs A) 
   int2* c_ub = c_rn + kSegCache;                    // unit bases on routes 1 and 2
   int32_t* c_bits = reinterpret_cast<int32_t*>(c_ub + kSegCache);
   int32_t* c_flag = c_bits + kSegCache;             // overlap flags
-  int32_t* c_row = c_flag + kSegCache;              // packed row -> owning segment
+  int32_t* c_pf = c_flag + kSegCache;               // staged columns of prefill-route segments
+  int32_t* c_row = c_pf + kSegCache;                // packed row -> owning segment
   UnitRec* c_unit = reinterpret_cast<UnitRec*>(c_row + kRowCache);
 
   const Workspace& W = A.ws;
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_kernel(SchedArgs A) 
       } else {
         SegRec r;
         r.q_start = g[0]; r.q_len = g[1]; r.col = g[2]; r.kv_end = g[3];
-        r.route = kRouteNone; r.nrb = 0; r.bits = bits; r.pad = 0;
+        r.route = kRouteNone; r.nrb = 0; r.bits = bits; r.pf_col = 0;
         r.ubase[0] = r.ubase[1] = r.ubase[2] = r.ubase[3] = 0;
         r.causal = md.x; r.window = md.y;
         r.pad2[0] = r.pad2[1] = 0;
@@ -394,6 +395,16 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_kernel(SchedArgs A) 
         pw += prefill_work(A, g.y, g.w, cached ? c_mode[s].y : W.segs[s].window);
     }
     const bool big = block_sum(pw, s_fsum) >= kPrefillMinWork;
+    // staged columns go to the first segments of the prefill route, in segment order
+    int64_t pf[1] = {0};
+    if (A.pf_cols > 0) {
+      int64_t pf_all[1];
+      for (int64_t s = sa; s < sb; ++s) {
+        const int4 g = seg_of((int)s);
+        pf[0] += bits_of((int)s) == 0 && !flag[s] && g.y > 0 && route_of(A, g.y, big) == kRoutePrefill;
+      }
+      block_scan<1>(pf, pf_all, sh);
+    }
     int64_t n1 = 0, n2 = 0, nrows = 0;  // units on routes 1 and 2, packed rows of live segments
     for (int64_t s = sa; s < sb; ++s) {
       const int32_t bits = bits_of((int)s);
@@ -404,6 +415,10 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_kernel(SchedArgs A) 
       if (bits == 0 && !fl && g.y > 0) {
         const int64_t R = (int64_t)g.y * A.group;
         route = route_of(A, g.y, big);
+        if (A.pf_cols > 0 && route == kRoutePrefill) {
+          if (pf[0] >= A.pf_cols) route = kRouteSplitk;
+          (cached ? c_pf[s] : W.segs[s].pf_col) = (int32_t)pf[0]++;
+        }
         const int rpu = rows_per_unit(A, route);
         nrb = (int)udiv(R + rpu - 1, rpu);
         if (route == kRouteSplitk) n1 += (int64_t)A.Hkv * nrb; else n2 += (int64_t)A.Hkv * nrb;
@@ -471,6 +486,7 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_kernel(SchedArgs A) 
       g.ubase = q == 1 ? c_ub[s].x : c_ub[s].y;
       g.causal = c_mode[s].x;
       g.window = c_mode[s].y;
+      g.pf_col = c_pf[s];
     } else {
       const SegRec& r = W.segs[s];
       g.q_start = r.q_start; g.q_len = r.q_len; g.col = r.col; g.kv_end = r.kv_end;
@@ -478,6 +494,7 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_kernel(SchedArgs A) 
       g.ubase = q == 1 ? r.ubase[1] : r.ubase[2];
       g.causal = r.causal;
       g.window = r.window;
+      g.pf_col = r.pf_col;
     }
     return g;
   };
@@ -596,7 +613,7 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_kernel(SchedArgs A) 
       const int4 c = c_seg[s];
       SegRec r;
       r.q_start = c.x; r.q_len = c.y; r.col = c.z; r.kv_end = c.w;
-      r.route = c_rn[s].x; r.nrb = c_rn[s].y; r.bits = c_bits[s]; r.pad = 0;
+      r.route = c_rn[s].x; r.nrb = c_rn[s].y; r.bits = c_bits[s]; r.pf_col = c_pf[s];
       r.ubase[0] = 0; r.ubase[1] = c_ub[s].x; r.ubase[2] = c_ub[s].y; r.ubase[3] = 0;
       r.causal = c_mode[s].x; r.window = c_mode[s].y;
       r.pad2[0] = r.pad2[1] = 0;
@@ -670,6 +687,7 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_small_kernel(SchedAr
   __shared__ int2 c_mode[kSmallSegs];  // (causal, window)
   __shared__ int2 c_rn[kSmallSegs];    // (route, nrb)
   __shared__ int2 c_ub[kSmallSegs];    // unit bases on routes 1 and 2
+  __shared__ int32_t c_pf[kSmallSegs];  // staged columns of prefill-route segments
   __shared__ int64_t sh[3 * 32];
   __shared__ int64_t s_pb[3][kMaxPhases + 1];
   __shared__ int64_t s_pu0[3][kMaxPhases + 1];  // first unit of each phase; [np] = units
@@ -713,9 +731,13 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_small_kernel(SchedAr
     float pw = live ? prefill_work(A, g[1], g[3], md.y) : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) pw += __shfl_xor_sync(kAll, pw, o);
-    int route = kRouteNone, nrb = 0;
+    int route = live ? route_of(A, g[1], pw >= kPrefillMinWork) : kRouteNone, nrb = 0;
+    int pf_col = 0;
+    if (A.pf_cols > 0) {  // staged columns go to the first segments of the prefill route
+      pf_col = __popc(__ballot_sync(kAll, route == kRoutePrefill) & ((1u << lane) - 1u));
+      if (route == kRoutePrefill && pf_col >= A.pf_cols) route = kRouteSplitk;
+    }
     if (live) {
-      route = route_of(A, g[1], pw >= kPrefillMinWork);
       const int rpu = rows_per_unit(A, route);
       nrb = (int)(((uint32_t)g[1] * (uint32_t)A.group + rpu - 1) / (uint32_t)rpu);
     }
@@ -736,9 +758,10 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_small_kernel(SchedAr
       c_mode[lane] = md;
       c_rn[lane] = make_int2(route, nrb);
       c_ub[lane] = make_int2(x1 - n1, x2 - n2);
+      c_pf[lane] = pf_col;
       SegRec r;
       r.q_start = g[0]; r.q_len = g[1]; r.col = g[2]; r.kv_end = g[3];
-      r.route = route; r.nrb = nrb; r.bits = bits; r.pad = 0;
+      r.route = route; r.nrb = nrb; r.bits = bits; r.pf_col = pf_col;
       r.ubase[0] = 0; r.ubase[1] = x1 - n1; r.ubase[2] = x2 - n2; r.ubase[3] = 0;
       r.causal = md.x; r.window = md.y;
       r.pad2[0] = r.pad2[1] = 0;
@@ -793,6 +816,7 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_small_kernel(SchedAr
     gv.ubase = q == 1 ? c_ub[s].x : c_ub[s].y;
     gv.causal = c_mode[s].x;
     gv.window = c_mode[s].y;
+    gv.pf_col = c_pf[s];
     ur = make_unit(A, s, gv, q, uq, &span, &reuse);
     if (ur.ntiles == 0) s_work = 1;  // rows of a unit with no keys: zeroed by the combine pass
     if (q == kRouteSplitk) W.unit_done[uq] = 0;
