@@ -17,6 +17,8 @@ import varlen_gqa_attention_gb300 as pkg
 from oracle import sdpa_varlen_oracle as O
 from oracle import step_oracle as S
 
+from test_rope_gpu import assert_rotated
+
 pytestmark = pytest.mark.gpu
 
 
@@ -280,7 +282,8 @@ def test_a_decode_loop_in_one_captured_graph(dev):
                 dst[col, :, row] = torch.from_numpy(src[t])
         for a, b in zip(stored, store):
             assert torch.equal(a.cpu(), b)
-        check(out, 0, S.to_bf16(ref_q), store, seq, True, 50)
+        assert_rotated(qr, ref_q, new[0], D, False)
+        check(out, 0, qr.cpu(), store, seq, True, 50)
 
 
 def test_the_bf16_store_agrees_with_the_4_bit_one_on_its_values(dev):

@@ -1,7 +1,8 @@
 """GPU parity of the rotary positions (sdpa_rope) against the 64-bit oracle.
 
-A result is the exact one rounded to fp32 and then to bf16, so it is off by at most half a step of
-each (2^-8 and 2^-24 of the result) and by what the compensated sum leaves (2^-45 of the pair)."""
+A result is r = fma(a, cos, q), q = -(b sin), rounded to bf16.  q is off by 2^-24 of itself, r by 2^-24 of
+itself, both at most |a| + |b| (cosines are at most 1), and the rounding to bf16 by 2^-8 of r: all in
+all 2^-8 of the result and (1 + 2^-8) 2^-23, less than 2^-22, of the pair."""
 import numpy as np
 import pytest
 import torch
@@ -37,8 +38,9 @@ def assert_rotated(got, ref, x, R, interleaved, tag=""):
         u, w = S.pair_dims(j, half, interleaved)
         pair[..., u] = pair[..., w] = pair[..., u] + pair[..., w]
     err = np.abs(S.f64(got) - ref)
-    bound = (2.0 ** -8 + 2.0 ** -24) * np.abs(ref) + 2.0 ** -45 * pair
+    bound = 2.0 ** -8 * np.abs(ref) + 2.0 ** -22 * pair
     assert (err <= bound).all(), f"{tag}: {np.argwhere(err > bound)[:3]}"
+    assert np.array_equal(S.f64(got)[..., R:], ref[..., R:])  # the dims that are not turned
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
@@ -51,8 +53,6 @@ def test_rotation_matches_the_oracle(dev, D, interleaved, R, axes, T, H):
     ref, _ = S.rope(x, table, pos, sections, interleaved)
     got = pkg.sdpa_rope(x.to(dev), table.to(dev), pos.to(dev), sections=sections, interleaved=interleaved)
     assert_rotated(got, ref, x, R, interleaved)
-    # and bit for bit what 64 bits give once rounded to fp32 and bf16
-    assert torch.equal(got.cpu().view(torch.int16), S.to_bf16(ref).view(torch.int16))
 
 
 @pytest.mark.parametrize("interleaved", [False, True])
@@ -80,16 +80,16 @@ def test_the_inverse_is_the_gradient(dev, interleaved):
 
 def test_in_place_and_strided_rows(dev):
     x, table, pos, sections = inputs(40, 6, 128, 128, 1, 300, 8)
-    ref = S.to_bf16(S.rope(x, table, pos, sections)[0])
+    ref = S.rope(x, table, pos, sections)[0]
     y = x.to(dev)
     assert pkg.sdpa_rope(y, table.to(dev), pos[0].to(dev), out=y) is y
-    assert torch.equal(y.cpu().view(torch.int16), ref.view(torch.int16))
+    assert_rotated(y, ref, x, 128, False)
     wide = torch.full((40, 10, 136), 7.0, dtype=torch.bfloat16, device=dev)
     part = wide[:, 2:8, 8:]
     part.copy_(x)
     out = torch.full((40, 20, 128), 5.0, dtype=torch.bfloat16, device=dev)
     pkg.sdpa_rope(part, table.to(dev), pos.to(dev), out=out[:, ::2][:, 1:7])
-    assert torch.equal(out[:, 2:14:2].cpu().view(torch.int16), ref.view(torch.int16))
+    assert torch.equal(out[:, 2:14:2], y)
     assert bool((out[:, 1::2] == 5).all()) and bool((out[:, 14:] == 5).all()) and bool((out[:, 0] == 5).all())
     assert bool((wide[:, :2] == 7).all()) and torch.equal(part.cpu(), x)
 
@@ -102,7 +102,8 @@ def test_positions_outside_the_table_are_reported_and_zero(dev):
     got = pkg.sdpa_rope(x.to(dev), table.to(dev), pos.to(dev), sections=sections, status=status)
     ref, bad = S.rope(x, table, pos, sections)
     assert bad.nonzero()[0].tolist() == [2, 5, 7] and int(status) == pkg.ROPE_BAD_POS
-    assert torch.equal(got.cpu().view(torch.int16), S.to_bf16(ref).view(torch.int16))
+    assert_rotated(got, ref, x, 32, False)
+    assert not bool(got[[2, 5, 7]].any())
     status.zero_()  # an axis without pairs is not looked at
     pkg.sdpa_rope(x.to(dev), table.to(dev), pos[[0, 1]].clamp(0, 49).to(dev) * torch.tensor([[1], [1000]], device=dev,
                   dtype=torch.int32), sections=(16, 0), status=status)
@@ -121,13 +122,13 @@ def test_no_rows_another_stream_and_a_captured_graph(dev):
     x, table, pos, sections = inputs(20, 3, 128, 64, 1, 64, 11)
     tab, p = table.to(dev), pos.to(dev)
     assert pkg.sdpa_rope(x[:0].to(dev), tab, p[:, :0]).shape == (0, 3, 128)
-    ref = S.to_bf16(S.rope(x, table, pos, sections)[0])
+    ref = S.rope(x, table, pos, sections)[0]
     side = torch.cuda.Stream(dev)
     xd = x.to(dev)
     side.wait_stream(torch.cuda.current_stream())
     y = pkg.sdpa_rope(xd, tab, p, stream=side)
     torch.cuda.current_stream().wait_stream(side)
-    assert torch.equal(y.cpu().view(torch.int16), ref.view(torch.int16))
+    assert_rotated(y, ref, x, 64, False)
     out = torch.empty_like(xd)
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
@@ -137,4 +138,16 @@ def test_no_rows_another_stream_and_a_captured_graph(dev):
     p.copy_(pos2)
     g.replay()
     torch.cuda.synchronize()
-    assert torch.equal(out.cpu().view(torch.int16), S.to_bf16(S.rope(x2, table, pos2, sections)[0]).view(torch.int16))
+    assert_rotated(out, S.rope(x2, table, pos2, sections)[0], x2, 64, False)
+
+
+def test_many_rows_on_few_warps(dev):
+    # more rows than the launch has warps: each goes through several, the positions of some outside
+    x, table, pos, _ = inputs(9000, 3, 64, 64, 2, 300, 14)
+    sections = (20, 12)
+    pos[0, ::1000], pos[1, 17::3000] = -5, 300
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    got = pkg.sdpa_rope(x.to(dev), table.to(dev), pos.to(dev), sections=sections, status=status)
+    ref, bad = S.rope(x, table, pos, sections)
+    assert_rotated(got, ref, x, 64, False)
+    assert int(status) == pkg.ROPE_BAD_POS and not bool(got[torch.from_numpy(bad).to(dev)].any())

@@ -303,9 +303,9 @@ static sdpa_status launch_all(const SchedArgs& sa, const AttnArgs& aa, int D, co
   if (e == cudaSuccess && pf_possible && stage) {
     void* args[] = {(void*)stage};
     const int64_t chunks = sa.rows_pf * stage->Hkv * (D / 8);  // of one column
-    const int64_t per = std::max<int64_t>(1, std::min<int64_t>(8 * g.prefill, chunks / (4 * kQ4StageThreads)));
-    e = cudaLaunchKernel(q4_stage_kernel_ptr(D), dim3((unsigned)per, (unsigned)stage->pf_cols),
-                         dim3(kQ4StageThreads), args, 0, st);
+    const int64_t most = std::max<int64_t>(1, 8 * g.prefill / stage->pf_cols);
+    const int64_t per = std::max<int64_t>(1, std::min<int64_t>(most, chunks / (4 * kQ4StageThreads)));
+    e = launch_k(q4_stage_kernel_ptr(D), (unsigned)(per * stage->pf_cols), kQ4StageThreads, args, 0, st, true);
     if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "4-bit staging launch: %s", cudaGetErrorString(e));
   }
   if (e == cudaSuccess && pf_possible) {

@@ -34,14 +34,6 @@ __device__ __forceinline__ uint32_t q4_scale_byte(float amax) {
   const int32_t r = (int32_t)((u + 0x7FFFFu + ((u >> 20) & 1u)) >> 20) - (106 << 3);
   return (uint32_t)min(max(r, 0), 255);
 }
-// The code of x under scale s: 8 + x / s rounded to even and clamped to [-7, 7]; NaN takes 8.
-// x has 8 significant bits and a code border (n + 1/2) s at most 9, so the rounded quotient never
-// crosses a border that the exact one does not.
-__device__ __forceinline__ uint32_t q4_code(float x, float s) {
-  const float n = fminf(fmaxf(rintf(__fdiv_rn(x, s)), -7.f), 7.f);
-  return x == x ? (uint32_t)((int)n + 8) : 8u;
-}
-
 // (w & mask) | bits in one instruction: the compiler splits it in two when both are constants, so
 // `bits` comes in a register.
 template <uint32_t MASK>

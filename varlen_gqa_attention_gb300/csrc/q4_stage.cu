@@ -12,14 +12,18 @@
 
 namespace sdpa {
 
-// blockIdx.y: staged column; its segment is the prefill-route one that carries that number.
+// CTA b works on staged column b % pf_cols; its segment is the prefill-route one of that number.
 template <int D>
 __global__ void __launch_bounds__(kQ4StageThreads) sdpa_q4_stage_kernel(Q4StageArgs A) {
   __shared__ int s_seg;
+  const int64_t column = blockIdx.x % A.pf_cols, part = blockIdx.x / A.pf_cols;
+  const int64_t parts = gridDim.x / A.pf_cols;
   if (threadIdx.x == 0) s_seg = -1;
   __syncthreads();
+  griddep_wait();  // the scheduler's records, and the calls before that used the columns
+  griddep_launch();
   for (int s = threadIdx.x; s < A.S; s += blockDim.x)
-    if (A.segs[s].route == kRoutePrefill && A.segs[s].pf_col == (int)blockIdx.y) s_seg = s;
+    if (A.segs[s].route == kRoutePrefill && A.segs[s].pf_col == (int)column) s_seg = s;
   __syncthreads();
   if (s_seg < 0) return;
   const SegRec sg = A.segs[s_seg];
@@ -28,9 +32,9 @@ __global__ void __launch_bounds__(kQ4StageThreads) sdpa_q4_stage_kernel(Q4StageA
   const int64_t lo = w0.lo, n = (int64_t)sg.kv_end - lo;
   if (n <= 0) return;
   constexpr int W = D / 8;  // words of a row
-  const int64_t per_head = n * W, total = per_head * A.Hkv, stride = (int64_t)gridDim.x * blockDim.x;
+  const int64_t per_head = n * W, total = per_head * A.Hkv, stride = parts * blockDim.x;
   constexpr int U = 4;
-  for (int64_t i0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i0 < total; i0 += U * stride) {
+  for (int64_t i0 = part * blockDim.x + threadIdx.x; i0 < total; i0 += U * stride) {
     uint32_t kw[U], vw[U], kb[U], vb[U];
     int64_t dst[U];
 #pragma unroll
@@ -46,7 +50,7 @@ __global__ void __launch_bounds__(kQ4StageThreads) sdpa_q4_stage_kernel(Q4StageA
         vw[u] = *reinterpret_cast<const uint32_t*>(A.st.vc + cell * (D / 2) + 4 * c);
         kb[u] = A.st.ks[cell * (D / kQ4Group) + c / 4];
         vb[u] = A.st.vs[cell * (D / kQ4Group) + c / 4];
-        dst[u] = (((int64_t)((uint32_t)p % (uint32_t)A.rows_pf) * A.pf_cols + blockIdx.y) * A.Hkv + h) * D + 8 * c;
+        dst[u] = (((int64_t)((uint32_t)p % (uint32_t)A.rows_pf) * A.pf_cols + column) * A.Hkv + h) * D + 8 * c;
       }
     }
 #pragma unroll

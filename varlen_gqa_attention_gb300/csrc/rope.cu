@@ -6,15 +6,20 @@
 // orthogonal), so the backward pass is the same kernel with sin negated.  Dims beyond the rotated
 // ones pass unchanged.
 //
-// Products of a bf16 value and an fp32 cosine have 32 significant bits, and their difference can
-// cancel: each product's rounding error is recovered by a fused multiply-add and each sum's by the
-// two-sum identity, so that a result is the exact one rounded to fp32 (and then to bf16).  A 4-bit
-// code changes by a whole step at its border, so the same input has to fall on the same side of it
-// whatever order a sum was taken in.
+// A result is fma(a, cos, -(b sin)) in fp32, off by at most 2^-24 of |a cos| + |b sin|, rounded to bf16.
+// For keys that is not enough: a 4-bit code changes by a whole step at its border, so the same input
+// has to fall on the same side of it whatever order a sum was taken in, and what the bf16 store
+// holds is what the 4-bit one quantises.  They are the exact results rounded to fp32 and then to
+// bf16: the error bound decides nearly all of them (rot_ends), the others are taken with each
+// product's rounding error recovered by a fused multiply-add and the sum's by the two-sum identity
+// (rot_sum).  For queries, whose neighbours are rounded to bf16 anyway, the exact way would cost
+// half as many instructions again.
+// A lane takes 16 dims of a head, both halves of 8 pairs: 8 angles are loaded once for all the heads
+// of a row that its warp goes through, and nothing is exchanged between lanes.
 //
-// What bounds it: the rows' bytes, read once and written once (a lane holds 8 dims of a head, its
-// pairs' other halves come from a neighbour lane by shuffle, never by a second load), and for a
-// handful of rows the chain of dependent loads (segment, position, angles, row).
+// What bounds it: the rows' bytes, read once and written once, and nearly as much the issue slots
+// (about 9 instructions a dim); for a handful of rows the chain of dependent loads (segment,
+// position, angles), which the rows' own loads start ahead of.
 #include "q4.cuh"
 #include "rope.cuh"
 
@@ -31,136 +36,223 @@ __device__ __forceinline__ float rot_sum(float a, float c, float b, float s) {
   return fabsf(d) < INFINITY ? r : d;  // an infinite row stays what it is: its error terms are NaN
 }
 
+// A pair turned, the quick way: r = fma(a, c, b s) is off by at most 2^-24 of |r| + |b s|.  Rounding to
+// fp32 and to bf16 are both monotone, so where r - E and r + E (E a little more than that, each end
+// rounded once) come to the same bf16, the exact value does too.  Where they do not (one value in
+// some 2^14, or infinities) *unsure is set and the caller takes rot_sum.
+struct Ends {
+  float lo, hi;
+};
+__device__ __forceinline__ Ends rot_ends(float a, float c, float b, float s) {
+  constexpr float k = 0x1.001p-24f;
+  const float q = b * s, r = fmaf(a, c, q);
+  const float t = fabsf(q) + fabsf(r);
+  return {fmaf(t, -k, r), fmaf(t, k, r)};
+}
+__device__ __forceinline__ uint32_t pack_ends(const Ends& x, const Ends& y, uint32_t* unsure) {
+  const uint32_t lo = pack_bf16x2(x.lo, y.lo);
+  *unsure |= lo ^ pack_bf16x2(x.hi, y.hi);
+  return lo;
+}
+
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// What a lane needs to turn dims [8c, 8c + 8) of any head of one row.
-struct LaneTurn {
-  float cs[8], sn[8];  // half-split pairs: one per dim; interleaved: the first four, one per pair
-  int partner;         // lane with the pairs' other halves (half-split)
-  bool turn, second;   // the dims are rotated at all; they are the pairs' second halves
+// The 16 dims of a head that a lane takes: 8 from da on and 8 from db on.  The lanes of a head are
+// D / 16; the first rot_dims / 16 of them turn 8 pairs each, the others pass 16 dims on.
+template <bool IL>
+struct LaneDims {
+  int da, db, j0;  // j0: the first of the lane's pairs
+  bool turn;
+  __device__ __forceinline__ LaneDims(int half, int i) {
+    turn = 8 * i < half;
+    j0 = 8 * i;
+    da = IL || !turn ? 16 * i : 8 * i;
+    db = IL || !turn ? 16 * i + 8 : half + 8 * i;
+  }
+};
+struct Row16 {
+  uint4 a, b;
 };
 
-// Angles of chunk c of a row whose positions are pos[axis].  LPH: lanes per head.
-template <bool IL>
-__device__ __forceinline__ void lane_turn(const RopeArgs& R, const int (&pos)[kRopeAxes], int c, int lane,
-                                          LaneTurn* t) {
-  constexpr int N = IL ? 4 : 8;
-  const int d0 = 8 * c, half = R.half;
-  t->turn = d0 < 2 * half;
-  t->second = !IL && d0 >= half;
-  t->partner = lane;
-  if (!t->turn) return;
-  const int hc = half / 8;
-  if (!IL) t->partner = t->second ? lane - hc : lane + hc;
-  const int j0 = IL ? d0 / 2 : (t->second ? d0 - half : d0);
-  auto axis_pos = [&](int j) {
-    int p = pos[0];
+struct Angles {
+  float cs[8], sn[8];  // of a lane's pairs
+};
+
+// The angles of a row whose positions are pos[axis]: the warp fetches each pair's once (a pair's axis
+// is where its section lies), and the lanes take theirs from shared memory.
+struct PairAngles {
+  float2 v[4];  // pairs lane, lane + 32, ... of the row's (at most 128)
+};
+template <int D>
+__device__ __forceinline__ void fetch_angles(const RopeArgs& R, const int (&pos)[kRopeAxes], int lane, PairAngles* f) {
 #pragma unroll
-    for (int a = 1; a < kRopeAxes; ++a) p = j >= R.sec_end[a - 1] ? pos[a] : p;
-    return p;
-  };
-  const int pf = axis_pos(j0), pl = axis_pos(j0 + N - 1);
-  if (pf == pl) {
-    const float4* src = reinterpret_cast<const float4*>(R.table + (int64_t)pf * half + j0);
+  for (int k = 0; k < D / 64; ++k) {
+    const int j = lane + 32 * k;
+    if (j < R.half) {
+      int p = pos[0];
+      if (R.axes > 1) {
 #pragma unroll
-    for (int k = 0; k < N / 2; ++k) {
-      const float4 v = __ldg(src + k);
-      t->cs[2 * k] = v.x; t->sn[2 * k] = v.y;
-      t->cs[2 * k + 1] = v.z; t->sn[2 * k + 1] = v.w;
-    }
-    if constexpr (N > 2) {
-      // a section that begins and ends inside the chunk has a position of its own between them
-      bool mixed = false;
-#pragma unroll
-      for (int k = 1; k < N - 1; ++k) mixed |= axis_pos(j0 + k) != pf;
-      if (!mixed) {
-        if (R.inverse) {
-#pragma unroll
-          for (int k = 0; k < N; ++k) t->sn[k] = -t->sn[k];
-        }
-        return;
+        for (int a = 1; a < kRopeAxes; ++a) p = j >= R.sec_end[a - 1] ? pos[a] : p;
       }
+      f->v[k] = __ldg(R.table + (uint32_t)(p * R.half + j));  // below 2^31 (checked on the host)
     }
   }
+}
+// sh: the warp's own D / 2 pairs.  Every lane calls it.
+template <int D>
+__device__ __forceinline__ void share_angles(const RopeArgs& R, const PairAngles& f, int j0, int lane, float2* sh,
+                                             Angles* t) {
+  __syncwarp();
 #pragma unroll
-  for (int k = 0; k < N; ++k) {
-    const float2 v = __ldg(R.table + (int64_t)axis_pos(j0 + k) * half + j0 + k);
-    t->cs[k] = v.x;
-    t->sn[k] = R.inverse ? -v.y : v.y;
+  for (int k = 0; k < D / 64; ++k) {
+    const int j = lane + 32 * k;
+    if (j < R.half) sh[j] = R.inverse ? make_float2(f.v[k].x, -f.v[k].y) : f.v[k];
+  }
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float4 v = reinterpret_cast<const float4*>(sh + j0)[k];
+    t->cs[2 * k] = v.x; t->sn[2 * k] = v.y;
+    t->cs[2 * k + 1] = v.z; t->sn[2 * k + 1] = v.w;
   }
 }
 
-// Turns a lane's 8 dims.  Every lane of the warp calls it (shuffles).
-template <bool IL>
-__device__ __forceinline__ uint4 turn8(const uint4& x, const LaneTurn& t) {
-  const uint32_t own[4] = {x.x, x.y, x.z, x.w};
-  uint32_t r[4];
-  if constexpr (IL) {
+// Turns a lane's 8 pairs: (a, b) of pair k are dims da + k and db + k, or 2k and 2k + 1 of the 16.
+template <bool IL, bool EXACT>
+__device__ __forceinline__ void turn16(Row16* x, const Angles& t) {
+  const uint32_t a[4] = {x->a.x, x->a.y, x->a.z, x->a.w}, b[4] = {x->b.x, x->b.y, x->b.z, x->b.w};
+  uint32_t ra[4], rb[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float a = bf_lo(own[k]), b = bf_hi(own[k]);
-      r[k] = pack_bf16x2(rot_sum(a, t.cs[k], b, -t.sn[k]), rot_sum(b, t.cs[k], a, t.sn[k]));
+  for (int k = 0; k < 4; ++k) {
+    // pairs (u, v) at angle i and (w, z) at angle j
+    const float u = bf_lo(a[k]), v = IL ? bf_hi(a[k]) : bf_lo(b[k]);
+    const float w = IL ? bf_lo(b[k]) : bf_hi(a[k]), z = bf_hi(b[k]);
+    const int i = IL ? k : 2 * k, j = IL ? 4 + k : 2 * k + 1;
+    if constexpr (!EXACT) {
+      const float u0 = fmaf(u, t.cs[i], -(v * t.sn[i])), v0 = fmaf(v, t.cs[i], u * t.sn[i]);
+      const float w0 = fmaf(w, t.cs[j], -(z * t.sn[j])), z0 = fmaf(z, t.cs[j], w * t.sn[j]);
+      ra[k] = pack_bf16x2(u0, IL ? v0 : w0);
+      rb[k] = pack_bf16x2(IL ? w0 : v0, z0);
+      continue;
     }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t o = __shfl_sync(0xffffffffu, own[k], t.partner);
-      const float s0 = t.second ? t.sn[2 * k] : -t.sn[2 * k], s1 = t.second ? t.sn[2 * k + 1] : -t.sn[2 * k + 1];
-      r[k] = pack_bf16x2(rot_sum(bf_lo(own[k]), t.cs[2 * k], bf_lo(o), s0),
-                         rot_sum(bf_hi(own[k]), t.cs[2 * k + 1], bf_hi(o), s1));
+    const Ends u1 = rot_ends(u, t.cs[i], v, -t.sn[i]), v1 = rot_ends(v, t.cs[i], u, t.sn[i]);
+    const Ends w1 = rot_ends(w, t.cs[j], z, -t.sn[j]), z1 = rot_ends(z, t.cs[j], w, t.sn[j]);
+    uint32_t unsure = 0;
+    ra[k] = pack_ends(u1, IL ? v1 : w1, &unsure);
+    rb[k] = pack_ends(IL ? w1 : v1, z1, &unsure);
+    if (unsure) {
+      const float u2 = rot_sum(u, t.cs[i], v, -t.sn[i]), v2 = rot_sum(v, t.cs[i], u, t.sn[i]);
+      const float w2 = rot_sum(w, t.cs[j], z, -t.sn[j]), z2 = rot_sum(z, t.cs[j], w, t.sn[j]);
+      ra[k] = pack_bf16x2(u2, IL ? v2 : w2);
+      rb[k] = pack_bf16x2(IL ? w2 : v2, z2);
     }
   }
-  return t.turn ? make_uint4(r[0], r[1], r[2], r[3]) : x;
+  x->a = make_uint4(ra[0], ra[1], ra[2], ra[3]);
+  x->b = make_uint4(rb[0], rb[1], rb[2], rb[3]);
 }
 
-// Positions of row t on every axis that has pairs; false when one of them is outside the table.
-__device__ __forceinline__ bool row_positions(const RopeArgs& R, int64_t t, int64_t p, int (&pos)[kRopeAxes]) {
+__device__ __forceinline__ uint4 ldg16(const __nv_bfloat16* p) { return *reinterpret_cast<const uint4*>(p); }
+__device__ __forceinline__ void stg16(__nv_bfloat16* p, const uint4& v) { *reinterpret_cast<uint4*>(p) = v; }
+
+// Positions of row t on every axis (p where none are given).
+__device__ __forceinline__ void fetch_positions(const RopeArgs& R, int64_t t, int p, int (&pos)[kRopeAxes]) {
+#pragma unroll
+  for (int a = 0; a < kRopeAxes; ++a) {
+    pos[a] = p;
+    if (R.pos && a < R.axes) pos[a] = __ldg(R.pos + a * R.pos_stride + t);
+  }
+}
+// Whether those of the axes that have pairs lie in the table; the others, and all when one does not,
+// are set to a row that does.
+__device__ __forceinline__ bool check_positions(const RopeArgs& R, int (&pos)[kRopeAxes]) {
   bool ok = true;
 #pragma unroll
   for (int a = 0; a < kRopeAxes; ++a) {
-    pos[a] = 0;
-    const int begin = a > 0 ? R.sec_end[a - 1] : 0;
-    if (a < R.axes && R.sec_end[a] > begin) {
-      const int64_t v = R.pos ? (int64_t)R.pos[a * R.pos_stride + t] : p;
-      ok = ok && v >= 0 && v < R.P;
-      pos[a] = ok ? (int)v : 0;
-    }
+    const bool used = a < R.axes && R.sec_end[a] > (a > 0 ? R.sec_end[a - 1] : 0);
+    const bool in = (uint32_t)pos[a] < (uint32_t)R.P;
+    ok = ok && (in || !used);
+    pos[a] = in ? pos[a] : 0;
   }
   return ok;
 }
 
-constexpr int kRopeUnroll = 4;  // heads of one lane in flight
-
-// One warp: row t, 32 / LPH * kRopeUnroll heads.
+// A warp takes runs of a row's heads (`parts` runs a row), 32 / (D / 16) heads a pass, one run after
+// another.  Two passes are always on their way, those of the next run when its own come to an end,
+// with that run's angles and the positions of the run after it, so that the chain position - angle -
+// rows is waited for once.
 template <int D, bool IL>
-__global__ void __launch_bounds__(kRopeThreads) sdpa_rope_kernel(RopeRowsArgs A) {
-  constexpr int LPH = D / 8, HPP = 32 / LPH, HPW = HPP * kRopeUnroll;
-  const int lane = threadIdx.x & 31, c = lane % LPH;
-  const int64_t blocks = (A.H + HPW - 1) / HPW;
-  const int64_t n = A.T * blocks, stride = (int64_t)gridDim.x * (kRopeThreads / 32);
-  for (int64_t w = ((int64_t)blockIdx.x * kRopeThreads + threadIdx.x) >> 5; w < n; w += stride) {
-    const int64_t t = udiv(w, blocks);
-    const int h0 = (int)(w - t * blocks) * HPW + lane / LPH;
-    uint4 x[kRopeUnroll];
-#pragma unroll
-    for (int u = 0; u < kRopeUnroll; ++u)
-      if (h0 + u * HPP < A.H)
-        x[u] = *reinterpret_cast<const uint4*>(A.x + t * A.x_rs + (int64_t)(h0 + u * HPP) * A.x_hs + 8 * c);
-      else
-        x[u] = make_uint4(0, 0, 0, 0);
-    int pos[kRopeAxes];
-    const bool ok = row_positions(A.r, t, 0, pos);
-    if (!ok && h0 == 0 && c == 0 && A.status_dev) atomicOr(A.status_dev, SDPA_ROPE_BAD_POS);
-    LaneTurn lt;
-    lane_turn<IL>(A.r, pos, c, lane, &lt);
-#pragma unroll
-    for (int u = 0; u < kRopeUnroll; ++u) {
-      uint4 y = turn8<IL>(x[u], lt);
-      if (!ok) y = make_uint4(0, 0, 0, 0);
-      if (h0 + u * HPP < A.H)
-        *reinterpret_cast<uint4*>(A.out + t * A.o_rs + (int64_t)(h0 + u * HPP) * A.o_hs + 8 * c) = y;
+__global__ void __launch_bounds__(kRopeThreads, 3) sdpa_rope_kernel(RopeRowsArgs A) {
+  constexpr int LPH = D / 16, HPP = 32 / LPH;
+  __shared__ __align__(16) float2 s_angles[kRopeThreads / 32][D / 2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, hs = lane / LPH;
+  const LaneDims<IL> ld(A.r.half, lane % LPH);
+  const int j0 = ld.turn ? ld.j0 : 0;
+  const int passes = (A.H + HPP - 1) / HPP;
+  const int64_t n = A.T * A.parts, stride = (int64_t)gridDim.x * (kRopeThreads / 32);
+  struct Run {
+    int64_t t;
+    int p0, p1;
+  };
+  auto run_of = [&](int64_t w) -> Run {
+    if (A.parts == 1) return {w, 0, passes};
+    const int64_t t = udiv(w, A.parts);
+    const int part = (int)(w - t * A.parts);
+    return {t, passes * part / A.parts, passes * (part + 1) / A.parts};
+  };
+  Row16 x[2];
+  auto load = [&](Row16* y, const Run& run, int p) {
+    const int h = p * HPP + hs;
+    if (p < run.p1 && h < A.H) {
+      const __nv_bfloat16* src = A.x + run.t * A.x_rs + (int64_t)h * A.x_hs;
+      y->a = ldg16(src + ld.da);
+      y->b = ldg16(src + ld.db);
     }
+  };
+  int64_t w = (int64_t)blockIdx.x * (kRopeThreads / 32) + warp;
+  if (w >= n) return;
+  Run run = run_of(w);
+  load(&x[0], run, run.p0);
+  load(&x[1], run, run.p0 + 1);
+  int pos[kRopeAxes], pos1[kRopeAxes] = {0, 0, 0, 0};  // of this run's row and the next one's
+  fetch_positions(A.r, run.t, 0, pos);
+  if (w + stride < n) fetch_positions(A.r, run_of(w + stride).t, 0, pos1);
+  bool ok = check_positions(A.r, pos);
+  PairAngles pa;
+  fetch_angles<D>(A.r, pos, lane, &pa);
+  for (;; w += stride) {
+    Angles an;
+    share_angles<D>(A.r, pa, j0, lane, s_angles[warp], &an);
+    if (!ok && run.p0 == 0 && lane == 0 && A.status_dev) atomicOr(A.status_dev, SDPA_ROPE_BAD_POS);
+    const bool more = w + stride < n;
+    const Run next = run_of(more ? w + stride : w);
+    bool ok1 = true;
+    if (more) {
+      ok1 = check_positions(A.r, pos1);
+      fetch_angles<D>(A.r, pos1, lane, &pa);
+      if (w + 2 * stride < n) fetch_positions(A.r, run_of(w + 2 * stride).t, 0, pos1);
+    }
+    for (int p = run.p0; p < run.p1; p += 2) {
+      const bool last = p + 2 >= run.p1;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int h = (p + u) * HPP + hs;
+        if (p + u < run.p1 && h < A.H) {
+          if (ld.turn) turn16<IL, false>(&x[u], an);
+          if (!ok) x[u].a = x[u].b = make_uint4(0, 0, 0, 0);
+          __nv_bfloat16* y = A.out + run.t * A.o_rs + (int64_t)h * A.o_hs;
+          stg16(y + ld.da, x[u].a);
+          stg16(y + ld.db, x[u].b);
+        }
+        if (!last)
+          load(&x[u], run, p + 2 + u);
+        else if (more)
+          load(&x[u], next, next.p0 + u);
+      }
+    }
+    if (!more) return;
+    run = next;
+    ok = ok1;
   }
 }
 
@@ -176,20 +268,24 @@ struct RowTable {
 };
 
 __device__ __forceinline__ void find_rows(const StepArgs& A, int64_t t0, int n, RowTable* s) {
-  for (int r = threadIdx.x; r < n; r += blockDim.x) {
-    s->owner[r] = -1;
-    s->dead[r] = 0;
-  }
-  __syncthreads();
   auto load = [&](int i, int4* g) -> int32_t {
     *g = __ldg(reinterpret_cast<const int4*>(A.seq_info) + i);
     const int window = A.seg_mode ? __ldg(A.seg_mode + 2 * i + 1) : A.window;
     return segment_bits(g->x, g->y, g->z, g->w, A.T, A.rows, A.cols, window);
   };
+  const int tid = threadIdx.x;
+  int4 g0 = make_int4(0, 0, 0, 0);  // a thread keeps its first segment
+  int32_t bits0 = 0;
+  if (tid < A.S) bits0 = load(tid, &g0);
+  if (tid < n) {
+    s->owner[tid] = -1;
+    s->dead[tid] = 0;
+  }
+  __syncthreads();
   int32_t bits = 0;
-  for (int i = threadIdx.x; i < A.S; i += blockDim.x) {
-    int4 g;
-    const int32_t b = load(i, &g);
+  for (int i = tid; i < A.S; i += kRopeThreads) {
+    int4 g = g0;
+    const int32_t b = i == tid ? bits0 : load(i, &g);
     bits |= b;
     if (b || g.y <= 0) continue;
     const int a = (int)max((int64_t)0, (int64_t)g.x - t0), e = (int)min((int64_t)n, (int64_t)g.x + g.y - t0);
@@ -202,10 +298,12 @@ __device__ __forceinline__ void find_rows(const StepArgs& A, int64_t t0, int n, 
   }
   if (blockIdx.x == 0 && bits && A.status_dev) atomicOr(A.status_dev, bits);
   __syncthreads();
+  if (A.S <= 1) return;
   // whether another valid segment meets an owner outside these rows
-  for (int i = threadIdx.x; i < A.S; i += blockDim.x) {
-    int4 g;
-    if (load(i, &g) || g.y <= 0) continue;
+  for (int i = tid; i < A.S; i += kRopeThreads) {
+    int4 g = g0;
+    const int32_t b = i == tid ? bits0 : load(i, &g);
+    if (b || g.y <= 0) continue;
     for (int r = 0; r < n; ++r) {
       const int o = s->owner[r];
       if (o < 0 || o == i) continue;
@@ -214,8 +312,7 @@ __device__ __forceinline__ void find_rows(const StepArgs& A, int64_t t0, int n, 
     }
   }
   __syncthreads();
-  for (int r = threadIdx.x; r < n; r += blockDim.x)
-    if (s->dead[r] && A.status_dev) atomicOr(A.status_dev, SDPA_SEG_OVERLAP);
+  if (tid < n && s->dead[tid] && A.status_dev) atomicOr(A.status_dev, SDPA_SEG_OVERLAP);
 }
 
 // Position of row t0 + r in its sequence, or -1 when no live segment holds it (or it has none).
@@ -226,88 +323,189 @@ __device__ __forceinline__ int64_t row_place(const RowTable* s, int64_t t0, int 
   return (int64_t)g.w - g.y + (t0 + r - g.x);
 }
 
-// Largest magnitude of a lane's 8 bf16 values (NaN counts as 0), over the 4 lanes of a scale group.
-__device__ __forceinline__ float group_amax(const uint4& x) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+// A lane's 8 bf16 values with NaN as 0, clamped to what the largest scale holds (7 * 1920).
+__device__ __forceinline__ uint32_t q4_storable(uint32_t w) {
+  __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&w);
+  const uint32_t clean = w & __heq2_mask(v, v);
+  v = *reinterpret_cast<const __nv_bfloat162*>(&clean);
+  v = __hmin2(__hmax2(v, __float2bfloat162_rn(-13440.f)), __float2bfloat162_rn(13440.f));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float amax8(const uint32_t (&w)[4]) {
   float m = 0.f;
 #pragma unroll
   for (int k = 0; k < 4; ++k) m = fmaxf(m, fmaxf(fabsf(bf_lo(w[k])), fabsf(bf_hi(w[k]))));
-  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  return m;
 }
-__device__ __forceinline__ uint32_t codes8(const uint4& x, float s) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+// The codes of 8 values.  A code is the quotient x / s rounded to even.  The quotient comes from s's
+// rounded reciprocal with one Newton step, which leaves it exact where it is a short number, as at
+// a border between two codes; elsewhere it is at least 2^-11 away from one (x has 8 significant
+// bits, s has 4).  Adding 1.5 * 2^23 rounds it and leaves the code's two's complement in the low bits;
+// the nibble is that with its top bit turned.  |x| / s < 7.5 (see q4_scale_byte) needs no clamp.
+__device__ __forceinline__ uint32_t codes8(const uint32_t (&w)[4], uint32_t scale_byte) {
+  const float s = q4_scale(scale_byte), r = __frcp_rn(s);
+  auto code = [&](float v) {
+    float q = v * r;
+    q = fmaf(fmaf(-q, s, v), r, q);
+    return __float_as_uint(q + 12582912.f) & 15u;
+  };
   uint32_t c = 0;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) c |= (q4_code(bf_lo(w[k]), s) | q4_code(bf_hi(w[k]), s) << 4) << (8 * k);
-  return c;
+  for (int k = 0; k < 4; ++k) c |= code(bf_lo(w[k])) << (8 * k) | code(bf_hi(w[k])) << (8 * k + 4);
+  return c ^ 0x88888888u;
+}
+// Largest magnitudes of the scale groups that a lane's two chunks belong to, from the chunks' own.
+// `side`: the chunks lie side by side (dims 16 i ..), so that a group is two neighbouring lanes'; else
+// they are half apart, and a group is four lanes' when half is whole groups.  Every lane calls it.
+template <int LPH>
+__device__ __forceinline__ void group_amax(float* ma, float* mb, bool side_by_side, int half, int lane) {
+  if (side_by_side) {
+    const float m = fmaxf(*ma, *mb);
+    *ma = *mb = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  } else if (half % 32 == 0) {
+    // (lanes past the turned ones hold side-by-side chunks, in whole groups too)
+    const bool mine = 8 * (lane % LPH) < half;
+    const float m = fmaxf(*ma, *mb);
+    const float two = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    float a = fmaxf(*ma, __shfl_xor_sync(0xffffffffu, *ma, 1));
+    float b = fmaxf(*mb, __shfl_xor_sync(0xffffffffu, *mb, 1));
+    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+    b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 2));
+    *ma = mine ? a : two;
+    *mb = mine ? b : two;
+  } else {
+    // any other split: look each chunk of both groups up where it lies
+    const int base = lane - lane % LPH, h8 = half / 8, i = lane % LPH;
+    const int ca = i < h8 ? i : 2 * i, cb = i < h8 ? h8 + i : 2 * i + 1;
+    float out[2] = {0.f, 0.f};
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int c = ((g ? cb : ca) & ~3) + k;
+        const int at = c < h8 ? c : c < 2 * h8 ? c - h8 : c / 2;
+        const bool first = c < h8 || (c >= 2 * h8 && c % 2 == 0);
+        const float va = __shfl_sync(0xffffffffu, *ma, base + at), vb = __shfl_sync(0xffffffffu, *mb, base + at);
+        out[g] = fmaxf(out[g], first ? va : vb);
+      }
+    }
+    *ma = out[0];
+    *mb = out[1];
+  }
 }
 
 // A step's rows: queries rotated into q_out, keys rotated and values as they are into the store.
-// A CTA takes `cr` packed rows; a warp takes a row and 32 / LPH * kRopeUnroll heads of its q, k or v.
+// A CTA takes `cr` packed rows; a warp takes one of `parts` runs of a row's passes (32 / (D / 16)
+// heads each), which are those of q, then k, then v.  The next pass is on its way while one is
+// worked on, and the first ones while the rows' segments are looked up.
 template <int D, bool IL, bool Q4>
-__global__ void __launch_bounds__(kRopeThreads) sdpa_rope_append_kernel(StepArgs A) {
+__global__ void __launch_bounds__(kRopeThreads, 3) sdpa_rope_append_kernel(StepArgs A) {
+  constexpr int LPH = D / 16, HPP = 32 / LPH;
   __shared__ RowTable s_rows;
-  constexpr int LPH = D / 8, HPP = 32 / LPH, HPW = HPP * kRopeUnroll;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane % LPH, hs = lane / LPH;
+  __shared__ __align__(16) float2 s_angles[kRopeThreads / 32][D / 2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, hs = lane / LPH;
+  const LaneDims<IL> ld(A.r.half, lane % LPH);
   const int64_t t0 = (int64_t)blockIdx.x * A.cr;
   const int n = (int)min((int64_t)A.cr, A.T - t0);
+  const int pq = (A.Hq + HPP - 1) / HPP, pk = (A.Hkv + HPP - 1) / HPP, passes = pq + 2 * pk;
+
+  Row16 x[2];
+  auto load = [&](Row16* y, int64_t t, int q, int p1) {
+    y->a = y->b = make_uint4(0, 0, 0, 0);
+    const int what = q < pq ? 0 : q < pq + pk ? 1 : 2;
+    const int h = (q - (what == 0 ? 0 : what == 1 ? pq : pq + pk)) * HPP + hs;
+    if (q < p1 && h < (what == 0 ? A.Hq : A.Hkv)) {
+      const __nv_bfloat16* z = what == 0 ? A.q + t * A.q_rs + (int64_t)h * A.q_hs
+                               : what == 1 ? A.k + t * A.k_rs + (int64_t)h * A.k_hs
+                                           : A.v + t * A.v_rs + (int64_t)h * A.v_hs;
+      y->a = ldg16(z + ld.da);
+      y->b = ldg16(z + ld.db);
+    }
+  };
+  auto run_of = [&](int w, int* r, int* p0, int* p1) {
+    *r = w;
+    *p0 = 0;
+    *p1 = passes;
+    if (A.parts > 1) {
+      *r = w / A.parts;
+      const int part = w - *r * A.parts;
+      *p0 = passes * part / A.parts;
+      *p1 = passes * (part + 1) / A.parts;
+    }
+  };
+  int r = 0, p0 = 0, p1 = 0;
+  run_of(warp, &r, &p0, &p1);
+  if (warp < n * A.parts) {
+    load(&x[0], t0 + r, p0, p1);
+    load(&x[1], t0 + r, p0 + 1, p1);
+  }
   find_rows(A, t0, n, &s_rows);
 
-  const int qb = (A.Hq + HPW - 1) / HPW, kb = (A.Hkv + HPW - 1) / HPW, per = qb + 2 * kb;
-  for (int w = warp; w < n * per; w += kRopeThreads / 32) {
-    const int r = w / per, b = w - r * per;
+  for (int w = warp; w < n * A.parts; w += kRopeThreads / 32) {
+    if (w != warp) {
+      run_of(w, &r, &p0, &p1);
+      load(&x[0], t0 + r, p0, p1);
+      load(&x[1], t0 + r, p0 + 1, p1);
+    }
     const int64_t t = t0 + r;
-    const int what = b < qb ? 0 : b < qb + kb ? 1 : 2;  // q, k, v
-    const int h0 = (b - (what == 0 ? 0 : what == 1 ? qb : qb + kb)) * HPW + hs;
-    const int H = what == 0 ? A.Hq : A.Hkv;
-    const __nv_bfloat16* src = what == 0 ? A.q : what == 1 ? A.k : A.v;
-    const int64_t rs = what == 0 ? A.q_rs : what == 1 ? A.k_rs : A.v_rs;
-    const int64_t xs = what == 0 ? A.q_hs : what == 1 ? A.k_hs : A.v_hs;
-    uint4 x[kRopeUnroll];
-#pragma unroll
-    for (int u = 0; u < kRopeUnroll; ++u) {
-      x[u] = make_uint4(0, 0, 0, 0);
-      if (h0 + u * HPP < H)
-        x[u] = *reinterpret_cast<const uint4*>(src + t * rs + (int64_t)(h0 + u * HPP) * xs + 8 * c);
-    }
     int col = 0;
-    const int64_t p = row_place(&s_rows, t0, r, &col);
-    int pos[kRopeAxes];
-    const bool in = p < 0 || row_positions(A.r, t, p, pos);
-    const bool ok = p >= 0 && in;
-    if (!in && what == 0 && h0 == 0 && c == 0 && A.status_dev) atomicOr(A.status_dev, SDPA_ROPE_BAD_POS);
-    if (what > 0 && !ok) continue;  // nothing of the row is kept (the warp has one row)
-    if (what < 2 && ok) {
-      LaneTurn lt;
-      lane_turn<IL>(A.r, pos, c, lane, &lt);
-#pragma unroll
-      for (int u = 0; u < kRopeUnroll; ++u) x[u] = turn8<IL>(x[u], lt);
+    const int64_t place = row_place(&s_rows, t0, r, &col);
+    int pos[kRopeAxes] = {0, 0, 0, 0};
+    if (place >= 0) fetch_positions(A.r, t, (int)place, pos);
+    const bool in = check_positions(A.r, pos);
+    const bool ok = place >= 0 && in;
+    if (!in && p0 == 0 && lane == 0 && A.status_dev) atomicOr(A.status_dev, SDPA_ROPE_BAD_POS);
+    Angles an;
+    if (ok && p0 < pq + pk) {
+      PairAngles pa;
+      fetch_angles<D>(A.r, pos, lane, &pa);
+      share_angles<D>(A.r, pa, ld.turn ? ld.j0 : 0, lane, s_angles[warp], &an);
     }
-    if (what == 0) {
-#pragma unroll
-      for (int u = 0; u < kRopeUnroll; ++u)
-        if (h0 + u * HPP < H)
-          *reinterpret_cast<uint4*>(A.q_out + t * A.o_rs + (int64_t)(h0 + u * HPP) * A.o_hs + 8 * c) =
-              ok ? x[u] : make_uint4(0, 0, 0, 0);
-      continue;
-    }
-    const int64_t row = (uint32_t)p % (uint32_t)A.rows;  // both below 2^31
-#pragma unroll
-    for (int u = 0; u < kRopeUnroll; ++u) {
-      const int h = h0 + u * HPP;
-      if constexpr (Q4) {
-        const uint32_t sb = q4_scale_byte(group_amax(x[u]));
-        if (h < H) {
-          const int64_t cell = ((int64_t)col * A.Hkv + h) * A.rows + row;
-          uint8_t* codes = what == 1 ? A.q4.kc : A.q4.vc;
-          uint8_t* scales = what == 1 ? A.q4.ks : A.q4.vs;
-          *reinterpret_cast<uint32_t*>(codes + cell * (D / 2) + 4 * c) = codes8(x[u], q4_scale(sb));
-          if (c % 4 == 0) scales[cell * (D / kQ4Group) + c / 4] = (uint8_t)sb;
+    const uint32_t row = (uint32_t)place % (uint32_t)A.rows;  // both below 2^31
+    const int64_t cell0 = Q4 ? (int64_t)col * A.Hkv * A.rows + row : ((int64_t)row * A.cols + col) * A.Hkv;
+
+    auto work = [&](Row16& y, int q) {
+      const int what = q < pq ? 0 : q < pq + pk ? 1 : 2;
+      const int h = (q - (what == 0 ? 0 : what == 1 ? pq : pq + pk)) * HPP + hs;
+      if (what > 0 && !ok) return;  // nothing of the row is kept
+      if (what == 0) {
+        if (ok && ld.turn) turn16<IL, false>(&y, an);
+        if (h < A.Hq) {
+          if (!ok) y.a = y.b = make_uint4(0, 0, 0, 0);
+          __nv_bfloat16* z = A.q_out + t * A.o_rs + (int64_t)h * A.o_hs;
+          stg16(z + ld.da, y.a);
+          stg16(z + ld.db, y.b);
         }
-      } else if (h < H) {
-        __nv_bfloat16* st = what == 1 ? A.k_store : A.v_store;
-        *reinterpret_cast<uint4*>(st + ((row * A.cols + col) * A.Hkv + h) * (int64_t)D + 8 * c) = x[u];
+        return;
+      }
+      if (what == 1 && ld.turn) turn16<IL, true>(&y, an);
+      if constexpr (Q4) {
+        const uint32_t wa[4] = {q4_storable(y.a.x), q4_storable(y.a.y), q4_storable(y.a.z), q4_storable(y.a.w)};
+        const uint32_t wb[4] = {q4_storable(y.b.x), q4_storable(y.b.y), q4_storable(y.b.z), q4_storable(y.b.w)};
+        float ma = amax8(wa), mb = amax8(wb);
+        group_amax<LPH>(&ma, &mb, IL, A.r.half, lane);
+        const uint32_t ba = q4_scale_byte(ma), bb = q4_scale_byte(mb);
+        if (h < A.Hkv) {
+          const int64_t cell = cell0 + (int64_t)h * A.rows;
+          uint8_t* codes = (what == 1 ? A.q4.kc : A.q4.vc) + cell * (D / 2);
+          uint8_t* scales = (what == 1 ? A.q4.ks : A.q4.vs) + cell * (D / kQ4Group);
+          *reinterpret_cast<uint32_t*>(codes + ld.da / 2) = codes8(wa, ba);
+          *reinterpret_cast<uint32_t*>(codes + ld.db / 2) = codes8(wb, bb);
+          if (ld.da % kQ4Group == 0) scales[ld.da / kQ4Group] = (uint8_t)ba;
+          if (ld.db % kQ4Group == 0) scales[ld.db / kQ4Group] = (uint8_t)bb;
+        }
+      } else if (h < A.Hkv) {
+        __nv_bfloat16* z = (what == 1 ? A.k_store : A.v_store) + (cell0 + h) * (int64_t)D;
+        stg16(z + ld.da, y.a);
+        stg16(z + ld.db, y.b);
+      }
+    };
+    for (int p = p0; p < p1; p += 2) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (p + u >= p1) break;
+        work(x[u], p + u);
+        load(&x[u], t, p + u + 2, p1);
       }
     }
   }
@@ -318,23 +516,39 @@ __global__ void __launch_bounds__(kRopeThreads) sdpa_rope_append_kernel(StepArgs
 template <int D>
 __global__ void __launch_bounds__(kRopeThreads) sdpa_q4_unpack_kernel(StepArgs A) {
   __shared__ RowTable s_rows;
-  constexpr int LPH = D / 8;
+  constexpr int LPH = D / 8, U = 4;
   const int64_t t0 = (int64_t)blockIdx.x * A.cr;
   const int n = (int)min((int64_t)A.cr, A.T - t0);
   find_rows(A, t0, n, &s_rows);
   const int per = A.Hkv * LPH;  // chunks of 8 dims of a row
-  for (int w = threadIdx.x; w < n * per; w += kRopeThreads) {
-    const int r = w / per, x = w - r * per, h = x / LPH, c = x % LPH;
-    int col = 0;
-    const int64_t p = row_place(&s_rows, t0, r, &col);
-    const int64_t cell = p < 0 ? 0 : ((int64_t)col * A.Hkv + h) * A.rows + (uint32_t)p % (uint32_t)A.rows;
+  for (int w0 = threadIdx.x; w0 < n * per; w0 += U * kRopeThreads) {
+    uint32_t kw[U], vw[U], kb[U], vb[U];
+    int64_t dst[U];
+    bool there[U];
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      uint4 y = make_uint4(0, 0, 0, 0);
-      if (p >= 0) y = q4_words8(*reinterpret_cast<const uint32_t*>((v ? A.q4.vc : A.q4.kc) + cell * (D / 2) + 4 * c),
-                                (v ? A.q4.vs : A.q4.ks)[cell * (D / kQ4Group) + c / 4]);
-      __nv_bfloat16* dst = v ? A.v_out : A.k_out;
-      *reinterpret_cast<uint4*>(dst + (t0 + r) * A.o_rs + (int64_t)h * A.o_hs + 8 * c) = y;
+    for (int u = 0; u < U; ++u) {
+      const int w = w0 + u * kRopeThreads;
+      dst[u] = -1;
+      if (w >= n * per) continue;
+      const int r = w / per, x = w - r * per, h = x / LPH, c = x % LPH;
+      int col = 0;
+      const int64_t p = row_place(&s_rows, t0, r, &col);
+      there[u] = p >= 0;
+      if (there[u]) {
+        const int64_t cell = ((int64_t)col * A.Hkv + h) * A.rows + (uint32_t)p % (uint32_t)A.rows;
+        kw[u] = *reinterpret_cast<const uint32_t*>(A.q4.kc + cell * (D / 2) + 4 * c);
+        vw[u] = *reinterpret_cast<const uint32_t*>(A.q4.vc + cell * (D / 2) + 4 * c);
+        kb[u] = A.q4.ks[cell * (D / kQ4Group) + c / 4];
+        vb[u] = A.q4.vs[cell * (D / kQ4Group) + c / 4];
+      }
+      dst[u] = (t0 + r) * A.o_rs + (int64_t)h * A.o_hs + 8 * c;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (dst[u] < 0) continue;
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      stg16(A.k_out + dst[u], there[u] ? q4_words8(kw[u], kb[u]) : zero);
+      stg16(A.v_out + dst[u], there[u] ? q4_words8(vw[u], vb[u]) : zero);
     }
   }
 }
@@ -365,6 +579,6 @@ const void* q4_unpack_kernel_ptr(int D) {
     default: return (const void*)sdpa_q4_unpack_kernel<256>;
   }
 }
-int rope_heads_per_warp(int D) { return 32 / (D / 8) * kRopeUnroll; }
+int rope_heads_per_pass(int D) { return 32 / (D / 16); }
 
 }  // namespace sdpa

@@ -26,7 +26,7 @@ struct RopeRowsArgs {
   const __nv_bfloat16* x;
   __nv_bfloat16* out;
   int64_t x_rs, x_hs, o_rs, o_hs, T;
-  int H;
+  int H, parts;  // parts: warps that share a row
   int32_t* status_dev;
 };
 
@@ -36,7 +36,7 @@ struct StepArgs {
   const int32_t* seq_info;
   const int32_t* seg_mode;  // NULL, or [S, 2] (causal, window)
   int S, window, cols, Hq, Hkv;
-  int cr;                   // packed rows per CTA
+  int cr, parts;            // packed rows per CTA; warps that share a row
   int64_t T, rows;
   const __nv_bfloat16 *q, *k, *v;
   int64_t q_rs, q_hs, k_rs, k_hs, v_rs, v_hs;
@@ -50,6 +50,6 @@ struct StepArgs {
 const void* rope_kernel_ptr(int D, bool interleaved);
 const void* rope_append_kernel_ptr(int D, bool interleaved, bool q4);
 const void* q4_unpack_kernel_ptr(int D);
-int rope_heads_per_warp(int D);  // heads of one row that a warp takes
+int rope_heads_per_pass(int D);  // heads of one row that a warp takes at a time
 
 }  // namespace sdpa

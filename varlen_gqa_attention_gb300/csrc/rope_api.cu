@@ -39,6 +39,9 @@ sdpa_status take_rotation(const sdpa_rotation* r, int64_t T, int D, bool own_pos
     return fail(SDPA_ERR_SHAPE, "table_rows %lld outside [1, 2^31)", (long long)r->table_rows);
   if (r->rot_dims < 16 || r->rot_dims > D || r->rot_dims % 16)
     return fail(SDPA_ERR_ARG, "rot_dims %d: a multiple of 16, at most the head dim %d", r->rot_dims, D);
+  if (r->table_rows * (r->rot_dims / 2) > INT_MAX)
+    return fail(SDPA_ERR_SHAPE, "a table of %lld x %d pairs: at most 2^31 - 1", (long long)r->table_rows,
+                r->rot_dims / 2);
   if (r->axes < 1 || r->axes > kRopeAxes) return fail(SDPA_ERR_ARG, "%d position axes: 1 to %d", r->axes, kRopeAxes);
   if (!r->positions && T > 0 && !(own_position && r->axes == 1))
     return fail(SDPA_ERR_NULL, "positions is NULL%s", own_position ? " and there are several axes" : "");
@@ -76,14 +79,27 @@ sdpa_status check_step(int64_t T, int Hq, int Hkv, int D, int S, int64_t rows, i
   return SDPA_OK;
 }
 
-// A CTA looks through the whole table for its rows, so it takes several rows once there are enough
-// for every SM to have a few CTAs.
-sdpa_status launch_step(const void* f, StepArgs& A, cudaStream_t stream, const char* what) {
+// Warps that share a row of `passes` passes: enough for 24 warps on every SM, at most one a pass.
+int row_parts(int64_t T, int passes, int sms) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>(passes, 24 * (int64_t)sms / std::max<int64_t>(T, 1)));
+}
+
+// `passes` of a row, or 0 for a kernel whose threads share its CTA's rows.  A CTA looks through the
+// whole table for its rows, so it takes as many as its warps have work for, and twice that once
+// every SM has three such CTAs.
+sdpa_status launch_step(const void* f, StepArgs& A, int passes, cudaStream_t stream, const char* what) {
   if (A.T == 0) return SDPA_OK;
   int sms = 0;
   sdpa_status st = device_sms(&sms);
   if (st) return st;
-  A.cr = (int)std::max<int64_t>(1, std::min<int64_t>(kStepRows, A.T / (8 * (int64_t)sms)));
+  if (passes > 0) {
+    A.parts = row_parts(A.T, passes, sms);
+    A.cr = std::max(1, kRopeThreads / 32 / A.parts);
+    if (A.T >= 6 * (int64_t)sms * A.cr) A.cr *= 2;
+  } else {
+    A.cr = (int)(A.T / (3 * (int64_t)sms));
+  }
+  A.cr = std::max(1, std::min(kStepRows, A.cr));
   void* args[] = {(void*)&A};
   const int64_t grid = (A.T + A.cr - 1) / A.cr;
   cudaError_t e = cudaLaunchKernel(f, dim3((unsigned)grid), dim3(kRopeThreads), args, 0, stream);
@@ -137,8 +153,9 @@ sdpa_status rope_append(const void* q, int64_t q_rs, int64_t q_hs, const void* k
   A.k_store = (__nv_bfloat16*)k_store;
   A.v_store = (__nv_bfloat16*)v_store;
   A.status_dev = status_dev;
-  return launch_step(rope_append_kernel_ptr(D, rotation->interleaved != 0, q4 != nullptr), A, (cudaStream_t)stream,
-                     "rotated append");
+  const int hpp = rope_heads_per_pass(D), passes = (Hq + hpp - 1) / hpp + 2 * ((Hkv + hpp - 1) / hpp);
+  return launch_step(rope_append_kernel_ptr(D, rotation->interleaved != 0, q4 != nullptr), A, passes,
+                     (cudaStream_t)stream, "rotated append");
 }
 
 }  // namespace
@@ -173,9 +190,10 @@ sdpa_status sdpa_rope(const void* x, int64_t T, int H, int D, int64_t x_row_stri
   A.T = T;
   A.H = H;
   A.status_dev = status_dev;
-  const int hpw = rope_heads_per_warp(D);
-  const int64_t warps = T * ((H + hpw - 1) / hpw);
-  const int64_t blocks = std::min<int64_t>((warps * 32 + kRopeThreads - 1) / kRopeThreads, (int64_t)sms * 64);
+  const int hpp = rope_heads_per_pass(D);
+  A.parts = row_parts(T, (H + hpp - 1) / hpp, sms);
+  const int64_t warps = T * A.parts;
+  const int64_t blocks = std::min<int64_t>((warps * 32 + kRopeThreads - 1) / kRopeThreads, (int64_t)sms * 3);
   void* args[] = {(void*)&A};
   cudaError_t e = cudaLaunchKernel(rope_kernel_ptr(D, rotation->interleaved != 0), dim3((unsigned)blocks),
                                    dim3(kRopeThreads), args, 0, (cudaStream_t)stream);
@@ -236,7 +254,7 @@ sdpa_status sdpa_fourbit_unpack(const sdpa_q4_store* store, int64_t rows, int co
   A.o_rs = o_row_stride;
   A.o_hs = o_head_stride;
   A.status_dev = status_dev;
-  return launch_step(q4_unpack_kernel_ptr(D), A, (cudaStream_t)stream, "4-bit unpack");
+  return launch_step(q4_unpack_kernel_ptr(D), A, 0, (cudaStream_t)stream, "4-bit unpack");
 }
 
 }  // extern "C"
