@@ -264,7 +264,9 @@ __global__ void __launch_bounds__(kRopeThreads, 3) sdpa_rope_kernel(RopeRowsArgs
 struct RowTable {
   int owner[kStepRows];
   int dead[kStepRows];
-  int4 seg[kStepRows];  // the owner's entry
+  int4 seg[kStepRows];   // the owner's entry
+  int2 cell[kStepRows];  // (store row, column), or (-1, 0): nothing of the row is kept
+  int pos[kStepRows][kRopeAxes];
 };
 
 __device__ __forceinline__ void find_rows(const StepArgs& A, int64_t t0, int n, RowTable* s) {
@@ -394,120 +396,139 @@ __device__ __forceinline__ void group_amax(float* ma, float* mb, bool side_by_si
   }
 }
 
+// The rest of what the warps need of rows [t0, t0 + n): where each goes, and its positions.
+__device__ __forceinline__ void place_rows(const StepArgs& A, int64_t t0, int n, RowTable* s) {
+  const int r = threadIdx.x;
+  if (r < n) {
+    int col = 0;
+    const int64_t place = row_place(s, t0, r, &col);
+    int pos[kRopeAxes] = {0, 0, 0, 0};
+    if (place >= 0) fetch_positions(A.r, t0 + r, (int)place, pos);
+    const bool in = check_positions(A.r, pos);
+    if (!in && A.status_dev) atomicOr(A.status_dev, SDPA_ROPE_BAD_POS);
+    // (positions and rows are below 2^31)
+    s->cell[r] = place >= 0 && in ? make_int2((int)((uint32_t)place % (uint32_t)A.rows), col) : make_int2(-1, 0);
+#pragma unroll
+    for (int a = 0; a < kRopeAxes; ++a) s->pos[r][a] = pos[a];
+  }
+  __syncthreads();
+}
+
 // A step's rows: queries rotated into q_out, keys rotated and values as they are into the store.
-// A CTA takes `cr` packed rows; a warp takes one of `parts` runs of a row's passes (32 / (D / 16)
-// heads each), which are those of q, then k, then v.  The next pass is on its way while one is
-// worked on, and the first ones while the rows' segments are looked up.
+// The work is a line of passes (32 / (D / 16) heads each), a row's being those of q, then k, then v;
+// a CTA takes `per` of them in order, at most kStepRows rows at a time, its warps even shares of
+// those.  Two passes are always on their way, the first ones while the rows' segments are looked
+// up, and the angles of a warp's next row while it is at one.
 template <int D, bool IL, bool Q4>
 __global__ void __launch_bounds__(kRopeThreads, 3) sdpa_rope_append_kernel(StepArgs A) {
-  constexpr int LPH = D / 16, HPP = 32 / LPH;
+  constexpr int LPH = D / 16, HPP = 32 / LPH, kWarps = kRopeThreads / 32;
   __shared__ RowTable s_rows;
-  __shared__ __align__(16) float2 s_angles[kRopeThreads / 32][D / 2];
+  __shared__ __align__(16) float2 s_angles[kWarps][D / 2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, hs = lane / LPH;
   const LaneDims<IL> ld(A.r.half, lane % LPH);
-  const int64_t t0 = (int64_t)blockIdx.x * A.cr;
-  const int n = (int)min((int64_t)A.cr, A.T - t0);
+  const int j0 = ld.turn ? ld.j0 : 0;
   const int pq = (A.Hq + HPP - 1) / HPP, pk = (A.Hkv + HPP - 1) / HPP, passes = pq + 2 * pk;
+  const int64_t f_end = min((int64_t)(blockIdx.x + 1) * A.per, A.T * passes);
 
-  Row16 x[2];
-  auto load = [&](Row16* y, int64_t t, int q, int p1) {
-    y->a = y->b = make_uint4(0, 0, 0, 0);
-    const int what = q < pq ? 0 : q < pq + pk ? 1 : 2;
-    const int h = (q - (what == 0 ? 0 : what == 1 ? pq : pq + pk)) * HPP + hs;
-    if (q < p1 && h < (what == 0 ? A.Hq : A.Hkv)) {
-      const __nv_bfloat16* z = what == 0 ? A.q + t * A.q_rs + (int64_t)h * A.q_hs
-                               : what == 1 ? A.k + t * A.k_rs + (int64_t)h * A.k_hs
-                                           : A.v + t * A.v_rs + (int64_t)h * A.v_hs;
-      y->a = ldg16(z + ld.da);
-      y->b = ldg16(z + ld.db);
-    }
-  };
-  auto run_of = [&](int w, int* r, int* p0, int* p1) {
-    *r = w;
-    *p0 = 0;
-    *p1 = passes;
-    if (A.parts > 1) {
-      *r = w / A.parts;
-      const int part = w - *r * A.parts;
-      *p0 = passes * part / A.parts;
-      *p1 = passes * (part + 1) / A.parts;
-    }
-  };
-  int r = 0, p0 = 0, p1 = 0;
-  run_of(warp, &r, &p0, &p1);
-  if (warp < n * A.parts) {
-    load(&x[0], t0 + r, p0, p1);
-    load(&x[1], t0 + r, p0 + 1, p1);
-  }
-  find_rows(A, t0, n, &s_rows);
+  // passes [fa, fb) of the line, rows [t0, t0 + n), and this warp's share [wa, wb) counted from row t0
+  for (int64_t fa = (int64_t)blockIdx.x * A.per; fa < f_end;) {
+    const int64_t t0 = udiv(fa, passes);
+    const int64_t fb = min(f_end, (t0 + kStepRows) * passes);
+    const int n = (int)udiv(fb - 1, passes) - (int)t0 + 1;
+    const int off = (int)(fa - t0 * passes), len = (int)(fb - fa);
+    const int wa = off + len * warp / kWarps, wb = off + len * (warp + 1) / kWarps;
+    fa = fb;
 
-  for (int w = warp; w < n * A.parts; w += kRopeThreads / 32) {
-    if (w != warp) {
-      run_of(w, &r, &p0, &p1);
-      load(&x[0], t0 + r, p0, p1);
-      load(&x[1], t0 + r, p0 + 1, p1);
-    }
-    const int64_t t = t0 + r;
-    int col = 0;
-    const int64_t place = row_place(&s_rows, t0, r, &col);
-    int pos[kRopeAxes] = {0, 0, 0, 0};
-    if (place >= 0) fetch_positions(A.r, t, (int)place, pos);
-    const bool in = check_positions(A.r, pos);
-    const bool ok = place >= 0 && in;
-    if (!in && p0 == 0 && lane == 0 && A.status_dev) atomicOr(A.status_dev, SDPA_ROPE_BAD_POS);
-    Angles an;
-    if (ok && p0 < pq + pk) {
+    Row16 x[2];
+    int lr = wa / passes, lp = wa - lr * passes;  // the next pass to load
+    auto load = [&](Row16* y) {
+      y->a = y->b = make_uint4(0, 0, 0, 0);
+      if (lr * passes + lp >= wb) return;
+      const int what = lp < pq ? 0 : lp < pq + pk ? 1 : 2;
+      const int h = (lp - (what == 0 ? 0 : what == 1 ? pq : pq + pk)) * HPP + hs;
+      if (h < (what == 0 ? A.Hq : A.Hkv)) {
+        const int64_t t = t0 + lr;
+        const __nv_bfloat16* z = what == 0 ? A.q + t * A.q_rs + (int64_t)h * A.q_hs
+                                 : what == 1 ? A.k + t * A.k_rs + (int64_t)h * A.k_hs
+                                             : A.v + t * A.v_rs + (int64_t)h * A.v_hs;
+        y->a = ldg16(z + ld.da);
+        y->b = ldg16(z + ld.db);
+      }
+      if (++lp == passes) {
+        lp = 0;
+        ++lr;
+      }
+    };
+    int r = lr, p = lp;  // the pass at hand
+    load(&x[0]);
+    load(&x[1]);
+    find_rows(A, t0, n, &s_rows);
+    place_rows(A, t0, n, &s_rows);
+
+    if (wa < wb) {
       PairAngles pa;
-      fetch_angles<D>(A.r, pos, lane, &pa);
-      share_angles<D>(A.r, pa, ld.turn ? ld.j0 : 0, lane, s_angles[warp], &an);
-    }
-    const uint32_t row = (uint32_t)place % (uint32_t)A.rows;  // both below 2^31
-    const int64_t cell0 = Q4 ? (int64_t)col * A.Hkv * A.rows + row : ((int64_t)row * A.cols + col) * A.Hkv;
-
-    auto work = [&](Row16& y, int q) {
-      const int what = q < pq ? 0 : q < pq + pk ? 1 : 2;
-      const int h = (q - (what == 0 ? 0 : what == 1 ? pq : pq + pk)) * HPP + hs;
-      if (what > 0 && !ok) return;  // nothing of the row is kept
-      if (what == 0) {
-        if (ok && ld.turn) turn16<IL, false>(&y, an);
-        if (h < A.Hq) {
+      fetch_angles<D>(A.r, s_rows.pos[r], lane, &pa);
+      Angles an;
+      int2 cell;
+      auto enter_row = [&]() {
+        cell = s_rows.cell[r];
+        share_angles<D>(A.r, pa, j0, lane, s_angles[warp], &an);
+        if ((r + 1) * passes < wb) fetch_angles<D>(A.r, s_rows.pos[r + 1], lane, &pa);
+      };
+      enter_row();
+      auto work = [&](Row16& y) {
+        const int what = p < pq ? 0 : p < pq + pk ? 1 : 2;
+        const int h = (p - (what == 0 ? 0 : what == 1 ? pq : pq + pk)) * HPP + hs;
+        const bool ok = cell.x >= 0;
+        if (what == 0) {
+          if (ld.turn) turn16<IL, false>(&y, an);
           if (!ok) y.a = y.b = make_uint4(0, 0, 0, 0);
-          __nv_bfloat16* z = A.q_out + t * A.o_rs + (int64_t)h * A.o_hs;
+          if (h < A.Hq) {
+            __nv_bfloat16* z = A.q_out + (t0 + r) * A.o_rs + (int64_t)h * A.o_hs;
+            stg16(z + ld.da, y.a);
+            stg16(z + ld.db, y.b);
+          }
+          return;
+        }
+        if (!ok) return;  // (the warp has one row)
+        if (what == 1 && ld.turn) turn16<IL, true>(&y, an);
+        if constexpr (Q4) {
+          const uint32_t ca[4] = {q4_storable(y.a.x), q4_storable(y.a.y), q4_storable(y.a.z), q4_storable(y.a.w)};
+          const uint32_t cb[4] = {q4_storable(y.b.x), q4_storable(y.b.y), q4_storable(y.b.z), q4_storable(y.b.w)};
+          float ma = amax8(ca), mb = amax8(cb);
+          group_amax<LPH>(&ma, &mb, IL, A.r.half, lane);
+          const uint32_t ba = q4_scale_byte(ma), bb = q4_scale_byte(mb);
+          if (h < A.Hkv) {
+            const int64_t at = ((int64_t)cell.y * A.Hkv + h) * A.rows + cell.x;
+            uint8_t* codes = (what == 1 ? A.q4.kc : A.q4.vc) + at * (D / 2);
+            uint8_t* scales = (what == 1 ? A.q4.ks : A.q4.vs) + at * (D / kQ4Group);
+            *reinterpret_cast<uint32_t*>(codes + ld.da / 2) = codes8(ca, ba);
+            *reinterpret_cast<uint32_t*>(codes + ld.db / 2) = codes8(cb, bb);
+            if (ld.da % kQ4Group == 0) scales[ld.da / kQ4Group] = (uint8_t)ba;
+            if (ld.db % kQ4Group == 0) scales[ld.db / kQ4Group] = (uint8_t)bb;
+          }
+        } else if (h < A.Hkv) {
+          __nv_bfloat16* z =
+              (what == 1 ? A.k_store : A.v_store) + (((int64_t)cell.x * A.cols + cell.y) * A.Hkv + h) * D;
           stg16(z + ld.da, y.a);
           stg16(z + ld.db, y.b);
         }
-        return;
-      }
-      if (what == 1 && ld.turn) turn16<IL, true>(&y, an);
-      if constexpr (Q4) {
-        const uint32_t wa[4] = {q4_storable(y.a.x), q4_storable(y.a.y), q4_storable(y.a.z), q4_storable(y.a.w)};
-        const uint32_t wb[4] = {q4_storable(y.b.x), q4_storable(y.b.y), q4_storable(y.b.z), q4_storable(y.b.w)};
-        float ma = amax8(wa), mb = amax8(wb);
-        group_amax<LPH>(&ma, &mb, IL, A.r.half, lane);
-        const uint32_t ba = q4_scale_byte(ma), bb = q4_scale_byte(mb);
-        if (h < A.Hkv) {
-          const int64_t cell = cell0 + (int64_t)h * A.rows;
-          uint8_t* codes = (what == 1 ? A.q4.kc : A.q4.vc) + cell * (D / 2);
-          uint8_t* scales = (what == 1 ? A.q4.ks : A.q4.vs) + cell * (D / kQ4Group);
-          *reinterpret_cast<uint32_t*>(codes + ld.da / 2) = codes8(wa, ba);
-          *reinterpret_cast<uint32_t*>(codes + ld.db / 2) = codes8(wb, bb);
-          if (ld.da % kQ4Group == 0) scales[ld.da / kQ4Group] = (uint8_t)ba;
-          if (ld.db % kQ4Group == 0) scales[ld.db / kQ4Group] = (uint8_t)bb;
-        }
-      } else if (h < A.Hkv) {
-        __nv_bfloat16* z = (what == 1 ? A.k_store : A.v_store) + (cell0 + h) * (int64_t)D;
-        stg16(z + ld.da, y.a);
-        stg16(z + ld.db, y.b);
-      }
-    };
-    for (int p = p0; p < p1; p += 2) {
+      };
+      for (int f = wa; f < wb; f += 2) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        if (p + u >= p1) break;
-        work(x[u], p + u);
-        load(&x[u], t, p + u + 2, p1);
+        for (int u = 0; u < 2; ++u) {
+          if (f + u >= wb) break;
+          work(x[u]);
+          load(&x[u]);
+          if (++p == passes && f + u + 1 < wb) {
+            p = 0;
+            ++r;
+            enter_row();
+          }
+        }
       }
     }
+    if (fa < f_end) __syncthreads();  // the rows' records are written again
   }
 }
 
@@ -520,35 +541,38 @@ __global__ void __launch_bounds__(kRopeThreads) sdpa_q4_unpack_kernel(StepArgs A
   const int64_t t0 = (int64_t)blockIdx.x * A.cr;
   const int n = (int)min((int64_t)A.cr, A.T - t0);
   find_rows(A, t0, n, &s_rows);
-  const int per = A.Hkv * LPH;  // chunks of 8 dims of a row
-  for (int w0 = threadIdx.x; w0 < n * per; w0 += U * kRopeThreads) {
-    uint32_t kw[U], vw[U], kb[U], vb[U];
-    int64_t dst[U];
-    bool there[U];
+  if (threadIdx.x < n) {
+    int col = 0;
+    const int64_t p = row_place(&s_rows, t0, threadIdx.x, &col);
+    s_rows.cell[threadIdx.x] = p >= 0 ? make_int2((int)((uint32_t)p % (uint32_t)A.rows), col) : make_int2(-1, 0);
+  }
+  __syncthreads();
+  const int per = A.Hkv * LPH;  // chunks of 8 dims of a row; a warp takes a row
+  for (int r = threadIdx.x / 32; r < n; r += kRopeThreads / 32) {
+    const int2 at = s_rows.cell[r];
+    const int64_t dst = (t0 + r) * A.o_rs;
+    for (int x0 = threadIdx.x % 32; x0 < per; x0 += 32 * U) {
+      uint32_t kw[U], vw[U], kb[U], vb[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int w = w0 + u * kRopeThreads;
-      dst[u] = -1;
-      if (w >= n * per) continue;
-      const int r = w / per, x = w - r * per, h = x / LPH, c = x % LPH;
-      int col = 0;
-      const int64_t p = row_place(&s_rows, t0, r, &col);
-      there[u] = p >= 0;
-      if (there[u]) {
-        const int64_t cell = ((int64_t)col * A.Hkv + h) * A.rows + (uint32_t)p % (uint32_t)A.rows;
-        kw[u] = *reinterpret_cast<const uint32_t*>(A.q4.kc + cell * (D / 2) + 4 * c);
-        vw[u] = *reinterpret_cast<const uint32_t*>(A.q4.vc + cell * (D / 2) + 4 * c);
-        kb[u] = A.q4.ks[cell * (D / kQ4Group) + c / 4];
-        vb[u] = A.q4.vs[cell * (D / kQ4Group) + c / 4];
+      for (int u = 0; u < U; ++u) {
+        const int x = x0 + 32 * u, h = x / LPH, c = x % LPH;
+        if (x < per && at.x >= 0) {
+          const int64_t cell = ((int64_t)at.y * A.Hkv + h) * A.rows + at.x;
+          kw[u] = *reinterpret_cast<const uint32_t*>(A.q4.kc + cell * (D / 2) + 4 * c);
+          vw[u] = *reinterpret_cast<const uint32_t*>(A.q4.vc + cell * (D / 2) + 4 * c);
+          kb[u] = A.q4.ks[cell * (D / kQ4Group) + c / 4];
+          vb[u] = A.q4.vs[cell * (D / kQ4Group) + c / 4];
+        }
       }
-      dst[u] = (t0 + r) * A.o_rs + (int64_t)h * A.o_hs + 8 * c;
-    }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (dst[u] < 0) continue;
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-      stg16(A.k_out + dst[u], there[u] ? q4_words8(kw[u], kb[u]) : zero);
-      stg16(A.v_out + dst[u], there[u] ? q4_words8(vw[u], vb[u]) : zero);
+      for (int u = 0; u < U; ++u) {
+        const int x = x0 + 32 * u, h = x / LPH, c = x % LPH;
+        if (x >= per) break;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        const int64_t to = dst + (int64_t)h * A.o_hs + 8 * c;
+        stg16(A.k_out + to, at.x >= 0 ? q4_words8(kw[u], kb[u]) : zero);
+        stg16(A.v_out + to, at.x >= 0 ? q4_words8(vw[u], vb[u]) : zero);
+      }
     }
   }
 }

@@ -36,7 +36,8 @@ struct StepArgs {
   const int32_t* seq_info;
   const int32_t* seg_mode;  // NULL, or [S, 2] (causal, window)
   int S, window, cols, Hq, Hkv;
-  int cr, parts;            // packed rows per CTA; warps that share a row
+  int cr;                   // read-back: packed rows per CTA
+  int per;                  // append: passes per CTA
   int64_t T, rows;
   const __nv_bfloat16 *q, *k, *v;
   int64_t q_rs, q_hs, k_rs, k_hs, v_rs, v_hs;

@@ -11,6 +11,8 @@
 namespace sdpa {
 namespace {
 
+constexpr int kMaxHeads = 1 << 20;  // of one row (the kernels count a CTA's passes over them in 32 bits)
+
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 bool bad_strides(int64_t rs, int64_t hs) { return rs < 0 || hs < 0 || rs % 8 || hs % 8; }
 
@@ -73,6 +75,7 @@ sdpa_status check_step(int64_t T, int Hq, int Hkv, int D, int S, int64_t rows, i
                        const int32_t* seq_info, const int32_t* seg_mode) {
   sdpa_status st = check_common(T, Hq, Hkv, D, S, rows, cols, window, 1.f);
   if (st) return st;
+  if (Hq + 2 * (int64_t)Hkv > kMaxHeads) return fail(SDPA_ERR_SHAPE, "more than %d heads", kMaxHeads);
   if (!seq_info && S > 0) return fail(SDPA_ERR_NULL, "seq_info is NULL");
   if (!aligned16(seq_info) || !aligned16(seg_mode))
     return fail(SDPA_ERR_ALIGN, "seq_info and seg_mode must be 16-byte aligned");
@@ -84,24 +87,26 @@ int row_parts(int64_t T, int passes, int sms) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(passes, 24 * (int64_t)sms / std::max<int64_t>(T, 1)));
 }
 
-// `passes` of a row, or 0 for a kernel whose threads share its CTA's rows.  A CTA looks through the
-// whole table for its rows, so it takes as many as its warps have work for, and twice that once
-// every SM has three such CTAs.
+// A step's kernel: `passes` of a row, or 0 for the read-back, whose CTAs take whole rows.  The grid is
+// one wave of three CTAs per SM, or as many CTAs as give each of their warps one pass.
 sdpa_status launch_step(const void* f, StepArgs& A, int passes, cudaStream_t stream, const char* what) {
   if (A.T == 0) return SDPA_OK;
   int sms = 0;
   sdpa_status st = device_sms(&sms);
   if (st) return st;
+  const int64_t wave = 3 * (int64_t)sms;
+  int64_t grid;
   if (passes > 0) {
-    A.parts = row_parts(A.T, passes, sms);
-    A.cr = std::max(1, kRopeThreads / 32 / A.parts);
-    if (A.T >= 6 * (int64_t)sms * A.cr) A.cr *= 2;
+    const int64_t all = A.T * passes;
+    const int64_t per = std::max<int64_t>(kRopeThreads / 32, (all + wave - 1) / wave);
+    if (per > INT_MAX) return fail(SDPA_ERR_SHAPE, "%lld rows of %d heads", (long long)A.T, A.Hq + 2 * A.Hkv);
+    A.per = (int)per;
+    grid = (all + per - 1) / per;
   } else {
-    A.cr = (int)(A.T / (3 * (int64_t)sms));
+    A.cr = (int)std::max<int64_t>(1, std::min<int64_t>(kStepRows, A.T / wave));
+    grid = (A.T + A.cr - 1) / A.cr;
   }
-  A.cr = std::max(1, std::min(kStepRows, A.cr));
   void* args[] = {(void*)&A};
-  const int64_t grid = (A.T + A.cr - 1) / A.cr;
   cudaError_t e = cudaLaunchKernel(f, dim3((unsigned)grid), dim3(kRopeThreads), args, 0, stream);
   if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
   return SDPA_OK;
@@ -169,7 +174,7 @@ sdpa_status sdpa_rope(const void* x, int64_t T, int H, int D, int64_t x_row_stri
                       const sdpa_rotation* rotation, int inverse, void* out, int64_t o_row_stride,
                       int64_t o_head_stride, int32_t* status_dev, void* stream) {
   set_last_error("");
-  if (T < 0 || T > INT_MAX || H <= 0) return fail(SDPA_ERR_SHAPE, "bad sizes: T=%lld H=%d", (long long)T, H);
+  if (T < 0 || T > INT_MAX || H <= 0 || H > kMaxHeads) return fail(SDPA_ERR_SHAPE, "bad sizes: T=%lld H=%d", (long long)T, H);
   if (D != 64 && D != 128 && D != 256) return fail(SDPA_ERR_HEAD_DIM, "head dim %d not in {64,128,256}", D);
   RopeRowsArgs A{};
   sdpa_status st = take_rotation(rotation, T, D, false, inverse, &A.r);
