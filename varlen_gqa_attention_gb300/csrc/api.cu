@@ -51,7 +51,7 @@ struct DevInfo {
   bool ready = false;
   int sms = 0;
   int splitk_per_sm[3] = {0, 0, 0};  // D = 64, 128, 256
-  int q4_per_sm[3] = {0, 0, 0};
+  int q4_per_sm[2][3] = {};          // narrow, wide
   bool prefill_ok[3] = {false, false, false};
 };
 static std::mutex g_mu;
@@ -93,14 +93,17 @@ static sdpa_status device_info(DevInfo* out) {
       e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, f, kSplitkThreads, smem);
       if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "occupancy: %s", cudaGetErrorString(e));
       di.splitk_per_sm[k] = nb > 0 ? nb : 1;
-      const void* q4 = q4_splitk_kernel_ptr(Ds[k]);
-      e = cudaFuncSetAttribute(q4, cudaFuncAttributeMaxDynamicSharedMemorySize, q4_splitk_smem_bytes(Ds[k]));
-      if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "smem attribute: %s", cudaGetErrorString(e));
-      e = cudaFuncSetAttribute(q4, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-      if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "carveout attribute: %s", cudaGetErrorString(e));
-      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, q4, kQ4Threads, q4_splitk_smem_bytes(Ds[k]));
-      if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "occupancy: %s", cudaGetErrorString(e));
-      di.q4_per_sm[k] = nb > 0 ? nb : 1;
+      for (int wide = 0; wide < 2; ++wide) {
+        const void* q4 = q4_splitk_kernel_ptr(Ds[k], wide);
+        const int q4_smem = q4_splitk_smem_bytes(Ds[k], wide);
+        e = cudaFuncSetAttribute(q4, cudaFuncAttributeMaxDynamicSharedMemorySize, q4_smem);
+        if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "smem attribute: %s", cudaGetErrorString(e));
+        e = cudaFuncSetAttribute(q4, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+        if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "carveout attribute: %s", cudaGetErrorString(e));
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, q4, kQ4Threads, q4_smem);
+        if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "occupancy: %s", cudaGetErrorString(e));
+        di.q4_per_sm[wide][k] = nb > 0 ? nb : 1;
+      }
       e = cudaFuncSetAttribute(combine_kernel_ptr(Ds[k]), cudaFuncAttributePreferredSharedMemoryCarveout, 100);
       if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "carveout attribute: %s", cudaGetErrorString(e));
       const void* pf = prefill_kernel_ptr(Ds[k]);
@@ -163,10 +166,20 @@ static bool make_tensor_maps(const void* q, int64_t T, int Hq, int D, int64_t q_
 struct Grids {
   int64_t splitk, prefill;
 };
-static Grids grids_for(const DevInfo& di, int D, bool q4 = false) {
+static Grids grids_for(const DevInfo& di, int D) {
   Grids g;
-  g.splitk = (int64_t)di.sms * (q4 ? di.q4_per_sm : di.splitk_per_sm)[d_index(D)];
+  g.splitk = (int64_t)di.sms * di.splitk_per_sm[d_index(D)];
   g.prefill = di.sms;
+  return g;
+}
+
+// The 4-bit split-K kernel: the wide build when the average segment has more than 8 packed rows (what
+// the host knows of them).  64 x 32768-key decode, 4 rows a segment: narrow XXN us, wide XXW;
+// 16 segments of 64 rows over 4112 keys: narrow XXn, wide XXw.
+static bool q4_wide(int64_t T, int Hq, int Hkv, int S) { return T * (Hq / Hkv) > 8 * (int64_t)S; }
+static Grids q4_grids_for(const DevInfo& di, int D, bool wide) {
+  Grids g = grids_for(di, D);
+  g.splitk = (int64_t)di.sms * di.q4_per_sm[wide][d_index(D)];
   return g;
 }
 
@@ -321,7 +334,9 @@ static sdpa_status launch_all(const SchedArgs& sa, const AttnArgs& aa, int D, co
   if (e == cudaSuccess && q4) {
     Q4AttnArgs ga{aa, *q4};
     void* args[] = {(void*)&ga};
-    e = launch_k(q4_splitk_kernel_ptr(D), (unsigned)g.splitk, kQ4Threads, args, q4_splitk_smem_bytes(D), st, true);
+    const bool wide = q4_wide(aa.T, aa.Hq, aa.Hkv, sa.S);
+    e = launch_k(q4_splitk_kernel_ptr(D, wide), (unsigned)g.splitk, kQ4Threads, args, q4_splitk_smem_bytes(D, wide), st,
+                 true);
     if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "4-bit split-K launch: %s", cudaGetErrorString(e));
   } else if (e == cudaSuccess) {
     void* args[] = {(void*)&aa};
@@ -360,7 +375,7 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
 
   DevInfo di;
   if ((st = device_info(&di))) return st;
-  const Grids g = grids_for(di, D, q4 != nullptr);
+  const Grids g = q4 ? q4_grids_for(di, D, q4_wide(T, Hq, Hkv, S)) : grids_for(di, D);
   Workspace W;
   size_t need = layout_workspace((char*)ws, T, Hq, Hkv, D, S, g.splitk, g.prefill, &W);
   Q4StageArgs sg{};
@@ -524,7 +539,7 @@ size_t sdpa_varlen_fourbit_workspace_bytes(int64_t T, int Hq, int Hkv, int D, in
   DevInfo di;
   Grids g;
   if (device_info(&di) == SDPA_OK) {
-    g = grids_for(di, D, true);
+    g = q4_grids_for(di, D, q4_wide(T, Hq, Hkv, S));
   } else {
     g.splitk = 4096;  // no device: a bound above any real grid
     g.prefill = 1024;

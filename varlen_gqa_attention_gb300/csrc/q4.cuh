@@ -121,7 +121,7 @@ const void* q4_stage_kernel_ptr(int D);
 
 // Entry points (q4_attn.cu).
 constexpr int kQ4Threads = 160;  // four warps of attention, one that loads
-const void* q4_splitk_kernel_ptr(int D);
-int q4_splitk_smem_bytes(int D);
+const void* q4_splitk_kernel_ptr(int D, bool wide);
+int q4_splitk_smem_bytes(int D, bool wide);
 
 }  // namespace sdpa

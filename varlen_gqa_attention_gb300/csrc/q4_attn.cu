@@ -37,14 +37,19 @@ namespace sdpa {
 constexpr int kQ4Consumers = 128; // threads of the four attention warps
 constexpr float kQ4PLift = 7.f;    // P is held 2^7 times larger
 
-template <int D>
-struct Q4Smem {
+// Two builds of the kernel: the narrow one takes 8 query rows a warp (one token's heads) and the wide
+// one 16, whose output takes twice the registers; each takes units of any size, the narrow one
+// repeating the conversion for every 8 rows.  At D = 256 the output of 16 rows would be 128
+// registers, and there is only the narrow one.
+template <int D, bool WIDE>
+struct Q4Cfg {
+  static constexpr int kRows = WIDE ? 16 : 8;   // query rows of a warp
+  static constexpr int kRun = WIDE ? 1 : D == 256 ? 2 : 4;  // 16-key blocks between two looks at the maximum
+  static constexpr int kKeys = WIDE ? 128 : 64 * kRun;  // keys per stage of the ring
+  static constexpr int kStages = WIDE ? 3 : D == 64 ? 3 : 2;
+  static constexpr int kPerSm = !WIDE && D == 64 ? 3 : 2;  // CTAs per SM that registers and shared memory allow
   static constexpr int kRowBytes = D / 2;
   static constexpr int kScaleBytes = D / kQ4Group;
-  static constexpr int kKeys = D == 256 ? 64 : 128;  // keys per stage of the ring
-  static constexpr int kStages = D == 128 ? 3 : 4;
-  // CTAs per SM that registers and shared memory allow
-  static constexpr int kPerSm = D == 256 ? 2 : 3;
   static constexpr int kCodes = kKeys * kRowBytes;
   static constexpr int kScales = kKeys * kScaleBytes;
   static constexpr int kStageBytes = 2 * (kCodes + kScales);
@@ -119,12 +124,12 @@ __device__ __forceinline__ void lds_words(const char* p, uint32_t (&w)[N]) {
 }
 
 // The four attention warps on one piece.  4 / NCS groups of 8 NR query rows; the NCS warps of a group
-// take every NCS-th run of 16 KT keys.
-template <int D, int NR, int NCS, int KT>
-__device__ __forceinline__ void q4_unit(const AttnArgs& A, const Q4Piece& pc, const char* ring, char* sQ,
+// share a stage's keys.
+template <int D, typename S>
+__device__ __forceinline__ void q4_unit(const AttnArgs& A, const Q4Piece& pc, int NCS, const char* ring, char* sQ,
                                         float* merge, uint32_t full, uint32_t empty, uint32_t qempty, uint32_t& it,
                                         volatile int* abort, float2* s_ml, int32_t** s_count) {
-  using S = Q4Smem<D>;
+  constexpr int NR = S::kRows / 8;
   constexpr int WK = D / 32;  // words of a lane's K chunk (D / 4 dims)
   constexpr int WV = D / 64;  // words of a lane's V chunk (D / 8 dims)
   constexpr int ND = D / 16;  // m16 blocks of the output
@@ -188,11 +193,12 @@ __device__ __forceinline__ void q4_unit(const AttnArgs& A, const Q4Piece& pc, co
   for (int nd = 0; nd < ND; ++nd)
 #pragma unroll
     for (int r = 0; r < NR; ++r) o[nd][r][0] = o[nd][r][1] = o[nd][r][2] = o[nd][r][3] = 0.f;
-  float m[NR][2], l[NR][2];
+  float m[NR][2], l[NR][2], nmu[NR][2];  // nmu: what is added to a score before exp2
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
     m[r][0] = m[r][1] = -INFINITY;
     l[r][0] = l[r][1] = 0.f;
+    nmu[r][0] = nmu[r][1] = 0.f;
   }
   const float sl2 = A.scale_log2;
   const uint32_t kbits = in_register(kQ4Bf16), vbits = in_register(kQ4F16);
@@ -203,15 +209,17 @@ __device__ __forceinline__ void q4_unit(const AttnArgs& A, const Q4Piece& pc, co
 
   for (int base = 0; base < nkeys; base += S::kKeys, ++it) {
     const uint32_t st = it % S::kStages;
-    q4_wait(full + 8 * st, (it / S::kStages) & 1, abort);
+    // (a wait that gave up goes on with what is there: the CTA's control flow stays whole)
+    if (!mbar_try_wait(full + 8 * st, (it / S::kStages) & 1)) mbar_wait(full + 8 * st, (it / S::kStages) & 1, abort);
     const char* kc = ring + st * S::kStageBytes;
     const char* vc = kc + S::kCodes;
     const char* ks = vc + S::kCodes;
     const char* vs = ks + S::kScales;
     const int nst = min(S::kKeys, nkeys - base);
-#pragma unroll 1
-    for (int k0 = cs * (16 * KT); k0 < nst; k0 += NCS * 16 * KT) {
-      // S^T = K Q^T over 16 KT keys
+    // One run of 16 KT keys from k0 on.
+    auto keys = [&](auto kt_const, int k0) {
+      constexpr int KT = decltype(kt_const)::value;
+      // S^T = K Q^T
       float s[KT][NR][4];
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
@@ -269,8 +277,10 @@ __device__ __forceinline__ void q4_unit(const AttnArgs& A, const Q4Piece& pc, co
               if (j >= count[r][e & 1]) s[kt][r][e] = -INFINITY;
             }
       }
-      float mx[NR][2], alpha[NR][2], nmu[NR][2];
-      bool resc = false;
+      // (the lanes compare their own scores with the maximum; only when one is beyond it are the
+      // rows' maxima taken across the lanes)
+      float mx[NR][2];
+      bool up = false;
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
 #pragma unroll
@@ -279,37 +289,30 @@ __device__ __forceinline__ void q4_unit(const AttnArgs& A, const Q4Piece& pc, co
 #pragma unroll
           for (int kt = 1; kt < KT; ++kt) x = fmaxf(x, fmaxf(s[kt][r][c], s[kt][r][c + 2]));
           mx[r][c] = x;
+          up |= x * sl2 > m[r][c] + 8.f;  // false while nothing is visible
         }
       }
-#pragma unroll
-      for (int d = 4; d < 32; d <<= 1)
-#pragma unroll
-        for (int r = 0; r < NR; ++r)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) mx[r][c] = fmaxf(mx[r][c], __shfl_xor_sync(0xffffffffu, mx[r][c], d));
-#pragma unroll
-      for (int r = 0; r < NR; ++r) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float mn = fmaxf(m[r][c], mx[r][c] * sl2);
-          const bool up = mn > m[r][c] + 8.f;  // false while nothing is visible
-          alpha[r][c] = up ? exp2_approx(m[r][c] - mn) : 1.f;
-          if (up) m[r][c] = mn;
-          resc |= up;
-          nmu[r][c] = m[r][c] == -INFINITY ? 0.f : kQ4PLift - m[r][c];
-        }
-      }
-      if (__any_sync(0xffffffffu, resc)) {
+      if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-          l[r][0] *= alpha[r][0];
-          l[r][1] *= alpha[r][1];
 #pragma unroll
-          for (int nd = 0; nd < ND; ++nd) {
-            o[nd][r][0] *= alpha[r][0];
-            o[nd][r][1] *= alpha[r][1];
-            o[nd][r][2] *= alpha[r][0];
-            o[nd][r][3] *= alpha[r][1];
+          for (int c = 0; c < 2; ++c) {
+            float x = mx[r][c];
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+            const float mn = fmaxf(m[r][c], x * sl2);
+            float alpha = 1.f;
+            if (mn > m[r][c] + 8.f) {
+              alpha = exp2_approx(m[r][c] - mn);
+              m[r][c] = mn;
+              nmu[r][c] = kQ4PLift - mn;
+            }
+            l[r][c] *= alpha;
+#pragma unroll
+            for (int nd = 0; nd < ND; ++nd) {
+              o[nd][r][c] *= alpha;
+              o[nd][r][c + 2] *= alpha;
+            }
           }
         }
       }
@@ -362,6 +365,15 @@ __device__ __forceinline__ void q4_unit(const AttnArgs& A, const Q4Piece& pc, co
           }
         }
       }
+    };
+    // a stage's keys in runs; the blocks of a short last stage one by one, evenly over the warps
+    if (nst > S::kKeys - 16 * S::kRun) {
+#pragma unroll 1
+      for (int k0 = cs * (16 * S::kRun); k0 < nst; k0 += NCS * (16 * S::kRun))
+        keys(std::integral_constant<int, S::kRun>(), k0);
+    } else {
+#pragma unroll 1
+      for (int k0 = cs * 16; k0 < nst; k0 += NCS * 16) keys(std::integral_constant<int, 1>(), k0);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(empty + 8 * st);
@@ -416,13 +428,13 @@ __device__ __forceinline__ void q4_unit(const AttnArgs& A, const Q4Piece& pc, co
       const int rl = idx >> 3, n = idx & 7;
       const int w0 = rl / GR * NCS, rin = rl % GR;
       float M = -INFINITY;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < NCS; ++c) M = fmaxf(M, s_ml[(w0 + c) * GR + rin].x);
       const float Mu = M == -INFINITY ? 0.f : M;
       float L = 0.f, acc[XP];
 #pragma unroll
       for (int k = 0; k < XP; ++k) acc[k] = 0.f;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < NCS; ++c) {
         const int w = (w0 + c) * GR + rin;
         const float2 ml = s_ml[w];
@@ -461,10 +473,9 @@ __device__ __forceinline__ void q4_unit(const AttnArgs& A, const Q4Piece& pc, co
 // The loading warp: walks the CTA's pieces, hands each on with its query rows, and streams its keys
 // through the ring.  A piece's keys [pos_lo, pos_hi) begin at a multiple of 16 and span at most
 // rows + 15 positions, so a stage is at most two runs of store rows, both of whole 16-row blocks.
-template <int D>
+template <int D, typename S>
 __device__ __forceinline__ void q4_load(const Q4AttnArgs& G, char* ring, char* sQ, Q4Piece* pieces, uint32_t full,
                                         uint32_t empty, uint32_t qfull, uint32_t qempty, volatile int* abort) {
-  using S = Q4Smem<D>;
   const AttnArgs& A = G.a;
   const int lane = threadIdx.x & 31;
   PieceWalk wk;
@@ -539,9 +550,9 @@ __device__ __forceinline__ void q4_load(const Q4AttnArgs& G, char* ring, char* s
   if (n > 0) mbar_wait(qfull, (n - 1) & 1, &none);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kQ4Threads, Q4Smem<D>::kPerSm) sdpa_q4_splitk_kernel(Q4AttnArgs G) {
-  using S = Q4Smem<D>;
+template <int D, bool WIDE>
+__global__ void __launch_bounds__(kQ4Threads, Q4Cfg<D, WIDE>::kPerSm) sdpa_q4_splitk_kernel(Q4AttnArgs G) {
+  using S = Q4Cfg<D, WIDE>;
   extern __shared__ __align__(128) char smem[];
   __shared__ __align__(8) uint64_t bars[2 * S::kStages + 2];
   __shared__ __align__(16) Q4Piece pieces[2];
@@ -571,7 +582,7 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Smem<D>::kPerSm) sdpa_q4_splitk_
   griddep_launch();
 
   if (threadIdx.x >= kQ4Consumers) {
-    q4_load<D>(G, ring, sQ, pieces, full, empty, qfull, qempty, &s_abort);
+    q4_load<D, S>(G, ring, sQ, pieces, full, empty, qfull, qempty, &s_abort);
   } else {
     uint32_t it = 0;
     for (uint32_t n = 0;; ++n) {
@@ -581,27 +592,10 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Smem<D>::kPerSm) sdpa_q4_splitk_
       const Q4Piece& pc = pieces[n & 1];
       if (!pc.valid) break;
       if (threadIdx.x == 0) s_count[1] = pc.ur.nslots > 1 ? A.ws.unit_done + pc.unit : nullptr;
-      auto unit = [&](auto nr, auto ncs, auto kt) {
-        q4_unit<D, decltype(nr)::value, decltype(ncs)::value, decltype(kt)::value>(
-            A, pc, ring, sQ, merge, full, empty, qempty, it, &s_abort, s_ml, s_count);
-      };
-      using std::integral_constant;
-      const int rows = pc.ur.rows;
-      if constexpr (D == 256) {  // an output of 16 rows would take 128 registers
-        if (rows <= 8)
-          unit(integral_constant<int, 1>(), integral_constant<int, 4>(), integral_constant<int, 1>());
-        else if (rows <= 16)
-          unit(integral_constant<int, 1>(), integral_constant<int, 2>(), integral_constant<int, 1>());
-        else
-          unit(integral_constant<int, 1>(), integral_constant<int, 1>(), integral_constant<int, 1>());
-      } else {
-        if (rows <= 8)
-          unit(integral_constant<int, 1>(), integral_constant<int, 4>(), integral_constant<int, 2>());
-        else if (rows <= 16)
-          unit(integral_constant<int, 2>(), integral_constant<int, 4>(), integral_constant<int, 1>());
-        else
-          unit(integral_constant<int, 2>(), integral_constant<int, 2>(), integral_constant<int, 1>());
-      }
+      // warps that share the keys of a group of rows: 4, 2 or 1
+      const int groups = (pc.ur.rows + S::kRows - 1) / S::kRows;
+      q4_unit<D, S>(A, pc, groups == 1 ? 4 : groups == 2 ? 2 : 1, ring, sQ, merge, full, empty, qempty, it, &s_abort,
+                    s_ml, s_count);
       // (the unit ended on a barrier of the four warps)
       if (threadIdx.x == 0) s_count[0] = s_count[1];
     }
@@ -614,23 +608,27 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Smem<D>::kPerSm) sdpa_q4_splitk_
   }
 }
 
-template __global__ void sdpa_q4_splitk_kernel<64>(Q4AttnArgs);
-template __global__ void sdpa_q4_splitk_kernel<128>(Q4AttnArgs);
-template __global__ void sdpa_q4_splitk_kernel<256>(Q4AttnArgs);
+template __global__ void sdpa_q4_splitk_kernel<64, false>(Q4AttnArgs);
+template __global__ void sdpa_q4_splitk_kernel<64, true>(Q4AttnArgs);
+template __global__ void sdpa_q4_splitk_kernel<128, false>(Q4AttnArgs);
+template __global__ void sdpa_q4_splitk_kernel<128, true>(Q4AttnArgs);
+template __global__ void sdpa_q4_splitk_kernel<256, false>(Q4AttnArgs);
 
-int q4_splitk_smem_bytes(int D) {
+int q4_splitk_smem_bytes(int D, bool wide) {
   switch (D) {
-    case 64: return Q4Smem<64>::kBytes;
-    case 128: return Q4Smem<128>::kBytes;
-    default: return Q4Smem<256>::kBytes;
+    case 64: return wide ? Q4Cfg<64, true>::kBytes : Q4Cfg<64, false>::kBytes;
+    case 128: return wide ? Q4Cfg<128, true>::kBytes : Q4Cfg<128, false>::kBytes;
+    default: return Q4Cfg<256, false>::kBytes;
   }
 }
 
-const void* q4_splitk_kernel_ptr(int D) {
+const void* q4_splitk_kernel_ptr(int D, bool wide) {
   switch (D) {
-    case 64: return (const void*)sdpa_q4_splitk_kernel<64>;
-    case 128: return (const void*)sdpa_q4_splitk_kernel<128>;
-    default: return (const void*)sdpa_q4_splitk_kernel<256>;
+    case 64:
+      return wide ? (const void*)sdpa_q4_splitk_kernel<64, true> : (const void*)sdpa_q4_splitk_kernel<64, false>;
+    case 128:
+      return wide ? (const void*)sdpa_q4_splitk_kernel<128, true> : (const void*)sdpa_q4_splitk_kernel<128, false>;
+    default: return (const void*)sdpa_q4_splitk_kernel<256, false>;
   }
 }
 
