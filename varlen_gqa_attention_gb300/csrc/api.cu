@@ -104,6 +104,8 @@ static sdpa_status device_info(DevInfo* out) {
         if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "occupancy: %s", cudaGetErrorString(e));
         di.q4_per_sm[wide][k] = nb > 0 ? nb : 1;
       }
+      e = cudaFuncSetAttribute(combine_pair_kernel_ptr(Ds[k]), cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+      if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "carveout attribute: %s", cudaGetErrorString(e));
       e = cudaFuncSetAttribute(combine_kernel_ptr(Ds[k]), cudaFuncAttributePreferredSharedMemoryCarveout, 100);
       if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "carveout attribute: %s", cudaGetErrorString(e));
       const void* pf = prefill_kernel_ptr(Ds[k]);
@@ -348,7 +350,11 @@ static sdpa_status launch_all(const SchedArgs& sa, const AttnArgs& aa, int D, co
     void* args[] = {(void*)&aa};
     const int64_t warps = aa.T * aa.Hq;
     const int64_t blocks = std::min<int64_t>((warps * 32 + 255) / 256, 8 * (int64_t)g.prefill);
-    e = launch_k(combine_kernel_ptr(D), (unsigned)blocks, 256, args, 0, st, true);
+    // 4-bit calls with few pairs: a CTA each, as many as the SMs hold at once
+    if (q4 && warps <= 8 * (int64_t)g.prefill)
+      e = launch_k(combine_pair_kernel_ptr(D), (unsigned)warps, 256, args, 0, st, true);
+    else
+      e = launch_k(combine_kernel_ptr(D), (unsigned)blocks, 256, args, 0, st, true);
     if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "combine launch: %s", cudaGetErrorString(e));
   }
   if (e == cudaSuccess) e = mark(4, st);

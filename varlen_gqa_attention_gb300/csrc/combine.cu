@@ -148,9 +148,120 @@ __global__ void __launch_bounds__(kCombineThreads) sdpa_combine_kernel(AttnArgs 
     combine_row<D>(A, gw, lane, U1, U2);
 }
 
+// The same for calls with few (row, head) pairs, whose units may be cut over many CTAs (one long
+// sequence over the whole grid): a CTA per pair, whose warps share a unit's slots, warp w those
+// congruent to w, and join their results in warp order.  One warp going through 152 slots of a
+// 65536-key sequence took 25 us, a CTA 8.
+constexpr int kCombineShare = 8;  // slots up to which one warp does it alone
+template <int D>
+__global__ void __launch_bounds__(kCombineThreads) sdpa_combine_pair_kernel(AttnArgs A) {
+  constexpr int PER = D / 32, kWarps = kCombineThreads / 32;
+  __shared__ float s_o[kWarps][D];
+  __shared__ float2 s_ml[kWarps];
+  __shared__ int s_late;
+  const Workspace& W = A.ws;
+  const int64_t work = W.hdr->combine_work;
+  const int64_t U1 = W.hdr->units[kRouteSplitk], U2 = W.hdr->units[kRoutePrefill];
+  if (!work) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t gw = blockIdx.x, t = udiv(gw, A.Hq);
+  const int h = (int)(gw - t * A.Hq);
+  const int4 ri = W.row_info[t];
+  UnitRec ur;
+  ur.nslots = 0;
+  int64_t r = 0, u = 0;
+  if (ri.x == kRouteSplitk) {
+    const int hk = h / A.group;
+    r = (int64_t)ri.w * A.group + (h % A.group);
+    u = (int64_t)ri.y + (int64_t)hk * ri.z + r / kSplitkRows;
+    if (u < U1) ur = W.units[kRouteSplitk][u];
+  }
+  if (ur.nslots <= kCombineShare) {  // (the same for the whole CTA)
+    if (warp == 0) combine_row<D>(A, gw, lane, U1, U2);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    s_late = !wait_done(W.unit_done + u, ur.nslots);
+    if (s_late) {
+      atomicOr((unsigned long long*)&W.hdr->status, (unsigned long long)SDPA_DEV_TIMEOUT);
+      if (A.status_dev) atomicOr(A.status_dev, SDPA_DEV_TIMEOUT);
+    }
+  }
+  __syncthreads();
+  if (s_late) return;
+  // every thread's own acquire of the slots that the count stands for
+  ld_acquire(W.unit_done + u);
+  const int64_t rl = r % kSplitkRows, stride = ur.rows;
+  const float2* ml = W.part_ml[kRouteSplitk] + ur.slot_base + rl;
+  const float* po = W.part_o[kRouteSplitk] + (ur.slot_base + rl) * D + lane * PER;
+  float M = -INFINITY, L = 0.f, acc[PER];
+#pragma unroll
+  for (int k = 0; k < PER; ++k) acc[k] = 0.f;
+  constexpr int kBatch = 4;
+  for (int c0 = warp; c0 < ur.nslots; c0 += kBatch * kWarps) {
+    float2 v[kBatch];
+    float o[kBatch][PER];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int64_t c = c0 + b * kWarps;
+      v[b] = make_float2(-INFINITY, 0.f);
+      if (c < ur.nslots) {
+        v[b] = __ldcg(ml + c * stride);
+#pragma unroll
+        for (int k = 0; k < PER; k += 2) {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(po + c * stride * D + k));
+          o[b][k] = x.x; o[b][k + 1] = x.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      if (v[b].x == -INFINITY) continue;  // an empty (or absent) slot adds nothing
+      const float Mn = fmaxf(M, v[b].x);
+      const float fo = exp2_approx(M - Mn), fc = exp2_approx(v[b].x - Mn);
+      M = Mn;
+      L = L * fo + v[b].y * fc;
+#pragma unroll
+      for (int k = 0; k < PER; ++k) acc[k] = acc[k] * fo + o[b][k] * fc;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < PER; ++k) s_o[warp][lane * PER + k] = acc[k];
+  if (lane == 0) s_ml[warp] = make_float2(M, L);
+  __syncthreads();
+  if (threadIdx.x >= D / 2) return;  // two dims a thread
+  float Ma = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) Ma = fmaxf(Ma, s_ml[w].x);
+  const float Mu = Ma == -INFINITY ? 0.f : Ma;
+  float La = 0.f, x = 0.f, y = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const float f = exp2_approx(s_ml[w].x - Mu);
+    const float2 v = *reinterpret_cast<const float2*>(&s_o[w][2 * threadIdx.x]);
+    La += s_ml[w].y * f;
+    x += v.x * f;
+    y += v.y * f;
+  }
+  const float inv = La > 0.f ? 1.f / La : 0.f;
+  *reinterpret_cast<uint32_t*>(A.out + t * A.o_rs + (int64_t)h * A.o_hs + 2 * threadIdx.x) =
+      pack_bf16x2(x * inv, y * inv);
+}
+
+template __global__ void sdpa_combine_pair_kernel<64>(AttnArgs);
+template __global__ void sdpa_combine_pair_kernel<128>(AttnArgs);
+template __global__ void sdpa_combine_pair_kernel<256>(AttnArgs);
 template __global__ void sdpa_combine_kernel<64>(AttnArgs);
 template __global__ void sdpa_combine_kernel<128>(AttnArgs);
 template __global__ void sdpa_combine_kernel<256>(AttnArgs);
+
+const void* combine_pair_kernel_ptr(int D) {
+  switch (D) {
+    case 64: return (const void*)sdpa_combine_pair_kernel<64>;
+    case 128: return (const void*)sdpa_combine_pair_kernel<128>;
+    default: return (const void*)sdpa_combine_pair_kernel<256>;
+  }
+}
 
 const void* combine_kernel_ptr(int D) {
   switch (D) {

@@ -246,6 +246,7 @@ const void* clone_kernel_ptr();
 const void* splitk_kernel_ptr(int D);
 int splitk_smem_bytes(int D);
 const void* combine_kernel_ptr(int D);
+const void* combine_pair_kernel_ptr(int D);  // a CTA per (row, head) pair
 const void* prefill_kernel_ptr(int D);
 const void* prefill_pair_kernel_ptr(int D);  // D = 64, 128
 int prefill_pair_smem_bytes(int D);
