@@ -93,6 +93,13 @@ static sdpa_status device_info(DevInfo* out) {
       e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, f, kSplitkThreads, smem);
       if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "occupancy: %s", cudaGetErrorString(e));
       di.splitk_per_sm[k] = nb > 0 ? nb : 1;
+      if (Ds[k] <= 128) {
+        e = cudaFuncSetAttribute(q4_tile_kernel_ptr(Ds[k]), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 q4_tile_smem_bytes(Ds[k]));
+        if (e == cudaSuccess)
+          e = cudaFuncSetAttribute(q4_tile_kernel_ptr(Ds[k]), cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+        if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "4-bit tile kernel attributes: %s", cudaGetErrorString(e));
+      }
       for (int wide = 0; wide < 2; ++wide) {
         const void* q4 = q4_splitk_kernel_ptr(Ds[k], wide);
         const int q4_smem = q4_splitk_smem_bytes(Ds[k], wide);
@@ -175,13 +182,15 @@ static Grids grids_for(const DevInfo& di, int D) {
   return g;
 }
 
-// The 4-bit split-K kernel: the wide build when the average segment has more than 8 packed rows (what
-// the host knows of them).  64 x 32768-key decode, 4 rows a segment: narrow XXN us, wide XXW;
-// 16 segments of 64 rows over 4112 keys: narrow XXn, wide XXw.
-static bool q4_wide(int64_t T, int Hq, int Hkv, int S) { return T * (Hq / Hkv) > 8 * (int64_t)S; }
-static Grids q4_grids_for(const DevInfo& di, int D, bool wide) {
+// The 4-bit store's kernel for the split-K route: the tensor-memory one when the average segment (what the
+// host knows of them) has more than 8 packed rows, which is what the other one converts a key for at a
+// time.  16 segments of 64 rows over 4112 keys, D = 128: XXt us against XXn; ...
+static bool q4_tiles(int64_t T, int Hq, int Hkv, int D, int S) {
+  return D <= 128 && T * (Hq / Hkv) > 8 * (int64_t)S;
+}
+static Grids q4_grids_for(const DevInfo& di, int D, bool tiles) {
   Grids g = grids_for(di, D);
-  g.splitk = (int64_t)di.sms * di.q4_per_sm[wide][d_index(D)];
+  g.splitk = tiles ? di.sms : (int64_t)di.sms * di.q4_per_sm[0][d_index(D)];
   return g;
 }
 
@@ -336,9 +345,11 @@ static sdpa_status launch_all(const SchedArgs& sa, const AttnArgs& aa, int D, co
   if (e == cudaSuccess && q4) {
     Q4AttnArgs ga{aa, *q4};
     void* args[] = {(void*)&ga};
-    const bool wide = q4_wide(aa.T, aa.Hq, aa.Hkv, sa.S);
-    e = launch_k(q4_splitk_kernel_ptr(D, wide), (unsigned)g.splitk, kQ4Threads, args, q4_splitk_smem_bytes(D, wide), st,
-                 true);
+    if (aa.sk_rows == kQ4TileRows)
+      e = launch_k(q4_tile_kernel_ptr(D), (unsigned)g.splitk, kQ4TileThreads, args, q4_tile_smem_bytes(D), st, true);
+    else
+      e = launch_k(q4_splitk_kernel_ptr(D, false), (unsigned)g.splitk, kQ4Threads, args, q4_splitk_smem_bytes(D, false),
+                   st, true);
     if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "4-bit split-K launch: %s", cudaGetErrorString(e));
   } else if (e == cudaSuccess) {
     void* args[] = {(void*)&aa};
@@ -381,9 +392,11 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
 
   DevInfo di;
   if ((st = device_info(&di))) return st;
-  const Grids g = q4 ? q4_grids_for(di, D, q4_wide(T, Hq, Hkv, S)) : grids_for(di, D);
+  const bool tiles = q4 && q4_tiles(T, Hq, Hkv, D, S);
+  const Grids g = q4 ? q4_grids_for(di, D, tiles) : grids_for(di, D);
+  const int sk_rows = tiles ? kQ4TileRows : kSplitkRows;
   Workspace W;
-  size_t need = layout_workspace((char*)ws, T, Hq, Hkv, D, S, g.splitk, g.prefill, &W);
+  size_t need = layout_workspace((char*)ws, T, Hq, Hkv, D, S, g.splitk, g.prefill, &W, true, sk_rows);
   Q4StageArgs sg{};
   if (q4 && (sg.pf_cols = q4_stage_cols(T, Hq, Hkv, D, S, rows)) > 0) {
     const int64_t store = align_up(q4_stage_bytes_per_column(rows, Hkv, D) * sg.pf_cols, 256);
@@ -414,6 +427,8 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
   const int group = Hq / Hkv;
   const bool group_fits = group <= kPrefillRows && (kPrefillRows % group) == 0;
   sa.tile_pf = prefill_tile_keys(D);
+  sa.sk_rows = sk_rows;
+  sa.sk_tile = tiles ? kQ4TileKeys : kSplitkTile;
   sa.lo_align = q4 ? kQ4RowAlign : 1;
   sa.pf_cols = sg.pf_cols;
   // (a call-wide window bounds the positions that a staged column has to hold)
@@ -447,6 +462,7 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
   aa.o_rs = o_rs;
   aa.o_hs = o_hs;
   aa.T = T;
+  aa.sk_rows = sk_rows;
   aa.ws = W;
   aa.status_dev = status_dev;
   AppendArgs apw;
@@ -545,14 +561,16 @@ size_t sdpa_varlen_fourbit_workspace_bytes(int64_t T, int Hq, int Hkv, int D, in
   DevInfo di;
   Grids g;
   if (device_info(&di) == SDPA_OK) {
-    g = q4_grids_for(di, D, q4_wide(T, Hq, Hkv, S));
+    g = q4_grids_for(di, D, q4_tiles(T, Hq, Hkv, D, S));
   } else {
     g.splitk = 4096;  // no device: a bound above any real grid
     g.prefill = 1024;
     g_err[0] = 0;
   }
   const int64_t store = align_up(q4_stage_bytes_per_column(rows, Hkv, D) * q4_stage_cols(T, Hq, Hkv, D, S, rows), 256);
-  return layout_workspace(nullptr, T, Hq, Hkv, D, S, g.splitk, g.prefill, nullptr) + 2 * store;
+  return layout_workspace(nullptr, T, Hq, Hkv, D, S, g.splitk, g.prefill, nullptr, true,
+                          q4_tiles(T, Hq, Hkv, D, S) ? kQ4TileRows : kSplitkRows) +
+         2 * store;
 }
 
 sdpa_status sdpa_varlen_fourbit(const void* q, int64_t T, int Hq, int D, int64_t q_row_stride, int64_t q_head_stride,

@@ -55,7 +55,7 @@ __device__ __forceinline__ void combine_row(const AttnArgs& A, int64_t gw, int l
   if (q != kRouteNone) {
     // route-indexed fields picked by select: a runtime index would copy them to local memory
     const bool pf = q == kRoutePrefill;
-    const int rpu = pf ? prefill_unit_rows(D) : kSplitkRows;
+    const int rpu = pf ? prefill_unit_rows(D) : A.sk_rows;
     const int hk = h / A.group;
     const int64_t r = (int64_t)ri.w * A.group + (h % A.group);
     const int64_t rb = r / rpu;
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kCombineThreads) sdpa_combine_pair_kernel(Attn
   if (ri.x == kRouteSplitk) {
     const int hk = h / A.group;
     r = (int64_t)ri.w * A.group + (h % A.group);
-    u = (int64_t)ri.y + (int64_t)hk * ri.z + r / kSplitkRows;
+    u = (int64_t)ri.y + (int64_t)hk * ri.z + r / A.sk_rows;
     if (u < U1) ur = W.units[kRouteSplitk][u];
   }
   if (ur.nslots <= kCombineShare) {  // (the same for the whole CTA)
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kCombineThreads) sdpa_combine_pair_kernel(Attn
   if (s_late) return;
   // every thread's own acquire of the slots that the count stands for
   ld_acquire(W.unit_done + u);
-  const int64_t rl = r % kSplitkRows, stride = ur.rows;
+  const int64_t rl = r % A.sk_rows, stride = ur.rows;
   const float2* ml = W.part_ml[kRouteSplitk] + ur.slot_base + rl;
   const float* po = W.part_o[kRouteSplitk] + (ur.slot_base + rl) * D + lane * PER;
   float M = -INFINITY, L = 0.f, acc[PER];

@@ -132,7 +132,8 @@ __host__ __device__ inline int64_t part_cap(int64_t ucap, int64_t grid, int rows
 // that route's unit table and partial slots are empty.
 __host__ inline size_t layout_workspace(char* base, int64_t T, int Hq, int Hkv, int D, int S,
                                         int64_t grid_splitk, int64_t grid_prefill,
-                                        Workspace* ws, bool with_prefill = true) {
+                                        Workspace* ws, bool with_prefill = true,
+                                        int splitk_rows = kSplitkRows) {
   int64_t off = 0;
   auto take = [&](int64_t bytes) {
     int64_t o = off;
@@ -145,7 +146,7 @@ __host__ inline size_t layout_workspace(char* base, int64_t T, int Hq, int Hkv, 
   w.row_seg = (int32_t*)take(4 * (T > 0 ? T : 1));
   w.row_info = (int4*)take(16 * (T > 0 ? T : 1));
   w.seg_flag = (int32_t*)take(4 * (S > 0 ? S : 1));
-  const int rpu[3] = {0, kSplitkRows, prefill_unit_rows(D)};
+  const int rpu[3] = {0, splitk_rows, prefill_unit_rows(D)};
   const int64_t grid[3] = {0, grid_splitk, grid_prefill};
   for (int r = 1; r < 3; ++r) {
     const bool used = r == kRouteSplitk || with_prefill;
@@ -174,6 +175,7 @@ struct AttnArgs {
   __nv_bfloat16* out;
   int64_t o_rs, o_hs;
   int64_t T;
+  int sk_rows;         // packed rows of a split-K unit
   Workspace ws;
   int32_t* status_dev;
 };
@@ -213,6 +215,8 @@ struct SchedArgs {
   int policy;      // SDPA_ROUTE_*
   int prefill_ok;  // prefill kernel usable for this call (group divides 128, tensor maps made)
   int tile_pf;     // keys per prefill tile
+  int sk_rows;     // packed rows of a split-K unit, and keys of its tiles
+  int sk_tile;
   int lo_align;    // split-K units' key ranges begin at a multiple of this (a power of two, at least 1)
   int64_t rows_pf; // store rows the prefill kernel sees (a ring wraps there)
   int pf_cols;     // 4-bit store: columns staged for the prefill kernel, the first pf_cols segments

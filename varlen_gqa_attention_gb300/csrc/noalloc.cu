@@ -135,6 +135,8 @@ extern "C" sdpa_status sdpa_varlen_splitk_static(
   sa.policy = SDPA_ROUTE_SPLITK;
   sa.prefill_ok = 0;
   sa.tile_pf = kPrefillTile;
+  sa.sk_rows = kSplitkRows;
+  sa.sk_tile = kSplitkTile;
   sa.lo_align = 1;
   sa.rows_pf = rows;
   sa.grid[0] = 0;
@@ -162,6 +164,7 @@ extern "C" sdpa_status sdpa_varlen_splitk_static(
   aa.o_rs = o_row_stride;
   aa.o_hs = o_head_stride;
   aa.T = T;
+  aa.sk_rows = kSplitkRows;
   aa.ws = W;
   aa.status_dev = status_dev;
 

@@ -19,6 +19,7 @@
 namespace sdpa {
 
 constexpr int kQ4Group = 32;     // dims that share a scale
+constexpr float kQ4PLift = 7.f;  // the attention kernels hold their fp16 probabilities 2^7 times larger
 constexpr int kQ4RowAlign = 16;  // store rows are a multiple of this, so that 16 rows of codes and
                                  // of scales are whole 16-byte blocks at every head dim
 
@@ -89,6 +90,27 @@ __device__ __forceinline__ void q4_scales_f16(uint32_t a, uint32_t b, __half2* s
   *z2 = __hmul2(*s2, __float2half2_rn(-12.f));
 }
 
+// 8 dims of a query row (16 bytes) as the operand words of two k-steps: the conversion of K pairs
+// nibbles i and i + 4 of a word, so the fragments pair dims i and i + 4.
+__device__ __forceinline__ uint4 q4_q_order(const uint4& a) {
+  return make_uint4(__byte_perm(a.x, a.z, 0x5410), __byte_perm(a.x, a.z, 0x7632),
+                    __byte_perm(a.y, a.w, 0x5410), __byte_perm(a.y, a.w, 0x7632));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+
+// 16-byte blocks from global to shared memory, counted on an mbarrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
 // Device pointers of a 4-bit store.
 struct Q4Store {
   uint8_t* kc;
@@ -121,6 +143,13 @@ const void* q4_stage_kernel_ptr(int D);
 
 // Entry points (q4_attn.cu).
 constexpr int kQ4Threads = 160;  // four warps of attention, one that loads
+// The tensor-memory kernel for segments of several rows (q4_tile.cu; D = 64, 128): one CTA per SM, units of
+// kQ4TileRows packed rows, tiles of kQ4TileKeys keys.
+constexpr int kQ4TileRows = 128;
+constexpr int kQ4TileKeys = 128;
+constexpr int kQ4TileThreads = 448;
+const void* q4_tile_kernel_ptr(int D);
+int q4_tile_smem_bytes(int D);
 const void* q4_splitk_kernel_ptr(int D, bool wide);
 int q4_splitk_smem_bytes(int D, bool wide);
 

@@ -35,7 +35,6 @@
 namespace sdpa {
 
 constexpr int kQ4Consumers = 128; // threads of the four attention warps
-constexpr float kQ4PLift = 7.f;    // P is held 2^7 times larger
 
 // Two builds of the kernel: the narrow one takes 8 query rows a warp (one token's heads) and the wide
 // one 16, whose output takes twice the registers; each takes units of any size, the narrow one
@@ -67,13 +66,6 @@ struct Q4Piece {
   int32_t slot, valid;     // valid 0: no more work
 };
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
-
 // D(16x8 f32) += A(16x16 f16, row) * B(16x8 f16, col)
 __device__ __forceinline__ void mma_f16_16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -88,22 +80,10 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(v));
   return r;
 }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
 // Waits for a phase unless the CTA has given up already; false when it has (or now does).  The
 // lanes of a warp agree on the answer.
 __device__ __forceinline__ bool q4_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
   return __all_sync(0xffffffffu, !*abort && mbar_wait(bar, parity, abort));
-}
-
-// 8 dims of a query row (16 bytes) as the operand words of two k-steps: the conversion of K pairs
-// nibbles i and i + 4 of a word, so the fragments pair dims i and i + 4.
-__device__ __forceinline__ uint4 q4_q_order(const uint4& a) {
-  return make_uint4(__byte_perm(a.x, a.z, 0x5410), __byte_perm(a.x, a.z, 0x7632),
-                    __byte_perm(a.y, a.w, 0x5410), __byte_perm(a.y, a.w, 0x7632));
 }
 
 // Bytes [p, p + 4 N) of shared memory into N words.

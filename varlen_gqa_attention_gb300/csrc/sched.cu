@@ -148,10 +148,10 @@ __device__ __forceinline__ void load_seg(const SchedArgs& A, int s, int32_t* seg
 }
 
 __device__ __forceinline__ int rows_per_unit(const SchedArgs& A, int route) {
-  return route == kRoutePrefill ? prefill_unit_rows(A.D) : kSplitkRows;
+  return route == kRoutePrefill ? prefill_unit_rows(A.D) : A.sk_rows;
 }
 __device__ __forceinline__ int tile_len(const SchedArgs& A, int route) {
-  return route == kRoutePrefill ? A.tile_pf : kSplitkTile;
+  return route == kRoutePrefill ? A.tile_pf : A.sk_tile;
 }
 
 // Route of a live segment.  The prefill kernel takes segments that fill at least one
