@@ -7,18 +7,22 @@
 // K and V in shared memory, S, P and O in tensor memory.  Per CTA (one per SM), 14 warps:
 //   * a loading warp walks the CTA's pieces (the split-K route's, in units of 128 packed rows and tiles of
 //     128 keys), hands them on, and streams their codes and scales into a ring by bulk copies;
-//   * eight converting warps turn a tile's codes into bf16 K and fp16 V tiles (exactly: see q4.cuh),
+//   * four converting warps turn a tile's codes into bf16 K and fp16 V tiles (exactly: see q4.cuh),
 //     written in the 128-byte swizzle that the products read, and a piece's query rows likewise;
-//   * one warp issues the products, S two tiles ahead of PV;
-//   * four softmax warps, a thread a row (= tensor-memory lane): a warp none of whose rows exist skips its
-//     work, so that a unit of 64 rows costs half of one of 128.
+//   * one warp issues the products: S(0) S(1) | PV(0) S(2) | PV(1) S(3) ...  P lies over the scores it came
+//     from, which the next scores of that buffer overwrite behind PV (one thread's products run in order);
+//   * eight softmax warps, a thread a row (= tensor-memory lane), four for a tile's first 64 keys and four
+//     for the others.  The two halves keep a maximum, a sum and an output of their own, as if they were two
+//     CTAs' pieces, and are joined when the piece ends: nothing passes between them in between.  A warp
+//     none of whose rows exist skips its work, so that a unit of 64 rows costs half of one of 128.
 // A word of codes gives its values in pairs (dim i, dim i + 4); K and V tiles keep that order, and so do
 // the query rows, and the output's columns are put in order as they are written.
 // P is fp16, held 2^7 times larger, as in q4_attn.cu.
 //
-// Bound by shared memory and the issue slots: a tile of 128 keys at D = 128 is 64 KB written by the
-// converting warps and 96 KB read by the products (1.3 thousand cycles at 128 bytes a cycle), and about
-// 1.8 thousand warp instructions of conversion with 0.8 thousand for each 32 rows of softmax.
+// Bound by the issue slots and by each role's own latency: a tile at D = 128 is about 1.8 thousand warp
+// instructions of conversion and 0.9 thousand for each 32 rows of softmax.  With one warp a row quarter
+// for all 128 keys (half the softmax warps, twice the converting ones) a tile of 64 rows took 3.7 thousand
+// cycles, waiting for its two softmax warps: 16 segments of 64 rows over 4112 keys 55 us, and XX us so.
 #include "q4.cuh"
 #include "tc.cuh"
 
@@ -41,10 +45,9 @@ struct Q4TileCfg {
   // (at D = 64 too, more than half of an SM's: a second CTA would only wait for tensor memory)
   static constexpr int kUsed = kOffCodes + kCodeStages * kCodeBytes + 1024;  // + alignment slack
   static constexpr int kBytes = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
-  // tensor memory columns: S_b fp32, P_b as fp16 pairs, O
+  // tensor memory columns: S_b fp32 (P_b as fp16 pairs over the first 32 of each half's 64), O of each half
   static constexpr int kColS = 0;
-  static constexpr int kColP = 256;
-  static constexpr int kColO = 384;
+  static constexpr int kColO = 256;
 };
 
 // mbarriers
@@ -54,9 +57,9 @@ struct Q4TileBars {
   static constexpr int K_READY = 6;   // [2] K tile written
   static constexpr int V_READY = 8;   // [2]
   static constexpr int S_FULL = 10;   // [2] S(g) done: also, K stage g % 2 may be written again
-  static constexpr int S_FREE = 12;   // [2] S_b read by the softmax
-  static constexpr int P_FULL = 14;   // [2]
-  static constexpr int PV_DONE = 16;  // [2] also, V stage g % 2 and P_b may be written again
+  static constexpr int P_FULL = 12;   // [2]
+  static constexpr int PV_DONE = 14;  // [2] also, V stage g % 2 may be written again
+  static constexpr int ML = 16;       // the halves' maxima and sums of a piece are in shared memory
   static constexpr int Q_READY = 18;
   static constexpr int Q_EMPTY = 19;  // every S of the piece is done
   static constexpr int PC_FULL = 20;  // [2] piece record written
@@ -64,7 +67,7 @@ struct Q4TileBars {
   static constexpr int DRAIN = 24;
   static constexpr int N = 25;
 };
-constexpr int kQ4SoftWarps = 4, kQ4ConvWarps = 8;
+constexpr int kQ4SoftWarps = 8, kQ4ConvWarps = 4;
 constexpr int kQ4TileRoles = kQ4SoftWarps + kQ4ConvWarps + 1;  // warps that read piece records
 
 struct Q4TilePiece {
@@ -78,7 +81,7 @@ struct Q4TilePiece {
 constexpr uint32_t kIdescPV64 = (1u << 4) | (1u << 16) | ((64u >> 3) << 17) | ((128u >> 4) << 24);
 constexpr uint32_t kIdescPV128 = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 
-// 32 consecutive keys' scores of a row: those outside [lo, hi) (offsets from the first) are masked.
+// 64 consecutive keys' scores of a row: those outside [lo, hi) (offsets from the first) are masked.
 __device__ __forceinline__ void tile_mask64(float (&x)[64], int lo, int hi) {
 #pragma unroll
   for (int k = 0; k < 64; ++k) x[k] = k >= lo && k < hi ? x[k] : -INFINITY;
@@ -94,6 +97,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) sdpa_q4_tile_kernel(Q4AttnA
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ int s_written[2];  // softmax warps whose partial rows of a piece are written
+  __shared__ float2 s_ml[2][128];
   const AttnArgs& A = G.a;
 
   griddep_wait();  // the scheduler's output (and the prefill kernel's end)
@@ -125,7 +129,6 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) sdpa_q4_tile_kernel(Q4AttnA
       mbar_init(bar(B::K_READY + b), kQ4ConvWarps);
       mbar_init(bar(B::V_READY + b), kQ4ConvWarps);
       mbar_init(bar(B::S_FULL + b), 1);
-      mbar_init(bar(B::S_FREE + b), kQ4SoftWarps);
       mbar_init(bar(B::P_FULL + b), kQ4SoftWarps);
       mbar_init(bar(B::PV_DONE + b), 1);
       mbar_init(bar(B::PC_FULL + b), 1);
@@ -133,6 +136,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) sdpa_q4_tile_kernel(Q4AttnA
       s_written[b] = 0;
     }
     mbar_init(bar(B::Q_READY), kQ4ConvWarps);
+    mbar_init(bar(B::ML), kQ4SoftWarps);
     mbar_init(bar(B::Q_EMPTY), 1);
     mbar_init(bar(B::DRAIN), 1);
     s_abort = 0;
@@ -221,7 +225,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) sdpa_q4_tile_kernel(Q4AttnA
     const uint64_t v_desc = sdesc_sw128(sbase + C::kOffV, 128 * 128, 1024);
     auto issue_s = [&](uint32_t g) -> bool {
       const uint32_t b = g & 1, use = g >> 1;
-      if (!all(wait(B::K_READY + b, use) && wait(B::S_FREE + b, use + 1))) return false;
+      if (!all(wait(B::K_READY + b, use))) return false;
       tc_fence_after();
       const uint64_t kd = k_desc + (uint64_t)((b * C::kTileBytes) >> 4);
 #pragma unroll
@@ -246,18 +250,18 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) sdpa_q4_tile_kernel(Q4AttnA
       if (ok && tiles <= 2) tc_commit_w(bar(B::Q_EMPTY));
       for (int j = 0; ok && j < tiles; ++j) {
         const uint32_t g = g0 + j, b = g & 1, use = g >> 1;
-        if (j + 2 < tiles) {
-          if (!(ok = issue_s(g + 2))) break;
-          if (j + 3 == tiles) tc_commit_w(bar(B::Q_EMPTY));
-        }
         if (!(ok = all(wait(B::P_FULL + b, use) && wait(B::V_READY + b, use)))) break;
         tc_fence_after();
         const uint64_t vd = v_desc + (uint64_t)((b * C::kTileBytes) >> 4);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          tc_mma_ts_w(tmem + C::kColO, tmem + C::kColP + b * 64 + 8 * k, vd + (uint64_t)((k * 16 * 128) >> 4),
-                      kIdescPV, j > 0 || k > 0 ? 1u : 0u);
+          tc_mma_ts_w(tmem + C::kColO + (k >> 2) * D, tmem + C::kColS + b * 128 + (k >> 2) * 64 + 8 * (k & 3),
+                      vd + (uint64_t)((k * 16 * 128) >> 4), kIdescPV, j > 0 || (k & 3) ? 1u : 0u);
         tc_commit_w(bar(B::PV_DONE + b));
+        if (j + 2 < tiles) {
+          if (!(ok = issue_s(g + 2))) break;
+          if (j + 3 == tiles) tc_commit_w(bar(B::Q_EMPTY));
+        }
       }
       g0 += tiles;
     }
@@ -270,9 +274,9 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) sdpa_q4_tile_kernel(Q4AttnA
     // ---------------------------------------------------------------- converting warps
     const int cw = warp - W_CONV, tid = cw * 32 + lane;
     const uint32_t kbits = in_register(kQ4Bf16), vbits = in_register(kQ4F16);
-    // this lane's key of the tile, and which 32 dims of every 64 it converts: eight lanes that store
-    // together then meet eight different 16-byte columns of the swizzle
-    const int key = cw * 16 + (lane >> 1), half = lane & 1;
+    // this lane's keys of the tile (key0 and key0 + 64), and which 32 dims of every 64 it converts: eight
+    // lanes that store together then meet eight different 16-byte columns of the swizzle
+    const int key0 = cw * 16 + (lane >> 1), half = lane & 1;
     uint32_t g = 0;
     bool ok = true;
     for (uint32_t n = 0; ok; ++n) {
@@ -280,30 +284,39 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) sdpa_q4_tile_kernel(Q4AttnA
       const Q4TilePiece& pc = s_piece[n & 1];
       const bool valid = pc.valid;
       const int tiles = valid ? (pc.nkeys + C::kKeys - 1) / C::kKeys : 0;
-      // the piece's query rows, in flight until the last piece's scores are done
-      constexpr int kQ = 128 * (D / 8) / (kQ4ConvWarps * 32);  // 16-byte chunks of a thread
+      const int chunks = valid ? pc.ur.rows * (D / 8) : 0;  // 16-byte chunks of the piece's query rows
+      const int64_t q0 = (int64_t)pc.ur.rb * kQ4TileRows;
+      const int q_start = pc.ur.q_start, hk = pc.ur.hk;
+      constexpr int kQ = 8, kT = kQ4ConvWarps * 32;
       uint4 q[kQ];
-      if (valid) {
+      auto load_q = [&](int i0) {
 #pragma unroll
         for (int i = 0; i < kQ; ++i) {
-          const int idx = tid + i * (kQ4ConvWarps * 32), rl = idx / (D / 8), c = idx % (D / 8);
-          q[i] = make_uint4(0, 0, 0, 0);
-          if (rl < pc.ur.rows) {
-            const int64_t r = (int64_t)pc.ur.rb * kQ4TileRows + rl;
-            const int64_t t = pc.ur.q_start + udiv(r, A.group);
-            const int h = pc.ur.hk * A.group + (int)(r % A.group);
-            q[i] = *reinterpret_cast<const uint4*>(A.q + t * A.q_rs + (int64_t)h * A.q_hs + 8 * c);
+          const int idx = tid + (i0 + i) * kT, rl = idx / (D / 8), c = idx % (D / 8);
+          if (idx < chunks) {
+            const int64_t r = q0 + rl, t = udiv(r, A.group);
+            const int h = hk * A.group + (int)(r - t * A.group);
+            q[i] = *reinterpret_cast<const uint4*>(A.q + (q_start + t) * A.q_rs + (int64_t)h * A.q_hs + 8 * c);
           }
         }
-      }
+      };
+      auto store_q = [&](int i0) {
+#pragma unroll
+        for (int i = 0; i < kQ; ++i) {
+          const int idx = tid + (i0 + i) * kT, rl = idx / (D / 8), c = idx % (D / 8);
+          if (idx < chunks)
+            *reinterpret_cast<uint4*>(smem + C::kOffQ + (c / 8) * (128 * 128) + swz(rl, c % 8, 128)) = q4_q_order(q[i]);
+        }
+      };
+      load_q(0);  // in flight until the last piece's scores are done
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B::PC_EMPTY + (n & 1)));
       if (!valid) break;
       if (n > 0 && !(ok = all(wait(B::Q_EMPTY, n - 1)))) break;
-#pragma unroll
-      for (int i = 0; i < kQ; ++i) {
-        const int idx = tid + i * (kQ4ConvWarps * 32), rl = idx / (D / 8), c = idx % (D / 8);
-        *reinterpret_cast<uint4*>(smem + C::kOffQ + (c / 8) * (128 * 128) + swz(rl, c % 8, 128)) = q4_q_order(q[i]);
+      store_q(0);
+      for (int i0 = kQ; i0 * kT < chunks; i0 += kQ) {
+        load_q(i0);
+        store_q(i0);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -315,31 +328,37 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) sdpa_q4_tile_kernel(Q4AttnA
         const uint8_t* codes = smem + C::kOffCodes + st * C::kCodeBytes;
         const uint8_t* scales = codes + 2 * C::kCodes;
         constexpr int NH = D / 64;  // 64-dim columns of the tile
-        uint4 w[2][NH];
-        uint32_t sb[2][NH];
+        uint4 w[2][2][NH];          // [K, V][key0, key0 + 64]
+        uint32_t sb[2][2][NH];
 #pragma unroll
         for (int v = 0; v < 2; ++v)
 #pragma unroll
-          for (int c = 0; c < NH; ++c) {
-            w[v][c] = *reinterpret_cast<const uint4*>(codes + v * C::kCodes + key * C::kRowBytes + c * 32 + half * 16);
-            sb[v][c] = scales[v * C::kScales + key * C::kScaleBytes + c * 2 + half];
-          }
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int c = 0; c < NH; ++c) {
+              const int key = key0 + 64 * x;
+              w[v][x][c] =
+                  *reinterpret_cast<const uint4*>(codes + v * C::kCodes + key * C::kRowBytes + c * 32 + half * 16);
+              sb[v][x][c] = scales[v * C::kScales + key * C::kScaleBytes + c * 2 + half];
+            }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B::C_EMPTY + st));
         // K, once the scores that read this stage are done
         if (g >= 2 && !(ok = all(wait(B::S_FULL + b, use - 1)))) break;
         uint8_t* kt = smem + C::kOffK + b * C::kTileBytes;
 #pragma unroll
-        for (int c = 0; c < NH; ++c) {
-          __nv_bfloat162 s2, z2;
-          q4_scales_bf16(sb[0][c], &s2, &z2);
-          const uint32_t x[4] = {w[0][c].x, w[0][c].y, w[0][c].z, w[0][c].w};
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4*>(kt + c * (128 * 128) + swz(key, half * 4 + i, 128)) =
-                make_uint4(q4_pair_bf16(x[i], kbits, s2, z2), q4_pair_bf16(x[i] >> 4, kbits, s2, z2),
-                           q4_pair_bf16(x[i] >> 8, kbits, s2, z2), q4_pair_bf16(x[i] >> 12, kbits, s2, z2));
-        }
+          for (int c = 0; c < NH; ++c) {
+            __nv_bfloat162 s2, z2;
+            q4_scales_bf16(sb[0][x][c], &s2, &z2);
+            const uint32_t y[4] = {w[0][x][c].x, w[0][x][c].y, w[0][x][c].z, w[0][x][c].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(kt + c * (128 * 128) + swz(key0 + 64 * x, half * 4 + i, 128)) =
+                  make_uint4(q4_pair_bf16(y[i], kbits, s2, z2), q4_pair_bf16(y[i] >> 4, kbits, s2, z2),
+                             q4_pair_bf16(y[i] >> 8, kbits, s2, z2), q4_pair_bf16(y[i] >> 12, kbits, s2, z2));
+          }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B::K_READY + b));
@@ -347,16 +366,18 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) sdpa_q4_tile_kernel(Q4AttnA
         if (g >= 2 && !(ok = all(wait(B::PV_DONE + b, use - 1)))) break;
         uint8_t* vt = smem + C::kOffV + b * C::kTileBytes;
 #pragma unroll
-        for (int c = 0; c < NH; ++c) {
-          __half2 s2, z2;
-          q4_scales_f16(sb[1][c], sb[1][c], &s2, &z2);
-          const uint32_t x[4] = {w[1][c].x, w[1][c].y, w[1][c].z, w[1][c].w};
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4*>(vt + c * (128 * 128) + swz(key, half * 4 + i, 128)) =
-                make_uint4(q4_pair_f16(x[i] << 6, vbits, s2, z2), q4_pair_f16(x[i] << 2, vbits, s2, z2),
-                           q4_pair_f16(x[i] >> 2, vbits, s2, z2), q4_pair_f16(x[i] >> 6, vbits, s2, z2));
-        }
+          for (int c = 0; c < NH; ++c) {
+            __half2 s2, z2;
+            q4_scales_f16(sb[1][x][c], sb[1][x][c], &s2, &z2);
+            const uint32_t y[4] = {w[1][x][c].x, w[1][x][c].y, w[1][x][c].z, w[1][x][c].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(vt + c * (128 * 128) + swz(key0 + 64 * x, half * 4 + i, 128)) =
+                  make_uint4(q4_pair_f16(y[i] << 6, vbits, s2, z2), q4_pair_f16(y[i] << 2, vbits, s2, z2),
+                             q4_pair_f16(y[i] >> 2, vbits, s2, z2), q4_pair_f16(y[i] >> 6, vbits, s2, z2));
+          }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B::V_READY + b));
@@ -364,10 +385,9 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) sdpa_q4_tile_kernel(Q4AttnA
     }
   } else {
     // ---------------------------------------------------------------- softmax warps
-    const int row = warp * 32 + lane;
-    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
-    const uint32_t t_s = tmem + lane_off + C::kColS, t_p = tmem + lane_off + C::kColP;
-    const uint32_t t_o = tmem + lane_off + C::kColO;
+    const int hf = warp >> 2, row = (warp & 3) * 32 + lane;  // half of the tile's keys; row of the unit
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lane_off + C::kColS + hf * 64, t_o = tmem + lane_off + C::kColO;
     const float sl2 = A.scale_log2;
     // a piece's partial rows, written a piece ago, are counted in the next one's epilogue: by then the
     // fence has nothing to wait for.  The last of the warps that wrote some counts the slot.
@@ -396,7 +416,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) sdpa_q4_tile_kernel(Q4AttnA
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B::PC_EMPTY + (n & 1)));
       const int tiles = (nkeys + C::kKeys - 1) / C::kKeys;
-      const bool here = warp * 32 < ur.rows;  // the warp has rows of this unit
+      const bool here = (warp & 3) * 32 < ur.rows;  // the warp has rows of this unit
       const bool live = row < ur.rows;
       const int64_t r = (int64_t)ur.rb * kQ4TileRows + row;
       const int64_t qi = udiv(r, A.group);
@@ -411,22 +431,15 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) sdpa_q4_tile_kernel(Q4AttnA
         const uint32_t b = g & 1, use = g >> 1;
         if (!(ok = all(wait(B::S_FULL + b, use)))) break;
         if (here) {
-          const int lo = first - j * C::kKeys, hi = last - j * C::kKeys;
-          const bool edge = __any_sync(0xffffffffu, live && (lo > 0 || hi < C::kKeys));
+          const int off = j * C::kKeys + hf * 64, lo = first - off, hi = last - off;
           tc_fence_after();
           float x[64];
           tmem_ld64(t_s + b * 128, x);
-          if (edge) tile_mask64(x, lo, hi);
-          float mx = x[0];
+          if (__any_sync(0xffffffffu, live && (lo > 0 || hi < 64))) tile_mask64(x, lo, hi);
+          float mx4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-          for (int k = 1; k < 64; ++k) mx = fmaxf(mx, x[k]);
-          tmem_ld64(t_s + b * 128 + 64, x);
-          if (edge) tile_mask64(x, lo - 64, hi - 64);
-#pragma unroll
-          for (int k = 0; k < 64; ++k) mx = fmaxf(mx, x[k]);
-          // P_b was last read by PV(g - 2)
-          if (g >= 2 && !(ok = all(wait(B::PV_DONE + b, use - 1)))) break;
-          const float mn = fmaxf(m, mx * sl2);
+          for (int k = 4; k < 64; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], x[k]);
+          const float mn = fmaxf(m, fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2);
           const bool up = live && mn > m + 8.f;  // false while nothing is visible
           if (__any_sync(0xffffffffu, up)) {
             const float alpha = up ? exp2_approx(m - mn) : 1.f;
@@ -441,60 +454,63 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) sdpa_q4_tile_kernel(Q4AttnA
 #pragma unroll 1
               for (int c = 0; c < D / 32; ++c) {
                 float o[32];
-                tmem_ld32(t_o + 32 * c, o);
+                tmem_ld32(t_o + hf * D + 32 * c, o);
 #pragma unroll
                 for (int k = 0; k < 32; ++k) o[k] *= alpha;
-                tmem_st32(t_o + 32 * c, o);
+                tmem_st32(t_o + hf * D + 32 * c, o);
               }
             }
           }
-          tc_fence_after();
+          uint32_t pw[32];
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int hf = 1; hf >= 0; --hf) {
-            if (hf == 0) {
-              tmem_ld64(t_s + b * 128, x);
-              if (edge) tile_mask64(x, lo, hi);
-            }
-            uint32_t pw[32];
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const float p0 = exp2_approx(fmaf(x[2 * k], sl2, nmu)), p1 = exp2_approx(fmaf(x[2 * k + 1], sl2, nmu));
-              sum[(2 * k) & 3] += p0;
-              sum[(2 * k + 1) & 3] += p1;
-              pw[k] = pack_f16x2(p0, p1);
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_st32u(t_p + b * 64 + 32 * hf, pw);
+          for (int k = 0; k < 32; ++k) {
+            const float p0 = exp2_approx(fmaf(x[2 * k], sl2, nmu)), p1 = exp2_approx(fmaf(x[2 * k + 1], sl2, nmu));
+            sum[(2 * k) & 3] += p0;
+            sum[(2 * k + 1) & 3] += p1;
+            pw[k] = pack_f16x2(p0, p1);
           }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_st32u(t_s + b * 128, pw);  // over the scores
           tc_fence_before();
         }
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(B::S_FREE + b));
-          mbar_arrive(bar(B::P_FULL + b));
-        }
+        if (lane == 0) mbar_arrive(bar(B::P_FULL + b));
       }
       if (!ok) break;
       count_late();
-      if (!here) continue;
+      // the halves' maxima and sums change hands once the piece's last product is done: every warp has then
+      // left the last piece's
       if (!(ok = all(wait(B::PV_DONE + ((g - 1) & 1), (g - 1) >> 1)))) break;
       tc_fence_after();
       if (l != l) m = 0.f;  // a row whose scores are NaN has no maximum: it is joined as one
+      s_ml[hf][row] = make_float2(m, l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B::ML));
+      if (!(ok = all(wait(B::ML, n)))) break;
+      if (!here) continue;
+      const float2 ml0 = s_ml[0][row], ml1 = s_ml[1][row];
+      const float M = fmaxf(ml0.x, ml1.x), Mu = M == -INFINITY ? 0.f : M;
+      const float e0 = exp2_approx(ml0.x - Mu), e1 = exp2_approx(ml1.x - Mu);
+      const float L = ml0.y * e0 + ml1.y * e1;
       const bool direct = ur.nslots == 1;
-      const bool empty = l == 0.f;  // a row that sees no key writes zeros (never 0 * O)
-      const float wgt = direct ? 1.f / l : 1.f;
+      const bool empty = L == 0.f;  // a row that sees no key writes zeros (never 0 * O)
+      const float wgt = direct ? 1.f / L : 1.f;
+      const float f0 = e0 * wgt, f1 = e1 * wgt;
       const int h = ur.hk * A.group + (int)(r - qi * A.group);
-      __nv_bfloat16* orow = A.out + (ur.q_start + qi) * A.o_rs + (int64_t)h * A.o_hs;
+      // each half's warps write half of the dims
+      __nv_bfloat16* orow = A.out + (ur.q_start + qi) * A.o_rs + (int64_t)h * A.o_hs + hf * (D / 2);
       const int64_t pidx = ur.slot_base + (int64_t)slot * ur.rows + row;
-      float* prow = A.ws.part_o[kRouteSplitk] + pidx * D;
+      float* prow = A.ws.part_o[kRouteSplitk] + pidx * D + hf * (D / 2);
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        float o[32];
-        tmem_ld32(t_o + 32 * c, o);
+      for (int c = 0; c < D / 64; ++c) {
+        float o[32], o1[32];
+        __syncwarp();
+        tmem_ld32(t_o + hf * (D / 2) + 32 * c, o);
+        tmem_ld32(t_o + D + hf * (D / 2) + 32 * c, o1);
         if (!live) continue;
 #pragma unroll
-        for (int k = 0; k < 32; ++k) o[k] = empty ? 0.f : o[k] * wgt;
+        for (int k = 0; k < 32; ++k) o[k] = empty ? 0.f : o[k] * f0 + o1[k] * f1;
 #pragma unroll
         for (int k = 0; k < 32; k += 8) {  // columns of eight dims: 0 4 1 5 2 6 3 7
           const float* y = o + k;
@@ -510,9 +526,9 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) sdpa_q4_tile_kernel(Q4AttnA
       }
       tc_fence_before();
       if (!direct) {
-        if (live) A.ws.part_ml[kRouteSplitk][pidx] = make_float2(m, l);
+        if (live && hf == 0) A.ws.part_ml[kRouteSplitk][pidx] = make_float2(M, L);
         late = A.ws.unit_done + unit;
-        late_warps = (ur.rows + 31) / 32;
+        late_warps = 2 * ((ur.rows + 31) / 32);
         late_at = n & 1;
       }
     }
