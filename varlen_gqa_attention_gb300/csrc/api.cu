@@ -51,7 +51,7 @@ struct DevInfo {
   bool ready = false;
   int sms = 0;
   int splitk_per_sm[3] = {0, 0, 0};  // D = 64, 128, 256
-  int q4_per_sm[2][3] = {};          // narrow, wide
+  int q4_per_sm[3] = {0, 0, 0};
   bool prefill_ok[3] = {false, false, false};
 };
 static std::mutex g_mu;
@@ -100,17 +100,15 @@ static sdpa_status device_info(DevInfo* out) {
           e = cudaFuncSetAttribute(q4_tile_kernel_ptr(Ds[k]), cudaFuncAttributePreferredSharedMemoryCarveout, 100);
         if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "4-bit tile kernel attributes: %s", cudaGetErrorString(e));
       }
-      for (int wide = 0; wide < 2; ++wide) {
-        const void* q4 = q4_splitk_kernel_ptr(Ds[k], wide);
-        const int q4_smem = q4_splitk_smem_bytes(Ds[k], wide);
-        e = cudaFuncSetAttribute(q4, cudaFuncAttributeMaxDynamicSharedMemorySize, q4_smem);
-        if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "smem attribute: %s", cudaGetErrorString(e));
-        e = cudaFuncSetAttribute(q4, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-        if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "carveout attribute: %s", cudaGetErrorString(e));
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, q4, kQ4Threads, q4_smem);
-        if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "occupancy: %s", cudaGetErrorString(e));
-        di.q4_per_sm[wide][k] = nb > 0 ? nb : 1;
-      }
+      const void* q4 = q4_splitk_kernel_ptr(Ds[k]);
+      const int q4_smem = q4_splitk_smem_bytes(Ds[k]);
+      e = cudaFuncSetAttribute(q4, cudaFuncAttributeMaxDynamicSharedMemorySize, q4_smem);
+      if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "smem attribute: %s", cudaGetErrorString(e));
+      e = cudaFuncSetAttribute(q4, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+      if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "carveout attribute: %s", cudaGetErrorString(e));
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, q4, kQ4Threads, q4_smem);
+      if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "occupancy: %s", cudaGetErrorString(e));
+      di.q4_per_sm[k] = nb > 0 ? nb : 1;
       e = cudaFuncSetAttribute(combine_pair_kernel_ptr(Ds[k]), cudaFuncAttributePreferredSharedMemoryCarveout, 100);
       if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "carveout attribute: %s", cudaGetErrorString(e));
       e = cudaFuncSetAttribute(combine_kernel_ptr(Ds[k]), cudaFuncAttributePreferredSharedMemoryCarveout, 100);
@@ -182,15 +180,17 @@ static Grids grids_for(const DevInfo& di, int D) {
   return g;
 }
 
-// The 4-bit store's kernel for the split-K route: the tensor-memory one when the average segment (what the
-// host knows of them) has more than 8 packed rows, which is what the other one converts a key for at a
-// time.  16 segments of 64 rows over 4112 keys, D = 128: XXt us against XXn; ...
+// The 4-bit store's kernel for the split-K route: the tensor-memory one (q4_tile.cu), which converts a key
+// once for up to 128 packed rows, when the average segment (what the host knows of them) has more than
+// 16; the other one, which converts a key again for every 8, otherwise.  64 segments over 6144 keys on
+// average, 8 KV heads, D = 128, tensor-memory / other: 16 rows 221 / 166 us, 24 rows 221 / 303 us; 16 segments
+// of 64 rows over 3100 keys 45 / 100 us.  At D = 256 the output of 128 rows leaves no room for the first.
 static bool q4_tiles(int64_t T, int Hq, int Hkv, int D, int S) {
-  return D <= 128 && T * (Hq / Hkv) > 8 * (int64_t)S;
+  return D <= 128 && T * (Hq / Hkv) > 16 * (int64_t)S;
 }
 static Grids q4_grids_for(const DevInfo& di, int D, bool tiles) {
   Grids g = grids_for(di, D);
-  g.splitk = tiles ? di.sms : (int64_t)di.sms * di.q4_per_sm[0][d_index(D)];
+  g.splitk = tiles ? di.sms : (int64_t)di.sms * di.q4_per_sm[d_index(D)];
   return g;
 }
 
@@ -348,8 +348,7 @@ static sdpa_status launch_all(const SchedArgs& sa, const AttnArgs& aa, int D, co
     if (aa.sk_rows == kQ4TileRows)
       e = launch_k(q4_tile_kernel_ptr(D), (unsigned)g.splitk, kQ4TileThreads, args, q4_tile_smem_bytes(D), st, true);
     else
-      e = launch_k(q4_splitk_kernel_ptr(D, false), (unsigned)g.splitk, kQ4Threads, args, q4_splitk_smem_bytes(D, false),
-                   st, true);
+      e = launch_k(q4_splitk_kernel_ptr(D), (unsigned)g.splitk, kQ4Threads, args, q4_splitk_smem_bytes(D), st, true);
     if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "4-bit split-K launch: %s", cudaGetErrorString(e));
   } else if (e == cudaSuccess) {
     void* args[] = {(void*)&aa};

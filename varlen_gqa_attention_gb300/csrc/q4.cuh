@@ -150,7 +150,7 @@ constexpr int kQ4TileKeys = 128;
 constexpr int kQ4TileThreads = 448;
 const void* q4_tile_kernel_ptr(int D);
 int q4_tile_smem_bytes(int D);
-const void* q4_splitk_kernel_ptr(int D, bool wide);
-int q4_splitk_smem_bytes(int D, bool wide);
+const void* q4_splitk_kernel_ptr(int D);
+int q4_splitk_smem_bytes(int D);
 
 }  // namespace sdpa

@@ -20,8 +20,8 @@
 //   * the products are taken transposed, S^T = K Q^T and O^T = V^T P^T: keys and dims fill the
 //     16 rows of an m16n8k16 product and the query rows its 8 columns, so that a decode unit of up
 //     to 8 rows (one token's heads) wastes no half of each product, score and output register.
-//     (With the query rows as the 16 rows the 64-sequence, 32768-key decode took 675 us against
-//     XXX.)  P^T is the transpose of what S^T leaves in the lanes: one movmatrix per 8 x 8 block.
+//     (With the query rows as the 16 rows a decode of 64 sequences over 24576 keys on average, 8 KV heads,
+//     D = 128, took 675 us, and 466 so; 332 us, 5.2 TB/s of codes and scales, with what follows.)  P^T is the transpose of what S^T leaves in the lanes: one movmatrix per 8 x 8 block.
 // P is rounded to fp16 (half a step is at most 2^-11 of it, against 2^-8 in bf16) and V is exact in
 // fp16; Q and K are multiplied in bf16, where both are exact.  Sums are fp32.  The lazily updated
 // maximum leaves P at most 2^8 above it, so P is kept 2^7 times larger, its sum too: at most 2^15,
@@ -36,17 +36,15 @@ namespace sdpa {
 
 constexpr int kQ4Consumers = 128; // threads of the four attention warps
 
-// Two builds of the kernel: the narrow one takes 8 query rows a warp (one token's heads) and the wide
-// one 16, whose output takes twice the registers; each takes units of any size, the narrow one
-// repeating the conversion for every 8 rows.  At D = 256 the output of 16 rows would be 128
-// registers, and there is only the narrow one.
-template <int D, bool WIDE>
+// A unit of more than 8 rows is converted again for every 8 of them.  (16 rows a warp, twice the registers
+// of output, made a CTA of 168 registers and units of 8 rows slower by a tenth; segments of more than 16
+// rows have a kernel of their own, q4_tile.cu.)
+template <int D>
 struct Q4Cfg {
-  static constexpr int kRows = WIDE ? 16 : 8;   // query rows of a warp
-  static constexpr int kRun = WIDE ? 1 : D == 256 ? 2 : 4;  // 16-key blocks between two looks at the maximum
-  static constexpr int kKeys = WIDE ? 128 : 64 * kRun;  // keys per stage of the ring
-  static constexpr int kStages = WIDE ? 3 : D == 64 ? 3 : 2;
-  static constexpr int kPerSm = !WIDE && D == 64 ? 3 : 2;  // CTAs per SM that registers and shared memory allow
+  static constexpr int kRun = D == 256 ? 2 : 4;  // 16-key blocks between two looks at the maximum
+  static constexpr int kKeys = 64 * kRun;        // keys per stage of the ring
+  static constexpr int kStages = D == 64 ? 3 : 2;
+  static constexpr int kPerSm = D == 64 ? 3 : 2;  // CTAs per SM that registers and shared memory allow
   static constexpr int kRowBytes = D / 2;
   static constexpr int kScaleBytes = D / kQ4Group;
   static constexpr int kCodes = kKeys * kRowBytes;
@@ -54,7 +52,7 @@ struct Q4Cfg {
   static constexpr int kStageBytes = 2 * (kCodes + kScales);
   static constexpr int kQPitch = D * 2 + 16;
   static constexpr int kQBytes = kSplitkRows * kQPitch;
-  static constexpr int kMergeBytes = 4 * 16 * 36 * 4;
+  static constexpr int kMergeBytes = 4 * 8 * 68 * 4;  // 64 dims of the warps' rows
   static constexpr int kBytes = kStages * kStageBytes + kQBytes + kMergeBytes;
 };
 
@@ -103,18 +101,15 @@ __device__ __forceinline__ void lds_words(const char* p, uint32_t (&w)[N]) {
   }
 }
 
-// The four attention warps on one piece.  4 / NCS groups of 8 NR query rows; the NCS warps of a group
-// share a stage's keys.
+// The four attention warps on one piece.  4 / NCS groups of 8 query rows; the NCS warps of a group share a
+// stage's keys.
 template <int D, typename S>
 __device__ __forceinline__ void q4_unit(const AttnArgs& A, const Q4Piece& pc, int NCS, const char* ring, char* sQ,
                                         float* merge, uint32_t full, uint32_t empty, uint32_t qempty, uint32_t& it,
                                         volatile int* abort, float2* s_ml, int32_t** s_count) {
-  constexpr int NR = S::kRows / 8;
   constexpr int WK = D / 32;  // words of a lane's K chunk (D / 4 dims)
   constexpr int WV = D / 64;  // words of a lane's V chunk (D / 8 dims)
   constexpr int ND = D / 16;  // m16 blocks of the output
-  constexpr int GR = 8 * NR;  // query rows of a group
-  constexpr bool kQRegs = NR == 1;  // query fragments stay in registers
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int grp = warp / NCS, cs = warp % NCS;
@@ -125,61 +120,42 @@ __device__ __forceinline__ void q4_unit(const AttnArgs& A, const Q4Piece& pc, in
   const int64_t pos_lo = pc.pos_lo;
   const int nkeys = (int)(pc.pos_hi - pos_lo);
 
-  // this lane's query rows, 2 tq and 2 tq + 1 of every 8: the keys each sees, as offsets from
-  // pos_lo: [first, first + count)
-  int first[NR][2];
-  uint32_t count[NR][2];
+  // this lane's query rows, 2 tq and 2 tq + 1 of the group's 8: the keys each sees, as offsets from pos_lo:
+  // [first, first + count)
+  int first[2];
+  uint32_t count[2];
   int lo_max = 0, hi_min = INT32_MAX;
 #pragma unroll
-  for (int r = 0; r < NR; ++r) {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int rl = grp * GR + r * 8 + 2 * tq + c;
-      first[r][c] = 0;
-      count[r][c] = INT32_MAX;  // rows past the unit's: never stored, whatever they come to
-      if (rl < R) {
-        const RowWin w = row_window((int)((r0 + rl) / A.group), ur.q_len, ur.kv_end, ur.causal, ur.window);
-        const int a = (int)min(max((int64_t)w.lo - pos_lo, (int64_t)0), (int64_t)nkeys);
-        const int b = (int)min(max((int64_t)w.hi - pos_lo, (int64_t)a), (int64_t)nkeys);
-        first[r][c] = a;
-        count[r][c] = b - a;
-        lo_max = max(lo_max, a);
-        hi_min = min(hi_min, b);
-      }
+  for (int c = 0; c < 2; ++c) {
+    const int rl = grp * 8 + 2 * tq + c;
+    first[c] = 0;
+    count[c] = INT32_MAX;  // rows past the unit's: never stored, whatever they come to
+    if (rl < R) {
+      const RowWin w = row_window((int)((r0 + rl) / A.group), ur.q_len, ur.kv_end, ur.causal, ur.window);
+      const int a = (int)min(max((int64_t)w.lo - pos_lo, (int64_t)0), (int64_t)nkeys);
+      const int b = (int)min(max((int64_t)w.hi - pos_lo, (int64_t)a), (int64_t)nkeys);
+      first[c] = a;
+      count[c] = b - a;
+      lo_max = max(lo_max, a);
+      hi_min = min(hi_min, b);
     }
   }
   // keys that every row of the warp sees
   lo_max = __reduce_max_sync(0xffffffffu, lo_max);
   hi_min = __reduce_min_sync(0xffffffffu, hi_min);
 
-  const char* qrow = sQ + (grp * GR + gq) * S::kQPitch + tq * (D / 2);
-  uint4 qf[kQRegs ? WK : 1];
-  if constexpr (kQRegs) {
+  // the query row of this lane as operand fragments
+  uint4 qf[WK];
+  const char* qrow = sQ + (grp * 8 + gq) * S::kQPitch + tq * (D / 2);
 #pragma unroll
-    for (int w = 0; w < WK; ++w) qf[w] = q4_q_order(*reinterpret_cast<const uint4*>(qrow + 16 * w));
-    __syncwarp();
-    if (lane == 0) mbar_arrive(qempty);
-  } else {
-    // reordered in place once, read again for every run of keys
-    for (int idx = tid; idx < R * (D / 8); idx += kQ4Consumers) {
-      uint4* p = reinterpret_cast<uint4*>(sQ + (idx / (D / 8)) * S::kQPitch + (idx % (D / 8)) * 16);
-      *p = q4_q_order(*p);
-    }
-    bar_sync_n(1, kQ4Consumers);
-  }
+  for (int w = 0; w < WK; ++w) qf[w] = q4_q_order(*reinterpret_cast<const uint4*>(qrow + 16 * w));
+  __syncwarp();
+  if (lane == 0) mbar_arrive(qempty);
 
-  float o[ND][NR][4];
+  float o[ND][4];
 #pragma unroll
-  for (int nd = 0; nd < ND; ++nd)
-#pragma unroll
-    for (int r = 0; r < NR; ++r) o[nd][r][0] = o[nd][r][1] = o[nd][r][2] = o[nd][r][3] = 0.f;
-  float m[NR][2], l[NR][2], nmu[NR][2];  // nmu: what is added to a score before exp2
-#pragma unroll
-  for (int r = 0; r < NR; ++r) {
-    m[r][0] = m[r][1] = -INFINITY;
-    l[r][0] = l[r][1] = 0.f;
-    nmu[r][0] = nmu[r][1] = 0.f;
-  }
+  for (int nd = 0; nd < ND; ++nd) o[nd][0] = o[nd][1] = o[nd][2] = o[nd][3] = 0.f;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, nmu[2] = {0.f, 0.f};  // nmu: added before exp2
   const float sl2 = A.scale_log2;
   const uint32_t kbits = in_register(kQ4Bf16), vbits = in_register(kQ4F16);
   // Row n of 8 keys stands for key n, with the two of every other pair swapped: the four lanes of a
@@ -200,11 +176,10 @@ __device__ __forceinline__ void q4_unit(const AttnArgs& A, const Q4Piece& pc, in
     auto keys = [&](auto kt_const, int k0) {
       constexpr int KT = decltype(kt_const)::value;
       // S^T = K Q^T
-      float s[KT][NR][4];
+      float s[KT][4];
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
-#pragma unroll
-        for (int r = 0; r < NR; ++r) s[kt][r][0] = s[kt][r][1] = s[kt][r][2] = s[kt][r][3] = 0.f;
+        s[kt][0] = s[kt][1] = s[kt][2] = s[kt][3] = 0.f;
         const int key = k0 + kt * 16 + kn;
         uint32_t kw[2][WK];  // keys key and key + 8
         __nv_bfloat162 s2[2], z2[2];
@@ -230,15 +205,7 @@ __device__ __forceinline__ void q4_unit(const AttnArgs& A, const Q4Piece& pc, in
               a[2 * i] = q4_pair_bf16(kw[0][w] >> (8 * x + 4 * i), kbits, s2[0], z2[0]);
               a[2 * i + 1] = q4_pair_bf16(kw[1][w] >> (8 * x + 4 * i), kbits, s2[1], z2[1]);
             }
-#pragma unroll
-            for (int r = 0; r < NR; ++r) {
-              uint2 b;
-              if constexpr (kQRegs)
-                b = x ? make_uint2(qf[w].z, qf[w].w) : make_uint2(qf[w].x, qf[w].y);
-              else
-                b = *reinterpret_cast<const uint2*>(qrow + r * 8 * S::kQPitch + 16 * w + 8 * x);
-              mma_bf16_16816(s[kt][r], a, b.x, b.y);
-            }
+            mma_bf16_16816(s[kt], a, x ? qf[w].z : qf[w].x, x ? qf[w].w : qf[w].y);
           }
         }
       }
@@ -250,71 +217,57 @@ __device__ __forceinline__ void q4_unit(const AttnArgs& A, const Q4Piece& pc, in
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-          for (int r = 0; r < NR; ++r)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t j = off + kt * 16 + 8 * (e >> 1) + kn - first[r][e & 1];
-              if (j >= count[r][e & 1]) s[kt][r][e] = -INFINITY;
-            }
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t j = off + kt * 16 + 8 * (e >> 1) + kn - first[e & 1];
+            if (j >= count[e & 1]) s[kt][e] = -INFINITY;
+          }
       }
       // (the lanes compare their own scores with the maximum; only when one is beyond it are the
       // rows' maxima taken across the lanes)
-      float mx[NR][2];
+      float mx[2];
       bool up = false;
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
+      for (int c = 0; c < 2; ++c) {
+        float x = fmaxf(s[0][c], s[0][c + 2]);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float x = fmaxf(s[0][r][c], s[0][r][c + 2]);
-#pragma unroll
-          for (int kt = 1; kt < KT; ++kt) x = fmaxf(x, fmaxf(s[kt][r][c], s[kt][r][c + 2]));
-          mx[r][c] = x;
-          up |= x * sl2 > m[r][c] + 8.f;  // false while nothing is visible
-        }
+        for (int kt = 1; kt < KT; ++kt) x = fmaxf(x, fmaxf(s[kt][c], s[kt][c + 2]));
+        mx[c] = x;
+        up |= x * sl2 > m[c] + 8.f;  // false while nothing is visible
       }
       if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
+        for (int c = 0; c < 2; ++c) {
+          float x = mx[c];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float x = mx[r][c];
+          for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+          const float mn = fmaxf(m[c], x * sl2);
+          float alpha = 1.f;
+          if (mn > m[c] + 8.f) {
+            alpha = exp2_approx(m[c] - mn);
+            m[c] = mn;
+            nmu[c] = kQ4PLift - mn;
+          }
+          l[c] *= alpha;
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-            const float mn = fmaxf(m[r][c], x * sl2);
-            float alpha = 1.f;
-            if (mn > m[r][c] + 8.f) {
-              alpha = exp2_approx(m[r][c] - mn);
-              m[r][c] = mn;
-              nmu[r][c] = kQ4PLift - mn;
-            }
-            l[r][c] *= alpha;
-#pragma unroll
-            for (int nd = 0; nd < ND; ++nd) {
-              o[nd][r][c] *= alpha;
-              o[nd][r][c + 2] *= alpha;
-            }
+          for (int nd = 0; nd < ND; ++nd) {
+            o[nd][c] *= alpha;
+            o[nd][c + 2] *= alpha;
           }
         }
       }
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-        for (int r = 0; r < NR; ++r)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s[kt][r][e] = exp2_approx(fmaf(s[kt][r][e], sl2, nmu[r][e & 1]));
-            l[r][e & 1] += s[kt][r][e];
-          }
+        for (int e = 0; e < 4; ++e) {
+          s[kt][e] = exp2_approx(fmaf(s[kt][e], sl2, nmu[e & 1]));
+          l[e & 1] += s[kt][e];
+        }
 
       // O^T += V^T P^T, 16 keys at a time
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
-        uint32_t b[NR][2];
-#pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          b[r][0] = transpose_8x8(pack_f16x2(s[kt][r][0], s[kt][r][1]));
-          b[r][1] = transpose_8x8(pack_f16x2(s[kt][r][2], s[kt][r][3]));
-        }
+        const uint32_t b0 = transpose_8x8(pack_f16x2(s[kt][0], s[kt][1]));
+        const uint32_t b1 = transpose_8x8(pack_f16x2(s[kt][2], s[kt][3]));
         uint32_t vw[4][WV];  // keys ko, ko ^ 1 of the first 8, then of the second
         uint32_t sb[4];
 #pragma unroll
@@ -339,8 +292,7 @@ __device__ __forceinline__ void q4_unit(const AttnArgs& A, const Q4Piece& pc, in
               a[1] = q4_pair_f16(i == 0 ? x0 << 2 : x0 >> 6, vbits, s2[0], z2[0]);
               a[2] = q4_pair_f16(i == 0 ? x1 << 6 : x1 >> 2, vbits, s2[1], z2[1]);
               a[3] = q4_pair_f16(i == 0 ? x1 << 2 : x1 >> 6, vbits, s2[1], z2[1]);
-#pragma unroll
-              for (int r = 0; r < NR; ++r) mma_f16_16816(o[4 * w + 2 * hf + i / 2][r], a, b[r][0], b[r][1]);
+              mma_f16_16816(o[4 * w + 2 * hf + i / 2], a, b0, b1);
             }
           }
         }
@@ -358,43 +310,30 @@ __device__ __forceinline__ void q4_unit(const AttnArgs& A, const Q4Piece& pc, in
     __syncwarp();
     if (lane == 0) mbar_arrive(empty + 8 * st);
   }
-  if constexpr (!kQRegs) {
-    fence_proxy_async_smem();  // the rows were written here, and a bulk copy writes them next
-    __syncwarp();
-    if (lane == 0) mbar_arrive(qempty);
-  }
 
   // row sums over the lanes that share a row
 #pragma unroll
-  for (int r = 0; r < NR; ++r) {
+  for (int c = 0; c < 2; ++c) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-#pragma unroll
-      for (int d = 4; d < 32; d <<= 1) l[r][c] += __shfl_xor_sync(0xffffffffu, l[r][c], d);
-      // a row whose scores are NaN has no maximum: it is joined as one, and comes out NaN
-      if (l[r][c] != l[r][c]) m[r][c] = 0.f;
-      if (gq == 0) s_ml[warp * GR + r * 8 + 2 * tq + c] = make_float2(m[r][c], l[r][c]);
-    }
+    for (int d = 4; d < 32; d <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], d);
+    // a row whose scores are NaN has no maximum: it is joined as one, and comes out NaN
+    if (l[c] != l[c]) m[c] = 0.f;
+    if (gq == 0) s_ml[warp * 8 + 2 * tq + c] = make_float2(m[c], l[c]);
   }
 
   // The warps' runs are joined through shared memory.  A lane has the D / 8 dims [gq D / 8, ...) of its
-  // rows; a pass takes XP of them.
-  constexpr int XP = NR == 1 ? 8 : 4;
-  constexpr int kPitch = 8 * XP + 4;
+  // rows; a pass takes 8 of them.
+  constexpr int kPitch = 68;  // floats: 64 dims, and a step that spreads banks
   const bool direct = ur.nslots == 1;
 #pragma unroll
-  for (int p = 0; p < D / (8 * XP); ++p) {
+  for (int p = 0; p < D / 64; ++p) {
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
+    for (int c = 0; c < 2; ++c) {
+      float* dst = merge + (warp * 8 + 2 * tq + c) * kPitch + gq * 8;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float* dst = merge + (warp * GR + r * 8 + 2 * tq + c) * kPitch + gq * XP;
-#pragma unroll
-        for (int x = 0; x < XP; x += 4) {
-          const int nd = (p * XP + x) / 2;
-          *reinterpret_cast<float4*>(dst + x) =
-              make_float4(o[nd][r][c], o[nd][r][2 + c], o[nd + 1][r][c], o[nd + 1][r][2 + c]);
-        }
+      for (int x = 0; x < 8; x += 4) {
+        const int nd = (p * 8 + x) / 2;
+        *reinterpret_cast<float4*>(dst + x) = make_float4(o[nd][c], o[nd][2 + c], o[nd + 1][c], o[nd + 1][2 + c]);
       }
     }
     bar_sync_n(1, kQ4Consumers);
@@ -406,43 +345,41 @@ __device__ __forceinline__ void q4_unit(const AttnArgs& A, const Q4Piece& pc, in
     }
     for (int idx = tid; idx < R * 8; idx += kQ4Consumers) {
       const int rl = idx >> 3, n = idx & 7;
-      const int w0 = rl / GR * NCS, rin = rl % GR;
+      const int w0 = rl / 8 * NCS, rin = rl % 8;
       float M = -INFINITY;
 #pragma unroll 1
-      for (int c = 0; c < NCS; ++c) M = fmaxf(M, s_ml[(w0 + c) * GR + rin].x);
+      for (int c = 0; c < NCS; ++c) M = fmaxf(M, s_ml[(w0 + c) * 8 + rin].x);
       const float Mu = M == -INFINITY ? 0.f : M;
-      float L = 0.f, acc[XP];
+      float L = 0.f, acc[8];
 #pragma unroll
-      for (int k = 0; k < XP; ++k) acc[k] = 0.f;
+      for (int k = 0; k < 8; ++k) acc[k] = 0.f;
 #pragma unroll 1
       for (int c = 0; c < NCS; ++c) {
-        const int w = (w0 + c) * GR + rin;
+        const int w = (w0 + c) * 8 + rin;
         const float2 ml = s_ml[w];
         const float f = exp2_approx(ml.x - Mu);
         L += ml.y * f;
 #pragma unroll
-        for (int x = 0; x < XP; x += 4) {
-          const float4 u = *reinterpret_cast<const float4*>(merge + w * kPitch + n * XP + x);
+        for (int x = 0; x < 8; x += 4) {
+          const float4 u = *reinterpret_cast<const float4*>(merge + w * kPitch + n * 8 + x);
           acc[x] += u.x * f; acc[x + 1] += u.y * f; acc[x + 2] += u.z * f; acc[x + 3] += u.w * f;
         }
       }
-      const int d0 = n * (D / 8) + XP * p;
+      const int d0 = n * (D / 8) + 8 * p;
       if (direct) {
         const float inv = L > 0.f ? 1.f / L : 0.f;
         const int64_t r = r0 + rl;
         const int64_t i = r / A.group;
         const int h = ur.hk * A.group + (int)(r % A.group);
-        __nv_bfloat16* dst = A.out + (ur.q_start + i) * A.o_rs + (int64_t)h * A.o_hs + d0;
-#pragma unroll
-        for (int x = 0; x < XP; x += 4)
-          *reinterpret_cast<uint2*>(dst + x) = make_uint2(pack_bf16x2(acc[x] * inv, acc[x + 1] * inv),
-                                                          pack_bf16x2(acc[x + 2] * inv, acc[x + 3] * inv));
+        *reinterpret_cast<uint4*>(A.out + (ur.q_start + i) * A.o_rs + (int64_t)h * A.o_hs + d0) =
+            make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
+                       pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
       } else {
         const int64_t pi = ur.slot_base + (int64_t)pc.slot * R + rl;
         if (p == 0 && n == 0) A.ws.part_ml[kRouteSplitk][pi] = make_float2(M, L);
         float* dst = A.ws.part_o[kRouteSplitk] + pi * D + d0;
 #pragma unroll
-        for (int x = 0; x < XP; x += 4)
+        for (int x = 0; x < 8; x += 4)
           *reinterpret_cast<float4*>(dst + x) = make_float4(acc[x], acc[x + 1], acc[x + 2], acc[x + 3]);
       }
     }
@@ -465,8 +402,8 @@ __device__ __forceinline__ void q4_load(const Q4AttnArgs& G, char* ring, char* s
   uint32_t it = 0, n = 0;
   for (;; ++n) {
     const bool more = walk_next(wk, ur, ta, tb);
-    // (the rows' buffer is free once every warp has read them, or is past them; the record of the
-    // piece before that is then no longer in use)
+    // (the rows' buffer is free once every warp has read them; the record of the piece before that is then no
+    // longer in use)
     if (n > 0 && !q4_wait(qempty, (n - 1) & 1, abort)) break;
     const int64_t pos_lo = (int64_t)ur.lo + ta * kSplitkTile;
     const int64_t pos_hi = min((int64_t)ur.lo + tb * kSplitkTile, (int64_t)ur.hi);
@@ -530,13 +467,13 @@ __device__ __forceinline__ void q4_load(const Q4AttnArgs& G, char* ring, char* s
   if (n > 0) mbar_wait(qfull, (n - 1) & 1, &none);
 }
 
-template <int D, bool WIDE>
-__global__ void __launch_bounds__(kQ4Threads, Q4Cfg<D, WIDE>::kPerSm) sdpa_q4_splitk_kernel(Q4AttnArgs G) {
-  using S = Q4Cfg<D, WIDE>;
+template <int D>
+__global__ void __launch_bounds__(kQ4Threads, Q4Cfg<D>::kPerSm) sdpa_q4_splitk_kernel(Q4AttnArgs G) {
+  using S = Q4Cfg<D>;
   extern __shared__ __align__(128) char smem[];
   __shared__ __align__(8) uint64_t bars[2 * S::kStages + 2];
   __shared__ __align__(16) Q4Piece pieces[2];
-  __shared__ float2 s_ml[4 * 16];
+  __shared__ float2 s_ml[4 * 8];
   __shared__ int32_t* s_count[2];
   __shared__ int s_abort;
   const AttnArgs& A = G.a;
@@ -573,7 +510,7 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Cfg<D, WIDE>::kPerSm) sdpa_q4_sp
       if (!pc.valid) break;
       if (threadIdx.x == 0) s_count[1] = pc.ur.nslots > 1 ? A.ws.unit_done + pc.unit : nullptr;
       // warps that share the keys of a group of rows: 4, 2 or 1
-      const int groups = (pc.ur.rows + S::kRows - 1) / S::kRows;
+      const int groups = (pc.ur.rows + 7) / 8;
       q4_unit<D, S>(A, pc, groups == 1 ? 4 : groups == 2 ? 2 : 1, ring, sQ, merge, full, empty, qempty, it, &s_abort,
                     s_ml, s_count);
       // (the unit ended on a barrier of the four warps)
@@ -588,27 +525,23 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Cfg<D, WIDE>::kPerSm) sdpa_q4_sp
   }
 }
 
-template __global__ void sdpa_q4_splitk_kernel<64, false>(Q4AttnArgs);
-template __global__ void sdpa_q4_splitk_kernel<64, true>(Q4AttnArgs);
-template __global__ void sdpa_q4_splitk_kernel<128, false>(Q4AttnArgs);
-template __global__ void sdpa_q4_splitk_kernel<128, true>(Q4AttnArgs);
-template __global__ void sdpa_q4_splitk_kernel<256, false>(Q4AttnArgs);
+template __global__ void sdpa_q4_splitk_kernel<64>(Q4AttnArgs);
+template __global__ void sdpa_q4_splitk_kernel<128>(Q4AttnArgs);
+template __global__ void sdpa_q4_splitk_kernel<256>(Q4AttnArgs);
 
-int q4_splitk_smem_bytes(int D, bool wide) {
+int q4_splitk_smem_bytes(int D) {
   switch (D) {
-    case 64: return wide ? Q4Cfg<64, true>::kBytes : Q4Cfg<64, false>::kBytes;
-    case 128: return wide ? Q4Cfg<128, true>::kBytes : Q4Cfg<128, false>::kBytes;
-    default: return Q4Cfg<256, false>::kBytes;
+    case 64: return Q4Cfg<64>::kBytes;
+    case 128: return Q4Cfg<128>::kBytes;
+    default: return Q4Cfg<256>::kBytes;
   }
 }
 
-const void* q4_splitk_kernel_ptr(int D, bool wide) {
+const void* q4_splitk_kernel_ptr(int D) {
   switch (D) {
-    case 64:
-      return wide ? (const void*)sdpa_q4_splitk_kernel<64, true> : (const void*)sdpa_q4_splitk_kernel<64, false>;
-    case 128:
-      return wide ? (const void*)sdpa_q4_splitk_kernel<128, true> : (const void*)sdpa_q4_splitk_kernel<128, false>;
-    default: return (const void*)sdpa_q4_splitk_kernel<256, false>;
+    case 64: return (const void*)sdpa_q4_splitk_kernel<64>;
+    case 128: return (const void*)sdpa_q4_splitk_kernel<128>;
+    default: return (const void*)sdpa_q4_splitk_kernel<256>;
   }
 }
 

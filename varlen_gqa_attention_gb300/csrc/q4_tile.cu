@@ -22,7 +22,9 @@
 // Bound by the issue slots and by each role's own latency: a tile at D = 128 is about 1.8 thousand warp
 // instructions of conversion and 0.9 thousand for each 32 rows of softmax.  With one warp a row quarter
 // for all 128 keys (half the softmax warps, twice the converting ones) a tile of 64 rows took 3.7 thousand
-// cycles, waiting for its two softmax warps: 16 segments of 64 rows over 4112 keys 55 us, and XX us so.
+// cycles, waiting for its two softmax warps: 16 segments of 64 rows over 3100 keys 55 us, and 45 us so.  (K a
+// tile ahead of V, and the converting warps off the partitions that the softmax of few rows has to run on,
+// came to the same.)
 #include "q4.cuh"
 #include "tc.cuh"
 
