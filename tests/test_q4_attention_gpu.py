@@ -369,3 +369,150 @@ def test_a_long_chunk_beside_single_tokens(dev):
     check(got, st, q, store, seq, True, p_step=2.0 ** -8, rows_subset=rows)
     got, st = run_q4(q, store, seq, dev, causal=True, window=100)
     check(got, st, q, store, seq, True, 100, p_step=2.0 ** -8, rows_subset=rows)
+
+
+# ----------------------------------------- both split-K kernels over their whole range of segments
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv,lens", [
+    (8, 2, [(32, 6000)]),                        # one unit of 128 rows, its keys cut over many CTAs
+    (8, 1, [(17, 5003), (16, 4096), (1, 6143)]),  # 136, 128 and 8 packed rows: a block of 8 rows, a full one
+    (128, 1, [(1, 4500), (2, 130), (3, 129)]),   # a token's heads fill a unit
+    (8, 8, [(129, 3000), (128, 2999), (5, 5)]),  # no shared heads, rows that no block divides
+    (24, 2, [(40, 2111), (11, 64), (10, 63)]),   # 12 rows a token: tokens end inside a unit
+])
+def test_tile_kernel_pieces(dev, D, Hq, Hkv, lens):
+    seq, t = [], 1
+    for i, (n, kv) in enumerate(lens):
+        seq.append([t, n, i, kv])
+        t += n + i
+    rows = -(-max(kv for _, kv in lens) // 16) * 16
+    store, q = random_store(rows, len(lens), Hkv, D, D + Hq), queries(t + 1, Hq, D, 40)
+    subset = sorted({0, t} | {r for s in seq for r in (s[0], s[0] + 1, s[0] + s[1] // 2, s[0] + s[1] - 1, s[0] + s[1])
+                              if r <= t})
+    for causal, window in ((True, 0), (False, 0), (True, 700)):
+        got, st = run_q4(q, store, seq, dev, causal=causal, window=window)
+        check(got, st, q, store, seq, causal, window, rows_subset=subset, tag=f"{causal} {window}")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("blocks", [[12, 9, 1, 1, 1, 1, 1, 1], [70, 3, 2, 1, 1, 1, 1, 1], [40, 40]])
+def test_few_rows_on_average_with_longer_blocks_among_them(dev, D, blocks):
+    # 8 x 2 packed rows a token: blocks of 17 to 32 rows and several units of 32 in the split-K kernel
+    seq, t = [], 0
+    for i, n in enumerate(blocks):
+        seq.append([t, n, i, 900 + 37 * i])
+        t += n
+    pad = len(blocks)
+    seq += [[t, 0, 0, 1]] * max(0, t * 2 - 16 * pad)  # (empty segments count towards the average)
+    store, q = random_store(1200, 8, 2, D, D), queries(t, 4, D, 41)
+    got, st = run_q4(q, store, seq, dev, causal=True)
+    check(got, st, q, store, seq, True)
+
+
+def test_many_segments_of_several_rows(dev):
+    # more segments than the small scheduler takes, on the tensor-memory kernel: several units a CTA
+    seq = [[6 * i, 5 + i % 2, (3 * i) % 44, 130 + 9 * (i % 50)] for i in range(88)]
+    store, q = random_store(608, 44, 4, 128, 42), queries(6 * 88, 16, 128, 42)
+    assert 6 * 88 * 4 > 16 * 88
+    for modes in (None, [[i % 2, [0, 1, 64, 200][i % 4]] for i in range(88)]):
+        got, st = run_q4(q, store, seq, dev, causal=True, seg_mode=modes)
+        check(got, st, q, store, seq, True, 0, modes)
+
+
+def test_a_scale_of_zero_is_the_mean_of_the_visible_values(dev):
+    store = random_store(512, 2, 2, 128, 43)
+    for seq in ([[0, 1, 0, 500], [1, 1, 1, 3]], [[0, 30, 0, 500], [30, 30, 1, 31]]):
+        T = seq[-1][0] + seq[-1][1]
+        q = queries(T, 8, 128, 43)
+        got, st = run_q4(q, store, seq, dev, causal=True, scale=0.0)
+        check(got, st, q, store, seq, True, scale=0.0)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_tile_kernel_keeps_a_row_of_nan_or_infinity_alone(dev, D):
+    seq = [[0, 24, 0, 3000], [24, 24, 1, 90]]
+    q, store = queries(48, 8, D, 44), random_store(3008, 2, 1, D, 44)
+    clean, _ = run_q4(q, store, seq, dev, causal=True)
+    for t, h, d, x in ((2, 1, 5, "nan"), (17, 7, 63, "inf"), (30, 3, 0, "nan"), (47, 0, 1, "-inf")):
+        q[t, h, d] = float(x)
+    got, _ = run_q4(q, store, seq, dev, causal=True)
+    for t, h in ((2, 1), (17, 7), (30, 3), (47, 0)):
+        assert bool(got[t, h].isnan().any()), (t, h)
+        got[t, h] = clean[t, h]
+    assert torch.equal(got.view(torch.int16), clean.view(torch.int16))
+
+
+def test_the_same_call_gives_the_same_bits(dev):
+    store = random_store(4096, 6, 2, 128, 45)
+    for seq, Hq in (([[i, 1, i, 4000 - i] for i in range(6)], 16), ([[40 * i, 40, i, 4000 - i] for i in range(6)], 8)):
+        q = queries(seq[-1][0] + seq[-1][1], Hq, 128, 45)
+        first, _ = run_q4(q, store, seq, dev, causal=True)
+        for _ in range(10):
+            again, _ = run_q4(q, store, seq, dev, causal=True)
+            assert torch.equal(first.view(torch.int16), again.view(torch.int16))
+
+
+def test_one_workspace_for_calls_of_different_sizes(dev):
+    # the workspace of the largest call serves the smaller ones, whichever kernel they take
+    store = random_store(2048, 6, 2, 128, 46)
+    stored = pkg.Q4Store(*(t.to(dev) for t in store))
+    ws = torch.full((pkg.q4_workspace_bytes(240, 16, stored, 6),), 255, dtype=torch.uint8, device=dev)
+    for n in (40, 1, 3, 2, 17):
+        seq = [[n * i, n, i, 2000 - 300 * i] for i in range(6)]
+        q = queries(6 * n, 16, 128, 46)
+        got = pkg.sdpa_varlen_q4(q.to(dev), stored, torch.tensor(seq, dtype=torch.int32, device=dev), causal=True,
+                                 workspace=ws)
+        check(got, 0, q, store, seq, True)
+
+
+def test_two_captured_graphs_of_one_workspace_replayed_in_turn(dev):
+    store = random_store(1024, 4, 2, 128, 47)
+    stored = pkg.Q4Store(*(t.to(dev) for t in store))
+    ws = torch.empty(pkg.q4_workspace_bytes(120, 8, stored, 4), dtype=torch.uint8, device=dev)
+    sides = []
+    for n in (1, 30):
+        seq = [[n * i, n, i, 1000 - 99 * i] for i in range(4)]
+        q = queries(4 * n, 8, 128, 47 + n)
+        qd, seqd = q.to(dev), torch.tensor(seq, dtype=torch.int32, device=dev)
+        out = torch.empty_like(qd)
+        call = lambda qd=qd, seqd=seqd, out=out: pkg.sdpa_varlen_q4(qd, stored, seqd, causal=True, out=out, workspace=ws)
+        call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        sides.append((g, q, seq, out))
+    for _ in range(3):
+        for g, q, seq, out in sides:
+            out.fill_(float("nan"))
+            g.replay()
+            check(out, 0, q, store, seq, True)
+
+
+def test_python_entries_refuse_mixed_devices_and_foreign_streams(dev):
+    store = pkg.q4_store(64, 2, 2, 64, device=dev)
+    q, seq = queries(3, 4, 64, 48).to(dev), torch.tensor([[0, 3, 0, 5]], dtype=torch.int32, device=dev)
+    k = queries(3, 2, 64, 49).to(dev)
+    table = pkg.rope_table(16, 64, device=dev)
+
+    class Foreign:
+        device_index, cuda_stream = 7, 0
+
+    with pytest.raises(ValueError, match="stream is on device 7"):
+        pkg.sdpa_rope(q, table, seq[0, :3].contiguous(), out=torch.empty_like(q), stream=Foreign())
+    for call in (lambda: pkg.sdpa_rope(q, table.cpu(), seq[0, :3].contiguous()),
+                 lambda: pkg.sdpa_rope_append_q4(q, k, k.cpu(), store, seq, table),
+                 lambda: pkg.sdpa_rope_append_q4(q, k, k, store, seq.cpu(), table),
+                 lambda: pkg.sdpa_q4_unpack(store._replace(v_scales=store.v_scales.cpu()), seq, 3),
+                 lambda: pkg.sdpa_varlen_q4(q, store, seq, causal=True, out=torch.empty(3, 4, 64, dtype=q.dtype))):
+        with pytest.raises(ValueError, match="same CUDA device"):
+            call()
+    with pytest.raises(pkg.SdpaError, match="workspace of"):
+        pkg.sdpa_varlen_q4(q, store, seq, causal=True, workspace=torch.empty(1024, dtype=torch.uint8, device=dev))
+    with pytest.raises(pkg.SdpaError, match="16-byte aligned|multiples of 8"):
+        pkg.sdpa_rope(torch.empty(3, 4 * 64 + 2, dtype=q.dtype, device=dev)[:, 2:].unflatten(1, (4, 64)), table,
+                      seq[0, :3].contiguous())
+    small = pkg.Q4Store(*(t[:, :, :24].contiguous() for t in store))
+    with pytest.raises(pkg.SdpaError, match="multiple of 16 rows"):
+        pkg.sdpa_varlen_q4(q, small, seq, causal=True)

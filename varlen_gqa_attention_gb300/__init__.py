@@ -504,10 +504,10 @@ def sdpa_rope(x: torch.Tensor, table: torch.Tensor, positions: torch.Tensor, *,
     if positions is None:
         raise ValueError("positions must be given")
     rot = _rotation(table, positions, sections, interleaved, T)
+    ors, ohs = _strides("out", out, shape) if out is not None else (H * D, D)
     dev = _device_of(x, table, positions, out, status)
     if out is None:
         out = _rows_like(x, shape, stream)
-    ors, ohs = _strides("out", out, shape)
     _call(library().sdpa_rope, dev, stream, x.data_ptr(), T, H, D, rs, hs, rot, 1 if inverse else 0, out.data_ptr(),
           ors, ohs, _status_ptr(status))
     return out
@@ -557,10 +557,10 @@ def _rope_append(entry, q, k_new, v_new, store_tensors, store_args, rows, cols, 
     vrs, vhs = _strides("v_new", v_new, (T, Hkv, D))
     seq_ptr, mode_ptr, S = _table(seq_info, seg_mode)
     rot = _rotation(table, positions, sections, interleaved, T)
+    ors, ohs = _strides("q_out", q_out, shape) if q_out is not None else (Hq * D, D)
     dev = _device_of(q, k_new, v_new, *store_tensors, seq_info, table, positions, seg_mode, q_out, status)
     if q_out is None:
         q_out = _rows_like(q, shape, stream)
-    ors, ohs = _strides("q_out", q_out, shape)
     _call(entry, dev, stream, q.data_ptr(), qrs, qhs, k_new.data_ptr(), krs, khs, v_new.data_ptr(), vrs, vhs, T, Hq,
           Hkv, D, rot, *store_args, rows, cols, seq_ptr, mode_ptr, S, int(window), q_out.data_ptr(), ors, ohs,
           _status_ptr(status))
@@ -612,14 +612,14 @@ def sdpa_q4_unpack(store: Q4Store, seq_info: torch.Tensor, T: int, *, window: in
     rows, cols, Hkv, D, ptrs = _q4(store)
     seq_ptr, mode_ptr, S = _table(seq_info, seg_mode)
     shape = (T, Hkv, D)
+    rs, hs = _strides("k_out", k_out, shape) if k_out is not None else (Hkv * D, D)
+    if (_strides("v_out", v_out, shape) if v_out is not None else (Hkv * D, D)) != (rs, hs):
+        raise ValueError("k_out and v_out must share strides")
     dev = _device_of(*store, seq_info, seg_mode, k_out, v_out, status)
     if k_out is None:
         k_out = _rows_like(seq_info, shape, stream)
     if v_out is None:
         v_out = _rows_like(seq_info, shape, stream)
-    rs, hs = _strides("k_out", k_out, shape)
-    if _strides("v_out", v_out, shape) != (rs, hs):
-        raise ValueError("k_out and v_out must share strides")
     _call(library().sdpa_fourbit_unpack, dev, stream, ptrs, rows, cols, Hkv, D, seq_ptr, mode_ptr, S, int(window), T,
           k_out.data_ptr(), v_out.data_ptr(), rs, hs, _status_ptr(status))
     return k_out, v_out
@@ -645,10 +645,10 @@ def sdpa_varlen_q4(q: torch.Tensor, store: Q4Store, seq_info: torch.Tensor, *, c
     if Ds != D:
         raise ValueError("head dims of q and the store differ")
     seq_ptr, mode_ptr, S = _table(seq_info, seg_mode)
+    ors, ohs = _strides("out", out, shape) if out is not None else (Hq * D, D)
     dev = _device_of(q, *store, seq_info, seg_mode, out, workspace, status)
     if out is None:
         out = _rows_like(q, shape, stream)
-    ors, ohs = _strides("out", out, shape)
     if workspace is None:
         with torch.cuda.stream(stream):
             workspace = torch.empty(max(q4_workspace_bytes(T, Hq, store, S), 256), dtype=_u8, device=q.device)

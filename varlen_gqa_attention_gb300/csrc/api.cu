@@ -5,6 +5,7 @@
 // the device scheduler reads the segment table when the graph replays.
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -186,7 +187,7 @@ static Grids grids_for(const DevInfo& di, int D) {
 // average, 8 KV heads, D = 128, tensor-memory / other: 16 rows 221 / 166 us, 24 rows 221 / 303 us; 16 segments
 // of 64 rows over 3100 keys 45 / 100 us.  At D = 256 the output of 128 rows leaves no room for the first.
 static bool q4_tiles(int64_t T, int Hq, int Hkv, int D, int S) {
-  return D <= 128 && T * (Hq / Hkv) > 16 * (int64_t)S;
+  return D <= 128 && T * (Hq / Hkv) > 16 * (int64_t)std::max(S, 1);
 }
 static Grids q4_grids_for(const DevInfo& di, int D, bool tiles) {
   Grids g = grids_for(di, D);
@@ -457,6 +458,8 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
   aa.causal = sa.causal;
   aa.window = window;
   aa.scale_log2 = scale * 1.4426950408889634f;
+  // (the 4-bit kernels scale after they mask: a scale of 0 must leave -infinity what it is)
+  if (q4) aa.scale_log2 = std::max(aa.scale_log2, FLT_MIN);
   aa.out = (__nv_bfloat16*)out;
   aa.o_rs = o_rs;
   aa.o_hs = o_hs;
@@ -555,21 +558,25 @@ sdpa_status sdpa_varlen_modes(const void* q, int64_t T, int Hq, int D, int64_t q
 }
 
 size_t sdpa_varlen_fourbit_workspace_bytes(int64_t T, int Hq, int Hkv, int D, int S, int64_t rows, int cols) {
-  if (T < 0 || S < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || rows <= 0 || cols <= 0) return 0;
+  if (T < 0 || S < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || rows <= 0 || rows > INT32_MAX || cols <= 0) return 0;
   if (D != 64 && D != 128 && D != 256) return 0;
   DevInfo di;
-  Grids g;
+  // without a device: bounds above any real grid
+  Grids other{4096, 1024}, tile{4096, 1024};
   if (device_info(&di) == SDPA_OK) {
-    g = q4_grids_for(di, D, q4_tiles(T, Hq, Hkv, D, S));
+    other = q4_grids_for(di, D, false);
+    tile = q4_grids_for(di, D, true);
   } else {
-    g.splitk = 4096;  // no device: a bound above any real grid
-    g.prefill = 1024;
     g_err[0] = 0;
   }
-  const int64_t store = align_up(q4_stage_bytes_per_column(rows, Hkv, D) * q4_stage_cols(T, Hq, Hkv, D, S, rows), 256);
-  return layout_workspace(nullptr, T, Hq, Hkv, D, S, g.splitk, g.prefill, nullptr, true,
-                          q4_tiles(T, Hq, Hkv, D, S) ? kQ4TileRows : kSplitkRows) +
-         2 * store;
+  // Calls within the bounds take either kernel, the one that is not q4_tiles with at most 16 packed rows
+  // a segment on average: the larger of the two layouts serves them all.
+  const int64_t few = D <= 128 ? std::min<int64_t>(T, 16 * (int64_t)S / (Hq / Hkv)) : T;
+  size_t need = layout_workspace(nullptr, few, Hq, Hkv, D, S, other.splitk, other.prefill, nullptr);
+  if (q4_tiles(T, Hq, Hkv, D, 1))
+    need = std::max(need, layout_workspace(nullptr, T, Hq, Hkv, D, S, tile.splitk, tile.prefill, nullptr, true,
+                                           kQ4TileRows));
+  return need + 2 * align_up(q4_stage_bytes_per_column(rows, Hkv, D) * q4_stage_cols(T, Hq, Hkv, D, S, rows), 256);
 }
 
 sdpa_status sdpa_varlen_fourbit(const void* q, int64_t T, int Hq, int D, int64_t q_row_stride, int64_t q_head_stride,
