@@ -263,8 +263,8 @@ sdpa_status sdpa_rope_append(const void* q, int64_t q_row_stride, int64_t q_head
  * Nibble c under scale byte b stands for (c - 8) * 2^((b >> 3) - 21) * (1 + (b & 7) / 8): exact in
  * bf16, and finite for every byte pattern.  rows is a multiple of 16 (a ring may have more rows than
  * it needs).  Position j of a column lives in store row j % rows, as in the bf16 store.
- * A group of 32 bf16 values x is stored under the scale nearest to max|x| / 7 (ties to the even
- * byte), with codes 8 + clamp(round(x / scale), -7, 7), halves to even: no value is off by more than
+ * A group of 32 bf16 values x is stored under the scale nearest to max|x| times 1/7 (in fp32; ties to
+ * the even byte), with codes 8 + clamp(round(x / scale), -7, 7), halves to even: no value is off by more than
  * half a step, 0.54 / 7 of its group's largest magnitude at most.  Magnitudes above 13440 saturate;
  * a NaN is stored as 0.
  */

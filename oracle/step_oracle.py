@@ -73,11 +73,12 @@ def q4_unpack(codes, scales) -> np.ndarray:
 
 def q4_pack(x):
     """bf16 [..., D] -> (codes [..., D / 2], scales [..., D / 32]) uint8.  The nearest of the 256
-    scales to max|x| / 7 (the even byte where two are as near), then the nearest code in [-7, 7]."""
+    scales to max|x| times 1/7, a product of 32 bits (the even byte where two are as near), then the nearest
+    code in [-7, 7]."""
     v = f64(x)
     v = np.where(np.isnan(v), 0.0, v)
     g = v.reshape(v.shape[:-1] + (-1, GROUP))
-    want = np.abs(g).max(-1) / 7.0
+    want = (np.abs(g).max(-1).astype(np.float32) * np.float32(1 / 7)).astype(np.float64)
     every = scale_of(np.arange(256))
     off = np.abs(every - np.minimum(want, 1e6)[..., None])
     near = off.min(-1, keepdims=True)

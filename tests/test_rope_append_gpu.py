@@ -189,3 +189,22 @@ def test_queries_in_place(dev):
                                    q_out=qd) is qd
     assert_rotated(qd, qr, q, 128, False)
     assert not bool(qd[5].any())
+
+
+def test_every_largest_magnitude_takes_the_oracles_scale(dev):
+    # all 2^15 - 2^7 bf16 magnitudes, each the largest of a group whose other values are its fractions
+    mag = torch.arange(0x7F80, dtype=torch.int16).view(torch.bfloat16)
+    frac = torch.linspace(-1, 1, 32)
+    x = (mag.float()[:, None] * frac).to(torch.bfloat16)
+    x[:, 5] = mag
+    T = mag.numel() // 2
+    x = x.view(T, 1, 64)
+    rows = -(-T // 16) * 16
+    store = pkg.q4_store(rows, 1, 1, 64, device=dev)
+    xd = x.to(dev)
+    flat = torch.tensor([1.0, 0.0], device=dev).expand(T, 32, 2).contiguous()
+    seq = torch.tensor([[0, T, 0, T]], dtype=torch.int32, device=dev)
+    pkg.sdpa_rope_append_q4(xd, torch.zeros_like(xd), xd, store, seq, flat)
+    c, s = S.q4_pack(x)
+    assert torch.equal(store.v_scales[0, 0, :T].cpu(), torch.from_numpy(s[:, 0]))
+    assert torch.equal(store.v_codes[0, 0, :T].cpu(), torch.from_numpy(c[:, 0]))

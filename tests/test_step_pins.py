@@ -104,12 +104,17 @@ def test_packing_at_borders_and_extremes():
 
 def test_a_tie_between_two_scales_goes_to_the_even_byte():
     x = torch.zeros(1, 32)
-    x[0, 0] = 7 * (1 + 1 / 16)  # amax / 7 halfway between scale 1 (byte 168) and 9/8 (byte 169)
+    x[0, 0] = 7 * (1 + 1 / 16)  # a seventh of it halfway between scale 1 (byte 168) and 9/8 (byte 169)
     _, b = S.q4_pack(x.to(torch.bfloat16))
     assert b[0, 0] == 168
     x[0, 0] = 7 * (1 + 3 / 16)  # between 9/8 (169) and 10/8 (170)
     _, b = S.q4_pack(x.to(torch.bfloat16))
     assert b[0, 0] == 170
+    # 1/7 in 32 bits is 4.2e-8 too large, relatively: beyond half a step of 32 bits above a product of
+    # about 1.43, which then lies above the border
+    x[0, 0] = 7 * (1 + 9 / 16)  # between 12/8 (172) and 13/8 (173)
+    _, b = S.q4_pack(x.to(torch.bfloat16))
+    assert b[0, 0] == 173
 
 
 def test_append_places_rows_as_the_plain_append_does():

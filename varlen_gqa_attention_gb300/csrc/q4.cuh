@@ -27,11 +27,13 @@ constexpr int kQ4RowAlign = 16;  // store rows are a multiple of this, so that 1
 __device__ __forceinline__ float q4_scale(uint32_t b) { return __uint_as_float((b << 20) + (106u << 23)); }
 __device__ __forceinline__ float q4_scale2(uint32_t b) { return __uint_as_float((b << 20) + (107u << 23)); }
 
-// The scale byte of a group whose largest magnitude is amax: the scale nearest to amax / 7 (ties to
-// the even byte), so that |x| / s <= 7 * 17/16 < 7.5 and no code is off by more than half a step.
+// The scale byte of a group whose largest magnitude is amax: the scale nearest to a seventh of it (ties
+// to the even byte), so that |x| / s <= 7 * 17/16 < 7.5 and no code is off by more than half a step.
+// The seventh is the fp32 product with 1 / 7: it decides groups within 2^-23 of a border, and is part
+// of the format's definition.
 // Magnitudes beyond 7 * 1920 take the largest scale and saturate; amax = 0 gives byte 0.
 __device__ __forceinline__ uint32_t q4_scale_byte(float amax) {
-  const uint32_t u = __float_as_uint(__fdiv_rn(amax, 7.f));
+  const uint32_t u = __float_as_uint(__fmul_rn(amax, 1.f / 7.f));
   const int32_t r = (int32_t)((u + 0x7FFFFu + ((u >> 20) & 1u)) >> 20) - (106 << 3);
   return (uint32_t)min(max(r, 0), 255);
 }
