@@ -149,7 +149,7 @@ constexpr int kQ4Threads = 160;  // four warps of attention, one that loads
 // kQ4TileRows packed rows, tiles of kQ4TileKeys keys.
 constexpr int kQ4TileRows = 128;
 constexpr int kQ4TileKeys = 128;
-constexpr int kQ4TileThreads = 448;
+constexpr int kQ4TileThreads = 576;
 const void* q4_tile_kernel_ptr(int D);
 int q4_tile_smem_bytes(int D);
 const void* q4_splitk_kernel_ptr(int D);

@@ -4,27 +4,29 @@
 // The split-K kernel of q4_attn.cu turns every key into operands once for 8 query rows; a block of 16
 // draft rows with 4 heads a KV head is 64, and converting is what that kernel does most.  Here a key is
 // converted once for up to 128 rows: S = Q K^T (128 rows x 128 keys) and O += P V are tcgen05 products, Q,
-// K and V in shared memory, S, P and O in tensor memory.  Per CTA (one per SM), 14 warps:
+// K and V in shared memory, S, P and O in tensor memory.  Per CTA (one per SM), 18 warps:
 //   * a loading warp walks the CTA's pieces (the split-K route's, in units of 128 packed rows and tiles of
 //     128 keys), hands them on, and streams their codes and scales into a ring by bulk copies;
-//   * four converting warps turn a tile's codes into bf16 K and fp16 V tiles (exactly: see q4.cuh),
-//     written in the 128-byte swizzle that the products read, and a piece's query rows likewise;
+//   * eight converting warps, four for every other tile, turn a tile's codes into bf16 K and fp16 V tiles
+//     (exactly: see q4.cuh), written in the 128-byte swizzle that the products read; all eight bring a
+//     piece's query rows there;
 //   * one warp issues the products: S(0) S(1) | PV(0) S(2) | PV(1) S(3) ...  P lies over the scores it came
 //     from, which the next scores of that buffer overwrite behind PV (one thread's products run in order);
-//   * eight softmax warps, a thread a row (= tensor-memory lane), four for a tile's first 64 keys and four
-//     for the others.  The two halves keep a maximum, a sum and an output of their own, as if they were two
-//     CTAs' pieces, and are joined when the piece ends: nothing passes between them in between.  A warp
-//     none of whose rows exist skips its work, so that a unit of 64 rows costs half of one of 128.
+//   * eight softmax warps, four for a tile's first 64 keys and four for the others.  The two halves keep
+//     maxima, sums and an output of their own, as if they were two CTAs' pieces, and are joined when the
+//     piece ends: nothing passes between them in between.  A warp can reach the tensor-memory lanes of one
+//     quarter only, so a unit of up to 64 rows has 16 of them in each quarter (8, when 32 are all), and the
+//     four threads of a quad share a row; a larger unit has a thread a row.
 // A word of codes gives its values in pairs (dim i, dim i + 4); K and V tiles keep that order, and so do
 // the query rows, and the output's columns are put in order as they are written.
 // P is fp16, held 2^7 times larger, as in q4_attn.cu.
 //
-// Bound by the issue slots and by each role's own latency: a tile at D = 128 is about 1.8 thousand warp
-// instructions of conversion and 0.9 thousand for each 32 rows of softmax.  With one warp a row quarter
-// for all 128 keys (half the softmax warps, twice the converting ones) a tile of 64 rows took 3.7 thousand
-// cycles, waiting for its two softmax warps: 16 segments of 64 rows over 3100 keys 55 us, and 45 us so.  (K a
-// tile ahead of V, and the converting warps off the partitions that the softmax of few rows has to run on,
-// came to the same.)
+// Bound by the instructions that the warps can issue between them: a tile of 64 rows at D = 128 is about six
+// thousand (conversion two of them) at two a cycle, while the tensor cores are busy a third of the time and
+// shared memory two fifths.  64 segments over 6144 keys on average, 8 KV heads, D = 128: 24 rows 150 us, 64
+// rows 158 us.  With the rows packed (the softmax of 32 rows all in one quarter, on one scheduler) and four
+// converting warps: 221 and 205 us.  (Products of 64 rows instead of 128, and codes read without bank
+// conflicts, came to the same; so did rows copied to every quarter, each with its share of the keys.)
 #include "q4.cuh"
 #include "tc.cuh"
 
@@ -69,7 +71,7 @@ struct Q4TileBars {
   static constexpr int DRAIN = 24;
   static constexpr int N = 25;
 };
-constexpr int kQ4SoftWarps = 8, kQ4ConvWarps = 4;
+constexpr int kQ4SoftWarps = 8, kQ4ConvTeam = 4, kQ4ConvWarps = 2 * kQ4ConvTeam;
 constexpr int kQ4TileRoles = kQ4SoftWarps + kQ4ConvWarps + 1;  // warps that read piece records
 
 struct Q4TilePiece {
@@ -83,10 +85,13 @@ struct Q4TilePiece {
 constexpr uint32_t kIdescPV64 = (1u << 4) | (1u << 16) | ((64u >> 3) << 17) | ((128u >> 4) << 24);
 constexpr uint32_t kIdescPV128 = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 
-// 64 consecutive keys' scores of a row: those outside [lo, hi) (offsets from the first) are masked.
-__device__ __forceinline__ void tile_mask64(float (&x)[64], int lo, int hi) {
+// Rows of a unit in each quarter of tensor memory's 128 lanes.
+__device__ __forceinline__ int tile_quarter(int rows) { return rows <= 32 ? 8 : rows <= 64 ? 16 : 32; }
+
+// 32 consecutive keys' scores of a row: those outside [lo, hi) (offsets from the first) are masked.
+__device__ __forceinline__ void tile_mask32(float (&x)[32], int lo, int hi) {
 #pragma unroll
-  for (int k = 0; k < 64; ++k) x[k] = k >= lo && k < hi ? x[k] : -INFINITY;
+  for (int k = 0; k < 32; ++k) x[k] = k >= lo && k < hi ? x[k] : -INFINITY;
 }
 
 template <int D>
@@ -128,8 +133,8 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) sdpa_q4_tile_kernel(Q4AttnA
       mbar_init(bar(B::C_EMPTY + s), kQ4ConvWarps);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(bar(B::K_READY + b), kQ4ConvWarps);
-      mbar_init(bar(B::V_READY + b), kQ4ConvWarps);
+      mbar_init(bar(B::K_READY + b), kQ4ConvTeam);
+      mbar_init(bar(B::V_READY + b), kQ4ConvTeam);
       mbar_init(bar(B::S_FULL + b), 1);
       mbar_init(bar(B::P_FULL + b), kQ4SoftWarps);
       mbar_init(bar(B::PV_DONE + b), 1);
@@ -274,7 +279,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) sdpa_q4_tile_kernel(Q4AttnA
     __syncwarp();
   } else if (warp >= W_CONV) {
     // ---------------------------------------------------------------- converting warps
-    const int cw = warp - W_CONV, tid = cw * 32 + lane;
+    const int team = (warp - W_CONV) / kQ4ConvTeam, cw = warp % kQ4ConvTeam, tid = (warp - W_CONV) * 32 + lane;
     const uint32_t kbits = in_register(kQ4Bf16), vbits = in_register(kQ4F16);
     // this lane's keys of the tile (key0 and key0 + 64), and which 32 dims of every 64 it converts: eight
     // lanes that store together then meet eight different 16-byte columns of the swizzle
@@ -287,9 +292,10 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) sdpa_q4_tile_kernel(Q4AttnA
       const bool valid = pc.valid;
       const int tiles = valid ? (pc.nkeys + C::kKeys - 1) / C::kKeys : 0;
       const int chunks = valid ? pc.ur.rows * (D / 8) : 0;  // 16-byte chunks of the piece's query rows
+      const int quarter = valid ? tile_quarter(pc.ur.rows) : 32;
       const int64_t q0 = (int64_t)pc.ur.rb * kQ4TileRows;
       const int q_start = pc.ur.q_start, hk = pc.ur.hk;
-      constexpr int kQ = 8, kT = kQ4ConvWarps * 32;
+      constexpr int kQ = 4, kT = kQ4ConvWarps * 32;
       uint4 q[kQ];
       auto load_q = [&](int i0) {
 #pragma unroll
@@ -306,8 +312,9 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) sdpa_q4_tile_kernel(Q4AttnA
 #pragma unroll
         for (int i = 0; i < kQ; ++i) {
           const int idx = tid + (i0 + i) * kT, rl = idx / (D / 8), c = idx % (D / 8);
+          const int at = rl / quarter * 32 + rl % quarter;  // its lane of tensor memory
           if (idx < chunks)
-            *reinterpret_cast<uint4*>(smem + C::kOffQ + (c / 8) * (128 * 128) + swz(rl, c % 8, 128)) = q4_q_order(q[i]);
+            *reinterpret_cast<uint4*>(smem + C::kOffQ + (c / 8) * (128 * 128) + swz(at, c % 8, 128)) = q4_q_order(q[i]);
         }
       };
       load_q(0);  // in flight until the last piece's scores are done
@@ -327,6 +334,10 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) sdpa_q4_tile_kernel(Q4AttnA
       for (int j = 0; j < tiles; ++j, ++g) {
         const uint32_t st = g % C::kCodeStages, b = g & 1, use = g >> 1;
         if (!(ok = all(wait(B::C_FULL + st, g / C::kCodeStages)))) break;
+        if (b != (uint32_t)team) {  // the other team's (seen here too, so that no phase goes by unseen)
+          if (lane == 0) mbar_arrive(bar(B::C_EMPTY + st));
+          continue;
+        }
         const uint8_t* codes = smem + C::kOffCodes + st * C::kCodeBytes;
         const uint8_t* scales = codes + 2 * C::kCodes;
         constexpr int NH = D / 64;  // 64-dim columns of the tile
@@ -387,8 +398,9 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) sdpa_q4_tile_kernel(Q4AttnA
     }
   } else {
     // ---------------------------------------------------------------- softmax warps
-    const int hf = warp >> 2, row = (warp & 3) * 32 + lane;  // half of the tile's keys; row of the unit
-    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const int hf = warp >> 2, part = warp & 3;  // half of a tile's keys; quarter of tensor memory's lanes
+    const int tq = lane & 3;
+    const uint32_t lane_off = (uint32_t)(part * 32) << 16;
     const uint32_t t_s = tmem + lane_off + C::kColS + hf * 64, t_o = tmem + lane_off + C::kColO;
     const float sl2 = A.scale_log2;
     // a piece's partial rows, written a piece ago, are counted in the next one's epilogue: by then the
@@ -418,66 +430,182 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) sdpa_q4_tile_kernel(Q4AttnA
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B::PC_EMPTY + (n & 1)));
       const int tiles = (nkeys + C::kKeys - 1) / C::kKeys;
-      const bool here = (warp & 3) * 32 < ur.rows;  // the warp has rows of this unit
-      const bool live = row < ur.rows;
-      const int64_t r = (int64_t)ur.rb * kQ4TileRows + row;
-      const int64_t qi = udiv(r, A.group);
-      int first = 0, last = 0;  // the keys the row sees, as offsets from pos_lo
-      if (live) {
-        const RowWin w = row_window((int)qi, ur.q_len, ur.kv_end, ur.causal, ur.window);
-        first = (int)min(max((int64_t)w.lo - pos_lo, (int64_t)0), (int64_t)nkeys);
-        last = (int)min(max((int64_t)w.hi - pos_lo, (int64_t)first), (int64_t)nkeys);
+      const int quarter = tile_quarter(ur.rows);
+      const bool here = part * quarter < ur.rows;  // the warp has rows of this unit
+      // Units of up to 64 rows: a row over the four threads of a quad, two rows (of 16 keys in a half each) a
+      // thread, or one for up to 32 rows.  Larger ones: a thread a row.
+      const bool quads = quarter < 32, two = quarter == 16;
+      const int row0 = part * quarter + (quads ? lane >> 2 : lane);
+      bool live[2];
+      int first[2], last[2];  // the keys a row sees, as offsets from pos_lo
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        live[c] = row0 + 8 * c < ur.rows && (c == 0 || two);
+        first[c] = last[c] = 0;
+        if (live[c]) {
+          const int64_t qi = udiv((int64_t)ur.rb * kQ4TileRows + row0 + 8 * c, A.group);
+          const RowWin w = row_window((int)qi, ur.q_len, ur.kv_end, ur.causal, ur.window);
+          first[c] = (int)min(max((int64_t)w.lo - pos_lo, (int64_t)0), (int64_t)nkeys);
+          last[c] = (int)min(max((int64_t)w.hi - pos_lo, (int64_t)first[c]), (int64_t)nkeys);
+        }
       }
-      float m = -INFINITY, nmu = 0.f, l = 0.f;
-      for (int j = 0; j < tiles; ++j, ++g) {
-        const uint32_t b = g & 1, use = g >> 1;
-        if (!(ok = all(wait(B::S_FULL + b, use)))) break;
-        if (here) {
-          const int off = j * C::kKeys + hf * 64, lo = first - off, hi = last - off;
-          tc_fence_after();
-          float x[64];
-          tmem_ld64(t_s + b * 128, x);
-          if (__any_sync(0xffffffffu, live && (lo > 0 || hi < 64))) tile_mask64(x, lo, hi);
-          float mx4[4] = {x[0], x[1], x[2], x[3]};
+      float m[2] = {-INFINITY, -INFINITY}, nmu[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};
+      // O holds the tiles up to the last one, once its product is done
+      auto rescalable = [&]() -> bool {
+        if (!all(wait(B::PV_DONE + ((g & 1) ^ 1), (g - 1) >> 1))) return false;
+        tc_fence_after();
+        return true;
+      };
+      auto quad_tile = [&](int j) -> bool {
+        const uint32_t t = t_s + (g & 1) * 128;
+        const int off = j * C::kKeys + hf * 64;
+        float x[32];  // [4 k + 2 c + e]: row c, key 8 k + 2 tq + e
+        tc_fence_after();
+        tmem_ld_quads64(t, x);
+        bool edge = false, up = false;
 #pragma unroll
-          for (int k = 4; k < 64; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], x[k]);
-          const float mn = fmaxf(m, fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2);
-          const bool up = live && mn > m + 8.f;  // false while nothing is visible
-          if (__any_sync(0xffffffffu, up)) {
-            const float alpha = up ? exp2_approx(m - mn) : 1.f;
-            if (up) {
-              m = mn;
-              nmu = kQ4PLift - mn;
-            }
-            l *= alpha;
-            if (j > 0) {  // O holds the tiles up to the last one, once its product is done
-              if (!(ok = all(wait(B::PV_DONE + (b ^ 1), (g - 1) >> 1)))) break;
-              tc_fence_after();
-#pragma unroll 1
-              for (int c = 0; c < D / 32; ++c) {
-                float o[32];
-                tmem_ld32(t_o + hf * D + 32 * c, o);
+        for (int c = 0; c < 2; ++c) edge |= live[c] && (first[c] > off || last[c] < off + 64);
+        if (__any_sync(0xffffffffu, edge)) {
 #pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] *= alpha;
-                tmem_st32(t_o + hf * D + 32 * c, o);
-              }
+          for (int c = 0; c < 2; ++c) {
+            const int lo = first[c] - off, hi = last[c] - off;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const int key = 8 * (k >> 1) + 2 * tq + (k & 1);
+              float& y = x[4 * (k >> 1) + 2 * c + (k & 1)];
+              y = key >= lo && key < hi ? y : -INFINITY;
             }
           }
-          uint32_t pw[32];
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        }
+        float mx[2];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const float p0 = exp2_approx(fmaf(x[2 * k], sl2, nmu)), p1 = exp2_approx(fmaf(x[2 * k + 1], sl2, nmu));
-            sum[(2 * k) & 3] += p0;
-            sum[(2 * k + 1) & 3] += p1;
+        for (int c = 0; c < 2; ++c) {
+          float a = x[2 * c], b = x[2 * c + 1];
+#pragma unroll
+          for (int k = 1; k < 8; ++k) {
+            a = fmaxf(a, x[4 * k + 2 * c]);
+            b = fmaxf(b, x[4 * k + 2 * c + 1]);
+          }
+          mx[c] = fmaxf(a, b);
+          up |= live[c] && mx[c] * sl2 > m[c] + 8.f;  // false while nothing is visible
+        }
+        if (__any_sync(0xffffffffu, up)) {
+          float alpha[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float a = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], 1));
+            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+            const float mn = fmaxf(m[c], a * sl2);
+            alpha[c] = 1.f;
+            if (live[c] && mn > m[c] + 8.f) {
+              alpha[c] = exp2_approx(m[c] - mn);
+              m[c] = mn;
+              nmu[c] = kQ4PLift - mn;
+            }
+            l[c] *= alpha[c];
+          }
+          if (j > 0) {
+            if (!rescalable()) return false;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              float o[16];
+              tmem_ld_quads32(t_o + hf * D + 32 * c, o);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] *= alpha[(k >> 1) & 1];
+              tmem_st_quads32(t_o + hf * D + 32 * c, o);
+            }
+          }
+        }
+        uint32_t pw[16];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (c == 0 || two) {
+            float sum[2] = {0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float p0 = exp2_approx(fmaf(x[4 * k + 2 * c], sl2, nmu[c]));
+              const float p1 = exp2_approx(fmaf(x[4 * k + 2 * c + 1], sl2, nmu[c]));
+              sum[0] += p0;
+              sum[1] += p1;
+              pw[2 * k + c] = pack_f16x2(p0, p1);
+            }
+            l[c] += sum[0] + sum[1];
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) pw[2 * k + c] = 0u;
+          }
+        }
+        tmem_st_quad_pairs(t, pw);  // over the scores
+        tc_fence_before();
+        return true;
+      };
+      // a row's 64 keys in two steps of 32, read twice: once for the maximum, once for the exponentials
+      auto row_tile = [&](int j) -> bool {
+        const uint32_t t = t_s + (g & 1) * 128;
+        const int lo = first[0] - (j * C::kKeys + hf * 64), hi = last[0] - (j * C::kKeys + hf * 64);
+        const bool edge = __any_sync(0xffffffffu, live[0] && (lo > 0 || hi < 64));
+        float mx = -INFINITY;
+        tc_fence_after();
+#pragma unroll 1
+        for (int s = 0; s < 2; ++s) {
+          float x[32];
+          tmem_ld32(t + 32 * s, x);
+          if (edge) tile_mask32(x, lo - 32 * s, hi - 32 * s);
+          float a = x[0], b = x[1];
+#pragma unroll
+          for (int k = 2; k < 32; k += 2) {
+            a = fmaxf(a, x[k]);
+            b = fmaxf(b, x[k + 1]);
+          }
+          mx = fmaxf(mx, fmaxf(a, b));
+        }
+        const float mn = fmaxf(m[0], mx * sl2);
+        const bool up = live[0] && mn > m[0] + 8.f;  // false while nothing is visible
+        if (__any_sync(0xffffffffu, up)) {
+          const float alpha = up ? exp2_approx(m[0] - mn) : 1.f;
+          if (up) {
+            m[0] = mn;
+            nmu[0] = kQ4PLift - mn;
+          }
+          l[0] *= alpha;
+          if (j > 0) {
+            if (!rescalable()) return false;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              float o[32];
+              tmem_ld32(t_o + hf * D + 32 * c, o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] *= alpha;
+              tmem_st32(t_o + hf * D + 32 * c, o);
+            }
+          }
+        }
+#pragma unroll 1
+        for (int s = 0; s < 2; ++s) {
+          float x[32];
+          tmem_ld32(t + 32 * s, x);
+          if (edge) tile_mask32(x, lo - 32 * s, hi - 32 * s);
+          uint32_t pw[16];
+          float sum[2] = {0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float p0 = exp2_approx(fmaf(x[2 * k], sl2, nmu[0]));
+            const float p1 = exp2_approx(fmaf(x[2 * k + 1], sl2, nmu[0]));
+            sum[0] += p0;
+            sum[1] += p1;
             pw[k] = pack_f16x2(p0, p1);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          tmem_st32u(t_s + b * 128, pw);  // over the scores
-          tc_fence_before();
+          l[0] += sum[0] + sum[1];
+          tmem_st16u(t + 16 * s, pw);  // over the scores: the second 32 lie behind all of the pairs
         }
+        tc_fence_before();
+        return true;
+      };
+      for (int j = 0; j < tiles; ++j, ++g) {
+        if (!(ok = all(wait(B::S_FULL + (g & 1), g >> 1)))) break;
+        if (here && !(ok = quads ? quad_tile(j) : row_tile(j))) break;
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B::P_FULL + b));
+        if (lane == 0) mbar_arrive(bar(B::P_FULL + (g & 1)));
       }
       if (!ok) break;
       count_late();
@@ -485,52 +613,98 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) sdpa_q4_tile_kernel(Q4AttnA
       // left the last piece's
       if (!(ok = all(wait(B::PV_DONE + ((g - 1) & 1), (g - 1) >> 1)))) break;
       tc_fence_after();
-      if (l != l) m = 0.f;  // a row whose scores are NaN has no maximum: it is joined as one
-      s_ml[hf][row] = make_float2(m, l);
+      const bool direct = ur.nslots == 1;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        if (quads) {
+          l[c] += __shfl_xor_sync(0xffffffffu, l[c], 1);
+          l[c] += __shfl_xor_sync(0xffffffffu, l[c], 2);
+        }
+        if (l[c] != l[c]) m[c] = 0.f;  // a row whose scores are NaN has no maximum: it is joined as one
+        if (live[c]) s_ml[hf][row0 + 8 * c] = make_float2(m[c], l[c]);
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B::ML));
       if (!(ok = all(wait(B::ML, n)))) break;
       if (!here) continue;
-      const float2 ml0 = s_ml[0][row], ml1 = s_ml[1][row];
-      const float M = fmaxf(ml0.x, ml1.x), Mu = M == -INFINITY ? 0.f : M;
-      const float e0 = exp2_approx(ml0.x - Mu), e1 = exp2_approx(ml1.x - Mu);
-      const float L = ml0.y * e0 + ml1.y * e1;
-      const bool direct = ur.nslots == 1;
-      const bool empty = L == 0.f;  // a row that sees no key writes zeros (never 0 * O)
-      const float wgt = direct ? 1.f / L : 1.f;
-      const float f0 = e0 * wgt, f1 = e1 * wgt;
-      const int h = ur.hk * A.group + (int)(r - qi * A.group);
       // each half's warps write half of the dims
-      __nv_bfloat16* orow = A.out + (ur.q_start + qi) * A.o_rs + (int64_t)h * A.o_hs + hf * (D / 2);
-      const int64_t pidx = ur.slot_base + (int64_t)slot * ur.rows + row;
-      float* prow = A.ws.part_o[kRouteSplitk] + pidx * D + hf * (D / 2);
+      float f[2][2];  // [row][half]
+      int64_t to[2];  // the row's place in the output, or among the partial rows
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        f[c][0] = f[c][1] = 0.f;
+        to[c] = 0;
+        if (!live[c]) continue;
+        const float2 ml0 = s_ml[0][row0 + 8 * c], ml1 = s_ml[1][row0 + 8 * c];
+        const float M = fmaxf(ml0.x, ml1.x), Mu = M == -INFINITY ? 0.f : M;
+        const float e0 = exp2_approx(ml0.x - Mu), e1 = exp2_approx(ml1.x - Mu);
+        const float L = ml0.y * e0 + ml1.y * e1;
+        // (a row that sees no key has zeros of either sign in O: its products were of P = 0)
+        const float wgt = !direct ? 1.f : L == 0.f ? 0.f : 1.f / L;
+        f[c][0] = e0 * wgt;
+        f[c][1] = e1 * wgt;
+        const int64_t r = (int64_t)ur.rb * kQ4TileRows + row0 + 8 * c, qi = udiv(r, A.group);
+        const int64_t pidx = ur.slot_base + (int64_t)slot * ur.rows + row0 + 8 * c;
+        if (direct) {
+          const int h = ur.hk * A.group + (int)(r - qi * A.group);
+          to[c] = (ur.q_start + qi) * A.o_rs + (int64_t)h * A.o_hs + hf * (D / 2);
+        } else {
+          to[c] = pidx * D + hf * (D / 2);
+          if (hf == 0 && (!quads || tq == 0)) A.ws.part_ml[kRouteSplitk][pidx] = make_float2(M, L);
+        }
+      }
+      float* part_o = A.ws.part_o[kRouteSplitk];
 #pragma unroll 1
-      for (int c = 0; c < D / 64; ++c) {
-        float o[32], o1[32];
-        __syncwarp();
-        tmem_ld32(t_o + hf * (D / 2) + 32 * c, o);
-        tmem_ld32(t_o + D + hf * (D / 2) + 32 * c, o1);
-        if (!live) continue;
+      for (int c32 = 0; c32 < D / 64; ++c32) {
+        if (quads) {
+          float o[16], o1[16];
+          tmem_ld_quads32(t_o + hf * (D / 2) + 32 * c32, o);
+          tmem_ld_quads32(t_o + D + hf * (D / 2) + 32 * c32, o1);
 #pragma unroll
-        for (int k = 0; k < 32; ++k) o[k] = empty ? 0.f : o[k] * f0 + o1[k] * f1;
+          for (int k = 0; k < 8; ++k) {
+            const int c = k & 1;
+            // this thread has dims tq and tq + 4 of eight; with its neighbour's, two side by side
+            const float a = o[2 * k] * f[c][0] + o1[2 * k] * f[c][1] + 0.f;
+            const float b = o[2 * k + 1] * f[c][0] + o1[2 * k + 1] * f[c][1] + 0.f;
+            const float y = __shfl_xor_sync(0xffffffffu, tq & 1 ? a : b, 1);
+            const float y0 = tq & 1 ? y : a, y1 = tq & 1 ? b : y;
+            const int64_t at = to[c] + 32 * c32 + 8 * (k >> 1) + (tq & 1 ? tq + 3 : tq);
+            if (!live[c]) continue;
+            if (direct)
+              *reinterpret_cast<uint32_t*>(A.out + at) = pack_bf16x2(y0, y1);
+            else
+              *reinterpret_cast<float2*>(part_o + at) = make_float2(y0, y1);
+          }
+        } else {
+#pragma unroll 1
+          for (int s = 0; s < 32; s += 16) {
+            float o[16], o1[16];
+            __syncwarp();
+            tmem_ld16(t_o + hf * (D / 2) + 32 * c32 + s, o);
+            tmem_ld16(t_o + D + hf * (D / 2) + 32 * c32 + s, o1);
+            if (!live[0]) continue;
 #pragma unroll
-        for (int k = 0; k < 32; k += 8) {  // columns of eight dims: 0 4 1 5 2 6 3 7
-          const float* y = o + k;
-          if (direct) {
-            *reinterpret_cast<uint4*>(orow + 32 * c + k) =
-                make_uint4(pack_bf16x2(y[0], y[2]), pack_bf16x2(y[4], y[6]), pack_bf16x2(y[1], y[3]),
-                           pack_bf16x2(y[5], y[7]));
-          } else {
-            *reinterpret_cast<float4*>(prow + 32 * c + k) = make_float4(y[0], y[2], y[4], y[6]);
-            *reinterpret_cast<float4*>(prow + 32 * c + k + 4) = make_float4(y[1], y[3], y[5], y[7]);
+            for (int k = 0; k < 16; ++k) o[k] = o[k] * f[0][0] + o1[k] * f[0][1] + 0.f;
+#pragma unroll
+            for (int k = 0; k < 16; k += 8) {  // columns of eight dims: 0 4 1 5 2 6 3 7
+              const float* y = o + k;
+              const int64_t at = to[0] + 32 * c32 + s + k;
+              if (direct) {
+                *reinterpret_cast<uint4*>(A.out + at) = make_uint4(pack_bf16x2(y[0], y[2]), pack_bf16x2(y[4], y[6]),
+                                                                   pack_bf16x2(y[1], y[3]), pack_bf16x2(y[5], y[7]));
+              } else {
+                *reinterpret_cast<float4*>(part_o + at) = make_float4(y[0], y[2], y[4], y[6]);
+                *reinterpret_cast<float4*>(part_o + at + 4) = make_float4(y[1], y[3], y[5], y[7]);
+              }
+            }
           }
         }
+        __syncwarp();
       }
       tc_fence_before();
       if (!direct) {
-        if (live && hf == 0) A.ws.part_ml[kRouteSplitk][pidx] = make_float2(M, L);
         late = A.ws.unit_done + unit;
-        late_warps = 2 * ((ur.rows + 31) / 32);
+        late_warps = 2 * ((ur.rows + quarter - 1) / quarter);
         late_at = n & 1;
       }
     }
