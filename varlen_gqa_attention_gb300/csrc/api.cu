@@ -253,9 +253,17 @@ static cudaError_t launch_k(const void* f, unsigned grid, unsigned block, void**
   return cudaLaunchKernelExC(&cfg, f, args);
 }
 
-// Columns a 4-bit call stages in bf16 for the prefill kernel: one per segment that can fill a 128-row
-// tile, as far as 2 GiB of workspace hold them (at least one while that takes at most 8 GiB); none
-// when the automatic route cannot reach kPrefillMinWork.  Depends on sizes and the route policy only.
+// The prefill route over a 4-bit store: its columns are staged first, which many rows have to pay for, and the
+// route it competes with is the tensor-memory kernel of q4_tile.cu at D <= 128.  Split-K / prefill route, 32/8
+// heads, D = 128, in us: one segment over 4096 keys, 128 rows a head 37 / 39, 256 rows 48 / 47, 512 rows
+// 69 / 65, 2048 rows 160 / 135; 128 rows over 32768 keys 113 / 146, 512 rows 316 / 266; four segments of 128 rows
+// over 4096 keys 82 / 98.  At D = 256 the split-K kernel converts a key again for every 8 rows: 64 rows a head
+// over 4096 keys 76 / 45.
+static int q4_prefill_min_rows(int D) { return D <= 128 ? 1024 : kPrefillRows; }
+static float q4_prefill_min_work(int D) { return D <= 128 ? 4 * kPrefillMinWork : kPrefillMinWork; }
+// Columns a 4-bit call stages in bf16 for the prefill kernel: one per segment that can have
+// q4_prefill_min_rows, as far as 2 GiB of workspace hold them (at least one while that takes at most 8 GiB); none
+// when the automatic route cannot reach q4_prefill_min_work.  Depends on sizes and the route policy only.
 static int64_t q4_stage_bytes_per_column(int64_t rows, int Hkv, int D) { return rows * Hkv * D * 2; }
 static int q4_stage_cols(int64_t T, int Hq, int Hkv, int D, int S, int64_t rows) {
   const int policy = g_policy.load();
@@ -264,8 +272,8 @@ static int q4_stage_cols(int64_t T, int Hq, int Hkv, int D, int S, int64_t rows)
   const int64_t packed = T * group;
   int64_t n = S;
   if (policy == SDPA_ROUTE_AUTO) {
-    if (packed < kPrefillRows || (double)packed * Hkv * D * (double)rows < (double)kPrefillMinWork) return 0;
-    n = std::min<int64_t>(n, packed / kPrefillRows);
+    if (packed < q4_prefill_min_rows(D) || (double)packed * Hkv * D * (double)rows < (double)q4_prefill_min_work(D)) return 0;
+    n = std::min<int64_t>(n, packed / q4_prefill_min_rows(D));
   }
   const int64_t col = 2 * q4_stage_bytes_per_column(rows, Hkv, D);  // K and V
   if (col > (8ll << 30)) return 0;
@@ -273,8 +281,8 @@ static int q4_stage_cols(int64_t T, int Hq, int Hkv, int D, int S, int64_t rows)
 }
 
 // Whether a call may route segments to the prefill kernel: not under the split-K policy, and
-// (automatic routing) not when no segment can fill a 128-row tile (T * group < 128) or the
-// call cannot hold kPrefillMinWork of prefill work: that is at most packed rows * Hkv * D *
+// (automatic routing) not when no segment can have pf_min_rows packed rows or the
+// call cannot hold pf_min_work of prefill work: that is at most packed rows * Hkv * D *
 // the longest needed key span, which is at most the store's rows (longer spans are invalid)
 // and, with a call-wide window, T + window - 1.  The scheduler takes the result as
 // prefill_ok, so it never routes work to a prefill kernel that is not launched.
@@ -284,7 +292,7 @@ static bool prefill_launch(const SchedArgs& sa, int64_t T) {
   const int64_t packed = T * sa.group;
   int64_t span_max = sa.rows;
   if (!sa.seg_mode && sa.window > 0) span_max = std::min<int64_t>(span_max, T + sa.window - 1);
-  return packed >= kPrefillRows && (double)packed * sa.Hkv * sa.D * (double)span_max >= (double)kPrefillMinWork;
+  return packed >= sa.pf_min_rows && (double)packed * sa.Hkv * sa.D * (double)span_max >= (double)sa.pf_min_work;
 }
 
 static sdpa_status launch_all(const SchedArgs& sa, const AttnArgs& aa, int D, const Grids& g,
@@ -427,6 +435,8 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
   const int group = Hq / Hkv;
   const bool group_fits = group <= kPrefillRows && (kPrefillRows % group) == 0;
   sa.tile_pf = prefill_tile_keys(D);
+  sa.pf_min_rows = q4 ? q4_prefill_min_rows(D) : kPrefillRows;
+  sa.pf_min_work = q4 ? q4_prefill_min_work(D) : kPrefillMinWork;
   sa.sk_rows = sk_rows;
   sa.sk_tile = tiles ? kQ4TileKeys : kSplitkTile;
   sa.lo_align = q4 ? kQ4RowAlign : 1;

@@ -215,6 +215,8 @@ struct SchedArgs {
   int policy;      // SDPA_ROUTE_*
   int prefill_ok;  // prefill kernel usable for this call (group divides 128, tensor maps made)
   int tile_pf;     // keys per prefill tile
+  int pf_min_rows;    // least packed rows of a segment, and work of a call, of the prefill route: kPrefillRows
+  float pf_min_work;  // and kPrefillMinWork, or the 4-bit store's
   int sk_rows;     // packed rows of a split-K unit, and keys of its tiles
   int sk_tile;
   int lo_align;    // split-K units' key ranges begin at a multiple of this (a power of two, at least 1)

@@ -135,6 +135,8 @@ extern "C" sdpa_status sdpa_varlen_splitk_static(
   sa.policy = SDPA_ROUTE_SPLITK;
   sa.prefill_ok = 0;
   sa.tile_pf = kPrefillTile;
+  sa.pf_min_rows = kPrefillRows;
+  sa.pf_min_work = kPrefillMinWork;
   sa.sk_rows = kSplitkRows;
   sa.sk_tile = kSplitkTile;
   sa.lo_align = 1;

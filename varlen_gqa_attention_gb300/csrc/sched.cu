@@ -155,22 +155,22 @@ __device__ __forceinline__ int tile_len(const SchedArgs& A, int route) {
 }
 
 // Route of a live segment.  The prefill kernel takes segments that fill at least one
-// 128-row tile (on a ring store too: its key tiles stop at the wrap, so a TMA box never
+// 128-row tile, or have the rows that pay for staging a 4-bit column (on a ring store too: its key tiles stop at the wrap, so a TMA box never
 // wraps), when the call holds enough such work to pay for that kernel's fixed cost (`big`:
-// the segments' prefill_work sums to at least kPrefillMinWork); everything else, and
+// the segments' prefill_work sums to at least pf_min_work); everything else, and
 // everything when the prefill kernel is unusable, goes to the split-K kernel.
 __device__ __forceinline__ int route_of(const SchedArgs& A, int32_t q_len, bool big) {
   const int64_t R = (int64_t)q_len * A.group;
   if (A.policy == SDPA_ROUTE_SPLITK || !A.prefill_ok) return kRouteSplitk;
   if (A.policy == SDPA_ROUTE_PREFILL) return kRoutePrefill;
-  return R >= kPrefillRows && big ? kRoutePrefill : kRouteSplitk;
+  return R >= A.pf_min_rows && big ? kRoutePrefill : kRouteSplitk;
 }
 // A live segment's share of the prefill route's work measure: packed rows * needed key
-// span * Hkv * D when it fills a 128-row tile, else 0 (in fp32: no overflow, ample for a
+// span * Hkv * D when it has pf_min_rows of them, else 0 (in fp32: no overflow, ample for a
 // threshold, and fast; fp64 runs at a small fraction of the fp32 rate here).
 __device__ __forceinline__ float prefill_work(const SchedArgs& A, int32_t q_len, int32_t kv_end, int32_t window) {
   const int64_t R = (int64_t)q_len * A.group;
-  if (R < kPrefillRows) return 0.f;
+  if (R < A.pf_min_rows) return 0.f;
   int64_t span = kv_end;
   if (window > 0) span = min(span, (int64_t)q_len + window - 1);
   return (float)R * (float)span * (float)A.Hkv * (float)A.D;
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_kernel(SchedArgs A) 
       if (bits_of((int)s) == 0 && !flag[s] && g.y > 0)
         pw += prefill_work(A, g.y, g.w, cached ? c_mode[s].y : W.segs[s].window);
     }
-    const bool big = block_sum(pw, s_fsum) >= kPrefillMinWork;
+    const bool big = block_sum(pw, s_fsum) >= A.pf_min_work;
     // staged columns go to the first segments of the prefill route, in segment order
     int64_t pf[1] = {0};
     if (A.pf_cols > 0) {
@@ -731,7 +731,7 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_small_kernel(SchedAr
     float pw = live ? prefill_work(A, g[1], g[3], md.y) : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) pw += __shfl_xor_sync(kAll, pw, o);
-    int route = live ? route_of(A, g[1], pw >= kPrefillMinWork) : kRouteNone, nrb = 0;
+    int route = live ? route_of(A, g[1], pw >= A.pf_min_work) : kRouteNone, nrb = 0;
     int pf_col = 0;
     if (A.pf_cols > 0) {  // staged columns go to the first segments of the prefill route
       pf_col = __popc(__ballot_sync(kAll, route == kRoutePrefill) & ((1u << lane) - 1u));
