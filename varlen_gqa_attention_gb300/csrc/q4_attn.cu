@@ -20,8 +20,11 @@
 //   * the products are taken transposed, S^T = K Q^T and O^T = V^T P^T: keys and dims fill the
 //     16 rows of an m16n8k16 product and the query rows its 8 columns, so that a decode unit of up
 //     to 8 rows (one token's heads) wastes no half of each product, score and output register.
-//     (With the query rows as the 16 rows a decode of 64 sequences over 24576 keys on average, 8 KV heads,
-//     D = 128, took 675 us, and 466 so; 332 us, 5.2 TB/s of codes and scales, with what follows.)  P^T is the transpose of what S^T leaves in the lanes: one movmatrix per 8 x 8 block.
+//     P^T is the transpose of what S^T leaves in the lanes: one movmatrix per 8 x 8 block.
+//     (With the query rows as the 16 rows a decode of 64 sequences over 24576 keys on average, 8 KV
+//     heads, D = 128, took 675 us, and 466 so; 335 us, 5.2 TB/s of codes and scales, with what
+//     follows: the ALU pipe is then busy 55 % of the time, at 2.3 instructions a cycle.  A third CTA
+//     on an SM, with runs of 32 keys to fit its registers, took 356 us.)
 // P is rounded to fp16 (half a step is at most 2^-11 of it, against 2^-8 in bf16) and V is exact in
 // fp16; Q and K are multiplied in bf16, where both are exact.  Sums are fp32.  The lazily updated
 // maximum leaves P at most 2^8 above it, so P is kept 2^7 times larger, its sum too: at most 2^15,
