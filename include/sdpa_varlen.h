@@ -292,11 +292,11 @@ sdpa_status sdpa_fourbit_unpack(const sdpa_q4_store* store, int64_t rows, int co
                            void* k_out, void* v_out, int64_t o_row_stride, int64_t o_head_stride,
                            int32_t* status_dev, void* stream);
 
-/* Bytes of device workspace sdpa_varlen_fourbit needs for up to T rows and S segments of a store of
- * these sizes.  Long chunks have their columns staged in it in bf16 (up to 2 GiB of them, or one of up
- * to 8 GiB; segments beyond take the split-K route), and which calls may do so depends on the route
- * policy: ask again after sdpa_set_route_policy (a call refuses a workspace that is too small).  Two
- * calls that may run at the same time, captured or not, need one each. */
+/* Bytes of device workspace sdpa_varlen_fourbit takes for up to T rows and S segments of a store of
+ * these sizes.  Long chunks have their columns staged in it in bf16, up to 2 GiB of them (or one of up to
+ * 8 GiB), as this call of T rows and S segments may have under the present route policy; a call stages as
+ * many as its workspace holds, and the other segments take the split-K route.  Two calls that may run at the
+ * same time, captured or not, need one each. */
 size_t sdpa_varlen_fourbit_workspace_bytes(int64_t T, int Hq, int Hkv, int D, int S, int64_t rows, int cols);
 
 /*

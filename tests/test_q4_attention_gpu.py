@@ -458,12 +458,12 @@ def test_one_workspace_for_calls_of_different_sizes(dev):
     store = random_store(2048, 6, 2, 128, 46)
     stored = pkg.Q4Store(*(t.to(dev) for t in store))
     ws = torch.full((pkg.q4_workspace_bytes(240, 16, stored, 6),), 255, dtype=torch.uint8, device=dev)
-    for n in (40, 1, 3, 2, 17):
-        seq = [[n * i, n, i, 2000 - 300 * i] for i in range(6)]
-        q = queries(6 * n, 16, 128, 46)
+    for n, S_ in ((40, 6), (1, 6), (3, 6), (2, 6), (17, 6), (240, 1), (1, 1), (70, 2), (200, 1)):
+        seq = [[n * i, n, i, 2000 - 300 * i] for i in range(S_)]
+        q = queries(S_ * n, 16, 128, 46)
         got = pkg.sdpa_varlen_q4(q.to(dev), stored, torch.tensor(seq, dtype=torch.int32, device=dev), causal=True,
                                  workspace=ws)
-        check(got, 0, q, store, seq, True)
+        check(got, 0, q, store, seq, True, p_step=2.0 ** -8, rows_subset=sorted({0, S_ * n // 2, S_ * n - 1}))
 
 
 def test_two_captured_graphs_of_one_workspace_replayed_in_turn(dev):
@@ -516,3 +516,26 @@ def test_python_entries_refuse_mixed_devices_and_foreign_streams(dev):
     small = pkg.Q4Store(*(t[:, :, :24].contiguous() for t in store))
     with pytest.raises(pkg.SdpaError, match="multiple of 16 rows"):
         pkg.sdpa_varlen_q4(q, small, seq, causal=True)
+
+
+@pytest.mark.parametrize("S_", [20, 70])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("chunk,kv,long", [
+    (120, 130, 1500),   # a chunk over few keys among tokens over many: the split-K kernel for few rows
+    (120, 1500, 40),    # over many keys: the tensor-memory one
+    (400, 1500, 1500),  # long enough to be staged in bf16, tokens beside it
+])
+def test_a_chunk_among_single_tokens_takes_the_cheaper_kernel(dev, S_, D, chunk, kv, long):
+    seq, t = [], 0
+    for i in range(S_):
+        n = chunk if i == S_ // 2 else 1
+        seq.append([t, n, i, max(n, kv) if n > 1 else long - i % 9])
+        t += n
+    seq[3][2] = S_ + 5  # one segment of no column
+    store, q = random_store(1504, S_, 2, D, D + S_), queries(t + 2, 32, D, 50)
+    rows = sorted({0, 1, 3, t - 1, t, t + 1} | {S_ // 2 + i for i in (-1, 0, 1, chunk // 2, chunk - 1, chunk)})
+    for causal in (True, False):
+        got, st = run_q4(q, store, seq, dev, causal=causal)
+        check(got, st, q, store, seq, causal, p_step=2.0 ** -8, rows_subset=rows)
+    got, st = run_q4(q, store, seq, dev, causal=True, window=100)
+    check(got, st, q, store, seq, True, 100, p_step=2.0 ** -8, rows_subset=rows)

@@ -154,15 +154,38 @@ def test_attend(kw, code):
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_a_workspace_for_bounds_serves_every_smaller_call(D):
     need = pkg.library().sdpa_varlen_fourbit_workspace_bytes
-    for Hq, Hkv in ((8, 8), (32, 8), (16, 1), (256, 2)):
-        for T in (1, 16, 64, 257, 2048):
-            for S_ in (0, 1, 7, 64, 500):
-                bound = need(T, Hq, Hkv, D, S_, 4096, 64)
-                for t in (0, 1, 3, 40, 200, T):
-                    for s in (0, 1, 6, 63, S_):
-                        if t <= T and s <= S_:
-                            assert need(t, Hq, Hkv, D, s, 4096, 64) <= bound, (Hq, Hkv, T, S_, t, s)
+    pkg.set_route_policy(pkg.ROUTE_SPLITK)  # without staged columns, of which a call takes what it is given
+    try:
+        for Hq, Hkv in ((8, 8), (32, 8), (16, 1), (256, 2)):
+            for T in (1, 16, 64, 257, 2048):
+                for S_ in (0, 1, 7, 64, 500):
+                    bound = need(T, Hq, Hkv, D, S_, 4096, 64)
+                    for t in (0, 1, 3, 40, 200, T):
+                        for s in (0, 1, 6, 63, S_):
+                            if t <= T and s <= S_:
+                                assert need(t, Hq, Hkv, D, s, 4096, 64) <= bound, (Hq, Hkv, T, S_, t, s)
+    finally:
+        pkg.set_route_policy(pkg.ROUTE_AUTO)
     assert need(1, 3, 2, D, 1, 64, 1) == 0 and need(1, 2, 2, 96, 1, 64, 1) == 0 and need(1, 2, 2, D, 1, 1 << 31, 1) == 0
+
+
+def test_staged_columns_follow_the_longest_segment():
+    need = pkg.library().sdpa_varlen_fourbit_workspace_bytes
+    col = 2 * 32768 * 8 * 128 * 2  # K and V of one column in bf16
+
+    def staged(T, S_, D=128):
+        pkg.set_route_policy(pkg.ROUTE_SPLITK)
+        plain = need(T, 32, 8, D, S_, 32768, 64)
+        pkg.set_route_policy(pkg.ROUTE_AUTO)
+        return (need(T, 32, 8, D, S_, 32768, 64) - plain) / col
+
+    assert staged(64, 64) == 0               # single tokens
+    assert staged(94, 64) == 0               # a segment of 31 rows among them (124 packed)
+    assert staged(95, 64) == 2               # of 32: the rows that fill a tile, twice over
+    assert staged(64 + 300, 64) == 1         # more than 16 packed rows on average: 1024 of a segment
+    assert staged(64 + 150, 16) == 0
+    assert staged(256, 1) == 1 and staged(255, 1) == 0
+    assert staged(8192, 4) == 4 and staged(1 << 16, 64) == 16  # 2 GiB of them
 
 
 # ------------------------------------------------------------------------------- the Python entries

@@ -70,13 +70,16 @@ static sdpa_status device_info(DevInfo* out) {
   if (!di.ready) {
     e = cudaDeviceGetAttribute(&di.sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "SM count: %s", cudaGetErrorString(e));
-    e = cudaFuncSetAttribute(sched_kernel_ptr(), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)sched_smem_bytes());
-    if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "scheduler smem attribute: %s", cudaGetErrorString(e));
+    for (int q4 = 0; q4 < 2; ++q4) {
+      e = cudaFuncSetAttribute(sched_kernel_ptr(q4), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)sched_smem_bytes());
+      if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "scheduler smem attribute: %s", cudaGetErrorString(e));
+    }
     // every kernel of a call asks for the whole shared-memory carveout, so that the SMs keep
     // one L1 / shared split from kernel to kernel (the clone kernel runs alone and keeps the
     // default split, its L1 to itself)
-    const void* others[3] = {sched_kernel_ptr(), sched_small_kernel_ptr(), append_kernel_ptr()};
+    const void* others[5] = {sched_kernel_ptr(false), sched_small_kernel_ptr(false), append_kernel_ptr(),
+                             sched_kernel_ptr(true), sched_small_kernel_ptr(true)};
     for (const void* f : others) {
       e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
       if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "carveout attribute: %s", cudaGetErrorString(e));
@@ -112,8 +115,10 @@ static sdpa_status device_info(DevInfo* out) {
       di.q4_per_sm[k] = nb > 0 ? nb : 1;
       e = cudaFuncSetAttribute(combine_pair_kernel_ptr(Ds[k]), cudaFuncAttributePreferredSharedMemoryCarveout, 100);
       if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "carveout attribute: %s", cudaGetErrorString(e));
-      e = cudaFuncSetAttribute(combine_kernel_ptr(Ds[k]), cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-      if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "carveout attribute: %s", cudaGetErrorString(e));
+      for (int q = 0; q < 2; ++q) {
+        e = cudaFuncSetAttribute(combine_kernel_ptr(Ds[k], q), cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+        if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "carveout attribute: %s", cudaGetErrorString(e));
+      }
       const void* pf = prefill_kernel_ptr(Ds[k]);
       e = cudaFuncSetAttribute(pf, cudaFuncAttributeMaxDynamicSharedMemorySize, prefill_smem_bytes(Ds[k]));
       if (e == cudaSuccess) e = cudaFuncSetAttribute(pf, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
@@ -181,19 +186,25 @@ static Grids grids_for(const DevInfo& di, int D) {
   return g;
 }
 
-// The 4-bit store's kernel for the split-K route: the tensor-memory one (q4_tile.cu), which converts a key
-// once for up to 128 packed rows, when the average segment (what the host knows of them) has more than
-// 16; the other one, which converts a key again for every 8, otherwise.  64 segments over 6144 keys on
-// average, 8 KV heads, D = 128, tensor-memory / other: 16 rows 221 / 166 us, 24 rows 221 / 303 us; 16 segments
-// of 64 rows over 3100 keys 45 / 100 us.  At D = 256 the output of 128 rows leaves no room for the first.
-static bool q4_tiles(int64_t T, int Hq, int Hkv, int D, int S) {
-  return D <= 128 && T * (Hq / Hkv) > 16 * (int64_t)std::max(S, 1);
+// The 4-bit store's kernels for the split-K route: the tensor-memory one (q4_tile.cu), which converts a key
+// once for up to 128 packed rows, and the other one (q4_attn.cu), which converts a key again for every 8.
+// 64 segments over 6144 keys on average, 8 KV heads, D = 128, tensor-memory / other: 16 rows 150 / 131 us, 24
+// rows 150 / 303 us; 16 segments of 64 rows over 3100 keys 43 / 100 us.  The host knows how many rows the average
+// segment has: with at most 16 it launches the other one, with more (of several segments, which may be one
+// chunk and many single tokens) both, and the schedule is the cheaper one's; the other leaves at once.  At
+// D = 256 the output of 128 rows leaves no room for the first.
+enum class Q4Split { kFew, kTile, kEither };
+static Q4Split q4_split(int64_t T, int Hq, int Hkv, int D, int S) {
+  if (D > 128 || T * (Hq / Hkv) <= 16 * (int64_t)std::max(S, 1)) return Q4Split::kFew;
+  return S <= 1 ? Q4Split::kTile : Q4Split::kEither;
 }
-static Grids q4_grids_for(const DevInfo& di, int D, bool tiles) {
-  Grids g = grids_for(di, D);
-  g.splitk = tiles ? di.sms : (int64_t)di.sms * di.q4_per_sm[d_index(D)];
-  return g;
+// The tensor-memory kernel's cost of a key for a unit, in those of the other one for 8 rows (full loads: 0.066
+// and 0.027 ns at D = 128, 0.054 and 0.015 at D = 64).
+static float q4_tile_ratio(int D) { return D == 64 ? 3.5f : 2.5f; }
+static SkShape q4_few_shape(const DevInfo& di, int D) {
+  return {kSplitkRows, kSplitkTile, kSkQ4Few, (int64_t)di.sms * di.q4_per_sm[d_index(D)]};
 }
+static SkShape q4_tile_shape(const DevInfo& di) { return {kQ4TileRows, kQ4TileKeys, kSkQ4Tile, di.sms}; }
 
 sdpa_status check_common(int64_t T, int Hq, int Hkv, int D, int S, int64_t rows, int cols, int window,
                          float scale) {
@@ -259,8 +270,11 @@ static cudaError_t launch_k(const void* f, unsigned grid, unsigned block, void**
 // 69 / 65, 2048 rows 160 / 135; 128 rows over 32768 keys 113 / 146, 512 rows 316 / 266; four segments of 128 rows
 // over 4096 keys 82 / 98.  At D = 256 the split-K kernel converts a key again for every 8 rows: 64 rows a head
 // over 4096 keys 76 / 45.
-static int q4_prefill_min_rows(int D) { return D <= 128 ? 1024 : kPrefillRows; }
-static float q4_prefill_min_work(int D) { return D <= 128 ? 4 * kPrefillMinWork : kPrefillMinWork; }
+// So the bf16 entry's thresholds hold where that kernel would do without the tensor-memory one.
+static int q4_prefill_min_rows(Q4Split sp) { return sp == Q4Split::kFew ? kPrefillRows : 1024; }
+static float q4_prefill_min_work(Q4Split sp) { return sp == Q4Split::kFew ? kPrefillMinWork : 4 * kPrefillMinWork; }
+// Packed rows of a call's longest segment when none is empty.
+static int64_t q4_longest(int64_t T, int group, int S) { return std::max<int64_t>(1, T - std::max(S, 1) + 1) * group; }
 // Columns a 4-bit call stages in bf16 for the prefill kernel: one per segment that can have
 // q4_prefill_min_rows, as far as 2 GiB of workspace hold them (at least one while that takes at most 8 GiB); none
 // when the automatic route cannot reach q4_prefill_min_work.  Depends on sizes and the route policy only.
@@ -272,8 +286,11 @@ static int q4_stage_cols(int64_t T, int Hq, int Hkv, int D, int S, int64_t rows)
   const int64_t packed = T * group;
   int64_t n = S;
   if (policy == SDPA_ROUTE_AUTO) {
-    if (packed < q4_prefill_min_rows(D) || (double)packed * Hkv * D * (double)rows < (double)q4_prefill_min_work(D)) return 0;
-    n = std::min<int64_t>(n, packed / q4_prefill_min_rows(D));
+    const Q4Split sp = q4_split(T, Hq, Hkv, D, S);
+    if (q4_longest(T, group, S) < q4_prefill_min_rows(sp) ||
+        (double)packed * Hkv * D * (double)rows < (double)q4_prefill_min_work(sp))
+      return 0;
+    n = std::min<int64_t>(n, packed / q4_prefill_min_rows(sp));
   }
   const int64_t col = 2 * q4_stage_bytes_per_column(rows, Hkv, D);  // K and V
   if (col > (8ll << 30)) return 0;
@@ -352,12 +369,12 @@ static sdpa_status launch_all(const SchedArgs& sa, const AttnArgs& aa, int D, co
   }
   if (e == cudaSuccess) e = mark(2, st);
   if (e == cudaSuccess && q4) {
-    Q4AttnArgs ga{aa, *q4};
+    Q4AttnArgs ga{aa, *q4, sa.sk_choice};
     void* args[] = {(void*)&ga};
-    if (aa.sk_rows == kQ4TileRows)
-      e = launch_k(q4_tile_kernel_ptr(D), (unsigned)g.splitk, kQ4TileThreads, args, q4_tile_smem_bytes(D), st, true);
-    else
-      e = launch_k(q4_splitk_kernel_ptr(D), (unsigned)g.splitk, kQ4Threads, args, q4_splitk_smem_bytes(D), st, true);
+    if (sa.sk_choice || sa.sk[0].rows == kSplitkRows)
+      e = launch_k(q4_splitk_kernel_ptr(D), (unsigned)sa.sk[0].grid, kQ4Threads, args, q4_splitk_smem_bytes(D), st, true);
+    if (e == cudaSuccess && (sa.sk_choice || sa.sk[0].rows == kQ4TileRows))
+      e = launch_k(q4_tile_kernel_ptr(D), (unsigned)sa.sk[1].grid, kQ4TileThreads, args, q4_tile_smem_bytes(D), st, true);
     if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "4-bit split-K launch: %s", cudaGetErrorString(e));
   } else if (e == cudaSuccess) {
     void* args[] = {(void*)&aa};
@@ -373,7 +390,7 @@ static sdpa_status launch_all(const SchedArgs& sa, const AttnArgs& aa, int D, co
     if (q4 && warps <= 8 * (int64_t)g.prefill)
       e = launch_k(combine_pair_kernel_ptr(D), (unsigned)warps, 256, args, 0, st, true);
     else
-      e = launch_k(combine_kernel_ptr(D), (unsigned)blocks, 256, args, 0, st, true);
+      e = launch_k(combine_kernel_ptr(D, q4 != nullptr), (unsigned)blocks, 256, args, 0, st, true);
     if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "combine launch: %s", cudaGetErrorString(e));
   }
   if (e == cudaSuccess) e = mark(4, st);
@@ -400,20 +417,26 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
 
   DevInfo di;
   if ((st = device_info(&di))) return st;
-  const bool tiles = q4 && q4_tiles(T, Hq, Hkv, D, S);
-  const Grids g = q4 ? q4_grids_for(di, D, tiles) : grids_for(di, D);
-  const int sk_rows = tiles ? kQ4TileRows : kSplitkRows;
-  Workspace W;
-  size_t need = layout_workspace((char*)ws, T, Hq, Hkv, D, S, g.splitk, g.prefill, &W, true, sk_rows);
-  Q4StageArgs sg{};
-  if (q4 && (sg.pf_cols = q4_stage_cols(T, Hq, Hkv, D, S, rows)) > 0) {
-    const int64_t store = align_up(q4_stage_bytes_per_column(rows, Hkv, D) * sg.pf_cols, 256);
-    sg.k = (__nv_bfloat16*)((char*)ws + need);
-    sg.v = (__nv_bfloat16*)((char*)ws + need + store);
-    need += 2 * store;
+  Grids g = grids_for(di, D);
+  Q4Split sp = Q4Split::kFew;
+  SkShape few{kSplitkRows, kSplitkTile, kSkBf16, g.splitk}, tile = q4_tile_shape(di);
+  if (q4) {
+    sp = q4_split(T, Hq, Hkv, D, S);
+    few = q4_few_shape(di, D);
+    g.splitk = few.grid;
   }
+  Workspace W;
+  size_t need = layout_workspace((char*)ws, T, Hq, Hkv, D, S, g.splitk, g.prefill, &W, true,
+                                 q4 && D <= 128 ? &tile : nullptr);
   if (ws_bytes < need)
     return fail(SDPA_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need);
+  Q4StageArgs sg{};
+  if (q4) {  // as many staged columns as the workspace holds
+    const int64_t col = q4_stage_bytes_per_column(rows, Hkv, D);  // (a multiple of 256)
+    sg.pf_cols = (int)std::min<int64_t>(q4_stage_cols(T, Hq, Hkv, D, S, rows), (int64_t)(ws_bytes - need) / (2 * col));
+    sg.k = (__nv_bfloat16*)((char*)ws + need);
+    sg.v = (__nv_bfloat16*)((char*)ws + need + col * sg.pf_cols);
+  }
 
   SchedArgs sa{};
   sa.seq_info = seq_info;
@@ -435,10 +458,13 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
   const int group = Hq / Hkv;
   const bool group_fits = group <= kPrefillRows && (kPrefillRows % group) == 0;
   sa.tile_pf = prefill_tile_keys(D);
-  sa.pf_min_rows = q4 ? q4_prefill_min_rows(D) : kPrefillRows;
-  sa.pf_min_work = q4 ? q4_prefill_min_work(D) : kPrefillMinWork;
-  sa.sk_rows = sk_rows;
-  sa.sk_tile = tiles ? kQ4TileKeys : kSplitkTile;
+  sa.pf_min_rows = q4 ? q4_prefill_min_rows(sp) : kPrefillRows;
+  sa.pf_min_work = q4 ? q4_prefill_min_work(sp) : kPrefillMinWork;
+  sa.q4 = q4 != nullptr;
+  sa.sk[0] = sp == Q4Split::kTile ? tile : few;
+  sa.sk[1] = tile;
+  sa.sk_choice = sp == Q4Split::kEither;
+  sa.sk_ratio = q4_tile_ratio(D);
   sa.lo_align = q4 ? kQ4RowAlign : 1;
   sa.pf_cols = sg.pf_cols;
   // (a call-wide window bounds the positions that a staged column has to hold)
@@ -448,7 +474,6 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
                                    q4 ? sg.pf_cols : cols, Hkv, group, sa.tile_pf, &tm.q, &tm.k, &tm.v);
   if (!sa.prefill_ok) sa.pf_cols = 0;
   sa.grid[0] = 0;
-  sa.grid[1] = g.splitk;
   sa.grid[2] = g.prefill;
   sa.ws = W;
   sa.status_dev = status_dev;
@@ -474,7 +499,6 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
   aa.o_rs = o_rs;
   aa.o_hs = o_hs;
   aa.T = T;
-  aa.sk_rows = sk_rows;
   aa.ws = W;
   aa.status_dev = status_dev;
   AppendArgs apw;
@@ -571,22 +595,16 @@ size_t sdpa_varlen_fourbit_workspace_bytes(int64_t T, int Hq, int Hkv, int D, in
   if (T < 0 || S < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || rows <= 0 || rows > INT32_MAX || cols <= 0) return 0;
   if (D != 64 && D != 128 && D != 256) return 0;
   DevInfo di;
-  // without a device: bounds above any real grid
-  Grids other{4096, 1024}, tile{4096, 1024};
+  Grids g{4096, 1024};  // without a device: bounds above any real grid
+  SkShape tile{kQ4TileRows, kQ4TileKeys, kSkQ4Tile, 1024};
   if (device_info(&di) == SDPA_OK) {
-    other = q4_grids_for(di, D, false);
-    tile = q4_grids_for(di, D, true);
+    g = {q4_few_shape(di, D).grid, grids_for(di, D).prefill};
+    tile = q4_tile_shape(di);
   } else {
     g_err[0] = 0;
   }
-  // Calls within the bounds take either kernel, the one that is not q4_tiles with at most 16 packed rows
-  // a segment on average: the larger of the two layouts serves them all.
-  const int64_t few = D <= 128 ? std::min<int64_t>(T, 16 * (int64_t)S / (Hq / Hkv)) : T;
-  size_t need = layout_workspace(nullptr, few, Hq, Hkv, D, S, other.splitk, other.prefill, nullptr);
-  if (q4_tiles(T, Hq, Hkv, D, 1))
-    need = std::max(need, layout_workspace(nullptr, T, Hq, Hkv, D, S, tile.splitk, tile.prefill, nullptr, true,
-                                           kQ4TileRows));
-  return need + 2 * align_up(q4_stage_bytes_per_column(rows, Hkv, D) * q4_stage_cols(T, Hq, Hkv, D, S, rows), 256);
+  return layout_workspace(nullptr, T, Hq, Hkv, D, S, g.splitk, g.prefill, nullptr, true, D <= 128 ? &tile : nullptr) +
+         2 * q4_stage_bytes_per_column(rows, Hkv, D) * q4_stage_cols(T, Hq, Hkv, D, S, rows);
 }
 
 sdpa_status sdpa_varlen_fourbit(const void* q, int64_t T, int Hq, int D, int64_t q_row_stride, int64_t q_head_stride,

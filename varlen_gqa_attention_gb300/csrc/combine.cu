@@ -42,7 +42,7 @@ __device__ __forceinline__ bool wait_done(const int32_t* count, int32_t n) {
 
 // One warp: packed row t, query head h (gw = t * Hq + h).
 template <int D>
-__device__ __forceinline__ void combine_row(const AttnArgs& A, int64_t gw, int lane, int64_t U1, int64_t U2) {
+__device__ __forceinline__ void combine_row(const AttnArgs& A, int64_t gw, int lane, int64_t U1, int64_t U2, int sk_rows) {
   constexpr int PER = D / 32;  // elements per lane
   const int64_t t = gw / A.Hq;
   const int h = (int)(gw % A.Hq);
@@ -55,7 +55,7 @@ __device__ __forceinline__ void combine_row(const AttnArgs& A, int64_t gw, int l
   if (q != kRouteNone) {
     // route-indexed fields picked by select: a runtime index would copy them to local memory
     const bool pf = q == kRoutePrefill;
-    const int rpu = pf ? prefill_unit_rows(D) : A.sk_rows;
+    const int rpu = pf ? prefill_unit_rows(D) : sk_rows;
     const int hk = h / A.group;
     const int64_t r = (int64_t)ri.w * A.group + (h % A.group);
     const int64_t rb = r / rpu;
@@ -135,17 +135,19 @@ __device__ __forceinline__ void combine_row(const AttnArgs& A, int64_t gw, int l
 // A grid of at most 8 CTAs per SM (a full SM's worth of warps) walks the (row, head) pairs,
 // so that a call with many rows and nothing to merge does not pay for launching a CTA per 8
 // pairs.
-template <int D>
+// Q4: the schedule's own units, of a 4-bit call.
+template <int D, bool Q4>
 __global__ void __launch_bounds__(kCombineThreads) sdpa_combine_kernel(AttnArgs A) {
   const Workspace& W = A.ws;
   // independent loads, issued together: whether there is work and the routes' unit counts
   const int64_t work = W.hdr->combine_work;
   const int64_t U1 = W.hdr->units[kRouteSplitk], U2 = W.hdr->units[kRoutePrefill];
+  const int sk_rows = Q4 ? (int)W.hdr->sk_rows : kSplitkRows;
   if (!work) return;
   const int lane = threadIdx.x & 31;
   const int64_t n = A.T * A.Hq, stride = (int64_t)gridDim.x * (kCombineThreads / 32);
   for (int64_t gw = ((int64_t)blockIdx.x * kCombineThreads + threadIdx.x) >> 5; gw < n; gw += stride)
-    combine_row<D>(A, gw, lane, U1, U2);
+    combine_row<D>(A, gw, lane, U1, U2, sk_rows);
 }
 
 // The same for calls with few (row, head) pairs, whose units may be cut over many CTAs (one long
@@ -162,6 +164,7 @@ __global__ void __launch_bounds__(kCombineThreads) sdpa_combine_pair_kernel(Attn
   const Workspace& W = A.ws;
   const int64_t work = W.hdr->combine_work;
   const int64_t U1 = W.hdr->units[kRouteSplitk], U2 = W.hdr->units[kRoutePrefill];
+  const int sk_rows = (int)W.hdr->sk_rows;
   if (!work) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t gw = blockIdx.x, t = udiv(gw, A.Hq);
@@ -173,11 +176,11 @@ __global__ void __launch_bounds__(kCombineThreads) sdpa_combine_pair_kernel(Attn
   if (ri.x == kRouteSplitk) {
     const int hk = h / A.group;
     r = (int64_t)ri.w * A.group + (h % A.group);
-    u = (int64_t)ri.y + (int64_t)hk * ri.z + r / A.sk_rows;
+    u = (int64_t)ri.y + (int64_t)hk * ri.z + r / sk_rows;
     if (u < U1) ur = W.units[kRouteSplitk][u];
   }
   if (ur.nslots <= kCombineShare) {  // (the same for the whole CTA)
-    if (warp == 0) combine_row<D>(A, gw, lane, U1, U2);
+    if (warp == 0) combine_row<D>(A, gw, lane, U1, U2, sk_rows);
     return;
   }
   if (threadIdx.x == 0) {
@@ -191,7 +194,7 @@ __global__ void __launch_bounds__(kCombineThreads) sdpa_combine_pair_kernel(Attn
   if (s_late) return;
   // every thread's own acquire of the slots that the count stands for
   ld_acquire(W.unit_done + u);
-  const int64_t rl = r % A.sk_rows, stride = ur.rows;
+  const int64_t rl = r % sk_rows, stride = ur.rows;
   const float2* ml = W.part_ml[kRouteSplitk] + ur.slot_base + rl;
   const float* po = W.part_o[kRouteSplitk] + (ur.slot_base + rl) * D + lane * PER;
   float M = -INFINITY, L = 0.f, acc[PER];
@@ -251,10 +254,6 @@ __global__ void __launch_bounds__(kCombineThreads) sdpa_combine_pair_kernel(Attn
 template __global__ void sdpa_combine_pair_kernel<64>(AttnArgs);
 template __global__ void sdpa_combine_pair_kernel<128>(AttnArgs);
 template __global__ void sdpa_combine_pair_kernel<256>(AttnArgs);
-template __global__ void sdpa_combine_kernel<64>(AttnArgs);
-template __global__ void sdpa_combine_kernel<128>(AttnArgs);
-template __global__ void sdpa_combine_kernel<256>(AttnArgs);
-
 const void* combine_pair_kernel_ptr(int D) {
   switch (D) {
     case 64: return (const void*)sdpa_combine_pair_kernel<64>;
@@ -263,12 +262,14 @@ const void* combine_pair_kernel_ptr(int D) {
   }
 }
 
-const void* combine_kernel_ptr(int D) {
+template <bool Q4>
+static const void* combine_ptr(int D) {
   switch (D) {
-    case 64: return (const void*)sdpa_combine_kernel<64>;
-    case 128: return (const void*)sdpa_combine_kernel<128>;
-    default: return (const void*)sdpa_combine_kernel<256>;
+    case 64: return (const void*)sdpa_combine_kernel<64, Q4>;
+    case 128: return (const void*)sdpa_combine_kernel<128, Q4>;
+    default: return (const void*)sdpa_combine_kernel<256, Q4>;
   }
 }
+const void* combine_kernel_ptr(int D, bool q4) { return q4 ? combine_ptr<true>(D) : combine_ptr<false>(D); }
 
 }  // namespace sdpa

@@ -87,6 +87,7 @@ struct SchedHdr {
   // Non-zero when the combine pass has rows to write: rows no live segment covers, units
   // with no keys, or units split over several CTAs.
   int64_t combine_work;
+  int64_t sk_rows;  // packed rows of a split-K unit
 };
 
 struct Workspace {
@@ -127,13 +128,20 @@ __host__ __device__ inline int64_t part_cap(int64_t ucap, int64_t grid, int rows
   return (ucap + kPartPhases * grid + 1) * rows_per_unit;
 }
 
+// What the split-K route's schedule depends on: the packed rows of a unit, the keys of a tile, the CTAs.
+struct SkShape {
+  int rows, tile, kind;  // kind: SkKind
+  int64_t grid;
+};
+
 // Lays the workspace out from `base` (base may be null to only measure). Returns bytes.
 // Without the prefill route (`with_prefill` false: every segment takes the split-K kernel)
-// that route's unit table and partial slots are empty.
+// that route's unit table and partial slots are empty; `sk2` is a second shape that the split-K route's
+// schedule may take.
 __host__ inline size_t layout_workspace(char* base, int64_t T, int Hq, int Hkv, int D, int S,
                                         int64_t grid_splitk, int64_t grid_prefill,
                                         Workspace* ws, bool with_prefill = true,
-                                        int splitk_rows = kSplitkRows) {
+                                        const SkShape* sk2 = nullptr) {
   int64_t off = 0;
   auto take = [&](int64_t bytes) {
     int64_t o = off;
@@ -146,12 +154,17 @@ __host__ inline size_t layout_workspace(char* base, int64_t T, int Hq, int Hkv, 
   w.row_seg = (int32_t*)take(4 * (T > 0 ? T : 1));
   w.row_info = (int4*)take(16 * (T > 0 ? T : 1));
   w.seg_flag = (int32_t*)take(4 * (S > 0 ? S : 1));
-  const int rpu[3] = {0, splitk_rows, prefill_unit_rows(D)};
-  const int64_t grid[3] = {0, grid_splitk, grid_prefill};
+  const int rpu[3] = {0, kSplitkRows, prefill_unit_rows(D)};
+  int64_t grid[3] = {0, grid_splitk, grid_prefill};
   for (int r = 1; r < 3; ++r) {
     const bool used = r == kRouteSplitk || with_prefill;
     w.unit_cap[r] = used ? unit_cap(T, Hq, Hkv, S, rpu[r]) : 0;
     w.part_cap[r] = used ? part_cap(w.unit_cap[r], grid[r], rpu[r]) : 0;
+    if (r == kRouteSplitk && sk2) {
+      const int64_t cap = part_cap(unit_cap(T, Hq, Hkv, S, sk2->rows), sk2->grid, sk2->rows);
+      if (cap > w.part_cap[r]) w.part_cap[r] = cap;
+      if (sk2->grid > grid[r]) grid[r] = sk2->grid;
+    }
     w.units[r] = (UnitRec*)take((int64_t)sizeof(UnitRec) * w.unit_cap[r]);
     w.first_unit[r] = (int32_t*)take(4 * (int64_t)kMaxPhases * (grid[r] > 0 ? grid[r] : 1));
     w.part_ml[r] = (float2*)take(8 * w.part_cap[r]);
@@ -175,7 +188,6 @@ struct AttnArgs {
   __nv_bfloat16* out;
   int64_t o_rs, o_hs;
   int64_t T;
-  int sk_rows;         // packed rows of a split-K unit
   Workspace ws;
   int32_t* status_dev;
 };
@@ -215,16 +227,18 @@ struct SchedArgs {
   int policy;      // SDPA_ROUTE_*
   int prefill_ok;  // prefill kernel usable for this call (group divides 128, tensor maps made)
   int tile_pf;     // keys per prefill tile
-  int pf_min_rows;    // least packed rows of a segment, and work of a call, of the prefill route: kPrefillRows
-  float pf_min_work;  // and kPrefillMinWork, or the 4-bit store's
-  int sk_rows;     // packed rows of a split-K unit, and keys of its tiles
-  int sk_tile;
-  int lo_align;    // split-K units' key ranges begin at a multiple of this (a power of two, at least 1)
-  int64_t rows_pf; // store rows the prefill kernel sees (a ring wraps there)
-  int pf_cols;     // 4-bit store: columns staged for the prefill kernel, the first pf_cols segments
-                   // of that route taking one each and the others the split-K route; 0: the
-                   // prefill kernel reads the store itself, every segment its own column
-  int64_t grid[3];
+  // the split-K route's shapes: the first, and the one that the schedule may take instead (sk_choice)
+  SkShape sk[2];
+  int q4;             // a call over a 4-bit store: the fields below are read for those only
+  int sk_choice;
+  float sk_ratio;     // cost of a key for a unit of the second shape against that for 8 rows in the first
+  int pf_min_rows;    // least packed rows of a segment, and work of a call, of the prefill route
+  float pf_min_work;  // (kPrefillRows and kPrefillMinWork otherwise)
+  int lo_align;       // split-K units' key ranges begin at a multiple of this (a power of two)
+  int64_t rows_pf;    // store rows the prefill kernel sees (a ring wraps there)
+  int pf_cols;        // columns staged for the prefill kernel, the first pf_cols segments of that route
+                      // taking one each and the others the split-K route
+  int64_t grid[3]; // CTAs of the prefill route (the split-K route's are in sk)
   Workspace ws;
   int32_t* status_dev;
 };
@@ -242,8 +256,8 @@ __host__ __device__ inline bool sched_small_ok(int64_t T, int Hq, int Hkv, int S
 }
 
 // Kernel entry points (defined in their own translation units).
-const void* sched_kernel_ptr();
-const void* sched_small_kernel_ptr();  // calls with sched_small_ok
+const void* sched_kernel_ptr(bool q4);
+const void* sched_small_kernel_ptr(bool q4);  // calls with sched_small_ok
 // Launches the scheduler kernel that suits the call (one CTA of kSchedThreads threads).
 cudaError_t launch_sched(const SchedArgs& sa, cudaStream_t st);
 size_t sched_smem_bytes();  // dynamic shared memory of the scheduler kernel
@@ -251,7 +265,7 @@ const void* append_kernel_ptr();
 const void* clone_kernel_ptr();
 const void* splitk_kernel_ptr(int D);
 int splitk_smem_bytes(int D);
-const void* combine_kernel_ptr(int D);
+const void* combine_kernel_ptr(int D, bool q4);
 const void* combine_pair_kernel_ptr(int D);  // a CTA per (row, head) pair
 const void* prefill_kernel_ptr(int D);
 const void* prefill_pair_kernel_ptr(int D);  // D = 64, 128
@@ -303,7 +317,7 @@ __device__ __forceinline__ RowWin row_window(int i, int q_len, int kv_end, int c
 // sequence.
 struct PieceWalk {
   const Workspace* W;
-  int route;
+  int route, kind;  // kind: SkKind of the split-K route
   int64_t G;        // launched grid
   int64_t nphase;
   int64_t p;        // current phase
@@ -376,14 +390,23 @@ __host__ __device__ inline void key_tile(const KeyTiles& k, int64_t t, int bn, i
 // the mixed steps), so the split-K route's line counts 4 and 6 units per tile and 20 units
 // of lead (leads of 16 or 24 by rows measured no better).  Prefill tiles cost 1 and a prefill
 // piece 6 (about 4 us against 0.7 us per 128-key tile).
-__host__ __device__ __forceinline__ int64_t tile_cost(int route, int rows) {
-  return route == kRouteSplitk ? (rows > 16 ? 6 : 4) : 1;
+// The 4-bit store's split-K kernels have tiles of their own kind: the one for few rows turns a key into
+// operands again for every 8 rows of a unit, and the tensor-memory one takes 1.2 times as long over more
+// than 64 rows and starts a piece in the time of 4 tiles.  64 tokens over 16384 to 32768 keys beside a
+// 512-token chunk over 512, 32/8 heads, D = 128, all on the first: 674 us with the bf16 kernel's costs, 415 so.
+enum SkKind : int { kSkBf16 = 0, kSkQ4Few = 1, kSkQ4Tile = 2 };
+__host__ __device__ __forceinline__ int64_t tile_cost(int route, int rows, int kind = kSkBf16) {
+  if (route != kRouteSplitk) return 1;
+  return kind == kSkBf16 ? (rows > 16 ? 6 : 4) : kind == kSkQ4Few ? 4 * ((rows + 7) / 8) : (rows > 64 ? 5 : 4);
 }
-__host__ __device__ __forceinline__ int64_t lead_cost(int route) { return route == kRouteSplitk ? 20 : 6; }
+__host__ __device__ __forceinline__ int64_t lead_cost(int route, int kind = kSkBf16) {
+  return route != kRouteSplitk ? 6 : kind == kSkQ4Tile ? 16 : 20;
+}
 // CTAs that share a phase of Wp line units: at most one per costliest tile, so that every
 // CTA's share holds the start of a tile of each unit it crosses (nslots stays exact).
-__host__ __device__ __forceinline__ int64_t phase_ctas(int64_t G, int64_t Wp, int route) {
-  const int64_t g = Wp / (route == kRouteSplitk ? 6 : 1);
+__host__ __device__ __forceinline__ int64_t phase_ctas(int64_t G, int64_t Wp, int route, int kind = kSkBf16) {
+  // (divisions by constants)
+  const int64_t g = route != kRouteSplitk ? Wp : kind == kSkBf16 ? Wp / 6 : kind == kSkQ4Few ? Wp / (4 * (kSplitkRows / 8)) : Wp / 5;
   return g < 1 ? 1 : (g < G ? g : G);
 }
 // The tiles [ta, tb) of a unit whose first tile starts at line position k0 (nt tiles of tw
@@ -406,10 +429,11 @@ __host__ __device__ inline int64_t sk_owner(int64_t x, int64_t W, int64_t G) {
 // All loads here are independent, so they travel together: the header, phase 0's bounds
 // and this CTA's entry in phase 0 (read with the launched grid, which is the grid the
 // scheduler planned for; the entry is only used if the CTA works in phase 0).
-__device__ inline void walk_begin(PieceWalk& w, const Workspace& W, int route) {
+__device__ inline void walk_begin(PieceWalk& w, const Workspace& W, int route, int kind = kSkBf16) {
   const SchedHdr* h = W.hdr;
   w.W = &W;
   w.route = route;
+  w.kind = kind;
   w.G = gridDim.x;
   w.nphase = h->nphase[route];
   w.U = h->units[route];
@@ -436,11 +460,11 @@ __device__ inline bool walk_phase(PieceWalk& w) {
       const UnitRec& r = w.W->units[w.route][u];
       if (r.ntiles == 0) continue;
       w.t0 = r.tile_base;
-      w.t1 = r.tile_base + lead_cost(w.route) + (int64_t)r.ntiles * tile_cost(w.route, r.rows);
+      w.t1 = r.tile_base + lead_cost(w.route, w.kind) + (int64_t)r.ntiles * tile_cost(w.route, r.rows, w.kind);
       w.u = u;
       return true;
     }
-    const int64_t Gp = phase_ctas(w.G, Wp, w.route);
+    const int64_t Gp = phase_ctas(w.G, Wp, w.route, w.kind);
     if ((int64_t)blockIdx.x >= Gp) continue;
     w.t0 = b0 + sk_start(blockIdx.x, Wp, Gp);
     w.t1 = b0 + sk_start(blockIdx.x + 1, Wp, Gp);
@@ -457,8 +481,8 @@ __device__ inline bool walk_next(PieceWalk& w, UnitRec& ur, int64_t& ta, int64_t
   for (;;) {
     while (w.t0 < w.t1 && w.u < w.U) {
       const UnitRec r = w.W->units[w.route][w.u];
-      const int64_t tw = tile_cost(w.route, r.rows);
-      const int64_t k0 = r.tile_base + lead_cost(w.route), k1 = k0 + r.ntiles * tw;  // its key tiles
+      const int64_t tw = tile_cost(w.route, r.rows, w.kind);
+      const int64_t k0 = r.tile_base + lead_cost(w.route, w.kind), k1 = k0 + r.ntiles * tw;  // its key tiles
       if (r.ntiles == 0 || w.t0 >= k1) {
         ++w.u;
         continue;

@@ -60,7 +60,7 @@ sdpa_status static_setup(StaticDev* out) {
     }
     if (cudaDeviceGetAttribute(&sd.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
       return static_fail(SDPA_ERR_CUDA, "SM count query failed");
-    if (cudaFuncSetAttribute(sched_kernel_ptr(), cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(sched_kernel_ptr(false), cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)sched_smem_bytes()) != cudaSuccess)
       return static_fail(SDPA_ERR_CUDA, "scheduler kernel setup failed");
     const int Ds[3] = {64, 128, 256};
@@ -135,14 +135,8 @@ extern "C" sdpa_status sdpa_varlen_splitk_static(
   sa.policy = SDPA_ROUTE_SPLITK;
   sa.prefill_ok = 0;
   sa.tile_pf = kPrefillTile;
-  sa.pf_min_rows = kPrefillRows;
-  sa.pf_min_work = kPrefillMinWork;
-  sa.sk_rows = kSplitkRows;
-  sa.sk_tile = kSplitkTile;
-  sa.lo_align = 1;
-  sa.rows_pf = rows;
+  sa.sk[0] = {kSplitkRows, kSplitkTile, kSkBf16, grid};
   sa.grid[0] = 0;
-  sa.grid[1] = grid;
   sa.grid[2] = 0;
   sa.ws = W;
   sa.status_dev = status_dev;
@@ -166,7 +160,6 @@ extern "C" sdpa_status sdpa_varlen_splitk_static(
   aa.o_rs = o_row_stride;
   aa.o_hs = o_head_stride;
   aa.T = T;
-  aa.sk_rows = kSplitkRows;
   aa.ws = W;
   aa.status_dev = status_dev;
 
@@ -181,7 +174,7 @@ extern "C" sdpa_status sdpa_varlen_splitk_static(
   if (e == cudaSuccess && T > 0) {
     void* args[] = {(void*)&aa};
     const int64_t blocks = std::min<int64_t>((T * Hq * 32 + 255) / 256, 8 * (int64_t)sd.sms);
-    e = cudaLaunchKernel(combine_kernel_ptr(D), dim3((unsigned)blocks), dim3(256), args, 0, s);
+    e = cudaLaunchKernel(combine_kernel_ptr(D, false), dim3((unsigned)blocks), dim3(256), args, 0, s);
   }
   if (e != cudaSuccess) {
     char msg[256];

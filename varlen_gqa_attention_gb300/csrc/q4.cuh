@@ -127,6 +127,7 @@ sdpa_status check_q4_store(const Q4Store& q4, int64_t rows);
 struct Q4AttnArgs {
   AttnArgs a;  // k, v unused
   Q4Store st;
+  int choice;  // both split-K kernels are launched, and the schedule is one's (hdr->sk_rows)
 };
 
 // The keys and values of the prefill route's segments, brought to bf16 for the tensor-memory kernel:

@@ -399,7 +399,7 @@ __device__ __forceinline__ void q4_load(const Q4AttnArgs& G, char* ring, char* s
   const AttnArgs& A = G.a;
   const int lane = threadIdx.x & 31;
   PieceWalk wk;
-  walk_begin(wk, A.ws, kRouteSplitk);
+  walk_begin(wk, A.ws, kRouteSplitk, kSkQ4Few);
   UnitRec ur;
   int64_t ta, tb;
   uint32_t it = 0, n = 0;
@@ -500,6 +500,7 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Cfg<D>::kPerSm) sdpa_q4_splitk_k
   __syncthreads();
   griddep_wait();  // the scheduler's output (and the prefill kernel's end)
   griddep_launch();
+  if (G.choice && A.ws.hdr->sk_rows != kSplitkRows) return;
 
   if (threadIdx.x >= kQ4Consumers) {
     q4_load<D, S>(G, ring, sQ, pieces, full, empty, qfull, qempty, &s_abort);

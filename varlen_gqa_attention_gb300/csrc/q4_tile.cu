@@ -109,9 +109,10 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) sdpa_q4_tile_kernel(Q4AttnA
 
   griddep_wait();  // the scheduler's output (and the prefill kernel's end)
   griddep_launch();
+  if (G.choice && A.ws.hdr->sk_rows != kQ4TileRows) return;
   {
     PieceWalk probe;  // nothing to do for this CTA: leave before any set-up
-    walk_begin(probe, A.ws, kRouteSplitk);
+    walk_begin(probe, A.ws, kRouteSplitk, kSkQ4Tile);
     if (!walk_phase(probe)) return;
   }
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) sdpa_q4_tile_kernel(Q4AttnA
   if (warp == W_LOAD) {
     // ---------------------------------------------------------------- loading warp
     PieceWalk wk;
-    walk_begin(wk, A.ws, kRouteSplitk);
+    walk_begin(wk, A.ws, kRouteSplitk, kSkQ4Tile);
     UnitRec ur;
     int64_t ta, tb;
     uint32_t it = 0;

@@ -147,11 +147,33 @@ __device__ __forceinline__ void load_seg(const SchedArgs& A, int s, int32_t* seg
   }
 }
 
-__device__ __forceinline__ int rows_per_unit(const SchedArgs& A, int route) {
-  return route == kRoutePrefill ? prefill_unit_rows(A.D) : A.sk_rows;
+// What only the 4-bit store's calls set; the others' kernels have it as constants.
+template <bool Q4>
+__device__ __forceinline__ int pf_cols(const SchedArgs& A) { return Q4 ? A.pf_cols : 0; }
+template <bool Q4>
+__device__ __forceinline__ int lo_align(const SchedArgs& A) { return Q4 ? A.lo_align : 1; }
+template <bool Q4>
+__device__ __forceinline__ int64_t rows_pf(const SchedArgs& A) { return Q4 ? A.rows_pf : A.rows; }
+template <bool Q4>
+__device__ __forceinline__ int pf_min_rows(const SchedArgs& A) { return Q4 ? A.pf_min_rows : kPrefillRows; }
+template <bool Q4>
+__device__ __forceinline__ float pf_min_work(const SchedArgs& A) { return Q4 ? A.pf_min_work : kPrefillMinWork; }
+template <bool Q4>
+__device__ __forceinline__ bool sk_choice(const SchedArgs& A) { return Q4 && A.sk_choice; }
+template <bool Q4>
+__device__ __forceinline__ SkShape first_shape(const SchedArgs& A) {
+  if constexpr (Q4) return A.sk[0];
+  return {kSplitkRows, kSplitkTile, kSkBf16, A.sk[0].grid};
 }
-__device__ __forceinline__ int tile_len(const SchedArgs& A, int route) {
-  return route == kRoutePrefill ? A.tile_pf : A.sk_tile;
+
+__device__ __forceinline__ int rows_per_unit(const SchedArgs& A, const SkShape& k, int route) {
+  return route == kRoutePrefill ? prefill_unit_rows(A.D) : k.rows;
+}
+__device__ __forceinline__ int tile_len(const SchedArgs& A, const SkShape& k, int route) {
+  return route == kRoutePrefill ? A.tile_pf : k.tile;
+}
+__device__ __forceinline__ int64_t grid_of(const SchedArgs& A, const SkShape& k, int route) {
+  return route == kRouteSplitk ? k.grid : A.grid[route];
 }
 
 // Route of a live segment.  The prefill kernel takes segments that fill at least one
@@ -159,21 +181,33 @@ __device__ __forceinline__ int tile_len(const SchedArgs& A, int route) {
 // wraps), when the call holds enough such work to pay for that kernel's fixed cost (`big`:
 // the segments' prefill_work sums to at least pf_min_work); everything else, and
 // everything when the prefill kernel is unusable, goes to the split-K kernel.
+template <bool Q4>
 __device__ __forceinline__ int route_of(const SchedArgs& A, int32_t q_len, bool big) {
   const int64_t R = (int64_t)q_len * A.group;
   if (A.policy == SDPA_ROUTE_SPLITK || !A.prefill_ok) return kRouteSplitk;
   if (A.policy == SDPA_ROUTE_PREFILL) return kRoutePrefill;
-  return R >= A.pf_min_rows && big ? kRoutePrefill : kRouteSplitk;
+  return R >= pf_min_rows<Q4>(A) && big ? kRoutePrefill : kRouteSplitk;
 }
 // A live segment's share of the prefill route's work measure: packed rows * needed key
 // span * Hkv * D when it has pf_min_rows of them, else 0 (in fp32: no overflow, ample for a
 // threshold, and fast; fp64 runs at a small fraction of the fp32 rate here).
+template <bool Q4>
 __device__ __forceinline__ float prefill_work(const SchedArgs& A, int32_t q_len, int32_t kv_end, int32_t window) {
   const int64_t R = (int64_t)q_len * A.group;
-  if (R < A.pf_min_rows) return 0.f;
+  if (R < pf_min_rows<Q4>(A)) return 0.f;
   int64_t span = kv_end;
   if (window > 0) span = min(span, (int64_t)q_len + window - 1);
   return (float)R * (float)span * (float)A.Hkv * (float)A.D;
+}
+
+// What a split-K segment adds to the cost of the second shape over the first: a key costs 1 for every 8 packed
+// rows there, which turn it into operands again, and sk_ratio for every unit here.
+__device__ __forceinline__ float sk_cost(const SchedArgs& A, int32_t q_len, int32_t kv_end, int32_t window) {
+  const int64_t R = (int64_t)q_len * A.group;
+  int64_t span = kv_end;
+  if (window > 0) span = min(span, (int64_t)q_len + window - 1);
+  const int64_t n0 = (R + 7) / 8, n1 = (R + A.sk[1].rows - 1) / A.sk[1].rows;
+  return ((float)n1 * A.sk_ratio - (float)n0) * (float)span;
 }
 
 // A segment's entry as the unit builder reads it.
@@ -186,16 +220,17 @@ struct SegView {
 // placeholders and its key tiles; 0 when no key is visible); *reuse: the K/V bytes its
 // (segment, KV head) group reads again, counted once, on the group's last unit, and only for
 // groups of several units (phases are cut on these).
-__device__ __forceinline__ UnitRec make_unit(const SchedArgs& A, int s, const SegView& g, int q, int64_t uq,
-                                             int64_t* span, int64_t* reuse) {
-  const int rpu = rows_per_unit(A, q), tl = tile_len(A, q);
+template <bool Q4>
+__device__ __forceinline__ UnitRec make_unit(const SchedArgs& A, const SkShape& k, int s, const SegView& g, int q,
+                                             int64_t uq, int64_t* span, int64_t* reuse) {
+  const int rpu = rows_per_unit(A, k, q), tl = tile_len(A, k, q);
   UnitRec ur;
   const int64_t j = uq - g.ubase;
   const int64_t jh = udiv(j, g.nrb);
   ur.seg = s;
   ur.q_start = g.q_start;
   ur.q_len = g.q_len;
-  ur.col = q == kRoutePrefill && A.pf_cols > 0 ? g.pf_col : g.col;
+  ur.col = q == kRoutePrefill && pf_cols<Q4>(A) > 0 ? g.pf_col : g.col;
   ur.kv_end = g.kv_end;
   ur.causal = g.causal;
   ur.window = g.window;
@@ -210,10 +245,10 @@ __device__ __forceinline__ UnitRec make_unit(const SchedArgs& A, int s, const Se
   ur.lo = w0.lo;  // lo and hi grow with the query row
   ur.hi = max(w1.hi, w0.lo);
   // (keys added below a unit's first are masked like any other that a row does not see)
-  if (q == kRouteSplitk && ur.hi > ur.lo) ur.lo &= -A.lo_align;
+  if (q == kRouteSplitk && ur.hi > ur.lo) ur.lo &= -lo_align<Q4>(A);
   // key tiles: the prefill kernel's stop at a ring wrap (two TMA ranges), the split-K
   // kernel's wrap per row
-  const int64_t nt = q == kRoutePrefill ? key_tiles(ur.lo, ur.hi, A.rows_pf, tl).n
+  const int64_t nt = q == kRoutePrefill ? key_tiles(ur.lo, ur.hi, rows_pf<Q4>(A), tl).n
                                         : (ur.hi > ur.lo ? udiv((int64_t)(ur.hi - ur.lo) + tl - 1, tl) : 0);
   ur.nslots = 0;
   ur.g_first = 0;
@@ -221,7 +256,7 @@ __device__ __forceinline__ UnitRec make_unit(const SchedArgs& A, int s, const Se
   ur.phase = 0;
   ur.tile_base = 0;
   ur.slot_base = 0;
-  *span = nt > 0 ? nt * tile_cost(q, ur.rows) + lead_cost(q) : 0;
+  *span = nt > 0 ? nt * tile_cost(q, ur.rows, k.kind) + lead_cost(q, k.kind) : 0;
   *reuse = 0;
   if (g.nrb >= 2 && ur.rb == g.nrb - 1) {
     int64_t sp = g.kv_end;
@@ -251,11 +286,11 @@ __device__ __forceinline__ bool phase_is_aligned(const int64_t* pb, const int64_
   return Up > 0 && Up <= G && (int64_t)pmax[p] * G <= Wp + M * G;
 }
 
-__device__ __forceinline__ int64_t place_unit(const SchedArgs& A, UnitRec& ur, int q, int64_t uq,
+__device__ __forceinline__ int64_t place_unit(const SchedArgs& A, const SkShape& k, UnitRec& ur, int q, int64_t uq,
                                               const int64_t* pb, const int64_t* pu0, bool aligned) {
   const int64_t nt = ur.ntiles;
   if (nt <= 0) return 0;
-  const int64_t G = A.grid[q];
+  const int64_t G = grid_of(A, k, q);
   if (aligned) {  // CTA g of the phase takes its unit g whole and writes `out` itself
     const int64_t g = uq - pu0[ur.phase];
     ur.g_first = (int32_t)g;
@@ -263,11 +298,11 @@ __device__ __forceinline__ int64_t place_unit(const SchedArgs& A, UnitRec& ur, i
     A.ws.first_unit[q][ur.phase * G + g] = (int32_t)uq;
     return 0;
   }
-  const int64_t tw = tile_cost(q, ur.rows);
+  const int64_t tw = tile_cost(q, ur.rows, k.kind);
   const int64_t b0 = pb[ur.phase];
   const int64_t Wp = pb[ur.phase + 1] - b0;
-  const int64_t Gp = phase_ctas(G, Wp, q);
-  const int64_t k0 = ur.tile_base + lead_cost(q) - b0;  // the key tiles, phase-relative
+  const int64_t Gp = phase_ctas(G, Wp, q, k.kind);
+  const int64_t k0 = ur.tile_base + lead_cost(q, k.kind) - b0;  // the key tiles, phase-relative
   const int64_t g0 = sk_owner(k0, Wp, Gp);
   const int64_t g1 = sk_owner(k0 + (nt - 1) * tw, Wp, Gp);  // the owners of the first and last tile starts
   ur.g_first = (int32_t)g0;
@@ -292,6 +327,7 @@ constexpr int kUnitCache = 1024;
 constexpr size_t kSchedSmem = (size_t)kSegCache * (16 + 8 + 8 + 8 + 4 + 4 + 4) + (size_t)kRowCache * 4 +
                               (size_t)kUnitCache * sizeof(UnitRec);
 
+template <bool Q4>
 __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_kernel(SchedArgs A) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ int64_t sh[4 * 32];
@@ -325,6 +361,7 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_kernel(SchedArgs A) 
   };
   auto bits_of = [&](int s) -> int32_t { return cached ? c_bits[s] : W.segs[s].bits; };
 
+  SkShape sk = first_shape<Q4>(A);
   {
     griddep_launch();  // the attention kernels may start launching; they wait for this grid
     if (threadIdx.x == 0) {
@@ -392,16 +429,26 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_kernel(SchedArgs A) 
     for (int64_t s = sa; s < sb; ++s) {
       const int4 g = seg_of((int)s);
       if (bits_of((int)s) == 0 && !flag[s] && g.y > 0)
-        pw += prefill_work(A, g.y, g.w, cached ? c_mode[s].y : W.segs[s].window);
+        pw += prefill_work<Q4>(A, g.y, g.w, cached ? c_mode[s].y : W.segs[s].window);
     }
-    const bool big = block_sum(pw, s_fsum) >= A.pf_min_work;
+    const bool big = block_sum(pw, s_fsum) >= pf_min_work<Q4>(A);
+    if (sk_choice<Q4>(A)) {
+      float more = 0.f;
+      for (int64_t s = sa; s < sb; ++s) {
+        const int4 g = seg_of((int)s);
+        if (bits_of((int)s) == 0 && !flag[s] && g.y > 0 && route_of<Q4>(A, g.y, big) == kRouteSplitk)
+          more += sk_cost(A, g.y, g.w, cached ? c_mode[s].y : W.segs[s].window);
+      }
+      __syncthreads();  // (s_fsum is read)
+      if (block_sum(more, s_fsum) < 0.f) sk = A.sk[1];
+    }
     // staged columns go to the first segments of the prefill route, in segment order
     int64_t pf[1] = {0};
-    if (A.pf_cols > 0) {
+    if (pf_cols<Q4>(A) > 0) {
       int64_t pf_all[1];
       for (int64_t s = sa; s < sb; ++s) {
         const int4 g = seg_of((int)s);
-        pf[0] += bits_of((int)s) == 0 && !flag[s] && g.y > 0 && route_of(A, g.y, big) == kRoutePrefill;
+        pf[0] += bits_of((int)s) == 0 && !flag[s] && g.y > 0 && route_of<Q4>(A, g.y, big) == kRoutePrefill;
       }
       block_scan<1>(pf, pf_all, sh);
     }
@@ -414,12 +461,12 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_kernel(SchedArgs A) 
       int route = kRouteNone, nrb = 0;
       if (bits == 0 && !fl && g.y > 0) {
         const int64_t R = (int64_t)g.y * A.group;
-        route = route_of(A, g.y, big);
-        if (A.pf_cols > 0 && route == kRoutePrefill) {
-          if (pf[0] >= A.pf_cols) route = kRouteSplitk;
+        route = route_of<Q4>(A, g.y, big);
+        if (pf_cols<Q4>(A) > 0 && route == kRoutePrefill) {
+          if (pf[0] >= pf_cols<Q4>(A)) route = kRouteSplitk;
           (cached ? c_pf[s] : W.segs[s].pf_col) = (int32_t)pf[0]++;
         }
-        const int rpu = rows_per_unit(A, route);
+        const int rpu = rows_per_unit(A, sk, route);
         nrb = (int)udiv(R + rpu - 1, rpu);
         if (route == kRouteSplitk) n1 += (int64_t)A.Hkv * nrb; else n2 += (int64_t)A.Hkv * nrb;
         nrows += g.y;
@@ -512,7 +559,7 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_kernel(SchedArgs A) 
       const int64_t uq = q == 1 ? u : u - U1;
       const int s = owner(q, uq);
       int64_t span, reuse;
-      UnitRec ur = make_unit(A, s, view_of(s, q), q, uq, &span, &reuse);
+      UnitRec ur = make_unit<Q4>(A, sk, s, view_of(s, q), q, uq, &span, &reuse);
       if (ur.ntiles == 0) s_work = 1;  // rows of a unit with no keys: zeroed by the combine pass
       if (q == kRouteSplitk) W.unit_done[uq] = 0;
       ur.tile_base = span;
@@ -557,7 +604,7 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_kernel(SchedArgs A) 
         s_pu0[q][k] = uq;
       }
       if (ur.ntiles > 0)
-        atomicMax(&s_pmax[q][cp], (int32_t)(ur.ntiles * tile_cost(q, ur.rows) + lead_cost(q)));
+        atomicMax(&s_pmax[q][cp], (int32_t)(ur.ntiles * tile_cost(q, ur.rows, sk.kind) + lead_cost(q, sk.kind)));
     }
     if (threadIdx.x < 2) {
       const int q = 1 + threadIdx.x;
@@ -577,8 +624,8 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_kernel(SchedArgs A) 
       const int q = u < U1 ? 1 : 2;
       const int64_t uq = q == 1 ? u : u - U1;
       UnitRec& ur = unit_at(u);
-      const int64_t pr = place_unit(A, ur, q, uq, s_pb[q], s_pu0[q],
-                                    phase_is_aligned(s_pb[q], s_pu0[q], s_pmax[q], ur.phase, A.grid[q], q));
+      const int64_t pr = place_unit(A, sk, ur, q, uq, s_pb[q], s_pu0[q],
+                                    phase_is_aligned(s_pb[q], s_pu0[q], s_pmax[q], ur.phase, grid_of(A, sk, q), q));
       if (ur.nslots > 1) s_work = 1;  // split units the combine pass merges
       (q == 1 ? p1 : p2) += pr;
     }
@@ -613,7 +660,7 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_kernel(SchedArgs A) 
       const int4 c = c_seg[s];
       SegRec r;
       r.q_start = c.x; r.q_len = c.y; r.col = c.z; r.kv_end = c.w;
-      r.route = c_rn[s].x; r.nrb = c_rn[s].y; r.bits = c_bits[s]; r.pf_col = c_pf[s];
+      r.route = c_rn[s].x; r.nrb = c_rn[s].y; r.bits = c_bits[s]; r.pf_col = Q4 ? c_pf[s] : 0;
       r.ubase[0] = 0; r.ubase[1] = c_ub[s].x; r.ubase[2] = c_ub[s].y; r.ubase[3] = 0;
       r.causal = c_mode[s].x; r.window = c_mode[s].y;
       r.pad2[0] = r.pad2[1] = 0;
@@ -654,15 +701,16 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_kernel(SchedArgs A) 
     const int q = 1 + threadIdx.x;
     int64_t am = 0;
     for (int k = 0; k < s_np[q]; ++k)
-      if (phase_is_aligned(s_pb[q], s_pu0[q], s_pmax[q], k, A.grid[q], q)) am |= (int64_t)1 << k;
+      if (phase_is_aligned(s_pb[q], s_pu0[q], s_pmax[q], k, grid_of(A, sk, q), q)) am |= (int64_t)1 << k;
     W.hdr->aligned[q] = am;
     W.hdr->tiles[q] = s_pb[q][s_np[q]];
     W.hdr->units[q] = s_U[q];
-    W.hdr->grid[q] = A.grid[q];
+    W.hdr->grid[q] = grid_of(A, sk, q);
     W.hdr->nphase[q] = s_np[q];
   }
   if (threadIdx.x == 0) {
     W.hdr->combine_work = s_work;
+    W.hdr->sk_rows = sk.rows;
     W.hdr->status = s_status;
     if (A.status_dev && s_status) atomicOr(A.status_dev, s_status);
   }
@@ -682,6 +730,7 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_kernel(SchedArgs A) 
 //     at a warp boundary, so a warp holds one route) with one barrier each, and one barrier
 //     for the phase bases, which each thread writes for the next unit of its route from its
 //     own prefix and span.
+template <bool Q4>
 __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_small_kernel(SchedArgs A) {
   __shared__ int4 c_seg[kSmallSegs];   // (q_start, q_len, col, kv_end)
   __shared__ int2 c_mode[kSmallSegs];  // (causal, window)
@@ -692,7 +741,7 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_small_kernel(SchedAr
   __shared__ int64_t s_pb[3][kMaxPhases + 1];
   __shared__ int64_t s_pu0[3][kMaxPhases + 1];  // first unit of each phase; [np] = units
   __shared__ int32_t s_pmax[3][kMaxPhases];      // longest unit span of each phase
-  __shared__ int32_t s_U[3], s_np[3], s_status, s_work;
+  __shared__ int32_t s_U[3], s_np[3], s_status, s_work, s_sk;
   const Workspace& W = A.ws;
   const int S = A.S;
   const int T = (int)A.T;
@@ -728,17 +777,25 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_small_kernel(SchedAr
       ov = ov && ok;
     }
     const bool live = ok && !ov;
-    float pw = live ? prefill_work(A, g[1], g[3], md.y) : 0.f;
+    float pw = live ? prefill_work<Q4>(A, g[1], g[3], md.y) : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) pw += __shfl_xor_sync(kAll, pw, o);
-    int route = live ? route_of(A, g[1], pw >= A.pf_min_work) : kRouteNone, nrb = 0;
+    int route = live ? route_of<Q4>(A, g[1], pw >= pf_min_work<Q4>(A)) : kRouteNone, nrb = 0;
     int pf_col = 0;
-    if (A.pf_cols > 0) {  // staged columns go to the first segments of the prefill route
+    SkShape sk = first_shape<Q4>(A);
+    if (sk_choice<Q4>(A)) {
+      float more = route == kRouteSplitk ? sk_cost(A, g[1], g[3], md.y) : 0.f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) more += __shfl_xor_sync(kAll, more, o);
+      if (more < 0.f) sk = A.sk[1];
+      if (lane == 0) s_sk = more < 0.f;
+    }
+    if (pf_cols<Q4>(A) > 0) {  // staged columns go to the first segments of the prefill route
       pf_col = __popc(__ballot_sync(kAll, route == kRoutePrefill) & ((1u << lane) - 1u));
-      if (route == kRoutePrefill && pf_col >= A.pf_cols) route = kRouteSplitk;
+      if (route == kRoutePrefill && pf_col >= pf_cols<Q4>(A)) route = kRouteSplitk;
     }
     if (live) {
-      const int rpu = rows_per_unit(A, route);
+      const int rpu = rows_per_unit(A, sk, route);
       nrb = (int)(((uint32_t)g[1] * (uint32_t)A.group + rpu - 1) / (uint32_t)rpu);
     }
     const int32_t n1 = route == kRouteSplitk ? A.Hkv * nrb : 0, n2 = route == kRoutePrefill ? A.Hkv * nrb : 0;
@@ -779,6 +836,8 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_small_kernel(SchedAr
     for (int t = threadIdx.x - 32; t < T; t += blockDim.x - 32) W.row_info[t] = make_int4(kRouteNone, 0, 0, 0);
   }
   __syncthreads();  // (also orders the row records above before the ones below)
+  SkShape sk = first_shape<Q4>(A);
+  if (sk_choice<Q4>(A) && s_sk) sk = A.sk[1];
 
   // each live segment's row records
   for (int s = warp; s < S; s += nw) {
@@ -817,7 +876,7 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_small_kernel(SchedAr
     gv.causal = c_mode[s].x;
     gv.window = c_mode[s].y;
     gv.pf_col = c_pf[s];
-    ur = make_unit(A, s, gv, q, uq, &span, &reuse);
+    ur = make_unit<Q4>(A, sk, s, gv, q, uq, &span, &reuse);
     if (ur.ntiles == 0) s_work = 1;  // rows of a unit with no keys: zeroed by the combine pass
     if (q == kRouteSplitk) W.unit_done[uq] = 0;
   }
@@ -852,8 +911,8 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_small_kernel(SchedAr
   __syncthreads();
   int64_t pv[1] = {0}, ptot[1];
   if (q != 0) {
-    pv[0] = place_unit(A, ur, q, uq, s_pb[q], s_pu0[q],
-                       phase_is_aligned(s_pb[q], s_pu0[q], s_pmax[q], ur.phase, A.grid[q], q));
+    pv[0] = place_unit(A, sk, ur, q, uq, s_pb[q], s_pu0[q],
+                       phase_is_aligned(s_pb[q], s_pu0[q], s_pmax[q], ur.phase, grid_of(A, sk, q), q));
     if (ur.nslots > 1) s_work = 1;  // split units the combine pass merges
   }
   route_scan<1>(pv, ptot, sh + 2 * 32, wroute);  // (its barrier also publishes s_work)
@@ -874,28 +933,33 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_small_kernel(SchedAr
     const int hq = 1 + i;
     int64_t am = 0;
     for (int k = 0; k < s_np[hq]; ++k)
-      if (phase_is_aligned(s_pb[hq], s_pu0[hq], s_pmax[hq], k, A.grid[hq], hq)) am |= (int64_t)1 << k;
+      if (phase_is_aligned(s_pb[hq], s_pu0[hq], s_pmax[hq], k, grid_of(A, sk, hq), hq)) am |= (int64_t)1 << k;
     W.hdr->aligned[hq] = am;
     W.hdr->tiles[hq] = s_pb[hq][s_np[hq]];
     W.hdr->units[hq] = s_U[hq];
-    W.hdr->grid[hq] = A.grid[hq];
+    W.hdr->grid[hq] = grid_of(A, sk, hq);
     W.hdr->nphase[hq] = s_np[hq];
   }
   if (i == 0) {
     W.hdr->combine_work = s_work;
+    W.hdr->sk_rows = sk.rows;
     W.hdr->status = s_status;
     if (A.status_dev && s_status) atomicOr(A.status_dev, s_status);
   }
 }
 
-const void* sched_kernel_ptr() { return (const void*)sdpa_sched_kernel; }
-const void* sched_small_kernel_ptr() { return (const void*)sdpa_sched_small_kernel; }
+const void* sched_kernel_ptr(bool q4) {
+  return q4 ? (const void*)sdpa_sched_kernel<true> : (const void*)sdpa_sched_kernel<false>;
+}
+const void* sched_small_kernel_ptr(bool q4) {
+  return q4 ? (const void*)sdpa_sched_small_kernel<true> : (const void*)sdpa_sched_small_kernel<false>;
+}
 
 cudaError_t launch_sched(const SchedArgs& sa, cudaStream_t st) {
   void* args[] = {(void*)&sa};
   if (sched_small_ok(sa.T, sa.group * sa.Hkv, sa.Hkv, sa.S))
-    return cudaLaunchKernel(sched_small_kernel_ptr(), dim3(1), dim3(kSchedThreads), args, 0, st);
-  return cudaLaunchKernel(sched_kernel_ptr(), dim3(1), dim3(kSchedThreads), args, sched_smem_bytes(), st);
+    return cudaLaunchKernel(sched_small_kernel_ptr(sa.q4), dim3(1), dim3(kSchedThreads), args, 0, st);
+  return cudaLaunchKernel(sched_kernel_ptr(sa.q4), dim3(1), dim3(kSchedThreads), args, sched_smem_bytes(), st);
 }
 size_t sched_smem_bytes() { return kSchedSmem; }
 
