@@ -182,10 +182,10 @@ def test_staged_columns_follow_the_longest_segment():
     assert staged(64, 64) == 0               # single tokens
     assert staged(94, 64) == 0               # a segment of 31 rows among them (124 packed)
     assert staged(95, 64) == 2               # of 32: the rows that fill a tile, twice over
-    assert staged(64 + 300, 64) == 1         # more than 16 packed rows on average: 1024 of a segment
-    assert staged(64 + 150, 16) == 0
+    assert staged(64 + 300, 64) == 2         # more than 16 packed rows on average: 512 of a segment
+    assert staged(15 + 127, 16) == 0 and staged(15 + 128, 16) == 1
     assert staged(256, 1) == 1 and staged(255, 1) == 0
-    assert staged(8192, 4) == 4 and staged(1 << 16, 64) == 16  # 2 GiB of them
+    assert staged(8192, 4) == 4 and staged(1 << 16, 64) == 16  # of all, and of 2 GiB of them
 
 
 # ------------------------------------------------------------------------------- the Python entries

@@ -265,13 +265,18 @@ static cudaError_t launch_k(const void* f, unsigned grid, unsigned block, void**
 }
 
 // The prefill route over a 4-bit store: its columns are staged first, which many rows have to pay for, and the
-// route it competes with is the tensor-memory kernel of q4_tile.cu at D <= 128.  Split-K / prefill route, 32/8
+// route it competes with is the tensor-memory kernel of q4_tile.cu, where that one runs.  Split-K / prefill, 32/8
 // heads, D = 128, in us: one segment over 4096 keys, 128 rows a head 37 / 39, 256 rows 48 / 47, 512 rows
 // 69 / 65, 2048 rows 160 / 135; 128 rows over 32768 keys 113 / 146, 512 rows 316 / 266; four segments of 128 rows
 // over 4096 keys 82 / 98.  At D = 256 the split-K kernel converts a key again for every 8 rows: 64 rows a head
 // over 4096 keys 76 / 45.
-// So the bf16 entry's thresholds hold where that kernel would do without the tensor-memory one.
-static int q4_prefill_min_rows(Q4Split sp) { return sp == Q4Split::kFew ? kPrefillRows : 1024; }
+// So the bf16 entry's thresholds hold where the tensor-memory one is not launched, and 512 rows where the
+// schedule takes the other one: 64 tokens over 16384 to 32768 keys beside 250 over 32768 842 / 579 us (fewer
+// rows do not pay for the launches when there are none, 5 us).
+constexpr int kQ4TilePrefillRows = 1024;
+static int q4_prefill_min_rows(Q4Split sp) {
+  return sp == Q4Split::kFew ? kPrefillRows : sp == Q4Split::kEither ? 512 : kQ4TilePrefillRows;
+}
 static float q4_prefill_min_work(Q4Split sp) { return sp == Q4Split::kFew ? kPrefillMinWork : 4 * kPrefillMinWork; }
 // Packed rows of a call's longest segment when none is empty.
 static int64_t q4_longest(int64_t T, int group, int S) { return std::max<int64_t>(1, T - std::max(S, 1) + 1) * group; }
@@ -459,6 +464,7 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
   const bool group_fits = group <= kPrefillRows && (kPrefillRows % group) == 0;
   sa.tile_pf = prefill_tile_keys(D);
   sa.pf_min_rows = q4 ? q4_prefill_min_rows(sp) : kPrefillRows;
+  sa.pf_tile_rows = kQ4TilePrefillRows;
   sa.pf_min_work = q4 ? q4_prefill_min_work(sp) : kPrefillMinWork;
   sa.q4 = q4 != nullptr;
   sa.sk[0] = sp == Q4Split::kTile ? tile : few;

@@ -232,8 +232,9 @@ struct SchedArgs {
   int q4;             // a call over a 4-bit store: the fields below are read for those only
   int sk_choice;
   float sk_ratio;     // cost of a key for a unit of the second shape against that for 8 rows in the first
-  int pf_min_rows;    // least packed rows of a segment, and work of a call, of the prefill route
-  float pf_min_work;  // (kPrefillRows and kPrefillMinWork otherwise)
+  int pf_min_rows;    // least packed rows of a segment of the prefill route (otherwise kPrefillRows)
+  int pf_tile_rows;   // those when the schedule has taken the second shape
+  float pf_min_work;  // least work of a call of the prefill route (otherwise kPrefillMinWork)
   int lo_align;       // split-K units' key ranges begin at a multiple of this (a power of two)
   int64_t rows_pf;    // store rows the prefill kernel sees (a ring wraps there)
   int pf_cols;        // columns staged for the prefill kernel, the first pf_cols segments of that route

@@ -181,32 +181,36 @@ __device__ __forceinline__ int64_t grid_of(const SchedArgs& A, const SkShape& k,
 // wraps), when the call holds enough such work to pay for that kernel's fixed cost (`big`:
 // the segments' prefill_work sums to at least pf_min_work); everything else, and
 // everything when the prefill kernel is unusable, goes to the split-K kernel.
-template <bool Q4>
-__device__ __forceinline__ int route_of(const SchedArgs& A, int32_t q_len, bool big) {
+__device__ __forceinline__ int route_of(const SchedArgs& A, int32_t q_len, bool big, int pf_rows) {
   const int64_t R = (int64_t)q_len * A.group;
   if (A.policy == SDPA_ROUTE_SPLITK || !A.prefill_ok) return kRouteSplitk;
   if (A.policy == SDPA_ROUTE_PREFILL) return kRoutePrefill;
-  return R >= pf_min_rows<Q4>(A) && big ? kRoutePrefill : kRouteSplitk;
+  return R >= pf_rows && big ? kRoutePrefill : kRouteSplitk;
 }
 // A live segment's share of the prefill route's work measure: packed rows * needed key
-// span * Hkv * D when it has pf_min_rows of them, else 0 (in fp32: no overflow, ample for a
+// span * Hkv * D when it has pf_rows of them, else 0 (in fp32: no overflow, ample for a
 // threshold, and fast; fp64 runs at a small fraction of the fp32 rate here).
-template <bool Q4>
-__device__ __forceinline__ float prefill_work(const SchedArgs& A, int32_t q_len, int32_t kv_end, int32_t window) {
+__device__ __forceinline__ float prefill_work(const SchedArgs& A, int32_t q_len, int32_t kv_end, int32_t window,
+                                              int pf_rows) {
   const int64_t R = (int64_t)q_len * A.group;
-  if (R < pf_min_rows<Q4>(A)) return 0.f;
+  if (R < pf_rows) return 0.f;
   int64_t span = kv_end;
   if (window > 0) span = min(span, (int64_t)q_len + window - 1);
   return (float)R * (float)span * (float)A.Hkv * (float)A.D;
 }
 
-// What a split-K segment adds to the cost of the second shape over the first: a key costs 1 for every 8 packed
-// rows there, which turn it into operands again, and sk_ratio for every unit here.
+// What a segment adds to the cost of the second shape over the first: a key costs 1 for every 8 packed rows
+// there, which turn it into operands again, and sk_ratio for every unit here.  A segment that only the first
+// shape's schedule gives to the prefill kernel (taken to be one with work enough of its own) costs about
+// 4 + rows / 64 a key there, staged and attended.
 __device__ __forceinline__ float sk_cost(const SchedArgs& A, int32_t q_len, int32_t kv_end, int32_t window) {
   const int64_t R = (int64_t)q_len * A.group;
   int64_t span = kv_end;
   if (window > 0) span = min(span, (int64_t)q_len + window - 1);
-  const int64_t n0 = (R + 7) / 8, n1 = (R + A.sk[1].rows - 1) / A.sk[1].rows;
+  const bool pf = A.prefill_ok && (float)R * (float)span * (float)A.Hkv * (float)A.D >= A.pf_min_work;
+  if (pf && R >= A.pf_tile_rows) return 0.f;  // the prefill kernel's in both
+  const int64_t n0 = pf && R >= A.pf_min_rows ? 4 + R / 64 : (R + 7) / 8;
+  const int64_t n1 = (R + A.sk[1].rows - 1) / A.sk[1].rows;
   return ((float)n1 * A.sk_ratio - (float)n0) * (float)span;
 }
 
@@ -422,33 +426,38 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_kernel(SchedArgs A) 
     __syncthreads();
 
     // 3. route each live segment and count its units (contiguous segment ranges per thread);
-    // first the call's prefill work, which decides whether the prefill route is taken
+    // first which shape the split-K route takes, and the call's prefill work, which decides whether the
+    // prefill route is taken
     int64_t sa, sb;
     my_range(S, &sa, &sb);
-    float pw = 0.f;
-    for (int64_t s = sa; s < sb; ++s) {
-      const int4 g = seg_of((int)s);
-      if (bits_of((int)s) == 0 && !flag[s] && g.y > 0)
-        pw += prefill_work<Q4>(A, g.y, g.w, cached ? c_mode[s].y : W.segs[s].window);
-    }
-    const bool big = block_sum(pw, s_fsum) >= pf_min_work<Q4>(A);
+    int pf_rows = pf_min_rows<Q4>(A);
     if (sk_choice<Q4>(A)) {
       float more = 0.f;
       for (int64_t s = sa; s < sb; ++s) {
         const int4 g = seg_of((int)s);
-        if (bits_of((int)s) == 0 && !flag[s] && g.y > 0 && route_of<Q4>(A, g.y, big) == kRouteSplitk)
+        if (bits_of((int)s) == 0 && !flag[s] && g.y > 0)
           more += sk_cost(A, g.y, g.w, cached ? c_mode[s].y : W.segs[s].window);
       }
+      if (block_sum(more, s_fsum) < 0.f) {
+        sk = A.sk[1];
+        pf_rows = A.pf_tile_rows;
+      }
       __syncthreads();  // (s_fsum is read)
-      if (block_sum(more, s_fsum) < 0.f) sk = A.sk[1];
     }
+    float pw = 0.f;
+    for (int64_t s = sa; s < sb; ++s) {
+      const int4 g = seg_of((int)s);
+      if (bits_of((int)s) == 0 && !flag[s] && g.y > 0)
+        pw += prefill_work(A, g.y, g.w, cached ? c_mode[s].y : W.segs[s].window, pf_rows);
+    }
+    const bool big = block_sum(pw, s_fsum) >= pf_min_work<Q4>(A);
     // staged columns go to the first segments of the prefill route, in segment order
     int64_t pf[1] = {0};
     if (pf_cols<Q4>(A) > 0) {
       int64_t pf_all[1];
       for (int64_t s = sa; s < sb; ++s) {
         const int4 g = seg_of((int)s);
-        pf[0] += bits_of((int)s) == 0 && !flag[s] && g.y > 0 && route_of<Q4>(A, g.y, big) == kRoutePrefill;
+        pf[0] += bits_of((int)s) == 0 && !flag[s] && g.y > 0 && route_of(A, g.y, big, pf_rows) == kRoutePrefill;
       }
       block_scan<1>(pf, pf_all, sh);
     }
@@ -461,7 +470,7 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_kernel(SchedArgs A) 
       int route = kRouteNone, nrb = 0;
       if (bits == 0 && !fl && g.y > 0) {
         const int64_t R = (int64_t)g.y * A.group;
-        route = route_of<Q4>(A, g.y, big);
+        route = route_of(A, g.y, big, pf_rows);
         if (pf_cols<Q4>(A) > 0 && route == kRoutePrefill) {
           if (pf[0] >= pf_cols<Q4>(A)) route = kRouteSplitk;
           (cached ? c_pf[s] : W.segs[s].pf_col) = (int32_t)pf[0]++;
@@ -777,19 +786,23 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_small_kernel(SchedAr
       ov = ov && ok;
     }
     const bool live = ok && !ov;
-    float pw = live ? prefill_work<Q4>(A, g[1], g[3], md.y) : 0.f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) pw += __shfl_xor_sync(kAll, pw, o);
-    int route = live ? route_of<Q4>(A, g[1], pw >= pf_min_work<Q4>(A)) : kRouteNone, nrb = 0;
-    int pf_col = 0;
     SkShape sk = first_shape<Q4>(A);
+    int pf_rows = pf_min_rows<Q4>(A);
     if (sk_choice<Q4>(A)) {
-      float more = route == kRouteSplitk ? sk_cost(A, g[1], g[3], md.y) : 0.f;
+      float more = live ? sk_cost(A, g[1], g[3], md.y) : 0.f;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) more += __shfl_xor_sync(kAll, more, o);
-      if (more < 0.f) sk = A.sk[1];
+      if (more < 0.f) {
+        sk = A.sk[1];
+        pf_rows = A.pf_tile_rows;
+      }
       if (lane == 0) s_sk = more < 0.f;
     }
+    float pw = live ? prefill_work(A, g[1], g[3], md.y, pf_rows) : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) pw += __shfl_xor_sync(kAll, pw, o);
+    int route = live ? route_of(A, g[1], pw >= pf_min_work<Q4>(A), pf_rows) : kRouteNone, nrb = 0;
+    int pf_col = 0;
     if (pf_cols<Q4>(A) > 0) {  // staged columns go to the first segments of the prefill route
       pf_col = __popc(__ballot_sync(kAll, route == kRoutePrefill) & ((1u << lane) - 1u));
       if (route == kRoutePrefill && pf_col >= pf_cols<Q4>(A)) route = kRouteSplitk;
