@@ -30,6 +30,14 @@ def dev():
     return torch.device("cuda:0")
 
 
+@pytest.fixture(params=["auto", "splitk"], autouse=True)
+def route(request):
+    """Every test under the automatic routes (short key ranges without a schedule) and with a schedule."""
+    pkg.set_route_policy(pkg.ROUTE_AUTO if request.param == "auto" else pkg.ROUTE_SPLITK)
+    yield request.param
+    pkg.set_route_policy(pkg.ROUTE_AUTO)
+
+
 def random_store(rows, cols, Hkv, D, seed, lo=150, hi=170):
     """Codes of every kind (0 among them), scale bytes in [lo, hi)."""
     g = torch.Generator().manual_seed(seed)
@@ -301,7 +309,9 @@ def test_the_bf16_store_agrees_with_the_4_bit_one_on_its_values(dev):
 # ------------------------------------------- the tensor-memory route: columns staged in bf16 first
 
 @pytest.fixture
-def prefill_route():
+def prefill_route(route):
+    if route != "auto":
+        pytest.skip("one policy at a time")
     pkg.set_route_policy(pkg.ROUTE_PREFILL)
     yield
     pkg.set_route_policy(pkg.ROUTE_AUTO)
@@ -539,3 +549,32 @@ def test_a_chunk_among_single_tokens_takes_the_cheaper_kernel(dev, S_, D, chunk,
         check(got, st, q, store, seq, causal, p_step=2.0 ** -8, rows_subset=rows)
     got, st = run_q4(q, store, seq, dev, causal=True, window=100)
     check(got, st, q, store, seq, True, 100, p_step=2.0 ** -8, rows_subset=rows)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("S_,Hq,Hkv", [(300, 8, 2), (512, 2, 1), (513, 2, 1), (170, 64, 2)])
+def test_tables_of_many_single_tokens(dev, D, S_, Hq, Hkv):
+    # with columns shared, empty and invalid entries, tokens out of order, and two that overlap
+    rng = np.random.default_rng(S_ + D)
+    order = rng.permutation(S_)
+    seq = [[int(order[i]), 1, i % 23, int(rng.integers(0, 129))] for i in range(S_)]
+    seq[5][1], seq[9][2], seq[11][3] = 0, 23, -4
+    seq[17][0] = seq[40][0]
+    seq[60][0] = -1
+    store, q = random_store(128, 23, Hkv, D, S_), queries(S_, Hq, D, 60)
+    modes = [[i % 2, [0, 1, 20, 128][i % 4]] for i in range(S_)]
+    rows = sorted({int(order[i]) for i in (0, 5, 9, 11, 17, 40, 60, 61, S_ - 1)} | set(range(0, S_, 37)))
+    for m in (None, modes):
+        got, st = run_q4(q, store, seq, dev, causal=True, seg_mode=m)
+        check(got, st, q, store, seq, True, 0, m, rows_subset=rows)
+
+
+def test_the_workspace_status_of_a_call_without_a_schedule(dev):
+    store = pkg.q4_store(64, 2, 1, 64, device=dev)
+    ws = torch.full((pkg.q4_workspace_bytes(4, 2, store, 3),), 255, dtype=torch.uint8, device=dev)
+    q = queries(4, 2, 64, 61).to(dev)
+    for seq in ([[0, 1, 0, 5], [1, 1, 1, 6], [2, 1, 0, 7]], [[0, 2, 0, 5], [1, 1, 1, 6], [3, 1, 7, 9]],
+                [[0, 2, 0, 5], [0, 0, 1, 6], [3, 1, 1, -9]]):
+        pkg.sdpa_varlen_q4(q, store, torch.tensor(seq, dtype=torch.int32, device=dev), causal=True, workspace=ws)
+        _, _, _, want = O.visible_interval(np.array(seq), 4, True, 0, 64, 2, None)
+        assert pkg.workspace_status(ws) == want

@@ -110,6 +110,10 @@ static sdpa_status device_info(DevInfo* out) {
       if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "smem attribute: %s", cudaGetErrorString(e));
       e = cudaFuncSetAttribute(q4, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
       if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "carveout attribute: %s", cudaGetErrorString(e));
+      e = cudaFuncSetAttribute(q4_direct_kernel_ptr(Ds[k]), cudaFuncAttributeMaxDynamicSharedMemorySize, q4_smem);
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(q4_direct_kernel_ptr(Ds[k]), cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+      if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "4-bit direct kernel attributes: %s", cudaGetErrorString(e));
       e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, q4, kQ4Threads, q4_smem);
       if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "occupancy: %s", cudaGetErrorString(e));
       di.q4_per_sm[k] = nb > 0 ? nb : 1;
@@ -262,6 +266,23 @@ static cudaError_t launch_k(const void* f, unsigned grid, unsigned block, void**
     cfg.numAttrs = 1;
   }
   return cudaLaunchKernelExC(&cfg, f, args);
+}
+
+// Whether a 4-bit call takes the kernel without a schedule, a CTA for every (token, KV head) pair: key ranges are
+// short, and there is at most one token a segment, or the pairs' CTAs all fit the SMs at once.  In us, direct /
+// scheduled, 32/8 heads, D = 128, every token's keys the same: 8 tokens 64 keys 5.2 / 12.8, 2048 keys 14.7 / 18.5, 4096
+// keys 23.7 / 22.6; 32 tokens 512 keys 8.9 / 22.6, 4096 keys 38 / 49; 64 tokens 64 keys 9.6 / 22.4, 2048 keys 41 / 62; two
+// segments of 16 tokens 1024 keys 13 / 26, 4096 keys 36 / 28; 60 tokens, D = 256, 2048 keys 75 / 96.  With few pairs a longer
+// range is better cut, and where lengths differ the call waits for its longest: 32 tokens of up to 4096 keys evenly
+// spread 34.5 / 33.6, one of 4096 and 31 of 256 keys 24 / 22, and at D = 256, whose limit is 2048, 68 / 55 and 50 / 28.
+static bool q4_direct(const DevInfo& di, int64_t T, int Hq, int Hkv, int D, int S, int64_t rows, int causal, int window,
+                      const int32_t* seg_mode) {
+  if (g_policy.load() != SDPA_ROUTE_AUTO || Hq / Hkv > kSplitkRows || S > kQ4DirectSegs) return false;
+  const int64_t pairs = T * Hkv;
+  if (T > S && pairs > (int64_t)di.sms * di.q4_per_sm[d_index(D)]) return false;
+  int64_t keys = rows;  // that a row may see
+  if (window > 0 && !seg_mode) keys = std::min<int64_t>(keys, causal ? window : T + window - 1);
+  return keys <= (D <= 128 && T <= S && pairs >= di.sms ? 4096 : 2048);
 }
 
 // The prefill route over a 4-bit store: its columns are staged first, which many rows have to pay for, and the
@@ -511,6 +532,18 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
   if (ap) {
     apw = *ap;
     apw.segs = W.segs;
+  }
+  if (q4 && q4_direct(di, T, Hq, Hkv, D, S, rows, causal, window, sa.seg_mode)) {
+    Q4DirectArgs da{{aa, *q4, 0}, S > 0 ? seq_info : nullptr, sa.seg_mode, S};
+    void* args[] = {(void*)&da};
+    const cudaStream_t cs = (cudaStream_t)stream;
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; i < 3 && e == cudaSuccess; ++i) e = mark(i, cs);
+    if (e == cudaSuccess)
+      e = launch_k(q4_direct_kernel_ptr(D), (unsigned)(T * Hkv), kQ4Threads, args, q4_splitk_smem_bytes(D), cs, false);
+    for (int i = 3; i < 5 && e == cudaSuccess; ++i) e = mark(i, cs);
+    if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "4-bit direct launch: %s", cudaGetErrorString(e));
+    return SDPA_OK;
   }
   if (sa.pf_cols > 0) {
     sg.segs = W.segs;

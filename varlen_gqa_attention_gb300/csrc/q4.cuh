@@ -130,6 +130,15 @@ struct Q4AttnArgs {
   int choice;  // both split-K kernels are launched, and the schedule is one's (hdr->sk_rows)
 };
 
+// A call without a schedule (q4_attn.cu): at most kQ4DirectSegs segments, at most kSplitkRows heads a KV head.
+constexpr int kQ4DirectSegs = 512;
+struct Q4DirectArgs {
+  Q4AttnArgs q4;
+  const int32_t* seq_info;
+  const int32_t* seg_mode;  // NULL, or [S, 2] (causal, window)
+  int S;
+};
+
 // The keys and values of the prefill route's segments, brought to bf16 for the tensor-memory kernel:
 // position p of the segment with staged column c goes to row p % rows_pf of column c of a bf16
 // column store [rows_pf, pf_cols, Hkv, D] (q4_stage.cu).
@@ -154,6 +163,7 @@ constexpr int kQ4TileThreads = 576;
 const void* q4_tile_kernel_ptr(int D);
 int q4_tile_smem_bytes(int D);
 const void* q4_splitk_kernel_ptr(int D);
+const void* q4_direct_kernel_ptr(int D);
 int q4_splitk_smem_bytes(int D);
 
 }  // namespace sdpa

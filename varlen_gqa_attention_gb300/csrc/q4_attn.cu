@@ -63,6 +63,7 @@ struct Q4Cfg {
 struct Q4Piece {
   UnitRec ur;
   int64_t pos_lo, pos_hi;  // key positions; pos_lo is a multiple of 16
+  int64_t r0;              // the unit's first packed row, counted from its segment's
   int64_t unit;            // index of the unit on its route
   int32_t slot, valid;     // valid 0: no more work
 };
@@ -119,7 +120,7 @@ __device__ __forceinline__ void q4_unit(const AttnArgs& A, const Q4Piece& pc, in
   const int gq = lane >> 2, tq = lane & 3;
   const UnitRec& ur = pc.ur;
   const int R = ur.rows;
-  const int64_t r0 = (int64_t)ur.rb * kSplitkRows;
+  const int64_t r0 = pc.r0;
   const int64_t pos_lo = pc.pos_lo;
   const int nkeys = (int)(pc.pos_hi - pos_lo);
 
@@ -390,9 +391,54 @@ __device__ __forceinline__ void q4_unit(const AttnArgs& A, const Q4Piece& pc, in
   }
 }
 
-// The loading warp: walks the CTA's pieces, hands each on with its query rows, and streams its keys
-// through the ring.  A piece's keys [pos_lo, pos_hi) begin at a multiple of 16 and span at most
-// rows + 15 positions, so a stage is at most two runs of store rows, both of whole 16-row blocks.
+// A loading warp's part of a piece: its query rows (r0 of the segment's packed rows on) and its keys through the
+// ring.  The keys [pos_lo, pos_hi) begin at a multiple of 16 and span at most rows + 15 positions, so a stage
+// is at most two runs of store rows, both of whole 16-row blocks.  False: a wait gave up.
+template <int D, typename S>
+__device__ __forceinline__ bool q4_load_piece(const Q4AttnArgs& G, const UnitRec& ur, int64_t r0, int64_t pos_lo,
+                                              int64_t pos_hi, char* ring, char* sQ, uint32_t full, uint32_t empty,
+                                              uint32_t qfull, uint32_t& it, volatile int* abort) {
+  const AttnArgs& A = G.a;
+  const int lane = threadIdx.x & 31;
+  if (lane < ur.rows) {
+    const int64_t r = r0 + lane;
+    const int64_t i = r / A.group;
+    const int h = ur.hk * A.group + (int)(r % A.group);
+    bulk_load(smem_u32(sQ + lane * S::kQPitch),
+              A.q + (ur.q_start + i) * A.q_rs + (int64_t)h * A.q_hs, D * 2, qfull);
+  }
+  const int64_t plane = ((int64_t)ur.col * A.Hkv + ur.hk) * A.rows;  // first row of the column's head
+  int64_t row = pos_lo % A.rows;
+  for (int64_t pos = pos_lo; pos < pos_hi; pos += S::kKeys, ++it) {
+    const uint32_t st = it % S::kStages;
+    if (it >= S::kStages && !q4_wait(empty + 8 * st, (it / S::kStages - 1) & 1, abort)) return false;
+    const int rows16 = (int)(min((int64_t)S::kKeys, pos_hi - pos) + 15) & ~15;
+    const int first = (int)min((int64_t)rows16, A.rows - row), second = rows16 - first;
+    if (lane == 0) {
+      const uint32_t bar = full + 8 * st;
+      const uint32_t dst = smem_u32(ring + st * S::kStageBytes);
+      mbar_expect_tx(bar, (uint32_t)rows16 * 2 * (S::kRowBytes + S::kScaleBytes));
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const uint8_t* codes = v ? G.st.vc : G.st.kc;
+        const uint8_t* scales = v ? G.st.vs : G.st.ks;
+        const uint32_t dc = dst + v * S::kCodes, ds = dst + 2 * S::kCodes + v * S::kScales;
+        bulk_load(dc, codes + (plane + row) * S::kRowBytes, first * S::kRowBytes, bar);
+        bulk_load(ds, scales + (plane + row) * S::kScaleBytes, first * S::kScaleBytes, bar);
+        if (second > 0) {
+          bulk_load(dc + first * S::kRowBytes, codes + plane * S::kRowBytes, second * S::kRowBytes, bar);
+          bulk_load(ds + first * S::kScaleBytes, scales + plane * S::kScaleBytes, second * S::kScaleBytes, bar);
+        }
+      }
+    }
+    row += rows16;
+    if (row >= A.rows) row -= A.rows;
+  }
+  return true;
+}
+
+// The loading warp: walks the CTA's pieces, hands each on with its query rows, and streams its keys through the
+// ring.
 template <int D, typename S>
 __device__ __forceinline__ void q4_load(const Q4AttnArgs& G, char* ring, char* sQ, Q4Piece* pieces, uint32_t full,
                                         uint32_t empty, uint32_t qfull, uint32_t qempty, volatile int* abort) {
@@ -410,6 +456,7 @@ __device__ __forceinline__ void q4_load(const Q4AttnArgs& G, char* ring, char* s
     if (n > 0 && !q4_wait(qempty, (n - 1) & 1, abort)) break;
     const int64_t pos_lo = (int64_t)ur.lo + ta * kSplitkTile;
     const int64_t pos_hi = min((int64_t)ur.lo + tb * kSplitkTile, (int64_t)ur.hi);
+    const int64_t r0 = (int64_t)ur.rb * kSplitkRows;
     if (lane == 0) {
       Q4Piece& p = pieces[n & 1];
       p.valid = more;
@@ -417,6 +464,7 @@ __device__ __forceinline__ void q4_load(const Q4AttnArgs& G, char* ring, char* s
         p.ur = ur;
         p.pos_lo = pos_lo;
         p.pos_hi = pos_hi;
+        p.r0 = r0;
         p.unit = wk.u - 1;  // the walk has moved past the piece's unit
         p.slot = (int32_t)(blockIdx.x - ur.g_first);
         mbar_expect_tx(qfull, (uint32_t)ur.rows * (D * 2));
@@ -426,42 +474,7 @@ __device__ __forceinline__ void q4_load(const Q4AttnArgs& G, char* ring, char* s
     }
     __syncwarp();
     if (!more) return;
-    if (lane < ur.rows) {
-      const int64_t r = (int64_t)ur.rb * kSplitkRows + lane;
-      const int64_t i = r / A.group;
-      const int h = ur.hk * A.group + (int)(r % A.group);
-      bulk_load(smem_u32(sQ + lane * S::kQPitch),
-                A.q + (ur.q_start + i) * A.q_rs + (int64_t)h * A.q_hs, D * 2, qfull);
-    }
-    const int64_t plane = ((int64_t)ur.col * A.Hkv + ur.hk) * A.rows;  // first row of the column's head
-    int64_t row = pos_lo % A.rows;
-    bool ok = true;
-    for (int64_t pos = pos_lo; pos < pos_hi; pos += S::kKeys, ++it) {
-      const uint32_t st = it % S::kStages;
-      if (it >= S::kStages && !(ok = q4_wait(empty + 8 * st, (it / S::kStages - 1) & 1, abort))) break;
-      const int rows16 = (int)(min((int64_t)S::kKeys, pos_hi - pos) + 15) & ~15;
-      const int first = (int)min((int64_t)rows16, A.rows - row), second = rows16 - first;
-      if (lane == 0) {
-        const uint32_t bar = full + 8 * st;
-        const uint32_t dst = smem_u32(ring + st * S::kStageBytes);
-        mbar_expect_tx(bar, (uint32_t)rows16 * 2 * (S::kRowBytes + S::kScaleBytes));
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const uint8_t* codes = v ? G.st.vc : G.st.kc;
-          const uint8_t* scales = v ? G.st.vs : G.st.ks;
-          const uint32_t dc = dst + v * S::kCodes, ds = dst + 2 * S::kCodes + v * S::kScales;
-          bulk_load(dc, codes + (plane + row) * S::kRowBytes, first * S::kRowBytes, bar);
-          bulk_load(ds, scales + (plane + row) * S::kScaleBytes, first * S::kScaleBytes, bar);
-          if (second > 0) {
-            bulk_load(dc + first * S::kRowBytes, codes + plane * S::kRowBytes, second * S::kRowBytes, bar);
-            bulk_load(ds + first * S::kScaleBytes, scales + plane * S::kScaleBytes, second * S::kScaleBytes, bar);
-          }
-        }
-      }
-      row += rows16;
-      if (row >= A.rows) row -= A.rows;
-    }
-    if (!ok) break;
+    if (!q4_load_piece<D, S>(G, ur, r0, pos_lo, pos_hi, ring, sQ, full, empty, qfull, it, abort)) break;
   }
   // gave up: no copy of this CTA may still be in flight when it ends
   int none = 0;
@@ -529,6 +542,150 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Cfg<D>::kPerSm) sdpa_q4_splitk_k
   }
 }
 
+// A token's heads of one KV head, whole, without a schedule: a CTA finds its token's segment itself and writes the
+// output.  The scheduler and the joining pass even out lengths; they cost 8 us, and 12 on a table of more than 32
+// segments, which is more than the call loses by its longest range when ranges are short (q4_direct in api.cu).
+// What bounds it: the chain segment - rows and first keys - output (5 us in all for one token over 128 keys), then
+// the conversion, as above.
+template <int D>
+__global__ void __launch_bounds__(kQ4Threads, Q4Cfg<D>::kPerSm) sdpa_q4_direct_kernel(Q4DirectArgs G) {
+  using S = Q4Cfg<D>;
+  extern __shared__ __align__(128) char smem[];
+  __shared__ __align__(8) uint64_t bars[2 * S::kStages + 2];
+  __shared__ __align__(16) Q4Piece piece;
+  __shared__ float2 s_ml[4 * 8];
+  __shared__ int32_t* s_count[2];
+  __shared__ int4 s_seg;  // the owner's entry
+  __shared__ int s_abort, s_owner, s_dead, s_bits;
+  const AttnArgs& A = G.q4.a;
+  char* ring = smem;
+  char* sQ = smem + S::kStages * S::kStageBytes;
+  float* merge = reinterpret_cast<float*>(sQ + S::kQBytes);
+  const uint32_t full = smem_u32(bars), empty = full + 8 * S::kStages;
+  const uint32_t qfull = empty + 8 * S::kStages, qempty = qfull + 8;
+  const int tid = threadIdx.x;
+  const int t = (int)(blockIdx.x / (uint32_t)A.Hkv), hk = (int)(blockIdx.x % (uint32_t)A.Hkv);
+
+  // entry i of the table, empty unless it is valid
+  auto entry = [&](int i, int32_t* bits) -> int4 {
+    int4 g = __ldg(reinterpret_cast<const int4*>(G.seq_info) + i);
+    const int window = G.seg_mode ? __ldg(G.seg_mode + 2 * i + 1) : A.window;
+    const int32_t b = segment_bits(g.x, g.y, g.z, g.w, A.T, A.rows, A.cols, window);
+    *bits |= b;
+    if (b || g.y <= 0) g = make_int4(0, 0, 0, 0);
+    return g;
+  };
+  auto meet = [](const int4& a, const int4& b) { return max(a.x, b.x) < min(a.x + a.y, b.x + b.y); };
+  if (tid == 0) {
+    s_abort = s_dead = s_bits = 0;
+    s_owner = -1;
+    s_count[0] = nullptr;
+    for (int k = 0; k < S::kStages; ++k) {
+      mbar_init(full + 8 * k, 1);
+      mbar_init(empty + 8 * k, 4);
+    }
+    mbar_init(qfull, 1);
+    mbar_init(qempty, 4);
+    mbar_fence_init();
+  }
+  __syncthreads();
+  int32_t bits = 0;
+  bool mixed = false;  // the valid segments are not in row order, or share a row
+  int4 mine = make_int4(0, 0, 0, 0);  // a thread keeps its first entry
+  for (int i = tid; i < G.S; i += kQ4Threads) {
+    const int4 g = entry(i, &bits);
+    if (i == tid) mine = g;
+    if (t >= g.x && t < g.x + g.y) {
+      if (atomicCAS(&s_owner, -1, i) == -1) s_seg = g;
+      else s_dead = 1;
+    }
+    if (blockIdx.x == 0 && g.y > 0) {
+      int32_t other = 0;
+      for (int j = i - 1; j >= 0; --j) {
+        const int4 o = entry(j, &other);
+        if (o.y == 0) continue;
+        mixed |= o.x + o.y > g.x;
+        break;
+      }
+    }
+  }
+  __syncthreads();
+  const int owner = s_owner;
+  if (owner >= 0) {  // a segment that shares any row with another valid one is dropped
+    const int4 o = s_seg;
+    for (int i = tid; i < G.S; i += kQ4Threads) {
+      const int4 g = i == tid ? mine : entry(i, &bits);
+      if (i != owner && meet(g, o)) s_dead = 1;
+    }
+  }
+  if (blockIdx.x == 0) {  // the call's status bits
+    if (__syncthreads_or(mixed)) {
+      for (int i = tid; i < G.S; i += kQ4Threads) {
+        const int4 g = i == tid ? mine : entry(i, &bits);
+        for (int j = 0; j < G.S; ++j)
+          if (j != i && meet(g, entry(j, &bits))) bits |= SDPA_SEG_OVERLAP;
+      }
+    }
+    if (bits) atomicOr(&s_bits, bits);
+  }
+  __syncthreads();
+  if (blockIdx.x == 0 && tid == 0) {
+    A.ws.hdr->status = s_bits;
+    if (A.status_dev && s_bits) atomicOr(A.status_dev, s_bits);
+  }
+
+  RowWin w{0, 0};
+  UnitRec ur{};
+  if (owner >= 0 && !s_dead) {
+    const int4 o = s_seg;
+    ur.hk = hk;
+    ur.rows = A.group;
+    ur.nslots = 1;
+    ur.q_start = o.x;
+    ur.q_len = o.y;
+    ur.col = o.z;
+    ur.kv_end = o.w;
+    ur.causal = G.seg_mode ? __ldg(G.seg_mode + 2 * owner) != 0 : A.causal;
+    ur.window = G.seg_mode ? __ldg(G.seg_mode + 2 * owner + 1) : A.window;
+    w = row_window(t - o.x, o.y, o.w, ur.causal, ur.window);
+  }
+  if (w.hi <= w.lo) {  // no segment, or no visible key
+    for (int i = tid; i < A.group * (D / 8); i += kQ4Threads)
+      *reinterpret_cast<uint4*>(A.out + (int64_t)t * A.o_rs + (int64_t)(hk * A.group + i / (D / 8)) * A.o_hs +
+                                i % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  const int64_t pos_lo = w.lo & -kQ4RowAlign, r0 = (int64_t)(t - ur.q_start) * A.group;
+  if (tid == 0) {
+    piece.ur = ur;
+    piece.pos_lo = pos_lo;
+    piece.pos_hi = w.hi;
+    piece.r0 = r0;
+    mbar_expect_tx(qfull, (uint32_t)A.group * (D * 2));
+  }
+  __syncthreads();
+  uint32_t it = 0;
+  if (tid >= kQ4Consumers) {
+    if (!q4_load_piece<D, S>(G.q4, ur, r0, pos_lo, w.hi, ring, sQ, full, empty, qfull, it, &s_abort)) {
+      int none = 0;  // no copy of this CTA may still be in flight when it ends
+      for (uint32_t k = it > S::kStages ? it - S::kStages : 0; k < it; ++k)
+        mbar_wait(full + 8 * (k % S::kStages), (k / S::kStages) & 1, &none);
+      mbar_wait(qfull, 0, &none);
+    }
+  } else {
+    const bool got = q4_wait(qfull, 0, &s_abort);
+    const int groups = (A.group + 7) / 8;
+    if (bar_and(1, kQ4Consumers, got))
+      q4_unit<D, S>(A, piece, groups == 1 ? 4 : groups == 2 ? 2 : 1, ring, sQ, merge, full, empty, qempty, it, &s_abort,
+                    s_ml, s_count);
+  }
+  __syncthreads();
+  if (tid == 0 && s_abort) {
+    atomicOr((unsigned long long*)&A.ws.hdr->status, (unsigned long long)SDPA_DEV_TIMEOUT);
+    if (A.status_dev) atomicOr(A.status_dev, SDPA_DEV_TIMEOUT);
+  }
+}
+
 template __global__ void sdpa_q4_splitk_kernel<64>(Q4AttnArgs);
 template __global__ void sdpa_q4_splitk_kernel<128>(Q4AttnArgs);
 template __global__ void sdpa_q4_splitk_kernel<256>(Q4AttnArgs);
@@ -546,6 +703,14 @@ const void* q4_splitk_kernel_ptr(int D) {
     case 64: return (const void*)sdpa_q4_splitk_kernel<64>;
     case 128: return (const void*)sdpa_q4_splitk_kernel<128>;
     default: return (const void*)sdpa_q4_splitk_kernel<256>;
+  }
+}
+
+const void* q4_direct_kernel_ptr(int D) {
+  switch (D) {
+    case 64: return (const void*)sdpa_q4_direct_kernel<64>;
+    case 128: return (const void*)sdpa_q4_direct_kernel<128>;
+    default: return (const void*)sdpa_q4_direct_kernel<256>;
   }
 }
 
