@@ -268,21 +268,27 @@ static cudaError_t launch_k(const void* f, unsigned grid, unsigned block, void**
   return cudaLaunchKernelExC(&cfg, f, args);
 }
 
-// Whether a 4-bit call takes the kernel without a schedule, a CTA for every (token, KV head) pair: key ranges are
-// short, and there is at most one token a segment, or the pairs' CTAs all fit the SMs at once.  In us, direct /
-// scheduled, 32/8 heads, D = 128, every token's keys the same: 8 tokens 64 keys 5.2 / 12.8, 2048 keys 14.7 / 18.5, 4096
-// keys 23.7 / 22.6; 32 tokens 512 keys 8.9 / 22.6, 4096 keys 38 / 49; 64 tokens 64 keys 9.6 / 22.4, 2048 keys 41 / 62; two
-// segments of 16 tokens 1024 keys 13 / 26, 4096 keys 36 / 28; 60 tokens, D = 256, 2048 keys 75 / 96.  With few pairs a longer
-// range is better cut, and where lengths differ the call waits for its longest: 32 tokens of up to 4096 keys evenly
-// spread 34.5 / 33.6, one of 4096 and 31 of 256 keys 24 / 22, and at D = 256, whose limit is 2048, 68 / 55 and 50 / 28.
-static bool q4_direct(const DevInfo& di, int64_t T, int Hq, int Hkv, int D, int S, int64_t rows, int causal, int window,
-                      const int32_t* seg_mode) {
-  if (g_policy.load() != SDPA_ROUTE_AUTO || Hq / Hkv > kSplitkRows || S > kQ4DirectSegs) return false;
-  const int64_t pairs = T * Hkv;
-  if (T > S && pairs > (int64_t)di.sms * di.q4_per_sm[d_index(D)]) return false;
+// CTAs that share a (token, KV head) pair's keys when a 4-bit call takes the kernel without a schedule; 0 when it
+// does not.  It does where a CTA's share of the longest range possible is short, and there is at most one token a
+// segment, or the pairs' CTAs all fit the SMs at once.  The shares are halved while there are SMs for them and more
+// than kQ4DirectPart keys in each.  In us, direct / scheduled, 32/8 heads, D = 128, all ranges full: 1 token 512 keys
+// 7.0 / 14.4, 16384 keys 15.8 / 19.4; 8 tokens 64 keys 6.0 / 13.0, 2048 keys 10.3 / 18.8, 16384 keys 40 / 45; 32 tokens
+// 512 keys 8.9 / 22.6, 4096 keys 38 / 49; 64 tokens 2048 keys 41 / 62; two segments of 16 tokens 1024 keys 13 / 26, 4096 keys
+// 36 / 28.  Where lengths differ the call waits for its longest: lengths evenly spread up to the limit (32 tokens of 4096
+// keys, 34.5 / 33.6; with 16/2 heads of 8192, 21 / 24, of 16384 beyond it 36 / 30; 16 tokens at D = 256 of 4096 30 / 32, of
+// 8192 52 / 47).
+constexpr int64_t kQ4DirectPart = 128;
+static int q4_direct(const DevInfo& di, int64_t T, int Hq, int Hkv, int D, int S, int64_t rows, int causal, int window,
+                     const int32_t* seg_mode) {
+  if (g_policy.load() != SDPA_ROUTE_AUTO || Hq / Hkv > kSplitkRows || S > kQ4DirectSegs) return 0;
+  const int64_t pairs = T * Hkv, resident = (int64_t)di.sms * di.q4_per_sm[d_index(D)];
+  if (T > S && pairs > resident) return 0;
   int64_t keys = rows;  // that a row may see
   if (window > 0 && !seg_mode) keys = std::min<int64_t>(keys, causal ? window : T + window - 1);
-  return keys <= (D <= 128 && T <= S && pairs >= di.sms ? 4096 : 2048);
+  int parts = 1;
+  while (parts < 8 && 2 * parts * pairs <= resident && keys > kQ4DirectPart * parts) parts *= 2;
+  const int64_t share = T <= S && (D == 64 || (D == 128 && parts <= 2)) ? 4096 : 2048;
+  return keys <= share * parts ? parts : 0;
 }
 
 // The prefill route over a 4-bit store: its columns are staged first, which many rows have to pay for, and the
@@ -533,14 +539,25 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
     apw = *ap;
     apw.segs = W.segs;
   }
-  if (q4 && q4_direct(di, T, Hq, Hkv, D, S, rows, causal, window, sa.seg_mode)) {
+  const int parts = q4 ? q4_direct(di, T, Hq, Hkv, D, S, rows, causal, window, sa.seg_mode) : 0;
+  if (parts > 0) {
     Q4DirectArgs da{{aa, *q4, 0}, S > 0 ? seq_info : nullptr, sa.seg_mode, S};
     void* args[] = {(void*)&da};
     const cudaStream_t cs = (cudaStream_t)stream;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(T * Hkv * parts));
+    cfg.blockDim = dim3(kQ4Threads);
+    cfg.dynamicSmemBytes = q4_splitk_smem_bytes(D);
+    cfg.stream = cs;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)parts;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
     cudaError_t e = cudaSuccess;
     for (int i = 0; i < 3 && e == cudaSuccess; ++i) e = mark(i, cs);
-    if (e == cudaSuccess)
-      e = launch_k(q4_direct_kernel_ptr(D), (unsigned)(T * Hkv), kQ4Threads, args, q4_splitk_smem_bytes(D), cs, false);
+    if (e == cudaSuccess) e = cudaLaunchKernelExC(&cfg, q4_direct_kernel_ptr(D), args);
     for (int i = 3; i < 5 && e == cudaSuccess; ++i) e = mark(i, cs);
     if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "4-bit direct launch: %s", cudaGetErrorString(e));
     return SDPA_OK;

@@ -106,11 +106,12 @@ __device__ __forceinline__ void lds_words(const char* p, uint32_t (&w)[N]) {
 }
 
 // The four attention warps on one piece.  4 / NCS groups of 8 query rows; the NCS warps of a group share a
-// stage's keys.
+// stage's keys.  part_o, part_ml: where a piece that is one of several of its unit leaves its rows.
 template <int D, typename S>
 __device__ __forceinline__ void q4_unit(const AttnArgs& A, const Q4Piece& pc, int NCS, const char* ring, char* sQ,
                                         float* merge, uint32_t full, uint32_t empty, uint32_t qempty, uint32_t& it,
-                                        volatile int* abort, float2* s_ml, int32_t** s_count) {
+                                        volatile int* abort, float2* s_ml, int32_t** s_count, float* part_o,
+                                        float2* part_ml) {
   constexpr int WK = D / 32;  // words of a lane's K chunk (D / 4 dims)
   constexpr int WV = D / 64;  // words of a lane's V chunk (D / 8 dims)
   constexpr int ND = D / 16;  // m16 blocks of the output
@@ -379,9 +380,8 @@ __device__ __forceinline__ void q4_unit(const AttnArgs& A, const Q4Piece& pc, in
             make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
                        pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
       } else {
-        const int64_t pi = ur.slot_base + (int64_t)pc.slot * R + rl;
-        if (p == 0 && n == 0) A.ws.part_ml[kRouteSplitk][pi] = make_float2(M, L);
-        float* dst = A.ws.part_o[kRouteSplitk] + pi * D + d0;
+        if (p == 0 && n == 0) part_ml[rl] = make_float2(M, L);
+        float* dst = part_o + rl * D + d0;
 #pragma unroll
         for (int x = 0; x < 8; x += 4)
           *reinterpret_cast<float4*>(dst + x) = make_float4(acc[x], acc[x + 1], acc[x + 2], acc[x + 3]);
@@ -528,8 +528,9 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Cfg<D>::kPerSm) sdpa_q4_splitk_k
       if (threadIdx.x == 0) s_count[1] = pc.ur.nslots > 1 ? A.ws.unit_done + pc.unit : nullptr;
       // warps that share the keys of a group of rows: 4, 2 or 1
       const int groups = (pc.ur.rows + 7) / 8;
+      const int64_t slot = pc.ur.slot_base + (int64_t)pc.slot * pc.ur.rows;
       q4_unit<D, S>(A, pc, groups == 1 ? 4 : groups == 2 ? 2 : 1, ring, sQ, merge, full, empty, qempty, it, &s_abort,
-                    s_ml, s_count);
+                    s_ml, s_count, A.ws.part_o[kRouteSplitk] + slot * D, A.ws.part_ml[kRouteSplitk] + slot);
       // (the unit ended on a barrier of the four warps)
       if (threadIdx.x == 0) s_count[0] = s_count[1];
     }
@@ -542,9 +543,43 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Cfg<D>::kPerSm) sdpa_q4_splitk_k
   }
 }
 
-// A token's heads of one KV head, whole, without a schedule: a CTA finds its token's segment itself and writes the
-// output.  The scheduler and the joining pass even out lengths; they cost 8 us, and 12 on a table of more than 32
-// segments, which is more than the call loses by its longest range when ranges are short (q4_direct in api.cu).
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;\n" : "=r"(r));
+  return r;
+}
+// All threads of a cluster; what they wrote before is visible after.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;\n" ::: "memory");
+}
+// Shared memory of the cluster's CTA `rank`, at this CTA's address.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 cluster_load4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 cluster_load2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];\n" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+// A token's heads of one KV head without a schedule: a CTA, or a cluster of up to 8 that share the keys evenly,
+// finds its token's segment itself and writes the output; a cluster's CTAs join their partial rows through each
+// other's shared memory, a slice of the output each.  The scheduler and the joining pass even out lengths; they
+// cost 8 us, and 12 on a table of more than 32 segments, which is more than the call loses by its longest range
+// when the ranges of a CTA are short (q4_direct in api.cu).
 // What bounds it: the chain segment - rows and first keys - output (5 us in all for one token over 128 keys), then
 // the conversion, as above.
 template <int D>
@@ -556,6 +591,7 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Cfg<D>::kPerSm) sdpa_q4_direct_k
   __shared__ float2 s_ml[4 * 8];
   __shared__ int32_t* s_count[2];
   __shared__ int4 s_seg;  // the owner's entry
+  __shared__ float2 s_part[kSplitkRows];  // maxima and sums of a cluster's part
   __shared__ int s_abort, s_owner, s_dead, s_bits;
   const AttnArgs& A = G.q4.a;
   char* ring = smem;
@@ -564,7 +600,8 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Cfg<D>::kPerSm) sdpa_q4_direct_k
   const uint32_t full = smem_u32(bars), empty = full + 8 * S::kStages;
   const uint32_t qfull = empty + 8 * S::kStages, qempty = qfull + 8;
   const int tid = threadIdx.x;
-  const int t = (int)(blockIdx.x / (uint32_t)A.Hkv), hk = (int)(blockIdx.x % (uint32_t)A.Hkv);
+  const uint32_t rank = cluster_rank(), parts = cluster_size(), pair = blockIdx.x / parts;
+  const int t = (int)(pair / (uint32_t)A.Hkv), hk = (int)(pair % (uint32_t)A.Hkv);
 
   // entry i of the table, empty unless it is valid
   auto entry = [&](int i, int32_t* bits) -> int4 {
@@ -640,7 +677,7 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Cfg<D>::kPerSm) sdpa_q4_direct_k
     const int4 o = s_seg;
     ur.hk = hk;
     ur.rows = A.group;
-    ur.nslots = 1;
+    ur.nslots = (int)parts;
     ur.q_start = o.x;
     ur.q_len = o.y;
     ur.col = o.z;
@@ -655,29 +692,63 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Cfg<D>::kPerSm) sdpa_q4_direct_k
                                 i % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
     return;
   }
-  const int64_t pos_lo = w.lo & -kQ4RowAlign, r0 = (int64_t)(t - ur.q_start) * A.group;
-  if (tid == 0) {
-    piece.ur = ur;
-    piece.pos_lo = pos_lo;
-    piece.pos_hi = w.hi;
-    piece.r0 = r0;
-    mbar_expect_tx(qfull, (uint32_t)A.group * (D * 2));
-  }
-  __syncthreads();
-  uint32_t it = 0;
-  if (tid >= kQ4Consumers) {
-    if (!q4_load_piece<D, S>(G.q4, ur, r0, pos_lo, w.hi, ring, sQ, full, empty, qfull, it, &s_abort)) {
-      int none = 0;  // no copy of this CTA may still be in flight when it ends
-      for (uint32_t k = it > S::kStages ? it - S::kStages : 0; k < it; ++k)
-        mbar_wait(full + 8 * (k % S::kStages), (k / S::kStages) & 1, &none);
-      mbar_wait(qfull, 0, &none);
+  // this CTA's keys: runs of 64, as even as they go
+  const int64_t r0 = (int64_t)(t - ur.q_start) * A.group, lo = w.lo & -kQ4RowAlign;
+  const int64_t per = (udiv((int64_t)w.hi - lo + parts - 1, parts) + 63) & ~(int64_t)63;
+  const int64_t pos_lo = lo + rank * per, pos_hi = min(pos_lo + per, (int64_t)w.hi);
+  if (pos_lo < pos_hi) {
+    if (tid == 0) {
+      piece.ur = ur;
+      piece.pos_lo = pos_lo;
+      piece.pos_hi = pos_hi;
+      piece.r0 = r0;
+      mbar_expect_tx(qfull, (uint32_t)A.group * (D * 2));
     }
-  } else {
-    const bool got = q4_wait(qfull, 0, &s_abort);
-    const int groups = (A.group + 7) / 8;
-    if (bar_and(1, kQ4Consumers, got))
-      q4_unit<D, S>(A, piece, groups == 1 ? 4 : groups == 2 ? 2 : 1, ring, sQ, merge, full, empty, qempty, it, &s_abort,
-                    s_ml, s_count);
+    __syncthreads();
+    uint32_t it = 0;
+    if (tid >= kQ4Consumers) {
+      if (!q4_load_piece<D, S>(G.q4, ur, r0, pos_lo, pos_hi, ring, sQ, full, empty, qfull, it, &s_abort)) {
+        int none = 0;  // no copy of this CTA may still be in flight when it ends
+        for (uint32_t k = it > S::kStages ? it - S::kStages : 0; k < it; ++k)
+          mbar_wait(full + 8 * (k % S::kStages), (k / S::kStages) & 1, &none);
+        mbar_wait(qfull, 0, &none);
+      }
+    } else {
+      const bool got = q4_wait(qfull, 0, &s_abort);
+      const int groups = (A.group + 7) / 8;
+      // (a cluster's parts lie in the ring, whose keys have been read when the warps' runs are joined)
+      if (bar_and(1, kQ4Consumers, got))
+        q4_unit<D, S>(A, piece, groups == 1 ? 4 : groups == 2 ? 2 : 1, ring, sQ, merge, full, empty, qempty, it,
+                      &s_abort, s_ml, s_count, reinterpret_cast<float*>(ring), s_part);
+    }
+  } else if (tid < A.group) {
+    s_part[tid] = make_float2(-INFINITY, 0.f);
+  }
+  if (parts > 1) {
+    cluster_sync();
+    for (int i = (int)rank * kQ4Threads + tid; i < A.group * (D / 8); i += (int)parts * kQ4Threads) {
+      const int rl = i / (D / 8), d0 = i % (D / 8) * 8;
+      const float* row = reinterpret_cast<const float*>(ring) + rl * D + d0;
+      float M = -INFINITY, L = 0.f, acc[8];
+      for (uint32_t k = 0; k < parts; ++k) M = fmaxf(M, cluster_load2(cluster_addr(&s_part[rl], k)).x);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) acc[x] = 0.f;
+      for (uint32_t k = 0; k < parts; ++k) {
+        const float2 ml = cluster_load2(cluster_addr(&s_part[rl], k));
+        if (ml.x == -INFINITY) continue;  // a part without keys of the row has none of it
+        const float f = exp2_approx(ml.x - M);
+        const uint32_t at = cluster_addr(row, k);
+        const float4 u = cluster_load4(at), v = cluster_load4(at + 16);
+        L += ml.y * f;
+        acc[0] += u.x * f; acc[1] += u.y * f; acc[2] += u.z * f; acc[3] += u.w * f;
+        acc[4] += v.x * f; acc[5] += v.y * f; acc[6] += v.z * f; acc[7] += v.w * f;
+      }
+      const float inv = L > 0.f ? 1.f / L : 0.f;
+      *reinterpret_cast<uint4*>(A.out + (int64_t)t * A.o_rs + (int64_t)(hk * A.group + rl) * A.o_hs + d0) =
+          make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
+                     pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
+    }
+    cluster_sync();  // a part is read by the others until here
   }
   __syncthreads();
   if (tid == 0 && s_abort) {
