@@ -381,7 +381,7 @@ def sdpa_varlen_splitk_static(q: torch.Tensor, k_store: torch.Tensor, v_store: t
 # A decode step calls these once a layer and its kernels take a few microseconds, so the checks read
 # each tensor's attributes once and the device and stream come as plain numbers.
 
-_bf16, _i32, _u8 = torch.bfloat16, torch.int32, torch.uint8
+_bf16, _f32, _i32, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
 def _device_of(*tensors) -> int:
@@ -424,51 +424,55 @@ def _rows_like(like: torch.Tensor, shape, stream) -> torch.Tensor:
 
 def _strides(name: str, t: torch.Tensor, shape=None):
     """Row and head strides of bf16 rows [T, heads, D], checked against `shape` when it is given."""
-    if t.dim() != 3 or t.dtype != _bf16:
+    strides = t.stride()
+    if t.dtype is not _bf16 or len(strides) != 3:
         raise ValueError(f"{name} must be bf16 [T, heads, D], not {t.dtype} {list(t.shape)}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
-    rs, hs, inner = t.stride()
-    if inner != 1:
+    if strides[2] != 1:
         raise ValueError(f"{name} must have unit inner stride")
-    return rs, hs
+    return strides[0], strides[1]
 
 
 def _status_ptr(status: Optional[torch.Tensor]):
     if status is None:
         return None
-    if status.dtype != _i32 or status.numel() < 1:
+    if status.dtype is not _i32 or status.numel() < 1:
         raise ValueError("status must be an int32 tensor")
     return status.data_ptr()
 
 
 def _table(seq_info: torch.Tensor, seg_mode: Optional[torch.Tensor]):
     """(seq_info pointer, seg_mode pointer, segments) of a segment table."""
-    S = seq_info.shape[0] if seq_info.dim() else 0
-    if seq_info.dtype != _i32 or not seq_info.is_contiguous() or (seq_info.numel() and
-                                                                  (seq_info.dim() != 2 or seq_info.shape[1] != 4)):
+    shape = seq_info.shape
+    S = shape[0] if shape else 0
+    if seq_info.dtype is not _i32 or not seq_info.is_contiguous() or \
+            (len(shape) != 2 or shape[1] != 4) and seq_info.numel():
         raise ValueError("seq_info must be a contiguous int32 [S, 4] tensor")
     if seg_mode is not None:
-        if seg_mode.dtype != _i32 or not seg_mode.is_contiguous() or (S and tuple(seg_mode.shape) != (S, 2)):
+        if seg_mode.dtype is not _i32 or not seg_mode.is_contiguous() or (S and seg_mode.shape != (S, 2)):
             raise ValueError("seg_mode must be a contiguous int32 [S, 2] tensor")
-    if not S or not seq_info.numel():
+    if not S or len(shape) != 2 or shape[1] != 4:
         return None, None, 0
     return seq_info.data_ptr(), None if seg_mode is None else seg_mode.data_ptr(), S
 
 
 def _rotation(table: torch.Tensor, positions: Optional[torch.Tensor], sections: Optional[Sequence[int]],
               interleaved: bool, T: int) -> bytes:
-    if table.dim() != 3 or table.shape[2] != 2 or table.dtype != torch.float32 or not table.is_contiguous():
+    shape = table.shape
+    if len(shape) != 3 or shape[2] != 2 or table.dtype is not _f32 or not table.is_contiguous():
         raise ValueError("table must be contiguous fp32 [positions, rotated pairs, 2]")
-    P, half, _ = table.shape
-    sections = (half,) if sections is None else tuple(sections)
-    axes = len(sections)
-    if not 1 <= axes <= 4:
-        raise ValueError(f"sections has {axes} position axes: 1 to 4")
+    P, half, _ = shape
+    if sections is None:
+        sections, axes = (half,), 1
+    else:
+        axes = len(sections)
+        if not 1 <= axes <= 4:
+            raise ValueError(f"sections has {axes} position axes: 1 to 4")
     ptr = stride = 0
     if positions is not None:
         shape = positions.shape
-        if positions.dtype != _i32 or not (shape == (axes, T) or (axes == 1 and shape == (T,))) or \
+        if positions.dtype is not _i32 or not (shape == (axes, T) or (axes == 1 and shape == (T,))) or \
                 (T > 1 and positions.stride(-1) != 1):
             raise ValueError(f"positions must be int32 [{axes}, {T}] with unit inner stride")
         ptr, stride = positions.data_ptr(), positions.stride(0) if axes > 1 else 0
@@ -539,9 +543,9 @@ def _q4(store: Q4Store):
     if len(shape) != 4 or vc.shape != shape or ks.shape != vs.shape or \
             ks.shape != (shape[0], shape[1], shape[2], shape[3] // 16):
         raise ValueError("a 4-bit store is codes [cols, Hkv, rows, D / 2] and scales [cols, Hkv, rows, D / 32], twice")
-    for t in store:
-        if t.dtype != _u8 or not t.is_contiguous():
-            raise ValueError("a 4-bit store's tensors must be contiguous uint8")
+    if not (kc.dtype is ks.dtype is vc.dtype is vs.dtype is _u8 and kc.is_contiguous() and ks.is_contiguous() and
+            vc.is_contiguous() and vs.is_contiguous()):
+        raise ValueError("a 4-bit store's tensors must be contiguous uint8")
     cols, Hkv, rows, half = shape
     return rows, cols, Hkv, 2 * half, _Q4_POINTERS.pack(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr())
 
