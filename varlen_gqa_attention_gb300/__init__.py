@@ -501,7 +501,8 @@ def sdpa_rope(x: torch.Tensor, table: torch.Tensor, positions: torch.Tensor, *,
     first 2 * pairs dims are turned.  positions: int32 [T], or [axes, T] with ``sections`` = the
     number of pairs of each axis (for example time, height and width).  Pairs are dims
     (j, j + pairs), or (2j, 2j + 1) when ``interleaved``.  ``inverse`` turns the other way: the
-    gradient.  Rows with a position outside the table are 0 and set ROPE_BAD_POS in ``status``."""
+    gradient (no autograd graph is kept: a training step turns the output's gradient back with the
+    same positions and ``inverse``).  Rows with a position outside the table are 0 and set ROPE_BAD_POS in ``status``."""
     rs, hs = _strides("x", x)
     shape = x.shape
     T, H, D = shape
