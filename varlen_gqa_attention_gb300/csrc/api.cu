@@ -462,8 +462,9 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
                                  q4 && D <= 128 ? &tile : nullptr);
   if (ws_bytes < need)
     return fail(SDPA_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need);
+  const int parts = q4 ? q4_direct(di, T, Hq, Hkv, D, S, rows, causal, window, S > 0 ? seg_mode : nullptr) : 0;
   Q4StageArgs sg{};
-  if (q4) {  // as many staged columns as the workspace holds
+  if (q4 && parts == 0) {  // as many staged columns as the workspace holds
     const int64_t col = q4_stage_bytes_per_column(rows, Hkv, D);  // (a multiple of 256)
     sg.pf_cols = (int)std::min<int64_t>(q4_stage_cols(T, Hq, Hkv, D, S, rows), (int64_t)(ws_bytes - need) / (2 * col));
     sg.k = (__nv_bfloat16*)((char*)ws + need);
@@ -539,7 +540,6 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
     apw = *ap;
     apw.segs = W.segs;
   }
-  const int parts = q4 ? q4_direct(di, T, Hq, Hkv, D, S, rows, causal, window, sa.seg_mode) : 0;
   if (parts > 0) {
     Q4DirectArgs da{{aa, *q4, 0}, S > 0 ? seq_info : nullptr, sa.seg_mode, S};
     void* args[] = {(void*)&da};

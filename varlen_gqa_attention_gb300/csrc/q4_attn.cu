@@ -448,8 +448,8 @@ __device__ __forceinline__ void q4_load(const Q4AttnArgs& G, char* ring, char* s
   walk_begin(wk, A.ws, kRouteSplitk, kSkQ4Few);
   UnitRec ur;
   int64_t ta, tb;
-  uint32_t it = 0, n = 0;
-  for (;; ++n) {
+  uint32_t it = 0, sent = 0;  // stages filled, pieces whose rows were sent for
+  for (uint32_t n = 0;; ++n) {
     const bool more = walk_next(wk, ur, ta, tb);
     // (the rows' buffer is free once every warp has read them; the record of the piece before that is then no
     // longer in use)
@@ -474,13 +474,14 @@ __device__ __forceinline__ void q4_load(const Q4AttnArgs& G, char* ring, char* s
     }
     __syncwarp();
     if (!more) return;
+    sent = n + 1;
     if (!q4_load_piece<D, S>(G, ur, r0, pos_lo, pos_hi, ring, sQ, full, empty, qfull, it, abort)) break;
   }
   // gave up: no copy of this CTA may still be in flight when it ends
   int none = 0;
   for (uint32_t k = it > S::kStages ? it - S::kStages : 0; k < it; ++k)
     mbar_wait(full + 8 * (k % S::kStages), (k / S::kStages) & 1, &none);
-  if (n > 0) mbar_wait(qfull, (n - 1) & 1, &none);
+  if (sent > 0) mbar_wait(qfull, (sent - 1) & 1, &none);
 }
 
 template <int D>
