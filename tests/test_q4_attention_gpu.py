@@ -578,3 +578,31 @@ def test_the_workspace_status_of_a_call_without_a_schedule(dev):
         pkg.sdpa_varlen_q4(q, store, torch.tensor(seq, dtype=torch.int32, device=dev), causal=True, workspace=ws)
         _, _, _, want = O.visible_interval(np.array(seq), 4, True, 0, 64, 2, None)
         assert pkg.workspace_status(ws) == want
+
+
+@pytest.mark.parametrize("n,Hq", [(1, 4), (5, 4), (3, 8)])
+def test_more_segments_than_the_scheduler_keeps_in_shared_memory(dev, n, Hq):
+    # 1100 segments, columns shared by many, one of them longer, some invalid, two overlapping
+    S_ = 1100
+    seq, t = [], 0
+    for i in range(S_):
+        m = 150 if i == 700 else n
+        seq.append([t, m, (7 * i) % 31, max(m, 1 + (13 * i) % 160)])
+        t += m
+    seq[3][2], seq[500][3], seq[900][0] = 31, -1, seq[899][0]
+    store, q = random_store(160, 31, 1, 64, n), queries(t, Hq, 64, 70)
+    chunk = seq[700][0]
+    rows = sorted({0, t - 1, chunk - 1, chunk, chunk + 77, chunk + 149, chunk + 150} |
+                  {seq[i][0] + j for i in (3, 4, 500, 501, 898, 899, 901, 1099) for j in range(n)} |
+                  {seq[900][0], seq[901][0] - 1})
+    for causal, window in ((True, 0), (False, 0), (True, 11)):
+        got, st = run_q4(q, store, seq, dev, causal=causal, window=window)
+        check(got, st, q, store, seq, causal, window, p_step=2.0 ** -8, rows_subset=rows)
+
+
+def test_staged_route_more_segments_than_the_scheduler_keeps_in_shared_memory(dev, prefill_route):
+    seq = [[2 * i, 2, (5 * i) % 29, 2 + (11 * i) % 150] for i in range(1100)]
+    seq[8][2] = 40
+    store, q = random_store(160, 29, 1, 64, 71), queries(2200, 2, 64, 71)
+    got, st = run_q4(q, store, seq, dev, causal=True)
+    check(got, st, q, store, seq, True, p_step=2.0 ** -8, rows_subset=[0, 1, 15, 16, 17, 1000, 1001, 2198, 2199])
