@@ -294,8 +294,8 @@ static int q4_direct(const DevInfo& di, int64_t T, int Hq, int Hkv, int D, int S
 // The prefill route over a 4-bit store: its columns are staged first, which many rows have to pay for, and the
 // route it competes with is the tensor-memory kernel of q4_tile.cu, where that one runs.  Split-K / prefill, 32/8
 // heads, D = 128, in us: one segment over 4096 keys, 128 rows a head 37 / 39, 256 rows 48 / 47, 512 rows
-// 69 / 65, 2048 rows 160 / 135; 128 rows over 32768 keys 113 / 146, 512 rows 316 / 266; four segments of 128 rows
-// over 4096 keys 82 / 98.  At D = 256 the split-K kernel converts a key again for every 8 rows: 64 rows a head
+// 70 / 65, 2048 rows 168 / 136; 128 rows over 32768 keys 92 / 143, 512 rows 292 / 265; four segments of 128 rows
+// over 4096 keys 73 / 102, sixteen 206 / 259.  At D = 256 the split-K kernel converts a key again for every 8 rows: 64 rows a head
 // over 4096 keys 76 / 45.
 // So the bf16 entry's thresholds hold where the tensor-memory one is not launched, and 512 rows where the
 // schedule takes the other one: 64 tokens over 16384 to 32768 keys beside 250 over 32768 842 / 579 us (fewer
