@@ -26,7 +26,9 @@
 // shared memory two fifths.  64 segments over 6144 keys on average, 8 KV heads, D = 128: 24 rows 150 us, 64
 // rows 158 us.  With the rows packed (the softmax of 32 rows all in one quarter, on one scheduler) and four
 // converting warps: 221 and 205 us.  (Products of 64 rows instead of 128, and codes read without bank
-// conflicts, came to the same; so did rows copied to every quarter, each with its share of the keys.)
+// conflicts, came to the same; so did rows copied to every quarter, each with its share of the keys, and one
+// team converting K and the other V.  Softmax teams that take whole tiles in turn: 203 us for 64 rows: the chain
+// scores - probabilities - product of a tile is then longer, and two tiles in flight do not hide it.)
 #include "q4.cuh"
 #include "tc.cuh"
 
