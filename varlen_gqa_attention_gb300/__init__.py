@@ -415,11 +415,14 @@ def _call(entry, dev: int, stream, *args) -> None:
 
 def _rows_like(like: torch.Tensor, shape, stream) -> torch.Tensor:
     """Uninitialised bf16 rows on `like`'s device, of memory that belongs to the stream that will
-    write them."""
+    write them.  The current stream's work on them counts too before that memory serves again: the
+    caller reads them there."""
     if stream is None:
         return torch.empty(shape, dtype=_bf16, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=_bf16, device=like.device)
+        rows = torch.empty(shape, dtype=_bf16, device=like.device)
+    rows.record_stream(torch.cuda.current_stream(like.device))
+    return rows
 
 
 def _strides(name: str, t: torch.Tensor, shape=None):
