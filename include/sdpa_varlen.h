@@ -293,15 +293,15 @@ sdpa_status sdpa_fourbit_unpack(const sdpa_q4_store* store, int64_t rows, int co
                            int32_t* status_dev, void* stream);
 
 /* Bytes of device workspace sdpa_varlen_fourbit takes for up to T rows and S segments of a store of
- * these sizes.  Long chunks have their columns staged in it in bf16, up to 2 GiB of them (or one of up to
+ * these sizes.  Long chunks have their columns staged in it in 16 bits, up to 2 GiB of them (or one of up to
  * 8 GiB), as this call of T rows and S segments may have under the present route policy; a call stages as
  * many as its workspace holds, and the other segments take the split-K route.  Two calls that may run at the
  * same time, captured or not, need one each. */
 size_t sdpa_varlen_fourbit_workspace_bytes(int64_t T, int Hq, int Hkv, int D, int S, int64_t rows, int cols);
 
 /*
- * sdpa_varlen over a 4-bit store: the attention of the values the codes stand for.  seg_mode is NULL,
- * or [S, 2] (causal, window) per segment as for sdpa_varlen_modes, replacing causal and window.
+ * sdpa_varlen over a 4-bit store: the attention of the values the codes stand for, with probabilities
+ * rounded to fp16 (2^-11 of each) whichever kernel a segment takes.  seg_mode is NULL, or [S, 2] (causal, window) per segment as for sdpa_varlen_modes, replacing causal and window.
  * Arguments, checks and status bits otherwise as for sdpa_varlen, with the store's own (pointers
  * 16-byte aligned, rows a multiple of 16), scale >= 0, and workspace of at least
  * sdpa_varlen_fourbit_workspace_bytes bytes.

@@ -123,9 +123,11 @@ static sdpa_status device_info(DevInfo* out) {
         e = cudaFuncSetAttribute(combine_kernel_ptr(Ds[k], q), cudaFuncAttributePreferredSharedMemoryCarveout, 100);
         if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "carveout attribute: %s", cudaGetErrorString(e));
       }
-      const void* pf = prefill_kernel_ptr(Ds[k]);
-      e = cudaFuncSetAttribute(pf, cudaFuncAttributeMaxDynamicSharedMemorySize, prefill_smem_bytes(Ds[k]));
-      if (e == cudaSuccess) e = cudaFuncSetAttribute(pf, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+      for (int f16 = 0; f16 < 2 && e == cudaSuccess; ++f16) {
+        const void* pf = prefill_kernel_ptr(Ds[k], f16);
+        e = cudaFuncSetAttribute(pf, cudaFuncAttributeMaxDynamicSharedMemorySize, prefill_smem_bytes(Ds[k]));
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(pf, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+      }
       di.prefill_ok[k] = e == cudaSuccess;
       if (e != cudaSuccess) cudaGetLastError();  // leave no sticky error; split-K covers it
     }
@@ -157,7 +159,7 @@ static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 // 64 dims x 1 head x 1 column x `bn` rows), all with 128-byte swizzle.
 static bool make_tensor_maps(const void* q, int64_t T, int Hq, int D, int64_t q_rs, int64_t q_hs,
                              const void* k, const void* v, int64_t rows, int cols, int Hkv, int group,
-                             int bn, CUtensorMap* mq, CUtensorMap* mk, CUtensorMap* mv) {
+                             int bn, bool v_f16, CUtensorMap* mq, CUtensorMap* mk, CUtensorMap* mv) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc || T <= 0 || q_hs <= 0 || q_rs <= 0) return false;
   const cuuint32_t es[4] = {1, 1, 1, 1};
@@ -172,7 +174,7 @@ static bool make_tensor_maps(const void* q, int64_t T, int Hq, int D, int64_t q_
   const cuuint64_t kstr[3] = {(cuuint64_t)D * 2, (cuuint64_t)Hkv * D * 2, (cuuint64_t)cols * Hkv * D * 2};
   const cuuint32_t kbox[4] = {64, 1, 1, (cuuint32_t)bn};
   for (int w = 0; w < 2; ++w) {
-    if (enc(w ? mv : mk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, (void*)(w ? v : k), kdim, kstr, kbox, es,
+    if (enc(w ? mv : mk, w && v_f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, (void*)(w ? v : k), kdim, kstr, kbox, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return false;
@@ -307,7 +309,7 @@ static int q4_prefill_min_rows(Q4Split sp) {
 static float q4_prefill_min_work(Q4Split sp) { return sp == Q4Split::kFew ? kPrefillMinWork : 4 * kPrefillMinWork; }
 // Packed rows of a call's longest segment when none is empty.
 static int64_t q4_longest(int64_t T, int group, int S) { return std::max<int64_t>(1, T - std::max(S, 1) + 1) * group; }
-// Columns a 4-bit call stages in bf16 for the prefill kernel: one per segment that can have
+// Columns a 4-bit call stages in 16 bits for the prefill kernel: one per segment that can have
 // q4_prefill_min_rows, as far as 2 GiB of workspace hold them (at least one while that takes at most 8 GiB); none
 // when the automatic route cannot reach q4_prefill_min_work.  Depends on sizes and the route policy only.
 static int64_t q4_stage_bytes_per_column(int64_t rows, int Hkv, int D) { return rows * Hkv * D * 2; }
@@ -395,7 +397,7 @@ static sdpa_status launch_all(const SchedArgs& sa, const AttnArgs& aa, int D, co
     pa.rows = sa.rows_pf;
     void* args[] = {(void*)&pa, (void*)&tm.q, (void*)&tm.k, (void*)&tm.v};
     const bool chained = packed < (int64_t)kPrefillRows * std::max(sa.S, 1);
-    e = launch_k(prefill_kernel_ptr(D), (unsigned)g.prefill, prefill_block_threads(D), args,
+    e = launch_k(prefill_kernel_ptr(D, q4 != nullptr), (unsigned)g.prefill, prefill_block_threads(D), args,
                  prefill_smem_bytes(D), st, chained);
     if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "prefill launch: %s", cudaGetErrorString(e));
   }
@@ -468,7 +470,7 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
     const int64_t col = q4_stage_bytes_per_column(rows, Hkv, D);  // (a multiple of 256)
     sg.pf_cols = (int)std::min<int64_t>(q4_stage_cols(T, Hq, Hkv, D, S, rows), (int64_t)(ws_bytes - need) / (2 * col));
     sg.k = (__nv_bfloat16*)((char*)ws + need);
-    sg.v = (__nv_bfloat16*)((char*)ws + need + col * sg.pf_cols);
+    sg.v = (__half*)((char*)ws + need + col * sg.pf_cols);
   }
 
   SchedArgs sa{};
@@ -505,7 +507,7 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
   sa.rows_pf = q4 && window > 0 && !sa.seg_mode ? std::min<int64_t>(rows, T + window - 1) : rows;
   sa.prefill_ok = (!q4 || sg.pf_cols > 0) && di.prefill_ok[d_index(D)] && group_fits && prefill_launch(sa, T) &&
                   make_tensor_maps(q, T, Hq, D, q_rs, q_hs, q4 ? sg.k : k, q4 ? sg.v : v, sa.rows_pf,
-                                   q4 ? sg.pf_cols : cols, Hkv, group, sa.tile_pf, &tm.q, &tm.k, &tm.v);
+                                   q4 ? sg.pf_cols : cols, Hkv, group, sa.tile_pf, q4 != nullptr, &tm.q, &tm.k, &tm.v);
   if (!sa.prefill_ok) sa.pf_cols = 0;
   sa.grid[0] = 0;
   sa.grid[2] = g.prefill;

@@ -268,8 +268,8 @@ const void* splitk_kernel_ptr(int D);
 int splitk_smem_bytes(int D);
 const void* combine_kernel_ptr(int D, bool q4);
 const void* combine_pair_kernel_ptr(int D);  // a CTA per (row, head) pair
-const void* prefill_kernel_ptr(int D);
-const void* prefill_pair_kernel_ptr(int D);  // D = 64, 128
+const void* prefill_kernel_ptr(int D, bool f16);  // f16: V is fp16
+const void* prefill_pair_kernel_ptr(int D, bool f16);  // D = 64, 128
 int prefill_pair_smem_bytes(int D);
 int prefill_pair_block_threads(int D);
 int prefill_smem_bytes(int D);

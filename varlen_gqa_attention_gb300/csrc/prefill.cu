@@ -35,6 +35,7 @@
 // unwinds, frees its tensor memory and exits.
 #include <cuda.h>
 
+#include "q4.cuh"
 #include "tc.cuh"
 
 namespace sdpa {
@@ -48,7 +49,7 @@ struct PfCfg {
   static constexpr int NREG = D / 64;                     // 64-element (128-byte) column regions
   static constexpr int Q_BYTES = BM * D * 2;
   static constexpr int KV_BYTES = BN * D * 2;             // K (or V) of one stage
-  // Tensor memory: S_b fp32 [b*BN, (b+1)*BN); P_b as bf16 pairs [P_COL + b*BN/2, +BN/2);
+  // Tensor memory: S_b fp32 [b*BN, (b+1)*BN); P_b as pairs [P_COL + b*BN/2, +BN/2);
   // one O accumulator of D columns.  Two softmax warpgroups split every tile's key columns.
   static constexpr int S_COL0 = 0;
   static constexpr int P_COL = 2 * BN;
@@ -135,7 +136,8 @@ __device__ __forceinline__ bool pf_next(PieceWalk& w, PfPiece& pc, int64_t rows)
   return true;
 }
 
-template <int D>
+// F16: P and V are fp16 (V of staged columns, see q4_stage.cu), P held 2^kQ4PLift times larger, its sum too.
+template <int D, bool F16>
 __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
     sdpa_prefill_kernel(const AttnArgs A, const __grid_constant__ CUtensorMap tmQ,
                         const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
@@ -296,7 +298,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
     // each MMA and commit.
     {
       constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, C::BN, false, false);
-      constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, false, true);
+      constexpr uint32_t IDESC_PV = F16 ? idesc_f16_f32(128, D, false, true) : idesc_bf16_f32(128, D, false, true);
       PieceWalk wk;
       walk_begin(wk, A.ws, kRoutePrefill);
       PfPiece pc;
@@ -534,8 +536,8 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
           okp = okp && __all_sync(0xffffffffu, pv_done(g2));
         }
         tc_fence_after();
-        const float nmu = m_use == -INFINITY ? 0.f : -m_use;
-        // p = 2^(scale*s - m) (masked columns give 0), row sum; P as bf16 pairs into P_b
+        const float nmu = m_use == -INFINITY ? 0.f : F16 ? kQ4PLift - m_use : -m_use;
+        // p = 2^(scale*s - m) (masked columns give 0), row sum; P as pairs into P_b
         float sum8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         uint32_t pw[C::HALF / 2];
 #pragma unroll
@@ -544,7 +546,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
           fma2f(a0, a1, x[2 * k], x[2 * k + 1], sl2, nmu);
           const float p0 = exp2_approx(a0), p1 = exp2_approx(a1);
           add2f(sum8[(2 * k) & 7], sum8[(2 * k + 1) & 7], p0, p1);
-          pw[k] = pack_bf16x2(p0, p1);
+          pw[k] = F16 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
         }
         if (okp) {
           if constexpr (C::HALF == 64)
@@ -618,13 +620,10 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
   if (warp == W_MMA) tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
-template __global__ void sdpa_prefill_kernel<256>(const AttnArgs, const __grid_constant__ CUtensorMap,
-                                                  const __grid_constant__ CUtensorMap,
-                                                  const __grid_constant__ CUtensorMap);
-
 // The prefill kernel of a head dim: this one at D = 256, the two-tile kernel otherwise.
-const void* prefill_kernel_ptr(int D) {
-  return D == 256 ? (const void*)sdpa_prefill_kernel<256> : prefill_pair_kernel_ptr(D);
+const void* prefill_kernel_ptr(int D, bool f16) {
+  if (D != 256) return prefill_pair_kernel_ptr(D, f16);
+  return f16 ? (const void*)sdpa_prefill_kernel<256, true> : (const void*)sdpa_prefill_kernel<256, false>;
 }
 int prefill_smem_bytes(int D) { return D == 256 ? PfCfg<256>::SMEM : prefill_pair_smem_bytes(D); }
 int prefill_block_threads(int D) { return D == 256 ? PfCfg<256>::THREADS : prefill_pair_block_threads(D); }

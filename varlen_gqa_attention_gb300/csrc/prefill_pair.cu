@@ -41,6 +41,7 @@
 // its MMAs, and the CTA frees its tensor memory and exits.
 #include <cuda.h>
 
+#include "q4.cuh"
 #include "tc.cuh"
 
 namespace sdpa {
@@ -187,7 +188,7 @@ struct PpLoopOut {
 
 // The softmax of one piece for one row of half h: per key tile, wait for S_h, read the row's
 // 128 scores, mask, keep the running max (rescaling O_h lazily), write P_h and signal it.
-template <int D>
+template <int D, bool F16>
 __device__ __noinline__ PpLoopOut pp_softmax_tiles(const PpLoop lp, volatile int* abort) {
   constexpr int BN = kPrefillTile;
   const uint32_t b_s = lp.bars + 8u * (uint32_t)(PpBars::S_FULL + lp.h);
@@ -234,8 +235,8 @@ __device__ __noinline__ PpLoopOut pp_softmax_tiles(const PpLoop lp, volatile int
       l *= f;
       m_use = m_new;
     }
-    const float nmu = m_use == -INFINITY ? 0.f : -m_use;
-    // p = 2^(scale*s - m) (masked columns give 0), row sum; P as bf16 pairs over S_h, in four
+    const float nmu = m_use == -INFINITY ? 0.f : F16 ? kQ4PLift - m_use : -m_use;
+    // p = 2^(scale*s - m) (masked columns give 0), row sum; P as pairs over S_h, in four
     // stores of 16 columns as they are ready (one wait for all of them)
     float sum4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -248,7 +249,7 @@ __device__ __noinline__ PpLoopOut pp_softmax_tiles(const PpLoop lp, volatile int
         pp_fma2(a0, a1, x[e], x[e + 1], lp.sl2, nmu);
         const float p0 = exp2_approx(a0), p1 = exp2_approx(a1);
         pp_add2(sum4[(2 * k) & 3], sum4[(2 * k + 1) & 3], p0, p1);
-        pw[k] = pack_bf16x2(p0, p1);
+        pw[k] = F16 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
       }
       tmem_st16u_nowait(lp.t_s + 16 * c, pw);
     }
@@ -279,7 +280,8 @@ __device__ __noinline__ PpLoopOut pp_softmax_tiles(const PpLoop lp, volatile int
   return out;
 }
 
-template <int D>
+// F16: P and V are fp16 (V of staged columns, see q4_stage.cu), P held 2^kQ4PLift times larger, its sum too.
+template <int D, bool F16>
 __global__ void __launch_bounds__(PpCfg<D>::THREADS, 1)
     sdpa_prefill_pair_kernel(const AttnArgs A, const __grid_constant__ CUtensorMap tmQ,
                              const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
@@ -444,7 +446,7 @@ __global__ void __launch_bounds__(PpCfg<D>::THREADS, 1)
     // The whole warp runs this loop with warp-uniform values; one elected lane issues each
     // MMA and commit.
     constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, C::BN, false, false);
-    constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, false, true);
+    constexpr uint32_t IDESC_PV = F16 ? idesc_f16_f32(128, D, false, true) : idesc_bf16_f32(128, D, false, true);
     constexpr int KS = D / 16, KP = C::BN / 16;  // k-steps of S and of PV
     PieceWalk wk;
     walk_begin(wk, A.ws, kRoutePrefill);
@@ -613,7 +615,7 @@ __global__ void __launch_bounds__(PpCfg<D>::THREADS, 1)
       lp.sl2 = A.scale_log2;
       lp.bars = sBar;
       lp.h = h;
-      const PpLoopOut lo = pp_softmax_tiles<D>(lp, abort);
+      const PpLoopOut lo = pp_softmax_tiles<D, F16>(lp, abort);
       ok = lo.ok;
       if (!ok) break;
       g += lp.n;
@@ -668,16 +670,11 @@ __global__ void __launch_bounds__(PpCfg<D>::THREADS, 1)
   if (warp == W_MMA) tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
-template __global__ void sdpa_prefill_pair_kernel<64>(const AttnArgs, const __grid_constant__ CUtensorMap,
-                                                      const __grid_constant__ CUtensorMap,
-                                                      const __grid_constant__ CUtensorMap);
-template __global__ void sdpa_prefill_pair_kernel<128>(const AttnArgs, const __grid_constant__ CUtensorMap,
-                                                       const __grid_constant__ CUtensorMap,
-                                                       const __grid_constant__ CUtensorMap);
-
-const void* prefill_pair_kernel_ptr(int D) {
-  return D == 64 ? (const void*)sdpa_prefill_pair_kernel<64> : (const void*)sdpa_prefill_pair_kernel<128>;
+template <bool F16>
+static const void* pair_ptr(int D) {
+  return D == 64 ? (const void*)sdpa_prefill_pair_kernel<64, F16> : (const void*)sdpa_prefill_pair_kernel<128, F16>;
 }
+const void* prefill_pair_kernel_ptr(int D, bool f16) { return f16 ? pair_ptr<true>(D) : pair_ptr<false>(D); }
 int prefill_pair_smem_bytes(int D) { return D == 64 ? PpCfg<64>::SMEM : PpCfg<128>::SMEM; }
 int prefill_pair_block_threads(int D) { return D == 64 ? PpCfg<64>::THREADS : PpCfg<128>::THREADS; }
 

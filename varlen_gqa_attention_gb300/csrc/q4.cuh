@@ -67,17 +67,6 @@ __device__ __forceinline__ void q4_scales_bf16(uint32_t b, __nv_bfloat162* s2, _
   *z2 = __hmul2(*s2, __float2bfloat162_rn(-136.f));
 }
 
-// The 8 bf16 values of one word of codes, in dim order.
-__device__ __forceinline__ uint4 q4_words8(uint32_t w, uint32_t scale_byte) {
-  __nv_bfloat162 s2, z2;
-  q4_scales_bf16(scale_byte, &s2, &z2);
-  uint32_t x[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = q4_pair_bf16(w >> (4 * i), kQ4Bf16, s2, z2);  // dims i and i + 4
-  return make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410),
-                    __byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632));
-}
-
 // Two fp16 values from nibbles shifted to bits 6-9 and 22-25: 0x4800 | c << 6 is 8 + c / 2, and
 // (8 + c / 2) 2s - 24 s = (c - 8) s; 24 s <= 46080 has 5 significant bits.
 constexpr uint32_t kQ4F16 = 0x48004800u;
@@ -90,6 +79,27 @@ __device__ __forceinline__ uint32_t q4_pair_f16(uint32_t w, uint32_t bits, __hal
 __device__ __forceinline__ void q4_scales_f16(uint32_t a, uint32_t b, __half2* s2, __half2* z2) {
   *s2 = __floats2half2_rn(q4_scale2(a), q4_scale2(b));
   *z2 = __hmul2(*s2, __float2half2_rn(-12.f));
+}
+
+// Pairs of nibbles i and i + 4 of a word, in dim order.
+__device__ __forceinline__ uint4 q4_in_order(const uint32_t (&x)[4]) {
+  return make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410),
+                    __byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632));
+}
+// The 8 values of one word of codes, in dim order, as bf16 and as fp16.
+__device__ __forceinline__ uint4 q4_words8(uint32_t w, uint32_t scale_byte) {
+  __nv_bfloat162 s2, z2;
+  q4_scales_bf16(scale_byte, &s2, &z2);
+  const uint32_t x[4] = {q4_pair_bf16(w, kQ4Bf16, s2, z2), q4_pair_bf16(w >> 4, kQ4Bf16, s2, z2),
+                         q4_pair_bf16(w >> 8, kQ4Bf16, s2, z2), q4_pair_bf16(w >> 12, kQ4Bf16, s2, z2)};
+  return q4_in_order(x);
+}
+__device__ __forceinline__ uint4 q4_words8_f16(uint32_t w, uint32_t scale_byte) {
+  __half2 s2, z2;
+  q4_scales_f16(scale_byte, scale_byte, &s2, &z2);
+  const uint32_t x[4] = {q4_pair_f16(w << 6, kQ4F16, s2, z2), q4_pair_f16(w << 2, kQ4F16, s2, z2),
+                         q4_pair_f16(w >> 2, kQ4F16, s2, z2), q4_pair_f16(w >> 6, kQ4F16, s2, z2)};
+  return q4_in_order(x);
 }
 
 // 8 dims of a query row (16 bytes) as the operand words of two k-steps: the conversion of K pairs
@@ -139,8 +149,8 @@ struct Q4DirectArgs {
   int S;
 };
 
-// The keys and values of the prefill route's segments, brought to bf16 for the tensor-memory kernel:
-// position p of the segment with staged column c goes to row p % rows_pf of column c of a bf16
+// The keys and values of the prefill route's segments, brought to bf16 and fp16 for the tensor-memory kernel:
+// position p of the segment with staged column c goes to row p % rows_pf of column c of a 16-bit
 // column store [rows_pf, pf_cols, Hkv, D] (q4_stage.cu).
 struct Q4StageArgs {
   const SegRec* segs;  // the scheduler's records
@@ -148,7 +158,7 @@ struct Q4StageArgs {
   int64_t rows, rows_pf;
   Q4Store st;
   __nv_bfloat16* k;
-  __nv_bfloat16* v;
+  __half* v;
 };
 constexpr int kQ4StageThreads = 256;
 const void* q4_stage_kernel_ptr(int D);

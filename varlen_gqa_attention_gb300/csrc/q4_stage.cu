@@ -1,9 +1,11 @@
-// q4_stage.cu - keys and values of the prefill route's segments brought from 4 bits to bf16.
+// q4_stage.cu - keys and values of the prefill route's segments brought from 4 bits to 16.
 //
 // The tensor-memory prefill kernel reads its K and V tiles by TMA, many times over (once per block
-// of query rows), so a long chunk's keys are converted once, exactly (every value of the 4-bit store
-// is a bf16 number), into a bf16 column store in the call's workspace, and the kernel that the bf16
-// entry uses runs over that.  Converting inside the kernel instead would repeat the conversion for
+// of query rows), so a long chunk's keys are converted once into a column store of 16-bit values in the
+// call's workspace, and the kernel that the bf16 entry uses runs over that.  The values are exact: K in
+// bf16, to be multiplied with bf16 queries, and V in fp16, to be multiplied with probabilities that are
+// rounded to fp16 as on the other routes (2^-11 of each; with bf16 ones, 2^-8, a 2048-token chunk over 32763
+// keys was off by 0.0023 of its norm where the output's own rounding is 0.0017).  Converting inside the kernel instead would repeat the conversion for
 // every 256 query rows, on the issue slots that its softmax needs.
 //
 // Bound by memory: D / 2 + D / 32 bytes read and 2 D written per key and KV head, twice.  A thread
@@ -57,7 +59,7 @@ __global__ void __launch_bounds__(kQ4StageThreads) sdpa_q4_stage_kernel(Q4StageA
     for (int u = 0; u < U; ++u) {
       if (dst[u] < 0) continue;
       *reinterpret_cast<uint4*>(A.k + dst[u]) = q4_words8(kw[u], kb[u]);
-      *reinterpret_cast<uint4*>(A.v + dst[u]) = q4_words8(vw[u], vb[u]);
+      *reinterpret_cast<uint4*>(A.v + dst[u]) = q4_words8_f16(vw[u], vb[u]);
     }
   }
 }

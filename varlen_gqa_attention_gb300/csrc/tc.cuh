@@ -182,6 +182,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn, b
          | ((uint32_t)(M >> 4) << 24);    // M / 16
 }
 
+// The same with fp16 A/B.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool a_mn, bool b_mn) {
+  return idesc_bf16_f32(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
+}
+
 // Shared-memory matrix descriptor, 128-byte swizzle (atoms of 8 rows x 128 bytes, rows
 // 1024-byte aligned): start address, leading-dimension and stride-dimension byte offsets.
 __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
