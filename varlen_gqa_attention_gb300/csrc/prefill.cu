@@ -580,7 +580,9 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
       const int64_t pidx = ur.slot_base + (int64_t)pc.slot * ur.rows + row;
       float* prow = A.ws.part_o[kRoutePrefill] + pidx * D + wg * (D / 2);
       // a row with no visible key has L = 0 and writes zeros (never 0 * O)
-      const bool empty = !(L > 0.f);
+      // (F16: a row whose scores are NaN has no maximum: it is joined as one, and comes out NaN)
+      const bool empty = F16 ? L == 0.f : !(L > 0.f);
+      if (F16 && L != L) m_use = 0.f;
       const float w = direct ? 1.f / L : 1.f;
 #pragma unroll 1
       for (int c = 0; c < D / 64; ++c) {

@@ -619,7 +619,8 @@ __global__ void __launch_bounds__(PpCfg<D>::THREADS, 1)
       ok = lo.ok;
       if (!ok) break;
       g += lp.n;
-      const float m_use = lo.m, l = lo.l;
+      // (F16: a row whose scores are NaN has no maximum: it is joined as one, and comes out NaN)
+      const float l = lo.l, m_use = F16 && l != l ? 0.f : lo.m;
       // epilogue: once the piece's last PV_h is done, normalise (direct) or write a partial
       ok = __all_sync(0xffffffffu, mbar_wait(bar(PpBars::PV_DONE + h), (g - 1) & 1, abort));
       if (!ok) break;
@@ -630,7 +631,7 @@ __global__ void __launch_bounds__(PpCfg<D>::THREADS, 1)
       const int64_t pidx = ur.slot_base + (int64_t)pc.slot * ur.rows + rl;
       float* prow = A.ws.part_o[kRoutePrefill] + pidx * D;
       // a row with no visible key has l = 0 and writes zeros (never 0 * O)
-      const bool empty = !(l > 0.f);
+      const bool empty = F16 ? l == 0.f : !(l > 0.f);
       const float w = direct ? (empty ? 0.f : 1.f / l) : 1.f;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
