@@ -504,11 +504,14 @@ def sdpa_rope(x: torch.Tensor, table: torch.Tensor, positions: torch.Tensor, *,
     first 2 * pairs dims are turned.  positions: int32 [T], or [axes, T] with ``sections`` = the
     number of pairs of each axis (for example time, height and width).  Pairs are dims
     (j, j + pairs), or (2j, 2j + 1) when ``interleaved``.  ``inverse`` turns the other way: the
-    gradient (no autograd graph is kept: a training step turns the output's gradient back with the
-    same positions and ``inverse``).  Rows with a position outside the table are 0 and set ROPE_BAD_POS in ``status``."""
+    gradient.  No autograd graph is kept: a training step turns the output's gradient back with the
+    same positions and ``inverse``, in a ``torch.autograd.Function`` of its own or by hand, and an x
+    that requires a gradient is refused while gradients are recorded.  Rows with a position outside the table are 0 and set ROPE_BAD_POS in ``status``."""
     rs, hs = _strides("x", x)
     shape = x.shape
     T, H, D = shape
+    if x.requires_grad and torch.is_grad_enabled():
+        raise ValueError("x requires a gradient, and no graph is kept: rotate x.detach(), and its gradient by inverse")
     if positions is None:
         raise ValueError("positions must be given")
     rot = _rotation(table, positions, sections, interleaved, T)
