@@ -14,3 +14,10 @@ def test_rows_that_want_a_gradient_are_refused():
     for x_ in (x.detach(), x):  # (what is next to refuse: no CUDA device)
         with torch.no_grad(), pytest.raises(ValueError, match="CUDA device"):
             pkg.sdpa_rope(x_, table, pos)
+
+
+@pytest.mark.parametrize("rot_dims", [0, -16, 17, 63, 24])
+def test_tables_of_other_than_whole_pairs_are_refused(rot_dims):
+    # 17 would be 8 pairs with the angles of 17 dims, which the entries cannot tell from 16
+    with pytest.raises(ValueError, match="rot_dims"):
+        pkg.rope_table(4, rot_dims)

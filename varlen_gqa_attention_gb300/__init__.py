@@ -487,7 +487,10 @@ def _rotation(table: torch.Tensor, positions: Optional[torch.Tensor], sections: 
 
 def rope_table(positions: int, rot_dims: int, base: float = 10000.0, device=None) -> torch.Tensor:
     """A rotation table fp32 [positions, rot_dims / 2, 2]: cos and sin of p * base ** (-2 j / rot_dims),
-    taken in 64 bits (a far position's angle needs them).  A program makes it once."""
+    taken in 64 bits (a far position's angle needs them).  rot_dims: a multiple of 16, as the entries
+    take it.  A program makes it once."""
+    if rot_dims <= 0 or rot_dims % 16:
+        raise ValueError(f"rot_dims must be a positive multiple of 16, not {rot_dims}")
     j = torch.arange(rot_dims // 2, dtype=torch.float64, device=device)
     p = torch.arange(positions, dtype=torch.float64, device=device)
     a = p[:, None] * base ** (-2.0 * j / rot_dims)
