@@ -265,8 +265,9 @@ sdpa_status sdpa_rope_append(const void* q, int64_t q_row_stride, int64_t q_head
  * it needs).  Position j of a column lives in store row j % rows, as in the bf16 store.
  * A group of 32 bf16 values x is stored under the scale nearest to max|x| times 1/7 (in fp32; ties to
  * the even byte), with codes 8 + clamp(round(x / scale), -7, 7), halves to even: no value is off by more than
- * half a step, 0.54 / 7 of its group's largest magnitude at most.  Magnitudes above 13440 saturate;
- * a NaN is stored as 0.
+ * half a step, which is 0.54 / 7 of its group's largest magnitude at most when that lies in
+ * [7 * 2^-21, 13440].  The smallest scale is 2^-21: in groups below 7 * 2^-21 (3.3e-6) a value may be off by
+ * 2^-22, and a group of at most 2^-22 becomes 0.  Magnitudes above 13440 saturate; a NaN is stored as 0.
  */
 typedef struct sdpa_q4_store {
   uint8_t* k_codes;

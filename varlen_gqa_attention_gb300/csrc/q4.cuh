@@ -31,7 +31,8 @@ __device__ __forceinline__ float q4_scale2(uint32_t b) { return __uint_as_float(
 // to the even byte), so that |x| / s <= 7 * 17/16 < 7.5 and no code is off by more than half a step.
 // The seventh is the fp32 product with 1 / 7: it decides groups within 2^-23 of a border, and is part
 // of the format's definition.
-// Magnitudes beyond 7 * 1920 take the largest scale and saturate; amax = 0 gives byte 0.
+// Magnitudes beyond 7 * 1920 take the largest scale and saturate; those below 7 * 2^-21 take byte 0, whose
+// half step is 2^-22.
 __device__ __forceinline__ uint32_t q4_scale_byte(float amax) {
   const uint32_t u = __float_as_uint(__fmul_rn(amax, 1.f / 7.f));
   const int32_t r = (int32_t)((u + 0x7FFFFu + ((u >> 20) & 1u)) >> 20) - (106 << 3);
