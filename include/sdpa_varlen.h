@@ -192,7 +192,7 @@ sdpa_status sdpa_causal_prefill(const void* q, const void* k, const void* v, int
  * position p (of the axis the pair belongs to) is turned by the angle whose cosine and sine are
  * table[p][j]: (a, b) -> (a cos - b sin, a sin + b cos).  Pairs are dims (j, j + rot_dims / 2), or
  * (2j, 2j + 1) when `interleaved`; dims from rot_dims on pass unchanged.  Results are taken in
- * fp32 (off by at most 2^-24 of |a cos| + |b sin| and of themselves) and rounded to bf16; those
+ * fp32 (off by at most 2^-24 of the sine's product and of themselves) and rounded to bf16; those
  * of keys on their way into a store are the exact ones rounded to fp32 and then to bf16.
  *  table       [table_rows, rot_dims / 2] pairs of fp32 (cos, sin), contiguous device memory,
  *              16-byte aligned, table_rows >= 1, at most 2^31 - 1 pairs.

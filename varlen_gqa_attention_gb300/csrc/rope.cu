@@ -6,7 +6,8 @@
 // orthogonal), so the backward pass is the same kernel with sin negated.  Dims beyond the rotated
 // ones pass unchanged.
 //
-// A result is fma(a, cos, -(b sin)) in fp32, off by at most 2^-24 of |a cos| + |b sin|, rounded to bf16.
+// A result is fma(a, cos, -(b sin)) in fp32, off by at most 2^-24 of |b sin| (that product's rounding) and
+// 2^-24 of itself, and is rounded to bf16 (the other one likewise: |a sin|).
 // For keys that is not enough: a 4-bit code changes by a whole step at its border, so the same input
 // has to fall on the same side of it whatever order a sum was taken in, and what the bf16 store
 // holds is what the 4-bit one quantises.  They are the exact results rounded to fp32 and then to
