@@ -296,7 +296,9 @@ sdpa_status sdpa_fourbit_unpack(const sdpa_q4_store* store, int64_t rows, int co
 /* Bytes of device workspace sdpa_varlen_fourbit takes for up to T rows and S segments of a store of
  * these sizes.  Long chunks have their columns staged in it in 16 bits, up to 2 GiB of them (or one of up to
  * 8 GiB), as this call of T rows and S segments may have under the present route policy; a call stages as
- * many as its workspace holds, and the other segments take the split-K route.  Two calls that may run at the
+ * many as its workspace holds, and the other segments take the split-K route.  Which kernels a call takes
+ * rests on T, S, rows and window, with an empty entry counted as a segment of one token: a table padded with
+ * empty entries computes the same, but a chunk in it may not get the kernels for chunks.  Two calls that may run at the
  * same time, captured or not, need one each. */
 size_t sdpa_varlen_fourbit_workspace_bytes(int64_t T, int Hq, int Hkv, int D, int S, int64_t rows, int cols);
 

@@ -196,7 +196,7 @@ static Grids grids_for(const DevInfo& di, int D) {
 // once for up to 128 packed rows, and the other one (q4_attn.cu), which converts a key again for every 8.
 // 64 segments over 6144 keys on average, 8 KV heads, D = 128, tensor-memory / other: 16 rows 150 / 131 us, 24
 // rows 150 / 303 us; 16 segments of 64 rows over 3100 keys 43 / 100 us.  The host knows how many rows the average
-// segment has: with at most 16 it launches the other one, with more (of several segments, which may be one
+// segment has (empty ones counted): with at most 16 it launches the other one, with more (of several segments, which may be one
 // chunk and many single tokens) both, and the schedule is the cheaper one's; the other leaves at once.  At
 // D = 256 the output of 128 rows leaves no room for the first.
 enum class Q4Split { kFew, kTile, kEither };
@@ -271,12 +271,17 @@ static cudaError_t launch_k(const void* f, unsigned grid, unsigned block, void**
 }
 
 // CTAs that share a (token, KV head) pair's keys when a 4-bit call takes the kernel without a schedule; 0 when it
-// does not.  It does where a CTA's share of the longest range possible is short, and there is at most one token a
-// segment, or the pairs' CTAs all fit the SMs at once.  The shares are halved while there are SMs for them and more
+// does not.  It does where a CTA's share of the longest range possible is short, and the table has an entry for every
+// token or more, or the pairs' CTAs all fit the SMs at once.  The host sees neither lengths nor empty entries: the
+// longest range is the store's rows (or a call-wide window; 128 keys, 4/1 heads, D = 64: 6.2 us in a store of 128
+// rows, 8.3 in one of 32768, where a cluster of 8 is taken, 14.4 scheduled), and an empty entry counts as a token of its own.  256 entries, one of them 200 tokens
+// over 2048 keys, 20 single tokens and the others empty: 117 us, 66 without the empty ones (256 single tokens of 2048
+// keys 140 / 209, which is why the rule is so).  The shares are halved while there are SMs for them and more
 // than kQ4DirectPart keys in each.  In us, direct / scheduled, 32/8 heads, D = 128, all ranges full: 1 token 512 keys
 // 7.0 / 14.4, 16384 keys 15.8 / 19.4; 8 tokens 64 keys 6.0 / 13.0, 2048 keys 10.3 / 18.8, 16384 keys 40 / 45; 32 tokens
 // 512 keys 8.9 / 22.6, 4096 keys 38 / 49; 64 tokens 2048 keys 41 / 62; two segments of 16 tokens 1024 keys 13 / 26, 4096 keys
-// 36 / 28.  Where lengths differ the call waits for its longest: lengths evenly spread up to the limit (32 tokens of 4096
+// 36 / 28.
+// Where lengths differ the call waits for its longest: lengths evenly spread up to the limit (32 tokens of 4096
 // keys, 34.5 / 33.6; with 16/2 heads of 8192, 21 / 24, of 16384 beyond it 36 / 30; 16 tokens at D = 256 of 4096 30 / 32, of
 // 8192 52 / 47).
 constexpr int64_t kQ4DirectPart = 128;
