@@ -29,6 +29,8 @@ constexpr int kPrefillTile = 128;  // prefill kernel: key positions per tile
 // or one (D = 256, whose output accumulator alone fills the tensor memory).
 __host__ __device__ constexpr int prefill_unit_rows(int D) { return D == 256 ? kPrefillRows : 2 * kPrefillRows; }
 
+constexpr int kQ4Group = 32;  // dims of a 4-bit store that share a scale
+
 constexpr int kRouteNone = 0;
 constexpr int kRouteSplitk = 1;
 constexpr int kRoutePrefill = 2;

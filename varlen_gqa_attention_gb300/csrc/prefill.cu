@@ -26,7 +26,8 @@
 //     (= tensor-memory lane): the thread reads its S half-row, masks by select (causal,
 //     window, the tile's end), keeps a base-2 running max shared by the two halves with lazy
 //     rescaling (one barrier per tile checks that no row's tile max left the 2^8 window; only
-//     then are maxima swapped and O rescaled) and writes P as bf16 pairs into tensor memory;
+//     then are maxima swapped and O rescaled) and writes P as bf16 pairs into tensor memory
+//     (fp16 ones over staged columns of a 4-bit store, whose V is fp16);
 //     at the end of a piece the two row-sum halves are added and each warpgroup writes its
 //     half of O's columns to `out` (the unit's only CTA) or to a partial for the combine pass;
 //   * V rows past the last visible key of a unit are zeroed in shared memory before the PV
@@ -35,7 +36,6 @@
 // unwinds, frees its tensor memory and exits.
 #include <cuda.h>
 
-#include "q4.cuh"
 #include "tc.cuh"
 
 namespace sdpa {
@@ -136,7 +136,7 @@ __device__ __forceinline__ bool pf_next(PieceWalk& w, PfPiece& pc, int64_t rows)
   return true;
 }
 
-// F16: P and V are fp16 (V of staged columns, see q4_stage.cu), P held 2^kQ4PLift times larger, its sum too.
+// F16: P and V are fp16 (V of staged columns, see q4_stage.cu), P held 2^kF16PLift times larger.
 template <int D, bool F16>
 __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
     sdpa_prefill_kernel(const AttnArgs A, const __grid_constant__ CUtensorMap tmQ,
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
           okp = okp && __all_sync(0xffffffffu, pv_done(g2));
         }
         tc_fence_after();
-        const float nmu = m_use == -INFINITY ? 0.f : F16 ? kQ4PLift - m_use : -m_use;
+        const float nmu = m_use == -INFINITY ? 0.f : F16 ? kF16PLift - m_use : -m_use;
         // p = 2^(scale*s - m) (masked columns give 0), row sum; P as pairs into P_b
         float sum8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         uint32_t pw[C::HALF / 2];

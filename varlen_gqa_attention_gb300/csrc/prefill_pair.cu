@@ -18,7 +18,8 @@
 //     a ring store is never formed (the key range is tiled in two parts at the wrap), so
 //     every tile is one box of the 4-d store tensor [rows, cols, Hkv, D];
 //   * tensor memory (512 columns): S_h (fp32, 128 keys) for each half h, the softmax's P_h
-//     written as bf16 pairs over the first 64 columns of S_h, and the output accumulators
+//     written as bf16 pairs (fp16 ones over staged columns of a 4-bit store, whose V is fp16)
+//     over the first 64 columns of S_h, and the output accumulators
 //     O_0, O_1 (D columns each);
 //   * the MMA warp issues tcgen05.mma (the whole warp runs the loop, one elected lane
 //     issues) in the order S_0(0) S_1(0) | PV_0(0) S_0(1) PV_1(0) S_1(1) | PV_0(1) ...:
@@ -41,7 +42,6 @@
 // its MMAs, and the CTA frees its tensor memory and exits.
 #include <cuda.h>
 
-#include "q4.cuh"
 #include "tc.cuh"
 
 namespace sdpa {
@@ -235,7 +235,7 @@ __device__ __noinline__ PpLoopOut pp_softmax_tiles(const PpLoop lp, volatile int
       l *= f;
       m_use = m_new;
     }
-    const float nmu = m_use == -INFINITY ? 0.f : F16 ? kQ4PLift - m_use : -m_use;
+    const float nmu = m_use == -INFINITY ? 0.f : F16 ? kF16PLift - m_use : -m_use;
     // p = 2^(scale*s - m) (masked columns give 0), row sum; P as pairs over S_h, in four
     // stores of 16 columns as they are ready (one wait for all of them)
     float sum4[4] = {0.f, 0.f, 0.f, 0.f};
@@ -280,7 +280,7 @@ __device__ __noinline__ PpLoopOut pp_softmax_tiles(const PpLoop lp, volatile int
   return out;
 }
 
-// F16: P and V are fp16 (V of staged columns, see q4_stage.cu), P held 2^kQ4PLift times larger, its sum too.
+// F16: P and V are fp16 (V of staged columns, see q4_stage.cu), P held 2^kF16PLift times larger.
 template <int D, bool F16>
 __global__ void __launch_bounds__(PpCfg<D>::THREADS, 1)
     sdpa_prefill_pair_kernel(const AttnArgs A, const __grid_constant__ CUtensorMap tmQ,

@@ -18,8 +18,6 @@
 
 namespace sdpa {
 
-constexpr int kQ4Group = 32;     // dims that share a scale
-constexpr float kQ4PLift = 7.f;  // the attention kernels hold their fp16 probabilities 2^7 times larger
 constexpr int kQ4RowAlign = 16;  // store rows are a multiple of this, so that 16 rows of codes and
                                  // of scales are whole 16-byte blocks at every head dim
 
@@ -108,11 +106,6 @@ __device__ __forceinline__ uint4 q4_words8_f16(uint32_t w, uint32_t scale_byte) 
 __device__ __forceinline__ uint4 q4_q_order(const uint4& a) {
   return make_uint4(__byte_perm(a.x, a.z, 0x5410), __byte_perm(a.x, a.z, 0x7632),
                     __byte_perm(a.y, a.w, 0x5410), __byte_perm(a.y, a.w, 0x7632));
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 

@@ -250,7 +250,7 @@ __device__ __forceinline__ void q4_unit(const AttnArgs& A, const Q4Piece& pc, in
           if (mn > m[c] + 8.f) {
             alpha = exp2_approx(m[c] - mn);
             m[c] = mn;
-            nmu[c] = kQ4PLift - mn;
+            nmu[c] = kF16PLift - mn;
           }
           l[c] *= alpha;
 #pragma unroll

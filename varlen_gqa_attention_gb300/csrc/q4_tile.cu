@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) sdpa_q4_tile_kernel(Q4AttnA
             if (live[c] && mn > m[c] + 8.f) {
               alpha[c] = exp2_approx(m[c] - mn);
               m[c] = mn;
-              nmu[c] = kQ4PLift - mn;
+              nmu[c] = kF16PLift - mn;
             }
             l[c] *= alpha[c];
           }
@@ -568,7 +568,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) sdpa_q4_tile_kernel(Q4AttnA
           const float alpha = up ? exp2_approx(m[0] - mn) : 1.f;
           if (up) {
             m[0] = mn;
-            nmu[0] = kQ4PLift - mn;
+            nmu[0] = kF16PLift - mn;
           }
           l[0] *= alpha;
           if (j > 0) {

@@ -32,7 +32,6 @@
 // segments, up to 8192 packed rows and up to 1024 units are built in shared memory; larger
 // calls run the same steps on the workspace copies.
 #include "common.cuh"
-#include "q4.cuh"
 
 namespace sdpa {
 

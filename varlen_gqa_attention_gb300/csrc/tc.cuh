@@ -3,9 +3,19 @@
 // allocation, MMA, commit, loads/stores).  All written from the PTX ISA descriptions.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 
 namespace sdpa {
+
+// Probabilities that are rounded to fp16 are held 2^kF16PLift times larger, their sums too: at most 2^15 with a maximum
+// that is up to 2^8 behind, and those too small for fp16's smallest step are less than 2^-32 of their row.
+constexpr float kF16PLift = 7.f;
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
 
 // ---------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
