@@ -86,17 +86,17 @@ KERNEL_SOURCES = {
 # when it was taken.  A kernel whose sources hash differently now reports traffic null until
 # the capture is repeated.
 NCU_TRAFFIC = {
-    "prefill_d128": (1207549440 + 65541888, "prefill", "91780631a32d4b44"),  # sdpa_prefill_pair_kernel<128>
-    "prefill_d64": (9903616 + 512, "prefill", "91780631a32d4b44"),  # sdpa_prefill_pair_kernel<64>
-    "prefill_d256": (334566912 + 47162368, "prefill", "91780631a32d4b44"),  # sdpa_prefill_kernel<256>
-    "ring_prefill": (14966016 + 0, "prefill", "91780631a32d4b44"),  # sdpa_prefill_pair_kernel<128>
-    "tiny": (159744 + 0, "splitk", "e448effc74ee4957"),  # sdpa_splitk_kernel<64> (tiny calls take the split-K route)
-    "decode": (141723648 + 3188224, "splitk", "e448effc74ee4957"),  # sdpa_splitk_kernel<128>
-    "decode_append": (141728000 + 3187456, "splitk", "e448effc74ee4957"),
-    "mixed": (285199872 + 11369472, "splitk", "e448effc74ee4957"),  # both calls
-    "mixed_modes": (220047104 + 8420096, "splitk", "e448effc74ee4957"),
+    "prefill_d128": (1172793088 + 65199104, "prefill", "499f62f23c746ac8"),  # sdpa_prefill_pair_kernel<128>
+    "prefill_d64": (9901568 + 768, "prefill", "499f62f23c746ac8"),  # sdpa_prefill_pair_kernel<64>
+    "prefill_d256": (339611392 + 46842112, "prefill", "499f62f23c746ac8"),  # sdpa_prefill_kernel<256>
+    "ring_prefill": (14965760 + 0, "prefill", "499f62f23c746ac8"),  # sdpa_prefill_pair_kernel<128>
+    "tiny": (159744 + 0, "splitk", "7dd0961a9a153041"),  # sdpa_splitk_kernel<64> (tiny calls take the split-K route)
+    "decode": (141725184 + 3264768, "splitk", "7dd0961a9a153041"),  # sdpa_splitk_kernel<128>
+    "decode_append": (141723136 + 3200000, "splitk", "7dd0961a9a153041"),
+    "mixed": (285208576 + 10821120, "splitk", "7dd0961a9a153041"),  # both calls
+    "mixed_modes": (220021248 + 8182016, "splitk", "7dd0961a9a153041"),
     # sdpa_clone_kernel: writes still dirty in L2 when the kernel ends are not counted
-    "seq_clone": (134241280 + 84925696, "clone", "c9b82a90a0e5fff4"),
+    "seq_clone": (134243328 + 84793088, "clone", "b4166982db05ef79"),
 }
 
 
