@@ -23,8 +23,9 @@
 //     P^T is the transpose of what S^T leaves in the lanes: one movmatrix per 8 x 8 block.
 //     (With the query rows as the 16 rows a decode of 64 sequences over 24576 keys on average, 8 KV
 //     heads, D = 128, took 675 us, and 466 so; 335 us, 5.2 TB/s of codes and scales, with what
-//     follows: the ALU pipe is then busy 55 % of the time, at 2.3 instructions a cycle.  A third CTA
-//     on an SM, with runs of 32 keys to fit its registers, took 356 us.)
+//     follows.  No pipe is full then: the ALU pipe is busy 55 % of the time, at 2.3 of 4 instructions a
+//     cycle, and the 10 warps of an SM wait for their own results (0.7 cycles an instruction) and loads
+//     (0.7).  A third CTA on an SM, with runs of 32 keys to fit its registers, took 356 us.)
 // P is rounded to fp16 (half a step is at most 2^-11 of it, against 2^-8 in bf16) and V is exact in
 // fp16; Q and K are multiplied in bf16, where both are exact.  Sums are fp32.  The lazily updated
 // maximum leaves P at most 2^8 above it, so P is kept 2^7 times larger, its sum too: at most 2^15,

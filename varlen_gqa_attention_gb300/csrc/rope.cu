@@ -18,9 +18,12 @@
 // A lane takes 16 dims of a head, both halves of 8 pairs: 8 angles are loaded once for all the heads
 // of a row that its warp goes through, and nothing is exchanged between lanes.
 //
-// What bounds it: the rows' bytes, read once and written once, and nearly as much the issue slots
-// (about 9 instructions a dim); for a handful of rows the chain of dependent loads (segment,
-// position, angles), which the rows' own loads start ahead of.
+// What bounds it: no pipe, but the latency of loads at 24 warps an SM with two passes each on their way
+// (long scoreboard 4 to 6 cycles an instruction, 1.7 to 2.1 of 4 instructions a cycle, with cold caches), and
+// the ramp and the uneven end of a launch of 15 to 20 us: 16384 rows of 16 x 64 take 13.1 us over buffers that are
+// not in the L2 (5.2 TB/s; 10.4 us over ones that are), 4097 of 20 x 256 17.1 (5.0 TB/s; two rows for some warps, one
+// for the others), 4093 tokens of 32/8 x 128 on their way into a store 21.2 (4.8 TB/s).  For a handful of rows it is
+// the chain of dependent loads (segment, position, angles), which the rows' own loads start ahead of.
 #include "q4.cuh"
 #include "rope.cuh"
 
