@@ -311,7 +311,7 @@ __device__ __forceinline__ RowWin row_window(int i, int q_len, int kv_end, int c
   int p = kv_end - q_len + i;
   RowWin w;
   w.hi = causal ? min(p + 1, kv_end) : kv_end;
-  w.lo = window > 0 ? max(0, p - window + 1) : 0;
+  w.lo = window > 0 && p >= window ? p - window + 1 : 0;  // (p may be negative, and window 2^31 - 1)
   return w;
 }
 
