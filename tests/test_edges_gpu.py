@@ -143,3 +143,21 @@ def test_the_scale_of_a_caller(dev, route):
     for scale in (1e-30, 0.5 / math.sqrt(128), 1.0):
         got, st = run_q4(q, store, seq, dev, causal=True, scale=scale)
         check(got, st, q, store, seq, True, scale=scale)
+
+
+@pytest.mark.parametrize("window", [2 ** 31, 2 ** 32 + 5, 2 ** 63 - 1, -2 ** 32 + 5])
+def test_windows_beyond_32_bits_are_refused(dev, window):
+    # 2^32 + 5 would be cut to 5
+    store = pkg.q4_store(64, 1, 2, 64, device=dev)
+    q, k = queries(3, 4, 64, 9).to(dev), queries(3, 2, 64, 10).to(dev)
+    seq, table = torch.tensor([[0, 3, 0, 40]], dtype=torch.int32, device=dev), pkg.rope_table(64, 64, device=dev)
+    cols = [torch.zeros(64, 1, 2, 64, dtype=torch.bfloat16, device=dev) for _ in range(2)]
+    for call in (lambda: pkg.sdpa_varlen(q, *cols, seq, causal=True, window=window),
+                 lambda: pkg.sdpa_varlen_append(q, k, k, *cols, seq, causal=True, window=window),
+                 lambda: pkg.sdpa_varlen_splitk_static(q, *cols, seq, causal=True, window=window),
+                 lambda: pkg.sdpa_rope_append(q, k, k, *cols, seq, table, window=window),
+                 lambda: pkg.sdpa_rope_append_q4(q, k, k, store, seq, table, window=window),
+                 lambda: pkg.sdpa_q4_unpack(store, seq, 3, window=window),
+                 lambda: pkg.sdpa_varlen_q4(q, store, seq, causal=True, window=window)):
+        with pytest.raises(ValueError, match="beyond 32 bits"):
+            call()

@@ -189,6 +189,14 @@ def _stream_ptr(stream) -> int:
     return s.cuda_stream
 
 
+def _window(window) -> int:
+    """A window as the C entries' 32-bit int, which ctypes would cut larger numbers to."""
+    w = int(window)
+    if not -2 ** 31 <= w < 2 ** 31:
+        raise ValueError(f"window {w} is beyond 32 bits")
+    return w
+
+
 def _check_attention_args(q, k_store, v_store, seq_info, out=None, seg_mode=None):
     """The tensor checks every attention entry makes before its C call: shapes, dtypes
     (bf16 data, int32 tables), layouts (contiguous stores and tables, unit inner strides) and
@@ -243,7 +251,7 @@ def sdpa_varlen(q: torch.Tensor, k_store: torch.Tensor, v_store: torch.Tensor, s
     st_ptr = status.data_ptr() if status is not None else None
     code = lib.sdpa_varlen(q.data_ptr(), T, Hq, D, q.stride(0), q.stride(1), k_store.data_ptr(),
                            v_store.data_ptr(), rows, cols, Hkv, seq_info.data_ptr() if S else None,
-                           S, int(bool(causal)), int(window), float(scale), out.data_ptr(),
+                           S, int(bool(causal)), _window(window), float(scale), out.data_ptr(),
                            out.stride(0), out.stride(1), workspace.data_ptr(), workspace.numel(),
                            st_ptr, _stream_ptr(stream))
     _check(code)
@@ -280,7 +288,7 @@ def sdpa_varlen_append(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor
     code = lib.sdpa_varlen_append(q.data_ptr(), T, Hq, D, q.stride(0), q.stride(1), k_new.data_ptr(),
                                   v_new.data_ptr(), k_new.stride(0), k_new.stride(1), k_store.data_ptr(),
                                   v_store.data_ptr(), rows, cols, Hkv, seq_info.data_ptr() if S else None,
-                                  S, int(bool(causal)), int(window), float(scale), out.data_ptr(),
+                                  S, int(bool(causal)), _window(window), float(scale), out.data_ptr(),
                                   out.stride(0), out.stride(1), workspace.data_ptr(), workspace.numel(),
                                   st_ptr, _stream_ptr(stream))
     _check(code)
@@ -370,7 +378,7 @@ def sdpa_varlen_splitk_static(q: torch.Tensor, k_store: torch.Tensor, v_store: t
         out = _on_stream(torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device), stream)
     code = lib.sdpa_varlen_splitk_static(
         q.data_ptr(), T, Hq, D, q.stride(0), q.stride(1), k_store.data_ptr(), v_store.data_ptr(), rows, cols, Hkv,
-        seq_info.data_ptr() if S else None, S, int(bool(causal)), int(window), float(scale), out.data_ptr(),
+        seq_info.data_ptr() if S else None, S, int(bool(causal)), _window(window), float(scale), out.data_ptr(),
         out.stride(0), out.stride(1), status.data_ptr() if status is not None else None, _stream_ptr(stream))
     _check(code)
     return out
@@ -576,7 +584,7 @@ def _rope_append(entry, q, k_new, v_new, store_tensors, store_args, rows, cols, 
     if q_out is None:
         q_out = _rows_like(q, shape, stream)
     _call(entry, dev, stream, q.data_ptr(), qrs, qhs, k_new.data_ptr(), krs, khs, v_new.data_ptr(), vrs, vhs, T, Hq,
-          Hkv, D, rot, *store_args, rows, cols, seq_ptr, mode_ptr, S, int(window), q_out.data_ptr(), ors, ohs,
+          Hkv, D, rot, *store_args, rows, cols, seq_ptr, mode_ptr, S, _window(window), q_out.data_ptr(), ors, ohs,
           _status_ptr(status))
     return q_out
 
@@ -634,7 +642,7 @@ def sdpa_q4_unpack(store: Q4Store, seq_info: torch.Tensor, T: int, *, window: in
         k_out = _rows_like(seq_info, shape, stream)
     if v_out is None:
         v_out = _rows_like(seq_info, shape, stream)
-    _call(library().sdpa_fourbit_unpack, dev, stream, ptrs, rows, cols, Hkv, D, seq_ptr, mode_ptr, S, int(window), T,
+    _call(library().sdpa_fourbit_unpack, dev, stream, ptrs, rows, cols, Hkv, D, seq_ptr, mode_ptr, S, _window(window), T,
           k_out.data_ptr(), v_out.data_ptr(), rs, hs, _status_ptr(status))
     return k_out, v_out
 
@@ -669,6 +677,6 @@ def sdpa_varlen_q4(q: torch.Tensor, store: Q4Store, seq_info: torch.Tensor, *, c
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     _call(library().sdpa_varlen_fourbit, dev, stream, q.data_ptr(), T, Hq, D, rs, hs, ptrs, rows, cols, Hkv, seq_ptr,
-          mode_ptr, S, 1 if causal else 0, int(window), D ** -0.5 if scale is None else float(scale), out.data_ptr(),
+          mode_ptr, S, 1 if causal else 0, _window(window), D ** -0.5 if scale is None else float(scale), out.data_ptr(),
           ors, ohs, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _status_ptr(status))
     return out
