@@ -59,6 +59,8 @@ _ROTATION = struct.Struct("@PqPq7i4x")
 _Q4_POINTERS = struct.Struct("@4P")
 
 
+_bf16, _f32, _i32, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -172,16 +174,24 @@ def set_timing_events(events) -> None:
     _check(lib.sdpa_set_timing_events(arr, len(events)))
 
 
-def _on_stream(t: torch.Tensor, stream) -> torch.Tensor:
-    """A tensor this module allocated on the current stream and hands to work on `stream`:
-    the caching allocator must not reuse its memory before that work is done."""
-    if stream is not None:
-        t.record_stream(stream)
-    return t
+def _rows_like(like: torch.Tensor, shape, stream) -> torch.Tensor:
+    """Uninitialised bf16 rows on `like`'s device, of memory that belongs to the stream that will
+    write them.  The current stream's work on them counts too before that memory serves again: the
+    caller reads them there."""
+    if stream is None:
+        return torch.empty(shape, dtype=_bf16, device=like.device)
+    with torch.cuda.stream(stream):
+        rows = torch.empty(shape, dtype=_bf16, device=like.device)
+    rows.record_stream(torch.cuda.current_stream(like.device))
+    return rows
 
 
 def _workspace(nbytes: int, device, stream=None) -> torch.Tensor:
-    return _on_stream(torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device), stream)
+    """Workspace for one call, of memory that belongs to the stream that uses it."""
+    if stream is None:
+        return torch.empty(max(nbytes, 256), dtype=_u8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(max(nbytes, 256), dtype=_u8, device=device)
 
 
 def _stream_ptr(stream) -> int:
@@ -244,7 +254,7 @@ def sdpa_varlen(q: torch.Tensor, k_store: torch.Tensor, v_store: torch.Tensor, s
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = _on_stream(torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device), stream)
+        out = _rows_like(q, (T, Hq, D), stream)
     need = workspace_bytes(T, Hq, Hkv, D, S)
     if workspace is None:
         workspace = _workspace(need, q.device, stream)
@@ -281,7 +291,7 @@ def sdpa_varlen_append(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = _on_stream(torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device), stream)
+        out = _rows_like(q, (T, Hq, D), stream)
     if workspace is None:
         workspace = _workspace(workspace_bytes(T, Hq, Hkv, D, S), q.device, stream)
     st_ptr = status.data_ptr() if status is not None else None
@@ -306,7 +316,7 @@ def sdpa_varlen_modes(q: torch.Tensor, k_store: torch.Tensor, v_store: torch.Ten
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = _on_stream(torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device), stream)
+        out = _rows_like(q, (T, Hq, D), stream)
     if workspace is None:
         workspace = _workspace(workspace_bytes(T, Hq, Hkv, D, S), q.device, stream)
     st_ptr = status.data_ptr() if status is not None else None
@@ -348,7 +358,7 @@ def sdpa_causal_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = _on_stream(torch.empty_like(q), stream)
+        out = _rows_like(q, q.shape, stream)
     need = workspace_bytes(Lq, Hq, Hkv, D, 1)
     if workspace is None:
         workspace = _workspace(need, q.device, stream)
@@ -375,7 +385,7 @@ def sdpa_varlen_splitk_static(q: torch.Tensor, k_store: torch.Tensor, v_store: t
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = _on_stream(torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device), stream)
+        out = _rows_like(q, (T, Hq, D), stream)
     code = lib.sdpa_varlen_splitk_static(
         q.data_ptr(), T, Hq, D, q.stride(0), q.stride(1), k_store.data_ptr(), v_store.data_ptr(), rows, cols, Hkv,
         seq_info.data_ptr() if S else None, S, int(bool(causal)), _window(window), float(scale), out.data_ptr(),
@@ -388,9 +398,6 @@ def sdpa_varlen_splitk_static(q: torch.Tensor, k_store: torch.Tensor, v_store: t
 #
 # A decode step calls these once a layer and its kernels take a few microseconds, so the checks read
 # each tensor's attributes once and the device and stream come as plain numbers.
-
-_bf16, _f32, _i32, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
-
 
 def _device_of(*tensors) -> int:
     """Index of the one CUDA device that every tensor given is on (None passes)."""
@@ -419,18 +426,6 @@ def _call(entry, dev: int, stream, *args) -> None:
             code = entry(*args, handle)
     if code != SDPA_OK:
         _check(code)
-
-
-def _rows_like(like: torch.Tensor, shape, stream) -> torch.Tensor:
-    """Uninitialised bf16 rows on `like`'s device, of memory that belongs to the stream that will
-    write them.  The current stream's work on them counts too before that memory serves again: the
-    caller reads them there."""
-    if stream is None:
-        return torch.empty(shape, dtype=_bf16, device=like.device)
-    with torch.cuda.stream(stream):
-        rows = torch.empty(shape, dtype=_bf16, device=like.device)
-    rows.record_stream(torch.cuda.current_stream(like.device))
-    return rows
 
 
 def _strides(name: str, t: torch.Tensor, shape=None):
@@ -672,8 +667,7 @@ def sdpa_varlen_q4(q: torch.Tensor, store: Q4Store, seq_info: torch.Tensor, *, c
     if out is None:
         out = _rows_like(q, shape, stream)
     if workspace is None:
-        with torch.cuda.stream(stream):
-            workspace = torch.empty(max(q4_workspace_bytes(T, Hq, store, S), 256), dtype=_u8, device=q.device)
+        workspace = _workspace(q4_workspace_bytes(T, Hq, store, S), q.device, stream)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     _call(library().sdpa_varlen_fourbit, dev, stream, q.data_ptr(), T, Hq, D, rs, hs, ptrs, rows, cols, Hkv, seq_ptr,
