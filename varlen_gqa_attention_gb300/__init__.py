@@ -207,7 +207,15 @@ def _window(window) -> int:
     return w
 
 
-def _check_attention_args(q, k_store, v_store, seq_info, out=None, seg_mode=None):
+def _check_scratch(q, workspace, status) -> None:
+    """What the kernels write beside their output: a caller's workspace and status word."""
+    if workspace is not None and (workspace.device != q.device or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous tensor on q's CUDA device")
+    if status is not None and (status.dtype != torch.int32 or status.device != q.device or status.numel() < 1):
+        raise ValueError("status must be an int32 tensor on q's CUDA device")
+
+
+def _check_attention_args(q, k_store, v_store, seq_info, out=None, seg_mode=None, workspace=None, status=None):
     """The tensor checks every attention entry makes before its C call: shapes, dtypes
     (bf16 data, int32 tables), layouts (contiguous stores and tables, unit inner strides) and
     one CUDA device for all of them.  Raises ValueError; returns (T, Hq, D, rows, cols, Hkv, S)."""
@@ -236,6 +244,7 @@ def _check_attention_args(q, k_store, v_store, seq_info, out=None, seg_mode=None
     tensors = [q, k_store, v_store, seq_info] + [t for t in (out, seg_mode) if t is not None]
     if not all(t.is_cuda for t in tensors) or len({t.device for t in tensors}) != 1:
         raise ValueError("every tensor must be on the same CUDA device")
+    _check_scratch(q, workspace, status)
     return T, Hq, D, rows, cols, Hkv, S
 
 
@@ -249,7 +258,8 @@ def sdpa_varlen(q: torch.Tensor, k_store: torch.Tensor, v_store: torch.Tensor, s
     contiguous; seq_info: int32 [S, 4] contiguous on the same device.  ``status`` (an int32
     device tensor, optional) receives the OR of the device status bits.
     """
-    T, Hq, D, rows, cols, Hkv, S = _check_attention_args(q, k_store, v_store, seq_info, out)
+    T, Hq, D, rows, cols, Hkv, S = _check_attention_args(q, k_store, v_store, seq_info, out, None, workspace,
+                                                            status)
     lib = library()
     if scale is None:
         scale = 1.0 / math.sqrt(D)
@@ -279,7 +289,8 @@ def sdpa_varlen_append(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor
     query row t; they go to store row (kv_end - q_len + i) % rows of each live segment's
     column.  The stores are modified in place; everything else is as ``sdpa_varlen``.
     """
-    T, Hq, D, rows, cols, Hkv, S = _check_attention_args(q, k_store, v_store, seq_info, out)
+    T, Hq, D, rows, cols, Hkv, S = _check_attention_args(q, k_store, v_store, seq_info, out, None, workspace,
+                                                            status)
     for name, t in (("k_new", k_new), ("v_new", v_new)):
         if t.dtype != torch.bfloat16 or not t.is_cuda or t.device != q.device:
             raise ValueError(f"{name} must be a bf16 tensor on q's CUDA device")
@@ -311,7 +322,8 @@ def sdpa_varlen_modes(q: torch.Tensor, k_store: torch.Tensor, v_store: torch.Ten
                       stream=None) -> torch.Tensor:
     """``sdpa_varlen`` with a mask mode per segment: seg_mode int32 [S, 2] = (causal, window)
     on the device, in place of the call's causal / window."""
-    T, Hq, D, rows, cols, Hkv, S = _check_attention_args(q, k_store, v_store, seq_info, out, seg_mode)
+    T, Hq, D, rows, cols, Hkv, S = _check_attention_args(q, k_store, v_store, seq_info, out, seg_mode, workspace,
+                                                            status)
     lib = library()
     if scale is None:
         scale = 1.0 / math.sqrt(D)
@@ -339,6 +351,8 @@ def sdpa_seq_clone(k_store: torch.Tensor, v_store: torch.Tensor, src_col: int, d
     for name, t in (("k_store", k_store), ("v_store", v_store)):
         if t.dtype != torch.bfloat16 or not t.is_cuda or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous bf16 CUDA tensor")
+    if k_store.device != v_store.device:
+        raise ValueError("the stores must be on the same CUDA device")
     rows, cols, Hkv, D = k_store.shape
     _check(lib.sdpa_seq_clone(k_store.data_ptr(), v_store.data_ptr(), rows, cols, Hkv, D, int(src_col),
                               int(dst_col), int(n), _stream_ptr(stream)))
@@ -354,7 +368,15 @@ def sdpa_causal_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale
         if t.dtype != torch.bfloat16 or not t.is_cuda or not t.is_contiguous() or t.dim() != 3:
             raise ValueError(f"{name} must be a contiguous 3-d bf16 CUDA tensor")
     Lq, Hq, D = q.shape
-    Lkv, Hkv, _ = k.shape
+    Lkv, Hkv, Dk = k.shape
+    if v.shape != k.shape or Dk != D:
+        raise ValueError("k and v must both be [Lkv, Hkv, D], with q's D")
+    if k.device != q.device or v.device != q.device:
+        raise ValueError("every tensor must be on the same CUDA device")
+    if out is not None and (out.dtype != torch.bfloat16 or out.shape != q.shape or out.device != q.device or
+                            not out.is_contiguous()):
+        raise ValueError("out must be a contiguous bf16 tensor of q's shape on its CUDA device")
+    _check_scratch(q, workspace, None)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
@@ -378,9 +400,7 @@ def sdpa_varlen_splitk_static(q: torch.Tensor, k_store: torch.Tensor, v_store: t
     the split-K kernel.  Pass ``out`` to allocate nothing at all.  Calls must not overlap on
     the GPU (they share the array); make the first call on a device outside stream capture.
     The tensors are checked as for ``sdpa_varlen``."""
-    T, Hq, D, rows, cols, Hkv, S = _check_attention_args(q, k_store, v_store, seq_info, out)
-    if status is not None and (status.dtype != torch.int32 or status.device != q.device):
-        raise ValueError("status must be an int32 tensor on q's CUDA device")
+    T, Hq, D, rows, cols, Hkv, S = _check_attention_args(q, k_store, v_store, seq_info, out, None, None, status)
     lib = library()
     if scale is None:
         scale = 1.0 / math.sqrt(D)
