@@ -86,17 +86,17 @@ KERNEL_SOURCES = {
 # when it was taken.  A kernel whose sources hash differently now reports traffic null until
 # the capture is repeated.
 NCU_TRAFFIC = {
-    "prefill_d128": (1172793088 + 65199104, "prefill", "499f62f23c746ac8"),  # sdpa_prefill_pair_kernel<128>
-    "prefill_d64": (9901568 + 768, "prefill", "499f62f23c746ac8"),  # sdpa_prefill_pair_kernel<64>
-    "prefill_d256": (339611392 + 46842112, "prefill", "499f62f23c746ac8"),  # sdpa_prefill_kernel<256>
-    "ring_prefill": (14965760 + 0, "prefill", "499f62f23c746ac8"),  # sdpa_prefill_pair_kernel<128>
-    "tiny": (159744 + 0, "splitk", "7dd0961a9a153041"),  # sdpa_splitk_kernel<64> (tiny calls take the split-K route)
-    "decode": (141725184 + 3264768, "splitk", "7dd0961a9a153041"),  # sdpa_splitk_kernel<128>
-    "decode_append": (141723136 + 3200000, "splitk", "7dd0961a9a153041"),
-    "mixed": (285208576 + 10821120, "splitk", "7dd0961a9a153041"),  # both calls
-    "mixed_modes": (220021248 + 8182016, "splitk", "7dd0961a9a153041"),
+    "prefill_d128": (1184279040 + 64862464, "prefill", "a0468b979ee8bad9"),  # sdpa_prefill_pair_kernel<128>
+    "prefill_d64": (9904128 + 256, "prefill", "a0468b979ee8bad9"),  # sdpa_prefill_pair_kernel<64>
+    "prefill_d256": (336229120 + 45867776, "prefill", "a0468b979ee8bad9"),  # sdpa_prefill_kernel<256>
+    "ring_prefill": (14963712 + 0, "prefill", "a0468b979ee8bad9"),  # sdpa_prefill_pair_kernel<128>
+    "tiny": (160512 + 0, "splitk", "4eb2a57bbb5940bf"),  # sdpa_splitk_kernel<64> (tiny calls take the split-K route)
+    "decode": (141727488 + 3381760, "splitk", "4eb2a57bbb5940bf"),  # sdpa_splitk_kernel<128>
+    "decode_append": (141725440 + 3236096, "splitk", "4eb2a57bbb5940bf"),
+    "mixed": (285244160 + 10999040, "splitk", "4eb2a57bbb5940bf"),  # both calls
+    "mixed_modes": (220137984 + 8155648, "splitk", "4eb2a57bbb5940bf"),
     # sdpa_clone_kernel: writes still dirty in L2 when the kernel ends are not counted
-    "seq_clone": (134243328 + 84793088, "clone", "b4166982db05ef79"),
+    "seq_clone": (134257920 + 85121280, "clone", "0b8c9a1ffb83a5cb"),
 }
 
 
