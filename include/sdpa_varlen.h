@@ -315,6 +315,46 @@ sdpa_status sdpa_varlen_fourbit(const void* q, int64_t T, int Hq, int D, int64_t
                            int64_t o_row_stride, int64_t o_head_stride, void* workspace, size_t ws_bytes,
                            int32_t* status_dev, void* stream);
 
+/*
+ * The 8-bit column store.  K and V are each a pair of byte arrays on the device, contiguous (codes 16-byte
+ * aligned):
+ *  codes   [cols, Hkv, rows, D], one byte a value;
+ *  scales  [cols, Hkv, rows / 16], one byte for each block of 16 store rows of a head.
+ * Code c under scale byte b stands for (c - 128) * 2^(min(b, 29) - 20): exact in bf16, and finite for every byte
+ * pattern.  rows is a multiple of 16 (a ring may have more rows than it needs).  Position j of a column lives in
+ * store row j % rows, as in the bf16 store.
+ * An append codes each block that it writes to as a whole: its new rows (bf16; magnitudes above 65024 taken as
+ * that, NaN as 0) together with the rows that it keeps, those whose store row holds a position from before the step
+ * (any position below the segment's first one counts as there).  The scale becomes the smallest one of which the
+ * largest magnitude is at most 127 (the smallest scale is 2^-20, the largest 2^9), and the codes
+ * 128 + round(x / scale), halves to even.  So a new value is off by at most half a step, a step being less than
+ * 1/63 of its block's largest magnitude when that lies in [127 * 2^-20, 65024].  A kept row changes only where the
+ * scale does: not at all as a value when the scale shrinks, and by at most half a step of the new scale when it grows; over all
+ * that happens to it while it stays, it is off by less than one step of the largest scale that it has had.  A
+ * block's other rows keep their bytes, which then stand for something else.
+ */
+typedef struct sdpa_q8_store {
+  uint8_t* k_codes;
+  uint8_t* k_scales;
+  uint8_t* v_codes;
+  uint8_t* v_scales;
+} sdpa_q8_store;
+
+/* sdpa_rope_append into an 8-bit store: the rotated keys, rounded to bf16, and the values take their 8 bits on
+ * the way.  Two live segments of one call that write to the same block of a column leave the block unspecified. */
+sdpa_status sdpa_rope_append_eightbit(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* k_new,
+                                 int64_t k_row_stride, int64_t k_head_stride, const void* v_new,
+                                 int64_t v_row_stride, int64_t v_head_stride, int64_t T, int Hq, int Hkv, int D,
+                                 const sdpa_rotation* rotation, const sdpa_q8_store* store, int64_t rows, int cols,
+                                 const int32_t* seq_info, const int32_t* seg_mode, int S, int window, void* q_out,
+                                 int64_t o_row_stride, int64_t o_head_stride, int32_t* status_dev, void* stream);
+
+/* sdpa_fourbit_unpack for an 8-bit store. */
+sdpa_status sdpa_eightbit_unpack(const sdpa_q8_store* store, int64_t rows, int cols, int Hkv, int D,
+                            const int32_t* seq_info, const int32_t* seg_mode, int S, int window, int64_t T,
+                            void* k_out, void* v_out, int64_t o_row_stride, int64_t o_head_stride,
+                            int32_t* status_dev, void* stream);
+
 /* Set the process-wide route policy (SDPA_ROUTE_*).  Returns SDPA_ERR_ARG if unknown. */
 sdpa_status sdpa_set_route_policy(int policy);
 

@@ -1,4 +1,4 @@
-"""Plain 64-bit statements of the rotary positions, the rotated append and the 4-bit column store.
+"""Plain 64-bit statements of the rotary positions, the rotated append and the 4-bit and 8-bit column stores.
 
 Written from the definitions with NumPy (torch only carries bf16 tensors), element by element where
 that is affordable; nothing here is shared with the library.
@@ -125,3 +125,51 @@ def rope_append(q, k_new, v_new, rows, cols, seq_info, window, table, sections, 
     keep = stays & ~bad
     qr[~keep] = 0.0
     return qr, to_bf16(kr), [(t, int(pos[t] % rows), int(col[t])) for t in range(T) if keep[t]], status
+
+
+# ------------------------------------------------------------------ the 8-bit column store
+
+BLOCK = 16
+Q8_SCALES = [2.0 ** (b - 20) for b in range(30)]
+
+
+def q8_unpack(codes, scales) -> np.ndarray:
+    """[cols, Hkv, rows, D] and [cols, Hkv, rows / 16] bytes -> [cols, Hkv, rows, D] in 64 bits."""
+    s = np.array(Q8_SCALES)[np.minimum(np.asarray(scales, dtype=np.int64), 29)]
+    return (np.asarray(codes, dtype=np.float64) - 128.0) * np.repeat(s, BLOCK, axis=-1)[..., None]
+
+
+def q8_code_block(new, kept=None):
+    """New rows [n, D] and rows that are kept as they are stored [m, D] -> (codes [n + m, D], the byte of the
+    scale that they share)."""
+    x = np.clip(np.where(np.isnan(new), 0.0, new), -65024.0, 65024.0)
+    if kept is not None:
+        x = np.concatenate([x, kept])
+    byte = next((b for b in range(30) if np.abs(x).max(initial=0.0) <= 127 * Q8_SCALES[b]), 29)
+    return (np.clip(np.rint(x / Q8_SCALES[byte]), -128, 127) + 128).astype(np.uint8), byte
+
+
+def q8_append(codes, scales, x, cells, seq_info, live, rows):
+    """Copies of a store's codes [cols, Hkv, rows, D] and scales after the rows x [T, Hkv, D] named by
+    cells [(t, row, col)] have been written; live: each packed row's segment."""
+    codes, scales, x = np.array(codes), np.array(scales), f64(x)
+    seq = np.asarray(seq_info, dtype=np.int64).reshape(-1, 4)
+    blocks = {}
+    for t, r, c in cells:
+        blocks.setdefault((int(live[t]), c, r // BLOCK), {})[r] = t
+    for (s, c, b), new in blocks.items():
+        first = max(int(seq[s, 3] - seq[s, 1]), 0)
+        here = range(b * BLOCK, (b + 1) * BLOCK)
+        # a row that is not written is kept when the last position before the step that it may hold exists
+        kept = [r for r in here if r not in new and first - 1 - (first - 1 - r) % rows >= 0]
+        for h in range(codes.shape[1]):
+            old = q8_unpack(codes[c:c + 1, h:h + 1], scales[c:c + 1, h:h + 1])[0, 0]
+            order = sorted(new) + kept
+            n, byte = q8_code_block(np.stack([x[new[r], h] for r in sorted(new)]), old[kept])
+            codes[c, h, order], scales[c, h, b] = n, byte
+    return codes, scales
+
+
+def q8_column_store(codes, scales) -> torch.Tensor:
+    """An 8-bit store's values laid out as the bf16 column store [rows, cols, Hkv, D] (64 bits)."""
+    return torch.from_numpy(np.ascontiguousarray(q8_unpack(codes, scales).transpose(2, 0, 1, 3)))

@@ -22,7 +22,8 @@ from . import _build
 __all__ = [
     "sdpa_varlen", "sdpa_varlen_modes", "sdpa_varlen_append", "sdpa_seq_clone", "sdpa_causal_prefill",
     "sdpa_varlen_splitk_static", "sdpa_rope", "sdpa_rope_append", "sdpa_rope_append_q4", "sdpa_q4_unpack",
-    "sdpa_varlen_q4", "Q4Store", "q4_store", "rope_table", "q4_workspace_bytes", "workspace_bytes", "workspace_status", "prefill_available", "set_route_policy",
+    "sdpa_varlen_q4", "Q4Store", "q4_store", "rope_table", "q4_workspace_bytes", "sdpa_rope_append_q8", "sdpa_q8_unpack",
+    "Q8Store", "q8_store", "workspace_bytes", "workspace_status", "prefill_available", "set_route_policy",
     "set_timing_events", "library",
     "SDPA_OK", "SEG_BAD_QRANGE", "SEG_BAD_COL", "SEG_BAD_KV", "SEG_SPAN", "SEG_OVERLAP",
     "DEV_TIMEOUT", "ROPE_BAD_POS", "ROUTE_AUTO", "ROUTE_SPLITK", "ROUTE_PREFILL", "SdpaError",
@@ -44,7 +45,7 @@ EXPORTS = [
     "sdpa_set_timing_events", "sdpa_last_error", "sdpa_version", "sdpa_varlen_splitk_static",
     "sdpa_varlen_append", "sdpa_seq_clone", "sdpa_varlen_modes", "sdpa_prefill_available",
     "sdpa_workspace_status", "sdpa_rope", "sdpa_rope_append", "sdpa_rope_append_fourbit", "sdpa_fourbit_unpack",
-    "sdpa_varlen_fourbit", "sdpa_varlen_fourbit_workspace_bytes",
+    "sdpa_varlen_fourbit", "sdpa_varlen_fourbit_workspace_bytes", "sdpa_rope_append_eightbit", "sdpa_eightbit_unpack",
 ]
 
 
@@ -54,9 +55,9 @@ class SdpaError(RuntimeError):
         self.code = code
 
 
-# the C structs sdpa_rotation and sdpa_q4_store, packed (their padding included) as bytes
+# the C structs sdpa_rotation, sdpa_q4_store and sdpa_q8_store, packed (their padding included) as bytes
 _ROTATION = struct.Struct("@PqPq7i4x")
-_Q4_POINTERS = struct.Struct("@4P")
+_Q4_POINTERS = _Q8_POINTERS = struct.Struct("@4P")
 
 
 _bf16, _f32, _i32, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
@@ -123,6 +124,10 @@ def library(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.sdpa_fourbit_unpack.restype = c_int
     lib.sdpa_fourbit_unpack.argtypes = [c_q4, c_i64, c_int, c_int, c_int, c_vp, c_vp, c_int, c_int, c_i64, c_vp, c_vp,
                                    c_i64, c_i64, c_vp, c_vp]
+    lib.sdpa_rope_append_eightbit.restype = c_int
+    lib.sdpa_rope_append_eightbit.argtypes = lib.sdpa_rope_append_fourbit.argtypes
+    lib.sdpa_eightbit_unpack.restype = c_int
+    lib.sdpa_eightbit_unpack.argtypes = lib.sdpa_fourbit_unpack.argtypes
     lib.sdpa_varlen_fourbit_workspace_bytes.restype = ctypes.c_size_t
     lib.sdpa_varlen_fourbit_workspace_bytes.argtypes = [c_i64, c_int, c_int, c_int, c_int, c_i64, c_int]
     lib.sdpa_varlen_fourbit.restype = c_int
@@ -641,12 +646,8 @@ def sdpa_rope_append_q4(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tenso
                         seq_info, table, positions, sections, interleaved, window, seg_mode, q_out, status, stream)
 
 
-def sdpa_q4_unpack(store: Q4Store, seq_info: torch.Tensor, T: int, *, window: int = 0,
-                   seg_mode: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
-                   v_out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
-    """(k, v) bf16 [T, Hkv, D]: the rows of a segment table as a 4-bit store holds them (exact).
-    Row i of a live segment is position kv_end - q_len + i; other rows are 0."""
-    rows, cols, Hkv, D, ptrs = _q4(store)
+def _unpack(entry, store, store_args, seq_info, T, window, seg_mode, k_out, v_out, status, stream):
+    rows, cols, Hkv, D, ptrs = store_args
     seq_ptr, mode_ptr, S = _table(seq_info, seg_mode)
     shape = (T, Hkv, D)
     rs, hs = _strides("k_out", k_out, shape) if k_out is not None else (Hkv * D, D)
@@ -657,9 +658,18 @@ def sdpa_q4_unpack(store: Q4Store, seq_info: torch.Tensor, T: int, *, window: in
         k_out = _rows_like(seq_info, shape, stream)
     if v_out is None:
         v_out = _rows_like(seq_info, shape, stream)
-    _call(library().sdpa_fourbit_unpack, dev, stream, ptrs, rows, cols, Hkv, D, seq_ptr, mode_ptr, S, _window(window), T,
+    _call(entry, dev, stream, ptrs, rows, cols, Hkv, D, seq_ptr, mode_ptr, S, _window(window), T,
           k_out.data_ptr(), v_out.data_ptr(), rs, hs, _status_ptr(status))
     return k_out, v_out
+
+
+def sdpa_q4_unpack(store: Q4Store, seq_info: torch.Tensor, T: int, *, window: int = 0,
+                   seg_mode: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                   v_out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
+    """(k, v) bf16 [T, Hkv, D]: the rows of a segment table as a 4-bit store holds them (exact).
+    Row i of a live segment is position kv_end - q_len + i; other rows are 0."""
+    return _unpack(library().sdpa_fourbit_unpack, store, _q4(store), seq_info, T, window, seg_mode, k_out, v_out, status,
+                   stream)
 
 
 def q4_workspace_bytes(T: int, Hq: int, store: Q4Store, S: int) -> int:
@@ -694,3 +704,61 @@ def sdpa_varlen_q4(q: torch.Tensor, store: Q4Store, seq_info: torch.Tensor, *, c
           mode_ptr, S, 1 if causal else 0, _window(window), D ** -0.5 if scale is None else float(scale), out.data_ptr(),
           ors, ohs, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _status_ptr(status))
     return out
+
+
+# ------------------------------------------------ the 8-bit column store
+
+class Q8Store(NamedTuple):
+    """An 8-bit column store: uint8 codes [cols, Hkv, rows, D] and scales [cols, Hkv, rows / 16] of the
+    keys, then of the values; 16 rows of a head share a scale.  Code c under scale byte b stands for
+    (c - 128) * 2**(min(b, 29) - 20)."""
+    k_codes: torch.Tensor
+    k_scales: torch.Tensor
+    v_codes: torch.Tensor
+    v_scales: torch.Tensor
+
+
+def q8_store(rows: int, cols: int, Hkv: int, D: int, device=None) -> Q8Store:
+    """An empty 8-bit store (every value 0); rows a multiple of 16."""
+    if rows <= 0 or rows % 16 or cols <= 0 or Hkv <= 0 or D not in (64, 128, 256):
+        raise ValueError("rows must be a multiple of 16, D 64, 128 or 256")
+    codes = lambda: torch.full((cols, Hkv, rows, D), 128, dtype=_u8, device=device)  # noqa: E731
+    scales = lambda: torch.zeros((cols, Hkv, rows // 16), dtype=_u8, device=device)  # noqa: E731
+    return Q8Store(codes(), scales(), codes(), scales())
+
+
+def _q8(store: Q8Store):
+    """(rows, cols, Hkv, D, packed pointers) of an 8-bit store."""
+    kc, ks, vc, vs = store
+    shape = kc.shape
+    if len(shape) != 4 or shape[2] % 16 or vc.shape != shape or ks.shape != vs.shape or \
+            ks.shape != (shape[0], shape[1], shape[2] // 16):
+        raise ValueError("an 8-bit store is codes [cols, Hkv, rows, D] and scales [cols, Hkv, rows / 16], twice")
+    if not (kc.dtype is ks.dtype is vc.dtype is vs.dtype is _u8 and kc.is_contiguous() and ks.is_contiguous() and
+            vc.is_contiguous() and vs.is_contiguous()):
+        raise ValueError("an 8-bit store's tensors must be contiguous uint8")
+    cols, Hkv, rows, D = shape
+    return rows, cols, Hkv, D, _Q8_POINTERS.pack(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr())
+
+
+def sdpa_rope_append_q8(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, store: Q8Store,
+                        seq_info: torch.Tensor, table: torch.Tensor, *, positions: Optional[torch.Tensor] = None,
+                        sections: Optional[Sequence[int]] = None, interleaved: bool = False, window: int = 0,
+                        seg_mode: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                        status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """``sdpa_rope_append`` into an 8-bit store, for ``sdpa_varlen_q8``: the rotated keys, rounded to
+    bf16, and the values take their 8 bits on the way.  Each block of 16 store rows that the step writes to
+    gets the smallest scale that holds its new rows and those that hold earlier positions, which are coded
+    again where the scale changes.  Two segments of one call may not write to the same block."""
+    rows, cols, Hkv, D, ptrs = _q8(store)
+    return _rope_append(library().sdpa_rope_append_eightbit, q, k_new, v_new, store, (ptrs,), rows, cols, Hkv, D,
+                        seq_info, table, positions, sections, interleaved, window, seg_mode, q_out, status, stream)
+
+
+def sdpa_q8_unpack(store: Q8Store, seq_info: torch.Tensor, T: int, *, window: int = 0,
+                   seg_mode: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                   v_out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
+    """(k, v) bf16 [T, Hkv, D]: the rows of a segment table as an 8-bit store holds them (exact).
+    Row i of a live segment is position kv_end - q_len + i; other rows are 0."""
+    return _unpack(library().sdpa_eightbit_unpack, store, _q8(store), seq_info, T, window, seg_mode, k_out, v_out,
+                   status, stream)

@@ -237,12 +237,13 @@ sdpa_status check_tensors(const void* q, const void* k, const void* v, void* out
   return SDPA_OK;
 }
 
-sdpa_status check_q4_store(const Q4Store& q4, int64_t rows) {
-  if (!q4.kc || !q4.ks || !q4.vc || !q4.vs) return fail(SDPA_ERR_NULL, "a 4-bit store pointer is NULL");
-  if (!aligned16(q4.kc) || !aligned16(q4.ks) || !aligned16(q4.vc) || !aligned16(q4.vs))
-    return fail(SDPA_ERR_ALIGN, "4-bit store pointers must be 16-byte aligned");
-  if (rows % kQ4RowAlign)
-    return fail(SDPA_ERR_SHAPE, "a 4-bit store has a multiple of %d rows, not %lld", kQ4RowAlign, (long long)rows);
+sdpa_status check_packed_store(const PackedStore& st, int bits, int64_t rows) {
+  if (!st.kc || !st.ks || !st.vc || !st.vs) return fail(SDPA_ERR_NULL, "a %d-bit store pointer is NULL", bits);
+  if (!aligned16(st.kc) || !aligned16(st.vc) || (bits == 4 && (!aligned16(st.ks) || !aligned16(st.vs))))
+    return fail(SDPA_ERR_ALIGN, "%d-bit store pointers must be 16-byte aligned", bits);
+  if (rows % kPackedRows)
+    return fail(SDPA_ERR_SHAPE, "a %d-bit store has a multiple of %d rows, not %lld", bits, kPackedRows,
+                (long long)rows);
   return SDPA_OK;
 }
 
@@ -352,7 +353,7 @@ static bool prefill_launch(const SchedArgs& sa, int64_t T) {
 }
 
 static sdpa_status launch_all(const SchedArgs& sa, const AttnArgs& aa, int D, const Grids& g,
-                              const TensorMaps& tm, const AppendArgs* ap, const Q4Store* q4,
+                              const TensorMaps& tm, const AppendArgs* ap, const PackedStore* q4,
                               const Q4StageArgs* stage, cudaStream_t st) {
   cudaError_t e = mark(0, st);
   if (e == cudaSuccess) {
@@ -442,11 +443,11 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
                        const int32_t* seq_info, int S, const int32_t* inl, int causal, int window,
                        float scale, void* out, int64_t o_rs, int64_t o_hs, void* ws, size_t ws_bytes,
                        int32_t* status_dev, void* stream, const AppendArgs* ap = nullptr,
-                       const int32_t* seg_mode = nullptr, const Q4Store* q4 = nullptr) {
+                       const int32_t* seg_mode = nullptr, const PackedStore* q4 = nullptr) {
   g_err[0] = 0;
   sdpa_status st = check_common(T, Hq, Hkv, D, S, rows, cols, window, scale);
   if (st) return st;
-  if (q4 && (st = check_q4_store(*q4, rows))) return st;
+  if (q4 && (st = check_packed_store(*q4, 4, rows))) return st;
   if (q4 && T == 0) return SDPA_OK;
   // the dense entry passes its one segment by value: no table pointer to check
   if ((st = check_tensors(q, k, v, out, seq_info, inl ? 0 : S, q_rs, q_hs, o_rs, o_hs))) return st;
@@ -506,7 +507,7 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
   sa.sk[1] = tile;
   sa.sk_choice = sp == Q4Split::kEither;
   sa.sk_ratio = q4_tile_ratio(D);
-  sa.lo_align = q4 ? kQ4RowAlign : 1;
+  sa.lo_align = q4 ? kPackedRows : 1;
   sa.pf_cols = sg.pf_cols;
   // (a call-wide window bounds the positions that a staged column has to hold)
   sa.rows_pf = q4 && window > 0 && !sa.seg_mode ? std::min<int64_t>(rows, T + window - 1) : rows;
@@ -679,7 +680,7 @@ sdpa_status sdpa_varlen_fourbit(const void* q, int64_t T, int Hq, int D, int64_t
   if (!store) return fail(SDPA_ERR_NULL, "store is NULL");
   // the running maximum is taken over unscaled scores
   if (scale < 0.f) return fail(SDPA_ERR_ARG, "scale %g < 0", (double)scale);
-  const Q4Store q4{store->k_codes, store->k_scales, store->v_codes, store->v_scales};
+  const PackedStore q4{store->k_codes, store->k_scales, store->v_codes, store->v_scales};
   return run(q, T, Hq, D, q_row_stride, q_head_stride, q4.kc, q4.vc, rows, cols, Hkv, seq_info, S, nullptr, causal,
              window, scale, out, o_row_stride, o_head_stride, workspace, ws_bytes, status_dev, stream, nullptr,
              seg_mode, &q4);

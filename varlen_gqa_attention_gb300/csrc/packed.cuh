@@ -1,0 +1,39 @@
+// packed.cuh - what the 4-bit and the 8-bit column store have in common.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace sdpa {
+
+// Store rows are a multiple of this: at 4 bits 16 rows of codes and of scales are whole 16-byte blocks at every
+// head dim, at 8 bits 16 rows of a head share a scale.
+constexpr int kPackedRows = 16;
+
+// Device pointers of a store of codes and scales.
+struct PackedStore {
+  uint8_t* kc;
+  uint8_t* ks;
+  uint8_t* vc;
+  uint8_t* vs;
+};
+
+// Pointers present and aligned, rows a multiple of kPackedRows; `bits` 4 or 8 (api.cu).
+sdpa_status check_packed_store(const PackedStore& st, int bits, int64_t rows);
+
+// A constant that the compiler keeps in a register.
+__device__ __forceinline__ uint32_t in_register(uint32_t v) {
+  asm volatile("" : "+r"(v));
+  return v;
+}
+
+// 16-byte blocks from global to shared memory, counted on an mbarrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+}  // namespace sdpa

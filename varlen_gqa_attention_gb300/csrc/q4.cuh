@@ -12,14 +12,9 @@
 // within a row: at 4 bits that would leave pieces of 32 to 128 bytes per row).
 #pragma once
 
-#include <cuda_fp16.h>
-
-#include "common.cuh"
+#include "packed.cuh"
 
 namespace sdpa {
-
-constexpr int kQ4RowAlign = 16;  // store rows are a multiple of this, so that 16 rows of codes and
-                                 // of scales are whole 16-byte blocks at every head dim
 
 // s(b) and twice it, as fp32.
 __device__ __forceinline__ float q4_scale(uint32_t b) { return __uint_as_float((b << 20) + (106u << 23)); }
@@ -43,11 +38,6 @@ __device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t bits) {
   uint32_t r;
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;\n" : "=r"(r) : "r"(w), "n"(MASK), "r"(bits));
   return r;
-}
-// A constant that the compiler keeps in a register.
-__device__ __forceinline__ uint32_t in_register(uint32_t v) {
-  asm volatile("" : "+r"(v));
-  return v;
 }
 
 // Two bf16 values from nibbles i and i + 4 of a word (shifted so that they are bits 0-3 and 16-19):
@@ -109,28 +99,9 @@ __device__ __forceinline__ uint4 q4_q_order(const uint4& a) {
 }
 
 
-// 16-byte blocks from global to shared memory, counted on an mbarrier.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
-
-// Device pointers of a 4-bit store.
-struct Q4Store {
-  uint8_t* kc;
-  uint8_t* ks;
-  uint8_t* vc;
-  uint8_t* vs;
-};
-
-// Pointers present and aligned, rows a multiple of kQ4RowAlign (api.cu).
-sdpa_status check_q4_store(const Q4Store& q4, int64_t rows);
-
 struct Q4AttnArgs {
   AttnArgs a;  // k, v unused
-  Q4Store st;
+  PackedStore st;
   int choice;  // both split-K kernels are launched, and the schedule is one's (hdr->sk_rows)
 };
 
@@ -150,7 +121,7 @@ struct Q4StageArgs {
   const SegRec* segs;  // the scheduler's records
   int S, Hkv, D, pf_cols;
   int64_t rows, rows_pf;
-  Q4Store st;
+  PackedStore st;
   __nv_bfloat16* k;
   __half* v;
 };

@@ -695,7 +695,7 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Cfg<D>::kPerSm) sdpa_q4_direct_k
     return;
   }
   // this CTA's keys: runs of 64, as even as they go
-  const int64_t r0 = (int64_t)(t - ur.q_start) * A.group, lo = w.lo & -kQ4RowAlign;
+  const int64_t r0 = (int64_t)(t - ur.q_start) * A.group, lo = w.lo & -kPackedRows;
   const int64_t per = (udiv((int64_t)w.hi - lo + parts - 1, parts) + 63) & ~(int64_t)63;
   const int64_t pos_lo = lo + rank * per, pos_hi = min(pos_lo + per, (int64_t)w.hi);
   if (pos_lo < pos_hi) {

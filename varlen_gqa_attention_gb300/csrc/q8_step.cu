@@ -1,0 +1,278 @@
+// q8_step.cu - a step's rows rotated and written into the 8-bit column store, and rows read back from it.
+//
+// A block of 16 rows of a head shares a scale, so a block is coded as a whole: a warp takes one block of one head
+// of K or of V, holds its new rows (keys rotated exactly to bf16, as for the 4-bit store: see rope.cu) and the
+// rows that it keeps, takes their largest magnitude, and writes the new rows' codes, and the others' again if the
+// scale changed.  Nothing is read twice, and nothing is exchanged between warps.
+//   * A CTA looks at a run of packed rows for those that are the first of their block in a segment, and takes
+//     these blocks one after another: their rows' cells and angles in shared memory, then a warp a (head, K or V).
+//   * A row that the step does not write is kept if it holds a position from before the step: the block's earlier
+//     rows, and on a ring that has wrapped the later ones too.  What else lies in the block (a former sequence's
+//     rows) counts for nothing and keeps its bytes.
+//   * A step that fills a whole ring may come back to the block it began in; the block's first visit then takes
+//     the rows of both.
+// The queries are rotated by CTAs of their own in the same launch.
+#include "q8.cuh"
+#include "step.cuh"
+
+namespace sdpa {
+
+// A lane's 8 bf16 values with NaN as 0, clamped to what the largest scale holds (127 * 512).
+__device__ __forceinline__ uint32_t q8_storable(uint32_t w) {
+  __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&w);
+  const uint32_t clean = w & __heq2_mask(v, v);
+  v = *reinterpret_cast<const __nv_bfloat162*>(&clean);
+  v = __hmin2(__hmax2(v, __float2bfloat162_rn(-65024.f)), __float2bfloat162_rn(65024.f));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// The low byte of round(v) + 128: adding 1.5 * 2^23 rounds (halves to even) and leaves the integer's two's
+// complement in the low bits.
+__device__ __forceinline__ uint32_t q8_code(float v) { return __float_as_uint(v + 12582912.f) ^ 128u; }
+__device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+// The codes of 8 bf16 values, inv being 1 / s (a power of two: the product is exact).
+__device__ __forceinline__ uint2 q8_codes8(const uint4& w, float inv) {
+  return make_uint2(bytes4(q8_code(bf_lo(w.x) * inv), q8_code(bf_hi(w.x) * inv), q8_code(bf_lo(w.y) * inv),
+                           q8_code(bf_hi(w.y) * inv)),
+                    bytes4(q8_code(bf_lo(w.z) * inv), q8_code(bf_hi(w.z) * inv), q8_code(bf_lo(w.w) * inv),
+                           q8_code(bf_hi(w.w) * inv)));
+}
+__device__ __forceinline__ float q8_int(uint32_t w, int k) { return (float)(int)((w >> (8 * k) & 255u) - 128); }
+// A word of codes under a scale `ratio` (s before / s after) times as coarse.
+__device__ __forceinline__ uint32_t q8_again(uint32_t w, float ratio) {
+  return bytes4(q8_code(q8_int(w, 0) * ratio), q8_code(q8_int(w, 1) * ratio), q8_code(q8_int(w, 2) * ratio),
+                q8_code(q8_int(w, 3) * ratio));
+}
+__device__ __forceinline__ float q8_amax4(uint32_t w) {
+  return fmaxf(fmaxf(fabsf(q8_int(w, 0)), fabsf(q8_int(w, 1))), fmaxf(fabsf(q8_int(w, 2)), fabsf(q8_int(w, 3))));
+}
+
+// What the warps need of a block: where its rows come from (a packed row, kKept or kNone), and where it lies.
+constexpr int kKept = -1, kNone = -2;
+struct BlockRows {
+  int src[kPackedRows];
+  int pos[kPackedRows][kRopeAxes];
+};
+
+template <int D, bool IL>
+__device__ __forceinline__ void code_blocks(const StepArgs& A, int block, RowTable& s_rows, BlockRows& s_block,
+                                            int (&s_first)[kStepRows], int& s_count,
+                                            float2 (*s_angles)[D / 2]) {
+  constexpr int LPH = D / 16, RPP = 32 / LPH, U = kPackedRows / RPP, kWarps = kRopeThreads / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, li = lane % LPH, ls = lane / LPH;
+  const LaneDims<IL> ld(A.r.half, li);
+  const int j0 = ld.turn ? ld.j0 : 0;
+  const int part = block % A.kv_parts;
+  const int64_t t0 = (int64_t)(block / A.kv_parts) * A.cr;
+  const int n = (int)min((int64_t)A.cr, A.T - t0);
+  const int ia = 2 * A.Hkv * part / A.kv_parts, ib = 2 * A.Hkv * (part + 1) / A.kv_parts;  // items: (head, K or V)
+  find_rows(A, t0, n, &s_rows, false);
+  // the rows that are the first of their block, in row order
+  if (warp == 0) {
+    bool first = false;
+    if (lane < n) {
+      int col;
+      const int64_t p = row_place(&s_rows, t0, lane, &col);
+      if (p >= 0) {
+        const int4 g = s_rows.seg[lane];
+        const int64_t begin = max((int64_t)g.w - g.y, (int64_t)0), b0 = p & -kPackedRows;
+        first = (p == b0 || p == begin) && b0 - (begin & -kPackedRows) < A.rows;
+      }
+    }
+    const uint32_t all = __ballot_sync(0xffffffffu, first);
+    if (first) s_first[__popc(all & ((1u << lane) - 1))] = lane;
+    if (lane == 0) s_count = __popc(all);
+  }
+  __syncthreads();
+  const int count = s_count;
+  for (int f = 0; f < count; ++f) {
+    const int r = s_first[f];
+    const int4 g = s_rows.seg[r];
+    const int64_t begin = max((int64_t)g.w - g.y, (int64_t)0);
+    const int64_t b0 = ((int64_t)g.w - g.y + (t0 + r - g.x)) & -kPackedRows;
+    bool fresh = false;
+    if (tid < kPackedRows) {
+      int64_t p = b0 + tid;
+      if (p >= g.w && p - A.rows >= 0) p -= A.rows;               // a row of the lap before
+      if (p < begin && p + A.rows < g.w) p += A.rows;             // (one that this step writes a lap later)
+      int src = p >= g.w || p < 0 ? kNone : p < begin ? kKept : (int)(g.x + (p - ((int64_t)g.w - g.y)));
+      int pos[kRopeAxes] = {0, 0, 0, 0};
+      if (src >= 0) {
+        fetch_positions(A.r, src, (int)p, pos);
+        if (!check_positions(A.r, pos)) src = p - A.rows >= 0 ? kKept : kNone;  // nothing of the row is written
+      }
+      s_block.src[tid] = src;
+      fresh = src >= 0;
+#pragma unroll
+      for (int a = 0; a < kRopeAxes; ++a) s_block.pos[tid][a] = pos[a];
+    }
+    if (!__syncthreads_or(fresh)) continue;  // (no row of the block has angles)
+    for (int i = tid; i < kPackedRows * A.r.half; i += kRopeThreads) {
+      const int o = i / A.r.half, j = i - o * A.r.half;
+      if (s_block.src[o] < 0) continue;
+      int p = s_block.pos[o][0];
+#pragma unroll
+      for (int a = 1; a < kRopeAxes; ++a) p = j >= A.r.sec_end[a - 1] ? s_block.pos[o][a] : p;
+      s_angles[o][j] = __ldg(A.r.table + (uint32_t)(p * A.r.half + j));  // below 2^31 (checked on the host)
+    }
+    __syncthreads();
+
+    const int64_t brow = (uint32_t)b0 % (uint32_t)A.rows;
+    for (int item = ia + warp; item < ib; item += kWarps) {
+      const int h = item >> 1;
+      const bool key = (item & 1) == 0;
+      const int64_t cell = ((int64_t)g.z * A.Hkv + h) * A.rows + brow;
+      uint8_t* codes = (key ? A.q4.kc : A.q4.vc) + cell * D;
+      uint8_t* scale = (key ? A.q4.ks : A.q4.vs) + cell / kPackedRows;
+      Row16 x[U];
+      int src[U];
+      const uint32_t was = min((uint32_t)*scale, (uint32_t)kQ8Top);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int o = u * RPP + ls;
+        src[u] = s_block.src[o];
+        if (src[u] >= 0) {
+          const __nv_bfloat16* z = key ? A.k + src[u] * A.k_rs + (int64_t)h * A.k_hs
+                                       : A.v + src[u] * A.v_rs + (int64_t)h * A.v_hs;
+          x[u].a = ldg16(z + ld.da);
+          x[u].b = ldg16(z + ld.db);
+        } else if (src[u] == kKept) {
+          const uint2 a = *reinterpret_cast<const uint2*>(codes + o * D + ld.da);
+          const uint2 b = *reinterpret_cast<const uint2*>(codes + o * D + ld.db);
+          x[u].a = make_uint4(a.x, a.y, b.x, b.y);
+        }
+      }
+      float amax = 0.f, kept = 0.f;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (src[u] >= 0) {
+          if (key && ld.turn) {
+            Angles an;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float4 v = reinterpret_cast<const float4*>(s_angles[u * RPP + ls] + j0)[k];
+              an.cs[2 * k] = v.x; an.sn[2 * k] = v.y;
+              an.cs[2 * k + 1] = v.z; an.sn[2 * k + 1] = v.w;
+            }
+            turn16<IL, true>(&x[u], an);
+          }
+          x[u].a = make_uint4(q8_storable(x[u].a.x), q8_storable(x[u].a.y), q8_storable(x[u].a.z), q8_storable(x[u].a.w));
+          x[u].b = make_uint4(q8_storable(x[u].b.x), q8_storable(x[u].b.y), q8_storable(x[u].b.z), q8_storable(x[u].b.w));
+          const uint32_t ca[4] = {x[u].a.x, x[u].a.y, x[u].a.z, x[u].a.w};
+          const uint32_t cb[4] = {x[u].b.x, x[u].b.y, x[u].b.z, x[u].b.w};
+          amax = fmaxf(amax, fmaxf(amax8(ca), amax8(cb)));
+        } else if (src[u] == kKept) {
+          kept = fmaxf(kept, fmaxf(fmaxf(q8_amax4(x[u].a.x), q8_amax4(x[u].a.y)),
+                                   fmaxf(q8_amax4(x[u].a.z), q8_amax4(x[u].a.w))));
+        }
+      }
+      amax = fmaxf(amax, kept * q8_scale(was));
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+      const uint32_t byte = q8_scale_byte(amax);
+      const float inv = __uint_as_float((127 + kQ8Bias - byte) << 23);
+      const float ratio = q8_scale(was) * inv;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        uint8_t* to = codes + (u * RPP + ls) * D;
+        if (src[u] >= 0) {
+          *reinterpret_cast<uint2*>(to + ld.da) = q8_codes8(x[u].a, inv);
+          *reinterpret_cast<uint2*>(to + ld.db) = q8_codes8(x[u].b, inv);
+        } else if (src[u] == kKept && byte != was) {
+          *reinterpret_cast<uint2*>(to + ld.da) = make_uint2(q8_again(x[u].a.x, ratio), q8_again(x[u].a.y, ratio));
+          *reinterpret_cast<uint2*>(to + ld.db) = make_uint2(q8_again(x[u].a.z, ratio), q8_again(x[u].a.w, ratio));
+        }
+      }
+      if (lane == 0) *scale = (uint8_t)byte;
+    }
+    if (f + 1 < count) __syncthreads();  // the block's records are written again
+  }
+}
+
+// CTAs [0, kv_ctas) code blocks, the others rotate queries.
+template <int D, bool IL>
+__global__ void __launch_bounds__(kRopeThreads, D == 256 ? 2 : 3) sdpa_rope_append_q8_kernel(StepArgs A) {
+  __shared__ RowTable s_rows;
+  __shared__ BlockRows s_block;
+  __shared__ int s_first[kStepRows], s_count;
+  __shared__ __align__(16) float2 s_angles[kPackedRows][D / 2];
+  if ((int)blockIdx.x < A.kv_ctas) {
+    code_blocks<D, IL>(A, blockIdx.x, s_rows, s_block, s_first, s_count, s_angles);
+  } else {
+    step_passes<D, IL, false>(A, blockIdx.x - A.kv_ctas, s_rows, s_angles,
+                              [](Row16&, const LaneDims<IL>&, const Angles&, bool, int, int, int2) {});
+  }
+}
+
+// The rows of a segment table read back from an 8-bit store as bf16 (exact), rows that no live segment holds and
+// rows before a sequence's beginning as 0.
+template <int D>
+__global__ void __launch_bounds__(kRopeThreads) sdpa_q8_unpack_kernel(StepArgs A) {
+  __shared__ RowTable s_rows;
+  constexpr int LPH = D / 8, U = 4;
+  const int64_t t0 = (int64_t)blockIdx.x * A.cr;
+  const int n = (int)min((int64_t)A.cr, A.T - t0);
+  find_rows(A, t0, n, &s_rows, blockIdx.x == 0);
+  if (threadIdx.x < n) {
+    int col = 0;
+    const int64_t p = row_place(&s_rows, t0, threadIdx.x, &col);
+    s_rows.cell[threadIdx.x] = p >= 0 ? make_int2((int)((uint32_t)p % (uint32_t)A.rows), col) : make_int2(-1, 0);
+  }
+  __syncthreads();
+  const int per = A.Hkv * LPH;  // chunks of 8 dims of a row; a warp takes a row
+  for (int r = threadIdx.x / 32; r < n; r += kRopeThreads / 32) {
+    const int2 at = s_rows.cell[r];
+    const int64_t dst = (t0 + r) * A.o_rs;
+    for (int x0 = threadIdx.x % 32; x0 < per; x0 += 32 * U) {
+      uint2 kw[U], vw[U];
+      uint32_t kb[U], vb[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int x = x0 + 32 * u, h = x / LPH, c = x % LPH;
+        if (x < per && at.x >= 0) {
+          const int64_t cell = ((int64_t)at.y * A.Hkv + h) * A.rows + at.x;
+          kw[u] = *reinterpret_cast<const uint2*>(A.q4.kc + cell * D + 8 * c);
+          vw[u] = *reinterpret_cast<const uint2*>(A.q4.vc + cell * D + 8 * c);
+          kb[u] = A.q4.ks[cell / kPackedRows];
+          vb[u] = A.q4.vs[cell / kPackedRows];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int x = x0 + 32 * u, h = x / LPH, c = x % LPH;
+        if (x >= per) break;
+        const int64_t to = dst + (int64_t)h * A.o_hs + 8 * c;
+        uint4 k = make_uint4(0, 0, 0, 0), v = k;
+        if (at.x >= 0) {
+          const __nv_bfloat162 ks = q8_scale_bf16(kb[u]), vs = q8_scale_bf16(vb[u]);
+          const uint2 k0 = q8_words4(kw[u].x, ks), k1 = q8_words4(kw[u].y, ks);
+          const uint2 v0 = q8_words4(vw[u].x, vs), v1 = q8_words4(vw[u].y, vs);
+          k = make_uint4(k0.x, k0.y, k1.x, k1.y);
+          v = make_uint4(v0.x, v0.y, v1.x, v1.y);
+        }
+        stg16(A.k_out + to, k);
+        stg16(A.v_out + to, v);
+      }
+    }
+  }
+}
+
+template <bool IL>
+static const void* append_ptr(int D) {
+  switch (D) {
+    case 64: return (const void*)sdpa_rope_append_q8_kernel<64, IL>;
+    case 128: return (const void*)sdpa_rope_append_q8_kernel<128, IL>;
+    default: return (const void*)sdpa_rope_append_q8_kernel<256, IL>;
+  }
+}
+const void* rope_append_q8_kernel_ptr(int D, bool il) { return il ? append_ptr<true>(D) : append_ptr<false>(D); }
+const void* q8_unpack_kernel_ptr(int D) {
+  switch (D) {
+    case 64: return (const void*)sdpa_q8_unpack_kernel<64>;
+    case 128: return (const void*)sdpa_q8_unpack_kernel<128>;
+    default: return (const void*)sdpa_q8_unpack_kernel<256>;
+  }
+}
+
+}  // namespace sdpa

@@ -112,10 +112,35 @@ sdpa_status launch_step(const void* f, StepArgs& A, int passes, cudaStream_t str
   return SDPA_OK;
 }
 
+// The 8-bit append: CTAs for blocks of keys and values, then CTAs for queries (`q_passes` of a row).  A run of
+// rows holds the beginnings of about T / 16 + S blocks over the whole table, and a CTA takes the rows of about one
+// block; where that leaves SMs idle, CTAs share a run's heads, down to one (head, K or V) a warp.
+sdpa_status launch_step_q8(const void* f, StepArgs& A, int q_passes, cudaStream_t stream) {
+  if (A.T == 0) return SDPA_OK;
+  int sms = 0;
+  sdpa_status st = device_sms(&sms);
+  if (st) return st;
+  const int64_t wave = 3 * (int64_t)sms, warps = kRopeThreads / 32;
+  const int64_t blocks = A.T / kPackedRows + std::min<int64_t>(A.S, A.T) + 1;
+  A.cr = (int)std::min<int64_t>(kStepRows, (A.T + blocks - 1) / blocks);
+  const int64_t runs = (A.T + A.cr - 1) / A.cr;
+  A.kv_parts = (int)std::max<int64_t>(1, std::min<int64_t>((2 * (int64_t)A.Hkv + warps - 1) / warps, wave / runs));
+  const int64_t kv = A.S > 0 ? runs * A.kv_parts : 0;
+  const int64_t all = A.T * q_passes, per = std::max<int64_t>(warps, (all + wave - 1) / wave);
+  const int64_t grid = kv + (all + per - 1) / per;
+  if (per > INT_MAX || grid > INT_MAX) return fail(SDPA_ERR_SHAPE, "%lld rows of %d heads", (long long)A.T, A.Hq + 2 * A.Hkv);
+  A.kv_ctas = (int)kv;
+  A.per = (int)per;
+  void* args[] = {(void*)&A};
+  cudaError_t e = cudaLaunchKernel(f, dim3((unsigned)grid), dim3(kRopeThreads), args, 0, stream);
+  if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "rotated 8-bit append launch: %s", cudaGetErrorString(e));
+  return SDPA_OK;
+}
+
 sdpa_status rope_append(const void* q, int64_t q_rs, int64_t q_hs, const void* k, int64_t k_rs, int64_t k_hs,
                         const void* v, int64_t v_rs, int64_t v_hs, int64_t T, int Hq, int Hkv, int D,
-                        const sdpa_rotation* rotation, void* k_store, void* v_store, const Q4Store* q4, int64_t rows,
-                        int cols, const int32_t* seq_info, const int32_t* seg_mode, int S, int window, void* q_out,
+                        const sdpa_rotation* rotation, void* k_store, void* v_store, const PackedStore* packed, int bits,
+                        int64_t rows, int cols, const int32_t* seq_info, const int32_t* seg_mode, int S, int window, void* q_out,
                         int64_t o_rs, int64_t o_hs, int32_t* status_dev, void* stream) {
   set_last_error("");
   sdpa_status st = check_step(T, Hq, Hkv, D, S, rows, cols, window, seq_info, seg_mode);
@@ -127,9 +152,9 @@ sdpa_status rope_append(const void* q, int64_t q_rs, int64_t q_hs, const void* k
     return fail(SDPA_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
   if (bad_strides(q_rs, q_hs) || bad_strides(k_rs, k_hs) || bad_strides(v_rs, v_hs) || bad_strides(o_rs, o_hs))
     return fail(SDPA_ERR_STRIDE, "row/head strides must be non-negative multiples of 8 elements");
-  if (q4) {
-    if ((st = check_q4_store(*q4, rows))) return st;
-    A.q4 = *q4;
+  if (packed) {
+    if ((st = check_packed_store(*packed, bits, rows))) return st;
+    A.q4 = *packed;
   } else {
     if (!k_store || !v_store) return fail(SDPA_ERR_NULL, "a store pointer is NULL");
     if (!aligned16(k_store) || !aligned16(v_store)) return fail(SDPA_ERR_ALIGN, "stores must be 16-byte aligned");
@@ -158,9 +183,41 @@ sdpa_status rope_append(const void* q, int64_t q_rs, int64_t q_hs, const void* k
   A.k_store = (__nv_bfloat16*)k_store;
   A.v_store = (__nv_bfloat16*)v_store;
   A.status_dev = status_dev;
-  const int hpp = rope_heads_per_pass(D), passes = (Hq + hpp - 1) / hpp + 2 * ((Hkv + hpp - 1) / hpp);
-  return launch_step(rope_append_kernel_ptr(D, rotation->interleaved != 0, q4 != nullptr), A, passes,
-                     (cudaStream_t)stream, "rotated append");
+  const int hpp = rope_heads_per_pass(D), q_passes = (Hq + hpp - 1) / hpp;
+  if (bits == 8)
+    return launch_step_q8(rope_append_q8_kernel_ptr(D, rotation->interleaved != 0), A, q_passes, (cudaStream_t)stream);
+  return launch_step(rope_append_kernel_ptr(D, rotation->interleaved != 0, bits == 4), A,
+                     q_passes + 2 * ((Hkv + hpp - 1) / hpp), (cudaStream_t)stream, "rotated append");
+}
+
+// Rows of a segment table read back from a store of codes.
+sdpa_status unpack(const PackedStore& store, int bits, int64_t rows, int cols, int Hkv, int D, const int32_t* seq_info,
+                   const int32_t* seg_mode, int S, int window, int64_t T, void* k_out, void* v_out, int64_t o_rs,
+                   int64_t o_hs, int32_t* status_dev, void* stream) {
+  sdpa_status st = check_step(T, Hkv, Hkv, D, S, rows, cols, window, seq_info, seg_mode);
+  if (st) return st;
+  StepArgs A{};
+  A.q4 = store;
+  if ((st = check_packed_store(store, bits, rows))) return st;
+  if (T > 0 && (!k_out || !v_out)) return fail(SDPA_ERR_NULL, "a required pointer is NULL");
+  if (!aligned16(k_out) || !aligned16(v_out)) return fail(SDPA_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
+  if (bad_strides(o_rs, o_hs))
+    return fail(SDPA_ERR_STRIDE, "row/head strides must be non-negative multiples of 8 elements");
+  A.seq_info = seq_info;
+  A.seg_mode = seg_mode;
+  A.S = S;
+  A.window = window;
+  A.cols = cols;
+  A.Hkv = Hkv;
+  A.T = T;
+  A.rows = rows;
+  A.k_out = (__nv_bfloat16*)k_out;
+  A.v_out = (__nv_bfloat16*)v_out;
+  A.o_rs = o_rs;
+  A.o_hs = o_hs;
+  A.status_dev = status_dev;
+  return launch_step(bits == 8 ? q8_unpack_kernel_ptr(D) : q4_unpack_kernel_ptr(D), A, 0, (cudaStream_t)stream,
+                     bits == 8 ? "8-bit unpack" : "4-bit unpack");
 }
 
 }  // namespace
@@ -213,7 +270,7 @@ sdpa_status sdpa_rope_append(const void* q, int64_t q_row_stride, int64_t q_head
                              const int32_t* seq_info, const int32_t* seg_mode, int S, int window, void* q_out,
                              int64_t o_row_stride, int64_t o_head_stride, int32_t* status_dev, void* stream) {
   return rope_append(q, q_row_stride, q_head_stride, k_new, k_row_stride, k_head_stride, v_new, v_row_stride,
-                     v_head_stride, T, Hq, Hkv, D, rotation, k_store, v_store, nullptr, rows, cols, seq_info,
+                     v_head_stride, T, Hq, Hkv, D, rotation, k_store, v_store, nullptr, 16, rows, cols, seq_info,
                      seg_mode, S, window, q_out, o_row_stride, o_head_stride, status_dev, stream);
 }
 
@@ -225,9 +282,23 @@ sdpa_status sdpa_rope_append_fourbit(const void* q, int64_t q_row_stride, int64_
                                 int64_t o_row_stride, int64_t o_head_stride, int32_t* status_dev, void* stream) {
   set_last_error("");
   if (!store) return fail(SDPA_ERR_NULL, "store is NULL");
-  const Q4Store q4{store->k_codes, store->k_scales, store->v_codes, store->v_scales};
+  const PackedStore q4{store->k_codes, store->k_scales, store->v_codes, store->v_scales};
   return rope_append(q, q_row_stride, q_head_stride, k_new, k_row_stride, k_head_stride, v_new, v_row_stride,
-                     v_head_stride, T, Hq, Hkv, D, rotation, nullptr, nullptr, &q4, rows, cols, seq_info, seg_mode, S,
+                     v_head_stride, T, Hq, Hkv, D, rotation, nullptr, nullptr, &q4, 4, rows, cols, seq_info, seg_mode, S,
+                     window, q_out, o_row_stride, o_head_stride, status_dev, stream);
+}
+
+sdpa_status sdpa_rope_append_eightbit(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* k_new,
+                                 int64_t k_row_stride, int64_t k_head_stride, const void* v_new,
+                                 int64_t v_row_stride, int64_t v_head_stride, int64_t T, int Hq, int Hkv, int D,
+                                 const sdpa_rotation* rotation, const sdpa_q8_store* store, int64_t rows, int cols,
+                                 const int32_t* seq_info, const int32_t* seg_mode, int S, int window, void* q_out,
+                                 int64_t o_row_stride, int64_t o_head_stride, int32_t* status_dev, void* stream) {
+  set_last_error("");
+  if (!store) return fail(SDPA_ERR_NULL, "store is NULL");
+  const PackedStore q8{store->k_codes, store->k_scales, store->v_codes, store->v_scales};
+  return rope_append(q, q_row_stride, q_head_stride, k_new, k_row_stride, k_head_stride, v_new, v_row_stride,
+                     v_head_stride, T, Hq, Hkv, D, rotation, nullptr, nullptr, &q8, 8, rows, cols, seq_info, seg_mode, S,
                      window, q_out, o_row_stride, o_head_stride, status_dev, stream);
 }
 
@@ -237,29 +308,18 @@ sdpa_status sdpa_fourbit_unpack(const sdpa_q4_store* store, int64_t rows, int co
                            int32_t* status_dev, void* stream) {
   set_last_error("");
   if (!store) return fail(SDPA_ERR_NULL, "store is NULL");
-  sdpa_status st = check_step(T, Hkv, Hkv, D, S, rows, cols, window, seq_info, seg_mode);
-  if (st) return st;
-  StepArgs A{};
-  A.q4 = Q4Store{store->k_codes, store->k_scales, store->v_codes, store->v_scales};
-  if ((st = check_q4_store(A.q4, rows))) return st;
-  if (T > 0 && (!k_out || !v_out)) return fail(SDPA_ERR_NULL, "a required pointer is NULL");
-  if (!aligned16(k_out) || !aligned16(v_out)) return fail(SDPA_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
-  if (bad_strides(o_row_stride, o_head_stride))
-    return fail(SDPA_ERR_STRIDE, "row/head strides must be non-negative multiples of 8 elements");
-  A.seq_info = seq_info;
-  A.seg_mode = seg_mode;
-  A.S = S;
-  A.window = window;
-  A.cols = cols;
-  A.Hkv = Hkv;
-  A.T = T;
-  A.rows = rows;
-  A.k_out = (__nv_bfloat16*)k_out;
-  A.v_out = (__nv_bfloat16*)v_out;
-  A.o_rs = o_row_stride;
-  A.o_hs = o_head_stride;
-  A.status_dev = status_dev;
-  return launch_step(q4_unpack_kernel_ptr(D), A, 0, (cudaStream_t)stream, "4-bit unpack");
+  return unpack(PackedStore{store->k_codes, store->k_scales, store->v_codes, store->v_scales}, 4, rows, cols, Hkv, D,
+                seq_info, seg_mode, S, window, T, k_out, v_out, o_row_stride, o_head_stride, status_dev, stream);
+}
+
+sdpa_status sdpa_eightbit_unpack(const sdpa_q8_store* store, int64_t rows, int cols, int Hkv, int D,
+                            const int32_t* seq_info, const int32_t* seg_mode, int S, int window, int64_t T,
+                            void* k_out, void* v_out, int64_t o_row_stride, int64_t o_head_stride,
+                            int32_t* status_dev, void* stream) {
+  set_last_error("");
+  if (!store) return fail(SDPA_ERR_NULL, "store is NULL");
+  return unpack(PackedStore{store->k_codes, store->k_scales, store->v_codes, store->v_scales}, 8, rows, cols, Hkv, D,
+                seq_info, seg_mode, S, window, T, k_out, v_out, o_row_stride, o_head_stride, status_dev, stream);
 }
 
 }  // extern "C"
