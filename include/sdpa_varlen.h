@@ -355,6 +355,23 @@ sdpa_status sdpa_eightbit_unpack(const sdpa_q8_store* store, int64_t rows, int c
                             void* k_out, void* v_out, int64_t o_row_stride, int64_t o_head_stride,
                             int32_t* status_dev, void* stream);
 
+/* Bytes of device workspace sdpa_varlen_eightbit takes for up to T rows and S segments of a store of these
+ * sizes: as sdpa_varlen_fourbit_workspace_bytes, staged columns and the counting of empty entries included. */
+size_t sdpa_varlen_eightbit_workspace_bytes(int64_t T, int Hq, int Hkv, int D, int S, int64_t rows, int cols);
+
+/*
+ * sdpa_varlen over an 8-bit store: the attention of the values the codes stand for, with probabilities rounded to
+ * fp16 (2^-11 of each) whichever kernel a segment takes.  A value of a query row that is less than 2^-31 of the
+ * row's largest magnitude may be off by 2^-40 of that.  seg_mode, checks and status bits as for
+ * sdpa_varlen_fourbit, with the store's own (code pointers 16-byte aligned, rows a multiple of 16, cols * Hkv below 2^31)
+ * and workspace of at least sdpa_varlen_eightbit_workspace_bytes bytes.
+ */
+sdpa_status sdpa_varlen_eightbit(const void* q, int64_t T, int Hq, int D, int64_t q_row_stride, int64_t q_head_stride,
+                            const sdpa_q8_store* store, int64_t rows, int cols, int Hkv, const int32_t* seq_info,
+                            const int32_t* seg_mode, int S, int causal, int window, float scale, void* out,
+                            int64_t o_row_stride, int64_t o_head_stride, void* workspace, size_t ws_bytes,
+                            int32_t* status_dev, void* stream);
+
 /* Set the process-wide route policy (SDPA_ROUTE_*).  Returns SDPA_ERR_ARG if unknown. */
 sdpa_status sdpa_set_route_policy(int policy);
 

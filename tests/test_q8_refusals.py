@@ -5,8 +5,9 @@ import torch
 
 import varlen_gqa_attention_gb300 as pkg
 
-from test_step_refusals import (ALIGN, ARG, BAD_ROTATIONS, FAKE, GQA, HEAD_DIM, NULL, SHAPE, STRIDE, WORKSPACE, bf, f32, i32,
-                                rotation, u8, z)
+from test_step_refusals import (ALIGN, ARG, BAD_ROTATIONS, FAKE, GQA, HEAD_DIM, NULL, SHAPE, STRIDE, WORKSPACE, f32, i32,
+                                rotation,
+                                u8, z)
 
 
 def store(**kw):
@@ -126,3 +127,53 @@ def test_python_unpack():
                        (dict(k_out=z(3, 2, 64), v_out=z(3, 4, 64)[:, ::2]), "share strides"), (dict(), "CUDA device")):
         with pytest.raises(ValueError, match=needle):
             pkg.sdpa_q8_unpack(q8(), seq, 3, **kw)
+
+
+def attend(**kw):
+    a = dict(q=FAKE, T=8, Hq=4, D=64, q_rs=256, q_hs=64, store=store(), rows=32, cols=2, Hkv=2, seq=FAKE, mode=None,
+             S=1, causal=1, window=0, scale=0.125, out=FAKE, o_rs=256, o_hs=64, ws=FAKE, ws_bytes=1 << 30,
+             status=None, stream=None)
+    assert set(kw) <= set(a)
+    a.update(kw)
+    return pkg.library().sdpa_varlen_eightbit(*a.values())
+
+
+@pytest.mark.parametrize("kw,code", BAD_STORES + [
+    (dict(q=None), NULL), (dict(out=None), NULL), (dict(seq=None), NULL), (dict(ws=None), WORKSPACE),
+    (dict(T=-1), SHAPE), (dict(rows=1 << 31), SHAPE), (dict(S=-1), SHAPE), (dict(D=112), HEAD_DIM), (dict(Hq=5), GQA),
+    (dict(Hq=258), GQA), (dict(window=-1), ARG), (dict(scale=float("inf")), ARG), (dict(scale=float("nan")), ARG),
+    (dict(scale=-0.125), ARG), (dict(q=FAKE + 2), ALIGN), (dict(out=FAKE + 8), ALIGN), (dict(seq=FAKE + 4), ALIGN),
+    (dict(mode=FAKE + 8), ALIGN), (dict(ws=FAKE + 16), ALIGN), (dict(q_rs=-8), STRIDE), (dict(q_hs=60), STRIDE),
+    (dict(o_rs=12), STRIDE), (dict(o_hs=-64), STRIDE), (dict(cols=1 << 30, Hkv=2), SHAPE),
+])
+def test_attend(kw, code):
+    assert attend(**kw) == code
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_workspace_for_bounds_serves_every_smaller_call(D):
+    need = pkg.library().sdpa_varlen_eightbit_workspace_bytes
+    pkg.set_route_policy(pkg.ROUTE_SPLITK)  # without staged columns, of which a call takes what it is given
+    try:
+        for Hq, Hkv in ((8, 8), (32, 8), (16, 1), (256, 2)):
+            for T in (1, 16, 64, 257, 2048):
+                for S_ in (0, 1, 7, 64, 500):
+                    bound = need(T, Hq, Hkv, D, S_, 4096, 64)
+                    for t in (0, 1, 3, 40, 200, T):
+                        for s in (0, 1, 6, 63, S_):
+                            if t <= T and s <= S_:
+                                assert need(t, Hq, Hkv, D, s, 4096, 64) <= bound, (Hq, Hkv, T, S_, t, s)
+    finally:
+        pkg.set_route_policy(pkg.ROUTE_AUTO)
+    assert need(1, 3, 2, D, 1, 64, 1) == 0 and need(1, 2, 2, 96, 1, 64, 1) == 0 and need(1, 2, 2, D, 1, 1 << 31, 1) == 0
+
+
+def test_python_attend():
+    seq = z(1, 4, dtype=i32)
+    for q, kw, needle in ((z(8, 4, 128), {}, "head dims"), (z(8, 4, 64, dtype=f32), {}, "q must be bf16"),
+                          (z(8, 4, 64), dict(seg_mode=z(1, 2)), "seg_mode"), (z(8, 4, 64), dict(out=z(8, 4, 128)), "out must be"),
+                          (z(8, 4, 64), {}, "CUDA device")):
+        with pytest.raises(ValueError, match=needle):
+            pkg.sdpa_varlen_q8(q, q8(), seq, causal=True, **kw)
+    with pytest.raises(ValueError, match="8-bit store"):
+        pkg.sdpa_varlen_q8(z(8, 4, 64), pkg.q4_store(32, 2, 2, 64), seq, causal=True)

@@ -23,7 +23,7 @@ __all__ = [
     "sdpa_varlen", "sdpa_varlen_modes", "sdpa_varlen_append", "sdpa_seq_clone", "sdpa_causal_prefill",
     "sdpa_varlen_splitk_static", "sdpa_rope", "sdpa_rope_append", "sdpa_rope_append_q4", "sdpa_q4_unpack",
     "sdpa_varlen_q4", "Q4Store", "q4_store", "rope_table", "q4_workspace_bytes", "sdpa_rope_append_q8", "sdpa_q8_unpack",
-    "Q8Store", "q8_store", "workspace_bytes", "workspace_status", "prefill_available", "set_route_policy",
+    "sdpa_varlen_q8", "Q8Store", "q8_store", "q8_workspace_bytes", "workspace_bytes", "workspace_status", "prefill_available", "set_route_policy",
     "set_timing_events", "library",
     "SDPA_OK", "SEG_BAD_QRANGE", "SEG_BAD_COL", "SEG_BAD_KV", "SEG_SPAN", "SEG_OVERLAP",
     "DEV_TIMEOUT", "ROPE_BAD_POS", "ROUTE_AUTO", "ROUTE_SPLITK", "ROUTE_PREFILL", "SdpaError",
@@ -46,6 +46,7 @@ EXPORTS = [
     "sdpa_varlen_append", "sdpa_seq_clone", "sdpa_varlen_modes", "sdpa_prefill_available",
     "sdpa_workspace_status", "sdpa_rope", "sdpa_rope_append", "sdpa_rope_append_fourbit", "sdpa_fourbit_unpack",
     "sdpa_varlen_fourbit", "sdpa_varlen_fourbit_workspace_bytes", "sdpa_rope_append_eightbit", "sdpa_eightbit_unpack",
+    "sdpa_varlen_eightbit", "sdpa_varlen_eightbit_workspace_bytes",
 ]
 
 
@@ -133,6 +134,10 @@ def library(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.sdpa_varlen_fourbit.restype = c_int
     lib.sdpa_varlen_fourbit.argtypes = [c_vp, c_i64, c_int, c_int, c_i64, c_i64, c_q4, c_i64, c_int, c_int, c_vp, c_vp,
                                    c_int, c_int, c_int, c_f, c_vp, c_i64, c_i64, c_vp, ctypes.c_size_t, c_vp, c_vp]
+    lib.sdpa_varlen_eightbit_workspace_bytes.restype = ctypes.c_size_t
+    lib.sdpa_varlen_eightbit_workspace_bytes.argtypes = lib.sdpa_varlen_fourbit_workspace_bytes.argtypes
+    lib.sdpa_varlen_eightbit.restype = c_int
+    lib.sdpa_varlen_eightbit.argtypes = lib.sdpa_varlen_fourbit.argtypes
     _lib = lib
     return lib
 
@@ -679,16 +684,13 @@ def q4_workspace_bytes(T: int, Hq: int, store: Q4Store, S: int) -> int:
         return int(library().sdpa_varlen_fourbit_workspace_bytes(T, Hq, Hkv, 2 * half, S, rows, cols))
 
 
-def sdpa_varlen_q4(q: torch.Tensor, store: Q4Store, seq_info: torch.Tensor, *, causal: bool, window: int = 0,
-                   seg_mode: Optional[torch.Tensor] = None, scale: Optional[float] = None,
-                   out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-                   status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """``sdpa_varlen`` over a 4-bit store: the attention of the values its codes stand for.
-    ``seg_mode`` (int32 [S, 2] (causal, window) per segment) replaces causal and window."""
+def _attend_packed(entry, workspace_bytes_of, q, store, store_args, seq_info, causal, window, seg_mode, scale, out,
+                   workspace, status, stream):
+    """Attention over a store of codes, whose checked parts are store_args."""
     rs, hs = _strides("q", q)
     shape = q.shape
     T, Hq, D = shape
-    rows, cols, Hkv, Ds, ptrs = _q4(store)
+    rows, cols, Hkv, Ds, ptrs = store_args
     if Ds != D:
         raise ValueError("head dims of q and the store differ")
     seq_ptr, mode_ptr, S = _table(seq_info, seg_mode)
@@ -697,13 +699,23 @@ def sdpa_varlen_q4(q: torch.Tensor, store: Q4Store, seq_info: torch.Tensor, *, c
     if out is None:
         out = _rows_like(q, shape, stream)
     if workspace is None:
-        workspace = _workspace(q4_workspace_bytes(T, Hq, store, S), q.device, stream)
+        workspace = _workspace(workspace_bytes_of(T, Hq, store, S), q.device, stream)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    _call(library().sdpa_varlen_fourbit, dev, stream, q.data_ptr(), T, Hq, D, rs, hs, ptrs, rows, cols, Hkv, seq_ptr,
+    _call(entry, dev, stream, q.data_ptr(), T, Hq, D, rs, hs, ptrs, rows, cols, Hkv, seq_ptr,
           mode_ptr, S, 1 if causal else 0, _window(window), D ** -0.5 if scale is None else float(scale), out.data_ptr(),
           ors, ohs, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _status_ptr(status))
     return out
+
+
+def sdpa_varlen_q4(q: torch.Tensor, store: Q4Store, seq_info: torch.Tensor, *, causal: bool, window: int = 0,
+                   seg_mode: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                   out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """``sdpa_varlen`` over a 4-bit store: the attention of the values its codes stand for.
+    ``seg_mode`` (int32 [S, 2] (causal, window) per segment) replaces causal and window."""
+    return _attend_packed(library().sdpa_varlen_fourbit, q4_workspace_bytes, q, store, _q4(store), seq_info, causal, window,
+                          seg_mode, scale, out, workspace, status, stream)
 
 
 # ------------------------------------------------ the 8-bit column store
@@ -762,3 +774,20 @@ def sdpa_q8_unpack(store: Q8Store, seq_info: torch.Tensor, T: int, *, window: in
     Row i of a live segment is position kv_end - q_len + i; other rows are 0."""
     return _unpack(library().sdpa_eightbit_unpack, store, _q8(store), seq_info, T, window, seg_mode, k_out, v_out,
                    status, stream)
+
+
+def q8_workspace_bytes(T: int, Hq: int, store: Q8Store, S: int) -> int:
+    """Bytes of workspace ``sdpa_varlen_q8`` needs for these sizes, on the store's device."""
+    cols, Hkv, rows, D = store.k_codes.shape
+    with torch.cuda.device(store.k_codes.device):
+        return int(library().sdpa_varlen_eightbit_workspace_bytes(T, Hq, Hkv, D, S, rows, cols))
+
+
+def sdpa_varlen_q8(q: torch.Tensor, store: Q8Store, seq_info: torch.Tensor, *, causal: bool, window: int = 0,
+                   seg_mode: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                   out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """``sdpa_varlen`` over an 8-bit store: the attention of the values its codes stand for.
+    ``seg_mode`` (int32 [S, 2] (causal, window) per segment) replaces causal and window."""
+    return _attend_packed(library().sdpa_varlen_eightbit, q8_workspace_bytes, q, store, _q8(store), seq_info, causal, window,
+                          seg_mode, scale, out, workspace, status, stream)

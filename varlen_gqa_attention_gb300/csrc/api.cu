@@ -16,6 +16,7 @@
 
 #include "common.cuh"
 #include "q4.cuh"
+#include "q8.cuh"
 
 namespace sdpa {
 
@@ -52,11 +53,16 @@ struct DevInfo {
   bool ready = false;
   int sms = 0;
   int splitk_per_sm[3] = {0, 0, 0};  // D = 64, 128, 256
-  int q4_per_sm[3] = {0, 0, 0};
+  int packed_per_sm[2][3] = {};  // 4 and 8 bits
   bool prefill_ok[3] = {false, false, false};
 };
 static std::mutex g_mu;
 static DevInfo g_dev[64];
+
+// The kernels of a store of codes.
+static const void* packed_splitk_ptr(int bits, int D) { return bits == 8 ? q8_splitk_kernel_ptr(D) : q4_splitk_kernel_ptr(D); }
+static const void* packed_direct_ptr(int bits, int D) { return bits == 8 ? q8_direct_kernel_ptr(D) : q4_direct_kernel_ptr(D); }
+static int packed_smem_bytes(int bits, int D) { return bits == 8 ? q8_splitk_smem_bytes(D) : q4_splitk_smem_bytes(D); }
 
 static int d_index(int D) { return D == 64 ? 0 : D == 128 ? 1 : 2; }
 
@@ -70,8 +76,8 @@ static sdpa_status device_info(DevInfo* out) {
   if (!di.ready) {
     e = cudaDeviceGetAttribute(&di.sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "SM count: %s", cudaGetErrorString(e));
-    for (int q4 = 0; q4 < 2; ++q4) {
-      e = cudaFuncSetAttribute(sched_kernel_ptr(q4), cudaFuncAttributeMaxDynamicSharedMemorySize,
+    for (int packed = 0; packed < 2; ++packed) {
+      e = cudaFuncSetAttribute(sched_kernel_ptr(packed), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)sched_smem_bytes());
       if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "scheduler smem attribute: %s", cudaGetErrorString(e));
     }
@@ -104,19 +110,18 @@ static sdpa_status device_info(DevInfo* out) {
           e = cudaFuncSetAttribute(q4_tile_kernel_ptr(Ds[k]), cudaFuncAttributePreferredSharedMemoryCarveout, 100);
         if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "4-bit tile kernel attributes: %s", cudaGetErrorString(e));
       }
-      const void* q4 = q4_splitk_kernel_ptr(Ds[k]);
-      const int q4_smem = q4_splitk_smem_bytes(Ds[k]);
-      e = cudaFuncSetAttribute(q4, cudaFuncAttributeMaxDynamicSharedMemorySize, q4_smem);
-      if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "smem attribute: %s", cudaGetErrorString(e));
-      e = cudaFuncSetAttribute(q4, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-      if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "carveout attribute: %s", cudaGetErrorString(e));
-      e = cudaFuncSetAttribute(q4_direct_kernel_ptr(Ds[k]), cudaFuncAttributeMaxDynamicSharedMemorySize, q4_smem);
-      if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(q4_direct_kernel_ptr(Ds[k]), cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-      if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "4-bit direct kernel attributes: %s", cudaGetErrorString(e));
-      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, q4, kQ4Threads, q4_smem);
-      if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "occupancy: %s", cudaGetErrorString(e));
-      di.q4_per_sm[k] = nb > 0 ? nb : 1;
+      for (int bits = 4; bits <= 8; bits += 4) {
+        const void* few = packed_splitk_ptr(bits, Ds[k]);
+        const int few_smem = packed_smem_bytes(bits, Ds[k]);
+        for (const void* f : {few, packed_direct_ptr(bits, Ds[k])}) {
+          e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, few_smem);
+          if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+          if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "%d-bit kernel attributes: %s", bits, cudaGetErrorString(e));
+        }
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, few, kPackedThreads, few_smem);
+        if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "occupancy: %s", cudaGetErrorString(e));
+        di.packed_per_sm[bits / 8][k] = nb > 0 ? nb : 1;
+      }
       e = cudaFuncSetAttribute(combine_pair_kernel_ptr(Ds[k]), cudaFuncAttributePreferredSharedMemoryCarveout, 100);
       if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "carveout attribute: %s", cudaGetErrorString(e));
       for (int q = 0; q < 2; ++q) {
@@ -182,6 +187,23 @@ static bool make_tensor_maps(const void* q, int64_t T, int Hq, int D, int64_t q_
   return true;
 }
 
+// TMA descriptors of an 8-bit store's codes [cols * Hkv, rows, D]: boxes of 16 rows of 128 bytes (64 at D = 64),
+// swizzled over their width.
+static bool make_q8_maps(const PackedStore& st, int64_t rows, int cols, int Hkv, int D, Q8AttnArgs* out) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint32_t es[3] = {1, 1, 1};
+  const cuuint64_t dim[3] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)cols * Hkv};
+  const cuuint64_t stride[2] = {(cuuint64_t)D, (cuuint64_t)rows * D};
+  const cuuint32_t box[3] = {(cuuint32_t)std::min(D, 128), kPackedRows, 1};
+  for (int v = 0; v < 2; ++v)
+    if (enc(v ? &out->v : &out->k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, v ? st.vc : st.kc, dim, stride, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+  return true;
+}
+
 struct Grids {
   int64_t splitk, prefill;
 };
@@ -200,15 +222,18 @@ static Grids grids_for(const DevInfo& di, int D) {
 // chunk and many single tokens) both, and the schedule is the cheaper one's; the other leaves at once.  At
 // D = 256 the output of 128 rows leaves no room for the first.
 enum class Q4Split { kFew, kTile, kEither };
-static Q4Split q4_split(int64_t T, int Hq, int Hkv, int D, int S) {
-  if (D > 128 || T * (Hq / Hkv) <= 16 * (int64_t)std::max(S, 1)) return Q4Split::kFew;
+static Q4Split q4_split(int bits, int64_t T, int Hq, int Hkv, int D, int S) {
+  if (bits == 8 || D > 128 || T * (Hq / Hkv) <= 16 * (int64_t)std::max(S, 1)) return Q4Split::kFew;
   return S <= 1 ? Q4Split::kTile : Q4Split::kEither;
 }
 // The tensor-memory kernel's cost of a key for a unit, in those of the other one for 8 rows (full loads: 0.066
 // and 0.027 ns at D = 128, 0.054 and 0.015 at D = 64).
 static float q4_tile_ratio(int D) { return D == 64 ? 3.5f : 2.5f; }
-static SkShape q4_few_shape(const DevInfo& di, int D) {
-  return {kSplitkRows, kSplitkTile, kSkQ4Few, (int64_t)di.sms * di.q4_per_sm[d_index(D)]};
+static int64_t packed_resident(const DevInfo& di, int bits, int D) {
+  return (int64_t)di.sms * di.packed_per_sm[bits / 8][d_index(D)];
+}
+static SkShape packed_few_shape(const DevInfo& di, int bits, int D) {
+  return {kSplitkRows, kSplitkTile, kSkQ4Few, packed_resident(di, bits, D)};
 }
 static SkShape q4_tile_shape(const DevInfo& di) { return {kQ4TileRows, kQ4TileKeys, kSkQ4Tile, di.sms}; }
 
@@ -251,6 +276,15 @@ struct TensorMaps {
   CUtensorMap q, k, v;
 };
 
+// A call over a store of codes: the kernels' arguments, of whichever store it is.
+struct PackedCall {
+  int bits;
+  PackedStore st;
+  Q8AttnArgs q8;
+  Q4AttnArgs q4;
+  void* args() { return bits == 8 ? (void*)&q8 : (void*)&q4; }
+};
+
 // Launch with programmatic stream serialisation (the kernel waits in-kernel for its
 // predecessor), except while the timing hook records events between the kernels: an event
 // between two kernels would only serialise them again, and each kernel is then timed alone.
@@ -286,10 +320,10 @@ static cudaError_t launch_k(const void* f, unsigned grid, unsigned block, void**
 // keys, 34.5 / 33.6; with 16/2 heads of 8192, 21 / 24, of 16384 beyond it 36 / 30; 16 tokens at D = 256 of 4096 30 / 32, of
 // 8192 52 / 47).
 constexpr int64_t kQ4DirectPart = 128;
-static int q4_direct(const DevInfo& di, int64_t T, int Hq, int Hkv, int D, int S, int64_t rows, int causal, int window,
-                     const int32_t* seg_mode) {
-  if (g_policy.load() != SDPA_ROUTE_AUTO || Hq / Hkv > kSplitkRows || S > kQ4DirectSegs) return 0;
-  const int64_t pairs = T * Hkv, resident = (int64_t)di.sms * di.q4_per_sm[d_index(D)];
+static int packed_direct_parts(const DevInfo& di, int bits, int64_t T, int Hq, int Hkv, int D, int S, int64_t rows,
+                               int causal, int window, const int32_t* seg_mode) {
+  if (g_policy.load() != SDPA_ROUTE_AUTO || Hq / Hkv > kSplitkRows || S > kPackedDirectSegs) return 0;
+  const int64_t pairs = T * Hkv, resident = packed_resident(di, bits, D);
   if (T > S && pairs > resident) return 0;
   int64_t keys = rows;  // that a row may see
   if (window > 0 && !seg_mode) keys = std::min<int64_t>(keys, causal ? window : T + window - 1);
@@ -319,14 +353,14 @@ static int64_t q4_longest(int64_t T, int group, int S) { return std::max<int64_t
 // q4_prefill_min_rows, as far as 2 GiB of workspace hold them (at least one while that takes at most 8 GiB); none
 // when the automatic route cannot reach q4_prefill_min_work.  Depends on sizes and the route policy only.
 static int64_t q4_stage_bytes_per_column(int64_t rows, int Hkv, int D) { return rows * Hkv * D * 2; }
-static int q4_stage_cols(int64_t T, int Hq, int Hkv, int D, int S, int64_t rows) {
+static int q4_stage_cols(int bits, int64_t T, int Hq, int Hkv, int D, int S, int64_t rows) {
   const int policy = g_policy.load();
   const int group = Hq / Hkv;
   if (policy == SDPA_ROUTE_SPLITK || group > kPrefillRows || kPrefillRows % group || S <= 0 || T <= 0) return 0;
   const int64_t packed = T * group;
   int64_t n = S;
   if (policy == SDPA_ROUTE_AUTO) {
-    const Q4Split sp = q4_split(T, Hq, Hkv, D, S);
+    const Q4Split sp = q4_split(bits, T, Hq, Hkv, D, S);
     if (q4_longest(T, group, S) < q4_prefill_min_rows(sp) ||
         (double)packed * Hkv * D * (double)rows < (double)q4_prefill_min_work(sp))
       return 0;
@@ -353,8 +387,8 @@ static bool prefill_launch(const SchedArgs& sa, int64_t T) {
 }
 
 static sdpa_status launch_all(const SchedArgs& sa, const AttnArgs& aa, int D, const Grids& g,
-                              const TensorMaps& tm, const AppendArgs* ap, const PackedStore* q4,
-                              const Q4StageArgs* stage, cudaStream_t st) {
+                              const TensorMaps& tm, const AppendArgs* ap, PackedCall* packed,
+                              const PackedStageArgs* stage, cudaStream_t st) {
   cudaError_t e = mark(0, st);
   if (e == cudaSuccess) {
     e = launch_sched(sa, st);
@@ -388,34 +422,35 @@ static sdpa_status launch_all(const SchedArgs& sa, const AttnArgs& aa, int D, co
   // launch is most likely empty; launched after the scheduler otherwise (measured: the
   // chained launch saves ~6 us on a decode step whose prefill kernel has nothing to do, and
   // costs ~5 us on prefill steps of a few tiles per CTA).
-  const int64_t packed = aa.T * aa.group;
+  const int64_t rows_packed = aa.T * aa.group;
   const bool pf_possible = sa.prefill_ok;
   if (e == cudaSuccess && pf_possible && stage) {
     void* args[] = {(void*)stage};
     const int64_t chunks = sa.rows_pf * stage->Hkv * (D / 8);  // of one column
     const int64_t most = std::max<int64_t>(1, 8 * g.prefill / stage->pf_cols);
-    const int64_t per = std::max<int64_t>(1, std::min<int64_t>(most, chunks / (4 * kQ4StageThreads)));
-    e = launch_k(q4_stage_kernel_ptr(D), (unsigned)(per * stage->pf_cols), kQ4StageThreads, args, 0, st, true);
-    if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "4-bit staging launch: %s", cudaGetErrorString(e));
+    const int64_t per = std::max<int64_t>(1, std::min<int64_t>(most, chunks / (4 * kPackedStageThreads)));
+    e = launch_k(packed->bits == 8 ? q8_stage_kernel_ptr(D) : q4_stage_kernel_ptr(D), (unsigned)(per * stage->pf_cols),
+                 kPackedStageThreads, args, 0, st, true);
+    if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "column staging launch: %s", cudaGetErrorString(e));
   }
   if (e == cudaSuccess && pf_possible) {
     AttnArgs pa = aa;
     pa.rows = sa.rows_pf;
     void* args[] = {(void*)&pa, (void*)&tm.q, (void*)&tm.k, (void*)&tm.v};
-    const bool chained = packed < (int64_t)kPrefillRows * std::max(sa.S, 1);
-    e = launch_k(prefill_kernel_ptr(D, q4 != nullptr), (unsigned)g.prefill, prefill_block_threads(D), args,
+    const bool chained = rows_packed < (int64_t)kPrefillRows * std::max(sa.S, 1);
+    e = launch_k(prefill_kernel_ptr(D, packed != nullptr), (unsigned)g.prefill, prefill_block_threads(D), args,
                  prefill_smem_bytes(D), st, chained);
     if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "prefill launch: %s", cudaGetErrorString(e));
   }
   if (e == cudaSuccess) e = mark(2, st);
-  if (e == cudaSuccess && q4) {
-    Q4AttnArgs ga{aa, *q4, sa.sk_choice};
-    void* args[] = {(void*)&ga};
+  if (e == cudaSuccess && packed) {
+    void* args[] = {packed->args()};
+    const int smem = packed_smem_bytes(packed->bits, D);
     if (sa.sk_choice || sa.sk[0].rows == kSplitkRows)
-      e = launch_k(q4_splitk_kernel_ptr(D), (unsigned)sa.sk[0].grid, kQ4Threads, args, q4_splitk_smem_bytes(D), st, true);
+      e = launch_k(packed_splitk_ptr(packed->bits, D), (unsigned)sa.sk[0].grid, kPackedThreads, args, smem, st, true);
     if (e == cudaSuccess && (sa.sk_choice || sa.sk[0].rows == kQ4TileRows))
       e = launch_k(q4_tile_kernel_ptr(D), (unsigned)sa.sk[1].grid, kQ4TileThreads, args, q4_tile_smem_bytes(D), st, true);
-    if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "4-bit split-K launch: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "%d-bit split-K launch: %s", packed->bits, cudaGetErrorString(e));
   } else if (e == cudaSuccess) {
     void* args[] = {(void*)&aa};
     e = launch_k(splitk_kernel_ptr(D), (unsigned)g.splitk, kSplitkThreads, args, splitk_smem_bytes(D), st, true);
@@ -426,11 +461,11 @@ static sdpa_status launch_all(const SchedArgs& sa, const AttnArgs& aa, int D, co
     void* args[] = {(void*)&aa};
     const int64_t warps = aa.T * aa.Hq;
     const int64_t blocks = std::min<int64_t>((warps * 32 + 255) / 256, 8 * (int64_t)g.prefill);
-    // 4-bit calls with few pairs: a CTA each, as many as the SMs hold at once
-    if (q4 && warps <= 8 * (int64_t)g.prefill)
+    // calls over codes with few pairs: a CTA each, as many as the SMs hold at once
+    if (packed && warps <= 8 * (int64_t)g.prefill)
       e = launch_k(combine_pair_kernel_ptr(D), (unsigned)warps, 256, args, 0, st, true);
     else
-      e = launch_k(combine_kernel_ptr(D, q4 != nullptr), (unsigned)blocks, 256, args, 0, st, true);
+      e = launch_k(combine_kernel_ptr(D, packed != nullptr), (unsigned)blocks, 256, args, 0, st, true);
     if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "combine launch: %s", cudaGetErrorString(e));
   }
   if (e == cudaSuccess) e = mark(4, st);
@@ -443,12 +478,15 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
                        const int32_t* seq_info, int S, const int32_t* inl, int causal, int window,
                        float scale, void* out, int64_t o_rs, int64_t o_hs, void* ws, size_t ws_bytes,
                        int32_t* status_dev, void* stream, const AppendArgs* ap = nullptr,
-                       const int32_t* seg_mode = nullptr, const PackedStore* q4 = nullptr) {
+                       const int32_t* seg_mode = nullptr, PackedCall* packed = nullptr) {
   g_err[0] = 0;
   sdpa_status st = check_common(T, Hq, Hkv, D, S, rows, cols, window, scale);
   if (st) return st;
-  if (q4 && (st = check_packed_store(*q4, 4, rows))) return st;
-  if (q4 && T == 0) return SDPA_OK;
+  const int bits = packed ? packed->bits : 16;
+  if (packed && (st = check_packed_store(packed->st, bits, rows))) return st;
+  if (bits == 8 && (int64_t)cols * Hkv > INT32_MAX)
+    return fail(SDPA_ERR_SHAPE, "an 8-bit store of %d columns of %d heads", cols, Hkv);
+  if (packed && T == 0) return SDPA_OK;
   // the dense entry passes its one segment by value: no table pointer to check
   if ((st = check_tensors(q, k, v, out, seq_info, inl ? 0 : S, q_rs, q_hs, o_rs, o_hs))) return st;
   if (!ws) return fail(SDPA_ERR_WORKSPACE, "workspace is NULL");
@@ -460,21 +498,22 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
   Grids g = grids_for(di, D);
   Q4Split sp = Q4Split::kFew;
   SkShape few{kSplitkRows, kSplitkTile, kSkBf16, g.splitk}, tile = q4_tile_shape(di);
-  if (q4) {
-    sp = q4_split(T, Hq, Hkv, D, S);
-    few = q4_few_shape(di, D);
+  if (packed) {
+    sp = q4_split(bits, T, Hq, Hkv, D, S);
+    few = packed_few_shape(di, bits, D);
     g.splitk = few.grid;
   }
   Workspace W;
   size_t need = layout_workspace((char*)ws, T, Hq, Hkv, D, S, g.splitk, g.prefill, &W, true,
-                                 q4 && D <= 128 ? &tile : nullptr);
+                                 bits == 4 && D <= 128 ? &tile : nullptr);
   if (ws_bytes < need)
     return fail(SDPA_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need);
-  const int parts = q4 ? q4_direct(di, T, Hq, Hkv, D, S, rows, causal, window, S > 0 ? seg_mode : nullptr) : 0;
-  Q4StageArgs sg{};
-  if (q4 && parts == 0) {  // as many staged columns as the workspace holds
+  const int parts =
+      packed ? packed_direct_parts(di, bits, T, Hq, Hkv, D, S, rows, causal, window, S > 0 ? seg_mode : nullptr) : 0;
+  PackedStageArgs sg{};
+  if (packed && parts == 0) {  // as many staged columns as the workspace holds
     const int64_t col = q4_stage_bytes_per_column(rows, Hkv, D);  // (a multiple of 256)
-    sg.pf_cols = (int)std::min<int64_t>(q4_stage_cols(T, Hq, Hkv, D, S, rows), (int64_t)(ws_bytes - need) / (2 * col));
+    sg.pf_cols = (int)std::min<int64_t>(q4_stage_cols(bits, T, Hq, Hkv, D, S, rows), (int64_t)(ws_bytes - need) / (2 * col));
     sg.k = (__nv_bfloat16*)((char*)ws + need);
     sg.v = (__half*)((char*)ws + need + col * sg.pf_cols);
   }
@@ -499,21 +538,22 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
   const int group = Hq / Hkv;
   const bool group_fits = group <= kPrefillRows && (kPrefillRows % group) == 0;
   sa.tile_pf = prefill_tile_keys(D);
-  sa.pf_min_rows = q4 ? q4_prefill_min_rows(sp) : kPrefillRows;
+  sa.pf_min_rows = packed ? q4_prefill_min_rows(sp) : kPrefillRows;
   sa.pf_tile_rows = kQ4TilePrefillRows;
-  sa.pf_min_work = q4 ? q4_prefill_min_work(sp) : kPrefillMinWork;
-  sa.q4 = q4 != nullptr;
+  sa.pf_min_work = packed ? q4_prefill_min_work(sp) : kPrefillMinWork;
+  sa.packed = packed != nullptr;
+  sa.key_bytes = bits == 8 ? 2 * D : D + D / (kQ4Group / 2);
   sa.sk[0] = sp == Q4Split::kTile ? tile : few;
   sa.sk[1] = tile;
   sa.sk_choice = sp == Q4Split::kEither;
   sa.sk_ratio = q4_tile_ratio(D);
-  sa.lo_align = q4 ? kPackedRows : 1;
+  sa.lo_align = packed ? kPackedRows : 1;
   sa.pf_cols = sg.pf_cols;
   // (a call-wide window bounds the positions that a staged column has to hold)
-  sa.rows_pf = q4 && window > 0 && !sa.seg_mode ? std::min<int64_t>(rows, T + window - 1) : rows;
-  sa.prefill_ok = (!q4 || sg.pf_cols > 0) && di.prefill_ok[d_index(D)] && group_fits && prefill_launch(sa, T) &&
-                  make_tensor_maps(q, T, Hq, D, q_rs, q_hs, q4 ? sg.k : k, q4 ? sg.v : v, sa.rows_pf,
-                                   q4 ? sg.pf_cols : cols, Hkv, group, sa.tile_pf, q4 != nullptr, &tm.q, &tm.k, &tm.v);
+  sa.rows_pf = packed && window > 0 && !sa.seg_mode ? std::min<int64_t>(rows, T + window - 1) : rows;
+  sa.prefill_ok = (!packed || sg.pf_cols > 0) && di.prefill_ok[d_index(D)] && group_fits && prefill_launch(sa, T) &&
+                  make_tensor_maps(q, T, Hq, D, q_rs, q_hs, packed ? sg.k : k, packed ? sg.v : v, sa.rows_pf,
+                                   packed ? sg.pf_cols : cols, Hkv, group, sa.tile_pf, packed != nullptr, &tm.q, &tm.k, &tm.v);
   if (!sa.prefill_ok) sa.pf_cols = 0;
   sa.grid[0] = 0;
   sa.grid[2] = g.prefill;
@@ -535,8 +575,8 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
   aa.causal = sa.causal;
   aa.window = window;
   aa.scale_log2 = scale * 1.4426950408889634f;
-  // (the 4-bit kernels scale after they mask: a scale of 0 must leave -infinity what it is)
-  if (q4) aa.scale_log2 = std::max(aa.scale_log2, FLT_MIN);
+  // (the kernels over codes scale after they mask: a scale of 0 must leave -infinity what it is)
+  if (packed) aa.scale_log2 = std::max(aa.scale_log2, FLT_MIN);
   aa.out = (__nv_bfloat16*)out;
   aa.o_rs = o_rs;
   aa.o_hs = o_hs;
@@ -548,14 +588,24 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
     apw = *ap;
     apw.segs = W.segs;
   }
+  if (bits == 4) packed->q4 = {aa, packed->st, sa.sk_choice};
+  if (bits == 8) {
+    packed->q8.a = aa;
+    packed->q8.st = packed->st;
+    packed->q8.choice = sa.sk_choice;
+    if (!make_q8_maps(packed->st, rows, cols, Hkv, D, &packed->q8))
+      return fail(SDPA_ERR_CUDA, "the 8-bit store's tensor maps could not be made");
+  }
   if (parts > 0) {
-    Q4DirectArgs da{{aa, *q4, 0}, S > 0 ? seq_info : nullptr, sa.seg_mode, S};
-    void* args[] = {(void*)&da};
+    const int32_t* table = S > 0 ? seq_info : nullptr;
+    PackedDirectArgs<Q4AttnArgs> d4{packed->q4, table, sa.seg_mode, S};
+    PackedDirectArgs<Q8AttnArgs> d8{packed->q8, table, sa.seg_mode, S};
+    void* args[] = {bits == 8 ? (void*)&d8 : (void*)&d4};
     const cudaStream_t cs = (cudaStream_t)stream;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(T * Hkv * parts));
-    cfg.blockDim = dim3(kQ4Threads);
-    cfg.dynamicSmemBytes = q4_splitk_smem_bytes(D);
+    cfg.blockDim = dim3(kPackedThreads);
+    cfg.dynamicSmemBytes = packed_smem_bytes(bits, D);
     cfg.stream = cs;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -565,9 +615,9 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
     cfg.numAttrs = 1;
     cudaError_t e = cudaSuccess;
     for (int i = 0; i < 3 && e == cudaSuccess; ++i) e = mark(i, cs);
-    if (e == cudaSuccess) e = cudaLaunchKernelExC(&cfg, q4_direct_kernel_ptr(D), args);
+    if (e == cudaSuccess) e = cudaLaunchKernelExC(&cfg, packed_direct_ptr(bits, D), args);
     for (int i = 3; i < 5 && e == cudaSuccess; ++i) e = mark(i, cs);
-    if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "4-bit direct launch: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "%d-bit direct launch: %s", bits, cudaGetErrorString(e));
     return SDPA_OK;
   }
   if (sa.pf_cols > 0) {
@@ -577,9 +627,41 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
     sg.D = D;
     sg.rows = rows;
     sg.rows_pf = sa.rows_pf;
-    sg.st = *q4;
+    sg.st = packed->st;
   }
-  return launch_all(sa, aa, D, g, tm, ap ? &apw : nullptr, q4, sa.pf_cols > 0 ? &sg : nullptr, (cudaStream_t)stream);
+  return launch_all(sa, aa, D, g, tm, ap ? &apw : nullptr, packed, sa.pf_cols > 0 ? &sg : nullptr, (cudaStream_t)stream);
+}
+
+// Bytes of workspace of a call over a store of codes; 0 for sizes that it does not take.
+static size_t packed_workspace_bytes(int bits, int64_t T, int Hq, int Hkv, int D, int S, int64_t rows, int cols) {
+  if (T < 0 || S < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || rows <= 0 || rows > INT32_MAX || cols <= 0) return 0;
+  if (D != 64 && D != 128 && D != 256) return 0;
+  DevInfo di;
+  Grids g{4096, 1024};  // without a device: bounds above any real grid
+  SkShape tile{kQ4TileRows, kQ4TileKeys, kSkQ4Tile, 1024};
+  if (device_info(&di) == SDPA_OK) {
+    g = {packed_resident(di, bits, D), grids_for(di, D).prefill};
+    tile = q4_tile_shape(di);
+  } else {
+    g_err[0] = 0;
+  }
+  return layout_workspace(nullptr, T, Hq, Hkv, D, S, g.splitk, g.prefill, nullptr, true,
+                          bits == 4 && D <= 128 ? &tile : nullptr) +
+         2 * q4_stage_bytes_per_column(rows, Hkv, D) * q4_stage_cols(bits, T, Hq, Hkv, D, S, rows);
+}
+
+static sdpa_status run_packed(int bits, const PackedStore& store, const void* q, int64_t T, int Hq, int D, int64_t q_rs,
+                              int64_t q_hs, int64_t rows, int cols, int Hkv, const int32_t* seq_info,
+                              const int32_t* seg_mode, int S, int causal, int window, float scale, void* out,
+                              int64_t o_rs, int64_t o_hs, void* ws, size_t ws_bytes, int32_t* status_dev,
+                              void* stream) {
+  // the running maximum is taken over unscaled scores
+  if (scale < 0.f) return fail(SDPA_ERR_ARG, "scale %g < 0", (double)scale);
+  PackedCall call{};
+  call.bits = bits;
+  call.st = store;
+  return run(q, T, Hq, D, q_rs, q_hs, store.kc, store.vc, rows, cols, Hkv, seq_info, S, nullptr, causal, window, scale,
+             out, o_rs, o_hs, ws, ws_bytes, status_dev, stream, nullptr, seg_mode, &call);
 }
 
 }  // namespace sdpa
@@ -656,19 +738,7 @@ sdpa_status sdpa_varlen_modes(const void* q, int64_t T, int Hq, int D, int64_t q
 }
 
 size_t sdpa_varlen_fourbit_workspace_bytes(int64_t T, int Hq, int Hkv, int D, int S, int64_t rows, int cols) {
-  if (T < 0 || S < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || rows <= 0 || rows > INT32_MAX || cols <= 0) return 0;
-  if (D != 64 && D != 128 && D != 256) return 0;
-  DevInfo di;
-  Grids g{4096, 1024};  // without a device: bounds above any real grid
-  SkShape tile{kQ4TileRows, kQ4TileKeys, kSkQ4Tile, 1024};
-  if (device_info(&di) == SDPA_OK) {
-    g = {q4_few_shape(di, D).grid, grids_for(di, D).prefill};
-    tile = q4_tile_shape(di);
-  } else {
-    g_err[0] = 0;
-  }
-  return layout_workspace(nullptr, T, Hq, Hkv, D, S, g.splitk, g.prefill, nullptr, true, D <= 128 ? &tile : nullptr) +
-         2 * q4_stage_bytes_per_column(rows, Hkv, D) * q4_stage_cols(T, Hq, Hkv, D, S, rows);
+  return packed_workspace_bytes(4, T, Hq, Hkv, D, S, rows, cols);
 }
 
 sdpa_status sdpa_varlen_fourbit(const void* q, int64_t T, int Hq, int D, int64_t q_row_stride, int64_t q_head_stride,
@@ -678,12 +748,25 @@ sdpa_status sdpa_varlen_fourbit(const void* q, int64_t T, int Hq, int D, int64_t
                            int32_t* status_dev, void* stream) {
   g_err[0] = 0;
   if (!store) return fail(SDPA_ERR_NULL, "store is NULL");
-  // the running maximum is taken over unscaled scores
-  if (scale < 0.f) return fail(SDPA_ERR_ARG, "scale %g < 0", (double)scale);
-  const PackedStore q4{store->k_codes, store->k_scales, store->v_codes, store->v_scales};
-  return run(q, T, Hq, D, q_row_stride, q_head_stride, q4.kc, q4.vc, rows, cols, Hkv, seq_info, S, nullptr, causal,
-             window, scale, out, o_row_stride, o_head_stride, workspace, ws_bytes, status_dev, stream, nullptr,
-             seg_mode, &q4);
+  return run_packed(4, {store->k_codes, store->k_scales, store->v_codes, store->v_scales}, q, T, Hq, D, q_row_stride,
+                    q_head_stride, rows, cols, Hkv, seq_info, seg_mode, S, causal, window, scale, out, o_row_stride,
+                    o_head_stride, workspace, ws_bytes, status_dev, stream);
+}
+
+size_t sdpa_varlen_eightbit_workspace_bytes(int64_t T, int Hq, int Hkv, int D, int S, int64_t rows, int cols) {
+  return packed_workspace_bytes(8, T, Hq, Hkv, D, S, rows, cols);
+}
+
+sdpa_status sdpa_varlen_eightbit(const void* q, int64_t T, int Hq, int D, int64_t q_row_stride, int64_t q_head_stride,
+                            const sdpa_q8_store* store, int64_t rows, int cols, int Hkv, const int32_t* seq_info,
+                            const int32_t* seg_mode, int S, int causal, int window, float scale, void* out,
+                            int64_t o_row_stride, int64_t o_head_stride, void* workspace, size_t ws_bytes,
+                            int32_t* status_dev, void* stream) {
+  g_err[0] = 0;
+  if (!store) return fail(SDPA_ERR_NULL, "store is NULL");
+  return run_packed(8, {store->k_codes, store->k_scales, store->v_codes, store->v_scales}, q, T, Hq, D, q_row_stride,
+                    q_head_stride, rows, cols, Hkv, seq_info, seg_mode, S, causal, window, scale, out, o_row_stride,
+                    o_head_stride, workspace, ws_bytes, status_dev, stream);
 }
 
 sdpa_status sdpa_seq_clone(void* k_store, void* v_store, int64_t rows, int cols, int Hkv, int D,

@@ -135,14 +135,14 @@ __device__ __forceinline__ void combine_row(const AttnArgs& A, int64_t gw, int l
 // A grid of at most 8 CTAs per SM (a full SM's worth of warps) walks the (row, head) pairs,
 // so that a call with many rows and nothing to merge does not pay for launching a CTA per 8
 // pairs.
-// Q4: the schedule's own units, of a 4-bit call.
-template <int D, bool Q4>
+// PACKED: the schedule's own units, of a call over a store of codes.
+template <int D, bool PACKED>
 __global__ void __launch_bounds__(kCombineThreads) sdpa_combine_kernel(AttnArgs A) {
   const Workspace& W = A.ws;
   // independent loads, issued together: whether there is work and the routes' unit counts
   const int64_t work = W.hdr->combine_work;
   const int64_t U1 = W.hdr->units[kRouteSplitk], U2 = W.hdr->units[kRoutePrefill];
-  const int sk_rows = Q4 ? (int)W.hdr->sk_rows : kSplitkRows;
+  const int sk_rows = PACKED ? (int)W.hdr->sk_rows : kSplitkRows;
   if (!work) return;
   const int lane = threadIdx.x & 31;
   const int64_t n = A.T * A.Hq, stride = (int64_t)gridDim.x * (kCombineThreads / 32);
@@ -262,14 +262,14 @@ const void* combine_pair_kernel_ptr(int D) {
   }
 }
 
-template <bool Q4>
+template <bool PACKED>
 static const void* combine_ptr(int D) {
   switch (D) {
-    case 64: return (const void*)sdpa_combine_kernel<64, Q4>;
-    case 128: return (const void*)sdpa_combine_kernel<128, Q4>;
-    default: return (const void*)sdpa_combine_kernel<256, Q4>;
+    case 64: return (const void*)sdpa_combine_kernel<64, PACKED>;
+    case 128: return (const void*)sdpa_combine_kernel<128, PACKED>;
+    default: return (const void*)sdpa_combine_kernel<256, PACKED>;
   }
 }
-const void* combine_kernel_ptr(int D, bool q4) { return q4 ? combine_ptr<true>(D) : combine_ptr<false>(D); }
+const void* combine_kernel_ptr(int D, bool packed) { return packed ? combine_ptr<true>(D) : combine_ptr<false>(D); }
 
 }  // namespace sdpa

@@ -41,7 +41,7 @@ struct SegRec {
   int32_t route;     // kRoute*: none for invalid, overlapping or empty segments
   int32_t nrb;       // row blocks per KV head (units per KV head)
   int32_t bits;      // SDPA_SEG_* bits of this segment
-  int32_t pf_col;    // 4-bit store: the staged column of a prefill-route segment
+  int32_t pf_col;    // store of codes: the staged column of a prefill-route segment
   int32_t ubase[4];  // per route: units of all earlier segments on that route (monotone in
                      // the segment index, so a binary search maps a unit to its segment)
   int32_t causal, window;  // the segment's mask mode (the call's, or its row of seg_mode)
@@ -231,8 +231,9 @@ struct SchedArgs {
   int tile_pf;     // keys per prefill tile
   // the split-K route's shapes: the first, and the one that the schedule may take instead (sk_choice)
   SkShape sk[2];
-  int q4;             // a call over a 4-bit store: the fields below are read for those only
+  int packed;         // a call over a store of codes: the fields below are read for those only
   int sk_choice;
+  int64_t key_bytes;  // of a key and its value in the store
   float sk_ratio;     // cost of a key for a unit of the second shape against that for 8 rows in the first
   int pf_min_rows;    // least packed rows of a segment of the prefill route (otherwise kPrefillRows)
   int pf_tile_rows;   // those when the schedule has taken the second shape
@@ -259,8 +260,8 @@ __host__ __device__ inline bool sched_small_ok(int64_t T, int Hq, int Hkv, int S
 }
 
 // Kernel entry points (defined in their own translation units).
-const void* sched_kernel_ptr(bool q4);
-const void* sched_small_kernel_ptr(bool q4);  // calls with sched_small_ok
+const void* sched_kernel_ptr(bool packed);
+const void* sched_small_kernel_ptr(bool packed);  // calls with sched_small_ok
 // Launches the scheduler kernel that suits the call (one CTA of kSchedThreads threads).
 cudaError_t launch_sched(const SchedArgs& sa, cudaStream_t st);
 size_t sched_smem_bytes();  // dynamic shared memory of the scheduler kernel
@@ -268,7 +269,7 @@ const void* append_kernel_ptr();
 const void* clone_kernel_ptr();
 const void* splitk_kernel_ptr(int D);
 int splitk_smem_bytes(int D);
-const void* combine_kernel_ptr(int D, bool q4);
+const void* combine_kernel_ptr(int D, bool packed);
 const void* combine_pair_kernel_ptr(int D);  // a CTA per (row, head) pair
 const void* prefill_kernel_ptr(int D, bool f16);  // f16: V is fp16
 const void* prefill_pair_kernel_ptr(int D, bool f16);  // D = 64, 128

@@ -22,6 +22,31 @@ struct PackedStore {
 // Pointers present and aligned, rows a multiple of kPackedRows; `bits` 4 or 8 (api.cu).
 sdpa_status check_packed_store(const PackedStore& st, int bits, int64_t rows);
 
+constexpr int kPackedThreads = 160;  // of the kernels for few rows: four warps of attention, one that loads
+// A call without a schedule (packed_attn.cuh): at most kPackedDirectSegs segments, at most kSplitkRows heads a KV
+// head.
+constexpr int kPackedDirectSegs = 512;
+template <class Args>
+struct PackedDirectArgs {
+  Args packed;
+  const int32_t* seq_info;
+  const int32_t* seg_mode;  // NULL, or [S, 2] (causal, window)
+  int S;
+};
+
+// The keys and values of the prefill route's segments, brought to bf16 and fp16 for the tensor-memory kernel:
+// position p of the segment with staged column c goes to row p % rows_pf of column c of a 16-bit
+// column store [rows_pf, pf_cols, Hkv, D] (q4_stage.cu, q8_stage.cu).
+struct PackedStageArgs {
+  const SegRec* segs;  // the scheduler's records
+  int S, Hkv, D, pf_cols;
+  int64_t rows, rows_pf;
+  PackedStore st;
+  __nv_bfloat16* k;
+  __half* v;
+};
+constexpr int kPackedStageThreads = 256;
+
 // A constant that the compiler keeps in a register.
 __device__ __forceinline__ uint32_t in_register(uint32_t v) {
   asm volatile("" : "+r"(v));

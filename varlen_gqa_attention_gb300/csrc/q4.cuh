@@ -105,31 +105,9 @@ struct Q4AttnArgs {
   int choice;  // both split-K kernels are launched, and the schedule is one's (hdr->sk_rows)
 };
 
-// A call without a schedule (q4_attn.cu): at most kQ4DirectSegs segments, at most kSplitkRows heads a KV head.
-constexpr int kQ4DirectSegs = 512;
-struct Q4DirectArgs {
-  Q4AttnArgs q4;
-  const int32_t* seq_info;
-  const int32_t* seg_mode;  // NULL, or [S, 2] (causal, window)
-  int S;
-};
-
-// The keys and values of the prefill route's segments, brought to bf16 and fp16 for the tensor-memory kernel:
-// position p of the segment with staged column c goes to row p % rows_pf of column c of a 16-bit
-// column store [rows_pf, pf_cols, Hkv, D] (q4_stage.cu).
-struct Q4StageArgs {
-  const SegRec* segs;  // the scheduler's records
-  int S, Hkv, D, pf_cols;
-  int64_t rows, rows_pf;
-  PackedStore st;
-  __nv_bfloat16* k;
-  __half* v;
-};
-constexpr int kQ4StageThreads = 256;
 const void* q4_stage_kernel_ptr(int D);
 
 // Entry points (q4_attn.cu).
-constexpr int kQ4Threads = 160;  // four warps of attention, one that loads
 // The tensor-memory kernel for segments of several rows (q4_tile.cu; D = 64, 128): one CTA per SM, units of
 // kQ4TileRows packed rows, tiles of kQ4TileKeys keys.
 constexpr int kQ4TileRows = 128;

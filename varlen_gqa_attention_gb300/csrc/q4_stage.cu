@@ -10,58 +10,27 @@
 //
 // Bound by memory: D / 2 + D / 32 bytes read and 2 D written per key and KV head, twice.  A thread
 // takes 8 dims (a word of codes, 16 bytes out) of a key and of its value.
+#include "packed_stage.cuh"
 #include "q4.cuh"
 
 namespace sdpa {
 
-// CTA b works on staged column b % pf_cols; its segment is the prefill-route one of that number.
 template <int D>
-__global__ void __launch_bounds__(kQ4StageThreads) sdpa_q4_stage_kernel(Q4StageArgs A) {
-  __shared__ int s_seg;
-  const int64_t column = blockIdx.x % A.pf_cols, part = blockIdx.x / A.pf_cols;
-  const int64_t parts = gridDim.x / A.pf_cols;
-  if (threadIdx.x == 0) s_seg = -1;
-  __syncthreads();
-  griddep_wait();  // the scheduler's records, and the calls before that used the columns
-  griddep_launch();
-  for (int s = threadIdx.x; s < A.S; s += blockDim.x)
-    if (A.segs[s].route == kRoutePrefill && A.segs[s].pf_col == (int)column) s_seg = s;
-  __syncthreads();
-  if (s_seg < 0) return;
-  const SegRec sg = A.segs[s_seg];
-  // the positions the segment's rows see together
-  const RowWin w0 = row_window(0, sg.q_len, sg.kv_end, sg.causal, sg.window);
-  const int64_t lo = w0.lo, n = (int64_t)sg.kv_end - lo;
-  if (n <= 0) return;
-  constexpr int W = D / 8;  // words of a row
-  const int64_t per_head = n * W, total = per_head * A.Hkv, stride = parts * blockDim.x;
-  constexpr int U = 4;
-  for (int64_t i0 = part * blockDim.x + threadIdx.x; i0 < total; i0 += U * stride) {
-    uint32_t kw[U], vw[U], kb[U], vb[U];
-    int64_t dst[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t i = i0 + u * stride;
-      dst[u] = -1;
-      if (i < total) {
-        const int64_t h = udiv(i, per_head), x = i - h * per_head;
-        const int64_t p = lo + x / W;
-        const int c = (int)(x % W);
-        const int64_t cell = ((int64_t)sg.col * A.Hkv + h) * A.rows + (uint32_t)p % (uint32_t)A.rows;
-        kw[u] = *reinterpret_cast<const uint32_t*>(A.st.kc + cell * (D / 2) + 4 * c);
-        vw[u] = *reinterpret_cast<const uint32_t*>(A.st.vc + cell * (D / 2) + 4 * c);
-        kb[u] = A.st.ks[cell * (D / kQ4Group) + c / 4];
-        vb[u] = A.st.vs[cell * (D / kQ4Group) + c / 4];
-        dst[u] = (((int64_t)((uint32_t)p % (uint32_t)A.rows_pf) * A.pf_cols + column) * A.Hkv + h) * D + 8 * c;
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (dst[u] < 0) continue;
-      *reinterpret_cast<uint4*>(A.k + dst[u]) = q4_words8(kw[u], kb[u]);
-      *reinterpret_cast<uint4*>(A.v + dst[u]) = q4_words8_f16(vw[u], vb[u]);
-    }
+struct Q4Chunk {
+  uint32_t kw, vw, kb, vb;
+  __device__ __forceinline__ void load(const PackedStore& st, int64_t cell, int c) {
+    kw = *reinterpret_cast<const uint32_t*>(st.kc + cell * (D / 2) + 4 * c);
+    vw = *reinterpret_cast<const uint32_t*>(st.vc + cell * (D / 2) + 4 * c);
+    kb = st.ks[cell * (D / kQ4Group) + c / 4];
+    vb = st.vs[cell * (D / kQ4Group) + c / 4];
   }
+  __device__ __forceinline__ uint4 keys() const { return q4_words8(kw, kb); }
+  __device__ __forceinline__ uint4 values() const { return q4_words8_f16(vw, vb); }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kPackedStageThreads) sdpa_q4_stage_kernel(PackedStageArgs A) {
+  packed_stage<D, Q4Chunk<D>>(A);
 }
 
 const void* q4_stage_kernel_ptr(int D) {

@@ -12,6 +12,10 @@
 // (Codes and not 8-bit floating-point numbers: normal values are off by a third as much, and no code is a NaN.)
 #pragma once
 
+#include <cfloat>
+
+#include <cuda.h>
+
 #include "packed.cuh"
 
 namespace sdpa {
@@ -42,5 +46,17 @@ __device__ __forceinline__ uint2 q8_words4(uint32_t w, __nv_bfloat162 s2) {
   return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 __device__ __forceinline__ __nv_bfloat162 q8_scale_bf16(uint32_t b) { return __float2bfloat162_rn(q8_scale(b)); }
+
+struct Q8AttnArgs {
+  CUtensorMap k, v;  // the store's codes as [cols * Hkv, rows, D] bytes, in boxes of 16 rows (api.cu)
+  AttnArgs a;        // k, v unused
+  PackedStore st;
+  int choice;  // both split-K kernels are launched, and the schedule is one's (hdr->sk_rows)
+};
+
+const void* q8_splitk_kernel_ptr(int D);
+const void* q8_direct_kernel_ptr(int D);
+int q8_splitk_smem_bytes(int D);
+const void* q8_stage_kernel_ptr(int D);
 
 }  // namespace sdpa

@@ -1,0 +1,51 @@
+// q8_stage.cu - keys and values of the prefill route's segments brought from 8 bits to 16, as q4_stage.cu does from 4:
+// exactly, K to bf16 and V to fp16 (but for -65536, which no append writes: -65504).
+//
+// Bound by memory: D and an eighth of a byte read and 2 D written per key and KV head, twice.
+#include "packed_stage.cuh"
+#include "q8.cuh"
+
+namespace sdpa {
+
+template <int D>
+struct Q8Chunk {
+  uint2 kw, vw;
+  uint32_t kb, vb;
+  __device__ __forceinline__ void load(const PackedStore& st, int64_t cell, int c) {
+    kw = *reinterpret_cast<const uint2*>(st.kc + cell * D + 8 * c);
+    vw = *reinterpret_cast<const uint2*>(st.vc + cell * D + 8 * c);
+    kb = st.ks[cell / kPackedRows];
+    vb = st.vs[cell / kPackedRows];
+  }
+  __device__ __forceinline__ uint4 keys() const {
+    const __nv_bfloat162 s = q8_scale_bf16(kb);
+    const uint2 a = q8_words4(kw.x, s), b = q8_words4(kw.y, s);
+    return make_uint4(a.x, a.y, b.x, b.y);
+  }
+  __device__ __forceinline__ uint4 values() const {
+    const __half2 s = __float2half2_rn(q8_scale(vb));
+    return make_uint4(pair(vw.x, 0x4140, s), pair(vw.x, 0x4342, s), pair(vw.y, 0x4140, s), pair(vw.y, 0x4342, s));
+  }
+  // 0x6400 | c is 1024 + c
+  __device__ __forceinline__ static uint32_t pair(uint32_t w, uint32_t which, __half2 s) {
+    const uint32_t u = __byte_perm(w, 0x64u, which);
+    const __half2 c = __hsub2(*reinterpret_cast<const __half2*>(&u), __float2half2_rn(1152.f));
+    const __half2 v = __hmax2(__hmul2(c, s), __float2half2_rn(-65504.f));
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kPackedStageThreads) sdpa_q8_stage_kernel(PackedStageArgs A) {
+  packed_stage<D, Q8Chunk<D>>(A);
+}
+
+const void* q8_stage_kernel_ptr(int D) {
+  switch (D) {
+    case 64: return (const void*)sdpa_q8_stage_kernel<64>;
+    case 128: return (const void*)sdpa_q8_stage_kernel<128>;
+    default: return (const void*)sdpa_q8_stage_kernel<256>;
+  }
+}
+
+}  // namespace sdpa

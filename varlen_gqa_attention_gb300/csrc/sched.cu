@@ -147,22 +147,22 @@ __device__ __forceinline__ void load_seg(const SchedArgs& A, int s, int32_t* seg
   }
 }
 
-// What only the 4-bit store's calls set; the others' kernels have it as constants.
-template <bool Q4>
-__device__ __forceinline__ int pf_cols(const SchedArgs& A) { return Q4 ? A.pf_cols : 0; }
-template <bool Q4>
-__device__ __forceinline__ int lo_align(const SchedArgs& A) { return Q4 ? A.lo_align : 1; }
-template <bool Q4>
-__device__ __forceinline__ int64_t rows_pf(const SchedArgs& A) { return Q4 ? A.rows_pf : A.rows; }
-template <bool Q4>
-__device__ __forceinline__ int pf_min_rows(const SchedArgs& A) { return Q4 ? A.pf_min_rows : kPrefillRows; }
-template <bool Q4>
-__device__ __forceinline__ float pf_min_work(const SchedArgs& A) { return Q4 ? A.pf_min_work : kPrefillMinWork; }
-template <bool Q4>
-__device__ __forceinline__ bool sk_choice(const SchedArgs& A) { return Q4 && A.sk_choice; }
-template <bool Q4>
+// What only the calls over a store of codes set; the others' kernels have it as constants.
+template <bool PACKED>
+__device__ __forceinline__ int pf_cols(const SchedArgs& A) { return PACKED ? A.pf_cols : 0; }
+template <bool PACKED>
+__device__ __forceinline__ int lo_align(const SchedArgs& A) { return PACKED ? A.lo_align : 1; }
+template <bool PACKED>
+__device__ __forceinline__ int64_t rows_pf(const SchedArgs& A) { return PACKED ? A.rows_pf : A.rows; }
+template <bool PACKED>
+__device__ __forceinline__ int pf_min_rows(const SchedArgs& A) { return PACKED ? A.pf_min_rows : kPrefillRows; }
+template <bool PACKED>
+__device__ __forceinline__ float pf_min_work(const SchedArgs& A) { return PACKED ? A.pf_min_work : kPrefillMinWork; }
+template <bool PACKED>
+__device__ __forceinline__ bool sk_choice(const SchedArgs& A) { return PACKED && A.sk_choice; }
+template <bool PACKED>
 __device__ __forceinline__ SkShape first_shape(const SchedArgs& A) {
-  if constexpr (Q4) return A.sk[0];
+  if constexpr (PACKED) return A.sk[0];
   return {kSplitkRows, kSplitkTile, kSkBf16, A.sk[0].grid};
 }
 
@@ -224,7 +224,7 @@ struct SegView {
 // placeholders and its key tiles; 0 when no key is visible); *reuse: the K/V bytes its
 // (segment, KV head) group reads again, counted once, on the group's last unit, and only for
 // groups of several units (phases are cut on these).
-template <bool Q4>
+template <bool PACKED>
 __device__ __forceinline__ UnitRec make_unit(const SchedArgs& A, const SkShape& k, int s, const SegView& g, int q,
                                              int64_t uq, int64_t* span, int64_t* reuse) {
   const int rpu = rows_per_unit(A, k, q), tl = tile_len(A, k, q);
@@ -234,7 +234,7 @@ __device__ __forceinline__ UnitRec make_unit(const SchedArgs& A, const SkShape& 
   ur.seg = s;
   ur.q_start = g.q_start;
   ur.q_len = g.q_len;
-  ur.col = q == kRoutePrefill && pf_cols<Q4>(A) > 0 ? g.pf_col : g.col;
+  ur.col = q == kRoutePrefill && pf_cols<PACKED>(A) > 0 ? g.pf_col : g.col;
   ur.kv_end = g.kv_end;
   ur.causal = g.causal;
   ur.window = g.window;
@@ -249,10 +249,10 @@ __device__ __forceinline__ UnitRec make_unit(const SchedArgs& A, const SkShape& 
   ur.lo = w0.lo;  // lo and hi grow with the query row
   ur.hi = max(w1.hi, w0.lo);
   // (keys added below a unit's first are masked like any other that a row does not see)
-  if (q == kRouteSplitk && ur.hi > ur.lo) ur.lo &= -lo_align<Q4>(A);
+  if (q == kRouteSplitk && ur.hi > ur.lo) ur.lo &= -lo_align<PACKED>(A);
   // key tiles: the prefill kernel's stop at a ring wrap (two TMA ranges), the split-K
   // kernel's wrap per row
-  const int64_t nt = q == kRoutePrefill ? key_tiles(ur.lo, ur.hi, rows_pf<Q4>(A), tl).n
+  const int64_t nt = q == kRoutePrefill ? key_tiles(ur.lo, ur.hi, rows_pf<PACKED>(A), tl).n
                                         : (ur.hi > ur.lo ? udiv((int64_t)(ur.hi - ur.lo) + tl - 1, tl) : 0);
   ur.nslots = 0;
   ur.g_first = 0;
@@ -267,7 +267,7 @@ __device__ __forceinline__ UnitRec make_unit(const SchedArgs& A, const SkShape& 
     if (g.window > 0) sp = min(sp, (int64_t)g.q_len + g.window - 1);
     // bytes of K and V per key (staged columns hold bf16; phases cut as if all did made 16 4-bit segments of 512
     // packed rows over 4096 keys 253 us, not 206)
-    *reuse = sp * (Q4 && q == kRouteSplitk ? A.D + A.D / (kQ4Group / 2) : (int64_t)A.D * 4);
+    *reuse = sp * (PACKED && q == kRouteSplitk ? A.key_bytes : (int64_t)A.D * 4);
   }
   return ur;
 }
@@ -333,7 +333,7 @@ constexpr int kUnitCache = 1024;
 constexpr size_t kSchedSmem = (size_t)kSegCache * (16 + 8 + 8 + 8 + 4 + 4 + 4) + (size_t)kRowCache * 4 +
                               (size_t)kUnitCache * sizeof(UnitRec);
 
-template <bool Q4>
+template <bool PACKED>
 __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_kernel(SchedArgs A) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ int64_t sh[4 * 32];
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_kernel(SchedArgs A) 
   };
   auto bits_of = [&](int s) -> int32_t { return cached ? c_bits[s] : W.segs[s].bits; };
 
-  SkShape sk = first_shape<Q4>(A);
+  SkShape sk = first_shape<PACKED>(A);
   {
     griddep_launch();  // the attention kernels may start launching; they wait for this grid
     if (threadIdx.x == 0) {
@@ -432,8 +432,8 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_kernel(SchedArgs A) 
     // prefill route is taken
     int64_t sa, sb;
     my_range(S, &sa, &sb);
-    int pf_rows = pf_min_rows<Q4>(A);
-    if (sk_choice<Q4>(A)) {
+    int pf_rows = pf_min_rows<PACKED>(A);
+    if (sk_choice<PACKED>(A)) {
       float more = 0.f;
       for (int64_t s = sa; s < sb; ++s) {
         const int4 g = seg_of((int)s);
@@ -452,10 +452,10 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_kernel(SchedArgs A) 
       if (bits_of((int)s) == 0 && !flag[s] && g.y > 0)
         pw += prefill_work(A, g.y, g.w, cached ? c_mode[s].y : W.segs[s].window, pf_rows);
     }
-    const bool big = block_sum(pw, s_fsum) >= pf_min_work<Q4>(A);
+    const bool big = block_sum(pw, s_fsum) >= pf_min_work<PACKED>(A);
     // staged columns go to the first segments of the prefill route, in segment order
     int64_t pf[1] = {0};
-    if (pf_cols<Q4>(A) > 0) {
+    if (pf_cols<PACKED>(A) > 0) {
       int64_t pf_all[1];
       for (int64_t s = sa; s < sb; ++s) {
         const int4 g = seg_of((int)s);
@@ -473,8 +473,8 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_kernel(SchedArgs A) 
       if (bits == 0 && !fl && g.y > 0) {
         const int64_t R = (int64_t)g.y * A.group;
         route = route_of(A, g.y, big, pf_rows);
-        if (pf_cols<Q4>(A) > 0 && route == kRoutePrefill) {
-          if (pf[0] >= pf_cols<Q4>(A)) route = kRouteSplitk;
+        if (pf_cols<PACKED>(A) > 0 && route == kRoutePrefill) {
+          if (pf[0] >= pf_cols<PACKED>(A)) route = kRouteSplitk;
           (cached ? c_pf[s] : W.segs[s].pf_col) = (int32_t)pf[0]++;
         }
         const int rpu = rows_per_unit(A, sk, route);
@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_kernel(SchedArgs A) 
       const int64_t uq = q == 1 ? u : u - U1;
       const int s = owner(q, uq);
       int64_t span, reuse;
-      UnitRec ur = make_unit<Q4>(A, sk, s, view_of(s, q), q, uq, &span, &reuse);
+      UnitRec ur = make_unit<PACKED>(A, sk, s, view_of(s, q), q, uq, &span, &reuse);
       if (ur.ntiles == 0) s_work = 1;  // rows of a unit with no keys: zeroed by the combine pass
       if (q == kRouteSplitk) W.unit_done[uq] = 0;
       ur.tile_base = span;
@@ -671,7 +671,7 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_kernel(SchedArgs A) 
       const int4 c = c_seg[s];
       SegRec r;
       r.q_start = c.x; r.q_len = c.y; r.col = c.z; r.kv_end = c.w;
-      r.route = c_rn[s].x; r.nrb = c_rn[s].y; r.bits = c_bits[s]; r.pf_col = Q4 ? c_pf[s] : 0;
+      r.route = c_rn[s].x; r.nrb = c_rn[s].y; r.bits = c_bits[s]; r.pf_col = PACKED ? c_pf[s] : 0;
       r.ubase[0] = 0; r.ubase[1] = c_ub[s].x; r.ubase[2] = c_ub[s].y; r.ubase[3] = 0;
       r.causal = c_mode[s].x; r.window = c_mode[s].y;
       r.pad2[0] = r.pad2[1] = 0;
@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_kernel(SchedArgs A) 
 //     at a warp boundary, so a warp holds one route) with one barrier each, and one barrier
 //     for the phase bases, which each thread writes for the next unit of its route from its
 //     own prefix and span.
-template <bool Q4>
+template <bool PACKED>
 __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_small_kernel(SchedArgs A) {
   __shared__ int4 c_seg[kSmallSegs];   // (q_start, q_len, col, kv_end)
   __shared__ int2 c_mode[kSmallSegs];  // (causal, window)
@@ -788,9 +788,9 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_small_kernel(SchedAr
       ov = ov && ok;
     }
     const bool live = ok && !ov;
-    SkShape sk = first_shape<Q4>(A);
-    int pf_rows = pf_min_rows<Q4>(A);
-    if (sk_choice<Q4>(A)) {
+    SkShape sk = first_shape<PACKED>(A);
+    int pf_rows = pf_min_rows<PACKED>(A);
+    if (sk_choice<PACKED>(A)) {
       float more = live ? sk_cost(A, g[1], g[3], md.y) : 0.f;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) more += __shfl_xor_sync(kAll, more, o);
@@ -803,11 +803,11 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_small_kernel(SchedAr
     float pw = live ? prefill_work(A, g[1], g[3], md.y, pf_rows) : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) pw += __shfl_xor_sync(kAll, pw, o);
-    int route = live ? route_of(A, g[1], pw >= pf_min_work<Q4>(A), pf_rows) : kRouteNone, nrb = 0;
+    int route = live ? route_of(A, g[1], pw >= pf_min_work<PACKED>(A), pf_rows) : kRouteNone, nrb = 0;
     int pf_col = 0;
-    if (pf_cols<Q4>(A) > 0) {  // staged columns go to the first segments of the prefill route
+    if (pf_cols<PACKED>(A) > 0) {  // staged columns go to the first segments of the prefill route
       pf_col = __popc(__ballot_sync(kAll, route == kRoutePrefill) & ((1u << lane) - 1u));
-      if (route == kRoutePrefill && pf_col >= pf_cols<Q4>(A)) route = kRouteSplitk;
+      if (route == kRoutePrefill && pf_col >= pf_cols<PACKED>(A)) route = kRouteSplitk;
     }
     if (live) {
       const int rpu = rows_per_unit(A, sk, route);
@@ -851,8 +851,8 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_small_kernel(SchedAr
     for (int t = threadIdx.x - 32; t < T; t += blockDim.x - 32) W.row_info[t] = make_int4(kRouteNone, 0, 0, 0);
   }
   __syncthreads();  // (also orders the row records above before the ones below)
-  SkShape sk = first_shape<Q4>(A);
-  if (sk_choice<Q4>(A) && s_sk) sk = A.sk[1];
+  SkShape sk = first_shape<PACKED>(A);
+  if (sk_choice<PACKED>(A) && s_sk) sk = A.sk[1];
 
   // each live segment's row records
   for (int s = warp; s < S; s += nw) {
@@ -891,7 +891,7 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_small_kernel(SchedAr
     gv.causal = c_mode[s].x;
     gv.window = c_mode[s].y;
     gv.pf_col = c_pf[s];
-    ur = make_unit<Q4>(A, sk, s, gv, q, uq, &span, &reuse);
+    ur = make_unit<PACKED>(A, sk, s, gv, q, uq, &span, &reuse);
     if (ur.ntiles == 0) s_work = 1;  // rows of a unit with no keys: zeroed by the combine pass
     if (q == kRouteSplitk) W.unit_done[uq] = 0;
   }
@@ -963,18 +963,18 @@ __global__ void __launch_bounds__(kSchedThreads) sdpa_sched_small_kernel(SchedAr
   }
 }
 
-const void* sched_kernel_ptr(bool q4) {
-  return q4 ? (const void*)sdpa_sched_kernel<true> : (const void*)sdpa_sched_kernel<false>;
+const void* sched_kernel_ptr(bool packed) {
+  return packed ? (const void*)sdpa_sched_kernel<true> : (const void*)sdpa_sched_kernel<false>;
 }
-const void* sched_small_kernel_ptr(bool q4) {
-  return q4 ? (const void*)sdpa_sched_small_kernel<true> : (const void*)sdpa_sched_small_kernel<false>;
+const void* sched_small_kernel_ptr(bool packed) {
+  return packed ? (const void*)sdpa_sched_small_kernel<true> : (const void*)sdpa_sched_small_kernel<false>;
 }
 
 cudaError_t launch_sched(const SchedArgs& sa, cudaStream_t st) {
   void* args[] = {(void*)&sa};
   if (sched_small_ok(sa.T, sa.group * sa.Hkv, sa.Hkv, sa.S))
-    return cudaLaunchKernel(sched_small_kernel_ptr(sa.q4), dim3(1), dim3(kSchedThreads), args, 0, st);
-  return cudaLaunchKernel(sched_kernel_ptr(sa.q4), dim3(1), dim3(kSchedThreads), args, sched_smem_bytes(), st);
+    return cudaLaunchKernel(sched_small_kernel_ptr(sa.packed), dim3(1), dim3(kSchedThreads), args, 0, st);
+  return cudaLaunchKernel(sched_kernel_ptr(sa.packed), dim3(1), dim3(kSchedThreads), args, sched_smem_bytes(), st);
 }
 size_t sched_smem_bytes() { return kSchedSmem; }
 
