@@ -62,6 +62,8 @@ static DevInfo g_dev[64];
 // The kernels of a store of codes.
 static const void* packed_splitk_ptr(int bits, int D) { return bits == 8 ? q8_splitk_kernel_ptr(D) : q4_splitk_kernel_ptr(D); }
 static const void* packed_direct_ptr(int bits, int D) { return bits == 8 ? q8_direct_kernel_ptr(D) : q4_direct_kernel_ptr(D); }
+static const void* packed_tile_ptr(int bits, int D) { return bits == 8 ? q8_tile_kernel_ptr(D) : q4_tile_kernel_ptr(D); }
+static int packed_tile_smem(int bits, int D) { return bits == 8 ? q8_tile_smem_bytes(D) : q4_tile_smem_bytes(D); }
 static int packed_smem_bytes(int bits, int D) { return bits == 8 ? q8_splitk_smem_bytes(D) : q4_splitk_smem_bytes(D); }
 
 static int d_index(int D) { return D == 64 ? 0 : D == 128 ? 1 : 2; }
@@ -103,14 +105,14 @@ static sdpa_status device_info(DevInfo* out) {
       e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, f, kSplitkThreads, smem);
       if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "occupancy: %s", cudaGetErrorString(e));
       di.splitk_per_sm[k] = nb > 0 ? nb : 1;
-      if (Ds[k] <= 128) {
-        e = cudaFuncSetAttribute(q4_tile_kernel_ptr(Ds[k]), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 q4_tile_smem_bytes(Ds[k]));
-        if (e == cudaSuccess)
-          e = cudaFuncSetAttribute(q4_tile_kernel_ptr(Ds[k]), cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-        if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "4-bit tile kernel attributes: %s", cudaGetErrorString(e));
-      }
       for (int bits = 4; bits <= 8; bits += 4) {
+        if (Ds[k] <= 128) {
+          const void* tile = packed_tile_ptr(bits, Ds[k]);
+          e = cudaFuncSetAttribute(tile, cudaFuncAttributeMaxDynamicSharedMemorySize, packed_tile_smem(bits, Ds[k]));
+          if (e == cudaSuccess) e = cudaFuncSetAttribute(tile, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+          if (e != cudaSuccess)
+            return fail(SDPA_ERR_CUDA, "%d-bit tile kernel attributes: %s", bits, cudaGetErrorString(e));
+        }
         const void* few = packed_splitk_ptr(bits, Ds[k]);
         const int few_smem = packed_smem_bytes(bits, Ds[k]);
         for (const void* f : {few, packed_direct_ptr(bits, Ds[k])}) {
@@ -221,21 +223,21 @@ static Grids grids_for(const DevInfo& di, int D) {
 // segment has (empty ones counted): with at most 16 it launches the other one, with more (of several segments, which may be one
 // chunk and many single tokens) both, and the schedule is the cheaper one's; the other leaves at once.  At
 // D = 256 the output of 128 rows leaves no room for the first.
-enum class Q4Split { kFew, kTile, kEither };
-static Q4Split q4_split(int bits, int64_t T, int Hq, int Hkv, int D, int S) {
-  if (bits == 8 || D > 128 || T * (Hq / Hkv) <= 16 * (int64_t)std::max(S, 1)) return Q4Split::kFew;
-  return S <= 1 ? Q4Split::kTile : Q4Split::kEither;
+enum class PackedSplit { kFew, kTile, kEither };
+static PackedSplit packed_split(int64_t T, int Hq, int Hkv, int D, int S) {
+  if (D > 128 || T * (Hq / Hkv) <= 16 * (int64_t)std::max(S, 1)) return PackedSplit::kFew;
+  return S <= 1 ? PackedSplit::kTile : PackedSplit::kEither;
 }
 // The tensor-memory kernel's cost of a key for a unit, in those of the other one for 8 rows (full loads: 0.066
 // and 0.027 ns at D = 128, 0.054 and 0.015 at D = 64).
-static float q4_tile_ratio(int D) { return D == 64 ? 3.5f : 2.5f; }
+static float packed_tile_ratio(int D) { return D == 64 ? 3.5f : 2.5f; }
 static int64_t packed_resident(const DevInfo& di, int bits, int D) {
   return (int64_t)di.sms * di.packed_per_sm[bits / 8][d_index(D)];
 }
 static SkShape packed_few_shape(const DevInfo& di, int bits, int D) {
   return {kSplitkRows, kSplitkTile, kSkQ4Few, packed_resident(di, bits, D)};
 }
-static SkShape q4_tile_shape(const DevInfo& di) { return {kQ4TileRows, kQ4TileKeys, kSkQ4Tile, di.sms}; }
+static SkShape packed_tile_shape(const DevInfo& di) { return {kPackedTileRows, kPackedTileKeys, kSkQ4Tile, di.sms}; }
 
 sdpa_status check_common(int64_t T, int Hq, int Hkv, int D, int S, int64_t rows, int cols, int window,
                          float scale) {
@@ -312,14 +314,14 @@ static cudaError_t launch_k(const void* f, unsigned grid, unsigned block, void**
 // rows, 8.3 in one of 32768, where a cluster of 8 is taken, 14.4 scheduled), and an empty entry counts as a token of its own.  256 entries, one of them 200 tokens
 // over 2048 keys, 20 single tokens and the others empty: 117 us, 66 without the empty ones (256 single tokens of 2048
 // keys 140 / 209, which is why the rule is so).  The shares are halved while there are SMs for them and more
-// than kQ4DirectPart keys in each.  In us, direct / scheduled, 32/8 heads, D = 128, all ranges full: 1 token 512 keys
+// than kDirectPart keys in each.  In us, direct / scheduled, 32/8 heads, D = 128, all ranges full: 1 token 512 keys
 // 7.0 / 14.4, 16384 keys 15.8 / 19.4; 8 tokens 64 keys 6.0 / 13.0, 2048 keys 10.3 / 18.8, 16384 keys 40 / 45; 32 tokens
 // 512 keys 8.9 / 22.6, 4096 keys 38 / 49; 64 tokens 2048 keys 41 / 62; two segments of 16 tokens 1024 keys 13 / 26, 4096 keys
 // 36 / 28.
 // Where lengths differ the call waits for its longest: lengths evenly spread up to the limit (32 tokens of 4096
 // keys, 34.5 / 33.6; with 16/2 heads of 8192, 21 / 24, of 16384 beyond it 36 / 30; 16 tokens at D = 256 of 4096 30 / 32, of
 // 8192 52 / 47).
-constexpr int64_t kQ4DirectPart = 128;
+constexpr int64_t kDirectPart = 128;
 static int packed_direct_parts(const DevInfo& di, int bits, int64_t T, int Hq, int Hkv, int D, int S, int64_t rows,
                                int causal, int window, const int32_t* seg_mode) {
   if (g_policy.load() != SDPA_ROUTE_AUTO || Hq / Hkv > kSplitkRows || S > kPackedDirectSegs) return 0;
@@ -328,7 +330,7 @@ static int packed_direct_parts(const DevInfo& di, int bits, int64_t T, int Hq, i
   int64_t keys = rows;  // that a row may see
   if (window > 0 && !seg_mode) keys = std::min<int64_t>(keys, causal ? window : T + window - 1);
   int parts = 1;
-  while (parts < 8 && 2 * parts * pairs <= resident && keys > kQ4DirectPart * parts) parts *= 2;
+  while (parts < 8 && 2 * parts * pairs <= resident && keys > kDirectPart * parts) parts *= 2;
   const int64_t share = T <= S && (D == 64 || (D == 128 && parts <= 2)) ? 4096 : 2048;
   return keys <= share * parts ? parts : 0;
 }
@@ -342,31 +344,31 @@ static int packed_direct_parts(const DevInfo& di, int bits, int64_t T, int Hq, i
 // So the bf16 entry's thresholds hold where the tensor-memory one is not launched, and 512 rows where the
 // schedule takes the other one: 64 tokens over 16384 to 32768 keys beside 250 over 32768 842 / 579 us (fewer
 // rows do not pay for the launches when there are none, 5 us).
-constexpr int kQ4TilePrefillRows = 1024;
-static int q4_prefill_min_rows(Q4Split sp) {
-  return sp == Q4Split::kFew ? kPrefillRows : sp == Q4Split::kEither ? 512 : kQ4TilePrefillRows;
+constexpr int kTilePrefillRows = 1024;
+static int packed_prefill_min_rows(PackedSplit sp) {
+  return sp == PackedSplit::kFew ? kPrefillRows : sp == PackedSplit::kEither ? 512 : kTilePrefillRows;
 }
-static float q4_prefill_min_work(Q4Split sp) { return sp == Q4Split::kFew ? kPrefillMinWork : 4 * kPrefillMinWork; }
+static float packed_prefill_min_work(PackedSplit sp) { return sp == PackedSplit::kFew ? kPrefillMinWork : 4 * kPrefillMinWork; }
 // Packed rows of a call's longest segment when none is empty.
-static int64_t q4_longest(int64_t T, int group, int S) { return std::max<int64_t>(1, T - std::max(S, 1) + 1) * group; }
+static int64_t packed_longest(int64_t T, int group, int S) { return std::max<int64_t>(1, T - std::max(S, 1) + 1) * group; }
 // Columns a 4-bit call stages in 16 bits for the prefill kernel: one per segment that can have
-// q4_prefill_min_rows, as far as 2 GiB of workspace hold them (at least one while that takes at most 8 GiB); none
-// when the automatic route cannot reach q4_prefill_min_work.  Depends on sizes and the route policy only.
-static int64_t q4_stage_bytes_per_column(int64_t rows, int Hkv, int D) { return rows * Hkv * D * 2; }
-static int q4_stage_cols(int bits, int64_t T, int Hq, int Hkv, int D, int S, int64_t rows) {
+// packed_prefill_min_rows, as far as 2 GiB of workspace hold them (at least one while that takes at most 8 GiB); none
+// when the automatic route cannot reach packed_prefill_min_work.  Depends on sizes and the route policy only.
+static int64_t stage_bytes_per_column(int64_t rows, int Hkv, int D) { return rows * Hkv * D * 2; }
+static int packed_stage_cols(int64_t T, int Hq, int Hkv, int D, int S, int64_t rows) {
   const int policy = g_policy.load();
   const int group = Hq / Hkv;
   if (policy == SDPA_ROUTE_SPLITK || group > kPrefillRows || kPrefillRows % group || S <= 0 || T <= 0) return 0;
   const int64_t packed = T * group;
   int64_t n = S;
   if (policy == SDPA_ROUTE_AUTO) {
-    const Q4Split sp = q4_split(bits, T, Hq, Hkv, D, S);
-    if (q4_longest(T, group, S) < q4_prefill_min_rows(sp) ||
-        (double)packed * Hkv * D * (double)rows < (double)q4_prefill_min_work(sp))
+    const PackedSplit sp = packed_split(T, Hq, Hkv, D, S);
+    if (packed_longest(T, group, S) < packed_prefill_min_rows(sp) ||
+        (double)packed * Hkv * D * (double)rows < (double)packed_prefill_min_work(sp))
       return 0;
-    n = std::min<int64_t>(n, packed / q4_prefill_min_rows(sp));
+    n = std::min<int64_t>(n, packed / packed_prefill_min_rows(sp));
   }
-  const int64_t col = 2 * q4_stage_bytes_per_column(rows, Hkv, D);  // K and V
+  const int64_t col = 2 * stage_bytes_per_column(rows, Hkv, D);  // K and V
   if (col > (8ll << 30)) return 0;
   return (int)std::min<int64_t>(n, std::max<int64_t>(1, (2ll << 30) / col));
 }
@@ -448,8 +450,9 @@ static sdpa_status launch_all(const SchedArgs& sa, const AttnArgs& aa, int D, co
     const int smem = packed_smem_bytes(packed->bits, D);
     if (sa.sk_choice || sa.sk[0].rows == kSplitkRows)
       e = launch_k(packed_splitk_ptr(packed->bits, D), (unsigned)sa.sk[0].grid, kPackedThreads, args, smem, st, true);
-    if (e == cudaSuccess && (sa.sk_choice || sa.sk[0].rows == kQ4TileRows))
-      e = launch_k(q4_tile_kernel_ptr(D), (unsigned)sa.sk[1].grid, kQ4TileThreads, args, q4_tile_smem_bytes(D), st, true);
+    if (e == cudaSuccess && (sa.sk_choice || sa.sk[0].rows == kPackedTileRows))
+      e = launch_k(packed_tile_ptr(packed->bits, D), (unsigned)sa.sk[1].grid, kPackedTileThreads, args,
+                   packed_tile_smem(packed->bits, D), st, true);
     if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "%d-bit split-K launch: %s", packed->bits, cudaGetErrorString(e));
   } else if (e == cudaSuccess) {
     void* args[] = {(void*)&aa};
@@ -496,24 +499,24 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
   DevInfo di;
   if ((st = device_info(&di))) return st;
   Grids g = grids_for(di, D);
-  Q4Split sp = Q4Split::kFew;
-  SkShape few{kSplitkRows, kSplitkTile, kSkBf16, g.splitk}, tile = q4_tile_shape(di);
+  PackedSplit sp = PackedSplit::kFew;
+  SkShape few{kSplitkRows, kSplitkTile, kSkBf16, g.splitk}, tile = packed_tile_shape(di);
   if (packed) {
-    sp = q4_split(bits, T, Hq, Hkv, D, S);
+    sp = packed_split(T, Hq, Hkv, D, S);
     few = packed_few_shape(di, bits, D);
     g.splitk = few.grid;
   }
   Workspace W;
   size_t need = layout_workspace((char*)ws, T, Hq, Hkv, D, S, g.splitk, g.prefill, &W, true,
-                                 bits == 4 && D <= 128 ? &tile : nullptr);
+                                 packed && D <= 128 ? &tile : nullptr);
   if (ws_bytes < need)
     return fail(SDPA_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need);
   const int parts =
       packed ? packed_direct_parts(di, bits, T, Hq, Hkv, D, S, rows, causal, window, S > 0 ? seg_mode : nullptr) : 0;
   PackedStageArgs sg{};
   if (packed && parts == 0) {  // as many staged columns as the workspace holds
-    const int64_t col = q4_stage_bytes_per_column(rows, Hkv, D);  // (a multiple of 256)
-    sg.pf_cols = (int)std::min<int64_t>(q4_stage_cols(bits, T, Hq, Hkv, D, S, rows), (int64_t)(ws_bytes - need) / (2 * col));
+    const int64_t col = stage_bytes_per_column(rows, Hkv, D);  // (a multiple of 256)
+    sg.pf_cols = (int)std::min<int64_t>(packed_stage_cols(T, Hq, Hkv, D, S, rows), (int64_t)(ws_bytes - need) / (2 * col));
     sg.k = (__nv_bfloat16*)((char*)ws + need);
     sg.v = (__half*)((char*)ws + need + col * sg.pf_cols);
   }
@@ -538,15 +541,15 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
   const int group = Hq / Hkv;
   const bool group_fits = group <= kPrefillRows && (kPrefillRows % group) == 0;
   sa.tile_pf = prefill_tile_keys(D);
-  sa.pf_min_rows = packed ? q4_prefill_min_rows(sp) : kPrefillRows;
-  sa.pf_tile_rows = kQ4TilePrefillRows;
-  sa.pf_min_work = packed ? q4_prefill_min_work(sp) : kPrefillMinWork;
+  sa.pf_min_rows = packed ? packed_prefill_min_rows(sp) : kPrefillRows;
+  sa.pf_tile_rows = kTilePrefillRows;
+  sa.pf_min_work = packed ? packed_prefill_min_work(sp) : kPrefillMinWork;
   sa.packed = packed != nullptr;
   sa.key_bytes = bits == 8 ? 2 * D : D + D / (kQ4Group / 2);
-  sa.sk[0] = sp == Q4Split::kTile ? tile : few;
+  sa.sk[0] = sp == PackedSplit::kTile ? tile : few;
   sa.sk[1] = tile;
-  sa.sk_choice = sp == Q4Split::kEither;
-  sa.sk_ratio = q4_tile_ratio(D);
+  sa.sk_choice = sp == PackedSplit::kEither;
+  sa.sk_ratio = packed_tile_ratio(D);
   sa.lo_align = packed ? kPackedRows : 1;
   sa.pf_cols = sg.pf_cols;
   // (a call-wide window bounds the positions that a staged column has to hold)
@@ -638,16 +641,16 @@ static size_t packed_workspace_bytes(int bits, int64_t T, int Hq, int Hkv, int D
   if (D != 64 && D != 128 && D != 256) return 0;
   DevInfo di;
   Grids g{4096, 1024};  // without a device: bounds above any real grid
-  SkShape tile{kQ4TileRows, kQ4TileKeys, kSkQ4Tile, 1024};
+  SkShape tile{kPackedTileRows, kPackedTileKeys, kSkQ4Tile, 1024};
   if (device_info(&di) == SDPA_OK) {
     g = {packed_resident(di, bits, D), grids_for(di, D).prefill};
-    tile = q4_tile_shape(di);
+    tile = packed_tile_shape(di);
   } else {
     g_err[0] = 0;
   }
   return layout_workspace(nullptr, T, Hq, Hkv, D, S, g.splitk, g.prefill, nullptr, true,
-                          bits == 4 && D <= 128 ? &tile : nullptr) +
-         2 * q4_stage_bytes_per_column(rows, Hkv, D) * q4_stage_cols(bits, T, Hq, Hkv, D, S, rows);
+                          D <= 128 ? &tile : nullptr) +
+         2 * stage_bytes_per_column(rows, Hkv, D) * packed_stage_cols(T, Hq, Hkv, D, S, rows);
 }
 
 static sdpa_status run_packed(int bits, const PackedStore& store, const void* q, int64_t T, int Hq, int D, int64_t q_rs,

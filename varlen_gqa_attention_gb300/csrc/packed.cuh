@@ -47,6 +47,12 @@ struct PackedStageArgs {
 };
 constexpr int kPackedStageThreads = 256;
 
+// The tensor-memory kernel for segments of several rows (packed_tile.cuh; D = 64, 128): one CTA per SM, units of
+// kPackedTileRows packed rows, tiles of kPackedTileKeys keys.
+constexpr int kPackedTileRows = 128;
+constexpr int kPackedTileKeys = 128;
+constexpr int kPackedTileThreads = 576;
+
 // A constant that the compiler keeps in a register.
 __device__ __forceinline__ uint32_t in_register(uint32_t v) {
   asm volatile("" : "+r"(v));

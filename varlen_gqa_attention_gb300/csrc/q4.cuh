@@ -108,11 +108,7 @@ struct Q4AttnArgs {
 const void* q4_stage_kernel_ptr(int D);
 
 // Entry points (q4_attn.cu).
-// The tensor-memory kernel for segments of several rows (q4_tile.cu; D = 64, 128): one CTA per SM, units of
-// kQ4TileRows packed rows, tiles of kQ4TileKeys keys.
-constexpr int kQ4TileRows = 128;
-constexpr int kQ4TileKeys = 128;
-constexpr int kQ4TileThreads = 576;
+constexpr int kQ4TileRows = kPackedTileRows, kQ4TileKeys = kPackedTileKeys;
 const void* q4_tile_kernel_ptr(int D);
 int q4_tile_smem_bytes(int D);
 const void* q4_splitk_kernel_ptr(int D);

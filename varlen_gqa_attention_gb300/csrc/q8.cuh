@@ -47,6 +47,53 @@ __device__ __forceinline__ uint2 q8_words4(uint32_t w, __nv_bfloat162 s2) {
 }
 __device__ __forceinline__ __nv_bfloat162 q8_scale_bf16(uint32_t b) { return __float2bfloat162_rn(q8_scale(b)); }
 
+// What the attention kernels multiply: values / 16 in fp16, exact, which one fused multiply-add makes of a code.
+// 0x6400 | c is 1024 + c, and (1024 + c) t - 1152 t = (c - 128) t with t = s / 16, whose largest addend is
+// 1152 * 2^5; every term and the result are exact.
+constexpr uint32_t kQ8Magic = 0x64646464u;  // the high byte of 1024 in fp16, four times
+// (t, t) of a scale byte: 2^(b - 24) in fp16, below 2^-14 a subnormal number.
+__device__ __forceinline__ uint32_t q8_scale_f16x2(uint32_t byte) {
+  const uint32_t b = min(byte, (uint32_t)kQ8Top);
+  const uint32_t t = b < 10 ? 1u << b : (b - 9) << 10;
+  return t | t << 16;
+}
+// Two values / 16 from bytes 0 and 1 (HI: 2 and 3) of x; magic: kQ8Magic in a register, z = -1152 t.
+template <bool HI>
+__device__ __forceinline__ uint32_t q8_pair_f16(uint32_t x, uint32_t magic, __half2 t, __half2 z) {
+  const uint32_t u = __byte_perm(x, magic, HI ? 0x4342 : 0x4140);
+  const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&u), t, z);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// Query rows in fp16: a row times 2^(14 - e), e being the exponent of its largest magnitude (but at most 2^126, so
+// that rows of less than 2^-112 stay as much below 2^14; a row with an infinity keeps it).  What is above 2^-31
+// of the largest magnitude is exact, what is below is off by at most 2^-40 of it.
+__device__ __forceinline__ float q8_row_amax(const uint4& w, float amax) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(x[k] << 16)), fabsf(__uint_as_float(x[k] & 0xFFFF0000u))));
+  return amax;
+}
+// The exponent field of the factor.
+__device__ __forceinline__ uint32_t q8_row_up(float amax) {
+  return 268u - min(max(__float_as_uint(amax) >> 23, 15u), 254u);
+}
+__device__ __forceinline__ uint4 q8_row_f16(const uint4& w, float mul) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+  uint32_t f[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const __half2 v = __floats2half2_rn(__uint_as_float(x[k] << 16) * mul, __uint_as_float(x[k] & 0xFFFF0000u) * mul);
+    f[k] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return make_uint4(f[0], f[1], f[2], f[3]);
+}
+// The scale of such a row's scores against keys / 16: finite and not 0, so that a masked score stays -infinity and
+// a score of 0 stays 0.
+__device__ __forceinline__ float q8_row_scale(uint32_t up, float scale_log2) {
+  return fminf(fmaxf(16.f * scale_log2 * __uint_as_float((254u - up) << 23), FLT_MIN), FLT_MAX);
+}
+
 struct Q8AttnArgs {
   CUtensorMap k, v;  // the store's codes as [cols * Hkv, rows, D] bytes, in boxes of 16 rows (api.cu)
   AttnArgs a;        // k, v unused
@@ -58,5 +105,7 @@ const void* q8_splitk_kernel_ptr(int D);
 const void* q8_direct_kernel_ptr(int D);
 int q8_splitk_smem_bytes(int D);
 const void* q8_stage_kernel_ptr(int D);
+const void* q8_tile_kernel_ptr(int D);
+int q8_tile_smem_bytes(int D);
 
 }  // namespace sdpa

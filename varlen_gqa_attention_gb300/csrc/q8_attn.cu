@@ -3,7 +3,7 @@
 // What bounds it: a key of one KV head is D bytes of K and of V and an eighth of a byte of scales, at the measured
 // copy rate one key per 11 SM cycles at D = 128; its 256 values take two instructions for every two of them to become
 // matrix operands (a byte permutation that puts the code under the exponent of 1024, then one fused
-// multiply-add, see pair below), so that converting takes a fifth of the issue slots of that time.
+// multiply-add, see q8.cuh), so that converting takes a fifth of the issue slots of that time.
 //   * K and V are both multiplied in fp16, of their values / 16: exact, and the fused multiply-add's
 //     addend -1152 s / 16 stays finite up to the largest scale.  The factor 16 goes into the scores' scale and the
 //     output.
@@ -18,8 +18,6 @@
 #include "q8.cuh"
 
 namespace sdpa {
-
-constexpr uint32_t kQ8Magic = 0x64646464u;  // the high byte of 1024 in fp16, four times
 
 template <int D>
 struct Q8Few {
@@ -75,12 +73,11 @@ struct Q8Few {
 #pragma unroll
         for (int p = 0; p < kPlanes; ++p)
           tma_load_3d(dst + p * kPlane, value ? &G.v : &G.k, bar, p * kPitch, (int)my_row(row), col_head);
-        const uint32_t b = min(byte, (uint32_t)kQ8Top);
-        t = b < 10 ? 1u << b : (b - 9) << 10;  // 2^(b - 24) in fp16
+        t = q8_scale_f16x2(byte);
       }
       if (value < 2)
         *reinterpret_cast<uint32_t*>(ring + kStages * kStageBytes + st * kSideBytes + (value * kBlocks + block) * 4) =
-            t | t << 16;
+            t;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     }
@@ -97,31 +94,19 @@ struct Q8Few {
         // (a plane's 32 dims of the lane are side by side)
         w[i] = *reinterpret_cast<const uint4*>(row + i / (kPitch / 32) * (2 * kPitch) + tq * (kPitch / 2) +
                                                i % (kPitch / 32) * 16);
-        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(x[k] << 16)), fabsf(__uint_as_float(x[k] & 0xFFFF0000u))));
+        amax = q8_row_amax(w[i], amax);
       }
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      // the row times 2^(14 - e), e being the exponent of its largest magnitude (at most 2^126: rows of less than
-      // 2^-112 stay as much below 2^14; a row with an infinity comes out as one with it)
-      const uint32_t up = 268u - min(max(__float_as_uint(amax) >> 23, 15u), 254u);
-      const float mul = __uint_as_float(up << 23);
+      const uint32_t up = q8_row_up(amax);
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          f[4 * i + k] = pack_f16x2(__uint_as_float(x[k] << 16) * mul, __uint_as_float(x[k] & 0xFFFF0000u) * mul);
+        const uint4 x = q8_row_f16(w[i], __uint_as_float(up << 23));
+        f[4 * i] = x.x; f[4 * i + 1] = x.y; f[4 * i + 2] = x.z; f[4 * i + 3] = x.w;
       }
-      const float down = __uint_as_float((254u - up) << 23);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        // finite and not 0, so that a masked score stays -infinity and a score of 0 stays 0
-        const float s = 16.f * scale_log2 * __shfl_sync(0xffffffffu, down, 4 * (2 * tq + c));
-        sl2[c] = fminf(fmaxf(s, FLT_MIN), FLT_MAX);
-      }
+      for (int c = 0; c < 2; ++c)
+        sl2[c] = q8_row_scale(__shfl_sync(0xffffffffu, up, 4 * (2 * tq + c)), scale_log2);
     }
     __device__ __forceinline__ float scale(int c) const { return sl2[c]; }
   };
@@ -137,13 +122,9 @@ struct Q8Few {
         : magic(in_register(kQ8Magic)), gq(lane >> 2), tq(lane & 3), kn(gq ^ ((gq >> 1) & 1)),
           ko(2 * tq + (tq & 1)) {}
 
-    // Two values / 16 in fp16 from bytes 0 and 1 (hi: 2 and 3) of x: 0x6400 | c is 1024 + c, and
-    // (1024 + c) t - 1152 t = (c - 128) t; every term and the result are exact.
     template <bool HI>
     __device__ __forceinline__ uint32_t pair(uint32_t x, __half2 t, __half2 z) const {
-      const uint32_t u = __byte_perm(x, magic, HI ? 0x4342 : 0x4140);
-      const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&u), t, z);
-      return *reinterpret_cast<const uint32_t*>(&v);
+      return q8_pair_f16<HI>(x, magic, t, z);
     }
     __device__ __forceinline__ static void scales(const char* side, int block, __half2* t, __half2* z) {
       *t = *reinterpret_cast<const __half2*>(side + 4 * block);
