@@ -224,18 +224,21 @@ static Grids grids_for(const DevInfo& di, int D) {
 // chunk and many single tokens) both, and the schedule is the cheaper one's; the other leaves at once.  At
 // D = 256 the output of 128 rows leaves no room for the first.
 enum class PackedSplit { kFew, kTile, kEither };
-static PackedSplit packed_split(int64_t T, int Hq, int Hkv, int D, int S) {
-  if (D > 128 || T * (Hq / Hkv) <= 16 * (int64_t)std::max(S, 1)) return PackedSplit::kFew;
+static PackedSplit packed_split(int bits, int64_t T, int Hq, int Hkv, int D, int S) {
+  const int few = bits == 8 && D == 64 ? 32 : 16;
+  if (D > 128 || T * (Hq / Hkv) <= few * (int64_t)std::max(S, 1)) return PackedSplit::kFew;
   return S <= 1 ? PackedSplit::kTile : PackedSplit::kEither;
 }
 // The tensor-memory kernel's cost of a key for a unit, in those of the other one for 8 rows (full loads: 0.066
 // and 0.027 ns at D = 128, 0.054 and 0.015 at D = 64).
-static float packed_tile_ratio(int D) { return D == 64 ? 3.5f : 2.5f; }
+// Over the 8-bit store, against the other one's 8 rows (the calls of tile_cost, common.cuh): 160 us for 24 rows and 177 for
+// 64 at D = 128, 157 for 32 and 165 for 64 at D = 64.
+static float packed_tile_ratio(int bits, int D) { return bits == 8 ? (D == 64 ? 3.6f : 2.1f) : D == 64 ? 3.5f : 2.5f; }
 static int64_t packed_resident(const DevInfo& di, int bits, int D) {
   return (int64_t)di.sms * di.packed_per_sm[bits / 8][d_index(D)];
 }
 static SkShape packed_few_shape(const DevInfo& di, int bits, int D) {
-  return {kSplitkRows, kSplitkTile, kSkQ4Few, packed_resident(di, bits, D)};
+  return {kSplitkRows, kSplitkTile, bits == 8 ? kSkQ8Few : kSkQ4Few, packed_resident(di, bits, D)};
 }
 static SkShape packed_tile_shape(const DevInfo& di) { return {kPackedTileRows, kPackedTileKeys, kSkQ4Tile, di.sms}; }
 
@@ -355,14 +358,14 @@ static int64_t packed_longest(int64_t T, int group, int S) { return std::max<int
 // packed_prefill_min_rows, as far as 2 GiB of workspace hold them (at least one while that takes at most 8 GiB); none
 // when the automatic route cannot reach packed_prefill_min_work.  Depends on sizes and the route policy only.
 static int64_t stage_bytes_per_column(int64_t rows, int Hkv, int D) { return rows * Hkv * D * 2; }
-static int packed_stage_cols(int64_t T, int Hq, int Hkv, int D, int S, int64_t rows) {
+static int packed_stage_cols(int bits, int64_t T, int Hq, int Hkv, int D, int S, int64_t rows) {
   const int policy = g_policy.load();
   const int group = Hq / Hkv;
   if (policy == SDPA_ROUTE_SPLITK || group > kPrefillRows || kPrefillRows % group || S <= 0 || T <= 0) return 0;
   const int64_t packed = T * group;
   int64_t n = S;
   if (policy == SDPA_ROUTE_AUTO) {
-    const PackedSplit sp = packed_split(T, Hq, Hkv, D, S);
+    const PackedSplit sp = packed_split(bits, T, Hq, Hkv, D, S);
     if (packed_longest(T, group, S) < packed_prefill_min_rows(sp) ||
         (double)packed * Hkv * D * (double)rows < (double)packed_prefill_min_work(sp))
       return 0;
@@ -502,7 +505,7 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
   PackedSplit sp = PackedSplit::kFew;
   SkShape few{kSplitkRows, kSplitkTile, kSkBf16, g.splitk}, tile = packed_tile_shape(di);
   if (packed) {
-    sp = packed_split(T, Hq, Hkv, D, S);
+    sp = packed_split(bits, T, Hq, Hkv, D, S);
     few = packed_few_shape(di, bits, D);
     g.splitk = few.grid;
   }
@@ -516,7 +519,7 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
   PackedStageArgs sg{};
   if (packed && parts == 0) {  // as many staged columns as the workspace holds
     const int64_t col = stage_bytes_per_column(rows, Hkv, D);  // (a multiple of 256)
-    sg.pf_cols = (int)std::min<int64_t>(packed_stage_cols(T, Hq, Hkv, D, S, rows), (int64_t)(ws_bytes - need) / (2 * col));
+    sg.pf_cols = (int)std::min<int64_t>(packed_stage_cols(bits, T, Hq, Hkv, D, S, rows), (int64_t)(ws_bytes - need) / (2 * col));
     sg.k = (__nv_bfloat16*)((char*)ws + need);
     sg.v = (__half*)((char*)ws + need + col * sg.pf_cols);
   }
@@ -549,7 +552,7 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
   sa.sk[0] = sp == PackedSplit::kTile ? tile : few;
   sa.sk[1] = tile;
   sa.sk_choice = sp == PackedSplit::kEither;
-  sa.sk_ratio = packed_tile_ratio(D);
+  sa.sk_ratio = packed_tile_ratio(bits, D);
   sa.lo_align = packed ? kPackedRows : 1;
   sa.pf_cols = sg.pf_cols;
   // (a call-wide window bounds the positions that a staged column has to hold)
@@ -650,7 +653,7 @@ static size_t packed_workspace_bytes(int bits, int64_t T, int Hq, int Hkv, int D
   }
   return layout_workspace(nullptr, T, Hq, Hkv, D, S, g.splitk, g.prefill, nullptr, true,
                           D <= 128 ? &tile : nullptr) +
-         2 * stage_bytes_per_column(rows, Hkv, D) * packed_stage_cols(T, Hq, Hkv, D, S, rows);
+         2 * stage_bytes_per_column(rows, Hkv, D) * packed_stage_cols(bits, T, Hq, Hkv, D, S, rows);
 }
 
 static sdpa_status run_packed(int bits, const PackedStore& store, const void* q, int64_t T, int Hq, int D, int64_t q_rs,

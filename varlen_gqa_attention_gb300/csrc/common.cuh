@@ -234,7 +234,7 @@ struct SchedArgs {
   int packed;         // a call over a store of codes: the fields below are read for those only
   int sk_choice;
   int64_t key_bytes;  // of a key and its value in the store
-  float sk_ratio;     // cost of a key for a unit of the second shape against that for 8 rows in the first
+  float sk_ratio;     // cost of a key for a unit of the second shape against that for up to 8 rows in the first
   int pf_min_rows;    // least packed rows of a segment of the prefill route (otherwise kPrefillRows)
   int pf_tile_rows;   // those when the schedule has taken the second shape
   float pf_min_work;  // least work of a call of the prefill route (otherwise kPrefillMinWork)
@@ -251,11 +251,12 @@ constexpr int kSchedThreads = 512;
 // Calls the small scheduler kernel takes: at most kSmallSegs segments and at most 8192 packed
 // rows, and units that fit one per thread with route 2's starting at a warp boundary.  Live
 // segments cover disjoint rows and a unit holds at least 32 packed rows, so the units number
-// at most Hkv * (ceil(T * group / 32) + S).
+// at most Hkv * (ceil(T * group / 32) + S); with unit_rows 128 where the tile kernel of a store of codes and the
+// prefill kernel are all that is launched.
 constexpr int kSmallSegs = 32;
-__host__ __device__ inline bool sched_small_ok(int64_t T, int Hq, int Hkv, int S) {
+__host__ __device__ inline bool sched_small_ok(int64_t T, int Hq, int Hkv, int S, int unit_rows = 32) {
   if (S > kSmallSegs || T > 8192 || Hkv <= 0) return false;
-  const int64_t units = (int64_t)Hkv * ((T * (Hq / Hkv) + 31) / 32 + S);
+  const int64_t units = (int64_t)Hkv * ((T * (Hq / Hkv) + unit_rows - 1) / unit_rows + S);
   return units + 31 <= kSchedThreads;
 }
 
@@ -398,9 +399,14 @@ __host__ __device__ inline void key_tile(const KeyTiles& k, int64_t t, int bn, i
 // operands again for every 8 rows of a unit, and the tensor-memory one takes 1.2 times as long over more
 // than 64 rows and starts a piece in the time of 4 tiles.  64 tokens over 16384 to 32768 keys beside a
 // 512-token chunk over 512, 32/8 heads, D = 128, all on the first: 674 us with the bf16 kernel's costs, 415 so.
-enum SkKind : int { kSkBf16 = 0, kSkQ4Few = 1, kSkQ4Tile = 2 };
+// The 8-bit one's for few rows is bound by memory with up to 8 rows a unit, and takes 1.33 times as long with up to 16,
+// whose keys are converted twice over, and 2.4 times with more (32 sequences of 8192 keys, 64/8 heads, D = 128 and
+// 64, and 32/4, D = 256, less 13 us of schedule and joining: 83, 45 and 88 us for 8 rows, 110, 60 and 117 for 16,
+// 211 for 24 and for 32 at D = 256).
+enum SkKind : int { kSkBf16 = 0, kSkQ4Few = 1, kSkQ4Tile = 2, kSkQ8Few = 3 };
 __host__ __device__ __forceinline__ int64_t tile_cost(int route, int rows, int kind = kSkBf16) {
   if (route != kRouteSplitk) return 1;
+  if (kind == kSkQ8Few) return rows > 16 ? 10 : rows > 8 ? 5 : 4;
   return kind == kSkBf16 ? (rows > 16 ? 6 : 4) : kind == kSkQ4Few ? 4 * ((rows + 7) / 8) : (rows > 64 ? 5 : 4);
 }
 __host__ __device__ __forceinline__ int64_t lead_cost(int route, int kind = kSkBf16) {
@@ -410,7 +416,7 @@ __host__ __device__ __forceinline__ int64_t lead_cost(int route, int kind = kSkB
 // CTA's share holds the start of a tile of each unit it crosses (nslots stays exact).
 __host__ __device__ __forceinline__ int64_t phase_ctas(int64_t G, int64_t Wp, int route, int kind = kSkBf16) {
   // (divisions by constants)
-  const int64_t g = route != kRouteSplitk ? Wp : kind == kSkBf16 ? Wp / 6 : kind == kSkQ4Few ? Wp / (4 * (kSplitkRows / 8)) : Wp / 5;
+  const int64_t g = route != kRouteSplitk ? Wp : kind == kSkBf16 ? Wp / 6 : kind == kSkQ4Few ? Wp / (4 * (kSplitkRows / 8)) : kind == kSkQ8Few ? Wp / 10 : Wp / 5;
   return g < 1 ? 1 : (g < G ? g : G);
 }
 // The tiles [ta, tb) of a unit whose first tile starts at line position k0 (nt tiles of tw

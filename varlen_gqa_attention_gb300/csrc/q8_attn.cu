@@ -39,7 +39,7 @@ struct Q8Few {
   static constexpr int kMergeBytes = 4 * 8 * 36 * 4;  // 32 dims of the warps' rows
   static constexpr int kAlign = 8 * kPitch, kFull = 2;
   static constexpr int kBytes = kRingBytes + kQBytes + kMergeBytes + kAlign;
-  static constexpr SkKind kKind = kSkQ4Few;
+  static constexpr SkKind kKind = kSkQ8Few;
   static constexpr float kOut = 16.f;
   static constexpr int NK = D == 64 ? 1 : 2;  // 16-byte chunks of a lane's K row in a plane
   static constexpr int NV = D == 256 ? 2 : 1;  // of its V row (D = 64: half a chunk)

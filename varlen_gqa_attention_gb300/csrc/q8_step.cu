@@ -25,28 +25,34 @@ __device__ __forceinline__ uint32_t q8_storable(uint32_t w) {
   v = __hmin2(__hmax2(v, __float2bfloat162_rn(-65024.f)), __float2bfloat162_rn(65024.f));
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-// The low byte of round(v) + 128: adding 1.5 * 2^23 rounds (halves to even) and leaves the integer's two's
-// complement in the low bits.
-__device__ __forceinline__ uint32_t q8_code(float v) { return __float_as_uint(v + 12582912.f) ^ 128u; }
-__device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+// The low byte of round(v): adding 1.5 * 2^23 rounds (halves to even) and leaves the integer's two's complement in
+// the low bits.  A code is that with its top bit turned.
+__device__ __forceinline__ uint32_t q8_low(float v) { return __float_as_uint(v + 12582912.f); }
+__device__ __forceinline__ uint32_t q8_codes4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410) ^ 0x80808080u;
 }
 // The codes of 8 bf16 values, inv being 1 / s (a power of two: the product is exact).
 __device__ __forceinline__ uint2 q8_codes8(const uint4& w, float inv) {
-  return make_uint2(bytes4(q8_code(bf_lo(w.x) * inv), q8_code(bf_hi(w.x) * inv), q8_code(bf_lo(w.y) * inv),
-                           q8_code(bf_hi(w.y) * inv)),
-                    bytes4(q8_code(bf_lo(w.z) * inv), q8_code(bf_hi(w.z) * inv), q8_code(bf_lo(w.w) * inv),
-                           q8_code(bf_hi(w.w) * inv)));
+  return make_uint2(q8_codes4(q8_low(bf_lo(w.x) * inv), q8_low(bf_hi(w.x) * inv), q8_low(bf_lo(w.y) * inv),
+                              q8_low(bf_hi(w.y) * inv)),
+                    q8_codes4(q8_low(bf_lo(w.z) * inv), q8_low(bf_hi(w.z) * inv), q8_low(bf_lo(w.w) * inv),
+                              q8_low(bf_hi(w.w) * inv)));
 }
 __device__ __forceinline__ float q8_int(uint32_t w, int k) { return (float)(int)((w >> (8 * k) & 255u) - 128); }
 // A word of codes under a scale `ratio` (s before / s after) times as coarse.
 __device__ __forceinline__ uint32_t q8_again(uint32_t w, float ratio) {
-  return bytes4(q8_code(q8_int(w, 0) * ratio), q8_code(q8_int(w, 1) * ratio), q8_code(q8_int(w, 2) * ratio),
-                q8_code(q8_int(w, 3) * ratio));
+  return q8_codes4(q8_low(q8_int(w, 0) * ratio), q8_low(q8_int(w, 1) * ratio), q8_low(q8_int(w, 2) * ratio),
+                   q8_low(q8_int(w, 3) * ratio));
 }
 __device__ __forceinline__ float q8_amax4(uint32_t w) {
   return fmaxf(fmaxf(fabsf(q8_int(w, 0)), fabsf(q8_int(w, 1))), fmaxf(fabsf(q8_int(w, 2)), fabsf(q8_int(w, 3))));
 }
+// Largest magnitudes of bf16 pairs, as bit patterns (they are ordered as the magnitudes are, NaN beyond infinity).
+__device__ __forceinline__ uint32_t pair_amax(uint32_t m, const uint4& w) {
+  m = __vmaxu2(m, __vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu));
+  return __vmaxu2(m, __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+}
+constexpr uint32_t kQ8Most = 0x477Eu;  // 65024 in bf16
 
 // What the warps need of a block: where its rows come from (a packed row, kKept or kNone), and where it lies.
 constexpr int kKept = -1, kNone = -2;
@@ -108,6 +114,12 @@ __device__ __forceinline__ void code_blocks(const StepArgs& A, int block, RowTab
       for (int a = 0; a < kRopeAxes; ++a) s_block.pos[tid][a] = pos[a];
     }
     if (!__syncthreads_or(fresh)) continue;  // (no row of the block has angles)
+
+    const int64_t brow = (uint32_t)b0 % (uint32_t)A.rows;
+    Row16 x[U];
+    int src[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) src[u] = s_block.src[u * RPP + ls];
     for (int i = tid; i < kPackedRows * A.r.half; i += kRopeThreads) {
       const int o = i / A.r.half, j = i - o * A.r.half;
       if (s_block.src[o] < 0) continue;
@@ -118,32 +130,28 @@ __device__ __forceinline__ void code_blocks(const StepArgs& A, int block, RowTab
     }
     __syncthreads();
 
-    const int64_t brow = (uint32_t)b0 % (uint32_t)A.rows;
     for (int item = ia + warp; item < ib; item += kWarps) {
-      const int h = item >> 1;
       const bool key = (item & 1) == 0;
+      const int h = item >> 1;
       const int64_t cell = ((int64_t)g.z * A.Hkv + h) * A.rows + brow;
       uint8_t* codes = (key ? A.q4.kc : A.q4.vc) + cell * D;
       uint8_t* scale = (key ? A.q4.ks : A.q4.vs) + cell / kPackedRows;
-      Row16 x[U];
-      int src[U];
       const uint32_t was = min((uint32_t)*scale, (uint32_t)kQ8Top);
+      const __nv_bfloat16* rows = key ? A.k + h * A.k_hs : A.v + h * A.v_hs;
+      const int64_t rs = key ? A.k_rs : A.v_rs;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int o = u * RPP + ls;
-        src[u] = s_block.src[o];
         if (src[u] >= 0) {
-          const __nv_bfloat16* z = key ? A.k + src[u] * A.k_rs + (int64_t)h * A.k_hs
-                                       : A.v + src[u] * A.v_rs + (int64_t)h * A.v_hs;
-          x[u].a = ldg16(z + ld.da);
-          x[u].b = ldg16(z + ld.db);
+          x[u].a = ldg16(rows + src[u] * rs + ld.da);
+          x[u].b = ldg16(rows + src[u] * rs + ld.db);
         } else if (src[u] == kKept) {
-          const uint2 a = *reinterpret_cast<const uint2*>(codes + o * D + ld.da);
-          const uint2 b = *reinterpret_cast<const uint2*>(codes + o * D + ld.db);
+          const uint2 a = *reinterpret_cast<const uint2*>(codes + (u * RPP + ls) * D + ld.da);
+          const uint2 b = *reinterpret_cast<const uint2*>(codes + (u * RPP + ls) * D + ld.db);
           x[u].a = make_uint4(a.x, a.y, b.x, b.y);
         }
       }
-      float amax = 0.f, kept = 0.f;
+      uint32_t pairs = 0;  // largest magnitudes of the new rows, of even dims and of odd ones
+      float kept = 0.f;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (src[u] >= 0) {
@@ -157,19 +165,26 @@ __device__ __forceinline__ void code_blocks(const StepArgs& A, int block, RowTab
             }
             turn16<IL, true>(&x[u], an);
           }
-          x[u].a = make_uint4(q8_storable(x[u].a.x), q8_storable(x[u].a.y), q8_storable(x[u].a.z), q8_storable(x[u].a.w));
-          x[u].b = make_uint4(q8_storable(x[u].b.x), q8_storable(x[u].b.y), q8_storable(x[u].b.z), q8_storable(x[u].b.w));
-          const uint32_t ca[4] = {x[u].a.x, x[u].a.y, x[u].a.z, x[u].a.w};
-          const uint32_t cb[4] = {x[u].b.x, x[u].b.y, x[u].b.z, x[u].b.w};
-          amax = fmaxf(amax, fmaxf(amax8(ca), amax8(cb)));
+          pairs = pair_amax(pair_amax(pairs, x[u].a), x[u].b);
         } else if (src[u] == kKept) {
           kept = fmaxf(kept, fmaxf(fmaxf(q8_amax4(x[u].a.x), q8_amax4(x[u].a.y)),
                                    fmaxf(q8_amax4(x[u].a.z), q8_amax4(x[u].a.w))));
         }
       }
-      amax = fmaxf(amax, kept * q8_scale(was));
+      uint32_t most = max(pairs & 0xFFFFu, pairs >> 16);
+      if (__any_sync(0xffffffffu, most > kQ8Most)) {  // NaN, infinities, magnitudes beyond the largest scale's
+        pairs = 0;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+        for (int u = 0; u < U; ++u) {
+          if (src[u] < 0) continue;
+          x[u].a = make_uint4(q8_storable(x[u].a.x), q8_storable(x[u].a.y), q8_storable(x[u].a.z), q8_storable(x[u].a.w));
+          x[u].b = make_uint4(q8_storable(x[u].b.x), q8_storable(x[u].b.y), q8_storable(x[u].b.z), q8_storable(x[u].b.w));
+          pairs = pair_amax(pair_amax(pairs, x[u].a), x[u].b);
+        }
+        most = max(pairs & 0xFFFFu, pairs >> 16);
+      }
+      const float amax = __uint_as_float(
+          __reduce_max_sync(0xffffffffu, max(most << 16, __float_as_uint(kept * q8_scale(was)))));
       const uint32_t byte = q8_scale_byte(amax);
       const float inv = __uint_as_float((127 + kQ8Bias - byte) << 23);
       const float ratio = q8_scale(was) * inv;
@@ -210,7 +225,7 @@ __global__ void __launch_bounds__(kRopeThreads, D == 256 ? 2 : 3) sdpa_rope_appe
 template <int D>
 __global__ void __launch_bounds__(kRopeThreads) sdpa_q8_unpack_kernel(StepArgs A) {
   __shared__ RowTable s_rows;
-  constexpr int LPH = D / 8, U = 4;
+  constexpr int CPH = D / 16, U = 4;  // chunks of a head
   const int64_t t0 = (int64_t)blockIdx.x * A.cr;
   const int n = (int)min((int64_t)A.cr, A.T - t0);
   find_rows(A, t0, n, &s_rows, blockIdx.x == 0);
@@ -220,40 +235,51 @@ __global__ void __launch_bounds__(kRopeThreads) sdpa_q8_unpack_kernel(StepArgs A
     s_rows.cell[threadIdx.x] = p >= 0 ? make_int2((int)((uint32_t)p % (uint32_t)A.rows), col) : make_int2(-1, 0);
   }
   __syncthreads();
-  const int per = A.Hkv * LPH;  // chunks of 8 dims of a row; a warp takes a row
-  for (int r = threadIdx.x / 32; r < n; r += kRopeThreads / 32) {
-    const int2 at = s_rows.cell[r];
-    const int64_t dst = (t0 + r) * A.o_rs;
-    for (int x0 = threadIdx.x % 32; x0 < per; x0 += 32 * U) {
-      uint2 kw[U], vw[U];
-      uint32_t kb[U], vb[U];
+  // A lane takes chunks of 16 dims, U at a time over the rows of its warp (warp, warp + 8, ...).  Two lanes change
+  // halves before they write, so that each write of a warp is 512 bytes in a row.
+  const int lane = threadIdx.x % 32, per = A.Hkv * CPH;
+  const bool odd = lane & 1;
+  int r = threadIdx.x / 32, x = lane;
+  while (r < n) {
+    uint4 kw[U], vw[U];
+    uint32_t kb[U], vb[U];
+    int row[U], at[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int x = x0 + 32 * u, h = x / LPH, c = x % LPH;
-        if (x < per && at.x >= 0) {
-          const int64_t cell = ((int64_t)at.y * A.Hkv + h) * A.rows + at.x;
-          kw[u] = *reinterpret_cast<const uint2*>(A.q4.kc + cell * D + 8 * c);
-          vw[u] = *reinterpret_cast<const uint2*>(A.q4.vc + cell * D + 8 * c);
-          kb[u] = A.q4.ks[cell / kPackedRows];
-          vb[u] = A.q4.vs[cell / kPackedRows];
-        }
+    for (int u = 0; u < U; ++u) {
+      row[u] = r < n && x < per ? r : -1;
+      at[u] = x;
+      if (row[u] >= 0) {
+        const int2 from = s_rows.cell[r];  // (a row that is not there reads another one's bytes)
+        const int h = x / CPH, c = x % CPH;
+        const int64_t cell = ((int64_t)from.y * A.Hkv + h) * A.rows + max(from.x, 0);
+        kw[u] = *reinterpret_cast<const uint4*>(A.q4.kc + cell * D + 16 * c);
+        vw[u] = *reinterpret_cast<const uint4*>(A.q4.vc + cell * D + 16 * c);
+        kb[u] = A.q4.ks[cell / kPackedRows];
+        vb[u] = A.q4.vs[cell / kPackedRows];
       }
+      x += 32;
+      if (x - lane >= per) {
+        x = lane;
+        r += kRopeThreads / 32;
+      }
+    }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int x = x0 + 32 * u, h = x / LPH, c = x % LPH;
-        if (x >= per) break;
-        const int64_t to = dst + (int64_t)h * A.o_hs + 8 * c;
-        uint4 k = make_uint4(0, 0, 0, 0), v = k;
-        if (at.x >= 0) {
-          const __nv_bfloat162 ks = q8_scale_bf16(kb[u]), vs = q8_scale_bf16(vb[u]);
-          const uint2 k0 = q8_words4(kw[u].x, ks), k1 = q8_words4(kw[u].y, ks);
-          const uint2 v0 = q8_words4(vw[u].x, vs), v1 = q8_words4(vw[u].y, vs);
-          k = make_uint4(k0.x, k0.y, k1.x, k1.y);
-          v = make_uint4(v0.x, v0.y, v1.x, v1.y);
-        }
-        stg16(A.k_out + to, k);
-        stg16(A.v_out + to, v);
-      }
+    for (int u = 0; u < U; ++u) {
+      auto out = [&](const uint4& w, uint32_t byte, __nv_bfloat16* to) {
+        const uint2 lo = make_uint2(w.x, w.y), hi = make_uint2(w.z, w.w), send = odd ? lo : hi;
+        const uint2 got = make_uint2(__shfl_xor_sync(0xffffffffu, send.x, 1), __shfl_xor_sync(0xffffffffu, send.y, 1));
+        if (row[u] < 0) return;
+        const uint2 w0 = odd ? got : lo, w1 = odd ? hi : got;
+        const bool there = s_rows.cell[row[u]].x >= 0;
+        const __nv_bfloat162 s = q8_scale_bf16(byte);
+        const uint2 a = q8_words4(w0.x, s), b = q8_words4(w0.y, s), c = q8_words4(w1.x, s), d = q8_words4(w1.y, s);
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        stg16(to, there ? make_uint4(a.x, a.y, b.x, b.y) : zero);
+        stg16(to + 16, there ? make_uint4(c.x, c.y, d.x, d.y) : zero);
+      };
+      const int64_t to = (t0 + max(row[u], 0)) * A.o_rs + (int64_t)(at[u] / CPH) * A.o_hs + at[u] % CPH / 2 * 32 + 8 * odd;
+      out(kw[u], kb[u], A.k_out + to);
+      out(vw[u], vb[u], A.v_out + to);
     }
   }
 }

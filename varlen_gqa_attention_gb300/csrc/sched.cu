@@ -199,8 +199,8 @@ __device__ __forceinline__ float prefill_work(const SchedArgs& A, int32_t q_len,
   return (float)R * (float)span * (float)A.Hkv * (float)A.D;
 }
 
-// What a segment adds to the cost of the second shape over the first: a key costs 1 for every 8 packed rows
-// there, which turn it into operands again, and sk_ratio for every unit here.  A segment that only the first
+// What a segment adds to the cost of the second shape over the first: a key costs 1 for up to 8 packed rows there,
+// and for more what the line's tiles do, and sk_ratio for every unit here.  A segment that only the first
 // shape's schedule gives to the prefill kernel (taken to be one with work enough of its own) costs about
 // 4 + rows / 64 a key there, staged and attended.
 __device__ __forceinline__ float sk_cost(const SchedArgs& A, int32_t q_len, int32_t kv_end, int32_t window) {
@@ -209,9 +209,12 @@ __device__ __forceinline__ float sk_cost(const SchedArgs& A, int32_t q_len, int3
   if (window > 0) span = min(span, (int64_t)q_len + window - 1);
   const bool pf = A.prefill_ok && (float)R * (float)span * (float)A.Hkv * (float)A.D >= A.pf_min_work;
   if (pf && R >= A.pf_tile_rows) return 0.f;  // the prefill kernel's in both
-  const int64_t n0 = pf && R >= A.pf_min_rows ? 4 + R / 64 : (R + 7) / 8;
+  const int64_t full = R / kSplitkRows, rest = R % kSplitkRows;
+  const int64_t few = full * tile_cost(kRouteSplitk, kSplitkRows, A.sk[0].kind) +
+                      (rest > 0 ? tile_cost(kRouteSplitk, (int)rest, A.sk[0].kind) : 0);
+  const float n0 = pf && R >= A.pf_min_rows ? (float)(4 + R / 64) : 0.25f * (float)few;
   const int64_t n1 = (R + A.sk[1].rows - 1) / A.sk[1].rows;
-  return ((float)n1 * A.sk_ratio - (float)n0) * (float)span;
+  return ((float)n1 * A.sk_ratio - n0) * (float)span;
 }
 
 // A segment's entry as the unit builder reads it.
@@ -972,7 +975,8 @@ const void* sched_small_kernel_ptr(bool packed) {
 
 cudaError_t launch_sched(const SchedArgs& sa, cudaStream_t st) {
   void* args[] = {(void*)&sa};
-  if (sched_small_ok(sa.T, sa.group * sa.Hkv, sa.Hkv, sa.S))
+  const bool tiles = sa.packed && !sa.sk_choice && sa.sk[0].rows >= 128;
+  if (sched_small_ok(sa.T, sa.group * sa.Hkv, sa.Hkv, sa.S, tiles ? 128 : 32))
     return cudaLaunchKernel(sched_small_kernel_ptr(sa.packed), dim3(1), dim3(kSchedThreads), args, 0, st);
   return cudaLaunchKernel(sched_kernel_ptr(sa.packed), dim3(1), dim3(kSchedThreads), args, sched_smem_bytes(), st);
 }
