@@ -189,20 +189,22 @@ static bool make_tensor_maps(const void* q, int64_t T, int Hq, int D, int64_t q_
   return true;
 }
 
-// TMA descriptors of an 8-bit store's codes [cols * Hkv, rows, D]: boxes of 16 rows of 128 bytes (64 at D = 64),
-// swizzled over their width.
+// TMA descriptors of an 8-bit store's codes [cols * Hkv, rows, D]: boxes of 16 rows and of q8_box_rows, 128 bytes wide
+// (64 at D = 64), swizzled over their width.
 static bool make_q8_maps(const PackedStore& st, int64_t rows, int cols, int Hkv, int D, Q8AttnArgs* out) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return false;
   const cuuint32_t es[3] = {1, 1, 1};
   const cuuint64_t dim[3] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)cols * Hkv};
   const cuuint64_t stride[2] = {(cuuint64_t)D, (cuuint64_t)rows * D};
-  const cuuint32_t box[3] = {(cuuint32_t)std::min(D, 128), kPackedRows, 1};
-  for (int v = 0; v < 2; ++v)
-    if (enc(v ? &out->v : &out->k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, v ? st.vc : st.kc, dim, stride, box, es,
+  CUtensorMap* const maps[4] = {&out->k, &out->v, &out->k_box, &out->v_box};
+  for (int i = 0; i < 4; ++i) {
+    const cuuint32_t box[3] = {(cuuint32_t)std::min(D, 128), (cuuint32_t)(i < 2 ? kPackedRows : q8_box_rows(D)), 1};
+    if (enc(maps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, i & 1 ? st.vc : st.kc, dim, stride, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return false;
+  }
   return true;
 }
 

@@ -94,8 +94,12 @@ __device__ __forceinline__ float q8_row_scale(uint32_t up, float scale_log2) {
   return fminf(fmaxf(16.f * scale_log2 * __uint_as_float((254u - up) << 23), FLT_MIN), FLT_MAX);
 }
 
+// The store's codes as [cols * Hkv, rows, D] bytes for TMA, in boxes of 16 rows and of q8_box_rows (api.cu).  (A
+// warp's copies go out one after another: the 16 small boxes of a stage of 128 keys took 0.5 us, which one
+// sequence's CTAs waited for.)
+constexpr int q8_box_rows(int D) { return D == 256 ? 64 : 128; }
 struct Q8AttnArgs {
-  CUtensorMap k, v;  // the store's codes as [cols * Hkv, rows, D] bytes, in boxes of 16 rows (api.cu)
+  CUtensorMap k, v, k_box, v_box;
   AttnArgs a;        // k, v unused
   PackedStore st;
   int choice;  // both split-K kernels are launched, and the schedule is one's (hdr->sk_rows)

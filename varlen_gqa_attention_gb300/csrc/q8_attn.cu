@@ -10,9 +10,9 @@
 //   * The queries come to fp16 by a power of two for each row, which brings the row's largest magnitude into
 //     [2^14, 2^15): what is above 2^-31 of it is exact, what is below is off by at most 2^-40 of it.  The opposite
 //     power goes into the scale of the row's scores.
-//   * A stage is loaded by TMA in boxes of 16 rows, swizzled so that both the K reads (16 codes of 8 rows) and the
-//     V reads (16 codes of 4 rows) of eight lanes meet all banks.  A lane each brings a box, and its block's scale
-//     byte, fetched while the stage before was waited for, as an fp16 pair.
+//   * A stage is loaded by TMA, in one box for K and one for V or in boxes of 16 rows at the ends, swizzled so that both the K reads (16 codes of 8 rows) and the
+//     V reads (16 codes of 4 rows) of eight lanes meet all banks.  A lane each brings a block's scale byte, fetched
+//     while the stage before was waited for, as an fp16 pair.
 // P is rounded to fp16 as over the 4-bit store (q4_attn.cu), sums are fp32.
 #include "packed_attn.cuh"
 #include "q8.cuh"
@@ -68,13 +68,23 @@ struct Q8Few {
       if (lane == 0) mbar_expect_tx(bar, (uint32_t)rows16 * 2 * D);
       __syncwarp();
       uint32_t t = 0;  // of a block that is not loaded: what lies there stays finite
-      if (mine(rows16)) {
-        const uint32_t dst = smem_u32(ring + st * kStageBytes) + value * kCodes + block * (kPackedRows * kPitch);
+      const uint32_t dst = smem_u32(ring + st * kStageBytes) + value * kCodes;
+      if (rows16 == kKeys && row + kKeys <= G.a.rows) {  // the stage in one run of store rows
+        if (value < 2 && block == 0) {
+          constexpr int kBox = q8_box_rows(D);
+#pragma unroll
+          for (int i = 0; i < kKeys; i += kBox)
+#pragma unroll
+            for (int p = 0; p < kPlanes; ++p)
+              tma_load_3d(dst + p * kPlane + i * kPitch, value ? &G.v_box : &G.k_box, bar, p * kPitch, (int)row + i, col_head);
+        }
+      } else if (mine(rows16)) {
 #pragma unroll
         for (int p = 0; p < kPlanes; ++p)
-          tma_load_3d(dst + p * kPlane, value ? &G.v : &G.k, bar, p * kPitch, (int)my_row(row), col_head);
-        t = q8_scale_f16x2(byte);
+          tma_load_3d(dst + p * kPlane + block * (kPackedRows * kPitch), value ? &G.v : &G.k, bar, p * kPitch,
+                      (int)my_row(row), col_head);
       }
+      if (mine(rows16)) t = q8_scale_f16x2(byte);
       if (value < 2)
         *reinterpret_cast<uint32_t*>(ring + kStages * kStageBytes + st * kSideBytes + (value * kBlocks + block) * 4) =
             t;

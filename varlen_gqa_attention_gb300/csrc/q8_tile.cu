@@ -60,11 +60,18 @@ struct Q8Tile {
       __syncwarp();
       if (value == part) {
         uint32_t t = 0;  // of a block that is not loaded: what lies there stays finite
-        if (block * kPackedRows < rows16) {
-          tma_load_3d(smem_u32(smem) + kOffCodes + st * kCodeBytes + block * (kPackedRows * kPitch),
-                      part ? &G.v : &G.k, bar, 0, (int)my_row(row), col_head);
-          t = q8_scale_f16x2(byte);
+        const uint32_t dst = smem_u32(smem) + kOffCodes + st * kCodeBytes;
+        if (rows16 == kKeys && row + kKeys <= G.a.rows) {  // the tile in one run of store rows
+          constexpr int kBox = q8_box_rows(D);
+          if (block == 0) {
+#pragma unroll
+            for (int i = 0; i < kKeys; i += kBox)
+              tma_load_3d(dst + i * kPitch, part ? &G.v_box : &G.k_box, bar, 0, (int)row + i, col_head);
+          }
+        } else if (block * kPackedRows < rows16) {
+          tma_load_3d(dst + block * (kPackedRows * kPitch), part ? &G.v : &G.k, bar, 0, (int)my_row(row), col_head);
         }
+        if (block * kPackedRows < rows16) t = q8_scale_f16x2(byte);
         *reinterpret_cast<uint32_t*>(smem + kOffScales + (st * kBlocks + block) * 4) = t;
       }
       __syncwarp();
