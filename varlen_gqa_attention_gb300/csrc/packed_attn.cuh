@@ -275,10 +275,13 @@ __device__ __forceinline__ void packed_unit(const AttnArgs& A, const PackedPiece
         const int64_t i = r / A.group;
         const int h = ur.hk * A.group + (int)(r % A.group);
         __nv_bfloat16* dst = A.out + (ur.q_start + i) * A.o_rs + (int64_t)h * A.o_hs + d0;
-        if constexpr (MD == 8) {
-          *reinterpret_cast<uint4*>(dst) =
-              make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
-                         pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
+        if constexpr (MD >= 8) {
+#pragma unroll
+          for (int x = 0; x < MD; x += 8)
+            *reinterpret_cast<uint4*>(dst + x) =
+                make_uint4(pack_bf16x2(acc[x] * inv, acc[x + 1] * inv), pack_bf16x2(acc[x + 2] * inv, acc[x + 3] * inv),
+                           pack_bf16x2(acc[x + 4] * inv, acc[x + 5] * inv),
+                           pack_bf16x2(acc[x + 6] * inv, acc[x + 7] * inv));
         } else {
           *reinterpret_cast<uint2*>(dst) =
               make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));

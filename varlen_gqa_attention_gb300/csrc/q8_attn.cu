@@ -35,8 +35,8 @@ struct Q8Few {
   static constexpr int kRingBytes = kStages * (kStageBytes + kSideBytes);
   static constexpr int kQPitch = D * 2 + 16;
   static constexpr int kQBytes = kSplitkRows * kQPitch;
-  static constexpr int kMerge = 4;
-  static constexpr int kMergeBytes = 4 * 8 * 36 * 4;  // 32 dims of the warps' rows
+  static constexpr int kMerge = D == 256 ? 16 : 4;  // (what shared memory leaves room for)
+  static constexpr int kMergeBytes = 4 * 8 * (8 * kMerge + 4) * 4;
   static constexpr int kAlign = 8 * kPitch, kFull = 2;
   static constexpr int kBytes = kRingBytes + kQBytes + kMergeBytes + kAlign;
   static constexpr SkKind kKind = kSkQ8Few;
