@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
       const bool live = row < ur.rows;
       const int64_t r = (int64_t)ur.rb * C::BM + row;
       const int qi = (int)(r / A.group);
-      int64_t rlo = 1, rhi = 0;  // padding rows see nothing
+      int64_t rlo = 0, rhi = INT32_MAX;  // padding rows see every key (prefill_pair.cu)
       if (live) {
         const RowWin w = row_window(qi, sg.q_len, sg.kv_end, sg.causal, sg.window);
         rlo = w.lo;
