@@ -72,7 +72,8 @@ __device__ __forceinline__ void code_blocks(const StepArgs& A, int block, RowTab
   const int part = block % A.kv_parts;
   const int64_t t0 = (int64_t)(block / A.kv_parts) * A.cr;
   const int n = (int)min((int64_t)A.cr, A.T - t0);
-  const int ia = 2 * A.Hkv * part / A.kv_parts, ib = 2 * A.Hkv * (part + 1) / A.kv_parts;  // items: (head, K or V)
+  // this CTA's heads; items: their keys (whose rotation takes most), then their values, so that the warps' shares are even
+  const int ha = A.Hkv * part / A.kv_parts, heads = A.Hkv * (part + 1) / A.kv_parts - ha;
   find_rows(A, t0, n, &s_rows, false);
   // the rows that are the first of their block, in row order
   if (warp == 0) {
@@ -130,9 +131,9 @@ __device__ __forceinline__ void code_blocks(const StepArgs& A, int block, RowTab
     }
     __syncthreads();
 
-    for (int item = ia + warp; item < ib; item += kWarps) {
-      const bool key = (item & 1) == 0;
-      const int h = item >> 1;
+    for (int item = warp; item < 2 * heads; item += kWarps) {
+      const bool key = item < heads;
+      const int h = ha + (key ? item : item - heads);
       const int64_t cell = ((int64_t)g.z * A.Hkv + h) * A.rows + brow;
       uint8_t* codes = (key ? A.q4.kc : A.q4.vc) + cell * D;
       uint8_t* scale = (key ? A.q4.ks : A.q4.vs) + cell / kPackedRows;

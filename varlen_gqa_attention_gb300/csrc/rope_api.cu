@@ -124,7 +124,7 @@ sdpa_status launch_step_q8(const void* f, StepArgs& A, int q_passes, cudaStream_
   const int64_t blocks = A.T / kPackedRows + std::min<int64_t>(A.S, A.T) + 1;
   A.cr = (int)std::min<int64_t>(kStepRows, (A.T + blocks - 1) / blocks);
   const int64_t runs = (A.T + A.cr - 1) / A.cr;
-  A.kv_parts = (int)std::max<int64_t>(1, std::min<int64_t>((2 * (int64_t)A.Hkv + warps - 1) / warps, wave / runs));
+  A.kv_parts = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>((2 * (int64_t)A.Hkv + warps - 1) / warps, A.Hkv), wave / runs));
   const int64_t kv = A.S > 0 ? runs * A.kv_parts : 0;
   const int64_t all = A.T * q_passes, per = std::max<int64_t>(warps, (all + wave - 1) / wave);
   const int64_t grid = kv + (all + per - 1) / per;
