@@ -312,7 +312,7 @@ static cudaError_t launch_k(const void* f, unsigned grid, unsigned block, void**
   return cudaLaunchKernelExC(&cfg, f, args);
 }
 
-// CTAs that share a (token, KV head) pair's keys when a 4-bit call takes the kernel without a schedule; 0 when it
+// CTAs that share a (token, KV head) pair's keys when a call over codes takes the kernel without a schedule; 0 when it
 // does not.  It does where a CTA's share of the longest range possible is short, and the table has an entry for every
 // token or more, or the pairs' CTAs all fit the SMs at once.  The host sees neither lengths nor empty entries: the
 // longest range is the store's rows (or a call-wide window; 128 keys, 4/1 heads, D = 64: 6.2 us in a store of 128
@@ -326,6 +326,12 @@ static cudaError_t launch_k(const void* f, unsigned grid, unsigned block, void**
 // Where lengths differ the call waits for its longest: lengths evenly spread up to the limit (32 tokens of 4096
 // keys, 34.5 / 33.6; with 16/2 heads of 8192, 21 / 24, of 16384 beyond it 36 / 30; 16 tokens at D = 256 of 4096 30 / 32, of
 // 8192 52 / 47).
+// Over the 8-bit store, all ranges full and evenly spread ones: 32/8 heads, D = 128: 32 tokens of 4096 keys 46 / 58 and 39 /
+// 41, of 8192 beyond it 83 / 94 and 66 / 61, 16 of 16384 83 / 92 and 65 / 53; with 16/2 heads 32 of 8192 29 / 39 and 22 / 25, of
+// 16384 47 / 56 and 41 / 42.  D = 64, 32/8 heads: 32 of 8192 48 / 57 and 36 / 37, 16 of 16384 beyond it 49 / 57 and 35 / 31.
+// D = 256, 16/4 heads: 16 of 4096 32 / 39 and 25 / 27, of 8192 51 / 57 and 42 / 39, 32 of 4096 50 / 59 and 40 / 38; clusters of 8,
+// whose CTAs are then few: 4 of 8192 26 / 26 and 17 / 22, of 16384 beyond it 45 / 39 and 43 / 32.  Segments of several tokens: 2 of
+// 16 tokens 1024 keys 15 / 28, beyond it 4096 keys 38 / 30.
 constexpr int64_t kDirectPart = 128;
 static int packed_direct_parts(const DevInfo& di, int bits, int64_t T, int Hq, int Hkv, int D, int S, int64_t rows,
                                int causal, int window, const int32_t* seg_mode) {
@@ -336,7 +342,12 @@ static int packed_direct_parts(const DevInfo& di, int bits, int64_t T, int Hq, i
   if (window > 0 && !seg_mode) keys = std::min<int64_t>(keys, causal ? window : T + window - 1);
   int parts = 1;
   while (parts < 8 && 2 * parts * pairs <= resident && keys > kDirectPart * parts) parts *= 2;
-  const int64_t share = T <= S && (D == 64 || (D == 128 && parts <= 2)) ? 4096 : 2048;
+  int64_t share = T <= S && (D == 64 || (D == 128 && parts <= 2)) ? 4096 : 2048;
+  if (bits == 8 && T <= S) {
+    if (D == 64) share = parts == 1 ? 8192 : 4096;
+    if (D == 128) share = parts == 8 ? 2048 : 4096;
+    if (D == 256) share = parts == 8 ? 1024 : 2048;
+  }
   return keys <= share * parts ? parts : 0;
 }
 
