@@ -362,7 +362,7 @@ size_t sdpa_varlen_eightbit_workspace_bytes(int64_t T, int Hq, int Hkv, int D, i
 /*
  * sdpa_varlen over an 8-bit store: the attention of the values the codes stand for, with probabilities rounded to
  * fp16 (2^-11 of each) whichever kernel a segment takes.  A value of a query row that is less than 2^-31 of the
- * row's largest magnitude may be off by 2^-40 of that.  seg_mode, checks and status bits as for
+ * row's largest magnitude may be off by 2^-39 of that.  seg_mode, checks and status bits as for
  * sdpa_varlen_fourbit, with the store's own (code pointers 16-byte aligned, rows a multiple of 16, cols * Hkv below 2^31)
  * and workspace of at least sdpa_varlen_eightbit_workspace_bytes bytes.
  */

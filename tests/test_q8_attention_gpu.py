@@ -5,7 +5,7 @@ round is what they round over the 4-bit store (tests/test_q4_attention_gpu.py): 
 step 2^-11) on every route, a score in fp32 (each of its D products and sums at most 2^-23 of the sum of
 magnitudes, taken twice for the softmax's two ends, and 2^-20 for exp2 and its argument's rounding), sums in fp32,
 and the output (bf16, 2^-8); a probability below fp16's smallest step is off by 2^-32 of its row's sum.  A query
-value that fp16 cannot hold beside its row's largest is off by 2^-40 of that, D of them by less than the 2^-23 above."""
+value that fp16 cannot hold beside its row's largest is off by 2^-39 of that, D of them by less than the 2^-23 above."""
 import numpy as np
 import pytest
 import torch

@@ -66,7 +66,7 @@ __device__ __forceinline__ uint32_t q8_pair_f16(uint32_t x, uint32_t magic, __ha
 }
 // Query rows in fp16: a row times 2^(14 - e), e being the exponent of its largest magnitude (but at most 2^126, so
 // that rows of less than 2^-112 stay as much below 2^14; a row with an infinity keeps it).  What is above 2^-31
-// of the largest magnitude is exact, what is below is off by at most 2^-40 of it.
+// of the largest magnitude is exact, what is below is off by at most 2^-39 of it.
 __device__ __forceinline__ float q8_row_amax(const uint4& w, float amax) {
   const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll

@@ -1,7 +1,8 @@
 // q8_stage.cu - keys and values of the prefill route's segments brought from 8 bits to 16, as q4_stage.cu does from 4:
 // exactly, K to bf16 and V to fp16 (but for -65536, which no append writes: -65504).
 //
-// Bound by memory: D and an eighth of a byte read and 2 D written per key and KV head, twice.
+// Bound by memory: D and an eighth of a byte read and 2 D written per key and KV head, twice.  24001 keys of 2 heads,
+// D = 128: 11 us (4-bit: 13 for 32763).
 #include "packed_stage.cuh"
 #include "q8.cuh"
 

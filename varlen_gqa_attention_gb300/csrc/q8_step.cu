@@ -12,6 +12,14 @@
 //   * A step that fills a whole ring may come back to the block it began in; the block's first visit then takes
 //     the rows of both.
 // The queries are rotated by CTAs of their own in the same launch.
+//
+// What bounds it: 4093 tokens of 32/8 heads, D = 128, three position axes, take 23.0 us (4.0 TB/s; a loop over the same
+// buffers): 11.6 the queries alone, 2.9 more the look-up of rows and angles, 8.5 the blocks, of which the rotation
+// is 2; no pipe is full (1.6 instructions a cycle at 24 warps an SM).  Two CTAs for a block's heads (27.8 us), the blocks'
+// CTAs behind the queries' (34.2), the queries' rest given to the blocks' CTAs so that all make one wave (31 to 34), a
+// block's queries rotated by its own CTA by the angles it has (31), and rows in shared memory instead of registers, with
+// loops that are not unrolled (24.3), were all slower.  32 single tokens: 5.1 us, the chain table - row and block - codes.
+// The read-back: 57025 tokens of 8 heads 59.5 us, 5.9 TB/s (0.87 of the measured copy rate).
 #include "q8.cuh"
 #include "step.cuh"
 
@@ -221,26 +229,69 @@ __global__ void __launch_bounds__(kRopeThreads, D == 256 ? 2 : 3) sdpa_rope_appe
   }
 }
 
+// Where packed row t is kept: (store row, column), or (-1, 0) when no live segment holds it or it lies before its
+// sequence's beginning.  A warp's lanes look at the segments together.  (With find_rows, which a CTA's warps do together
+// for 16 rows, they waited at its barriers more than for anything else: 57025 tokens of two segments 61.9 us, 59.5 so.)
+__device__ __forceinline__ int2 find_row(const StepArgs& A, int64_t t, int lane, bool report) {
+  int32_t bits = 0;
+  auto load = [&](int i) -> int4 {  // entry i, empty unless it is valid
+    int4 g = __ldg(reinterpret_cast<const int4*>(A.seq_info) + i);
+    const int window = A.seg_mode ? __ldg(A.seg_mode + 2 * i + 1) : A.window;
+    const int32_t b = segment_bits(g.x, g.y, g.z, g.w, A.T, A.rows, A.cols, window);
+    bits |= b;
+    if (b || g.y <= 0) g = make_int4(0, 0, 0, 0);
+    return g;
+  };
+  int owner = -1;
+  bool dead = false;
+  int4 own = make_int4(0, 0, 0, 0);
+  for (int base = 0; base < A.S; base += 32) {
+    int4 g = make_int4(0, 0, 0, 0);
+    if (base + lane < A.S) g = load(base + lane);
+    const uint32_t in = __ballot_sync(0xffffffffu, t >= g.x && t < (int64_t)g.x + g.y);
+    if (in == 0) continue;
+    dead |= owner >= 0 || (in & (in - 1)) != 0;
+    const int src = __ffs(in) - 1;
+    owner = base + src;
+    own = make_int4(__shfl_sync(0xffffffffu, g.x, src), __shfl_sync(0xffffffffu, g.y, src),
+                    __shfl_sync(0xffffffffu, g.z, src), __shfl_sync(0xffffffffu, g.w, src));
+  }
+  if (report) {
+    bits = __reduce_or_sync(0xffffffffu, bits);
+    if (lane == 0 && bits) atomicOr(A.status_dev, bits);
+  }
+  // a segment that shares any row with another valid one is dropped
+  for (int base = 0; owner >= 0 && !dead && base < A.S; base += 32) {
+    int4 g = make_int4(0, 0, 0, 0);
+    if (base + lane < A.S && base + lane != owner) g = load(base + lane);
+    dead = __any_sync(0xffffffffu, max(g.x, own.x) < min(g.x + g.y, own.x + own.y));
+  }
+  if (dead && lane == 0 && A.status_dev) atomicOr(A.status_dev, SDPA_SEG_OVERLAP);
+  const int64_t p = (int64_t)own.w - own.y + (t - own.x);
+  if (owner < 0 || dead || p < 0) return make_int2(-1, 0);
+  return make_int2((int)((uint32_t)p % (uint32_t)A.rows), own.z);
+}
+
 // The rows of a segment table read back from an 8-bit store as bf16 (exact), rows that no live segment holds and
 // rows before a sequence's beginning as 0.
 template <int D>
 __global__ void __launch_bounds__(kRopeThreads) sdpa_q8_unpack_kernel(StepArgs A) {
-  __shared__ RowTable s_rows;
-  constexpr int CPH = D / 16, U = 4;  // chunks of a head
+  constexpr int CPH = D / 16, U = 4, kWarps = kRopeThreads / 32;  // chunks of a head
   const int64_t t0 = (int64_t)blockIdx.x * A.cr;
   const int n = (int)min((int64_t)A.cr, A.T - t0);
-  find_rows(A, t0, n, &s_rows, blockIdx.x == 0);
-  if (threadIdx.x < n) {
-    int col = 0;
-    const int64_t p = row_place(&s_rows, t0, threadIdx.x, &col);
-    s_rows.cell[threadIdx.x] = p >= 0 ? make_int2((int)((uint32_t)p % (uint32_t)A.rows), col) : make_int2(-1, 0);
-  }
-  __syncthreads();
-  // A lane takes chunks of 16 dims, U at a time over the rows of its warp (warp, warp + 8, ...).  Two lanes change
+  // A lane takes chunks of 16 dims, U at a time over the rows of its warp (warp, warp + 8).  Two lanes change
   // halves before they write, so that each write of a warp is 512 bytes in a row.
-  const int lane = threadIdx.x % 32, per = A.Hkv * CPH;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, per = A.Hkv * CPH;
   const bool odd = lane & 1;
-  int r = threadIdx.x / 32, x = lane;
+  static_assert(kStepRows <= 2 * kWarps, "two rows a warp");
+  int2 cells[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    cells[k] = make_int2(-1, 0);
+    if (warp + k * kWarps < n)
+      cells[k] = find_row(A, t0 + warp + k * kWarps, lane, k == 0 && blockIdx.x == 0 && warp == 0 && A.status_dev);
+  }
+  int r = warp, x = lane;
   while (r < n) {
     uint4 kw[U], vw[U];
     uint32_t kb[U], vb[U];
@@ -250,7 +301,7 @@ __global__ void __launch_bounds__(kRopeThreads) sdpa_q8_unpack_kernel(StepArgs A
       row[u] = r < n && x < per ? r : -1;
       at[u] = x;
       if (row[u] >= 0) {
-        const int2 from = s_rows.cell[r];  // (a row that is not there reads another one's bytes)
+        const int2 from = r == warp ? cells[0] : cells[1];  // (a row that is not there reads another one's bytes)
         const int h = x / CPH, c = x % CPH;
         const int64_t cell = ((int64_t)from.y * A.Hkv + h) * A.rows + max(from.x, 0);
         kw[u] = *reinterpret_cast<const uint4*>(A.q4.kc + cell * D + 16 * c);
@@ -261,7 +312,7 @@ __global__ void __launch_bounds__(kRopeThreads) sdpa_q8_unpack_kernel(StepArgs A
       x += 32;
       if (x - lane >= per) {
         x = lane;
-        r += kRopeThreads / 32;
+        r += kWarps;
       }
     }
 #pragma unroll
@@ -271,7 +322,7 @@ __global__ void __launch_bounds__(kRopeThreads) sdpa_q8_unpack_kernel(StepArgs A
         const uint2 got = make_uint2(__shfl_xor_sync(0xffffffffu, send.x, 1), __shfl_xor_sync(0xffffffffu, send.y, 1));
         if (row[u] < 0) return;
         const uint2 w0 = odd ? got : lo, w1 = odd ? hi : got;
-        const bool there = s_rows.cell[row[u]].x >= 0;
+        const bool there = (row[u] == warp ? cells[0] : cells[1]).x >= 0;
         const __nv_bfloat162 s = q8_scale_bf16(byte);
         const uint2 a = q8_words4(w0.x, s), b = q8_words4(w0.y, s), c = q8_words4(w1.x, s), d = q8_words4(w1.y, s);
         const uint4 zero = make_uint4(0, 0, 0, 0);
