@@ -218,13 +218,13 @@ static Grids grids_for(const DevInfo& di, int D) {
   return g;
 }
 
-// The 4-bit store's kernels for the split-K route: the tensor-memory one (q4_tile.cu), which converts a key
-// once for up to 128 packed rows, and the other one (q4_attn.cu), which converts a key again for every 8.
-// 64 segments over 6144 keys on average, 8 KV heads, D = 128, tensor-memory / other: 16 rows 150 / 131 us, 24
-// rows 150 / 303 us; 16 segments of 64 rows over 3100 keys 43 / 100 us.  The host knows how many rows the average
-// segment has (empty ones counted): with at most 16 it launches the other one, with more (of several segments, which may be one
-// chunk and many single tokens) both, and the schedule is the cheaper one's; the other leaves at once.  At
-// D = 256 the output of 128 rows leaves no room for the first.
+// The kernels over codes for the split-K route: the tensor-memory one (packed_tile.cuh), which converts a key once
+// for up to 128 packed rows, and the other one (packed_attn.cuh), which converts a key again for every 8. Over the
+// 4-bit store, 64 segments over 6144 keys on average, 8 KV heads, D = 128, tensor-memory / other: 16 rows 150 / 131
+// us, 24 rows 150 / 303 us; 16 segments of 64 rows over 3100 keys 43 / 100 us.  The host knows how many rows the
+// average segment has (empty ones counted): with at most 16 (8 bits, D = 64: 32) it launches the other one, with more
+// (of several segments, which may be one chunk and many single tokens) both, and the schedule is the cheaper one's;
+// the other leaves at once.  At D = 256 the output of 128 rows leaves no room for the first.
 enum class PackedSplit { kFew, kTile, kEither };
 static PackedSplit packed_split(int bits, int64_t T, int Hq, int Hkv, int D, int S) {
   const int few = bits == 8 && D == 64 ? 32 : 16;
@@ -232,9 +232,8 @@ static PackedSplit packed_split(int bits, int64_t T, int Hq, int Hkv, int D, int
   return S <= 1 ? PackedSplit::kTile : PackedSplit::kEither;
 }
 // The tensor-memory kernel's cost of a key for a unit, in those of the other one for 8 rows (full loads: 0.066
-// and 0.027 ns at D = 128, 0.054 and 0.015 at D = 64).
-// Over the 8-bit store, against the other one's 8 rows (the calls of tile_cost, common.cuh): 160 us for 24 rows and 177 for
-// 64 at D = 128, 157 for 32 and 165 for 64 at D = 64.
+// and 0.027 ns at D = 128, 0.054 and 0.015 at D = 64).  Over the 8-bit store, against the other one's 8 rows (the calls
+// of tile_cost, common.cuh): 160 us for 24 rows and 177 for 64 at D = 128, 157 for 32 and 165 for 64 at D = 64.
 static float packed_tile_ratio(int bits, int D) { return bits == 8 ? (D == 64 ? 3.6f : 2.1f) : D == 64 ? 3.5f : 2.5f; }
 static int64_t packed_resident(const DevInfo& di, int bits, int D) {
   return (int64_t)di.sms * di.packed_per_sm[bits / 8][d_index(D)];
@@ -312,26 +311,25 @@ static cudaError_t launch_k(const void* f, unsigned grid, unsigned block, void**
   return cudaLaunchKernelExC(&cfg, f, args);
 }
 
-// CTAs that share a (token, KV head) pair's keys when a call over codes takes the kernel without a schedule; 0 when it
-// does not.  It does where a CTA's share of the longest range possible is short, and the table has an entry for every
-// token or more, or the pairs' CTAs all fit the SMs at once.  The host sees neither lengths nor empty entries: the
-// longest range is the store's rows (or a call-wide window; 128 keys, 4/1 heads, D = 64: 6.2 us in a store of 128
-// rows, 8.3 in one of 32768, where a cluster of 8 is taken, 14.4 scheduled), and an empty entry counts as a token of its own.  256 entries, one of them 200 tokens
-// over 2048 keys, 20 single tokens and the others empty: 117 us, 66 without the empty ones (256 single tokens of 2048
-// keys 140 / 209, which is why the rule is so).  The shares are halved while there are SMs for them and more
-// than kDirectPart keys in each.  In us, direct / scheduled, 32/8 heads, D = 128, all ranges full: 1 token 512 keys
-// 7.0 / 14.4, 16384 keys 15.8 / 19.4; 8 tokens 64 keys 6.0 / 13.0, 2048 keys 10.3 / 18.8, 16384 keys 40 / 45; 32 tokens
-// 512 keys 8.9 / 22.6, 4096 keys 38 / 49; 64 tokens 2048 keys 41 / 62; two segments of 16 tokens 1024 keys 13 / 26, 4096 keys
-// 36 / 28.
-// Where lengths differ the call waits for its longest: lengths evenly spread up to the limit (32 tokens of 4096
-// keys, 34.5 / 33.6; with 16/2 heads of 8192, 21 / 24, of 16384 beyond it 36 / 30; 16 tokens at D = 256 of 4096 30 / 32, of
-// 8192 52 / 47).
-// Over the 8-bit store, all ranges full and evenly spread ones: 32/8 heads, D = 128: 32 tokens of 4096 keys 46 / 58 and 39 /
-// 41, of 8192 beyond it 83 / 94 and 66 / 61, 16 of 16384 83 / 92 and 65 / 53; with 16/2 heads 32 of 8192 29 / 39 and 22 / 25, of
-// 16384 47 / 56 and 41 / 42.  D = 64, 32/8 heads: 32 of 8192 48 / 57 and 36 / 37, 16 of 16384 beyond it 49 / 57 and 35 / 31.
-// D = 256, 16/4 heads: 16 of 4096 32 / 39 and 25 / 27, of 8192 51 / 57 and 42 / 39, 32 of 4096 50 / 59 and 40 / 38; clusters of 8,
-// whose CTAs are then few: 4 of 8192 26 / 26 and 17 / 22, of 16384 beyond it 45 / 39 and 43 / 32.  Segments of several tokens: 2 of
-// 16 tokens 1024 keys 15 / 28, beyond it 4096 keys 38 / 30.
+// CTAs that share a (token, KV head) pair's keys when a call over codes takes the kernel without a schedule; 0 when
+// it does not.  It does where a CTA's share of the longest range possible is short, and the table has an entry for
+// every token or more, or the pairs' CTAs all fit the SMs at once.  The host sees neither lengths nor empty entries:
+// the longest range is the store's rows (or a call-wide window; 128 keys, 4/1 heads, D = 64: 6.2 us in a store of 128
+// rows, 8.3 in one of 32768, where a cluster of 8 is taken, 14.4 scheduled), and an empty entry counts as a token of
+// its own.  256 entries, one of them 200 tokens over 2048 keys, 20 single tokens and the others empty: 117 us, 66
+// without the empty ones (256 single tokens of 2048 keys 140 / 209, which is why the rule is so).  The shares are
+// halved while there are SMs for them and more than kDirectPart keys in each.  In us, direct / scheduled, 4 bits,
+// 32/8 heads, D = 128, all ranges full: 1 token 512 keys 7.0 / 14.4, 16384 keys 15.8 / 19.4; 8 tokens 64 keys 6.0 /
+// 13.0, 2048 keys 10.3 / 18.8, 16384 keys 40 / 45; 32 tokens 512 keys 8.9 / 22.6, 4096 keys 38 / 49; 64 tokens 2048
+// keys 41 / 62; two segments of 16 tokens 1024 keys 13 / 26, 4096 keys 36 / 28. Where lengths differ the call waits
+// for its longest: lengths evenly spread up to the limit (32 tokens of 4096 keys, 34.5 / 33.6; with 16/2 heads of
+// 8192, 21 / 24, of 16384 beyond it 36 / 30; 16 tokens at D = 256 of 4096 30 / 32, of 8192 52 / 47). Over the 8-bit
+// store, all ranges full and evenly spread ones: 32/8 heads, D = 128: 32 tokens of 4096 keys 46 / 58 and 39 / 41, of
+// 8192 beyond it 83 / 94 and 66 / 61, 16 of 16384 83 / 92 and 65 / 53; with 16/2 heads 32 of 8192 29 / 39 and 22 /
+// 25, of 16384 47 / 56 and 41 / 42.  D = 64, 32/8 heads: 32 of 8192 48 / 57 and 36 / 37, 16 of 16384 beyond it 49 /
+// 57 and 35 / 31. D = 256, 16/4 heads: 16 of 4096 32 / 39 and 25 / 27, of 8192 51 / 57 and 42 / 39, 32 of 4096 50 /
+// 59 and 40 / 38; clusters of 8, whose CTAs are then few: 4 of 8192 26 / 26 and 17 / 22, of 16384 beyond it 45 / 39
+// and 43 / 32.  Segments of several tokens: 2 of 16 tokens 1024 keys 15 / 28, beyond it 4096 keys 38 / 30.
 constexpr int64_t kDirectPart = 128;
 static int packed_direct_parts(const DevInfo& di, int bits, int64_t T, int Hq, int Hkv, int D, int S, int64_t rows,
                                int causal, int window, const int32_t* seg_mode) {
@@ -351,15 +349,14 @@ static int packed_direct_parts(const DevInfo& di, int bits, int64_t T, int Hq, i
   return keys <= share * parts ? parts : 0;
 }
 
-// The prefill route over a 4-bit store: its columns are staged first, which many rows have to pay for, and the
-// route it competes with is the tensor-memory kernel of q4_tile.cu, where that one runs.  Split-K / prefill, 32/8
-// heads, D = 128, in us: one segment over 4096 keys, 128 rows a head 37 / 39, 256 rows 48 / 47, 512 rows
-// 70 / 65, 2048 rows 168 / 136; 128 rows over 32768 keys 92 / 143, 512 rows 292 / 265; four segments of 128 rows
-// over 4096 keys 73 / 102, sixteen 206 / 259.  At D = 256 the split-K kernel converts a key again for every 8 rows: 64 rows a head
-// over 4096 keys 76 / 45.
-// So the bf16 entry's thresholds hold where the tensor-memory one is not launched, and 512 rows where the
-// schedule takes the other one: 64 tokens over 16384 to 32768 keys beside 250 over 32768 842 / 579 us (fewer
-// rows do not pay for the launches when there are none, 5 us).
+// The prefill route over codes: a store's columns are staged first, which many rows have to pay for, and the route it
+// competes with is the tensor-memory kernel of packed_tile.cuh, where that one runs.  Split-K / prefill, 4 bits, 32/8
+// heads, D = 128, in us: one segment over 4096 keys, 128 rows a head 37 / 39, 256 rows 48 / 47, 512 rows 70 / 65,
+// 2048 rows 168 / 136; 128 rows over 32768 keys 92 / 143, 512 rows 292 / 265; four segments of 128 rows over 4096
+// keys 73 / 102, sixteen 206 / 259.  At D = 256 the split-K kernel converts a key again for every 8 rows: 64 rows a
+// head over 4096 keys 76 / 45. So the bf16 entry's thresholds hold where the tensor-memory one is not launched, and
+// 512 rows where the schedule takes the other one: 64 tokens over 16384 to 32768 keys beside 250 over 32768 842 / 579
+// us (fewer rows do not pay for the launches when there are none, 5 us).
 constexpr int kTilePrefillRows = 1024;
 static int packed_prefill_min_rows(PackedSplit sp) {
   return sp == PackedSplit::kFew ? kPrefillRows : sp == PackedSplit::kEither ? 512 : kTilePrefillRows;
@@ -367,7 +364,7 @@ static int packed_prefill_min_rows(PackedSplit sp) {
 static float packed_prefill_min_work(PackedSplit sp) { return sp == PackedSplit::kFew ? kPrefillMinWork : 4 * kPrefillMinWork; }
 // Packed rows of a call's longest segment when none is empty.
 static int64_t packed_longest(int64_t T, int group, int S) { return std::max<int64_t>(1, T - std::max(S, 1) + 1) * group; }
-// Columns a 4-bit call stages in 16 bits for the prefill kernel: one per segment that can have
+// Columns a call over codes stages in 16 bits for the prefill kernel: one per segment that can have
 // packed_prefill_min_rows, as far as 2 GiB of workspace hold them (at least one while that takes at most 8 GiB); none
 // when the automatic route cannot reach packed_prefill_min_work.  Depends on sizes and the route policy only.
 static int64_t stage_bytes_per_column(int64_t rows, int Hkv, int D) { return rows * Hkv * D * 2; }

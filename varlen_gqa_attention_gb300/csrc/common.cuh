@@ -416,7 +416,10 @@ __host__ __device__ __forceinline__ int64_t lead_cost(int route, int kind = kSkB
 // CTA's share holds the start of a tile of each unit it crosses (nslots stays exact).
 __host__ __device__ __forceinline__ int64_t phase_ctas(int64_t G, int64_t Wp, int route, int kind = kSkBf16) {
   // (divisions by constants)
-  const int64_t g = route != kRouteSplitk ? Wp : kind == kSkBf16 ? Wp / 6 : kind == kSkQ4Few ? Wp / (4 * (kSplitkRows / 8)) : kind == kSkQ8Few ? Wp / 10 : Wp / 5;
+  const int64_t g = route != kRouteSplitk ? Wp : kind == kSkBf16    ? Wp / 6
+                                           : kind == kSkQ4Few ? Wp / (4 * (kSplitkRows / 8))
+                                           : kind == kSkQ8Few ? Wp / 10
+                                                              : Wp / 5;
   return g < 1 ? 1 : (g < G ? g : G);
 }
 // The tiles [ta, tb) of a unit whose first tile starts at line position k0 (nt tiles of tw

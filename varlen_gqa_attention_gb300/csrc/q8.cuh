@@ -8,8 +8,9 @@
 // finite number, so that a row that holds no position cannot spoil a product whose other factor is 0.
 // The scales are powers of two so that a block may be coded again as rows come to it: under a smaller scale that
 // is exact, and under a larger one it is one rounding by half a step, which adds up over all growths of a block
-// to less than one step of its last scale.
-// (Codes and not 8-bit floating-point numbers: normal values are off by a third as much, and no code is a NaN.)
+// to less than one step of the largest scale it has had.
+// (Codes and not 8-bit floating-point numbers: normal values are off by 0.011 of their deviation, root mean square at
+// D = 128, where e4m3 numbers are by 0.027, and no code is a NaN.)
 #pragma once
 
 #include <cfloat>

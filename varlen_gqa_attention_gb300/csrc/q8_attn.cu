@@ -13,11 +13,12 @@
 //   * A stage is loaded by TMA, in one box for K and one for V or in boxes of 16 rows at the ends, swizzled so that both
 //     the K reads (16 codes of 8 rows) and the V reads (16 codes of 4 rows) of eight lanes meet all banks.  A lane each
 //     brings a block's scale byte, fetched while the stage before was waited for, as an fp16 pair.  (Bytes fetched by the
-//     attention warps, a stage ahead, took 24.3 us for the 32 tokens below.)
-// Measured (one GB300, in a graph): 64 tokens over 16384 to 32768 keys, 32/8 heads, D = 128: 492 us, 6.7 TB/s of codes and
+//     attention warps, a stage ahead, took 24.3 us for the 32 tokens below, 22.6 so.)
+// Measured (one GB300, in a graph): 64 tokens over 16384 to 32768 keys, 32/8 heads, D = 128: 490 to 493 us, 6.7 TB/s of codes and
 // scales, the measured copy rate; D = 256 (16/4 heads, 16384 keys each) 6.6 TB/s, D = 64 5.8.  32 tokens over up to 8192
-// keys, 16/2 heads, without a schedule: 22.6 us, of which the longest range takes 15: 2048 keys a CTA at 0.9 us for each 128
-// of them, the latency of their scores, probabilities and products in turn.
+// keys, 16/2 heads, without a schedule: 20.1 us, 22.4 over cold keys.  The longest range alone among ranges of 16 keys takes
+// 17.9 (all of 16 keys 7.4): 2048 keys a CTA at 0.66 us for each 128 of them, the latency of their scores,
+// probabilities and products in turn.
 // P is rounded to fp16 as over the 4-bit store (q4_attn.cu), sums are fp32.
 #include "packed_attn.cuh"
 #include "q8.cuh"

@@ -177,8 +177,8 @@ __device__ __forceinline__ int64_t grid_of(const SchedArgs& A, const SkShape& k,
 }
 
 // Route of a live segment.  The prefill kernel takes segments that fill at least one
-// 128-row tile, or have the rows that pay for staging a 4-bit column (on a ring store too: its key tiles stop at the wrap, so a TMA box never
-// wraps), when the call holds enough such work to pay for that kernel's fixed cost (`big`:
+// 128-row tile, or have the rows that pay for staging a column of codes (on a ring store too: its key tiles stop at
+// the wrap, so a TMA box never wraps), when the call holds enough such work to pay for that kernel's fixed cost (`big`:
 // the segments' prefill_work sums to at least pf_min_work); everything else, and
 // everything when the prefill kernel is unusable, goes to the split-K kernel.
 __device__ __forceinline__ int route_of(const SchedArgs& A, int32_t q_len, bool big, int pf_rows) {
@@ -268,7 +268,7 @@ __device__ __forceinline__ UnitRec make_unit(const SchedArgs& A, const SkShape& 
   if (g.nrb >= 2 && ur.rb == g.nrb - 1) {
     int64_t sp = g.kv_end;
     if (g.window > 0) sp = min(sp, (int64_t)g.q_len + g.window - 1);
-    // bytes of K and V per key (staged columns hold bf16; phases cut as if all did made 16 4-bit segments of 512
+    // bytes of K and V per key (staged columns hold 16-bit values; phases cut as if all did made 16 4-bit segments of 512
     // packed rows over 4096 keys 253 us, not 206)
     *reuse = sp * (PACKED && q == kRouteSplitk ? A.key_bytes : (int64_t)A.D * 4);
   }
