@@ -86,17 +86,17 @@ KERNEL_SOURCES = {
 # when it was taken.  A kernel whose sources hash differently now reports traffic null until
 # the capture is repeated.
 NCU_TRAFFIC = {
-    "prefill_d128": (1184279040 + 64862464, "prefill", "a0468b979ee8bad9"),  # sdpa_prefill_pair_kernel<128>
-    "prefill_d64": (9904128 + 256, "prefill", "a0468b979ee8bad9"),  # sdpa_prefill_pair_kernel<64>
-    "prefill_d256": (336229120 + 45867776, "prefill", "a0468b979ee8bad9"),  # sdpa_prefill_kernel<256>
-    "ring_prefill": (14963712 + 0, "prefill", "a0468b979ee8bad9"),  # sdpa_prefill_pair_kernel<128>
-    "tiny": (160512 + 0, "splitk", "4eb2a57bbb5940bf"),  # sdpa_splitk_kernel<64> (tiny calls take the split-K route)
-    "decode": (141727488 + 3381760, "splitk", "4eb2a57bbb5940bf"),  # sdpa_splitk_kernel<128>
-    "decode_append": (141725440 + 3236096, "splitk", "4eb2a57bbb5940bf"),
-    "mixed": (285244160 + 10999040, "splitk", "4eb2a57bbb5940bf"),  # both calls
-    "mixed_modes": (220137984 + 8155648, "splitk", "4eb2a57bbb5940bf"),
+    "prefill_d128": (1131650560 + 65326848, "prefill", "d932284b0219b90b"),  # sdpa_prefill_pair_kernel<128>
+    "prefill_d64": (9902848 + 1792, "prefill", "d932284b0219b90b"),  # sdpa_prefill_pair_kernel<64>
+    "prefill_d256": (326336256 + 45988608, "prefill", "d932284b0219b90b"),  # sdpa_prefill_kernel<256>
+    "ring_prefill": (14963712 + 0, "prefill", "d932284b0219b90b"),  # sdpa_prefill_pair_kernel<128>
+    "tiny": (160768 + 0, "splitk", "093574ab8c16b1e4"),  # sdpa_splitk_kernel<64> (tiny calls take the split-K route)
+    "decode": (141733120 + 3200768, "splitk", "093574ab8c16b1e4"),  # sdpa_splitk_kernel<128>
+    "decode_append": (141726208 + 3512064, "splitk", "093574ab8c16b1e4"),
+    "mixed": (285204992 + 11159296, "splitk", "093574ab8c16b1e4"),  # both calls
+    "mixed_modes": (220261376 + 8444160, "splitk", "093574ab8c16b1e4"),
     # sdpa_clone_kernel: writes still dirty in L2 when the kernel ends are not counted
-    "seq_clone": (134257920 + 85121280, "clone", "0b8c9a1ffb83a5cb"),
+    "seq_clone": (134239488 + 84714240, "clone", "1dc2a706f04646f4"),
 }
 
 
