@@ -330,6 +330,8 @@ static cudaError_t launch_k(const void* f, unsigned grid, unsigned block, void**
 // 57 and 35 / 31. D = 256, 16/4 heads: 16 of 4096 32 / 39 and 25 / 27, of 8192 51 / 57 and 42 / 39, 32 of 4096 50 /
 // 59 and 40 / 38; clusters of 8, whose CTAs are then few: 4 of 8192 26 / 26 and 17 / 22, of 16384 beyond it 45 / 39
 // and 43 / 32.  Segments of several tokens: 2 of 16 tokens 1024 keys 15 / 28, beyond it 4096 keys 38 / 30.
+// Shares halved until the CTAs make two waves: 8 bits, 32 tokens of 8192 keys, 16/2 heads, full 27.4 us in one wave, 36.6 in
+// two, evenly spread 20.8 / 26.0 (one of 8192 keys among ones of 64, 17.9 / 14.6).
 constexpr int64_t kDirectPart = 128;
 static int packed_direct_parts(const DevInfo& di, int bits, int64_t T, int Hq, int Hkv, int D, int S, int64_t rows,
                                int causal, int window, const int32_t* seg_mode) {
