@@ -601,6 +601,7 @@ static sdpa_status run(const void* q, int64_t T, int Hq, int D, int64_t q_rs, in
   aa.T = T;
   aa.ws = W;
   aa.status_dev = status_dev;
+  aa.out_mul = bits == 8 ? kQ8StagedMul : 1.f;
   AppendArgs apw;
   if (ap) {
     apw = *ap;

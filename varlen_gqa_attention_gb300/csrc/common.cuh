@@ -192,6 +192,7 @@ struct AttnArgs {
   int64_t T;
   Workspace ws;
   int32_t* status_dev;
+  float out_mul;       // prefill kernels over staged columns: what the staged values are to be multiplied by
 };
 
 // Arguments of the KV append kernel (the step's new rows into the column store).

@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(PfCfg<D>::THREADS, 1)
       // (F16: a row whose scores are NaN has no maximum: it is joined as one, and comes out NaN)
       const bool empty = F16 ? L == 0.f : !(L > 0.f);
       if (F16 && L != L) m_use = 0.f;
-      const float w = direct ? 1.f / L : 1.f;
+      const float w = (direct ? 1.f / L : 1.f) * (F16 ? A.out_mul : 1.f);
 #pragma unroll 1
       for (int c = 0; c < D / 64; ++c) {
         float o[32];

@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(PpCfg<D>::THREADS, 1)
       float* prow = A.ws.part_o[kRoutePrefill] + pidx * D;
       // a row with no visible key has l = 0 and writes zeros (never 0 * O)
       const bool empty = F16 ? l == 0.f : !(l > 0.f);
-      const float w = direct ? (empty ? 0.f : 1.f / l) : 1.f;
+      const float w = (direct ? (empty ? 0.f : 1.f / l) : 1.f) * (F16 ? A.out_mul : 1.f);
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         float o[32];

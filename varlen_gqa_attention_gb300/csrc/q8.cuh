@@ -4,8 +4,8 @@
 // one byte for each block of 16 rows of a head.  A code c under scale byte b stands for
 //     (c - 128) * s(b),   s(b) = 2^(min(b, 29) - 20).
 // c - 128 has at most 8 significant bits, so every value is exact in bf16 and, being a multiple of 2^-20 of at
-// most 128 * 2^9, all but -65536 (which no append writes) is exact in fp16 too.  Every byte pattern stands for a
-// finite number, so that a row that holds no position cannot spoil a product whose other factor is 0.
+// most 128 * 2^9, a sixteenth of it is exact in fp16.  Every byte pattern stands for a finite number, so that a row
+// that holds no position cannot spoil a product whose other factor is 0.
 // The scales are powers of two so that a block may be coded again as rows come to it: under a smaller scale that
 // is exact, and under a larger one it is one rounding by half a step, which adds up over all growths of a block
 // to less than one step of the largest scale it has had.
@@ -110,6 +110,7 @@ const void* q8_splitk_kernel_ptr(int D);
 const void* q8_direct_kernel_ptr(int D);
 int q8_splitk_smem_bytes(int D);
 const void* q8_stage_kernel_ptr(int D);
+constexpr float kQ8StagedMul = 16.f;  // a staged value stands for this many times itself
 const void* q8_tile_kernel_ptr(int D);
 int q8_tile_smem_bytes(int D);
 

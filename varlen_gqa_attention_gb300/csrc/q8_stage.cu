@@ -1,5 +1,6 @@
 // q8_stage.cu - keys and values of the prefill route's segments brought from 8 bits to 16, as q4_stage.cu does from 4:
-// exactly, K to bf16 and V to fp16 (but for -65536, which no append writes: -65504).
+// exactly, K to bf16 and V / 16 to fp16 (V itself can be -65536, which fp16 does not hold); the prefill kernels multiply
+// their output by the 16 again.
 //
 // Bound by memory: D and an eighth of a byte read and 2 D written per key and KV head, twice.  24001 keys of 2 heads,
 // D = 128: 11 us (4-bit: 13 for 32763).
@@ -24,15 +25,10 @@ struct Q8Chunk {
     return make_uint4(a.x, a.y, b.x, b.y);
   }
   __device__ __forceinline__ uint4 values() const {
-    const __half2 s = __float2half2_rn(q8_scale(vb));
-    return make_uint4(pair(vw.x, 0x4140, s), pair(vw.x, 0x4342, s), pair(vw.y, 0x4140, s), pair(vw.y, 0x4342, s));
-  }
-  // 0x6400 | c is 1024 + c
-  __device__ __forceinline__ static uint32_t pair(uint32_t w, uint32_t which, __half2 s) {
-    const uint32_t u = __byte_perm(w, 0x64u, which);
-    const __half2 c = __hsub2(*reinterpret_cast<const __half2*>(&u), __float2half2_rn(1152.f));
-    const __half2 v = __hmax2(__hmul2(c, s), __float2half2_rn(-65504.f));
-    return *reinterpret_cast<const uint32_t*>(&v);
+    const uint32_t w = q8_scale_f16x2(vb);
+    const __half2 t = *reinterpret_cast<const __half2*>(&w), z = __hmul2(t, __float2half2_rn(-1152.f));
+    return make_uint4(q8_pair_f16<false>(vw.x, kQ8Magic, t, z), q8_pair_f16<true>(vw.x, kQ8Magic, t, z),
+                      q8_pair_f16<false>(vw.y, kQ8Magic, t, z), q8_pair_f16<true>(vw.y, kQ8Magic, t, z));
   }
 };
 
