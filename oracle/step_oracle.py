@@ -149,6 +149,20 @@ def q8_code_block(new, kept=None):
     return (np.clip(np.rint(x / Q8_SCALES[byte]), -128, 127) + 128).astype(np.uint8), byte
 
 
+SHARED_BLOCK = 128
+
+
+def q8_shared(seq_info, live, rows):
+    """Segments of a table, live (each packed row's segment), that write to a block of a column that another one does."""
+    seq = np.asarray(seq_info, dtype=np.int64).reshape(-1, 4)
+    writers = {}
+    for s in sorted(set(int(x) for x in live if x >= 0)):
+        _, n, c, end = seq[s]
+        for p in range(max(int(end - n), 0), int(end)):
+            writers.setdefault((int(c), p % rows // BLOCK), set()).add(s)
+    return sorted(set().union(*(w for w in writers.values() if len(w) > 1)))
+
+
 def q8_append(codes, scales, x, cells, seq_info, live, rows):
     """Copies of a store's codes [cols, Hkv, rows, D] and scales after the rows x [T, Hkv, D] named by
     cells [(t, row, col)] have been written; live: each packed row's segment."""

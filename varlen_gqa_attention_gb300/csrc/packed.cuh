@@ -11,6 +11,17 @@ namespace sdpa {
 // head dim, at 8 bits 16 rows of a head share a scale.
 constexpr int kPackedRows = 16;
 
+// Whether two segments (q_start, q_len, col, kv_end) of one column, q_len > 0, write to one block of kPackedRows store
+// rows.  Each writes a run of blocks, on a ring of all the column's blocks.
+__host__ __device__ inline bool blocks_meet(int32_t a_len, int32_t a_end, int32_t b_len, int32_t b_end, int64_t rows) {
+  if (a_end <= 0 || b_end <= 0) return false;  // no position: nothing is written
+  const int64_t ring = rows / kPackedRows;
+  const int64_t a0 = (a_end > a_len ? a_end - a_len : 0) / kPackedRows, an = (a_end - 1) / kPackedRows - a0 + 1;
+  const int64_t b0 = (b_end > b_len ? b_end - b_len : 0) / kPackedRows, bn = (b_end - 1) / kPackedRows - b0 + 1;
+  const int64_t d = ((b0 - a0) % ring + ring) % ring;  // where b's run begins, counted from a's
+  return d < an || d + bn > ring;
+}
+
 // Device pointers of a store of codes and scales.
 struct PackedStore {
   uint8_t* kc;

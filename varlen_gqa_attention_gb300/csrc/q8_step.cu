@@ -82,7 +82,7 @@ __device__ __forceinline__ void code_blocks(const StepArgs& A, int block, RowTab
   const int n = (int)min((int64_t)A.cr, A.T - t0);
   // this CTA's heads; items: their keys (whose rotation takes most), then their values, so that the warps' shares are even
   const int ha = A.Hkv * part / A.kv_parts, heads = A.Hkv * (part + 1) / A.kv_parts - ha;
-  find_rows(A, t0, n, &s_rows, false);
+  find_rows<true>(A, t0, n, &s_rows, false);
   // the rows that are the first of their block, in row order
   if (warp == 0) {
     bool first = false;

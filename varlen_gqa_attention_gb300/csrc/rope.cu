@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kRopeThreads) sdpa_q4_unpack_kernel(StepArgs A
   constexpr int LPH = D / 8, U = 4;
   const int64_t t0 = (int64_t)blockIdx.x * A.cr;
   const int n = (int)min((int64_t)A.cr, A.T - t0);
-  find_rows(A, t0, n, &s_rows, blockIdx.x == 0);
+  find_rows<false>(A, t0, n, &s_rows, blockIdx.x == 0);
   if (threadIdx.x < n) {
     int col = 0;
     const int64_t p = row_place(&s_rows, t0, threadIdx.x, &col);

@@ -162,15 +162,16 @@ __device__ __forceinline__ bool check_positions(const RopeArgs& R, int (&pos)[kR
 
 // A CTA's packed rows [t0, t0 + n): each row's segment, found by every thread looking at the
 // segments in turn.  A row is live when exactly one valid segment holds it and that segment shares
-// no packed row with another valid one, anywhere.
+// no packed row with another valid one, anywhere (BLOCKS: nor, both being live otherwise, a block that they write to).
 struct RowTable {
   int owner[kStepRows];
-  int dead[kStepRows];
+  int dead[kStepRows];   // the status bits that say why
   int4 seg[kStepRows];   // the owner's entry
   int2 cell[kStepRows];  // (store row, column), or (-1, 0): nothing of the row is kept
   int pos[kStepRows][kRopeAxes];
 };
 
+template <bool BLOCKS>
 __device__ __forceinline__ void find_rows(const StepArgs& A, int64_t t0, int n, RowTable* s, bool report) {
   auto load = [&](int i, int4* g) -> int32_t {
     *g = __ldg(reinterpret_cast<const int4*>(A.seq_info) + i);
@@ -197,26 +198,46 @@ __device__ __forceinline__ void find_rows(const StepArgs& A, int64_t t0, int n, 
       if (atomicCAS(&s->owner[r], -1, i) == -1)
         s->seg[r] = g;
       else
-        s->dead[r] = 1;
+        s->dead[r] = SDPA_SEG_OVERLAP;
     }
   }
   if (report && bits && A.status_dev) atomicOr(A.status_dev, bits);
   __syncthreads();
   if (A.S <= 1) return;
+  auto meet = [](const int4& a, const int4& b) { return max(a.x, b.x) < min(a.x + a.y, b.x + b.y); };
+  // whether no other valid segment has packed rows of entry k (asked of entries that share a block only)
+  auto alone = [&](int k, const int4& g) {
+    for (int j = 0; j < A.S; ++j) {
+      int4 o;
+      if (j != k && load(j, &o) == 0 && o.y > 0 && meet(g, o)) return false;
+    }
+    return true;
+  };
   // whether another valid segment meets an owner outside these rows
   for (int i = tid; i < A.S; i += kRopeThreads) {
     int4 g = g0;
     const int32_t b = i == tid ? bits0 : load(i, &g);
     if (b || g.y <= 0) continue;
+    bool column = false;
     for (int r = 0; r < n; ++r) {
       const int o = s->owner[r];
       if (o < 0 || o == i) continue;
       const int4 m = s->seg[r];
-      if (max(m.x, g.x) < min(m.x + m.y, g.x + g.y)) s->dead[r] = 1;
+      if (meet(m, g)) s->dead[r] = SDPA_SEG_OVERLAP;
+      column |= m.z == g.z;
+    }
+    if (!BLOCKS || !column) continue;
+    for (int r = 0; r < n; ++r) {
+      const int o = s->owner[r];
+      if (o < 0 || o == i || s->dead[r]) continue;
+      const int4 m = s->seg[r];
+      // (a segment that shares a packed row is dropped for that, and writes nothing)
+      if (m.z == g.z && blocks_meet(m.y, m.w, g.y, g.w, A.rows) && alone(o, m) && alone(i, g))
+        s->dead[r] = SDPA_SEG_SHARED_BLOCK;
     }
   }
   __syncthreads();
-  if (tid < n && s->dead[tid] && A.status_dev) atomicOr(A.status_dev, SDPA_SEG_OVERLAP);
+  if (tid < n && s->dead[tid] && A.status_dev) atomicOr(A.status_dev, s->dead[tid]);
 }
 
 // Position of row t0 + r in its sequence, or -1 when no live segment holds it (or it has none).
@@ -298,7 +319,7 @@ __device__ __forceinline__ void step_passes(const StepArgs& A, int block, RowTab
     int r = lr, p = lp;  // the pass at hand
     load(&x[0]);
     load(&x[1]);
-    find_rows(A, t0, n, &s_rows, block == 0);
+    find_rows<!KV>(A, t0, n, &s_rows, block == 0);  // (without keys and values: beside the 8-bit append's blocks)
     place_rows(A, t0, n, &s_rows);
 
     if (wa < wb) {
