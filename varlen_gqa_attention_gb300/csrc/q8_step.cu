@@ -230,8 +230,12 @@ __global__ void __launch_bounds__(kRopeThreads, D == 256 ? 2 : 3) sdpa_rope_appe
 }
 
 // Where packed row t is kept: (store row, column), or (-1, 0) when no live segment holds it or it lies before its
-// sequence's beginning.  A warp's lanes look at the segments together.  (With find_rows, which a CTA's warps do together
-// for 16 rows, they waited at its barriers more than for anything else: 57025 tokens of two segments 61.9 us, 59.5 so.)
+// sequence's beginning.  A warp's lanes look at the segments together, 32 at a time: for tables of up to kFewSegs.  With
+// find_rows, which a CTA's warps do together for 16 rows, they waited at its barriers more than for anything else: 57025
+// tokens of two segments 61.9 us, 59.5 so.  Tables of more take find_rows, whose 256 threads see a segment each and whose
+// CTA reads the table once.  Rows of 8 heads read back, this / find_rows, us: 16 rows of each of 32 segments 4.9 / 5.1, of
+// 64 6.2 / 5.9, of 256 13.3 / 8.2, of 2048 386 / 87; one row of each of 32 3.1 / 3.3, of 64 3.6 / 3.3, of 512 15.4 / 6.7.
+constexpr int kFewSegs = 32;
 __device__ __forceinline__ int2 find_row(const StepArgs& A, int64_t t, int lane, bool report) {
   int32_t bits = 0;
   auto load = [&](int i) -> int4 {  // entry i, empty unless it is valid
@@ -284,12 +288,22 @@ __global__ void __launch_bounds__(kRopeThreads) sdpa_q8_unpack_kernel(StepArgs A
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, per = A.Hkv * CPH;
   const bool odd = lane & 1;
   static_assert(kStepRows <= 2 * kWarps, "two rows a warp");
+  const bool few = A.S <= kFewSegs;
+  __shared__ RowTable s_rows;
+  if (!few) find_rows<false>(A, t0, n, &s_rows, blockIdx.x == 0);
   int2 cells[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
+    const int r = warp + k * kWarps;
     cells[k] = make_int2(-1, 0);
-    if (warp + k * kWarps < n)
-      cells[k] = find_row(A, t0 + warp + k * kWarps, lane, k == 0 && blockIdx.x == 0 && warp == 0 && A.status_dev);
+    if (r >= n) continue;
+    if (few) {
+      cells[k] = find_row(A, t0 + r, lane, k == 0 && blockIdx.x == 0 && warp == 0 && A.status_dev);
+    } else {
+      int col = 0;
+      const int64_t p = row_place(&s_rows, t0, r, &col);
+      if (p >= 0) cells[k] = make_int2((int)((uint32_t)p % (uint32_t)A.rows), col);
+    }
   }
   int r = warp, x = lane;
   while (r < n) {
