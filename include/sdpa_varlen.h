@@ -67,8 +67,6 @@ typedef enum sdpa_status {
 #define SDPA_DEV_TIMEOUT 32   /* a bounded device wait gave up; the output is unspecified */
 #define SDPA_ROPE_BAD_POS 64  /* a row's position lies outside the rotation table: the row is
                                  written as 0 and nothing of it goes into a store         */
-#define SDPA_SEG_SHARED_BLOCK 128 /* 8-bit append: two live segments write to one block of a
-                                 column: nothing of either is kept, their queries are 0   */
 
 /* Route policy (process-wide).  AUTO sends segments with q_len * (Hq / Hkv) >= 128 to the
  * tensor-memory prefill kernel when the call's such segments hold at least 2^30 of work
@@ -343,9 +341,8 @@ typedef struct sdpa_q8_store {
 } sdpa_q8_store;
 
 /* sdpa_rope_append into an 8-bit store: the rotated keys, rounded to bf16, and the values take their 8 bits on
- * the way.  Two live segments of one call whose positions lie in the same block of a column (whatever their places in
- * the rotation table) would each code it without the other's rows: neither is appended, and status_dev takes
- * SDPA_SEG_SHARED_BLOCK. */
+ * the way.  A block that several live segments of one call write to is coded once, with the new rows of all of them and
+ * the rows that any of them keeps; a cell that several write takes the row of the last one in the table. */
 sdpa_status sdpa_rope_append_eightbit(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* k_new,
                                  int64_t k_row_stride, int64_t k_head_stride, const void* v_new,
                                  int64_t v_row_stride, int64_t v_head_stride, int64_t T, int Hq, int Hkv, int D,

@@ -149,33 +149,32 @@ def q8_code_block(new, kept=None):
     return (np.clip(np.rint(x / Q8_SCALES[byte]), -128, 127) + 128).astype(np.uint8), byte
 
 
-SHARED_BLOCK = 128
-
-
-def q8_shared(seq_info, live, rows):
-    """Segments of a table, live (each packed row's segment), that write to a block of a column that another one does."""
+def q8_blocks(seq_info, live, rows):
+    """(column, block) -> live segments (live: each packed row's) whose positions of this step lie in it, in table order."""
     seq = np.asarray(seq_info, dtype=np.int64).reshape(-1, 4)
-    writers = {}
+    blocks = {}
     for s in sorted(set(int(x) for x in live if x >= 0)):
         _, n, c, end = seq[s]
-        for p in range(max(int(end - n), 0), int(end)):
-            writers.setdefault((int(c), p % rows // BLOCK), set()).add(s)
-    return sorted(set().union(*(w for w in writers.values() if len(w) > 1)))
+        for b in sorted({p % rows // BLOCK for p in range(max(int(end - n), 0), int(end))}):
+            blocks.setdefault((int(c), int(b)), []).append(s)
+    return blocks
 
 
 def q8_append(codes, scales, x, cells, seq_info, live, rows):
     """Copies of a store's codes [cols, Hkv, rows, D] and scales after the rows x [T, Hkv, D] named by
-    cells [(t, row, col)] have been written; live: each packed row's segment."""
+    cells [(t, row, col)] have been written; live: each packed row's segment.  A cell named twice takes the row of the
+    later segment."""
     codes, scales, x = np.array(codes), np.array(scales), f64(x)
     seq = np.asarray(seq_info, dtype=np.int64).reshape(-1, 4)
+    writers = q8_blocks(seq, live, rows)
     blocks = {}
-    for t, r, c in cells:
-        blocks.setdefault((int(live[t]), c, r // BLOCK), {})[r] = t
-    for (s, c, b), new in blocks.items():
-        first = max(int(seq[s, 3] - seq[s, 1]), 0)
+    for t, r, c in sorted(cells, key=lambda cell: int(live[cell[0]])):
+        blocks.setdefault((c, r // BLOCK), {})[r] = t
+    for (c, b), new in blocks.items():
+        firsts = [max(int(seq[s, 3] - seq[s, 1]), 0) for s in writers[c, b]]
         here = range(b * BLOCK, (b + 1) * BLOCK)
         # a row that is not written is kept when the last position before the step that it may hold exists
-        kept = [r for r in here if r not in new and first - 1 - (first - 1 - r) % rows >= 0]
+        kept = [r for r in here if r not in new and any(f - 1 - (f - 1 - r) % rows >= 0 for f in firsts)]
         for h in range(codes.shape[1]):
             old = q8_unpack(codes[c:c + 1, h:h + 1], scales[c:c + 1, h:h + 1])[0, 0]
             order = sorted(new) + kept

@@ -26,13 +26,12 @@ __all__ = [
     "sdpa_varlen_q8", "Q8Store", "q8_store", "q8_workspace_bytes", "workspace_bytes", "workspace_status", "prefill_available", "set_route_policy",
     "set_timing_events", "library",
     "SDPA_OK", "SEG_BAD_QRANGE", "SEG_BAD_COL", "SEG_BAD_KV", "SEG_SPAN", "SEG_OVERLAP",
-    "DEV_TIMEOUT", "ROPE_BAD_POS", "SEG_SHARED_BLOCK", "ROUTE_AUTO", "ROUTE_SPLITK", "ROUTE_PREFILL", "SdpaError",
+    "DEV_TIMEOUT", "ROPE_BAD_POS", "ROUTE_AUTO", "ROUTE_SPLITK", "ROUTE_PREFILL", "SdpaError",
 ]
 
 SDPA_OK = 0
 SEG_BAD_QRANGE, SEG_BAD_COL, SEG_BAD_KV, SEG_SPAN, SEG_OVERLAP, DEV_TIMEOUT = 1, 2, 4, 8, 16, 32
 ROPE_BAD_POS = 64
-SEG_SHARED_BLOCK = 128
 ROUTE_AUTO, ROUTE_SPLITK, ROUTE_PREFILL = 0, 1, 2
 
 STATUS_NAMES = {
@@ -762,8 +761,8 @@ def sdpa_rope_append_q8(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tenso
     """``sdpa_rope_append`` into an 8-bit store, for ``sdpa_varlen_q8``: the rotated keys, rounded to
     bf16, and the values take their 8 bits on the way.  Each block of 16 store rows that the step writes to
     gets the smallest scale that holds its new rows and those that hold earlier positions, which are coded
-    again where the scale changes.  Two segments of one call that write to the same block of a column are both left out
-    (their queries 0), with SEG_SHARED_BLOCK in ``status``."""
+    again where the scale changes.  Segments of one call may share a block of a column: it is coded once, with the
+    rows of all of them (a cell that several write takes the last one's)."""
     rows, cols, Hkv, D, ptrs = _q8(store)
     return _rope_append(library().sdpa_rope_append_eightbit, q, k_new, v_new, store, (ptrs,), rows, cols, Hkv, D,
                         seq_info, table, positions, sections, interleaved, window, seg_mode, q_out, status, stream)

@@ -11,15 +11,25 @@ namespace sdpa {
 // head dim, at 8 bits 16 rows of a head share a scale.
 constexpr int kPackedRows = 16;
 
-// Whether two segments (q_start, q_len, col, kv_end) of one column, q_len > 0, write to one block of kPackedRows store
-// rows.  Each writes a run of blocks, on a ring of all the column's blocks.
+// The blocks of kPackedRows store rows that a segment (q_len > 0, kv_end) writes to: `count` of them from `first` on, on a
+// ring of all of a column's blocks (count may be one more than those).
+struct BlockRun {
+  int64_t first, count;
+};
+__host__ __device__ inline BlockRun block_run(int32_t q_len, int32_t kv_end) {
+  if (kv_end <= 0) return {0, 0};  // no position: nothing is written
+  const int64_t first = (kv_end > q_len ? kv_end - q_len : 0) / kPackedRows;
+  return {first, (kv_end - 1) / kPackedRows - first + 1};
+}
+// Whether two runs share a block of a ring of `ring`.
+__host__ __device__ inline bool runs_meet(const BlockRun& a, const BlockRun& b, int64_t ring) {
+  if (a.count == 0 || b.count == 0) return false;
+  const int64_t d = ((b.first - a.first) % ring + ring) % ring;  // where b's begins, counted from a's
+  return d < a.count || d + b.count > ring;
+}
+// Whether two segments of one column write to one block.
 __host__ __device__ inline bool blocks_meet(int32_t a_len, int32_t a_end, int32_t b_len, int32_t b_end, int64_t rows) {
-  if (a_end <= 0 || b_end <= 0) return false;  // no position: nothing is written
-  const int64_t ring = rows / kPackedRows;
-  const int64_t a0 = (a_end > a_len ? a_end - a_len : 0) / kPackedRows, an = (a_end - 1) / kPackedRows - a0 + 1;
-  const int64_t b0 = (b_end > b_len ? b_end - b_len : 0) / kPackedRows, bn = (b_end - 1) / kPackedRows - b0 + 1;
-  const int64_t d = ((b0 - a0) % ring + ring) % ring;  // where b's run begins, counted from a's
-  return d < an || d + bn > ring;
+  return runs_meet(block_run(a_len, a_end), block_run(b_len, b_end), rows / kPackedRows);
 }
 
 // Device pointers of a store of codes and scales.

@@ -11,6 +11,7 @@
 //     rows) counts for nothing and keeps its bytes.
 //   * A step that fills a whole ring may come back to the block it began in; the block's first visit then takes
 //     the rows of both.
+//   * A block that several segments write to is coded by the first of them, with the rows of all.
 // The queries are rotated by CTAs of their own in the same launch.
 //
 // What bounds it: 4093 tokens of 32/8 heads, D = 128, three position axes, take 23.0 us (4.0 TB/s; a loop over the same
@@ -62,16 +63,113 @@ __device__ __forceinline__ uint32_t pair_amax(uint32_t m, const uint4& w) {
 }
 constexpr uint32_t kQ8Most = 0x477Eu;  // 65024 in bf16
 
-// What the warps need of a block: where its rows come from (a packed row, kKept or kNone), and where it lies.
+// What the warps need of a run's blocks: where a block lies (its first store row, its column), where its rows come
+// from (a packed row, kKept or kNone), and whether any comes from a packed row.
 constexpr int kKept = -1, kNone = -2;
 struct BlockRows {
-  int src[kPackedRows];
-  int pos[kPackedRows][kRopeAxes];
+  int2 at[kStepRows];
+  int fresh[kStepRows];
+  int src[kStepRows][kPackedRows];
+  int pos[kStepRows][kPackedRows][kRopeAxes];
+  __device__ __forceinline__ void put(int f, int row, int s, const int (&p)[kRopeAxes]) {
+    src[f][row] = s;
+#pragma unroll
+    for (int a = 0; a < kRopeAxes; ++a) pos[f][row][a] = p[a];
+  }
 };
+
+// Where a live segment's rows leave a store row of its column: the packed row that is written there (and that row's
+// positions), kKept, or kNone.
+__device__ __forceinline__ int block_row(const StepArgs& A, const int4& g, int64_t row, int (&pos)[kRopeAxes]) {
+  const int64_t last = (int64_t)g.w - 1, begin = max((int64_t)g.w - g.y, (int64_t)0);
+  if (row > last) return kNone;
+  const int64_t p = last - (uint32_t)(last - row) % (uint32_t)A.rows;  // the last position that the row may hold
+  if (p < begin) return kKept;
+  const int src = (int)(g.x + (p - ((int64_t)g.w - g.y)));
+  fetch_positions(A.r, src, (int)p, pos);
+  if (check_positions(A.r, pos)) return src;
+  return p - A.rows >= 0 ? kKept : kNone;  // nothing of the row is written
+}
+
+// The live segments that write to one block, where one of them is known to share a block with another: the first of
+// them, which codes it, and for each row the last one that writes it, and whether any keeps it.  All threads of the CTA
+// look at the table together.  A segment is live when no other valid one has packed rows of it, as all are when each
+// begins behind the one before; in other tables the thread asks all of them.
+struct BlockWriters {
+  int first;
+  int last[kPackedRows], kept[kPackedRows];
+};
+__device__ __forceinline__ void find_writers(const StepArgs& A, int col, int64_t brow, BlockWriters& w) {
+  if (threadIdx.x < kPackedRows) {
+    w.first = INT_MAX;
+    w.last[threadIdx.x] = -1;
+    w.kept[threadIdx.x] = 0;
+  }
+  bool mixed = false;
+  for (int i = threadIdx.x; i < A.S; i += kRopeThreads) {
+    int4 g, o;
+    if (load_entry(A, i, &g) || g.y <= 0) continue;
+    for (int j = i - 1; j >= 0; --j) {
+      if (load_entry(A, j, &o) || o.y <= 0) continue;
+      mixed |= o.x + o.y > g.x;
+      break;
+    }
+  }
+  mixed = __syncthreads_or(mixed);
+  for (int i = threadIdx.x; i < A.S; i += kRopeThreads) {
+    int4 g;
+    if (load_entry(A, i, &g) || g.y <= 0 || g.z != col) continue;
+    if (!runs_meet(block_run(g.y, g.w), {brow / kPackedRows, 1}, A.rows / kPackedRows)) continue;
+    bool live = true;
+    for (int j = 0; mixed && j < A.S; ++j) {
+      int4 o;
+      if (load_entry(A, j, &o) == 0 && o.y > 0 && j != i && rows_meet(g, o)) live = false;
+    }
+    if (!live) continue;
+    atomicMin(&w.first, i);
+#pragma unroll 1
+    for (int c = 0; c < kPackedRows; ++c) {
+      int pos[kRopeAxes];
+      const int src = block_row(A, g, brow + c, pos);
+      if (src >= 0) atomicMax(&w.last[c], i);
+      if (src == kKept) w.kept[c] = 1;
+    }
+  }
+  __syncthreads();
+}
+
+// The rows of those of a run's blocks that other segments write to as well.  Out of line: as part of the kernel, which has
+// next to no tables of this kind, it took the chunks of 4000 rows 2 us of 35.
+static __device__ __noinline__ void share_blocks(const StepArgs& A, const RowTable& rows, BlockRows& blocks, BlockWriters& w,
+                                                 const int* first, int count) {
+  const int lane = threadIdx.x & 31, row = lane % kPackedRows;
+  for (int f = 0; f < count; ++f) {
+    const int r = first[f];
+    if (!rows.shared[r]) continue;
+    const int2 at = blocks.at[f];
+    find_writers(A, at.y, at.x, w);
+    if (threadIdx.x < 32) {
+      int src = kNone, pos[kRopeAxes] = {0, 0, 0, 0};
+      if (w.first == rows.owner[r]) {  // (else that segment's visit codes the block)
+        if (w.last[row] >= 0) {
+          int4 g;
+          load_entry(A, w.last[row], &g);
+          src = block_row(A, g, at.x + row, pos);
+        } else if (w.kept[row]) {
+          src = kKept;
+        }
+      }
+      const bool fresh = __any_sync(0xffffffffu, src >= 0);
+      if (lane < kPackedRows) blocks.put(f, row, src, pos);
+      if (lane == 0) blocks.fresh[f] = fresh;
+    }
+    __syncthreads();
+  }
+}
 
 template <int D, bool IL>
 __device__ __forceinline__ void code_blocks(const StepArgs& A, int block, RowTable& s_rows, BlockRows& s_block,
-                                            int (&s_first)[kStepRows], int& s_count,
+                                            BlockWriters& s_writers, int (&s_first)[kStepRows], int& s_count, int& s_share,
                                             float2 (*s_angles)[D / 2]) {
   constexpr int LPH = D / 16, RPP = 32 / LPH, U = kPackedRows / RPP, kWarps = kRopeThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, li = lane % LPH, ls = lane / LPH;
@@ -97,44 +195,48 @@ __device__ __forceinline__ void code_blocks(const StepArgs& A, int block, RowTab
     }
     const uint32_t all = __ballot_sync(0xffffffffu, first);
     if (first) s_first[__popc(all & ((1u << lane) - 1))] = lane;
-    if (lane == 0) s_count = __popc(all);
+    if (lane == 0) {
+      s_count = __popc(all);
+      s_share = 0;
+    }
   }
   __syncthreads();
   const int count = s_count;
-  for (int f = 0; f < count; ++f) {
-    const int r = s_first[f];
-    const int4 g = s_rows.seg[r];
-    const int64_t begin = max((int64_t)g.w - g.y, (int64_t)0);
-    const int64_t b0 = ((int64_t)g.w - g.y + (t0 + r - g.x)) & -kPackedRows;
-    bool fresh = false;
-    if (tid < kPackedRows) {
-      int64_t p = b0 + tid;
-      if (p >= g.w && p - A.rows >= 0) p -= A.rows;               // a row of the lap before
-      if (p < begin && p + A.rows < g.w) p += A.rows;             // (one that this step writes a lap later)
-      int src = p >= g.w || p < 0 ? kNone : p < begin ? kKept : (int)(g.x + (p - ((int64_t)g.w - g.y)));
-      int pos[kRopeAxes] = {0, 0, 0, 0};
-      if (src >= 0) {
-        fetch_positions(A.r, src, (int)p, pos);
-        if (!check_positions(A.r, pos)) src = p - A.rows >= 0 ? kKept : kNone;  // nothing of the row is written
-      }
-      s_block.src[tid] = src;
-      fresh = src >= 0;
-#pragma unroll
-      for (int a = 0; a < kRopeAxes; ++a) s_block.pos[tid][a] = pos[a];
+  // every block's rows: a thread each
+  static_assert(kRopeThreads == kStepRows * kPackedRows, "a thread for each row of each block");
+  bool share = false;
+  {
+    const int f = tid / kPackedRows, row = tid % kPackedRows;
+    int src = kNone, pos[kRopeAxes] = {0, 0, 0, 0};
+    if (f < count) {
+      const int r = s_first[f];
+      const int4 g = s_rows.seg[r];
+      const int64_t b0 = ((int64_t)g.w - g.y + (t0 + r - g.x)) & -kPackedRows;
+      const int brow = (int)((uint32_t)b0 % (uint32_t)A.rows);
+      if (row == 0) s_block.at[f] = make_int2(brow, g.z);
+      src = block_row(A, g, brow + row, pos);
+      share = s_rows.shared[r];
     }
-    if (!__syncthreads_or(fresh)) continue;  // (no row of the block has angles)
-
-    const int64_t brow = (uint32_t)b0 % (uint32_t)A.rows;
+    s_block.put(f, row, src, pos);
+    const uint32_t fresh = __ballot_sync(0xffffffffu, src >= 0) >> (lane & kPackedRows) & 0xFFFFu;
+    if (row == 0) s_block.fresh[f] = fresh != 0;
+  }
+  if (share) s_share = 1;
+  __syncthreads();
+  if (__builtin_expect(s_share != 0, 0)) share_blocks(A, s_rows, s_block, s_writers, s_first, count);
+  for (int f = 0; f < count; ++f) {
+    if (!s_block.fresh[f]) continue;  // (no row of the block has angles)
+    const int2 at = s_block.at[f];
     Row16 x[U];
     int src[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) src[u] = s_block.src[u * RPP + ls];
+    for (int u = 0; u < U; ++u) src[u] = s_block.src[f][u * RPP + ls];
     for (int i = tid; i < kPackedRows * A.r.half; i += kRopeThreads) {
       const int o = i / A.r.half, j = i - o * A.r.half;
-      if (s_block.src[o] < 0) continue;
-      int p = s_block.pos[o][0];
+      if (s_block.src[f][o] < 0) continue;
+      int p = s_block.pos[f][o][0];
 #pragma unroll
-      for (int a = 1; a < kRopeAxes; ++a) p = j >= A.r.sec_end[a - 1] ? s_block.pos[o][a] : p;
+      for (int a = 1; a < kRopeAxes; ++a) p = j >= A.r.sec_end[a - 1] ? s_block.pos[f][o][a] : p;
       s_angles[o][j] = __ldg(A.r.table + (uint32_t)(p * A.r.half + j));  // below 2^31 (checked on the host)
     }
     __syncthreads();
@@ -142,7 +244,7 @@ __device__ __forceinline__ void code_blocks(const StepArgs& A, int block, RowTab
     for (int item = warp; item < 2 * heads; item += kWarps) {
       const bool key = item < heads;
       const int h = ha + (key ? item : item - heads);
-      const int64_t cell = ((int64_t)g.z * A.Hkv + h) * A.rows + brow;
+      const int64_t cell = ((int64_t)at.y * A.Hkv + h) * A.rows + at.x;
       uint8_t* codes = (key ? A.q4.kc : A.q4.vc) + cell * D;
       uint8_t* scale = (key ? A.q4.ks : A.q4.vs) + cell / kPackedRows;
       const uint32_t was = min((uint32_t)*scale, (uint32_t)kQ8Top);
@@ -210,19 +312,20 @@ __device__ __forceinline__ void code_blocks(const StepArgs& A, int block, RowTab
       }
       if (lane == 0) *scale = (uint8_t)byte;
     }
-    if (f + 1 < count) __syncthreads();  // the block's records are written again
+    if (f + 1 < count) __syncthreads();  // the angles are written again
   }
 }
 
 // CTAs [0, kv_ctas) code blocks, the others rotate queries.
 template <int D, bool IL>
-__global__ void __launch_bounds__(kRopeThreads, D == 256 ? 2 : 3) sdpa_rope_append_q8_kernel(StepArgs A) {
+__global__ void __launch_bounds__(kRopeThreads, D == 256 ? 2 : 3) sdpa_rope_append_q8_kernel(const __grid_constant__ StepArgs A) {
   __shared__ RowTable s_rows;
   __shared__ BlockRows s_block;
-  __shared__ int s_first[kStepRows], s_count;
+  __shared__ BlockWriters s_writers;
+  __shared__ int s_first[kStepRows], s_count, s_share;
   __shared__ __align__(16) float2 s_angles[kPackedRows][D / 2];
   if ((int)blockIdx.x < A.kv_ctas) {
-    code_blocks<D, IL>(A, blockIdx.x, s_rows, s_block, s_first, s_count, s_angles);
+    code_blocks<D, IL>(A, blockIdx.x, s_rows, s_block, s_writers, s_first, s_count, s_share, s_angles);
   } else {
     step_passes<D, IL, false>(A, blockIdx.x - A.kv_ctas, s_rows, s_angles,
                               [](Row16&, const LaneDims<IL>&, const Angles&, bool, int, int, int2) {});

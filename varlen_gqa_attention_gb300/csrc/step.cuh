@@ -162,22 +162,30 @@ __device__ __forceinline__ bool check_positions(const RopeArgs& R, int (&pos)[kR
 
 // A CTA's packed rows [t0, t0 + n): each row's segment, found by every thread looking at the
 // segments in turn.  A row is live when exactly one valid segment holds it and that segment shares
-// no packed row with another valid one, anywhere (BLOCKS: nor, both being live otherwise, a block that they write to).
+// no packed row with another valid one, anywhere.
 struct RowTable {
   int owner[kStepRows];
-  int dead[kStepRows];   // the status bits that say why
+  int dead[kStepRows];
+  int shared[kStepRows]; // BLOCKS: another valid segment writes to a block that the row's segment writes to
   int4 seg[kStepRows];   // the owner's entry
   int2 cell[kStepRows];  // (store row, column), or (-1, 0): nothing of the row is kept
   int pos[kStepRows][kRopeAxes];
 };
 
+// Entry i of the table, and its status bits.
+__device__ __forceinline__ int32_t load_entry(const StepArgs& A, int i, int4* g) {
+  *g = __ldg(reinterpret_cast<const int4*>(A.seq_info) + i);
+  const int window = A.seg_mode ? __ldg(A.seg_mode + 2 * i + 1) : A.window;
+  return segment_bits(g->x, g->y, g->z, g->w, A.T, A.rows, A.cols, window);
+}
+// Whether two segments share a packed row.
+__device__ __forceinline__ bool rows_meet(const int4& a, const int4& b) {
+  return max(a.x, b.x) < min(a.x + a.y, b.x + b.y);
+}
+
 template <bool BLOCKS>
 __device__ __forceinline__ void find_rows(const StepArgs& A, int64_t t0, int n, RowTable* s, bool report) {
-  auto load = [&](int i, int4* g) -> int32_t {
-    *g = __ldg(reinterpret_cast<const int4*>(A.seq_info) + i);
-    const int window = A.seg_mode ? __ldg(A.seg_mode + 2 * i + 1) : A.window;
-    return segment_bits(g->x, g->y, g->z, g->w, A.T, A.rows, A.cols, window);
-  };
+  auto load = [&](int i, int4* g) -> int32_t { return load_entry(A, i, g); };
   const int tid = threadIdx.x;
   int4 g0 = make_int4(0, 0, 0, 0);  // a thread keeps its first segment
   int32_t bits0 = 0;
@@ -185,6 +193,7 @@ __device__ __forceinline__ void find_rows(const StepArgs& A, int64_t t0, int n, 
   if (tid < n) {
     s->owner[tid] = -1;
     s->dead[tid] = 0;
+    if (BLOCKS) s->shared[tid] = 0;
   }
   __syncthreads();
   int32_t bits = 0;
@@ -198,21 +207,12 @@ __device__ __forceinline__ void find_rows(const StepArgs& A, int64_t t0, int n, 
       if (atomicCAS(&s->owner[r], -1, i) == -1)
         s->seg[r] = g;
       else
-        s->dead[r] = SDPA_SEG_OVERLAP;
+        s->dead[r] = 1;
     }
   }
   if (report && bits && A.status_dev) atomicOr(A.status_dev, bits);
   __syncthreads();
   if (A.S <= 1) return;
-  auto meet = [](const int4& a, const int4& b) { return max(a.x, b.x) < min(a.x + a.y, b.x + b.y); };
-  // whether no other valid segment has packed rows of entry k (asked of entries that share a block only)
-  auto alone = [&](int k, const int4& g) {
-    for (int j = 0; j < A.S; ++j) {
-      int4 o;
-      if (j != k && load(j, &o) == 0 && o.y > 0 && meet(g, o)) return false;
-    }
-    return true;
-  };
   // whether another valid segment meets an owner outside these rows
   for (int i = tid; i < A.S; i += kRopeThreads) {
     int4 g = g0;
@@ -223,21 +223,19 @@ __device__ __forceinline__ void find_rows(const StepArgs& A, int64_t t0, int n, 
       const int o = s->owner[r];
       if (o < 0 || o == i) continue;
       const int4 m = s->seg[r];
-      if (meet(m, g)) s->dead[r] = SDPA_SEG_OVERLAP;
+      if (rows_meet(m, g)) s->dead[r] = 1;
       column |= m.z == g.z;
     }
     if (!BLOCKS || !column) continue;
     for (int r = 0; r < n; ++r) {
       const int o = s->owner[r];
-      if (o < 0 || o == i || s->dead[r]) continue;
+      if (o < 0 || o == i) continue;
       const int4 m = s->seg[r];
-      // (a segment that shares a packed row is dropped for that, and writes nothing)
-      if (m.z == g.z && blocks_meet(m.y, m.w, g.y, g.w, A.rows) && alone(o, m) && alone(i, g))
-        s->dead[r] = SDPA_SEG_SHARED_BLOCK;
+      if (m.z == g.z && blocks_meet(m.y, m.w, g.y, g.w, A.rows)) s->shared[r] = 1;
     }
   }
   __syncthreads();
-  if (tid < n && s->dead[tid] && A.status_dev) atomicOr(A.status_dev, s->dead[tid]);
+  if (tid < n && s->dead[tid] && A.status_dev) atomicOr(A.status_dev, SDPA_SEG_OVERLAP);
 }
 
 // Position of row t0 + r in its sequence, or -1 when no live segment holds it (or it has none).
@@ -319,7 +317,7 @@ __device__ __forceinline__ void step_passes(const StepArgs& A, int block, RowTab
     int r = lr, p = lp;  // the pass at hand
     load(&x[0]);
     load(&x[1]);
-    find_rows<!KV>(A, t0, n, &s_rows, block == 0);  // (without keys and values: beside the 8-bit append's blocks)
+    find_rows<false>(A, t0, n, &s_rows, block == 0);
     place_rows(A, t0, n, &s_rows);
 
     if (wa < wb) {
