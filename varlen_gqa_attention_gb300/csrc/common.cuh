@@ -403,7 +403,9 @@ __host__ __device__ inline void key_tile(const KeyTiles& k, int64_t t, int bn, i
 // The 8-bit one's for few rows is bound by memory with up to 8 rows a unit, and takes 1.33 times as long with up to 16,
 // whose keys are converted twice over, and 2.4 times with more (32 sequences of 8192 keys, 64/8 heads, D = 128 and
 // 64, and 32/4, D = 256, less 13 us of schedule and joining: 83, 45 and 88 us for 8 rows, 110, 60 and 117 for 16,
-// 211 for 24 and for 32 at D = 256).
+// 211 for 24 and for 32 at D = 256).  On the line that is 1, 1.25 and 2.5, the nearest of the quarters that it counts in; in
+// twelfths (12, 16 and 29, lead 60) 13 to 40 sequences of 1000 to 8000 keys with up to 3 or 4 tokens each took 0 to 4 % less
+// at D = 128 and 256 (0 to 3 % less, or 1 % more, at 64), and with up to 8 tokens 1 % less to 2 % more at all of them.
 enum SkKind : int { kSkBf16 = 0, kSkQ4Few = 1, kSkQ4Tile = 2, kSkQ8Few = 3 };
 __host__ __device__ __forceinline__ int64_t tile_cost(int route, int rows, int kind = kSkBf16) {
   if (route != kRouteSplitk) return 1;

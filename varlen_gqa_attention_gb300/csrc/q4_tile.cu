@@ -24,7 +24,7 @@
 // Bound by latency: a tile of 64 rows at D = 128 is about six thousand instructions (conversion two of them), issued
 // at 1.7 of 4 a cycle, while the tensor cores are busy a third of the time and shared memory two fifths.  The
 // softmax warps wait for each tensor-memory load and store in the statement that issues it (long scoreboard
-// 3.5 cycles an instruction), and 576 threads leave 96 registers each, which spill (40 bytes at D = 128, 44
+// 3.5 cycles an instruction), and 576 threads leave 96 registers each, which spill (52 bytes at D = 128, 32
 // at 64).  64 segments over 6144 keys on average, 8 KV heads, D = 128: 24 rows 150 us, 64
 // rows 158 us.  With the rows packed (the softmax of 32 rows all in one quarter, on one scheduler) and four
 // converting warps: 221 and 205 us.  (Products of 64 rows instead of 128, and codes read without bank

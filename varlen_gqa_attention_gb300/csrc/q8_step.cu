@@ -14,13 +14,13 @@
 //   * A block that several segments write to is coded by the first of them, with the rows of all.
 // The queries are rotated by CTAs of their own in the same launch.
 //
-// What bounds it: 4093 tokens of 32/8 heads, D = 128, three position axes, take 23.0 us (4.0 TB/s; a loop over the same
+// What bounds it: 4093 tokens of 32/8 heads, D = 128, three position axes, take 23.2 us (4.0 TB/s; a loop over the same
 // buffers): 11.6 the queries alone, 2.9 more the look-up of rows and angles, 8.5 the blocks, of which the rotation
 // is 2; no pipe is full (1.6 instructions a cycle at 24 warps an SM).  Two CTAs for a block's heads (27.8 us), the blocks'
 // CTAs behind the queries' (34.2), the queries' rest given to the blocks' CTAs so that all make one wave (31 to 34), a
 // block's queries rotated by its own CTA by the angles it has (31), and rows in shared memory instead of registers, with
 // loops that are not unrolled (24.3), were all slower.  32 single tokens: 5.1 us, the chain table - row and block - codes.
-// The read-back: 57025 tokens of 8 heads 59.5 us, 5.9 TB/s (0.87 of the measured copy rate).
+// The read-back: 57025 tokens of 8 heads 61.8 us, 5.7 TB/s (0.84 of the measured copy rate), two thirds of it writes.
 #include "q8.cuh"
 #include "step.cuh"
 
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kRopeThreads, D == 256 ? 2 : 3) sdpa_rope_appe
 // Where packed row t is kept: (store row, column), or (-1, 0) when no live segment holds it or it lies before its
 // sequence's beginning.  A warp's lanes look at the segments together, 32 at a time: for tables of up to kFewSegs.  With
 // find_rows, which a CTA's warps do together for 16 rows, they waited at its barriers more than for anything else: 57025
-// tokens of two segments 61.9 us, 59.5 so.  Tables of more take find_rows, whose 256 threads see a segment each and whose
+// tokens of two segments 65.1 us, 61.8 so.  Tables of more take find_rows, whose 256 threads see a segment each and whose
 // CTA reads the table once.  Rows of 8 heads read back, this / find_rows, us: 16 rows of each of 32 segments 4.9 / 5.1, of
 // 64 6.2 / 5.9, of 256 13.3 / 8.2, of 2048 386 / 87; one row of each of 32 3.1 / 3.3, of 64 3.6 / 3.3, of 512 15.4 / 6.7.
 constexpr int kFewSegs = 32;
