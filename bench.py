@@ -86,17 +86,17 @@ KERNEL_SOURCES = {
 # when it was taken.  A kernel whose sources hash differently now reports traffic null until
 # the capture is repeated.
 NCU_TRAFFIC = {
-    "prefill_d128": (1131650560 + 65326848, "prefill", "d932284b0219b90b"),  # sdpa_prefill_pair_kernel<128>
-    "prefill_d64": (9902848 + 1792, "prefill", "d932284b0219b90b"),  # sdpa_prefill_pair_kernel<64>
-    "prefill_d256": (326336256 + 45988608, "prefill", "d932284b0219b90b"),  # sdpa_prefill_kernel<256>
-    "ring_prefill": (14963712 + 0, "prefill", "d932284b0219b90b"),  # sdpa_prefill_pair_kernel<128>
-    "tiny": (160768 + 0, "splitk", "093574ab8c16b1e4"),  # sdpa_splitk_kernel<64> (tiny calls take the split-K route)
-    "decode": (141733120 + 3200768, "splitk", "093574ab8c16b1e4"),  # sdpa_splitk_kernel<128>
-    "decode_append": (141726208 + 3512064, "splitk", "093574ab8c16b1e4"),
-    "mixed": (285204992 + 11159296, "splitk", "093574ab8c16b1e4"),  # both calls
-    "mixed_modes": (220261376 + 8444160, "splitk", "093574ab8c16b1e4"),
+    "prefill_d128": (1193512704 + 65383680, "prefill", "3e862cfaacb8e67b"),  # sdpa_prefill_pair_kernel<128>
+    "prefill_d64": (9903360 + 1792, "prefill", "3e862cfaacb8e67b"),  # sdpa_prefill_pair_kernel<64>
+    "prefill_d256": (487397888 + 46308608, "prefill", "3e862cfaacb8e67b"),  # sdpa_prefill_kernel<256>
+    "ring_prefill": (14964224 + 0, "prefill", "3e862cfaacb8e67b"),  # sdpa_prefill_pair_kernel<128>
+    "tiny": (160256 + 0, "splitk", "3c2fc271b6b84cfb"),  # sdpa_splitk_kernel<64> (tiny calls take the split-K route)
+    "decode": (141725952 + 3290880, "splitk", "3c2fc271b6b84cfb"),  # sdpa_splitk_kernel<128>
+    "decode_append": (141738496 + 3244032, "splitk", "3c2fc271b6b84cfb"),
+    "mixed": (285188864 + 11387392, "splitk", "3c2fc271b6b84cfb"),  # both calls
+    "mixed_modes": (219296512 + 8158464, "splitk", "3c2fc271b6b84cfb"),
     # sdpa_clone_kernel: writes still dirty in L2 when the kernel ends are not counted
-    "seq_clone": (134239488 + 84714240, "clone", "1dc2a706f04646f4"),
+    "seq_clone": (134243584 + 84749568, "clone", "c4f73559c9ec44bc"),
 }
 
 
